@@ -442,6 +442,99 @@ int sparcml_densify(const uint32_t* idx, const float* val, const uint32_t* nnz, 
  * ------------------------------------------------------------------------ */
 int sparcml_check_finite(const float* x, uint64_t n, int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the training step around the exchange: layer norm, whose
+ * backward pass makes part of the gradient that the nodes exchange, and the
+ * orthogonalised weight step, which uses the reduced gradient.
+ *
+ * Element types of their arrays. All sums, statistics and states are fp32;
+ * a 16-bit output is rounded once (RN). A row-major matrix has unit column
+ * stride and a row stride in elements; its base needs only the alignment of
+ * its element type (16-byte aligned rows take the fast path), so a slice of
+ * a flat parameter or gradient vector at any offset will do. Rows of an
+ * output must not overlap. */
+enum sparcml_type {
+  SPARCML_F32 = 0,
+  SPARCML_BF16 = 1,
+  SPARCML_F16 = 2
+};
+
+/* Layer norm of `rows` rows of `dim` elements:
+ *     mean = sum(x) / dim,  rstd = 1 / sqrt(sum((x - mean)^2) / dim + eps)
+ *     y    = (x - mean) * rstd * weight + bias
+ * A NaN or an inf makes its own row NaN and no other.
+ *   x, y      type `type`, strides x_stride >= 0 and y_stride >= dim. y may
+ *             be x itself (same strides).
+ *   weight, bias  [dim] of type weight_type, each may be NULL (ones, zeros).
+ *   mean, rstd  [rows] fp32, for the backward pass.
+ *   rows 0 .. 2^31 - 1 (0: nothing is done), dim 1 .. 2^31 - 1, eps >= 0. */
+int sparcml_layer_norm(const void* x, int32_t type, int64_t x_stride, const void* weight,
+                       const void* bias, int32_t weight_type, uint64_t rows, uint64_t dim,
+                       float eps, void* y, int64_t y_stride, float* mean, float* rstd,
+                       void* stream);
+
+/* Its gradients, with d = dy * weight and xh = (x - mean) * rstd:
+ *     dx      = rstd * (d - sum(d) / dim - xh * sum(d * xh) / dim)
+ *     dweight = sum over the rows of dy * xh,  dbias = sum over the rows of dy
+ *   dy, x, dx  type `type`. dx may be dy or x itself (same strides).
+ *   weight    [dim] of type weight_type, or NULL (ones).
+ *   mean, rstd  [rows], as sparcml_layer_norm wrote them.
+ *   dweight, dbias  [dim] fp32, each may be NULL: for example the layer's
+ *             slices of the node's flat gradient vector. accumulate != 0 adds
+ *             to what they hold. With rows = 0 they become (or keep) +0.
+ *   ws        >= sparcml_layer_norm_backward_workspace_size(rows, dim) bytes,
+ *             256-byte aligned. */
+size_t sparcml_layer_norm_backward_workspace_size(uint64_t rows, uint64_t dim);
+int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x,
+                                int64_t x_stride, int32_t type, const void* weight,
+                                int32_t weight_type, const float* mean, const float* rstd,
+                                uint64_t rows, uint64_t dim, void* dx, int64_t dx_stride,
+                                float* dweight, float* dbias, int32_t accumulate, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/* Orthogonalisation of an update by Newton-Schulz products: for each of
+ * `batch` matrices G [m][n],
+ *     X <- G / |G|_F  (0 where |G|_F = 0), then for each step (a, b, c)
+ *     X <- a X + b (X X') X + c (X X') (X X') X,
+ * which maps every singular value s of X to a s + b s^3 + c s^5 and keeps
+ * the singular vectors. |G|_F neither overflows nor underflows. A NaN or an
+ * inf in G makes its whole result NaN and no other matrix's.
+ *   g       type g_type, strides g_batch_stride, g_stride >= 0.
+ *   out     SPARCML_BF16 or SPARCML_F16, strides as above; no two of its
+ *           elements may share an address.
+ *   coeffs  HOST array [steps][3], read during the call only; steps 1 .. 64.
+ *           They must keep every singular value below 3 and |b s^2 + c s^4|
+ *           below 24 (the usual sets stay below 1.3 and 9): the products take
+ *           fp16 operands scaled by powers of two, and larger values overflow
+ *           to inf, then NaN.
+ *   ws      >= sparcml_orthogonalize_workspace_size(batch, m, n) bytes,
+ *           256-byte aligned; 0 for sizes out of range (batch 0 .. 65535,
+ *           m and n 1 .. 2^24, the smaller of them at most 32768). A wait
+ *           inside the products that runs out records SPARCML_ERR_TIMEOUT
+ *           in its status word; the outputs of that call are unspecified. */
+size_t sparcml_orthogonalize_workspace_size(int32_t batch, uint64_t m, uint64_t n);
+int sparcml_orthogonalize(const void* g, int32_t g_type, int64_t g_batch_stride,
+                          int64_t g_stride, void* out, int32_t out_type,
+                          int64_t out_batch_stride, int64_t out_stride, int32_t batch,
+                          uint64_t m, uint64_t n, const float* coeffs, int32_t steps, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* One weight step with orthogonalised momentum:
+ *     M <- mu M + G;   U = G + mu M if nesterov, else M
+ *     W <- W (1 - lr weight_decay) - lr scale O(U)
+ * with O as sparcml_orthogonalize computes it, in fp32 up to W's rounding.
+ *   weight    type w_type; grad type g_type; momentum fp32. Strides as above,
+ *             those of weight and momentum as for out; the three must not
+ *             overlap. Workspace as for
+ *             sparcml_orthogonalize. */
+int sparcml_muon_step(void* weight, int32_t w_type, int64_t w_batch_stride, int64_t w_stride,
+                      const void* grad, int32_t g_type, int64_t g_batch_stride,
+                      int64_t g_stride, float* momentum, int64_t m_batch_stride,
+                      int64_t m_stride, int32_t batch, uint64_t m, uint64_t n, float mu,
+                      int32_t nesterov, float lr, float weight_decay, float scale,
+                      const float* coeffs, int32_t steps, void* ws, size_t ws_bytes,
+                      void* stream);
+
 #ifdef __cplusplus
 }
 #endif

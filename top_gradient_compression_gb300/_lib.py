@@ -78,6 +78,20 @@ SIGNATURES = {
                                                 vp]),
     "sparcml_densify": (C.c_int, [vp, vp, vp, C.c_int32, C.c_uint64, C.c_uint64, vp, vp, vp]),
     "sparcml_check_finite": (C.c_int, [vp, C.c_uint64, vp, vp]),
+    "sparcml_layer_norm": (C.c_int, [vp, C.c_int32, C.c_int64, vp, vp, C.c_int32, C.c_uint64,
+                                     C.c_uint64, C.c_float, vp, C.c_int64, vp, vp, vp]),
+    "sparcml_layer_norm_backward_workspace_size": (C.c_size_t, [C.c_uint64, C.c_uint64]),
+    "sparcml_layer_norm_backward": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int32, vp,
+                                              C.c_int32, vp, vp, C.c_uint64, C.c_uint64, vp,
+                                              C.c_int64, vp, vp, C.c_int32, vp, C.c_size_t, vp]),
+    "sparcml_orthogonalize_workspace_size": (C.c_size_t, [C.c_int32, C.c_uint64, C.c_uint64]),
+    "sparcml_orthogonalize": (C.c_int, [vp, C.c_int32, C.c_int64, C.c_int64, vp, C.c_int32,
+                                        C.c_int64, C.c_int64, C.c_int32, C.c_uint64, C.c_uint64,
+                                        vp, C.c_int32, vp, C.c_size_t, vp]),
+    "sparcml_muon_step": (C.c_int, [vp, C.c_int32, C.c_int64, C.c_int64, vp, C.c_int32,
+                                    C.c_int64, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32,
+                                    C.c_uint64, C.c_uint64, C.c_float, C.c_int32, C.c_float,
+                                    C.c_float, C.c_float, vp, C.c_int32, vp, C.c_size_t, vp]),
 }
 
 

@@ -475,3 +475,207 @@ def check_finite(x: torch.Tensor, status: torch.Tensor, stream=None) -> None:
         raise ValueError("check_finite: x must be a contiguous float32 CUDA tensor")
     _check("sparcml_check_finite", _lib.load().sparcml_check_finite(
         x.data_ptr() if x.numel() else None, x.numel(), status.data_ptr(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# The training step around the exchange: layer norm with its gradients, and the
+# orthogonalised weight step.
+# ---------------------------------------------------------------------------
+TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+# a, b, c of five quintic steps that take singular values in about (0.01, 1] to (0.7, 1.2)
+NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
+
+
+def _typed(t, name: str, like=None):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in TYPES:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    if like is not None and t.dtype != like.dtype:
+        raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
+    return t
+
+
+def _rows(t, name: str):
+    """(rows, dim, row stride) of a tensor whose last axis is contiguous and whose
+    other axes step evenly; a view, never a copy."""
+    if t.dim() == 0 or t.shape[-1] == 0:
+        raise ValueError(f"{name} needs a last axis of at least one element")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    if t.dim() == 2:
+        return t.shape[0], t.shape[1], t.stride(0)
+    dim = t.shape[-1]
+    if t.numel() == 0:
+        return 0, dim, dim
+    step, rows = None, 1
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * rows:
+            raise ValueError(f"{name}: the axes before the last must step evenly")
+        rows *= size
+    return rows, dim, dim if step is None else step
+
+
+def _vector(t, dim: int, name: str):
+    if t is None:
+        return None
+    _typed(t, name)
+    if t.shape != (dim,) or (dim > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {dim} elements")
+    return t.data_ptr()
+
+
+def _affine(weight, bias, dim: int):
+    w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same type")
+    given = weight if weight is not None else bias
+    return w, b, 0 if given is None else TYPES[given.dtype]
+
+
+def _stat(t, rows: int, name: str):
+    ptr = _cuda(t, torch.float32, name)
+    if t.numel() != rows:
+        raise ValueError(f"{name} must hold {rows} elements")
+    return ptr
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
+               stream=None):
+    """Layer norm over the last axis of x (float32, bfloat16 or float16; the other
+    axes may be strided as one). weight and bias: vectors of one type, not
+    necessarily x's, or None. Returns (y, mean, rstd), the last two float32 with
+    one element per row, for layer_norm_backward. ``out`` may be x."""
+    rows, dim, xs = _rows(_typed(x, "x"), "x")
+    w, b, wt = _affine(weight, bias, dim)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        ys = dim
+    else:
+        orows, odim, ys = _rows(_typed(out, "out", x), "out")
+        if out.shape != x.shape:
+            raise ValueError("out and x shapes differ")
+    if mean is None:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _check("sparcml_layer_norm", _lib.load().sparcml_layer_norm(
+        x.data_ptr(), TYPES[x.dtype], xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys,
+        _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd"), _stream(stream)))
+    return out, mean, rstd
+
+
+def layer_norm_backward_workspace_size(rows: int, dim: int) -> int:
+    return int(_lib.load().sparcml_layer_norm_backward_workspace_size(rows, dim))
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, dbias=None,
+                        accumulate: bool = False, ws=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias). dweight and dbias are float32
+    vectors, for example the layer's slices of a node's flat gradient; with
+    ``accumulate`` the sums are added to what the given ones hold. ``dx`` may be
+    dy or x."""
+    rows, dim, xs = _rows(_typed(x, "x"), "x")
+    _, _, ds = _rows(_typed(dy, "dy", x), "dy")
+    if dy.shape != x.shape:
+        raise ValueError("dy and x shapes differ")
+    w, _, wt = _affine(weight, None, dim)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        os = dim
+    else:
+        _, _, os = _rows(_typed(dx, "dx", x), "dx")
+        if dx.shape != x.shape:
+            raise ValueError("dx and x shapes differ")
+    if accumulate and (dweight is None or dbias is None):
+        raise ValueError("accumulate needs dweight and dbias to add to")
+    if dweight is None:
+        dweight = torch.empty(dim, dtype=torch.float32, device=x.device)
+    if dbias is None:
+        dbias = torch.empty(dim, dtype=torch.float32, device=x.device)
+    if ws is None:
+        ws = workspace(layer_norm_backward_workspace_size(rows, dim), x.device)
+    _check("sparcml_layer_norm_backward", _lib.load().sparcml_layer_norm_backward(
+        dy.data_ptr(), ds, x.data_ptr(), xs, TYPES[x.dtype], w, wt, _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, _stat(dweight, dim, "dweight"),
+        _stat(dbias, dim, "dbias"), int(accumulate), ws.data_ptr(), ws.numel(), _stream(stream)))
+    return dx, dweight, dbias
+
+
+def _matrices(t, name: str, shape=None):
+    """(batch, m, n, batch stride, row stride) of a matrix or a batch of them."""
+    _typed(t, name)
+    if t.dim() not in (2, 3):
+        raise ValueError(f"{name} must have 2 or 3 dims, got {t.dim()}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    if t.dim() == 2:
+        return 1, t.shape[0], t.shape[1], 0, t.stride(0)
+    return t.shape[0], t.shape[1], t.shape[2], t.stride(0), t.stride(1)
+
+
+def _coeffs(coeffs):
+    c = _np.ascontiguousarray(_np.asarray(coeffs, dtype=_np.float32))
+    if c.ndim != 2 or c.shape[1] != 3:
+        raise ValueError("coeffs must be a sequence of (a, b, c)")
+    return c
+
+
+def orthogonalize_workspace_size(batch: int, m: int, n: int) -> int:
+    return int(_lib.load().sparcml_orthogonalize_workspace_size(batch, m, n))
+
+
+def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, ws=None,
+                  stream=None):
+    """Orthogonalises g, [m, n] or [batch, m, n] (float32, bfloat16 or float16), by one
+    Newton-Schulz step per (a, b, c) of ``coeffs``: singular values of g / |g|_F go
+    through a s + b s^3 + c s^5 of each step, singular vectors stay. Returns a
+    tensor of ``out_dtype`` (bfloat16 or float16)."""
+    batch, m, n, gb, gs = _matrices(g, "g")
+    if out is None:
+        out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
+    _, _, _, ob, os = _matrices(out, "out", g.shape)
+    if out.dtype == torch.float32:
+        raise TypeError("out must be bfloat16 or float16")
+    c = _coeffs(coeffs)
+    if ws is None:
+        ws = workspace(orthogonalize_workspace_size(batch, m, n), g.device)
+    _check("sparcml_orthogonalize", _lib.load().sparcml_orthogonalize(
+        g.data_ptr(), TYPES[g.dtype], gb, gs, out.data_ptr(), TYPES[out.dtype], ob, os, batch, m,
+        n, c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)))
+    return out
+
+
+def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: bool = True,
+              weight_decay: float = 0.0, scale: float | None = None, coeffs=NEWTON_SCHULZ,
+              ws=None, stream=None):
+    """One weight step with orthogonalised momentum, in place:
+
+        momentum <- mu momentum + grad;  u = grad + mu momentum (nesterov) or momentum
+        weight   <- weight (1 - lr weight_decay) - lr scale orthogonalize(u)
+
+    weight, grad: [m, n] or [batch, m, n], float32, bfloat16 or float16; momentum
+    float32. grad is, for example, the layer's slice of a dense reduced gradient.
+    ``scale`` defaults to sqrt(max(1, m / n)). Returns (weight, momentum)."""
+    batch, m, n, wb, wst = _matrices(weight, "weight")
+    _, _, _, gb, gs = _matrices(grad, "grad", weight.shape)
+    _, _, _, mb, ms = _matrices(momentum, "momentum", weight.shape)
+    if momentum.dtype != torch.float32:
+        raise TypeError(f"momentum must be torch.float32, got {momentum.dtype}")
+    if scale is None:
+        scale = max(1.0, m / max(n, 1)) ** 0.5
+    c = _coeffs(coeffs)
+    if ws is None:
+        ws = workspace(orthogonalize_workspace_size(batch, m, n), weight.device)
+    _check("sparcml_muon_step", _lib.load().sparcml_muon_step(
+        weight.data_ptr(), TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb,
+        gs, momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
+        c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)))
+    return weight, momentum
