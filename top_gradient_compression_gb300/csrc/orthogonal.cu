@@ -3,20 +3,29 @@
 //
 // With k the smaller side of X and S = X X' (or X' X where X is tall), a step is
 //     S = X X',  P = b S + c S S,  X <- a X + P X   (X <- a X + X P)
-// five products of which the first two are symmetric: only their tiles on and
+// three products of which the first two are symmetric: only their tiles on and
 // below the diagonal are computed, each written a second time as its mirror
 // image. The tall case needs no transpose: the same row-major X is read by the
 // tensor cores with its other side as the contiguous one.
 //
-// Operands are fp16 with fp32 accumulators. X is scaled by 2^12, S by 2^12 and
-// P by 2^11: singular values stay near 1 at most, so nothing overflows, and
-// entries far below the usual 1 / sqrt(m n) still have all their bits. bf16 operands
-// would lose 8 times as much: the result would be 1 % off where fp16 is 0.15 % off.
-// X itself is kept as a pair of fp16, hi + lo. The products read hi. The term
-// a X, repeated over the steps, multiplies small singular values several
-// hundred times, and with them any rounding of X, which has no rank of its
-// own: from the single fp16 a quickly decaying spectrum comes out 2 % off, from
-// the pair 0.02 %. The rounding of S and P is not multiplied so.
+// One launch runs all steps: a persistent grid of one block per SM, whose
+// blocks wait for one another between the products (15 products of five steps;
+// as launches of their own they cost the host 70 us, more than the products of
+// a small matrix take).
+//
+// Numbers. Operands are fp16 with fp32 accumulators. X and S are scaled by 2^12
+// and P by 2^11: singular values stay near 1, so nothing overflows, and entries
+// far below the usual 1 / sqrt(m n) still have all their bits. bf16 operands
+// would lose 8 times as much. Two things are kept beyond that:
+//   - X is a pair of fp16, hi + lo. The products read hi, the term a X both. It
+//     multiplies small singular values several hundred times over the steps, and
+//     with them any rounding of X: from hi alone a 1/i^2 spectrum comes out 2 %
+//     off, from the pair 0.03 %. The rounding of S and P is not multiplied so.
+//   - The diagonals of S and P are fp32 vectors s and p, and the fp16 matrices
+//     hold zeros there: with S = s + S', S S = S' S' + s S' + S' s + s s and
+//     P X = p X + P' X. X near orthogonal has S near the identity, and rounding
+//     that diagonal was most of the error (0.15 to 0.2 % on flat spectra, 0.03 to
+//     0.07 % so).
 
 #include <algorithm>
 
@@ -39,12 +48,11 @@ struct GatherArgs {
   int64_t m_batch, m_stride;
   float mu;
   int32_t nesterov;
+  int32_t vec_g, vec_m;  // rows of g, of mom: four elements are one aligned access
   uint64_t m, n;
   uint32_t blocks;  // per matrix
   float* sums;      // [batch][blocks][3]
-  __half* hi;       // [batch][m][pitch]
-  __half* lo;
-  uint64_t pitch;
+  uint32_t* turns;  // the grid's barrier, zeroed here
 };
 
 // Sums of squares in three ranges (Blue, ACM TOMS 4, 1978), so that no square
@@ -62,23 +70,82 @@ __device__ __forceinline__ void add_square(float v, float (&s)[3]) {
   }
 }
 
+// Four consecutive elements of a row, those from `n` on as zeros; `vec`: all rows allow
+// one access of four.
+__device__ __forceinline__ void load4(const void* p, int32_t type, uint64_t at, uint64_t c,
+                                      uint64_t n, bool vec, float (&v)[4]) {
+  if (vec && c + 4 <= n) {
+    if (type == SPARCML_F32) {
+      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+      v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+    } else if (type == SPARCML_BF16) {
+      const auto f = *reinterpret_cast<const Pack<__nv_bfloat16, 4>*>(
+          static_cast<const __nv_bfloat16*>(p) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = to_f32(f.e[i]);
+    } else {
+      const auto f =
+          *reinterpret_cast<const Pack<__half, 4>*>(static_cast<const __half*>(p) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = to_f32(f.e[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = c + i < n ? load_any(p, type, at + i) : 0.f;
+  }
+}
+
+// Rows are walked in pieces of 512 columns, a warp at a time, each lane with four
+// groups of four: 64 or 128 bytes per lane in flight.
+constexpr uint32_t kPiece = 512;
+
 // M <- mu M + G where there is a momentum, and the partial sums of squares of U.
 __global__ void __launch_bounds__(256) gather_norm_kernel(const GatherArgs a) {
   griddep_wait();
   __shared__ float warp_sums[8][3];
-  const uint64_t b = blockIdx.y, total = a.m * a.n;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.turns = 0;
+  const uint64_t b = blockIdx.y, pieces = (a.n + kPiece - 1) / kPiece, total = a.m * pieces;
+  const uint64_t warps = (uint64_t)a.blocks * 8, id = blockIdx.x * 8ull + (threadIdx.x >> 5);
+  const uint64_t end = total * (id + 1) / warps;
+  uint64_t u = total * id / warps, r = u / pieces, piece = u - r * pieces;
   float s[3] = {0.f, 0.f, 0.f};
-  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (uint64_t)a.blocks * 256) {
-    const uint64_t r = i / a.n, c = i % a.n;
-    float u = load_any(a.g, a.g_type, b * a.g_batch + r * a.g_stride + c);
-    if (a.mom) {
-      float* mp = a.mom + b * a.m_batch + r * a.m_stride + c;
-      const float m = a.mu * *mp + u;
-      *mp = m;
-      u = a.nesterov ? u + a.mu * m : m;
+  for (; u < end; ++u) {
+    const uint64_t c0 = piece * kPiece + lane_id() * 4;
+    const uint64_t at = b * a.g_batch + r * a.g_stride;
+    float v[4][4], mo[4][4];
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + 128 * q;
+      load4(a.g, a.g_type, at + c, c, a.n, a.vec_g, v[q]);
+      if (a.mom)
+        load4(a.mom, SPARCML_F32, b * a.m_batch + r * a.m_stride + c, c, a.n, a.vec_m, mo[q]);
     }
-    add_square(u, s);
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + 128 * q;
+      if (a.mom) {
+        float* mp = a.mom + b * a.m_batch + r * a.m_stride + c;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float t = a.mu * mo[q][i] + v[q][i];
+          mo[q][i] = t;
+          v[q][i] = a.nesterov ? v[q][i] + a.mu * t : t;
+        }
+        if (a.vec_m && c + 4 <= a.n) {
+          *reinterpret_cast<float4*>(mp) = make_float4(mo[q][0], mo[q][1], mo[q][2], mo[q][3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (c + i < a.n) mp[i] = mo[q][i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) add_square(v[q][i], s);
+    }
+    if (++piece == pieces) {
+      piece = 0;
+      ++r;
+    }
   }
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
@@ -93,259 +160,667 @@ __global__ void __launch_bounds__(256) gather_norm_kernel(const GatherArgs a) {
   }
 }
 
-// The scaled input as a pair of fp16. 2^12 / |U| is applied as two factors, each a
-// normal number, whatever the size of |U|.
-__global__ void __launch_bounds__(256) split_kernel(const GatherArgs a) {
-  griddep_wait();
-  __shared__ float factors[2];
-  const uint64_t b = blockIdx.y, total = a.m * a.n;
-  if (threadIdx.x < 32) {
-    double t[3] = {0.0, 0.0, 0.0};
-    for (uint32_t k = threadIdx.x; k < a.blocks; k += 32)
-      for (int q = 0; q < 3; ++q) t[q] += a.sums[(b * a.blocks + k) * 3 + q];
-    for (int d = 16; d > 0; d >>= 1)
-      for (int q = 0; q < 3; ++q) t[q] += __shfl_xor_sync(0xffffffffu, t[q], d);
-    const double norm = sqrt(t[0] * 0x1p-160 + t[1] + t[2] * 0x1p180);
-    if (threadIdx.x == 0) {
-      float f0 = 0.f, f1 = 0.f;
-      if (!(norm < __longlong_as_double(0x7ff0000000000000ll))) {
-        f0 = f1 = __int_as_float(0x7fffffff);  // an inf or a NaN in U: all of X is NaN
-      } else if (norm > 0.0) {
-        int e;
-        const double mant = frexp(norm, &e);
-        f0 = ldexpf(1.f, -e / 2);
-        f1 = (float)(ldexp((double)kScaleX, -(e - e / 2)) / mant);
-      }
-      factors[0] = f0;
-      factors[1] = f1;
-    }
-  }
-  __syncthreads();
-  const float f0 = factors[0], f1 = factors[1];
-  for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (uint64_t)gridDim.x * 256) {
-    const uint64_t r = i / a.n, c = i % a.n;
-    float u = load_any(a.g, a.g_type, b * a.g_batch + r * a.g_stride + c);
-    if (a.mom) {
-      const float m = a.mom[b * a.m_batch + r * a.m_stride + c];
-      u = a.nesterov ? u + a.mu * m : m;
-    }
-    const float x = u * f0 * f1;
-    const __half h = __float2half_rn(x);
-    const uint64_t o = (b * a.m + r) * a.pitch + c;
-    a.hi[o] = h;
-    a.lo[o] = __float2half_rn(x - __half2float(h));
-  }
-}
-
 // ---------------------------------------------------------------------------
-// The products.
+// The steps.
 
-enum Epilogue { kGram = 0, kPoly = 1, kApply = 2, kOrthogonal = 3, kWeight = 4 };
+constexpr uint32_t kMaxSteps = 64;
 
-struct ProductArgs {
-  uint32_t rows, cols, depth;  // of the product, per matrix
-  uint32_t tiles;              // per matrix
-  uint32_t tile_cols;          // 0: the tiles on and below the diagonal
-  float alpha, beta;           // result = alpha * product + beta * (what stands there)
-  const __half* in_hi;         // kPoly: S; kApply and on: X
+struct Product {       // one product of a step, of every matrix of the batch
+  uint32_t n;          // columns of a tile (rows: 128 per block)
+  uint32_t rows, cols;  // of the result
+  uint32_t blocks;     // of 64 along the summed axis
+  uint32_t tile_rows;  // tiles down, or 0: those on and below the diagonal
+  uint32_t tiles;      // per matrix
+  uint32_t splits;     // parts of the summed axis, each a tile of its own
+  uint32_t items;      // batch * tiles * splits
+};
+
+struct Maps {
+  // operands are read in boxes of 64 x 64, 128-byte swizzled; results and what is
+  // added to them move in boxes of 32 x 32, 64-byte swizzled
+  CUtensorMap x_in[2], s_in, p_in, x_out[2], lo_out, s_out, p_out;
+};
+
+struct StepArgs {
+  GatherArgs g;
+  uint32_t batch, steps, tall;
+  Product gram, poly, apply;
+  float coeffs[3 * kMaxSteps];
+  __half* hi;  // [batch][m][pitch]
   __half* lo;
-  __half* out_hi;
-  uint64_t pitch;  // of in_hi, lo and out_hi
-  void* out;       // kOrthogonal: O; kWeight: W
+  uint64_t pitch;
+  float* diag_s;  // [batch][k]
+  float* diag_p;
+  float* part;  // partial tiles of a split product
+  uint32_t k;
+  uint32_t weight;  // result: 1 the weight step, 0 the orthogonal matrix itself
+  void* out;
   int32_t out_type;
   int64_t out_batch, out_stride;
-  float keep;  // kWeight: W <- keep W + (result)
+  float alpha, keep;  // weight: W <- keep W + alpha X; else X
   int32_t* status;
 };
 
-constexpr uint32_t kTile = 128, kDepth = 64, kStages = 4;
-constexpr uint32_t kOperandBytes = kTile * kDepth * 2;
-constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr uint32_t kProductSmem = kStages * kStageBytes + 1024;
+enum Kind { kGram, kPart, kPoly, kApply, kLast };
 
-// One operand's tile of 128 rows and 64 k: two loads of 64 x 64.
-template <bool MN>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, uint32_t row,
-                                             uint32_t k, uint32_t b, uint32_t bar) {
-#pragma unroll
-  for (uint32_t h = 0; h < 2; ++h) {
-    if (MN)
-      tma_load_3d(dst + h * 8192, map, (int32_t)(row + 64 * h), (int32_t)k, (int32_t)b, bar);
-    else
-      tma_load_3d(dst + h * 8192, map, (int32_t)k, (int32_t)(row + 64 * h), (int32_t)b, bar);
-  }
-}
+constexpr uint32_t kWriters = 8;  // warps that write results; then a loader and an issuer
+constexpr uint32_t kThreads = 32 * (kWriters + 2);
+constexpr uint32_t kRingBytes = 160 * 1024, kMaxStages = 6;
+constexpr uint32_t kStageBuf = 4096;  // per writer, twice
+constexpr uint32_t kStepsSmem = kRingBytes + kWriters * 2 * kStageBuf + 1024;
+constexpr uint32_t kAccColumns = 256;  // two accumulators in the 512 columns of tensor memory
 
-template <bool MN>
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, uint32_t step) {
-  return MN ? tile_desc(addr + step * 2048, 8192, 1024) : tile_desc(addr + step * 32, 16, 1024);
-}
+struct Tile {
+  uint32_t b, row0, col0, first, last;  // blocks [first, last) of the summed axis
+  bool mirror;                          // write its mirror image too
+  bool none;                            // beyond the last column
+};
 
-// C = A B for one 128 x 128 tile per block: warp 0 loads, warp 1 issues the
-// products, warps 2 to 5 write the result.
-template <bool A_MN, bool B_MN, int EPI>
-__global__ void __launch_bounds__(192)
-product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-               const ProductArgs p) {
-  extern __shared__ uint8_t raw[];
-  __shared__ alignas(8) uint64_t bars[2 * kStages + 1];
-  __shared__ uint32_t tmem_slot;
-  __shared__ volatile uint32_t gave_up;
-  const uint32_t warp = threadIdx.x >> 5;
-  const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, done = full + 16 * kStages;
-
-  const uint32_t b = blockIdx.x / p.tiles, t = blockIdx.x % p.tiles;
-  uint32_t ti, tj;
-  if (p.tile_cols) {
-    ti = t / p.tile_cols;
-    tj = t % p.tile_cols;
+// Item i of a product: the splits of one tile are neighbours, and tiles run down
+// the columns first, so that the blocks working at one time share few columns
+// of the larger operand.
+template <int CG>
+__device__ __forceinline__ Tile tile_of(const Product& p, uint32_t item) {
+  Tile t;
+  const uint32_t split = item % p.splits;
+  uint32_t u = item / p.splits;
+  t.b = u / p.tiles;
+  u -= t.b * p.tiles;
+  uint32_t i, j;
+  t.mirror = false;
+  if (p.tile_rows) {
+    j = u / p.tile_rows;
+    i = u - j * p.tile_rows;
   } else {
-    ti = (uint32_t)((sqrtf(8.f * (float)t + 1.f) - 1.f) * 0.5f);
-    while (ti * (ti + 1) / 2 > t) --ti;
-    while ((ti + 1) * (ti + 2) / 2 <= t) ++ti;
-    tj = t - ti * (ti + 1) / 2;
+    const uint32_t ratio = 128 * CG / p.n, v = u / ratio;
+    i = (uint32_t)((sqrtf(8.f * (float)v + 1.f) - 1.f) * 0.5f);
+    while (i * (i + 1) / 2 > v) --i;
+    while ((i + 1) * (i + 2) / 2 <= v) ++i;
+    j = u - ratio * (i * (i + 1) / 2);
+    t.mirror = j < ratio * i;
   }
-  const uint32_t row0 = ti * kTile, col0 = tj * kTile;
+  t.row0 = i * 128 * CG;
+  t.col0 = j * p.n;
+  t.none = t.col0 >= p.cols;
+  t.first = (uint32_t)((uint64_t)p.blocks * split / p.splits);
+  t.last = (uint32_t)((uint64_t)p.blocks * (split + 1) / p.splits);
+  return t;
+}
+
+// Byte offset of 16-byte piece c of row r in a 32 x 32 fp16 box, 64-byte swizzled.
+__device__ __forceinline__ uint32_t box_at(uint32_t r, uint32_t c) {
+  return r * 64 + ((c ^ ((r >> 1) & 3u)) << 4);
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+// The state of one block.
+template <int CG>
+struct Worker {
+  uint32_t ring, stages, stage_bytes;      // operand ring
+  uint32_t full, empty, acc_full, acc_empty, in_bar;  // barriers
+  uint32_t lead_full, lead_acc_empty;      // the same of the pair's first block
+  uint32_t buf;                            // this writer's two buffers
+  uint32_t rank, cluster, clusters, tmem;
+  volatile uint32_t* gave_up;
+  uint32_t fill = 0;      // operand stages used so far (loader, issuer)
+  uint32_t acc = 0;       // accumulators used so far (issuer, writers)
+  uint32_t in_uses[2] = {0, 0};
+  uint32_t turn = 0;      // chunks written so far
+};
+
+template <int CG>
+__device__ void load_operands(Worker<CG>& w, const Product& p, const CUtensorMap* ma,
+                              const CUtensorMap* mb, bool a_mn, bool b_mn) {
+  const uint32_t b_rows = p.n / CG, bytes = 128 * 128 + b_rows * 128;
+  for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
+    const Tile t = tile_of<CG>(p, item);
+    if (t.none) continue;
+    const uint32_t ra = t.row0 + 128 * w.rank, rb = t.col0 + b_rows * w.rank;
+    for (uint32_t i = t.first; i < t.last; ++i, ++w.fill) {
+      const uint32_t s = w.fill % w.stages, use = w.fill / w.stages;
+      if (!mbar_wait(w.empty + 8 * s, (use & 1u) ^ 1u, w.gave_up)) return;
+      if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, CG * bytes);
+      const uint32_t bar = w.lead_full + 8 * s, k = i * 64;
+      uint32_t dst = w.ring + s * w.stage_bytes;
+      for (uint32_t h = 0; h < 128; h += 64, dst += 8192)
+        tma_load_3d<CG>(dst, ma, a_mn ? ra + h : k, a_mn ? k : ra + h, t.b, bar);
+      for (uint32_t h = 0; h < b_rows; h += 64, dst += 8192)
+        tma_load_3d<CG>(dst, mb, b_mn ? rb + h : k, b_mn ? k : rb + h, t.b, bar);
+    }
+  }
+}
+
+template <int CG>
+__device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool b_mn) {
+  const uint32_t idesc = mma_desc(128 * CG, p.n, a_mn, b_mn);
+  const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
+  for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
+    const Tile t = tile_of<CG>(p, item);
+    if (t.none) continue;
+    const uint32_t a = w.acc & 1u;
+    if (!mbar_wait(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return;
+    tmem_fence_after();
+    const uint32_t d = w.tmem + a * kAccColumns;
+    for (uint32_t i = t.first; i < t.last; ++i, ++w.fill) {
+      const uint32_t s = w.fill % w.stages;
+      if (!mbar_wait(w.full + 8 * s, (w.fill / w.stages) & 1u, w.gave_up)) return;
+      tmem_fence_after();
+      const uint32_t sa = w.ring + s * w.stage_bytes, sb = sa + 128 * 128;
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        mma_f16<CG>(d, tile_desc(sa + k * step_a, 8192, 1024),
+                    tile_desc(sb + k * step_b, 8192, 1024), idesc, i > t.first || k > 0);
+      mma_commit<CG>(w.empty + 8 * s);
+    }
+    mma_commit<CG>(w.acc_full + 8 * a);
+    ++w.acc;
+  }
+}
+
+// 32 x 32 of a symmetric result in v (one row per lane): the diagonal to `diag`,
+// the rest as fp16 to `out` and, for a tile below the diagonal, to its mirror
+// image.
+__device__ __forceinline__ void write_symmetric(const float (&v)[32], uint32_t buf, uint32_t b,
+                                                uint32_t row0, uint32_t col, bool mirror,
+                                                const CUtensorMap* out) {
+  const uint32_t lane = lane_id();
+  uint32_t h[16];
+#pragma unroll
+  for (uint32_t i = 0; i < 16; ++i) h[i] = pack_half(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (uint32_t c = 0; c < 4; ++c)
+    sts128(buf + box_at(lane, c), make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]));
+  if (mirror) {
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2048 + box_at(i, lane >> 3) +
+                                                   (lane & 7u) * 2),
+                   "h"((uint16_t)(i & 1 ? h[i / 2] >> 16 : h[i / 2]))
+                   : "memory");
+  }
+  proxy_fence();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(out, buf, col, row0, b);
+    if (mirror) tma_store_3d(out, buf + 2048, row0, col, b);
+    tma_store_commit();
+  }
+}
+
+// The entry of v on the diagonal, if this lane has one: kept in *diag, zeroed in v.
+__device__ __forceinline__ void take_diagonal(float (&v)[32], uint32_t row, uint32_t col,
+                                              float scale, float* diag, uint32_t k) {
+#pragma unroll
+  for (uint32_t i = 0; i < 32; ++i)
+    if (row == col + i) {
+      if (row < k) diag[row] = v[i] * scale;
+      v[i] = 0.f;
+    }
+}
+
+template <int CG>
+__device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p,
+                              int kind, uint32_t step) {
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  const uint32_t quarter = warp & 3u, half = warp >> 2, chunks = p.n / 64;
+  const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
+  const bool reads = kind == kPoly || kind == kApply || kind == kLast;
+  for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
+    const Tile t = tile_of<CG>(p, item);
+    if (t.none) continue;
+    const uint32_t row0 = t.row0 + 128 * w.rank + 32 * quarter, row = row0 + lane;
+    const uint32_t tile_col = half * chunks * 32, col0 = t.col0 + tile_col;
+    uint32_t count = 0;  // of this warp's chunks, those that exist
+    if (row0 < p.rows && col0 < p.cols) count = min(chunks, (p.cols - col0 + 31) / 32);
+    const uint32_t turn0 = w.turn;
+    auto fetch = [&](uint32_t q) {  // what is added to chunk q
+      if (lane == 0) {
+        const uint32_t slot = kind == kLast ? 0 : (turn0 + q) & 1u;
+        const uint32_t dst = w.buf + slot * kStageBuf, bar = w.in_bar + 8 * slot;
+        tma_store_wait_read<0>();
+        const uint32_t c = col0 + 32 * q;
+        mbar_expect_tx(bar, kind == kPoly ? 2048 : 4096);
+        if (kind == kPoly) {
+          tma_load_3d<1>(dst, &m.s_out, c, row0, t.b, bar);
+        } else {
+          tma_load_3d<1>(dst, &m.x_out[step & 1], c, row0, t.b, bar);
+          tma_load_3d<1>(dst + 2048, &m.lo_out, c, row0, t.b, bar);
+        }
+      }
+    };
+    if (reads && count) fetch(0);
+    float row_diag = 0.f;  // s or p of this lane's row
+    if (kind == kPoly && row < p.rows) row_diag = __ldcg(a.diag_s + (uint64_t)t.b * a.k + row);
+    if (!a.tall && (kind == kApply || kind == kLast) && row < p.rows)
+      row_diag = __ldcg(a.diag_p + (uint64_t)t.b * a.k + row);
+
+    const uint32_t acc = w.acc & 1u;
+    if (!__all_sync(0xffffffffu,
+                    mbar_wait(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)))
+      return;
+    tmem_fence_after();
+    const uint32_t src = w.tmem + acc * kAccColumns + (quarter << 21) + tile_col;
+    if (kind == kPart) count = chunks;
+    for (uint32_t q = 0; q < count; ++q) {
+      const uint32_t col = col0 + 32 * q;
+      float v[32];
+      tmem_load32(src + 32 * q, v);
+      if (kind == kPart) {
+        tmem_load_wait(v);
+        float* o = a.part + ((uint64_t)(item * CG + w.rank) * p.n + tile_col + 32 * q) * 128 +
+                   quarter * 32 + lane;
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) o[i * 128] = v[i];
+        continue;
+      }
+      const uint32_t slot = kind == kLast ? 0 : w.turn & 1u;
+      const uint32_t buf = w.buf + slot * kStageBuf;
+      if (reads && kind != kLast && q + 1 < count) fetch(q + 1);
+      float other = 0.f;  // s or p of column col + lane
+      if (kind == kPoly && col + lane < p.cols)
+        other = __ldcg(a.diag_s + (uint64_t)t.b * a.k + col + lane);
+      if (a.tall && (kind == kApply || kind == kLast) && col + lane < p.cols)
+        other = __ldcg(a.diag_p + (uint64_t)t.b * a.k + col + lane);
+      tmem_load_wait(v);
+      if (reads) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(w.in_bar + 8 * slot, w.in_uses[slot] & 1u, w.gave_up)))
+          return;
+        ++w.in_uses[slot];
+      } else {
+        if (lane == 0) tma_store_wait_read<1>();
+        __syncwarp();
+      }
+
+      if (kind == kGram) {
+        const float f = kScaleS / (kScaleX * kScaleX);
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) v[i] *= f;
+        take_diagonal(v, row, col, 1.f / kScaleS, a.diag_s + (uint64_t)t.b * a.k, a.k);
+        write_symmetric(v, buf, t.b, row0, col, t.mirror, &m.s_out);
+      } else if (kind == kPoly) {
+        // P' = (b + c (s_i + s_j)) S' + c S' S' off the diagonal, p = b s + c s^2 + c S' S' on it
+        const float f = cc * kScaleP / (kScaleS * kScaleS);
+        const float r0 = (cb + cc * row_diag) * (kScaleP / kScaleS);
+        const float r1 = cc * (kScaleP / kScaleS);
+        const float on = (cb + cc * row_diag) * row_diag * kScaleP;
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint4 q4 = lds128(buf + box_at(lane, c));
+          const uint32_t words[4] = {q4.x, q4.y, q4.z, q4.w};
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const float2 s2 = unpack_half(words[e]);
+            const uint32_t i = 8 * c + 2 * e;
+            const float d0 = __shfl_sync(0xffffffffu, other, i);
+            const float d1 = __shfl_sync(0xffffffffu, other, i + 1);
+            v[i] = v[i] * f + (r0 + r1 * d0) * s2.x;
+            v[i + 1] = v[i + 1] * f + (r0 + r1 * d1) * s2.y;
+          }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i)
+          if (row == col + i) v[i] += on;
+        take_diagonal(v, row, col, 1.f / kScaleP, a.diag_p + (uint64_t)t.b * a.k, a.k);
+        __syncwarp();
+        write_symmetric(v, buf, t.b, row0, col, t.mirror, &m.p_out);
+      } else {
+        // X <- (a + p) X + P' X
+        const float f = 1.f / kScaleP;
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint4 h4 = lds128(buf + box_at(lane, c));
+          const uint4 l4 = lds128(buf + 2048 + box_at(lane, c));
+          const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+          for (uint32_t e = 0; e < 4; ++e) {
+            const float2 h2 = unpack_half(hw[e]), l2 = unpack_half(lw[e]);
+            const uint32_t i = 8 * c + 2 * e;
+            float d0 = row_diag, d1 = row_diag;
+            if (a.tall) {
+              d0 = __shfl_sync(0xffffffffu, other, i);
+              d1 = __shfl_sync(0xffffffffu, other, i + 1);
+            }
+            v[i] = v[i] * f + (ca + d0) * (h2.x + l2.x);
+            v[i + 1] = v[i + 1] * f + (ca + d1) * (h2.y + l2.y);
+          }
+        }
+        if (kind == kApply) {
+#pragma unroll
+          for (uint32_t c = 0; c < 4; ++c) {
+            uint32_t hw[4], lw[4];
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint32_t i = 8 * c + 2 * e;
+              hw[e] = pack_half(v[i], v[i + 1]);
+              const float2 back = unpack_half(hw[e]);
+              lw[e] = pack_half(v[i] - back.x, v[i + 1] - back.y);
+            }
+            sts128(buf + box_at(lane, c), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+            sts128(buf + 2048 + box_at(lane, c), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+          }
+          proxy_fence();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&m.x_out[(step + 1) & 1], buf, col, row0, t.b);
+            tma_store_3d(&m.lo_out, buf + 2048, col, row0, t.b);
+            tma_store_commit();
+          }
+        } else {
+          // turned in shared memory so that a warp writes a row's 32 elements at once,
+          // whatever the alignment of the caller's rows
+          proxy_fence();
+          __syncwarp();
+          if (q + 1 < count) fetch(q + 1);
+          const uint32_t st = w.buf + kStageBuf;
+          const float g = a.alpha / kScaleX;
+#pragma unroll
+          for (uint32_t i = 0; i < 32; ++i)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + lane * 128 + ((i ^ lane) << 2)),
+                         "f"(v[i] * g)
+                         : "memory");
+          __syncwarp();
+          if (col + lane < p.cols) {
+            const int64_t o0 = (int64_t)t.b * a.out_batch + (int64_t)row0 * a.out_stride + col +
+                               lane;
+            const uint32_t n_rows = min(32u, p.rows - row0);
+            for (uint32_t r0 = 0; r0 < n_rows; r0 += 8) {
+              float old[8];
+              if (a.weight) {
+#pragma unroll
+                for (uint32_t r = 0; r < 8; ++r)
+                  if (r0 + r < n_rows)
+                    old[r] = load_any(a.out, a.out_type, o0 + (int64_t)(r0 + r) * a.out_stride);
+              }
+#pragma unroll
+              for (uint32_t r = 0; r < 8; ++r) {
+                if (r0 + r >= n_rows) break;
+                float x;
+                asm volatile("ld.shared.f32 %0, [%1];"
+                             : "=f"(x)
+                             : "r"(st + (r0 + r) * 128 + ((lane ^ (r0 + r)) << 2))
+                             : "memory");
+                if (a.weight) x += a.keep * old[r];
+                const int64_t o = o0 + (int64_t)(r0 + r) * a.out_stride;
+                if (a.out_type == SPARCML_F32) static_cast<float*>(a.out)[o] = x;
+                else if (a.out_type == SPARCML_BF16)
+                  static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x);
+                else static_cast<__half*>(a.out)[o] = __float2half_rn(x);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+      ++w.turn;
+    }
+    tmem_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
+    ++w.acc;
+  }
+}
+
+// S from the partial tiles of a split product, in the order of the splits.
+template <int CG>
+__device__ void join_parts(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p) {
+  const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
+  const uint32_t across = p.n / 32, per = 4 * CG * across;
+  const uint32_t total = a.batch * p.tiles * per;
+  for (uint32_t u = blockIdx.x + gridDim.x * warp; u < total; u += gridDim.x * kWriters) {
+    const uint32_t tile = u / per, r = u % per / across, c = u % across;
+    const Tile t = tile_of<CG>(p, tile * p.splits);
+    const uint32_t row0 = t.row0 + 32 * r, col = t.col0 + 32 * c;
+    if (row0 >= p.rows || col >= p.cols) continue;
+    float v[32];
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
+    for (uint32_t s = 0; s < p.splits; ++s) {
+      const float* o = a.part +
+                       ((uint64_t)((tile * p.splits + s) * CG + r / 4) * p.n + 32 * c) * 128 +
+                       (r & 3u) * 32 + lane;
+#pragma unroll
+      for (uint32_t i = 0; i < 32; ++i) v[i] += __ldcg(o + i * 128);
+    }
+    const float f = kScaleS / (kScaleX * kScaleX);
+#pragma unroll
+    for (uint32_t i = 0; i < 32; ++i) v[i] *= f;
+    if (lane == 0) tma_store_wait_read<1>();
+    __syncwarp();
+    take_diagonal(v, row0 + lane, col, 1.f / kScaleS, a.diag_s + (uint64_t)t.b * a.k, a.k);
+    write_symmetric(v, w.buf + (w.turn & 1u) * kStageBuf, t.b, row0, col, t.mirror, &m.s_out);
+    ++w.turn;
+  }
+}
+
+// The scaled input as a pair of fp16. 2^12 / |U| is applied as two factors, each a
+// normal number, whatever the size of |U|.
+__device__ __forceinline__ void norm_factors(const GatherArgs& g, uint64_t b, float& f0,
+                                             float& f1) {
+  double t[3] = {0.0, 0.0, 0.0};
+  for (uint32_t k = lane_id(); k < g.blocks; k += 32)
+    for (int q = 0; q < 3; ++q) t[q] += (double)__ldcg(g.sums + (b * g.blocks + k) * 3 + q);
+  for (int d = 16; d > 0; d >>= 1)
+    for (int q = 0; q < 3; ++q) t[q] += __shfl_xor_sync(0xffffffffu, t[q], d);
+  const double norm = sqrt(t[0] * 0x1p-160 + t[1] + t[2] * 0x1p180);
+  if (!(norm < __longlong_as_double(0x7ff0000000000000ll))) {
+    f0 = f1 = __int_as_float(0x7fffffff);  // an inf or a NaN in U: all of X is NaN
+  } else if (norm > 0.0) {
+    int e;
+    const double mant = frexp(norm, &e);
+    f0 = ldexpf(1.f, -e / 2);
+    f1 = (float)(ldexp((double)kScaleX, -(e + -e / 2)) / mant);
+  } else {
+    f0 = f1 = 0.f;
+  }
+}
+
+__device__ void split_input(const StepArgs& a) {
+  const GatherArgs& g = a.g;
+  const uint64_t pieces = (g.n + kPiece - 1) / kPiece, total = (uint64_t)a.batch * g.m * pieces;
+  const uint64_t warps = (uint64_t)gridDim.x * (kThreads / 32);
+  const uint64_t id = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  // each warp takes a run of pieces, which lies in few matrices
+  const uint64_t end = total * (id + 1) / warps;
+  uint64_t u = total * id / warps, line = u / pieces, piece = u - line * pieces;
+  uint64_t b = line / g.m, r = line - b * g.m;
+  bool known = false;
+  float f0 = 0.f, f1 = 0.f;
+  for (; u < end; ++u) {
+    if (!known) norm_factors(g, b, f0, f1);
+    known = true;
+    const uint64_t c0 = piece * kPiece + lane_id() * 4;
+    float v[4][4], mo[4][4];
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + 128 * q;
+      load4(g.g, g.g_type, b * g.g_batch + r * g.g_stride + c, c, g.n, g.vec_g, v[q]);
+      if (g.mom)
+        load4(g.mom, SPARCML_F32, b * g.m_batch + r * g.m_stride + c, c, g.n, g.vec_m, mo[q]);
+    }
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint64_t c = c0 + 128 * q;
+      if (c >= g.n) continue;  // the row's padding takes what is left of the last four
+      uint32_t hw[2], lw[2];
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        float x[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = v[q][i + e];
+          if (g.mom) t = g.nesterov ? t + g.mu * mo[q][i + e] : mo[q][i + e];
+          x[e] = t * f0 * f1;
+        }
+        hw[i / 2] = pack_half(x[0], x[1]);
+        const float2 back = unpack_half(hw[i / 2]);
+        lw[i / 2] = pack_half(x[0] - back.x, x[1] - back.y);
+      }
+      *reinterpret_cast<uint2*>(a.hi + line * a.pitch + c) = make_uint2(hw[0], hw[1]);
+      *reinterpret_cast<uint2*>(a.lo + line * a.pitch + c) = make_uint2(lw[0], lw[1]);
+    }
+    if (++piece == pieces) {
+      piece = 0;
+      ++line;
+      if (++r == g.m) {
+        r = 0;
+        ++b;
+        known = false;
+      }
+    }
+  }
+}
+
+// Every block waits until all have come this far, and sees what they wrote. The
+// wait ends after a few seconds at worst.
+__device__ __forceinline__ void grid_turn(uint32_t* turns, uint32_t& turn, uint32_t* gave_up) {
+  proxy_fence();
+  __syncthreads();
+  ++turn;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    atomicAdd(turns, 1u);
+    if (*reinterpret_cast<volatile uint32_t*>(gave_up) == 0) {
+      const uint32_t want = turn * gridDim.x;
+      const uint64_t end = global_ns() + 4 * kWaitNs;
+      uint32_t polls = 0;
+      while ((int32_t)(*reinterpret_cast<volatile uint32_t*>(turns) - want) < 0) {
+        if ((++polls & 63u) == 0 && global_ns() > end) {
+          *gave_up = 1;
+          break;
+        }
+      }
+    }
+    __threadfence();
+  }
+  __syncthreads();
+  proxy_fence();
+}
+
+template <int CG>
+__global__ void __launch_bounds__(kThreads, 1)
+steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a) {
+  extern __shared__ uint8_t raw[];
+  __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 4 + 2 * kWriters];
+  __shared__ uint32_t tmem_slot, gave_up;
+  griddep_wait();
+  const uint32_t warp = threadIdx.x >> 5;
+  Worker<CG> w;
+  w.ring = (smem_addr(raw) + 1023u) & ~1023u;
+  const uint32_t widest = max(a.gram.n, max(a.poly.n, a.apply.n));
+  w.stage_bytes = 128 * 128 + widest / CG * 128;
+  w.stages = min(kMaxStages, kRingBytes / w.stage_bytes);
+  w.full = smem_addr(bars);
+  w.empty = w.full + 8 * kMaxStages;
+  w.acc_full = w.empty + 8 * kMaxStages;
+  w.acc_empty = w.acc_full + 16;
+  w.in_bar = w.acc_empty + 16 + 16 * (warp % kWriters);
+  w.buf = w.ring + kRingBytes + (warp % kWriters) * 2 * kStageBuf;
+  w.rank = CG == 1 ? 0 : cluster_rank();
+  w.cluster = blockIdx.x / CG;
+  w.clusters = gridDim.x / CG;
+  w.gave_up = &gave_up;
+  w.lead_full = CG == 1 ? w.full : cluster_addr(w.full, 0);
+  w.lead_acc_empty = cluster_addr(w.acc_empty, 0);
 
   if (threadIdx.x == 0) {
     gave_up = 0;
-    for (uint32_t s = 0; s < kStages; ++s) {
-      mbar_init(full + 8 * s, 1);
-      mbar_init(empty + 8 * s, 1);
+    for (uint32_t s = 0; s < kMaxStages; ++s) {
+      mbar_init(w.full + 8 * s, 1);
+      mbar_init(w.empty + 8 * s, 1);
     }
-    mbar_init(done, 1);
+    for (uint32_t s = 0; s < 2; ++s) {
+      mbar_init(w.acc_full + 8 * s, 1);
+      mbar_init(w.acc_empty + 8 * s, CG * kWriters);
+    }
+    for (uint32_t s = 0; s < 2 * kWriters; ++s) mbar_init(w.acc_empty + 16 + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 128;" ::"r"(
-                     smem_addr(&tmem_slot))
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  if (warp == kWriters) tmem_alloc<CG>(smem_addr(&tmem_slot), 2 * kAccColumns);
+  tmem_fence_before();
+  __syncthreads();
+  if (CG > 1) cluster_sync();
+  tmem_fence_after();
+  w.tmem = tmem_slot;
+
+  uint32_t turn = 0;
+  split_input(a);
+  grid_turn(a.g.turns, turn, &gave_up);
+  const bool tall = a.tall != 0;
+  bool leader = false;
+  if (warp >= kWriters) leader = elect_one();
+  for (uint32_t step = 0; step < a.steps; ++step) {
+    const CUtensorMap* x = &m.x_in[step & 1];
+#pragma unroll 1
+    for (uint32_t ph = 0; ph < 3; ++ph) {
+      const Product& p = ph == 0 ? a.gram : ph == 1 ? a.poly : a.apply;
+      const CUtensorMap* ma = ph == 0 ? x : ph == 1 ? &m.s_in : tall ? x : &m.p_in;
+      const CUtensorMap* mb = ph == 0 ? x : ph == 1 ? &m.s_in : tall ? &m.p_in : x;
+      const bool a_mn = ph == 0 && tall, b_mn = (ph == 0 && tall) || (ph == 2 && !tall);
+      const int kind = ph == 0   ? (p.splits > 1 ? kPart : kGram)
+                       : ph == 1 ? kPoly
+                                 : (step + 1 == a.steps ? kLast : kApply);
+      const bool stop = __any_sync(0xffffffffu, *w.gave_up != 0);
+      if (warp < kWriters) {
+        if (!stop) write_results(w, a, m, p, kind, step);
+        if (lane_id() == 0) tma_store_wait_all();
+      } else if (warp == kWriters) {
+        if (leader && !stop) load_operands(w, p, ma, mb, a_mn, b_mn);
+      } else if (w.rank == 0) {
+        if (leader && !stop) issue_products(w, p, a_mn, b_mn);
+      }
+      __syncwarp();
+      if (kind == kLast) break;
+      grid_turn(a.g.turns, turn, &gave_up);
+      if (kind == kPart) {
+        if (warp < kWriters) {
+          if (!__any_sync(0xffffffffu, *w.gave_up != 0)) join_parts(w, a, m, p);
+          if (lane_id() == 0) tma_store_wait_all();
+        }
+        __syncwarp();
+        grid_turn(a.g.turns, turn, &gave_up);
+      }
+    }
+  }
+  if (gave_up) {
+    // Nothing of this block may still be in flight when its memory goes: wait, again
+    // with a limit, for the loads and products that were begun.
+    volatile uint32_t alone = 0;
+    if (warp == kWriters && leader && w.rank == 0)  // a pair's loads all report to rank 0
+      for (uint32_t i = w.fill > w.stages ? w.fill - w.stages : 0; i < w.fill; ++i)
+        mbar_wait(w.full + 8 * (i % w.stages), (i / w.stages) & 1u, &alone);
+    if (warp == kWriters + 1 && leader && w.rank == 0) {
+      const uint32_t bar = w.acc_full + 8 * (w.acc & 1u);
+      mma_commit<CG>(bar);
+      mbar_wait(bar, (w.acc >> 1) & 1u, &alone);
+    }
+    __syncwarp();
+    if (threadIdx.x == 0) set_status(a.status, SPARCML_ERR_TIMEOUT);
   }
   tmem_fence_before();
   __syncthreads();
+  if (CG > 1) cluster_sync();
   tmem_fence_after();
-  const uint32_t tmem = tmem_slot;
-  const uint32_t steps = (p.depth + kDepth - 1) / kDepth;
-  griddep_wait();
-
-  if (warp == 0) {
-    if (elect_one()) {
-      uint32_t issued = 0;
-      for (uint32_t i = 0; i < steps; ++i) {
-        const uint32_t s = i % kStages;
-        if (i >= kStages && !mbar_wait(empty + 8 * s, ((i / kStages) & 1u) ^ 1u, &gave_up)) break;
-        mbar_expect_tx(full + 8 * s, kStageBytes);
-        load_operand<A_MN>(base + s * kStageBytes, &map_a, row0, i * kDepth, b, full + 8 * s);
-        load_operand<B_MN>(base + s * kStageBytes + kOperandBytes, &map_b, col0, i * kDepth, b,
-                           full + 8 * s);
-        ++issued;
-      }
-      // nothing of this block may still be in flight when it ends
-      if (gave_up) {
-        volatile uint32_t alone = 0;
-        for (uint32_t i = issued > kStages ? issued - kStages : 0; i < issued; ++i)
-          mbar_wait(full + 8 * (i % kStages), (i / kStages) & 1u, &alone);
-      }
-    }
-  } else if (warp == 1) {
-    if (elect_one()) {
-      constexpr uint32_t idesc = mma_desc(kTile, kTile, A_MN, B_MN);
-      for (uint32_t i = 0; i < steps; ++i) {
-        const uint32_t s = i % kStages;
-        if (!mbar_wait(full + 8 * s, (i / kStages) & 1u, &gave_up)) break;
-        tmem_fence_after();
-        const uint32_t sa = base + s * kStageBytes, sb = sa + kOperandBytes;
-#pragma unroll
-        for (uint32_t k = 0; k < kDepth / 16; ++k) {
-          const uint64_t da = operand_desc<A_MN>(sa, k), db = operand_desc<B_MN>(sb, k);
-          const uint32_t add = i > 0 || k > 0;
-          asm volatile(
-              "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
-              "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n\t}" ::"r"(tmem),
-              "l"(da), "l"(db), "r"(idesc), "r"(add)
-              : "memory");
-        }
-        asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                empty + 8 * s)
-            : "memory");
-      }
-      asm volatile(
-          "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(done)
-          : "memory");
-      if (gave_up) {  // tensor memory is freed below: no product may still run then
-        volatile uint32_t alone = 0;
-        mbar_wait(done, 0, &alone);
-      }
-    }
-  } else if (__all_sync(0xffffffffu, mbar_wait(done, 0, &gave_up))) {
-    tmem_fence_after();
-    const uint32_t quarter = warp & 3u, lane = lane_id();
-    const uint32_t row = row0 + quarter * 32 + lane;
-    const uint64_t line = ((uint64_t)b * p.rows + row) * p.pitch;
-    for (uint32_t c0 = 0; c0 < kTile; c0 += 32) {
-      const uint32_t col = col0 + c0;
-      if (col >= p.cols) break;
-      float v[32];
-      tmem_load32(tmem + (quarter << 21) + c0, v);
-      tmem_load_wait();
-#pragma unroll
-      for (uint32_t i = 0; i < 32; ++i) v[i] *= p.alpha;
-      if (EPI != kGram && row < p.rows) {
-        if (EPI == kPoly) {
-#pragma unroll
-          for (uint32_t i = 0; i < 32; ++i)
-            if (col + i < p.cols) v[i] += p.beta * __half2float(p.in_hi[line + col + i]);
-        } else {
-#pragma unroll
-          for (uint32_t i = 0; i < 32; ++i)
-            if (col + i < p.cols)
-              v[i] += p.beta * (__half2float(p.in_hi[line + col + i]) +
-                                __half2float(p.lo[line + col + i]));
-        }
-      }
-      if (EPI == kGram || EPI == kPoly) {
-#pragma unroll
-        for (uint32_t i = 0; i < 32; ++i) {
-          const __half h = __float2half_rn(v[i]);
-          if (row < p.rows && col + i < p.cols) {
-            p.out_hi[line + col + i] = h;
-            if (ti != tj)
-              p.out_hi[((uint64_t)b * p.rows + col + i) * p.pitch + row] = h;
-          }
-        }
-      } else if (row < p.rows) {
-#pragma unroll
-        for (uint32_t i = 0; i < 32; ++i) {
-          if (col + i >= p.cols) continue;
-          if (EPI == kApply) {
-            const __half h = __float2half_rn(v[i]);
-            p.out_hi[line + col + i] = h;
-            p.lo[line + col + i] = __float2half_rn(v[i] - __half2float(h));
-          } else {
-            const int64_t o = (int64_t)b * p.out_batch + (int64_t)row * p.out_stride + col + i;
-            float r = v[i];
-            if (EPI == kWeight) r += p.keep * load_any(p.out, p.out_type, o);
-            if (p.out_type == SPARCML_F32) static_cast<float*>(p.out)[o] = r;
-            else if (p.out_type == SPARCML_BF16)
-              static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16_rn(r);
-            else static_cast<__half*>(p.out)[o] = __float2half_rn(r);
-          }
-        }
-      }
-    }
-    tmem_fence_before();
-  }
-  __syncthreads();
-  if (threadIdx.x == 0 && gave_up) set_status(p.status, SPARCML_ERR_TIMEOUT);
-  if (warp == 0) {
-    __syncwarp();
-    tmem_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 128;" ::"r"(tmem));
-  }
+  if (warp == kWriters) tmem_free<CG>(w.tmem, 2 * kAccColumns);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,24 +844,69 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// fp16 [batch][rows][pitch], of which `cols` columns exist; boxes of 64 x 64.
+// fp16 [batch][rows][pitch], of which `cols` columns exist; boxes of box x box.
 bool make_map(CUtensorMap* map, const void* p, uint64_t batch, uint64_t rows, uint64_t cols,
-              uint64_t pitch) {
+              uint64_t pitch, uint32_t box) {
   const EncodeTiled fn = encode_tiled();
   if (!fn) return false;
   const cuuint64_t dims[3] = {cols, rows, batch};
   const cuuint64_t strides[2] = {pitch * 2, rows * pitch * 2};
-  const cuuint32_t box[3] = {64, 64, 1}, step[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, box, step,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t size[3] = {box, box, 1}, step[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, size,
+            step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+constexpr uint32_t kSms = 152;
+
 struct Plan {
-  uint64_t batch, m, n, k, pitch, kpitch;
-  uint32_t blocks;
-  size_t sums, hi0, hi1, lo, s, p, bytes;
+  uint64_t batch, m, n, k, l, pitch, kpitch;
+  uint32_t blocks;  // of the norm, per matrix
+  uint32_t pair;    // blocks that share a tile: 1 or 2
+  Product gram, poly, apply;
+  size_t sums, hi0, hi1, lo, s, p, ds, dp, part, bytes;
 };
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+// Tiles of a product and the time of its slowest worker, in products of 64 x 64 x 64.
+Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t depth, bool symmetric,
+                      uint32_t pair, uint32_t n, bool may_split, double* time) {
+  Product p = {};
+  const uint64_t workers = kSms / pair, tr = ceil_div(rows, 128 * pair), tc = ceil_div(cols, n);
+  const uint64_t ratio = 128 * pair / n ? 128 * pair / n : 1;
+  p.n = n;
+  p.rows = (uint32_t)rows;
+  p.cols = (uint32_t)cols;
+  p.blocks = (uint32_t)ceil_div(depth, 64);
+  p.tile_rows = symmetric ? 0 : (uint32_t)tr;
+  const uint64_t tiles = symmetric ? ratio * tr * (tr + 1) / 2 : tr * tc;
+  p.tiles = (uint32_t)tiles;
+  p.splits = 1;
+  if (may_split && tiles * batch * 2 <= workers && p.blocks >= 16)
+    p.splits = (uint32_t)std::min<uint64_t>(workers / (tiles * batch), p.blocks / 8);
+  const uint64_t items = tiles * batch * p.splits;
+  p.items = items > 0xffffffffull ? 0 : (uint32_t)items;
+  *time = (double)ceil_div(items, workers) * ((double)ceil_div(p.blocks, p.splits) * (n / 64.0) +
+                                              4.0 + n / 32.0);
+  return p;
+}
+
+Product best_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t depth, bool symmetric,
+                     uint32_t pair, bool may_split, double* best) {
+  Product p = {};
+  *best = 0;
+  for (uint32_t n = 64 * pair; n <= 128 * pair; n *= 2) {
+    double t;
+    const Product q = shape_product(batch, rows, cols, depth, symmetric, pair, n, may_split, &t);
+    if (n == 64 * pair || t <= *best) {
+      p = q;
+      *best = t;
+    }
+  }
+  return p;
+}
 
 bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   if (batch < 0 || batch > 65535 || m < 1 || n < 1 || m > (1u << 24) || n > (1u << 24) ||
@@ -396,117 +916,128 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   q.m = m;
   q.n = n;
   q.k = std::min(m, n);
+  q.l = std::max(m, n);
   q.pitch = align_up(n, 64);
   q.kpitch = align_up(q.k, 64);
-  q.blocks = (uint32_t)std::min<uint64_t>((m * n + 4095) / 4096, 152 * 4);
-  const size_t x = align_up(q.batch * m * q.pitch * 2, 256);
-  const size_t s = align_up(q.batch * q.k * q.kpitch * 2, 256);
+  q.blocks = (uint32_t)std::min<uint64_t>(ceil_div(m * ceil_div(n, kPiece), 8), kSms * 4);
+  double best = 0;
+  for (uint32_t pair = 1; pair <= 2; ++pair) {
+    double t[3];
+    const Product g = best_product(batch, q.k, q.k, q.l, true, pair, true, &t[0]);
+    const Product p = best_product(batch, q.k, q.k, q.k, true, pair, false, &t[1]);
+    const Product a = best_product(batch, m, n, q.k, false, pair, false, &t[2]);
+    const double sum = t[0] + t[1] + t[2];
+    if (pair == 1 || sum <= best) {
+      best = sum;
+      q.pair = pair;
+      q.gram = g;
+      q.poly = p;
+      q.apply = a;
+    }
+  }
+  if (batch && (!q.gram.items || !q.poly.items || !q.apply.items)) return false;
+  const size_t x = q.batch * m * q.pitch * 2, s = q.batch * q.k * q.kpitch * 2;
   size_t at = 256;
-  auto take = [&](size_t bytes) { const size_t o = at; at += align_up(bytes, 256); return o; };
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += align_up(bytes, 256);
+    return o;
+  };
   q.sums = take(q.batch * q.blocks * 3 * sizeof(float));
   q.hi0 = take(x);
   q.hi1 = take(x);
   q.lo = take(x);
   q.s = take(s);
   q.p = take(s);
+  q.ds = take(q.batch * q.k * sizeof(float));
+  q.dp = take(q.batch * q.k * sizeof(float));
+  q.part = take(q.gram.splits > 1
+                    ? (size_t)q.gram.items * q.pair * 128 * q.gram.n * sizeof(float) : 0);
   q.bytes = at;
   return true;
 }
 
-template <bool A_MN, bool B_MN, int EPI>
-bool launch_product(const CUtensorMap& a, const CUtensorMap& b, ProductArgs p, uint64_t batch,
-                    bool symmetric, cudaStream_t s) {
-  auto kernel = product_kernel<A_MN, B_MN, EPI>;
-  if (!ensure_smem(reinterpret_cast<const void*>(kernel), kProductSmem)) return false;
-  const uint64_t tr = (p.rows + kTile - 1) / kTile, tc = (p.cols + kTile - 1) / kTile;
-  p.tile_cols = symmetric ? 0 : (uint32_t)tc;
-  p.tiles = (uint32_t)(symmetric ? tr * (tr + 1) / 2 : tr * tc);
-  if (p.tiles * batch > 0x7fffffffull) return false;
-  launch_pdl(kernel, (unsigned)(p.tiles * batch), 192, kProductSmem, s, a, b, p);
-  return true;
-}
-
 struct Target {  // where the result goes
-  int epilogue;  // kOrthogonal or kWeight
+  bool weight;
   void* out;
   int32_t type;
   int64_t batch, stride;
   float alpha, keep;
 };
 
+template <int CG>
+int launch_steps(const Maps& m, const StepArgs& a, cudaStream_t s) {
+  auto kernel = steps_kernel<CG>;
+  if (!ensure_smem(reinterpret_cast<const void*>(kernel), kStepsSmem)) return SPARCML_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSms);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kStepsSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeCooperative;  // all blocks run at one time
+  attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = CG;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  (void)cudaLaunchKernelEx(&cfg, kernel, m, a);
+  return launch_status();
+}
+
 int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs, int32_t steps,
               void* ws, cudaStream_t s) {
   char* w = static_cast<char*>(ws);
-  __half* hi[2] = {reinterpret_cast<__half*>(w + q.hi0), reinterpret_cast<__half*>(w + q.hi1)};
-  __half* lo = reinterpret_cast<__half*>(w + q.lo);
-  __half* gram = reinterpret_cast<__half*>(w + q.s);
-  __half* poly = reinterpret_cast<__half*>(w + q.p);
-  CUtensorMap map_x[2], map_s, map_p;
-  if (!make_map(&map_x[0], hi[0], q.batch, q.m, q.n, q.pitch) ||
-      !make_map(&map_x[1], hi[1], q.batch, q.m, q.n, q.pitch) ||
-      !make_map(&map_s, gram, q.batch, q.k, q.k, q.kpitch) ||
-      !make_map(&map_p, poly, q.batch, q.k, q.k, q.kpitch))
+  char *hi0 = w + q.hi0, *hi1 = w + q.hi1, *lo = w + q.lo, *sm = w + q.s, *pm = w + q.p;
+  Maps m;
+  if (!make_map(&m.x_in[0], hi0, q.batch, q.m, q.n, q.pitch, 64) ||
+      !make_map(&m.x_in[1], hi1, q.batch, q.m, q.n, q.pitch, 64) ||
+      !make_map(&m.s_in, sm, q.batch, q.k, q.k, q.kpitch, 64) ||
+      !make_map(&m.p_in, pm, q.batch, q.k, q.k, q.kpitch, 64) ||
+      !make_map(&m.x_out[0], hi0, q.batch, q.m, q.n, q.pitch, 32) ||
+      !make_map(&m.x_out[1], hi1, q.batch, q.m, q.n, q.pitch, 32) ||
+      !make_map(&m.lo_out, lo, q.batch, q.m, q.n, q.pitch, 32) ||
+      !make_map(&m.s_out, sm, q.batch, q.k, q.k, q.kpitch, 32) ||
+      !make_map(&m.p_out, pm, q.batch, q.k, q.k, q.kpitch, 32))
     return SPARCML_ERR_CUDA;
+  const int64_t ge = g.g_type == SPARCML_F32 ? 16 : 8;
+  g.vec_g = aligned_to(g.g, ge) && g.g_batch % 4 == 0 && g.g_stride % 4 == 0;
+  g.vec_m = aligned_to(g.mom, 16) && g.m_batch % 4 == 0 && g.m_stride % 4 == 0;
   g.m = q.m;
   g.n = q.n;
   g.blocks = q.blocks;
   g.sums = reinterpret_cast<float*>(w + q.sums);
-  g.hi = hi[0];
-  g.lo = lo;
-  g.pitch = q.pitch;
-  const dim3 grid(q.blocks, (unsigned)q.batch);
-  launch_pdl(gather_norm_kernel, grid, 256, 0, s, g);
-  launch_pdl(split_kernel, grid, 256, 0, s, g);
-  const bool tall = q.m > q.n;
-  const uint32_t k = (uint32_t)q.k, l = (uint32_t)std::max(q.m, q.n);
-  int32_t* status = reinterpret_cast<int32_t*>(w);
-  bool ok = true;
-  for (int32_t i = 0; i < steps && ok; ++i) {
-    const float ca = coeffs[3 * i], cb = coeffs[3 * i + 1], cc = coeffs[3 * i + 2];
-    const CUtensorMap& x = map_x[i & 1];
-    ProductArgs p = {};
-    p.status = status;
-    p.rows = p.cols = k;
-    p.depth = l;
-    p.pitch = q.kpitch;
-    p.alpha = kScaleS / (kScaleX * kScaleX);
-    p.out_hi = gram;
-    ok = tall ? launch_product<true, true, kGram>(x, x, p, q.batch, true, s)
-              : launch_product<false, false, kGram>(x, x, p, q.batch, true, s);
-    p.depth = k;
-    p.alpha = cc * kScaleP / (kScaleS * kScaleS);
-    p.beta = cb * kScaleP / kScaleS;
-    p.in_hi = gram;
-    p.out_hi = poly;
-    ok = ok && launch_product<false, false, kPoly>(map_s, map_s, p, q.batch, true, s);
-    p.rows = (uint32_t)q.m;
-    p.cols = (uint32_t)q.n;
-    p.pitch = q.pitch;
-    p.in_hi = hi[i & 1];
-    p.lo = lo;
-    p.out_hi = hi[(i + 1) & 1];
-    const bool last = i + 1 == steps;
-    const float f = last ? to.alpha / kScaleX : 1.f;
-    p.alpha = f / kScaleP;
-    p.beta = f * ca;
-    p.out = to.out;
-    p.out_type = to.type;
-    p.out_batch = to.batch;
-    p.out_stride = to.stride;
-    p.keep = to.keep;
-    const CUtensorMap& first = tall ? x : map_p;
-    const CUtensorMap& second = tall ? map_p : x;
-    auto apply = [&](auto epi) {
-      constexpr int E = decltype(epi)::value;
-      return tall ? launch_product<false, false, E>(first, second, p, q.batch, false, s)
-                  : launch_product<false, true, E>(first, second, p, q.batch, false, s);
-    };
-    ok = ok && (!last ? apply(std::integral_constant<int, kApply>{})
-                : to.epilogue == kWeight ? apply(std::integral_constant<int, kWeight>{})
-                                         : apply(std::integral_constant<int, kOrthogonal>{}));
-  }
-  if (launch_status() != SPARCML_OK || !ok) return SPARCML_ERR_CUDA;
-  note_launches(2 + 3 * steps);
+  g.turns = reinterpret_cast<uint32_t*>(w + 128);
+  StepArgs a = {};
+  a.g = g;
+  a.batch = (uint32_t)q.batch;
+  a.steps = (uint32_t)steps;
+  a.tall = q.m > q.n;
+  a.gram = q.gram;
+  a.poly = q.poly;
+  a.apply = q.apply;
+  std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
+  a.hi = reinterpret_cast<__half*>(hi0);
+  a.lo = reinterpret_cast<__half*>(lo);
+  a.pitch = q.pitch;
+  a.diag_s = reinterpret_cast<float*>(w + q.ds);
+  a.diag_p = reinterpret_cast<float*>(w + q.dp);
+  a.part = reinterpret_cast<float*>(w + q.part);
+  a.k = (uint32_t)q.k;
+  a.weight = to.weight;
+  a.out = to.out;
+  a.out_type = to.type;
+  a.out_batch = to.batch;
+  a.out_stride = to.stride;
+  a.alpha = to.alpha;
+  a.keep = to.keep;
+  a.status = reinterpret_cast<int32_t*>(w);
+  launch_pdl(gather_norm_kernel, dim3(q.blocks, (unsigned)q.batch), 256, 0, s, g);
+  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  const int r = q.pair == 1 ? launch_steps<1>(m, a, s) : launch_steps<2>(m, a, s);
+  if (r != SPARCML_OK) return r;
+  note_launches(2);
   return SPARCML_OK;
 }
 
@@ -560,7 +1091,7 @@ extern "C" int sparcml_orthogonalize(const void* g, int32_t g_type, int64_t g_ba
   a.g_type = g_type;
   a.g_batch = g_batch_stride;
   a.g_stride = g_stride;
-  const Target to{kOrthogonal, out, out_type, out_batch_stride, out_stride, 1.f, 0.f};
+  const Target to{false, out, out_type, out_batch_stride, out_stride, 1.f, 0.f};
   return run_steps(a, q, to, coeffs, steps, ws, static_cast<cudaStream_t>(stream));
 }
 
@@ -594,7 +1125,7 @@ extern "C" int sparcml_muon_step(void* weight, int32_t w_type, int64_t w_batch_s
   a.m_stride = m_stride;
   a.mu = mu;
   a.nesterov = nesterov;
-  const Target to{kWeight,  weight,      w_type, w_batch_stride,
+  const Target to{true,     weight,      w_type, w_batch_stride,
                   w_stride, -lr * scale, 1.f - lr * weight_decay};
   return run_steps(a, q, to, coeffs, steps, ws, static_cast<cudaStream_t>(stream));
 }
