@@ -176,9 +176,9 @@ struct Product {       // one product of a step, of every matrix of the batch
 };
 
 struct Maps {
-  // operands are read in boxes of 64 x 64, 128-byte swizzled; results and what is
-  // added to them move in boxes of 32 x 32, 64-byte swizzled
-  CUtensorMap x_in[2], s_in, p_in, x_out[2], lo_out, s_out, p_out;
+  // operands are read in boxes of 64 x 64, 128-byte swizzled; what is added to the
+  // products in boxes of 32 x 32, 64-byte swizzled
+  CUtensorMap x_in[2], s_in, p_in, x_out[2], lo_out, s_out;
 };
 
 struct StepArgs {
@@ -186,9 +186,11 @@ struct StepArgs {
   uint32_t batch, steps, tall;
   Product gram, poly, apply;
   float coeffs[3 * kMaxSteps];
-  __half* hi;  // [batch][m][pitch]
+  __half* hi[2];  // [batch][m][pitch]
   __half* lo;
-  uint64_t pitch;
+  __half* s;  // [batch][k][kpitch]
+  __half* p;
+  uint64_t pitch, kpitch;
   float* diag_s;  // [batch][k]
   float* diag_p;
   float* part;  // partial tiles of a split product
@@ -275,15 +277,22 @@ __device__ __forceinline__ float2 unpack_half(uint32_t v) {
 // The state of one block.
 template <int CG>
 struct Worker {
+  __device__ __forceinline__ void next_stage() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+
   uint32_t ring, stages, stage_bytes;      // operand ring
   uint32_t full, empty, acc_full, acc_empty, in_bar;  // barriers
   uint32_t lead_full, lead_acc_empty;      // the same of the pair's first block
   uint32_t buf;                            // this writer's two buffers
   uint32_t rank, cluster, clusters, tmem;
   volatile uint32_t* gave_up;
-  uint32_t fill = 0;      // operand stages used so far (loader, issuer)
+  uint32_t stage = 0, phase = 0;  // next operand stage and its turn's parity (loader, issuer)
   uint32_t acc = 0;       // accumulators used so far (issuer, writers)
-  uint32_t in_uses[2] = {0, 0};
+  uint32_t in_phase = 0;  // bit s: parity of buffer s's next load
   uint32_t turn = 0;      // chunks written so far
 };
 
@@ -291,13 +300,14 @@ template <int CG>
 __device__ void load_operands(Worker<CG>& w, const Product& p, const CUtensorMap* ma,
                               const CUtensorMap* mb, bool a_mn, bool b_mn) {
   const uint32_t b_rows = p.n / CG, bytes = 128 * 128 + b_rows * 128;
+  proxy_fence();  // the other blocks' results, read by asynchronous copies
   for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
     const Tile t = tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t ra = t.row0 + 128 * w.rank, rb = t.col0 + b_rows * w.rank;
-    for (uint32_t i = t.first; i < t.last; ++i, ++w.fill) {
-      const uint32_t s = w.fill % w.stages, use = w.fill / w.stages;
-      if (!mbar_wait(w.empty + 8 * s, (use & 1u) ^ 1u, w.gave_up)) return;
+    for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
+      const uint32_t s = w.stage;
+      if (!mbar_wait(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return;
       if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, CG * bytes);
       const uint32_t bar = w.lead_full + 8 * s, k = i * 64;
       uint32_t dst = w.ring + s * w.stage_bytes;
@@ -320,9 +330,9 @@ __device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool 
     if (!mbar_wait(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return;
     tmem_fence_after();
     const uint32_t d = w.tmem + a * kAccColumns;
-    for (uint32_t i = t.first; i < t.last; ++i, ++w.fill) {
-      const uint32_t s = w.fill % w.stages;
-      if (!mbar_wait(w.full + 8 * s, (w.fill / w.stages) & 1u, w.gave_up)) return;
+    for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
+      const uint32_t s = w.stage;
+      if (!mbar_wait(w.full + 8 * s, w.phase, w.gave_up)) return;
       tmem_fence_after();
       const uint32_t sa = w.ring + s * w.stage_bytes, sb = sa + 128 * 128;
 #pragma unroll
@@ -336,45 +346,144 @@ __device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool 
   }
 }
 
-// 32 x 32 of a symmetric result in v (one row per lane): the diagonal to `diag`,
-// the rest as fp16 to `out` and, for a tile below the diagonal, to its mirror
-// image.
-__device__ __forceinline__ void write_symmetric(const float (&v)[32], uint32_t buf, uint32_t b,
-                                                uint32_t row0, uint32_t col, bool mirror,
-                                                const CUtensorMap* out) {
+// A 32 x 32 fp16 box in shared memory to rows [row0, row0 + 32) below `rows`, from column
+// col, of a matrix whose padded rows hold whole boxes: eight rows of 64 bytes at a
+// time. (A TMA store of such a box takes over a microsecond when all SMs issue them:
+// 4096 x 4096 took 2.4 ms with it.)
+__device__ __forceinline__ void store_box(uint32_t box, __half* out, uint64_t pitch, uint32_t row0,
+                                          uint32_t rows, uint32_t col) {
+  const uint32_t lane = lane_id(), r = lane >> 2, c = lane & 3u;
+  __half* o = out + (uint64_t)(row0 + r) * pitch + col + 8 * c;
+#pragma unroll
+  for (uint32_t q = 0; q < 32; q += 8, o += 8 * pitch)
+    if (row0 + q + r < rows) *reinterpret_cast<uint4*>(o) = lds128(box + box_at(q + r, c));
+}
+
+// What becomes of a product's entry, for all products alike:
+//     r = f acc + (r0 + r1 d_j) in_ij
+// with d the diagonal vector of column j, and in what stands at that place:
+//     S = X X'                                    (nothing)
+//     P' = c S' S' + (b + c s_i + c s_j) S'       S', rows' s in r0, columns' s by r1
+//     X <- P' X + (a + p_i) X                     hi + lo; p_i in r0
+//     X <- X P' + (a + p_j) X                     (tall) hi + lo; p_j by r1
+// and on the diagonal of S and P the sum goes to an fp32 vector, with `on` added.
+struct Rule {
+  float f, r0, r1, on, diag_scale;
+  float* diag;   // this matrix's, or null
+  __half* out;   // this matrix's
+  __half* low;   // X: the lower half of the pair
+  uint64_t pitch;
+  uint32_t rows;  // of out
+};
+
+// Eight columns from column 8 c of the 32 x 32 box: v holds this lane's row.
+__device__ __forceinline__ void finish8(float (&v)[8], uint32_t c, uint32_t buf, bool reads,
+                                        bool pairs, float other, const Rule& u, bool on_diag,
+                                        uint32_t row) {
   const uint32_t lane = lane_id();
-  uint32_t h[16];
 #pragma unroll
-  for (uint32_t i = 0; i < 16; ++i) h[i] = pack_half(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 8; ++i) v[i] *= u.f;
+  if (reads) {
+    const uint4 h4 = lds128(buf + box_at(lane, c));
+    uint4 l4 = make_uint4(0, 0, 0, 0);
+    if (pairs) l4 = lds128(buf + 2048 + box_at(lane, c));
+    const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-  for (uint32_t c = 0; c < 4; ++c)
-    sts128(buf + box_at(lane, c), make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]));
-  if (mirror) {
-#pragma unroll
-    for (uint32_t i = 0; i < 32; ++i)
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2048 + box_at(i, lane >> 3) +
-                                                   (lane & 7u) * 2),
-                   "h"((uint16_t)(i & 1 ? h[i / 2] >> 16 : h[i / 2]))
-                   : "memory");
+    for (int e = 0; e < 4; ++e) {
+      const float2 h2 = unpack_half(hw[e]), l2 = unpack_half(lw[e]);
+      const float d0 = __shfl_sync(0xffffffffu, other, 8 * c + 2 * e);
+      const float d1 = __shfl_sync(0xffffffffu, other, 8 * c + 2 * e + 1);
+      v[2 * e] += (u.r0 + u.r1 * d0) * (h2.x + l2.x);
+      v[2 * e + 1] += (u.r0 + u.r1 * d1) * (h2.y + l2.y);
+    }
   }
-  proxy_fence();
-  __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(out, buf, col, row0, b);
-    if (mirror) tma_store_3d(out, buf + 2048, row0, col, b);
-    tma_store_commit();
+  if (on_diag) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (lane == 8 * c + i) {
+        if (row < u.rows) u.diag[row] = (v[i] + u.on) * u.diag_scale;
+        v[i] = 0.f;
+      }
   }
 }
 
-// The entry of v on the diagonal, if this lane has one: kept in *diag, zeroed in v.
-__device__ __forceinline__ void take_diagonal(float (&v)[32], uint32_t row, uint32_t col,
-                                              float scale, float* diag, uint32_t k) {
+// The eight results as fp16 (and what that rounding left, for a pair) into the box, and
+// into the box of its mirror image.
+__device__ __forceinline__ void stage8(const float (&v)[8], uint32_t c, uint32_t buf, bool pairs,
+                                       bool mirror) {
+  const uint32_t lane = lane_id();
+  uint32_t hw[4], lw[4];
 #pragma unroll
-  for (uint32_t i = 0; i < 32; ++i)
-    if (row == col + i) {
-      if (row < k) diag[row] = v[i] * scale;
-      v[i] = 0.f;
+  for (int e = 0; e < 4; ++e) hw[e] = pack_half(v[2 * e], v[2 * e + 1]);
+  sts128(buf + box_at(lane, c), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+  if (pairs) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 back = unpack_half(hw[e]);
+      lw[e] = pack_half(v[2 * e] - back.x, v[2 * e + 1] - back.y);
     }
+    sts128(buf + 2048 + box_at(lane, c), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+  } else if (mirror) {
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2048 + box_at(8 * c + i, lane >> 3) +
+                                                   (lane & 7u) * 2),
+                   "h"((uint16_t)(i & 1 ? hw[i / 2] >> 16 : hw[i / 2]))
+                   : "memory");
+  }
+}
+
+__device__ __forceinline__ void store_boxes(uint32_t buf, const Rule& u, uint32_t row0,
+                                            uint32_t col, bool pairs, bool mirror) {
+  __syncwarp();
+  store_box(buf, u.out, u.pitch, row0, u.rows, col);
+  if (pairs) store_box(buf + 2048, u.low, u.pitch, row0, u.rows, col);
+  if (mirror) store_box(buf + 2048, u.out, u.pitch, col, u.rows, row0);
+  proxy_fence_shared();  // the buffer's next load is an asynchronous copy
+  __syncwarp();
+}
+
+__device__ __forceinline__ Rule gram_rule(const StepArgs& a, uint32_t b) {
+  return {kScaleS / (kScaleX * kScaleX), 0.f, 0.f, 0.f, 1.f / kScaleS,
+          a.diag_s + (uint64_t)b * a.k, a.s + (uint64_t)b * a.k * a.kpitch, nullptr, a.kpitch,
+          a.k};
+}
+
+// The last step's 32 x 32 results, turned in shared memory (`box`: 4 KB) so that a warp
+// writes 32 elements of a row at once, whatever the alignment of the caller's rows.
+__device__ __forceinline__ void store_result(const StepArgs& a, uint32_t box, uint32_t b,
+                                             uint32_t row0, uint32_t rows, uint32_t col,
+                                             uint32_t cols) {
+  const uint32_t lane = lane_id();
+  __syncwarp();
+  if (col + lane < cols) {
+    const int64_t o0 = (int64_t)b * a.out_batch + (int64_t)row0 * a.out_stride + col + lane;
+    const uint32_t n = min(32u, rows - row0);
+    for (uint32_t r0 = 0; r0 < n; r0 += 8) {
+      float old[8];
+#pragma unroll
+      for (uint32_t r = 0; r < 8; ++r)
+        old[r] = a.weight && r0 + r < n
+                     ? load_any(a.out, a.out_type, o0 + (int64_t)(r0 + r) * a.out_stride)
+                     : 0.f;
+#pragma unroll
+      for (uint32_t r = 0; r < 8; ++r) {
+        if (r0 + r >= n) break;
+        float x;
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(x)
+                     : "r"(box + (r0 + r) * 128 + ((lane ^ (r0 + r)) << 2))
+                     : "memory");
+        if (a.weight) x += a.keep * old[r];
+        const int64_t o = o0 + (int64_t)(r0 + r) * a.out_stride;
+        if (a.out_type == SPARCML_F32) static_cast<float*>(a.out)[o] = x;
+        else if (a.out_type == SPARCML_BF16)
+          static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x);
+        else static_cast<__half*>(a.out)[o] = __float2half_rn(x);
+      }
+    }
+  }
+  __syncwarp();
 }
 
 template <int CG>
@@ -383,7 +492,8 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t quarter = warp & 3u, half = warp >> 2, chunks = p.n / 64;
   const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
-  const bool reads = kind == kPoly || kind == kApply || kind == kLast;
+  const bool pairs = kind == kApply || kind == kLast, reads = kind == kPoly || pairs;
+  if (reads) proxy_fence();  // the other blocks' results, read by asynchronous copies
   for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
     const Tile t = tile_of<CG>(p, item);
     if (t.none) continue;
@@ -396,22 +506,49 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
       if (lane == 0) {
         const uint32_t slot = kind == kLast ? 0 : (turn0 + q) & 1u;
         const uint32_t dst = w.buf + slot * kStageBuf, bar = w.in_bar + 8 * slot;
-        tma_store_wait_read<0>();
         const uint32_t c = col0 + 32 * q;
-        mbar_expect_tx(bar, kind == kPoly ? 2048 : 4096);
-        if (kind == kPoly) {
-          tma_load_3d<1>(dst, &m.s_out, c, row0, t.b, bar);
-        } else {
-          tma_load_3d<1>(dst, &m.x_out[step & 1], c, row0, t.b, bar);
-          tma_load_3d<1>(dst + 2048, &m.lo_out, c, row0, t.b, bar);
-        }
+        mbar_expect_tx(bar, pairs ? 4096 : 2048);
+        tma_load_3d<1>(dst, pairs ? &m.x_out[step & 1] : &m.s_out, c, row0, t.b, bar);
+        if (pairs) tma_load_3d<1>(dst + 2048, &m.lo_out, c, row0, t.b, bar);
       }
     };
     if (reads && count) fetch(0);
-    float row_diag = 0.f;  // s or p of this lane's row
-    if (kind == kPoly && row < p.rows) row_diag = __ldcg(a.diag_s + (uint64_t)t.b * a.k + row);
-    if (!a.tall && (kind == kApply || kind == kLast) && row < p.rows)
-      row_diag = __ldcg(a.diag_p + (uint64_t)t.b * a.k + row);
+
+    Rule u = gram_rule(a, t.b);
+    const float* columns = nullptr;  // the diagonal vector that columns go by
+    if (kind == kPoly) {
+      const float s = row < p.rows ? __ldcg(u.diag + row) : 0.f;
+      columns = u.diag;
+      u.f = cc * kScaleP / (kScaleS * kScaleS);
+      u.r0 = (cb + cc * s) * (kScaleP / kScaleS);
+      u.r1 = cc * (kScaleP / kScaleS);
+      u.on = (cb + cc * s) * s * kScaleP;
+      u.diag_scale = 1.f / kScaleP;
+      u.diag = a.diag_p + (uint64_t)t.b * a.k;
+      u.out = a.p + (uint64_t)t.b * a.k * a.kpitch;
+    } else if (pairs) {
+      const float* d = a.diag_p + (uint64_t)t.b * a.k;
+      columns = a.tall ? d : nullptr;
+      u.f = 1.f / kScaleP;
+      u.r0 = ca + (!a.tall && row < p.rows ? __ldcg(d + row) : 0.f);
+      u.r1 = a.tall ? 1.f : 0.f;
+      if (kind == kLast) {
+        const float g = a.alpha / kScaleX;
+        u.f *= g;
+        u.r0 *= g;
+        u.r1 *= g;
+      }
+      u.diag = nullptr;
+      u.out = a.hi[(step + 1) & 1] + (uint64_t)t.b * p.rows * a.pitch;
+      u.low = a.lo + (uint64_t)t.b * p.rows * a.pitch;
+      u.pitch = a.pitch;
+      u.rows = p.rows;
+    }
+    auto column_diag = [&](uint32_t q) {
+      const uint32_t c = col0 + 32 * q + lane;
+      return columns && q < count && c < p.cols ? __ldcg(columns + c) : 0.f;
+    };
+    float other = column_diag(0);
 
     const uint32_t acc = w.acc & 1u;
     if (!__all_sync(0xffffffffu,
@@ -420,157 +557,53 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
     tmem_fence_after();
     const uint32_t src = w.tmem + acc * kAccColumns + (quarter << 21) + tile_col;
     if (kind == kPart) count = chunks;
+#pragma unroll 1
     for (uint32_t q = 0; q < count; ++q) {
       const uint32_t col = col0 + 32 * q;
-      float v[32];
-      tmem_load32(src + 32 * q, v);
-      if (kind == kPart) {
-        tmem_load_wait(v);
-        float* o = a.part + ((uint64_t)(item * CG + w.rank) * p.n + tile_col + 32 * q) * 128 +
-                   quarter * 32 + lane;
-#pragma unroll
-        for (uint32_t i = 0; i < 32; ++i) o[i * 128] = v[i];
-        continue;
-      }
       const uint32_t slot = kind == kLast ? 0 : w.turn & 1u;
-      const uint32_t buf = w.buf + slot * kStageBuf;
+      const uint32_t buf = w.buf + slot * kStageBuf, turned = w.buf + kStageBuf;
       if (reads && kind != kLast && q + 1 < count) fetch(q + 1);
-      float other = 0.f;  // s or p of column col + lane
-      if (kind == kPoly && col + lane < p.cols)
-        other = __ldcg(a.diag_s + (uint64_t)t.b * a.k + col + lane);
-      if (a.tall && (kind == kApply || kind == kLast) && col + lane < p.cols)
-        other = __ldcg(a.diag_p + (uint64_t)t.b * a.k + col + lane);
-      tmem_load_wait(v);
+      const float next = column_diag(q + 1);
       if (reads) {
         if (!__all_sync(0xffffffffu,
-                        mbar_wait(w.in_bar + 8 * slot, w.in_uses[slot] & 1u, w.gave_up)))
+                        mbar_wait(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.gave_up)))
           return;
-        ++w.in_uses[slot];
-      } else {
-        if (lane == 0) tma_store_wait_read<1>();
-        __syncwarp();
+        w.in_phase ^= 1u << slot;
       }
-
-      if (kind == kGram) {
-        const float f = kScaleS / (kScaleX * kScaleX);
+      const bool on_diag = !pairs && row0 == col;
+#pragma unroll 1
+      for (uint32_t c = 0; c < 4; ++c) {
+        float v[8];
+        tmem_load8(src + 32 * q + 8 * c, v);
+        tmem_load_wait(v);
+        if (kind == kPart) {
+          float* o = a.part + ((uint64_t)(item * CG + w.rank) * p.n + tile_col + 32 * q + 8 * c) *
+                                  128 + quarter * 32 + lane;
 #pragma unroll
-        for (uint32_t i = 0; i < 32; ++i) v[i] *= f;
-        take_diagonal(v, row, col, 1.f / kScaleS, a.diag_s + (uint64_t)t.b * a.k, a.k);
-        write_symmetric(v, buf, t.b, row0, col, t.mirror, &m.s_out);
-      } else if (kind == kPoly) {
-        // P' = (b + c (s_i + s_j)) S' + c S' S' off the diagonal, p = b s + c s^2 + c S' S' on it
-        const float f = cc * kScaleP / (kScaleS * kScaleS);
-        const float r0 = (cb + cc * row_diag) * (kScaleP / kScaleS);
-        const float r1 = cc * (kScaleP / kScaleS);
-        const float on = (cb + cc * row_diag) * row_diag * kScaleP;
-#pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) {
-          const uint4 q4 = lds128(buf + box_at(lane, c));
-          const uint32_t words[4] = {q4.x, q4.y, q4.z, q4.w};
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const float2 s2 = unpack_half(words[e]);
-            const uint32_t i = 8 * c + 2 * e;
-            const float d0 = __shfl_sync(0xffffffffu, other, i);
-            const float d1 = __shfl_sync(0xffffffffu, other, i + 1);
-            v[i] = v[i] * f + (r0 + r1 * d0) * s2.x;
-            v[i + 1] = v[i + 1] * f + (r0 + r1 * d1) * s2.y;
-          }
+          for (int i = 0; i < 8; ++i) o[i * 128] = v[i];
+          continue;
         }
+        finish8(v, c, buf, reads, pairs, other, u, on_diag, row);
+        if (kind == kLast) {
 #pragma unroll
-        for (uint32_t i = 0; i < 32; ++i)
-          if (row == col + i) v[i] += on;
-        take_diagonal(v, row, col, 1.f / kScaleP, a.diag_p + (uint64_t)t.b * a.k, a.k);
-        __syncwarp();
-        write_symmetric(v, buf, t.b, row0, col, t.mirror, &m.p_out);
-      } else {
-        // X <- (a + p) X + P' X
-        const float f = 1.f / kScaleP;
-#pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) {
-          const uint4 h4 = lds128(buf + box_at(lane, c));
-          const uint4 l4 = lds128(buf + 2048 + box_at(lane, c));
-          const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const float2 h2 = unpack_half(hw[e]), l2 = unpack_half(lw[e]);
-            const uint32_t i = 8 * c + 2 * e;
-            float d0 = row_diag, d1 = row_diag;
-            if (a.tall) {
-              d0 = __shfl_sync(0xffffffffu, other, i);
-              d1 = __shfl_sync(0xffffffffu, other, i + 1);
-            }
-            v[i] = v[i] * f + (ca + d0) * (h2.x + l2.x);
-            v[i + 1] = v[i + 1] * f + (ca + d1) * (h2.y + l2.y);
-          }
-        }
-        if (kind == kApply) {
-#pragma unroll
-          for (uint32_t c = 0; c < 4; ++c) {
-            uint32_t hw[4], lw[4];
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e) {
-              const uint32_t i = 8 * c + 2 * e;
-              hw[e] = pack_half(v[i], v[i + 1]);
-              const float2 back = unpack_half(hw[e]);
-              lw[e] = pack_half(v[i] - back.x, v[i + 1] - back.y);
-            }
-            sts128(buf + box_at(lane, c), make_uint4(hw[0], hw[1], hw[2], hw[3]));
-            sts128(buf + 2048 + box_at(lane, c), make_uint4(lw[0], lw[1], lw[2], lw[3]));
-          }
-          proxy_fence();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_3d(&m.x_out[(step + 1) & 1], buf, col, row0, t.b);
-            tma_store_3d(&m.lo_out, buf + 2048, col, row0, t.b);
-            tma_store_commit();
-          }
-        } else {
-          // turned in shared memory so that a warp writes a row's 32 elements at once,
-          // whatever the alignment of the caller's rows
-          proxy_fence();
-          __syncwarp();
-          if (q + 1 < count) fetch(q + 1);
-          const uint32_t st = w.buf + kStageBuf;
-          const float g = a.alpha / kScaleX;
-#pragma unroll
-          for (uint32_t i = 0; i < 32; ++i)
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + lane * 128 + ((i ^ lane) << 2)),
-                         "f"(v[i] * g)
+          for (uint32_t i = 0; i < 8; ++i)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(turned + lane * 128 +
+                                                         (((8 * c + i) ^ lane) << 2)),
+                         "f"(v[i])
                          : "memory");
-          __syncwarp();
-          if (col + lane < p.cols) {
-            const int64_t o0 = (int64_t)t.b * a.out_batch + (int64_t)row0 * a.out_stride + col +
-                               lane;
-            const uint32_t n_rows = min(32u, p.rows - row0);
-            for (uint32_t r0 = 0; r0 < n_rows; r0 += 8) {
-              float old[8];
-              if (a.weight) {
-#pragma unroll
-                for (uint32_t r = 0; r < 8; ++r)
-                  if (r0 + r < n_rows)
-                    old[r] = load_any(a.out, a.out_type, o0 + (int64_t)(r0 + r) * a.out_stride);
-              }
-#pragma unroll
-              for (uint32_t r = 0; r < 8; ++r) {
-                if (r0 + r >= n_rows) break;
-                float x;
-                asm volatile("ld.shared.f32 %0, [%1];"
-                             : "=f"(x)
-                             : "r"(st + (r0 + r) * 128 + ((lane ^ (r0 + r)) << 2))
-                             : "memory");
-                if (a.weight) x += a.keep * old[r];
-                const int64_t o = o0 + (int64_t)(r0 + r) * a.out_stride;
-                if (a.out_type == SPARCML_F32) static_cast<float*>(a.out)[o] = x;
-                else if (a.out_type == SPARCML_BF16)
-                  static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x);
-                else static_cast<__half*>(a.out)[o] = __float2half_rn(x);
-              }
-            }
-          }
-          __syncwarp();
+        } else {
+          stage8(v, c, buf, pairs, t.mirror);
         }
       }
+      if (kind == kLast) {
+        proxy_fence_shared();
+        __syncwarp();
+        if (q + 1 < count) fetch(q + 1);
+        store_result(a, turned, t.b, row0, p.rows, col, p.cols);
+      } else if (kind != kPart) {
+        store_boxes(buf, u, row0, col, pairs, t.mirror);
+      }
+      other = next;
       ++w.turn;
     }
     tmem_fence_before();
@@ -582,33 +615,31 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
 
 // S from the partial tiles of a split product, in the order of the splits.
 template <int CG>
-__device__ void join_parts(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p) {
+__device__ void join_parts(Worker<CG>& w, const StepArgs& a, const Product& p) {
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t across = p.n / 32, per = 4 * CG * across;
   const uint32_t total = a.batch * p.tiles * per;
-  for (uint32_t u = blockIdx.x + gridDim.x * warp; u < total; u += gridDim.x * kWriters) {
-    const uint32_t tile = u / per, r = u % per / across, c = u % across;
+  for (uint32_t x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * kWriters) {
+    const uint32_t tile = x / per, r = x % per / across, q = x % across;
     const Tile t = tile_of<CG>(p, tile * p.splits);
-    const uint32_t row0 = t.row0 + 32 * r, col = t.col0 + 32 * c;
+    const uint32_t row0 = t.row0 + 32 * r, col = t.col0 + 32 * q;
     if (row0 >= p.rows || col >= p.cols) continue;
-    float v[32];
+    const Rule u = gram_rule(a, t.b);
+#pragma unroll 1
+    for (uint32_t c = 0; c < 4; ++c) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+      for (uint32_t s = 0; s < p.splits; ++s) {
+        const float* o = a.part +
+                         ((uint64_t)((tile * p.splits + s) * CG + r / 4) * p.n + 32 * q + 8 * c) *
+                             128 + (r & 3u) * 32 + lane;
 #pragma unroll
-    for (uint32_t i = 0; i < 32; ++i) v[i] = 0.f;
-    for (uint32_t s = 0; s < p.splits; ++s) {
-      const float* o = a.part +
-                       ((uint64_t)((tile * p.splits + s) * CG + r / 4) * p.n + 32 * c) * 128 +
-                       (r & 3u) * 32 + lane;
-#pragma unroll
-      for (uint32_t i = 0; i < 32; ++i) v[i] += __ldcg(o + i * 128);
+        for (int i = 0; i < 8; ++i) v[i] += __ldcg(o + i * 128);
+      }
+      finish8(v, c, w.buf, false, false, 0.f, u, row0 == col, row0 + lane);
+      stage8(v, c, w.buf, false, t.mirror);
     }
-    const float f = kScaleS / (kScaleX * kScaleX);
-#pragma unroll
-    for (uint32_t i = 0; i < 32; ++i) v[i] *= f;
-    if (lane == 0) tma_store_wait_read<1>();
-    __syncwarp();
-    take_diagonal(v, row0 + lane, col, 1.f / kScaleS, a.diag_s + (uint64_t)t.b * a.k, a.k);
-    write_symmetric(v, w.buf + (w.turn & 1u) * kStageBuf, t.b, row0, col, t.mirror, &m.s_out);
-    ++w.turn;
+    store_boxes(w.buf, u, row0, col, false, t.mirror);
   }
 }
 
@@ -675,7 +706,7 @@ __device__ void split_input(const StepArgs& a) {
         const float2 back = unpack_half(hw[i / 2]);
         lw[i / 2] = pack_half(x[0] - back.x, x[1] - back.y);
       }
-      *reinterpret_cast<uint2*>(a.hi + line * a.pitch + c) = make_uint2(hw[0], hw[1]);
+      *reinterpret_cast<uint2*>(a.hi[0] + line * a.pitch + c) = make_uint2(hw[0], hw[1]);
       *reinterpret_cast<uint2*>(a.lo + line * a.pitch + c) = make_uint2(lw[0], lw[1]);
     }
     if (++piece == pieces) {
@@ -693,27 +724,29 @@ __device__ void split_input(const StepArgs& a) {
 // Every block waits until all have come this far, and sees what they wrote. The
 // wait ends after a few seconds at worst.
 __device__ __forceinline__ void grid_turn(uint32_t* turns, uint32_t& turn, uint32_t* gave_up) {
-  proxy_fence();
   __syncthreads();
   ++turn;
   if (threadIdx.x == 0) {
-    __threadfence();
-    atomicAdd(turns, 1u);
+    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(turns) : "memory");
     if (*reinterpret_cast<volatile uint32_t*>(gave_up) == 0) {
       const uint32_t want = turn * gridDim.x;
-      const uint64_t end = global_ns() + 4 * kWaitNs;
-      uint32_t polls = 0;
-      while ((int32_t)(*reinterpret_cast<volatile uint32_t*>(turns) - want) < 0) {
-        if ((++polls & 63u) == 0 && global_ns() > end) {
-          *gave_up = 1;
-          break;
+      uint64_t end = 0;
+      for (uint32_t polls = 1;; ++polls) {
+        uint32_t now;
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(turns) : "memory");
+        if ((int32_t)(now - want) >= 0) break;
+        if ((polls & 63u) == 0) {
+          const uint64_t t = global_ns();
+          if (end == 0) end = t + 4 * kWaitNs;
+          if (t > end) {
+            *gave_up = 1;
+            break;
+          }
         }
       }
     }
-    __threadfence();
   }
   __syncthreads();
-  proxy_fence();
 }
 
 template <int CG>
@@ -742,6 +775,8 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   w.lead_full = CG == 1 ? w.full : cluster_addr(w.full, 0);
   w.lead_acc_empty = cluster_addr(w.acc_empty, 0);
 
+  if (threadIdx.x < sizeof(Maps) / sizeof(CUtensorMap))
+    tma_prefetch_map(reinterpret_cast<const CUtensorMap*>(&m) + threadIdx.x);
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (uint32_t s = 0; s < kMaxStages; ++s) {
@@ -782,7 +817,6 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       const bool stop = __any_sync(0xffffffffu, *w.gave_up != 0);
       if (warp < kWriters) {
         if (!stop) write_results(w, a, m, p, kind, step);
-        if (lane_id() == 0) tma_store_wait_all();
       } else if (warp == kWriters) {
         if (leader && !stop) load_operands(w, p, ma, mb, a_mn, b_mn);
       } else if (w.rank == 0) {
@@ -792,10 +826,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       if (kind == kLast) break;
       grid_turn(a.g.turns, turn, &gave_up);
       if (kind == kPart) {
-        if (warp < kWriters) {
-          if (!__any_sync(0xffffffffu, *w.gave_up != 0)) join_parts(w, a, m, p);
-          if (lane_id() == 0) tma_store_wait_all();
-        }
+        if (warp < kWriters && !__any_sync(0xffffffffu, *w.gave_up != 0)) join_parts(w, a, p);
         __syncwarp();
         grid_turn(a.g.turns, turn, &gave_up);
       }
@@ -806,8 +837,8 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
     // with a limit, for the loads and products that were begun.
     volatile uint32_t alone = 0;
     if (warp == kWriters && leader && w.rank == 0)  // a pair's loads all report to rank 0
-      for (uint32_t i = w.fill > w.stages ? w.fill - w.stages : 0; i < w.fill; ++i)
-        mbar_wait(w.full + 8 * (i % w.stages), (i / w.stages) & 1u, &alone);
+      for (uint32_t i = 0; i < w.stages; ++i, w.next_stage())
+        mbar_wait(w.full + 8 * w.stage, w.phase ^ 1u, &alone);
     if (warp == kWriters + 1 && leader && w.rank == 0) {
       const uint32_t bar = w.acc_full + 8 * (w.acc & 1u);
       mma_commit<CG>(bar);
@@ -888,8 +919,12 @@ Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dep
     p.splits = (uint32_t)std::min<uint64_t>(workers / (tiles * batch), p.blocks / 8);
   const uint64_t items = tiles * batch * p.splits;
   p.items = items > 0xffffffffull ? 0 : (uint32_t)items;
-  *time = (double)ceil_div(items, workers) * ((double)ceil_div(p.blocks, p.splits) * (n / 64.0) +
-                                              4.0 + n / 32.0);
+  // a block of 64 of the summed axis: the products, or the operands' way from L2 when
+  // many SMs fetch at one time
+  const double busy = std::min(1.0, (double)items / (double)workers);
+  const double each = std::max(n / 64.0, (128 + n / pair) / 45.0 * busy);
+  *time = (double)ceil_div(items, workers) *
+          ((double)ceil_div(p.blocks, p.splits) * each + 4.0 + n / 32.0);
   return p;
 }
 
@@ -998,8 +1033,7 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
       !make_map(&m.x_out[0], hi0, q.batch, q.m, q.n, q.pitch, 32) ||
       !make_map(&m.x_out[1], hi1, q.batch, q.m, q.n, q.pitch, 32) ||
       !make_map(&m.lo_out, lo, q.batch, q.m, q.n, q.pitch, 32) ||
-      !make_map(&m.s_out, sm, q.batch, q.k, q.k, q.kpitch, 32) ||
-      !make_map(&m.p_out, pm, q.batch, q.k, q.k, q.kpitch, 32))
+      !make_map(&m.s_out, sm, q.batch, q.k, q.k, q.kpitch, 32))
     return SPARCML_ERR_CUDA;
   const int64_t ge = g.g_type == SPARCML_F32 ? 16 : 8;
   g.vec_g = aligned_to(g.g, ge) && g.g_batch % 4 == 0 && g.g_stride % 4 == 0;
@@ -1018,9 +1052,13 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   a.poly = q.poly;
   a.apply = q.apply;
   std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
-  a.hi = reinterpret_cast<__half*>(hi0);
+  a.hi[0] = reinterpret_cast<__half*>(hi0);
+  a.hi[1] = reinterpret_cast<__half*>(hi1);
   a.lo = reinterpret_cast<__half*>(lo);
+  a.s = reinterpret_cast<__half*>(sm);
+  a.p = reinterpret_cast<__half*>(pm);
   a.pitch = q.pitch;
+  a.kpitch = q.kpitch;
   a.diag_s = reinterpret_cast<float*>(w + q.ds);
   a.diag_p = reinterpret_cast<float*>(w + q.dp);
   a.part = reinterpret_cast<float*>(w + q.part);
