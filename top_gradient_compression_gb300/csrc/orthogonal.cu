@@ -289,6 +289,7 @@ struct Worker {
   uint32_t lead_full, lead_acc_empty;      // the same of the pair's first block
   uint32_t buf;                            // this writer's two buffers
   uint32_t rank, cluster, clusters, tmem;
+  bool leader;                             // the lane that issues for its warp
   volatile uint32_t* gave_up;
   uint32_t stage = 0, phase = 0;  // next operand stage and its turn's parity (loader, issuer)
   uint32_t acc = 0;       // accumulators used so far (issuer, writers)
@@ -296,52 +297,64 @@ struct Worker {
   uint32_t turn = 0;      // chunks written so far
 };
 
+// The loader and the issuer run as whole warps, of which one lane issues: so the addresses
+// and the control flow are known to be uniform (a lane on its own took 700 cycles per
+// block of the summed axis, where the products take 512).
 template <int CG>
 __device__ void load_operands(Worker<CG>& w, const Product& p, const CUtensorMap* ma,
-                              const CUtensorMap* mb, bool a_mn, bool b_mn) {
+                              const CUtensorMap* mb, bool a_mn, bool b_mn, const Tile& first_tile) {
   const uint32_t b_rows = p.n / CG, bytes = 128 * 128 + b_rows * 128;
-  proxy_fence();  // the other blocks' results, read by asynchronous copies
+  proxy_fence_global();  // the other blocks' results, read by asynchronous copies
   for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
-    const Tile t = tile_of<CG>(p, item);
+    const Tile t = item == w.cluster ? first_tile : tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t ra = t.row0 + 128 * w.rank, rb = t.col0 + b_rows * w.rank;
     for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!mbar_wait(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return;
-      if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, CG * bytes);
-      const uint32_t bar = w.lead_full + 8 * s, k = i * 64;
-      uint32_t dst = w.ring + s * w.stage_bytes;
-      for (uint32_t h = 0; h < 128; h += 64, dst += 8192)
-        tma_load_3d<CG>(dst, ma, a_mn ? ra + h : k, a_mn ? k : ra + h, t.b, bar);
-      for (uint32_t h = 0; h < b_rows; h += 64, dst += 8192)
-        tma_load_3d<CG>(dst, mb, b_mn ? rb + h : k, b_mn ? k : rb + h, t.b, bar);
+      if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return;
+      if (w.leader) {
+        if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, CG * bytes);
+        const uint32_t bar = w.lead_full + 8 * s, k = i * 64;
+        uint32_t dst = w.ring + s * w.stage_bytes;
+#pragma unroll
+        for (uint32_t h = 0; h < 128; h += 64, dst += 8192)
+          tma_load_3d<CG>(dst, ma, a_mn ? ra + h : k, a_mn ? k : ra + h, t.b, bar);
+        for (uint32_t h = 0; h < b_rows; h += 64, dst += 8192)
+          tma_load_3d<CG>(dst, mb, b_mn ? rb + h : k, b_mn ? k : rb + h, t.b, bar);
+      }
+      __syncwarp();
     }
   }
 }
 
 template <int CG>
-__device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool b_mn) {
+__device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool b_mn,
+                               const Tile& first_tile) {
   const uint32_t idesc = mma_desc(128 * CG, p.n, a_mn, b_mn);
   const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
   for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
-    const Tile t = tile_of<CG>(p, item);
+    const Tile t = item == w.cluster ? first_tile : tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t a = w.acc & 1u;
-    if (!mbar_wait(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return;
+    if (!mbar_wait_warp(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return;
     tmem_fence_after();
     const uint32_t d = w.tmem + a * kAccColumns;
     for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!mbar_wait(w.full + 8 * s, w.phase, w.gave_up)) return;
+      if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.gave_up)) return;
       tmem_fence_after();
-      const uint32_t sa = w.ring + s * w.stage_bytes, sb = sa + 128 * 128;
+      if (w.leader) {
+        const uint32_t sa = w.ring + s * w.stage_bytes, sb = sa + 128 * 128;
 #pragma unroll
-      for (uint32_t k = 0; k < 4; ++k)
-        mma_f16<CG>(d, tile_desc(sa + k * step_a, 8192, 1024),
-                    tile_desc(sb + k * step_b, 8192, 1024), idesc, i > t.first || k > 0);
-      mma_commit<CG>(w.empty + 8 * s);
+        for (uint32_t k = 0; k < 4; ++k)
+          mma_f16<CG>(d, tile_desc(sa + k * step_a, 8192, 1024),
+                      tile_desc(sb + k * step_b, 8192, 1024), idesc, i > t.first || k > 0);
+        mma_commit<CG>(w.empty + 8 * s);
+      }
+      __syncwarp();
     }
-    mma_commit<CG>(w.acc_full + 8 * a);
+    if (w.leader) mma_commit<CG>(w.acc_full + 8 * a);
+    __syncwarp();
     ++w.acc;
   }
 }
@@ -439,7 +452,6 @@ __device__ __forceinline__ void store_boxes(uint32_t buf, const Rule& u, uint32_
   store_box(buf, u.out, u.pitch, row0, u.rows, col);
   if (pairs) store_box(buf + 2048, u.low, u.pitch, row0, u.rows, col);
   if (mirror) store_box(buf + 2048, u.out, u.pitch, col, u.rows, row0);
-  proxy_fence_shared();  // the buffer's next load is an asynchronous copy
   __syncwarp();
 }
 
@@ -488,14 +500,14 @@ __device__ __forceinline__ void store_result(const StepArgs& a, uint32_t box, ui
 
 template <int CG>
 __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p,
-                              int kind, uint32_t step) {
+                              int kind, uint32_t step, const Tile& first_tile) {
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t quarter = warp & 3u, half = warp >> 2, chunks = p.n / 64;
   const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
   const bool pairs = kind == kApply || kind == kLast, reads = kind == kPoly || pairs;
-  if (reads) proxy_fence();  // the other blocks' results, read by asynchronous copies
+  if (reads && lane == 0) proxy_fence_global();  // the other blocks' results, fetched below
   for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
-    const Tile t = tile_of<CG>(p, item);
+    const Tile t = item == w.cluster ? first_tile : tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t row0 = t.row0 + 128 * w.rank + 32 * quarter, row = row0 + lane;
     const uint32_t tile_col = half * chunks * 32, col0 = t.col0 + tile_col;
@@ -507,6 +519,7 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
         const uint32_t slot = kind == kLast ? 0 : (turn0 + q) & 1u;
         const uint32_t dst = w.buf + slot * kStageBuf, bar = w.in_bar + 8 * slot;
         const uint32_t c = col0 + 32 * q;
+        proxy_fence_shared();  // the buffer's last ordinary accesses come first
         mbar_expect_tx(bar, pairs ? 4096 : 2048);
         tma_load_3d<1>(dst, pairs ? &m.x_out[step & 1] : &m.s_out, c, row0, t.b, bar);
         if (pairs) tma_load_3d<1>(dst + 2048, &m.lo_out, c, row0, t.b, bar);
@@ -551,9 +564,7 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
     float other = column_diag(0);
 
     const uint32_t acc = w.acc & 1u;
-    if (!__all_sync(0xffffffffu,
-                    mbar_wait(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)))
-      return;
+    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)) return;
     tmem_fence_after();
     const uint32_t src = w.tmem + acc * kAccColumns + (quarter << 21) + tile_col;
     if (kind == kPart) count = chunks;
@@ -565,9 +576,7 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
       if (reads && kind != kLast && q + 1 < count) fetch(q + 1);
       const float next = column_diag(q + 1);
       if (reads) {
-        if (!__all_sync(0xffffffffu,
-                        mbar_wait(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.gave_up)))
-          return;
+        if (!mbar_wait_warp(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.gave_up)) return;
         w.in_phase ^= 1u << slot;
       }
       const bool on_diag = !pairs && row0 == col;
@@ -596,7 +605,6 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
         }
       }
       if (kind == kLast) {
-        proxy_fence_shared();
         __syncwarp();
         if (q + 1 < count) fetch(q + 1);
         store_result(a, turned, t.b, row0, p.rows, col, p.cols);
@@ -798,29 +806,30 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   w.tmem = tmem_slot;
 
   uint32_t turn = 0;
+  const bool tall = a.tall != 0;
+  w.leader = elect_one();
+  // the first tile of each product is the same in every step
+  const Tile first[3] = {tile_of<CG>(a.gram, min(w.cluster, a.gram.items - 1)),
+                         tile_of<CG>(a.poly, min(w.cluster, a.poly.items - 1)),
+                         tile_of<CG>(a.apply, min(w.cluster, a.apply.items - 1))};
   split_input(a);
   grid_turn(a.g.turns, turn, &gave_up);
-  const bool tall = a.tall != 0;
-  bool leader = false;
-  if (warp >= kWriters) leader = elect_one();
   for (uint32_t step = 0; step < a.steps; ++step) {
     const CUtensorMap* x = &m.x_in[step & 1];
 #pragma unroll 1
     for (uint32_t ph = 0; ph < 3; ++ph) {
       const Product& p = ph == 0 ? a.gram : ph == 1 ? a.poly : a.apply;
+      const Tile t = ph == 0 ? first[0] : ph == 1 ? first[1] : first[2];
       const CUtensorMap* ma = ph == 0 ? x : ph == 1 ? &m.s_in : tall ? x : &m.p_in;
       const CUtensorMap* mb = ph == 0 ? x : ph == 1 ? &m.s_in : tall ? &m.p_in : x;
       const bool a_mn = ph == 0 && tall, b_mn = (ph == 0 && tall) || (ph == 2 && !tall);
       const int kind = ph == 0   ? (p.splits > 1 ? kPart : kGram)
                        : ph == 1 ? kPoly
                                  : (step + 1 == a.steps ? kLast : kApply);
-      const bool stop = __any_sync(0xffffffffu, *w.gave_up != 0);
-      if (warp < kWriters) {
-        if (!stop) write_results(w, a, m, p, kind, step);
-      } else if (warp == kWriters) {
-        if (leader && !stop) load_operands(w, p, ma, mb, a_mn, b_mn);
-      } else if (w.rank == 0) {
-        if (leader && !stop) issue_products(w, p, a_mn, b_mn);
+      if (!__any_sync(0xffffffffu, *w.gave_up != 0)) {
+        if (warp < kWriters) write_results(w, a, m, p, kind, step, t);
+        else if (warp == kWriters) load_operands(w, p, ma, mb, a_mn, b_mn, t);
+        else if (w.rank == 0) issue_products(w, p, a_mn, b_mn, t);
       }
       __syncwarp();
       if (kind == kLast) break;
@@ -836,10 +845,10 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
     // Nothing of this block may still be in flight when its memory goes: wait, again
     // with a limit, for the loads and products that were begun.
     volatile uint32_t alone = 0;
-    if (warp == kWriters && leader && w.rank == 0)  // a pair's loads all report to rank 0
+    if (warp == kWriters && w.leader && w.rank == 0)  // a pair's loads all report to rank 0
       for (uint32_t i = 0; i < w.stages; ++i, w.next_stage())
         mbar_wait(w.full + 8 * w.stage, w.phase ^ 1u, &alone);
-    if (warp == kWriters + 1 && leader && w.rank == 0) {
+    if (warp == kWriters + 1 && w.leader && w.rank == 0) {
       const uint32_t bar = w.acc_full + 8 * (w.acc & 1u);
       mma_commit<CG>(bar);
       mbar_wait(bar, (w.acc >> 1) & 1u, &alone);

@@ -87,6 +87,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   return true;
 }
 
+// The same for a whole warp: true only if every lane's wait ended well.
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
+                                               volatile uint32_t* gave_up) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, gave_up));
+}
+
 // Tiled load; with a pair of blocks (CG = 2) the barrier may be the other block's.
 template <int CG>
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t x,
@@ -107,10 +113,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-// Orders this thread's ordinary accesses with the asynchronous copies' ones: of
-// all memory, or of shared memory alone (far cheaper).
-__device__ __forceinline__ void proxy_fence() {
-  asm volatile("fence.proxy.async;" ::: "memory");
+// Orders this thread's ordinary accesses to global or to shared memory with the
+// asynchronous copies' ones.
+__device__ __forceinline__ void proxy_fence_global() {
+  asm volatile("fence.proxy.async.global;" ::: "memory");
 }
 __device__ __forceinline__ void proxy_fence_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
