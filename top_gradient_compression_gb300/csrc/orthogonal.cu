@@ -389,57 +389,84 @@ struct Rule {
   uint32_t rows;  // of out
 };
 
-// Eight columns from column 8 c of the 32 x 32 box: v holds this lane's row.
-__device__ __forceinline__ void finish8(float (&v)[8], uint32_t c, uint32_t buf, bool reads,
-                                        bool pairs, float other, const Rule& u, bool on_diag,
-                                        uint32_t row) {
+// Sixteen columns from column 16 h of the 32 x 32 box: v holds this lane's row. All reads
+// come before all arithmetic: a writer's time is the latency of its chain (with eight
+// columns at a time a box took 1.2 us).
+__device__ __forceinline__ void finish16(float (&v)[16], uint32_t h, uint32_t buf, bool reads,
+                                         bool pairs, bool by_column, float other, const Rule& u,
+                                         bool on_diag, uint32_t row) {
   const uint32_t lane = lane_id();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] *= u.f;
   if (reads) {
-    const uint4 h4 = lds128(buf + box_at(lane, c));
-    uint4 l4 = make_uint4(0, 0, 0, 0);
-    if (pairs) l4 = lds128(buf + 2048 + box_at(lane, c));
-    const uint32_t hw[4] = {h4.x, h4.y, h4.z, h4.w}, lw[4] = {l4.x, l4.y, l4.z, l4.w};
+    uint4 h4[2], l4[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 h2 = unpack_half(hw[e]), l2 = unpack_half(lw[e]);
-      const float d0 = __shfl_sync(0xffffffffu, other, 8 * c + 2 * e);
-      const float d1 = __shfl_sync(0xffffffffu, other, 8 * c + 2 * e + 1);
-      v[2 * e] += (u.r0 + u.r1 * d0) * (h2.x + l2.x);
-      v[2 * e + 1] += (u.r0 + u.r1 * d1) * (h2.y + l2.y);
+    for (int c = 0; c < 2; ++c) h4[c] = lds128(buf + box_at(lane, 2 * h + c));
+    float w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = u.r0;
+    if (by_column) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        w[i] += u.r1 * __shfl_sync(0xffffffffu, other, (int)(16 * h) + i);
     }
+    if (pairs) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) l4[c] = lds128(buf + 2048 + box_at(lane, 2 * h + c));
+    } else {
+      l4[0] = l4[1] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t hw[4] = {h4[c].x, h4[c].y, h4[c].z, h4[c].w};
+      const uint32_t lw[4] = {l4[c].x, l4[c].y, l4[c].z, l4[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 h2 = unpack_half(hw[e]), l2 = unpack_half(lw[e]);
+        const int i = 8 * c + 2 * e;
+        v[i] = v[i] * u.f + w[i] * (h2.x + l2.x);
+        v[i + 1] = v[i + 1] * u.f + w[i + 1] * (h2.y + l2.y);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] *= u.f;
   }
   if (on_diag) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (lane == 8 * c + i) {
+    for (int i = 0; i < 16; ++i)
+      if (lane == 16 * h + i) {
         if (row < u.rows) u.diag[row] = (v[i] + u.on) * u.diag_scale;
         v[i] = 0.f;
       }
   }
 }
 
-// The eight results as fp16 (and what that rounding left, for a pair) into the box, and
+// The sixteen results as fp16 (and what that rounding left, for a pair) into the box, and
 // into the box of its mirror image.
-__device__ __forceinline__ void stage8(const float (&v)[8], uint32_t c, uint32_t buf, bool pairs,
-                                       bool mirror) {
+__device__ __forceinline__ void stage16(const float (&v)[16], uint32_t h, uint32_t buf, bool pairs,
+                                        bool mirror) {
   const uint32_t lane = lane_id();
-  uint32_t hw[4], lw[4];
+  uint32_t hw[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) hw[e] = pack_half(v[2 * e], v[2 * e + 1]);
-  sts128(buf + box_at(lane, c), make_uint4(hw[0], hw[1], hw[2], hw[3]));
+  for (int e = 0; e < 8; ++e) hw[e] = pack_half(v[2 * e], v[2 * e + 1]);
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    sts128(buf + box_at(lane, 2 * h + c),
+           make_uint4(hw[4 * c], hw[4 * c + 1], hw[4 * c + 2], hw[4 * c + 3]));
   if (pairs) {
+    uint32_t lw[8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
       const float2 back = unpack_half(hw[e]);
       lw[e] = pack_half(v[2 * e] - back.x, v[2 * e + 1] - back.y);
     }
-    sts128(buf + 2048 + box_at(lane, c), make_uint4(lw[0], lw[1], lw[2], lw[3]));
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+      sts128(buf + 2048 + box_at(lane, 2 * h + c),
+             make_uint4(lw[4 * c], lw[4 * c + 1], lw[4 * c + 2], lw[4 * c + 3]));
   } else if (mirror) {
 #pragma unroll
-    for (uint32_t i = 0; i < 8; ++i)
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2048 + box_at(8 * c + i, lane >> 3) +
+    for (uint32_t i = 0; i < 16; ++i)
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(buf + 2048 + box_at(16 * h + i, lane >> 3) +
                                                    (lane & 7u) * 2),
                    "h"((uint16_t)(i & 1 ? hw[i / 2] >> 16 : hw[i / 2]))
                    : "memory");
@@ -581,27 +608,28 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
       }
       const bool on_diag = !pairs && row0 == col;
 #pragma unroll 1
-      for (uint32_t c = 0; c < 4; ++c) {
-        float v[8];
-        tmem_load8(src + 32 * q + 8 * c, v);
+      for (uint32_t h = 0; h < 2; ++h) {
+        float v[16];
+        tmem_load16(src + 32 * q + 16 * h, v);
         tmem_load_wait(v);
         if (kind == kPart) {
-          float* o = a.part + ((uint64_t)(item * CG + w.rank) * p.n + tile_col + 32 * q + 8 * c) *
-                                  128 + quarter * 32 + lane;
+          float* o = a.part +
+                     ((uint64_t)(item * CG + w.rank) * p.n + tile_col + 32 * q + 16 * h) * 128 +
+                     quarter * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i * 128] = v[i];
+          for (int i = 0; i < 16; ++i) o[i * 128] = v[i];
           continue;
         }
-        finish8(v, c, buf, reads, pairs, other, u, on_diag, row);
+        finish16(v, h, buf, reads, pairs, columns != nullptr, other, u, on_diag, row);
         if (kind == kLast) {
 #pragma unroll
-          for (uint32_t i = 0; i < 8; ++i)
+          for (uint32_t i = 0; i < 16; ++i)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(turned + lane * 128 +
-                                                         (((8 * c + i) ^ lane) << 2)),
+                                                         (((16 * h + i) ^ lane) << 2)),
                          "f"(v[i])
                          : "memory");
         } else {
-          stage8(v, c, buf, pairs, t.mirror);
+          stage16(v, h, buf, pairs, t.mirror);
         }
       }
       if (kind == kLast) {
@@ -621,33 +649,51 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
   }
 }
 
-// S from the partial tiles of a split product, in the order of the splits.
+// S from the partial tiles of a split product, in the order of the splits: a warp takes
+// 32 rows and 8 columns, so that a few tiles give work to many SMs.
 template <int CG>
-__device__ void join_parts(Worker<CG>& w, const StepArgs& a, const Product& p) {
+__device__ void join_parts(const StepArgs& a, const Product& p) {
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
-  const uint32_t across = p.n / 32, per = 4 * CG * across;
+  const uint32_t across = p.n / 8, per = 4 * CG * across;
   const uint32_t total = a.batch * p.tiles * per;
-  for (uint32_t x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * kWriters) {
+  for (uint32_t x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * (kThreads / 32)) {
     const uint32_t tile = x / per, r = x % per / across, q = x % across;
     const Tile t = tile_of<CG>(p, tile * p.splits);
-    const uint32_t row0 = t.row0 + 32 * r, col = t.col0 + 32 * q;
+    const uint32_t row0 = t.row0 + 32 * r, col = t.col0 + 8 * q, row = row0 + lane;
     if (row0 >= p.rows || col >= p.cols) continue;
-    const Rule u = gram_rule(a, t.b);
-#pragma unroll 1
-    for (uint32_t c = 0; c < 4; ++c) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const uint64_t step = (uint64_t)CG * p.n * 128;
+    const float* o = a.part + ((uint64_t)(tile * p.splits * CG + r / 4) * p.n + 8 * q) * 128 +
+                     (r & 3u) * 32 + lane;
 #pragma unroll 4
-      for (uint32_t s = 0; s < p.splits; ++s) {
-        const float* o = a.part +
-                         ((uint64_t)((tile * p.splits + s) * CG + r / 4) * p.n + 32 * q + 8 * c) *
-                             128 + (r & 3u) * 32 + lane;
+    for (uint32_t s = 0; s < p.splits; ++s, o += step) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += __ldcg(o + i * 128);
-      }
-      finish8(v, c, w.buf, false, false, 0.f, u, row0 == col, row0 + lane);
-      stage8(v, c, w.buf, false, t.mirror);
+      for (int i = 0; i < 8; ++i) v[i] += __ldcg(o + i * 128);
     }
-    store_boxes(w.buf, u, row0, col, false, t.mirror);
+    const Rule u = gram_rule(a, t.b);
+    uint16_t half[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] *= u.f;
+      if (row == col + i) {
+        if (row < u.rows) u.diag[row] = v[i] * u.diag_scale;
+        v[i] = 0.f;
+      }
+      half[i] = __half_as_ushort(__float2half_rn(v[i]));
+    }
+    if (row < u.rows) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = half[2 * e] | (uint32_t)half[2 * e + 1] << 16;
+      *reinterpret_cast<uint4*>(u.out + (uint64_t)row * u.pitch + col) =
+          make_uint4(w[0], w[1], w[2], w[3]);
+      if (t.mirror) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (col + i < u.rows)
+            u.out[(uint64_t)(col + i) * u.pitch + row] = __ushort_as_half(half[i]);
+      }
+    }
   }
 }
 
@@ -835,7 +881,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       if (kind == kLast) break;
       grid_turn(a.g.turns, turn, &gave_up);
       if (kind == kPart) {
-        if (warp < kWriters && !__any_sync(0xffffffffu, *w.gave_up != 0)) join_parts(w, a, p);
+        if (!__any_sync(0xffffffffu, *w.gave_up != 0)) join_parts<CG>(a, p);
         __syncwarp();
         grid_turn(a.g.turns, turn, &gave_up);
       }
@@ -924,7 +970,8 @@ Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dep
   const uint64_t tiles = symmetric ? ratio * tr * (tr + 1) / 2 : tr * tc;
   p.tiles = (uint32_t)tiles;
   p.splits = 1;
-  if (may_split && tiles * batch * 2 <= workers && p.blocks >= 16)
+  // joining the parts costs a turn of the grid, the time of about 40 blocks
+  if (may_split && tiles * batch * 2 <= workers && p.blocks >= 64)
     p.splits = (uint32_t)std::min<uint64_t>(workers / (tiles * batch), p.blocks / 8);
   const uint64_t items = tiles * batch * p.splits;
   p.items = items > 0xffffffffull ? 0 : (uint32_t)items;
@@ -933,7 +980,8 @@ Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dep
   const double busy = std::min(1.0, (double)items / (double)workers);
   const double each = std::max(n / 64.0, (128 + n / pair) / 45.0 * busy);
   *time = (double)ceil_div(items, workers) *
-          ((double)ceil_div(p.blocks, p.splits) * each + 4.0 + n / 32.0);
+              ((double)ceil_div(p.blocks, p.splits) * each + 4.0 + n / 32.0) +
+          (p.splits > 1 ? 60.0 : 0.0);
   return p;
 }
 
