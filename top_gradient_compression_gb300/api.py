@@ -487,30 +487,40 @@ TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
 
 
+# These calls are short: what they check of their arguments costs as much as a launch.
+def _raw_stream(stream, t):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _typed(t, name: str, like=None):
+    """The type code of a CUDA tensor of one of the three types (of `like`'s)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in TYPES:
+    code = TYPES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     if like is not None and t.dtype != like.dtype:
         raise TypeError(f"{name} must be {like.dtype}, got {t.dtype}")
-    return t
+    return code
 
 
 def _rows(t, name: str):
     """(rows, dim, row stride) of a tensor whose last axis is contiguous and whose
     other axes step evenly; a view, never a copy."""
-    if t.dim() == 0 or t.shape[-1] == 0:
+    shape, strides = t.shape, t.stride()
+    if not shape or shape[-1] == 0:
         raise ValueError(f"{name} needs a last axis of at least one element")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    dim = shape[-1]
+    if strides[-1] != 1 and dim > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    if t.dim() == 2:
-        return t.shape[0], t.shape[1], t.stride(0)
-    dim = t.shape[-1]
+    if len(shape) == 2:
+        return shape[0], dim, strides[0]
     if t.numel() == 0:
         return 0, dim, dim
     step, rows = None, 1
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
             continue
         if step is None:
@@ -523,19 +533,11 @@ def _rows(t, name: str):
 
 def _vector(t, dim: int, name: str):
     if t is None:
-        return None
-    _typed(t, name)
-    if t.shape != (dim,) or (dim > 1 and t.stride(0) != 1):
+        return None, 0
+    code = _typed(t, name)
+    if t.dim() != 1 or t.shape[0] != dim or (dim > 1 and t.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous vector of {dim} elements")
-    return t.data_ptr()
-
-
-def _affine(weight, bias, dim: int):
-    w, b = _vector(weight, dim, "weight"), _vector(bias, dim, "bias")
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias must have the same type")
-    given = weight if weight is not None else bias
-    return w, b, 0 if given is None else TYPES[given.dtype]
+    return t.data_ptr(), code
 
 
 def _stat(t, rows: int, name: str):
@@ -551,22 +553,35 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
     axes may be strided as one). weight and bias: vectors of one type, not
     necessarily x's, or None. Returns (y, mean, rstd), the last two float32 with
     one element per row, for layer_norm_backward. ``out`` may be x."""
-    rows, dim, xs = _rows(_typed(x, "x"), "x")
-    w, b, wt = _affine(weight, bias, dim)
+    code = _typed(x, "x")
+    rows, dim, xs = _rows(x, "x")
+    w, wt = _vector(weight, dim, "weight")
+    b, bt = _vector(bias, dim, "bias")
+    if w is None:
+        wt = bt
+    elif b is not None and bt != wt:
+        raise TypeError("weight and bias must have the same type")
+    lead = x.shape[:-1]
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        ys = dim
+        out, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
     else:
-        orows, odim, ys = _rows(_typed(out, "out", x), "out")
+        _typed(out, "out", x)
+        ys = _rows(out, "out")[2]
         if out.shape != x.shape:
             raise ValueError("out and x shapes differ")
     if mean is None:
-        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mean = torch.empty(lead, dtype=torch.float32, device=x.device)
+        mp = mean.data_ptr()
+    else:
+        mp = _stat(mean, rows, "mean")
     if rstd is None:
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
+        rp = rstd.data_ptr()
+    else:
+        rp = _stat(rstd, rows, "rstd")
     _check("sparcml_layer_norm", _lib.load().sparcml_layer_norm(
-        x.data_ptr(), TYPES[x.dtype], xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys,
-        _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd"), _stream(stream)))
+        x.data_ptr(), code, xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys, mp, rp,
+        _raw_stream(stream, x)))
     return out, mean, rstd
 
 
@@ -580,30 +595,38 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     vectors, for example the layer's slices of a node's flat gradient; with
     ``accumulate`` the sums are added to what the given ones hold. ``dx`` may be
     dy or x."""
-    rows, dim, xs = _rows(_typed(x, "x"), "x")
-    _, _, ds = _rows(_typed(dy, "dy", x), "dy")
+    code = _typed(x, "x")
+    rows, dim, xs = _rows(x, "x")
+    _typed(dy, "dy", x)
+    ds = _rows(dy, "dy")[2]
     if dy.shape != x.shape:
         raise ValueError("dy and x shapes differ")
-    w, _, wt = _affine(weight, None, dim)
+    w, wt = _vector(weight, dim, "weight")
     if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        os = dim
+        dx, os = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
     else:
-        _, _, os = _rows(_typed(dx, "dx", x), "dx")
+        _typed(dx, "dx", x)
+        os = _rows(dx, "dx")[2]
         if dx.shape != x.shape:
             raise ValueError("dx and x shapes differ")
     if accumulate and (dweight is None or dbias is None):
         raise ValueError("accumulate needs dweight and dbias to add to")
     if dweight is None:
         dweight = torch.empty(dim, dtype=torch.float32, device=x.device)
+        dwp = dweight.data_ptr()
+    else:
+        dwp = _stat(dweight, dim, "dweight")
     if dbias is None:
         dbias = torch.empty(dim, dtype=torch.float32, device=x.device)
+        dbp = dbias.data_ptr()
+    else:
+        dbp = _stat(dbias, dim, "dbias")
     if ws is None:
         ws = workspace(layer_norm_backward_workspace_size(rows, dim), x.device)
     _check("sparcml_layer_norm_backward", _lib.load().sparcml_layer_norm_backward(
-        dy.data_ptr(), ds, x.data_ptr(), xs, TYPES[x.dtype], w, wt, _stat(mean, rows, "mean"),
-        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, _stat(dweight, dim, "dweight"),
-        _stat(dbias, dim, "dbias"), int(accumulate), ws.data_ptr(), ws.numel(), _stream(stream)))
+        dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt, _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dwp, dbp, int(accumulate),
+        ws.data_ptr(), ws.numel(), _raw_stream(stream, x)))
     return dx, dweight, dbias
 
 
@@ -649,7 +672,7 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
         ws = workspace(orthogonalize_workspace_size(batch, m, n), g.device)
     _check("sparcml_orthogonalize", _lib.load().sparcml_orthogonalize(
         g.data_ptr(), TYPES[g.dtype], gb, gs, out.data_ptr(), TYPES[out.dtype], ob, os, batch, m,
-        n, c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)))
+        n, c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(stream, g)))
     return out
 
 
@@ -677,5 +700,5 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     _check("sparcml_muon_step", _lib.load().sparcml_muon_step(
         weight.data_ptr(), TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb,
         gs, momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
-        c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _stream(stream)))
+        c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(stream, weight)))
     return weight, momentum

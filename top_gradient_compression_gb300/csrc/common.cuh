@@ -57,11 +57,14 @@ void note_launches(uint64_t n);
 // current device; the runtime call is made once per (device, kernel, size).
 bool ensure_smem(const void* func, size_t bytes);
 
-// Workspace header: the status word at byte 0, the fault-injection word at
+// Workspace header: the status word at byte 0, a ticket word at byte
+// kTicketOffset, the fault-injection word at
 // byte kInjectOffset (written by sparcml_set_fault_injection, kept across
 // calls). The word arms the injection only when it holds kInjectArmed, a
 // pattern that a workspace left uninitialised is very unlikely to contain.
 constexpr size_t kInjectOffset = 32;
+// Counts the blocks of a kernel that have finished; zero between kernels.
+constexpr size_t kTicketOffset = 16;
 constexpr uint8_t kInjectByte = 0xa5;
 constexpr uint32_t kInjectArmed = 0xa5a5a5a5u;
 // Polls of a bounded wait, normally and while a fault is injected (then a

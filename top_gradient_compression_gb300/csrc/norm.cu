@@ -17,19 +17,20 @@
 namespace sparcml {
 namespace {
 
-// Sum of two values over the threads that share a row: a warp, or the whole
-// block. `scratch` holds 2 * 33 float2 of shared memory; `turn` alternates
-// between its halves from call to call, so that one barrier per call is enough.
-template <bool BLOCK>
-__device__ __forceinline__ float2 row_sum(float2 v, float2* scratch, uint32_t& turn) {
+// Sum of two values over the `threads` threads that share a row: a warp, or a group of
+// whole warps with a named barrier and 2 * 33 float2 of shared memory of its own. `turn`
+// alternates between the halves of that from call to call, so that one barrier per
+// call is enough.
+__device__ __forceinline__ float2 row_sum(float2 v, uint32_t threads, uint32_t group,
+                                          float2* scratch, uint32_t& turn) {
   v.x = warp_sum_f(v.x);
   v.y = warp_sum_f(v.y);
-  if (!BLOCK) return v;
+  if (threads == 32) return v;
   float2* s = scratch + 33 * (turn & 1u);
   ++turn;
-  const uint32_t lane = lane_id(), nw = blockDim.x >> 5;
-  if (lane == 0) s[threadIdx.x >> 5] = v;
-  __syncthreads();
+  const uint32_t lane = lane_id(), nw = threads >> 5;
+  if (lane == 0) s[(threadIdx.x >> 5) - group * nw] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
   v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
   v.x = warp_sum_f(v.x);
   v.y = warp_sum_f(v.y);
@@ -44,22 +45,29 @@ __device__ __forceinline__ void load_affine(const void* w, int32_t type, bool ve
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = none;
   } else if (V > 1 && vec) {
+    // V = 4: one 16- or 8-byte access; V = 8: one of 16 bytes, or two
     if (type == SPARCML_F32) {
 #pragma unroll
       for (int q = 0; q < V / 4; ++q) {
         const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + 4 * q);
         out[4 * q] = f.x; out[4 * q + 1] = f.y; out[4 * q + 2] = f.z; out[4 * q + 3] = f.w;
       }
-    } else if (type == SPARCML_BF16) {
-      const auto p = *reinterpret_cast<const Pack<__nv_bfloat16, V>*>(
-          static_cast<const __nv_bfloat16*>(w) + c);
-#pragma unroll
-      for (int i = 0; i < V; ++i) out[i] = to_f32(p.e[i]);
     } else {
-      const auto p =
-          *reinterpret_cast<const Pack<__half, V>*>(static_cast<const __half*>(w) + c);
+      uint32_t h[V / 2 ? V / 2 : 1];
+      const uint16_t* p = static_cast<const uint16_t*>(w) + c;
+      if constexpr (V == 8) {
+        const uint4 q = *reinterpret_cast<const uint4*>(p);
+        h[0] = q.x; h[1] = q.y; h[2] = q.z; h[3] = q.w;
+      } else if constexpr (V == 4) {
+        const uint2 q = *reinterpret_cast<const uint2*>(p);
+        h[0] = q.x; h[1] = q.y;
+      }
 #pragma unroll
-      for (int i = 0; i < V; ++i) out[i] = to_f32(p.e[i]);
+      for (int e = 0; e < V / 2; ++e) {
+        const float2 f = type == SPARCML_BF16 ? unpack2<__nv_bfloat16>(h[e]) : unpack2<__half>(h[e]);
+        out[2 * e] = f.x;
+        out[2 * e + 1] = f.y;
+      }
     }
   } else {
 #pragma unroll
@@ -84,62 +92,77 @@ struct NormArgs {
 };
 
 // NV packs of V elements per thread; pack j of thread t starts at column
-// (j * threads + t) * V.
-template <typename T, int V, int NV, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 128) norm_forward_kernel(const NormArgs a) {
+// (j * threads + t) * V. A persistent grid: while a row is reduced and written, the next
+// one is already on its way into registers, which keeps 64 to 96 KB per SM in flight
+// (without it 16384 x 4096 bf16 took 62 us).
+template <typename T, int V, int NV, bool BLOCK, int MINB>
+__global__ void __launch_bounds__(BLOCK ? 1024 : 128, MINB) norm_forward_kernel(const NormArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
   uint32_t turn = 0;
   const uint32_t threads = BLOCK ? blockDim.x : 32u;
   const uint32_t t = BLOCK ? threadIdx.x : lane_id();
-  const uint64_t row = BLOCK ? blockIdx.x
-                             : (uint64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (!BLOCK && row >= a.rows) return;
-  const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride;
-  Pack<T, V> v[NV];
-  float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint64_t c = (uint64_t)(j * threads + t) * V;
-    if (c < a.dim) v[j] = *reinterpret_cast<const Pack<T, V>*>(x + c);
-  }
-#pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if ((uint64_t)(j * threads + t) * V < a.dim) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s.x += to_f32(v[j].e[i]);
-    }
+  const uint32_t per = BLOCK ? 1u : blockDim.x >> 5;
+  const uint64_t step = (uint64_t)gridDim.x * per;
+  uint64_t row = (uint64_t)blockIdx.x * per + (BLOCK ? 0u : threadIdx.x >> 5);
   const float inv = 1.0f / (float)a.dim;
-  const float mean = row_sum<BLOCK>(s, scratch, turn).x * inv;
-  s.x = 0.f;
+  Raw<T, V> v[NV], next[NV];
+  auto fetch = [&](Raw<T, V>(&to)[NV], uint64_t r) {
+    const T* x = static_cast<const T*>(a.x) + (int64_t)r * a.x_stride;
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if ((uint64_t)(j * threads + t) * V < a.dim) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float d = to_f32(v[j].e[i]) - mean;
-        s.x += d * d;
-      }
+    for (int j = 0; j < NV; ++j) {
+      const uint64_t c = (uint64_t)(j * threads + t) * V;
+      if (c < a.dim) to[j] = load_raw<T, V>(x + c);
     }
-  const float var = row_sum<BLOCK>(s, scratch, turn).x * inv;
-  const float rstd = 1.0f / sqrtf(var + a.eps);
-  if (t == 0) {
-    a.mean[row] = mean;
-    a.rstd[row] = rstd;
-  }
-  T* y = static_cast<T*>(a.y) + (int64_t)row * a.y_stride;
+  };
+  if (row < a.rows) fetch(next, row);
+  for (; row < a.rows; row += step) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const uint64_t c = (uint64_t)(j * threads + t) * V;
-    if (c < a.dim) {
-      float w[V], b[V];
-      load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
-      load_affine<V>(a.b, a.w_type, a.vec_w, c, 0.f, b);
-      Pack<T, V> o;
+    for (int j = 0; j < NV; ++j) v[j] = next[j];
+    if (row + step < a.rows) fetch(next, row + step);
+    float2 s = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        o.e[i] = from_f32<T>((to_f32(v[j].e[i]) - mean) * rstd * w[i] + b[i]);
-      *reinterpret_cast<Pack<T, V>*>(y + c) = o;
+    for (int j = 0; j < NV; ++j)
+      if ((uint64_t)(j * threads + t) * V < a.dim) {
+        float f[V];
+        unpack<T, V>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s.x += f[i];
+        v[j].forget();
+      }
+    const float mean = row_sum(s, threads, 0, scratch, turn).x * inv;
+    s.x = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if ((uint64_t)(j * threads + t) * V < a.dim) {
+        float f[V];
+        unpack<T, V>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = f[i] - mean;
+          s.x += d * d;
+        }
+        v[j].forget();
+      }
+    const float var = row_sum(s, threads, 0, scratch, turn).x * inv;
+    const float rstd = 1.0f / sqrtf(var + a.eps);
+    if (t == 0) {
+      a.mean[row] = mean;
+      a.rstd[row] = rstd;
+    }
+    T* y = static_cast<T*>(a.y) + (int64_t)row * a.y_stride;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint64_t c = (uint64_t)(j * threads + t) * V;
+      if (c < a.dim) {
+        float w[V], b[V], f[V];
+        load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
+        load_affine<V>(a.b, a.w_type, a.vec_w, c, 0.f, b);
+        unpack<T, V>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
+        store_raw<T, V>(y + c, pack<T, V>(f));
+      }
     }
   }
 }
@@ -156,13 +179,13 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs 
   const float inv = 1.0f / (float)a.dim;
   float2 s = make_float2(0.f, 0.f);
   for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) s.x += to_f32(x[c]);
-  const float mean = row_sum<true>(s, scratch, turn).x * inv;
+  const float mean = row_sum(s, blockDim.x, 0, scratch, turn).x * inv;
   s.x = 0.f;
   for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
     const float d = to_f32(x[c]) - mean;
     s.x += d * d;
   }
-  const float rstd = 1.0f / sqrtf(row_sum<true>(s, scratch, turn).x * inv + a.eps);
+  const float rstd = 1.0f / sqrtf(row_sum(s, blockDim.x, 0, scratch, turn).x * inv + a.eps);
   if (threadIdx.x == 0) {
     a.mean[blockIdx.x] = mean;
     a.rstd[blockIdx.x] = rstd;
@@ -188,24 +211,33 @@ struct NormGradArgs {
   uint64_t dim;
   void* dx;
   int64_t dx_stride;
-  float* part_w;  // [gridDim.x][dim] partial sums over the block's rows
+  float* part_w;  // [gridDim.x][dim] partial sums over the block's rows, or null
   float* part_b;
+  uint32_t threads;  // that share a row
+  uint32_t* ticket;  // null: norm_join_kernel joins the blocks' sums
+  float* dweight;
+  float* dbias;
+  int32_t accumulate;
 };
 
-// A block walks rows blockIdx.x, blockIdx.x + gridDim.x, ...; each thread keeps
-// the running dw and db of its own columns in registers, so x and dy are read
-// once for dx, dw and db together. Where a warp has a row of its own, the warps'
-// sums are joined in warp order at the end. Every order is fixed.
-template <typename T, int V, int NV, bool BLOCK, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormGradArgs a) {
+// A block's groups of `threads` threads walk the rows; each thread keeps the running dw and
+// db of its own columns in registers, so x and dy are read once for dx, dw and db
+// together. Rows of whole packs come through a ring in shared memory, in which each thread
+// copies ahead and reads back its own packs alone, so the ring needs no barrier. At the
+// end the groups' sums are joined in their order, and the blocks' by the last block to
+// finish (`ticket`, few sums) or by norm_join_kernel. Every order is fixed.
+constexpr int kRing = 3;
+
+template <typename T, int V, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
+norm_backward_kernel(const NormGradArgs a) {
   griddep_wait();
-  extern __shared__ float join[];  // !BLOCK: [2][dim]
-  __shared__ float2 scratch[66];
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float2 scratch[8 * 66];
+  __shared__ uint32_t last;
   uint32_t turn = 0;
-  const uint32_t threads = BLOCK ? blockDim.x : 32u;
-  const uint32_t t = BLOCK ? threadIdx.x : lane_id();
-  const uint32_t per = BLOCK ? 1u : blockDim.x >> 5;
-  const uint32_t slot = BLOCK ? 0u : threadIdx.x >> 5;
+  const uint32_t threads = a.threads, groups = blockDim.x / threads;
+  const uint32_t group = threadIdx.x / threads, t = threadIdx.x - group * threads;
   float gw[NV][V], gb[NV][V];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -213,19 +245,52 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormGradArgs 
     for (int i = 0; i < V; ++i) gw[j][i] = gb[j][i] = 0.f;
   }
   const float inv = 1.0f / (float)a.dim;
-  for (uint64_t row = (uint64_t)blockIdx.x * per + slot; row < a.rows;
-       row += (uint64_t)gridDim.x * per) {
-    const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride;
-    const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
-    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    Pack<T, V> vx[NV], vd[NV];
+  const uint64_t step = (uint64_t)gridDim.x * groups;
+  const uint64_t row0 = (uint64_t)blockIdx.x * groups + group;
+  auto fetch = [&](uint64_t row, uint32_t slot) {
+    if (row < a.rows) {
+      const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride;
+      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
+      uint8_t* to = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const uint64_t c = (uint64_t)(j * threads + t) * V;
-      if (c < a.dim) {
-        vx[j] = *reinterpret_cast<const Pack<T, V>*>(x + c);
-        vd[j] = *reinterpret_cast<const Pack<T, V>*>(dy + c);
+      for (int j = 0; j < NV; ++j) {
+        const uint64_t c = (uint64_t)(j * threads + t) * V;
+        if (c < a.dim) {
+          cp_async16(to + (uint64_t)j * blockDim.x * 16, x + c);
+          cp_async16(to + (uint64_t)(NV + j) * blockDim.x * 16, dy + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (V > 1) {
+#pragma unroll
+    for (int k = 0; k < kRing - 1; ++k) fetch(row0 + k * step, k);
+  }
+  uint32_t slot = 0;
+  for (uint64_t row = row0; row < a.rows; row += step) {
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    Raw<T, V> vx[NV], vd[NV];
+    if constexpr (V > 1) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      const uint8_t* from = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        vx[j].w = *reinterpret_cast<const uint4*>(from + (uint64_t)j * blockDim.x * 16);
+        vd[j].w = *reinterpret_cast<const uint4*>(from + (uint64_t)(NV + j) * blockDim.x * 16);
+      }
+      fetch(row + (kRing - 1) * step, slot == 0 ? kRing - 1 : slot - 1);
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+    } else {
+      const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride;
+      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint64_t c = (uint64_t)(j * threads + t) * V;
+        if (c < a.dim) {
+          vx[j] = load_raw<T, V>(x + c);
+          vd[j] = load_raw<T, V>(dy + c);
+        }
       }
     }
     float2 s = make_float2(0.f, 0.f);
@@ -233,40 +298,49 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormGradArgs 
     for (int j = 0; j < NV; ++j) {
       const uint64_t c = (uint64_t)(j * threads + t) * V;
       if (c < a.dim) {
-        float w[V];
+        float w[V], g[V], f[V];
         load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
+        unpack<T, V>(vd[j], g);
+        unpack<T, V>(vx[j], f);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float g = to_f32(vd[j].e[i]);
-          const float xh = (to_f32(vx[j].e[i]) - mean) * rstd;
-          gw[j][i] += g * xh;
-          gb[j][i] += g;
-          s.x += g * w[i];
-          s.y += g * w[i] * xh;
+          const float xh = (f[i] - mean) * rstd;
+          gw[j][i] += g[i] * xh;
+          gb[j][i] += g[i];
+          s.x += g[i] * w[i];
+          s.y += g[i] * w[i] * xh;
         }
+        vx[j].forget();
+        vd[j].forget();
       }
     }
-    s = row_sum<BLOCK>(s, scratch, turn);
+    s = row_sum(s, threads, group, scratch + 66 * group, turn);
     const float c1 = s.x * inv, c2 = s.y * inv;
+    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint64_t c = (uint64_t)(j * threads + t) * V;
       if (c < a.dim) {
-        float w[V];
+        float w[V], g[V], f[V];
         load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
-        Pack<T, V> o;
+        unpack<T, V>(vd[j], g);
+        unpack<T, V>(vx[j], f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (to_f32(vx[j].e[i]) - mean) * rstd;
-          o.e[i] = from_f32<T>(rstd * (to_f32(vd[j].e[i]) * w[i] - c1 - xh * c2));
-        }
-        *reinterpret_cast<Pack<T, V>*>(dx + c) = o;
+        for (int i = 0; i < V; ++i)
+          f[i] = rstd * (g[i] * w[i] - c1 - (f[i] - mean) * rstd * c2);
+        store_raw<T, V>(dx + c, pack<T, V>(f));
       }
     }
   }
-  if constexpr (!BLOCK) {
-    for (uint32_t k = 0; k < per; ++k) {
-      if (slot == k) {
+  if (a.part_w == nullptr) return;  // neither sum is wanted
+  float* to_w = a.part_w + (uint64_t)blockIdx.x * a.dim;
+  float* to_b = a.part_b + (uint64_t)blockIdx.x * a.dim;
+  if (groups > 1) {
+    float* join = reinterpret_cast<float*>(dynamic);  // [2][dim]
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncthreads();
+    for (uint32_t k = 0; k < groups; ++k) {
+      if (group == k) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -282,8 +356,8 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormGradArgs 
       __syncthreads();
     }
     for (uint32_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-      a.part_w[(uint64_t)blockIdx.x * a.dim + c] = join[c];
-      a.part_b[(uint64_t)blockIdx.x * a.dim + c] = join[a.dim + c];
+      to_w[c] = join[c];
+      to_b[c] = join[a.dim + c];
     }
   } else {
 #pragma unroll
@@ -292,12 +366,30 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(const NormGradArgs 
       for (int i = 0; i < V; ++i) {
         const uint64_t c = (uint64_t)(j * threads + t) * V + i;
         if (c < a.dim) {
-          a.part_w[(uint64_t)blockIdx.x * a.dim + c] = gw[j][i];
-          a.part_b[(uint64_t)blockIdx.x * a.dim + c] = gb[j][i];
+          to_w[c] = gw[j][i];
+          to_b[c] = gb[j][i];
         }
       }
     }
   }
+  if (a.ticket == nullptr) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (uint32_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
+    float w = 0.f, b = 0.f;
+#pragma unroll 4
+    for (uint32_t p = 0; p < gridDim.x; ++p) {
+      w += __ldcg(a.part_w + (uint64_t)p * a.dim + c);
+      b += __ldcg(a.part_b + (uint64_t)p * a.dim + c);
+    }
+    if (a.dweight) a.dweight[c] = a.accumulate ? a.dweight[c] + w : w;
+    if (a.dbias) a.dbias[c] = a.accumulate ? a.dbias[c] + b : b;
+  }
+  if (threadIdx.x == 0) *a.ticket = 0;  // as the next call needs it
 }
 
 // Rows too long for a block's registers: dx by re-reading the row, the column
@@ -318,7 +410,7 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGrad
     s.x += d;
     s.y += d * ((to_f32(x[c]) - mean) * rstd);
   }
-  s = row_sum<true>(s, scratch, turn);
+  s = row_sum(s, blockDim.x, 0, scratch, turn);
   const float c1 = s.x * inv, c2 = s.y * inv;
   for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
     const float d = to_f32(dy[c]) * (a.w ? load_any(a.w, a.w_type, c) : 1.f);
@@ -376,78 +468,88 @@ uint32_t threads_for(uint64_t dim, uint32_t per) {
   return (uint32_t)((dim + 32ull * per - 1) / (32ull * per)) * 32u;
 }
 
-constexpr uint32_t kForwardPer = 32, kForwardPer1 = 16;  // elements per thread, V > 1 and V = 1
-constexpr uint32_t kBackwardPer = 16;
+constexpr uint32_t kSms = 152;
 
-template <typename T, int V, int NV>
+template <typename T, int V, int NV, bool BLOCK, int MINB>
 void launch_forward(const NormArgs& a, cudaStream_t s) {
-  const uint32_t threads = threads_for(a.dim, V * NV);
-  if (threads == 32)
-    launch_pdl(norm_forward_kernel<T, V, NV, false>, (unsigned)((a.rows + 3) / 4), 128, 0, s, a);
-  else
-    launch_pdl(norm_forward_kernel<T, V, NV, true>, (unsigned)a.rows, threads, 0, s, a);
+  const uint32_t threads = BLOCK ? threads_for(a.dim, V * NV) : 128;
+  const uint64_t work = BLOCK ? a.rows : (a.rows + 3) / 4;
+  const uint32_t fit = kSms * (BLOCK ? std::max(1u, std::min(16u, 1024 / threads)) : MINB);
+  launch_pdl(norm_forward_kernel<T, V, NV, BLOCK, MINB>, (unsigned)std::min<uint64_t>(work, fit),
+             threads, 0, s, a);
 }
 
-// Packs of 16 bytes need 16-byte aligned rows and a whole number of packs; other
-// rows are read element by element.
+// Packs of 16 bytes need 16-byte aligned rows and a whole number of packs; other rows
+// are read element by element. A warp takes a row of up to 16 packs per lane, which needs
+// no barrier; a block takes longer ones.
 template <typename T>
 void forward_typed(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const bool vec = a.dim % V == 0 && a.x_stride % V == 0 && a.y_stride % V == 0 &&
                    aligned_to(a.x, 16) && aligned_to(a.y, 16);
-  if (vec && a.dim <= 1024ull * kForwardPer)
-    launch_forward<T, V, kForwardPer / V>(a, s);
-  else if (a.dim <= 1024ull * kForwardPer1)
-    launch_forward<T, 1, kForwardPer1>(a, s);
-  else
-    launch_pdl(norm_forward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
+  const uint64_t packs = a.dim / V;
+  if (vec && packs <= 32) launch_forward<T, V, 1, false, 11>(a, s);
+  else if (vec && packs <= 64) launch_forward<T, V, 2, false, 10>(a, s);
+  else if (vec && packs <= 128) launch_forward<T, V, 4, false, 7>(a, s);
+  else if (vec && packs <= 256) launch_forward<T, V, 8, false, 4>(a, s);
+  else if (vec && packs <= 512) launch_forward<T, V, 16, false, 3>(a, s);
+  else if (vec && packs <= 4 * 1024) launch_forward<T, V, 4, true, 1>(a, s);
+  else if (a.dim <= 32 * 16) launch_forward<T, 1, 16, false, 5>(a, s);
+  else if (a.dim <= 1024 * 8) launch_forward<T, 1, 8, true, 1>(a, s);
+  else launch_pdl(norm_forward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
 }
 
-// Blocks of the backward pass, each with a row of partial sums: enough to fill
-// 152 SMs, no more than there are rows. A function of the sizes alone, so that
-// the workspace and the order of the sums do not depend on the device's state.
-uint32_t backward_parts(uint64_t rows, uint64_t dim) {
-  const uint32_t threads = threads_for(dim, kBackwardPer);
-  uint64_t groups = rows, most = 152;
-  if (threads == 32) {
-    groups = (rows + 7) / 8;
-    most = 152 * 4;
-  } else if (threads <= 512) {
-    most = 152ull * std::min(4u, 1024u / threads);
-  }
-  return (uint32_t)std::max<uint64_t>(1, std::min(groups, most));
-}
+constexpr uint32_t kBackwardPer = 16;  // elements per thread
 
-template <typename T, int V>
-void launch_backward(const NormGradArgs& a, uint32_t parts, cudaStream_t s) {
+// Threads of a row and of a block, and the blocks, each with a row of partial sums:
+// three blocks per SM, no more than there are rows. A function of the sizes alone, so
+// that the workspace and the order of the sums do not depend on the device's state.
+struct BackwardShape {
+  uint32_t threads, block, parts;
+};
+BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
+  const uint32_t threads = (uint32_t)std::min<uint64_t>(512, threads_for(dim, kBackwardPer));
+  const uint32_t groups = std::max(1u, 256 / threads);
+  const uint64_t most = kSms * (threads <= 256 ? 3 : 1);
+  return {threads, threads * groups,
+          (uint32_t)std::max<uint64_t>(1, std::min((rows + groups - 1) / groups, most))};
+}
+// One block joins up to this many partial sums in less time than a launch takes.
+constexpr uint64_t kTicketSums = 16 * 1024;
+
+template <typename T, int V, int MAXT, int MINB>
+bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
   constexpr int NV = kBackwardPer / V;
-  const uint32_t threads = threads_for(a.dim, kBackwardPer);
-  if (threads == 32)
-    launch_pdl(norm_backward_kernel<T, V, NV, false, 256>, parts, 256, 2 * a.dim * sizeof(float),
-               s, a);
-  else if (threads <= 256)
-    launch_pdl(norm_backward_kernel<T, V, NV, true, 256>, parts, threads, 0, s, a);
-  else
-    launch_pdl(norm_backward_kernel<T, V, NV, true, 512>, parts, threads, 0, s, a);
+  auto kernel = norm_backward_kernel<T, V, NV, MAXT, MINB>;
+  const size_t ring = V > 1 ? (size_t)kRing * 2 * NV * h.block * 16 : 0;
+  const size_t join = h.block > h.threads ? 2 * a.dim * sizeof(float) : 0;
+  const size_t smem = std::max(ring, join);
+  if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
+  launch_pdl(kernel, h.parts, h.block, smem, s, a);
+  return true;
 }
 
 template <typename T>
-void backward_typed(const NormGradArgs& a, uint32_t parts, cudaStream_t s) {
+bool backward_typed(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const bool vec = a.dim % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 &&
                    a.dx_stride % V == 0 && aligned_to(a.x, 16) && aligned_to(a.dy, 16) &&
                    aligned_to(a.dx, 16);
   if (a.dim > 512ull * kBackwardPer) {
     launch_pdl(norm_backward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
-    launch_pdl(norm_columns_kernel<T>, dim3((unsigned)((a.dim + 255) / 256), parts), 256, 0, s, a);
-    note_launches(2);
-    return;
+    note_launches(1);
+    if (a.part_w) {
+      launch_pdl(norm_columns_kernel<T>, dim3((unsigned)((a.dim + 255) / 256), h.parts), 256, 0, s,
+                 a);
+      note_launches(1);
+    }
+    return true;
   }
-  if (vec)
-    launch_backward<T, V>(a, parts, s);
-  else
-    launch_backward<T, 1>(a, parts, s);
   note_launches(1);
+  if (h.block <= 256)
+    return vec ? launch_backward<T, V, 256, sizeof(T) == 2 ? 3 : 2>(a, h, s)
+               : launch_backward<T, 1, 256, 2>(a, h, s);
+  return vec ? launch_backward<T, V, 512, 1>(a, h, s) : launch_backward<T, 1, 512, 1>(a, h, s);
 }
 
 bool rows_ok(uint64_t rows, uint64_t dim) {
@@ -485,7 +587,7 @@ extern "C" int sparcml_layer_norm(const void* x, int32_t type, int64_t x_stride,
 
 extern "C" size_t sparcml_layer_norm_backward_workspace_size(uint64_t rows, uint64_t dim) {
   if (!rows_ok(rows, dim)) return 0;
-  return 256 + align_up(2 * sizeof(float) * dim * backward_parts(rows, dim), 256);
+  return 256 + align_up(2 * sizeof(float) * dim * backward_shape(rows, dim).parts, 256);
 }
 
 extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x,
@@ -508,21 +610,27 @@ extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, co
   if (ws_bytes < sparcml_layer_norm_backward_workspace_size(rows, dim))
     return SPARCML_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const uint32_t parts = rows ? backward_parts(rows, dim) : 0;
+  const BackwardShape h = backward_shape(rows, dim);
+  const bool sums = dweight || dbias;
   float* part_w = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
-  float* part_b = part_w + (uint64_t)parts * dim;
+  float* part_b = part_w + (uint64_t)h.parts * dim;
+  bool joined = !sums;
   if (rows) {
-    const NormGradArgs a{dy,   dy_stride, x,   x_stride, weight, weight_type,
-                         aligned_to(weight, 16), mean, rstd, rows, dim, dx,
-                         rows > 1 ? dx_stride : 0, part_w, part_b};
-    if (type == SPARCML_F32) backward_typed<float>(a, parts, s);
-    else if (type == SPARCML_BF16) backward_typed<__nv_bfloat16>(a, parts, s);
-    else backward_typed<__half>(a, parts, s);
-    if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+    NormGradArgs a{dy, dy_stride, x, x_stride, weight, weight_type, aligned_to(weight, 16), mean,
+                   rstd, rows, dim, dx, rows > 1 ? dx_stride : 0, sums ? part_w : nullptr, part_b,
+                   h.threads, nullptr, dweight, dbias, accumulate};
+    if (sums && dim <= 512ull * kBackwardPer && h.parts * dim <= kTicketSums) {
+      a.ticket = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kTicketOffset);
+      joined = true;
+    }
+    const bool ok = type == SPARCML_F32    ? backward_typed<float>(a, h, s)
+                    : type == SPARCML_BF16 ? backward_typed<__nv_bfloat16>(a, h, s)
+                                           : backward_typed<__half>(a, h, s);
+    if (launch_status() != SPARCML_OK || !ok) return SPARCML_ERR_CUDA;
   }
-  if (dweight || dbias) {
+  if (!joined) {
     launch_pdl(norm_join_kernel, dim3((unsigned)((dim + 31) / 32), 2), 512, 0, s, part_w, part_b,
-               parts, dim, dweight, dbias, accumulate);
+               rows ? h.parts : 0u, dim, dweight, dbias, accumulate);
     if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
     note_launches(1);
   }

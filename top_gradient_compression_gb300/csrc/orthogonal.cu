@@ -697,28 +697,30 @@ __device__ void join_parts(const StepArgs& a, const Product& p) {
   }
 }
 
-// The scaled input as a pair of fp16. 2^12 / |U| is applied as two factors, each a
-// normal number, whatever the size of |U|.
+// 2^12 / |U| as two factors, each a normal number whatever the size of |U|.
 __device__ __forceinline__ void norm_factors(const GatherArgs& g, uint64_t b, float& f0,
                                              float& f1) {
-  double t[3] = {0.0, 0.0, 0.0};
+  float t[3] = {0.f, 0.f, 0.f};
   for (uint32_t k = lane_id(); k < g.blocks; k += 32)
-    for (int q = 0; q < 3; ++q) t[q] += (double)__ldcg(g.sums + (b * g.blocks + k) * 3 + q);
-  for (int d = 16; d > 0; d >>= 1)
-    for (int q = 0; q < 3; ++q) t[q] += __shfl_xor_sync(0xffffffffu, t[q], d);
-  const double norm = sqrt(t[0] * 0x1p-160 + t[1] + t[2] * 0x1p180);
-  if (!(norm < __longlong_as_double(0x7ff0000000000000ll))) {
+    for (int q = 0; q < 3; ++q) t[q] += __ldcg(g.sums + (b * g.blocks + k) * 3 + q);
+  for (int q = 0; q < 3; ++q) t[q] = warp_sum_f(t[q]);
+  // |U|^2 = t0 2^-160 + t1 + t2 2^180, in the unit of the largest range that has any
+  const float all = t[0] + t[1] + t[2];
+  if (!(all < __int_as_float(0x7f800000))) {
     f0 = f1 = __int_as_float(0x7fffffff);  // an inf or a NaN in U: all of X is NaN
-  } else if (norm > 0.0) {
-    int e;
-    const double mant = frexp(norm, &e);
-    f0 = ldexpf(1.f, -e / 2);
-    f1 = (float)(ldexp((double)kScaleX, -(e + -e / 2)) / mant);
+  } else if (t[2] > 0.f) {
+    f0 = 0x1p-90f;
+    f1 = kScaleX / sqrtf(t[2] + t[1] * 0x1p-90f * 0x1p-90f);
+  } else if (t[1] > 0.f) {
+    f0 = 1.f;
+    f1 = kScaleX / sqrtf(t[1] + t[0] * 0x1p-80f * 0x1p-80f);
   } else {
-    f0 = f1 = 0.f;
+    f0 = 0x1p80f;
+    f1 = t[0] > 0.f ? kScaleX / sqrtf(t[0]) : 0.f;
   }
 }
 
+// The scaled input as a pair of fp16.
 __device__ void split_input(const StepArgs& a) {
   const GatherArgs& g = a.g;
   const uint64_t pieces = (g.n + kPiece - 1) / kPiece, total = (uint64_t)a.batch * g.m * pieces;
