@@ -17,62 +17,126 @@
 namespace sparcml {
 namespace {
 
-// Sum of two values over the `threads` threads that share a row: a warp, or a group of
-// whole warps with a named barrier and 2 * 33 float2 of shared memory of its own. `turn`
-// alternates between the halves of that from call to call, so that one barrier per
-// call is enough.
-__device__ __forceinline__ float2 row_sum(float2 v, uint32_t threads, uint32_t group,
-                                          float2* scratch, uint32_t& turn) {
-  v.x = warp_sum_f(v.x);
-  v.y = warp_sum_f(v.y);
-  if (threads == 32) return v;
-  float2* s = scratch + 33 * (turn & 1u);
-  ++turn;
-  const uint32_t lane = lane_id(), nw = threads >> 5;
-  if (lane == 0) s[(threadIdx.x >> 5) - group * nw] = v;
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(threads) : "memory");
-  v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
-  v.x = warp_sum_f(v.x);
-  v.y = warp_sum_f(v.y);
-  return v;
+// The `threads` threads that share a row: 8, 16 or 32 lanes of a warp, or whole warps
+// with a named barrier and 2 * 33 float2 of shared memory of their own.
+struct Group {
+  uint32_t threads, index, t;  // their number, which group of the block, this thread's place
+  float2* scratch;
+  uint32_t turn;
+
+  __device__ __forceinline__ void sync() const {
+    if (threads > 32)
+      asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(threads) : "memory");
+    else
+      __syncwarp();
+  }
+  __device__ __forceinline__ float sum(float2 v) { return sum2(make_float2(v.x + v.y, 0.f)).x; }
+  // Sums of two values. `turn` alternates between the halves of the scratch from call to
+  // call, so that one barrier per call is enough.
+  __device__ __forceinline__ float2 sum2(float2 v) {
+    const uint32_t width = threads < 32 ? threads : 32;
+    for (uint32_t d = width >> 1; d > 0; d >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+    }
+    if (threads <= 32) return v;
+    float2* s = scratch + 33 * (turn & 1u);
+    ++turn;
+    const uint32_t lane = lane_id(), nw = threads >> 5;
+    if (lane == 0) s[t >> 5] = v;
+    sync();
+    v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
+    for (uint32_t d = nw > 16 ? 16 : nw > 8 ? 8 : nw > 4 ? 4 : nw > 2 ? 2 : 1; d > 0; d >>= 1) {
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+    }
+    // the lanes that were added up hold the sum; the first one tells the rest
+    v.x = __shfl_sync(0xffffffffu, v.x, 0);
+    v.y = __shfl_sync(0xffffffffu, v.y, 0);
+    return v;
+  }
+};
+__device__ __forceinline__ Group make_group(uint32_t threads, float2* scratch) {
+  const uint32_t index = threadIdx.x / threads;
+  return {threads, index, threadIdx.x - index * threads, scratch + 66 * index, 0};
 }
 
-// V weights from column c; 1 where there is no weight.
-template <int V>
-__device__ __forceinline__ void load_affine(const void* w, int32_t type, bool vec, uint64_t c,
-                                            float none, float (&out)[V]) {
+// A row on its way into shared memory, as the aligned pieces of 16 bytes that cover it;
+// element c comes to lie at slot + row_skew + c. What a first piece holds before the row
+// is not used; where it could lie before the array, its elements are copied one by one.
+template <typename T>
+__device__ __forceinline__ uint32_t row_skew(const T* row) {
+  return (uint32_t)((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+}
+template <typename T>
+__device__ __forceinline__ void copy_row(T* slot, const T* row, uint32_t dim, uint64_t before,
+                                         const Group& g) {
+  const uint32_t skew = row_skew(row), per = 16 / sizeof(T);
+  const uint32_t pieces = (skew + dim + per - 1) / per;
+  const T* start = row - skew;
+  for (uint32_t p = g.t; p < pieces; p += g.threads) {
+    if (p == 0 && before < skew) {
+      for (uint32_t e = skew; e < min(per, skew + dim); ++e) slot[e] = start[e];
+    } else {
+      const uint32_t bytes = (uint32_t)min(16u, (skew + dim - p * per) * (uint32_t)sizeof(T));
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       (uint32_t)__cvta_generic_to_shared(slot + p * per)),
+                   "l"(start + p * per), "r"(bytes)
+                   : "memory");
+    }
+  }
+}
+// Elements that a slot for such a row takes: the row, its skew and the last piece's rest.
+__host__ __device__ constexpr uint32_t slot_elements(uint32_t dim, uint32_t bytes) {
+  const uint32_t per = 16 / bytes;
+  return (dim + 2 * per - 2) / per * per + per;
+}
+
+// V weights of type W from column c, as fp32 pairs; `none` where there are none.
+template <typename W, int V>
+__device__ __forceinline__ void load_affine(const void* w, uint32_t c, float none,
+                                            F2 (&out)[V / 2]) {
   if (w == nullptr) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = none;
-  } else if (V > 1 && vec) {
-    // V = 4: one 16- or 8-byte access; V = 8: one of 16 bytes, or two
-    if (type == SPARCML_F32) {
+    for (int e = 0; e < V / 2; ++e) out[e] = f2(none, none);
+    return;
+  }
+  const W* p = static_cast<const W*>(w) + c;
+  if constexpr (sizeof(W) == 4) {
 #pragma unroll
-      for (int q = 0; q < V / 4; ++q) {
-        const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + 4 * q);
-        out[4 * q] = f.x; out[4 * q + 1] = f.y; out[4 * q + 2] = f.z; out[4 * q + 3] = f.w;
-      }
-    } else {
-      uint32_t h[V / 2 ? V / 2 : 1];
-      const uint16_t* p = static_cast<const uint16_t*>(w) + c;
-      if constexpr (V == 8) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p);
-        h[0] = q.x; h[1] = q.y; h[2] = q.z; h[3] = q.w;
-      } else if constexpr (V == 4) {
-        const uint2 q = *reinterpret_cast<const uint2*>(p);
-        h[0] = q.x; h[1] = q.y;
-      }
-#pragma unroll
-      for (int e = 0; e < V / 2; ++e) {
-        const float2 f = type == SPARCML_BF16 ? unpack2<__nv_bfloat16>(h[e]) : unpack2<__half>(h[e]);
-        out[2 * e] = f.x;
-        out[2 * e + 1] = f.y;
-      }
+    for (int q = 0; q < V / 4; ++q) {
+      const float4 f = *reinterpret_cast<const float4*>(p + 4 * q);
+      out[2 * q] = f2(f.x, f.y);
+      out[2 * q + 1] = f2(f.z, f.w);
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) out[i] = load_any(w, type, c + i);
+    unpack<W, 8>(load_raw<W, 8>(p), out);
   }
+}
+
+// Columns of a thread. Rows of whole packs (V = 4 or 8): pack j of thread t starts at
+// column (j * threads + t) * V. Other rows (V = 2): its pair j is columns 2 j * threads + t
+// and `threads` further, so that a warp's accesses are consecutive elements.
+template <int V>
+__device__ __forceinline__ uint32_t column(int j, int i, uint32_t threads, uint32_t t) {
+  return V == 2 ? (2 * j + i) * threads + t : (j * threads + t) * V + i;
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* row, int j, uint32_t threads, uint32_t t,
+                                           uint32_t dim, const F2 (&f)[V / 2]) {
+  if constexpr (V == 2) {
+    const float2 p = split(f[0]);
+    const uint32_t c0 = column<V>(j, 0, threads, t), c1 = c0 + threads;
+    row[c0] = from_f32<T>(p.x);
+    if (c1 < dim) row[c1] = from_f32<T>(p.y);
+  } else {
+    *reinterpret_cast<uint4*>(row + column<V>(j, 0, threads, t)) = pack<T, V>(f);
+  }
+}
+// Such a pair of a vector in shared memory; zero beyond its end.
+template <typename T>
+__device__ __forceinline__ F2 pair_at(const T* v, uint32_t c0, uint32_t c1, uint32_t dim) {
+  return f2(to_f32(v[c0]), c1 < dim ? to_f32(v[c1]) : 0.f);
 }
 
 struct NormArgs {
@@ -81,7 +145,6 @@ struct NormArgs {
   const void* w;     // may be null: all ones
   const void* b;     // may be null: all zeros
   int32_t w_type;
-  int32_t vec_w;  // w and b may be read V at a time
   uint64_t rows;
   uint64_t dim;
   float eps;
@@ -89,79 +152,133 @@ struct NormArgs {
   int64_t y_stride;
   float* mean;
   float* rstd;
+  uint32_t threads;  // that share a row
 };
 
-// NV packs of V elements per thread; pack j of thread t starts at column
-// (j * threads + t) * V. A persistent grid: while a row is reduced and written, the next
-// one is already on its way into registers, which keeps 64 to 96 KB per SM in flight
-// (without it 16384 x 4096 bf16 took 62 us).
-template <typename T, int V, int NV, bool BLOCK, int MINB>
-__global__ void __launch_bounds__(BLOCK ? 1024 : 128, MINB) norm_forward_kernel(const NormArgs a) {
+// A persistent grid: while a row is reduced and written, the next one is already on its
+// way, which keeps 64 to 96 KB per SM in flight. Rows of whole, aligned packs go into
+// registers; others (V = 2) through shared memory, where the weights wait in fp32. (Loaded
+// from memory one element at a time, 16384 x 4095 bf16 took 181 us.)
+template <typename T, typename W, int V, int NV, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs a) {
   griddep_wait();
-  __shared__ float2 scratch[66];
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float2 scratch[MAXT >= 64 ? 66 * (MAXT / 64) : 1];
+  constexpr bool PACKS = V > 2;
+  constexpr int P = V / 2;
+  Group g = make_group(a.threads, scratch);
+  const uint32_t threads = a.threads, groups = blockDim.x / threads, dim = (uint32_t)a.dim;
+  const uint32_t t = g.t;
+  const uint64_t step = (uint64_t)gridDim.x * groups;
+  const float inv = 1.0f / (float)dim;
+  const T* xs = static_cast<const T*>(a.x);
+  // V = 2: [2][dim] weights, then two slots for each group
+  float* affine = reinterpret_cast<float*>(dynamic);
+  const uint32_t slot_size = slot_elements(dim, sizeof(T));
+  T* slots = reinterpret_cast<T*>(dynamic + (2 * dim * sizeof(float) + 15) / 16 * 16) +
+             (uint64_t)g.index * 2 * slot_size;
   uint32_t turn = 0;
-  const uint32_t threads = BLOCK ? blockDim.x : 32u;
-  const uint32_t t = BLOCK ? threadIdx.x : lane_id();
-  const uint32_t per = BLOCK ? 1u : blockDim.x >> 5;
-  const uint64_t step = (uint64_t)gridDim.x * per;
-  uint64_t row = (uint64_t)blockIdx.x * per + (BLOCK ? 0u : threadIdx.x >> 5);
-  const float inv = 1.0f / (float)a.dim;
   Raw<T, V> v[NV], next[NV];
-  auto fetch = [&](Raw<T, V>(&to)[NV], uint64_t r) {
-    const T* x = static_cast<const T*>(a.x) + (int64_t)r * a.x_stride;
+  auto fetch = [&](uint64_t row, uint32_t slot) {
+    if (row < a.rows) {
+      const T* x = xs + (int64_t)row * a.x_stride;
+      if constexpr (PACKS) {
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const uint64_t c = (uint64_t)(j * threads + t) * V;
-      if (c < a.dim) to[j] = load_raw<T, V>(x + c);
-    }
-  };
-  if (row < a.rows) fetch(next, row);
-  for (; row < a.rows; row += step) {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) v[j] = next[j];
-    if (row + step < a.rows) fetch(next, row + step);
-    float2 s = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if ((uint64_t)(j * threads + t) * V < a.dim) {
-        float f[V];
-        unpack<T, V>(v[j], f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) s.x += f[i];
-        v[j].forget();
-      }
-    const float mean = row_sum(s, threads, 0, scratch, turn).x * inv;
-    s.x = 0.f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-      if ((uint64_t)(j * threads + t) * V < a.dim) {
-        float f[V];
-        unpack<T, V>(v[j], f);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = f[i] - mean;
-          s.x += d * d;
+        for (int j = 0; j < NV; ++j) {
+          const uint32_t c = column<V>(j, 0, threads, t);
+          if (c < dim) next[j] = load_raw<T, V>(x + c);
         }
+      } else {
+        copy_row(slots + slot * slot_size, x, dim, row * (uint64_t)a.x_stride, g);
+      }
+    }
+    if constexpr (!PACKS) asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if constexpr (!PACKS) {
+    for (uint32_t c = threadIdx.x; c < dim; c += blockDim.x) {
+      affine[c] = a.w ? load_any(a.w, a.w_type, c) : 1.f;
+      affine[dim + c] = a.b ? load_any(a.b, a.w_type, c) : 0.f;
+    }
+  }
+  uint64_t base = (uint64_t)blockIdx.x * groups;
+  fetch(base + g.index, 0);
+  if constexpr (!PACKS) __syncthreads();
+  for (; base < a.rows; base += step) {  // the same turns for all groups
+    const uint64_t row = base + g.index;
+    const bool active = row < a.rows;
+    const uint32_t end = active ? dim : 0;
+    if constexpr (PACKS) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) v[j] = next[j];
+      fetch(row + step, 0);
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      g.sync();
+      const T* x = slots + turn * slot_size + (active ? row_skew(xs + (int64_t)row * a.x_stride) : 0);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const uint32_t c = column<V>(j, 0, threads, t);
+        if (c < end) v[j].w = pair_at(x, c, c + threads, dim);
+      }
+      turn ^= 1u;
+      fetch(row + step, turn);
+    }
+    F2 s = f2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (column<V>(j, 0, threads, t) < end) {
+        F2 f[P];
+        unpack<T, V>(v[j], f);
+#pragma unroll
+        for (int d = 1; d < P; d *= 2) {
+#pragma unroll
+          for (int i = 0; i < P; i += 2 * d) f[i] = f[i] + f[i + d];
+        }
+        s = s + f[0];
         v[j].forget();
       }
-    const float var = row_sum(s, threads, 0, scratch, turn).x * inv;
+    const float mean = g.sum(split(s)) * inv;
+    s = f2(0.f, 0.f);
+    const F2 minus = f2(-mean, -mean);
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (column<V>(j, 0, threads, t) < end) {
+        F2 f[P], q = f2(0.f, 0.f);
+        unpack<T, V>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          f[i] = f[i] + minus;
+          if (!PACKS && column<V>(j, 1, threads, t) >= dim) f[i] = f2(split(f[i]).x, 0.f);
+          q = fma2(f[i], f[i], q);
+        }
+        s = s + q;
+        v[j].forget();
+      }
+    const float var = g.sum(split(s)) * inv;
     const float rstd = 1.0f / sqrtf(var + a.eps);
+    if (!active) continue;
     if (t == 0) {
       a.mean[row] = mean;
       a.rstd[row] = rstd;
     }
+    const F2 by = f2(rstd, rstd);
     T* y = static_cast<T*>(a.y) + (int64_t)row * a.y_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint64_t c = (uint64_t)(j * threads + t) * V;
-      if (c < a.dim) {
-        float w[V], b[V], f[V];
-        load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
-        load_affine<V>(a.b, a.w_type, a.vec_w, c, 0.f, b);
+      const uint32_t c = column<V>(j, 0, threads, t);
+      if (c < dim) {
+        F2 w[P], b[P], f[P];
+        if constexpr (PACKS) {
+          load_affine<W, V>(a.w, c, 1.f, w);
+          load_affine<W, V>(a.b, c, 0.f, b);
+        } else {
+          w[0] = pair_at(affine, c, c + threads, dim);
+          b[0] = pair_at(affine + dim, c, c + threads, dim);
+        }
         unpack<T, V>(v[j], f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
-        store_raw<T, V>(y + c, pack<T, V>(f));
+        for (int i = 0; i < P; ++i) f[i] = fma2((f[i] + minus) * by, w[i], b[i]);
+        store_pack<T, V>(y, j, threads, t, dim, f);
       }
     }
   }
@@ -173,19 +290,19 @@ template <typename T>
 __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
-  uint32_t turn = 0;
+  Group g = make_group(blockDim.x, scratch);
   const T* x = static_cast<const T*>(a.x) + (int64_t)blockIdx.x * a.x_stride;
   T* y = static_cast<T*>(a.y) + (int64_t)blockIdx.x * a.y_stride;
   const float inv = 1.0f / (float)a.dim;
   float2 s = make_float2(0.f, 0.f);
   for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) s.x += to_f32(x[c]);
-  const float mean = row_sum(s, blockDim.x, 0, scratch, turn).x * inv;
+  const float mean = g.sum(s) * inv;
   s.x = 0.f;
   for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
     const float d = to_f32(x[c]) - mean;
     s.x += d * d;
   }
-  const float rstd = 1.0f / sqrtf(row_sum(s, blockDim.x, 0, scratch, turn).x * inv + a.eps);
+  const float rstd = 1.0f / sqrtf(g.sum(s) * inv + a.eps);
   if (threadIdx.x == 0) {
     a.mean[blockIdx.x] = mean;
     a.rstd[blockIdx.x] = rstd;
@@ -204,7 +321,6 @@ struct NormGradArgs {
   int64_t x_stride;
   const void* w;
   int32_t w_type;
-  int32_t vec_w;
   const float* mean;
   const float* rstd;
   uint64_t rows;
@@ -222,117 +338,162 @@ struct NormGradArgs {
 
 // A block's groups of `threads` threads walk the rows; each thread keeps the running dw and
 // db of its own columns in registers, so x and dy are read once for dx, dw and db
-// together. Rows of whole packs come through a ring in shared memory, in which each thread
-// copies ahead and reads back its own packs alone, so the ring needs no barrier. At the
+// together. Rows of whole, aligned packs come through a ring in shared memory, in which
+// each thread copies ahead and reads back its own packs alone, so the ring needs no
+// barrier; other rows (V = 2) as in the forward pass. At the
 // end the groups' sums are joined in their order, and the blocks' by the last block to
 // finish (`ticket`, few sums) or by norm_join_kernel. Every order is fixed.
 constexpr int kRing = 3;
 
-template <typename T, int V, int NV, int MAXT, int MINB>
+template <typename T, typename W, int V, int NV, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB)
 norm_backward_kernel(const NormGradArgs a) {
   griddep_wait();
   extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ float2 scratch[8 * 66];
+  __shared__ float2 scratch[66 * (MAXT / 64)];
   __shared__ uint32_t last;
-  uint32_t turn = 0;
-  const uint32_t threads = a.threads, groups = blockDim.x / threads;
-  const uint32_t group = threadIdx.x / threads, t = threadIdx.x - group * threads;
-  float gw[NV][V], gb[NV][V];
+  Group g = make_group(a.threads, scratch);
+  const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
+  const uint32_t dim = (uint32_t)a.dim;
+  constexpr bool PACKS = V > 2;
+  constexpr int P = V / 2;
+  F2 gw[NV][P], gb[NV][P];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) gw[j][i] = gb[j][i] = 0.f;
+    for (int i = 0; i < P; ++i) gw[j][i] = gb[j][i] = f2(0.f, 0.f);
   }
-  const float inv = 1.0f / (float)a.dim;
+  const float inv = 1.0f / (float)dim;
   const uint64_t step = (uint64_t)gridDim.x * groups;
-  const uint64_t row0 = (uint64_t)blockIdx.x * groups + group;
+  const T* xs = static_cast<const T*>(a.x);
+  const T* ds = static_cast<const T*>(a.dy);
+  // Packs: kRing slots of this thread's packs of x and dy; V = 2: [dim] weights, then two
+  // slots for x and for dy of each group
+  constexpr int kSlots = PACKS ? kRing : 2;
+  float* weights = reinterpret_cast<float*>(dynamic);
+  const uint32_t slot_size = slot_elements(dim, sizeof(T));
+  T* slots = reinterpret_cast<T*>(dynamic + (dim * sizeof(float) + 15) / 16 * 16) +
+             (uint64_t)g.index * 4 * slot_size;
   auto fetch = [&](uint64_t row, uint32_t slot) {
     if (row < a.rows) {
-      const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride;
-      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
-      uint8_t* to = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
+      const T* x = xs + (int64_t)row * a.x_stride;
+      const T* dy = ds + (int64_t)row * a.dy_stride;
+      if constexpr (PACKS) {
+        uint8_t* to = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint64_t c = (uint64_t)(j * threads + t) * V;
-        if (c < a.dim) {
-          cp_async16(to + (uint64_t)j * blockDim.x * 16, x + c);
-          cp_async16(to + (uint64_t)(NV + j) * blockDim.x * 16, dy + c);
+        for (int j = 0; j < NV; ++j) {
+          const uint32_t c = column<V>(j, 0, threads, t);
+          if (c < dim) {
+            cp_async16(to + j * blockDim.x * 16, x + c);
+            cp_async16(to + (NV + j) * blockDim.x * 16, dy + c);
+          }
         }
+      } else {
+        copy_row(slots + (2 * slot) * slot_size, x, dim, row * (uint64_t)a.x_stride, g);
+        copy_row(slots + (2 * slot + 1) * slot_size, dy, dim, row * (uint64_t)a.dy_stride, g);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if constexpr (V > 1) {
-#pragma unroll
-    for (int k = 0; k < kRing - 1; ++k) fetch(row0 + k * step, k);
+  if constexpr (!PACKS) {
+    for (uint32_t c = threadIdx.x; c < dim; c += blockDim.x)
+      weights[c] = a.w ? load_any(a.w, a.w_type, c) : 1.f;
   }
+  uint64_t base = (uint64_t)blockIdx.x * groups;
+  float next_mean = 0.f, next_rstd = 0.f;
+  if (base + g.index < a.rows) {
+    next_mean = a.mean[base + g.index];
+    next_rstd = a.rstd[base + g.index];
+  }
+#pragma unroll
+  for (int k = 0; k < kSlots - 1; ++k) fetch(base + g.index + k * step, k);
+  if constexpr (!PACKS) __syncthreads();
   uint32_t slot = 0;
-  for (uint64_t row = row0; row < a.rows; row += step) {
-    const float mean = a.mean[row], rstd = a.rstd[row];
+  for (; base < a.rows; base += step) {  // the same turns for all groups
+    const uint64_t row = base + g.index;
+    const bool active = row < a.rows;
+    const float mean = next_mean, rstd = next_rstd;
+    if (row + step < a.rows) {
+      next_mean = a.mean[row + step];
+      next_rstd = a.rstd[row + step];
+    }
     Raw<T, V> vx[NV], vd[NV];
-    if constexpr (V > 1) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
+    if constexpr (PACKS) {
       const uint8_t* from = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        vx[j].w = *reinterpret_cast<const uint4*>(from + (uint64_t)j * blockDim.x * 16);
-        vd[j].w = *reinterpret_cast<const uint4*>(from + (uint64_t)(NV + j) * blockDim.x * 16);
+        vx[j].w = *reinterpret_cast<const uint4*>(from + j * blockDim.x * 16);
+        vd[j].w = *reinterpret_cast<const uint4*>(from + (NV + j) * blockDim.x * 16);
       }
-      fetch(row + (kRing - 1) * step, slot == 0 ? kRing - 1 : slot - 1);
-      slot = slot + 1 == kRing ? 0 : slot + 1;
     } else {
-      const T* x = static_cast<const T*>(a.x) + (int64_t)row * a.x_stride;
-      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
+      g.sync();
+      const T* x = slots + (2 * slot) * slot_size;
+      const T* dy = slots + (2 * slot + 1) * slot_size;
+      if (active) {
+        x += row_skew(xs + (int64_t)row * a.x_stride);
+        dy += row_skew(ds + (int64_t)row * a.dy_stride);
+      }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const uint64_t c = (uint64_t)(j * threads + t) * V;
-        if (c < a.dim) {
-          vx[j] = load_raw<T, V>(x + c);
-          vd[j] = load_raw<T, V>(dy + c);
+        const uint32_t c = column<V>(j, 0, threads, t);
+        if (active && c < dim) {
+          vx[j].w = pair_at(x, c, c + threads, dim);
+          vd[j].w = pair_at(dy, c, c + threads, dim);
         }
       }
     }
-    float2 s = make_float2(0.f, 0.f);
+    fetch(row + (kSlots - 1) * step, slot == 0 ? kSlots - 1 : slot - 1);
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+    F2 s0 = f2(0.f, 0.f), s1 = s0;
+    const F2 minus = f2(-mean, -mean), by = f2(rstd, rstd);
+    auto weights_at = [&](uint32_t c, F2(&w)[P]) {
+      if constexpr (PACKS) load_affine<W, V>(a.w, c, 1.f, w);
+      else w[0] = pair_at(weights, c, c + threads, dim);
+    };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint64_t c = (uint64_t)(j * threads + t) * V;
-      if (c < a.dim) {
-        float w[V], g[V], f[V];
-        load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
-        unpack<T, V>(vd[j], g);
+      const uint32_t c = column<V>(j, 0, threads, t);
+      if (active && c < dim) {
+        F2 w[P], d[P], f[P];
+        weights_at(c, w);
+        unpack<T, V>(vd[j], d);
         unpack<T, V>(vx[j], f);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float xh = (f[i] - mean) * rstd;
-          gw[j][i] += g[i] * xh;
-          gb[j][i] += g[i];
-          s.x += g[i] * w[i];
-          s.y += g[i] * w[i] * xh;
+        for (int i = 0; i < P; ++i) {
+          const F2 xh = (f[i] + minus) * by;
+          gw[j][i] = fma2(d[i], xh, gw[j][i]);
+          gb[j][i] = gb[j][i] + d[i];
+          const F2 dw = d[i] * w[i];
+          s0 = s0 + dw;
+          s1 = fma2(dw, xh, s1);
         }
         vx[j].forget();
         vd[j].forget();
       }
     }
-    s = row_sum(s, threads, group, scratch + 66 * group, turn);
-    const float c1 = s.x * inv, c2 = s.y * inv;
+    const float2 t0 = split(s0), t1 = split(s1);
+    const float2 s = g.sum2(make_float2(t0.x + t0.y, t1.x + t1.y));
+    if (!active) continue;
+    const F2 c1 = f2(-s.x * inv, -s.x * inv), c2 = f2(-s.y * inv, -s.y * inv);
     T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint64_t c = (uint64_t)(j * threads + t) * V;
-      if (c < a.dim) {
-        float w[V], g[V], f[V];
-        load_affine<V>(a.w, a.w_type, a.vec_w, c, 1.f, w);
-        unpack<T, V>(vd[j], g);
+      const uint32_t c = column<V>(j, 0, threads, t);
+      if (c < dim) {
+        F2 w[P], d[P], f[P];
+        weights_at(c, w);
+        unpack<T, V>(vd[j], d);
         unpack<T, V>(vx[j], f);
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          f[i] = rstd * (g[i] * w[i] - c1 - (f[i] - mean) * rstd * c2);
-        store_raw<T, V>(dx + c, pack<T, V>(f));
+        for (int i = 0; i < P; ++i)
+          f[i] = by * fma2((f[i] + minus) * by, c2, fma2(d[i], w[i], c1));
+        store_pack<T, V>(dx, j, threads, t, dim, f);
       }
     }
   }
   if (a.part_w == nullptr) return;  // neither sum is wanted
+  auto part = [](F2 v, int i) { return i & 1 ? split(v).y : split(v).x; };
   float* to_w = a.part_w + (uint64_t)blockIdx.x * a.dim;
   float* to_b = a.part_b + (uint64_t)blockIdx.x * a.dim;
   if (groups > 1) {
@@ -340,15 +501,15 @@ norm_backward_kernel(const NormGradArgs a) {
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     for (uint32_t k = 0; k < groups; ++k) {
-      if (group == k) {
+      if (g.index == k) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const uint64_t c = (uint64_t)(j * threads + t) * V + i;
+            const uint32_t c = column<V>(j, i, threads, t);
             if (c < a.dim) {
-              join[c] = (k ? join[c] : 0.f) + gw[j][i];
-              join[a.dim + c] = (k ? join[a.dim + c] : 0.f) + gb[j][i];
+              join[c] = (k ? join[c] : 0.f) + part(gw[j][i / 2], i);
+              join[a.dim + c] = (k ? join[a.dim + c] : 0.f) + part(gb[j][i / 2], i);
             }
           }
         }
@@ -364,10 +525,10 @@ norm_backward_kernel(const NormGradArgs a) {
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint64_t c = (uint64_t)(j * threads + t) * V + i;
+        const uint32_t c = column<V>(j, i, threads, t);
         if (c < a.dim) {
-          to_w[c] = gw[j][i];
-          to_b[c] = gb[j][i];
+          to_w[c] = part(gw[j][i / 2], i);
+          to_b[c] = part(gb[j][i / 2], i);
         }
       }
     }
@@ -398,7 +559,7 @@ template <typename T>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGradArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
-  uint32_t turn = 0;
+  Group g = make_group(blockDim.x, scratch);
   const T* x = static_cast<const T*>(a.x) + (int64_t)blockIdx.x * a.x_stride;
   const T* dy = static_cast<const T*>(a.dy) + (int64_t)blockIdx.x * a.dy_stride;
   T* dx = static_cast<T*>(a.dx) + (int64_t)blockIdx.x * a.dx_stride;
@@ -410,7 +571,7 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGrad
     s.x += d;
     s.y += d * ((to_f32(x[c]) - mean) * rstd);
   }
-  s = row_sum(s, blockDim.x, 0, scratch, turn);
+  s = g.sum2(s);
   const float c1 = s.x * inv, c2 = s.y * inv;
   for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
     const float d = to_f32(dy[c]) * (a.w ? load_any(a.w, a.w_type, c) : 1.f);
@@ -470,33 +631,60 @@ uint32_t threads_for(uint64_t dim, uint32_t per) {
 
 constexpr uint32_t kSms = 152;
 
-template <typename T, int V, int NV, bool BLOCK, int MINB>
-void launch_forward(const NormArgs& a, cudaStream_t s) {
-  const uint32_t threads = BLOCK ? threads_for(a.dim, V * NV) : 128;
-  const uint64_t work = BLOCK ? a.rows : (a.rows + 3) / 4;
-  const uint32_t fit = kSms * (BLOCK ? std::max(1u, std::min(16u, 1024 / threads)) : MINB);
-  launch_pdl(norm_forward_kernel<T, V, NV, BLOCK, MINB>, (unsigned)std::min<uint64_t>(work, fit),
-             threads, 0, s, a);
+// `threads` for a row, blocks of at least `block` threads, `fit` of them per SM.
+template <typename T, typename W, int V, int NV, int MAXT, int MINB>
+bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, cudaStream_t s) {
+  auto kernel = norm_forward_kernel<T, W, V, NV, MAXT, MINB>;
+  a.threads = threads;
+  const uint32_t groups = std::max(1u, block / threads);
+  size_t smem = 0;
+  if (V == 2) {
+    smem = align_up(2 * a.dim * sizeof(float), 16) +
+           2ull * groups * slot_elements((uint32_t)a.dim, sizeof(T)) * sizeof(T);
+    if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem))
+      return false;
+    fit = (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>(fit, 220 * 1024 / (smem + 2048)));
+  }
+  launch_pdl(kernel, (unsigned)std::min<uint64_t>((a.rows + groups - 1) / groups, kSms * fit),
+             threads * groups, smem, s, a);
+  return true;
 }
 
-// Packs of 16 bytes need 16-byte aligned rows and a whole number of packs; other rows
-// are read element by element. A warp takes a row of up to 16 packs per lane, which needs
-// no barrier; a block takes longer ones.
-template <typename T>
-void forward_typed(const NormArgs& a, cudaStream_t s) {
+// Up to 16 packs per lane a warp takes a row alone, which needs no barrier; short rows
+// share a warp, and longer ones take several.
+template <typename T, typename W>
+bool forward_packs(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const bool vec = a.dim % V == 0 && a.x_stride % V == 0 && a.y_stride % V == 0 &&
-                   aligned_to(a.x, 16) && aligned_to(a.y, 16);
   const uint64_t packs = a.dim / V;
-  if (vec && packs <= 32) launch_forward<T, V, 1, false, 11>(a, s);
-  else if (vec && packs <= 64) launch_forward<T, V, 2, false, 10>(a, s);
-  else if (vec && packs <= 128) launch_forward<T, V, 4, false, 7>(a, s);
-  else if (vec && packs <= 256) launch_forward<T, V, 8, false, 4>(a, s);
-  else if (vec && packs <= 512) launch_forward<T, V, 16, false, 3>(a, s);
-  else if (vec && packs <= 4 * 1024) launch_forward<T, V, 4, true, 1>(a, s);
-  else if (a.dim <= 32 * 16) launch_forward<T, 1, 16, false, 5>(a, s);
-  else if (a.dim <= 1024 * 8) launch_forward<T, 1, 8, true, 1>(a, s);
-  else launch_pdl(norm_forward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
+  if (packs <= 32)
+    return launch_forward<T, W, V, 1, 128, 11>(a, packs <= 8 ? 8 : packs <= 16 ? 16 : 32, 128, 11,
+                                               s);
+  if (packs <= 64) return launch_forward<T, W, V, 2, 128, 10>(a, 32, 128, 10, s);
+  if (packs <= 128) return launch_forward<T, W, V, 4, 128, 7>(a, 32, 128, 7, s);
+  if (packs <= 256) return launch_forward<T, W, V, 8, 128, 4>(a, 32, 128, 4, s);
+  if (packs <= 512) return launch_forward<T, W, V, 16, 128, 3>(a, 32, 128, 3, s);
+  const uint32_t threads = threads_for(packs, 4);
+  return launch_forward<T, W, V, 4, 1024, 1>(a, threads, threads, std::max(1u, 1024 / threads), s);
+}
+
+// Whole packs: 16-byte aligned rows and weights of the rows' type or fp32. Everything else
+// goes element by element.
+template <typename T>
+bool forward_typed(const NormArgs& a, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const bool vec = a.dim % V == 0 && a.dim <= 4096 * V && a.x_stride % V == 0 &&
+                   a.y_stride % V == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) &&
+                   aligned_to(a.w, 16) && aligned_to(a.b, 16);
+  if (vec && (type_of<T>() == a.w_type || (!a.w && !a.b))) return forward_packs<T, T>(a, s);
+  if (sizeof(T) == 2 && vec && a.w_type == SPARCML_F32) return forward_packs<T, float>(a, s);
+  if (a.dim <= 512 * 16) {
+    const uint32_t threads = threads_for(a.dim, 16);
+    if (threads <= 256)
+      return launch_forward<T, T, 2, 8, 256, 3>(a, threads, 256, 3, s);
+    return launch_forward<T, T, 2, 8, 512, 1>(a, threads, threads, 2, s);
+  }
+  launch_pdl(norm_forward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
+  return true;
 }
 
 constexpr uint32_t kBackwardPer = 16;  // elements per thread
@@ -508,7 +696,10 @@ struct BackwardShape {
   uint32_t threads, block, parts;
 };
 BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
-  const uint32_t threads = (uint32_t)std::min<uint64_t>(512, threads_for(dim, kBackwardPer));
+  const uint32_t threads = dim <= 128   ? 8
+                           : dim <= 256 ? 16
+                                        : (uint32_t)std::min<uint64_t>(
+                                              512, threads_for(dim, kBackwardPer));
   const uint32_t groups = std::max(1u, 256 / threads);
   const uint64_t most = kSms * (threads <= 256 ? 3 : 1);
   return {threads, threads * groups,
@@ -517,12 +708,16 @@ BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
 // One block joins up to this many partial sums in less time than a launch takes.
 constexpr uint64_t kTicketSums = 16 * 1024;
 
-template <typename T, int V, int MAXT, int MINB>
+template <typename T, typename W, int V, int MAXT, int MINB>
 bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
   constexpr int NV = kBackwardPer / V;
-  auto kernel = norm_backward_kernel<T, V, NV, MAXT, MINB>;
-  const size_t ring = V > 1 ? (size_t)kRing * 2 * NV * h.block * 16 : 0;
-  const size_t join = h.block > h.threads ? 2 * a.dim * sizeof(float) : 0;
+  auto kernel = norm_backward_kernel<T, W, V, NV, MAXT, MINB>;
+  const uint32_t groups = h.block / h.threads;
+  const size_t ring = V > 2 ? (size_t)kRing * 2 * NV * h.block * 16
+                            : align_up(a.dim * sizeof(float), 16) +
+                                  4ull * groups * slot_elements((uint32_t)a.dim, sizeof(T)) *
+                                      sizeof(T);
+  const size_t join = groups > 1 ? 2 * a.dim * sizeof(float) : 0;
   const size_t smem = std::max(ring, join);
   if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
   launch_pdl(kernel, h.parts, h.block, smem, s, a);
@@ -534,7 +729,7 @@ bool backward_typed(const NormGradArgs& a, const BackwardShape& h, cudaStream_t 
   constexpr int V = 16 / sizeof(T);
   const bool vec = a.dim % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 &&
                    a.dx_stride % V == 0 && aligned_to(a.x, 16) && aligned_to(a.dy, 16) &&
-                   aligned_to(a.dx, 16);
+                   aligned_to(a.dx, 16) && aligned_to(a.w, 16);
   if (a.dim > 512ull * kBackwardPer) {
     launch_pdl(norm_backward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
     note_launches(1);
@@ -546,10 +741,16 @@ bool backward_typed(const NormGradArgs& a, const BackwardShape& h, cudaStream_t 
     return true;
   }
   note_launches(1);
-  if (h.block <= 256)
-    return vec ? launch_backward<T, V, 256, sizeof(T) == 2 ? 3 : 2>(a, h, s)
-               : launch_backward<T, 1, 256, 2>(a, h, s);
-  return vec ? launch_backward<T, V, 512, 1>(a, h, s) : launch_backward<T, 1, 512, 1>(a, h, s);
+  constexpr int kFit = sizeof(T) == 2 ? 3 : 2;  // blocks of 256 threads in the registers of an SM
+  const bool small = h.block <= 256;
+  if (vec && (type_of<T>() == a.w_type || !a.w))
+    return small ? launch_backward<T, T, V, 256, kFit>(a, h, s)
+                 : launch_backward<T, T, V, 512, 1>(a, h, s);
+  if (sizeof(T) == 2 && vec && a.w_type == SPARCML_F32)
+    return small ? launch_backward<T, float, V, 256, kFit>(a, h, s)
+                 : launch_backward<T, float, V, 512, 1>(a, h, s);
+  return small ? launch_backward<T, T, 2, 256, 2>(a, h, s)
+               : launch_backward<T, T, 2, 512, 1>(a, h, s);
 }
 
 bool rows_ok(uint64_t rows, uint64_t dim) {
@@ -573,14 +774,13 @@ extern "C" int sparcml_layer_norm(const void* x, int32_t type, int64_t x_stride,
   if (!x || !y || !mean || !rstd || x_stride < 0 || (rows > 1 && y_stride < (int64_t)dim) ||
       !aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, we) || !aligned_to(bias, we))
     return SPARCML_ERR_INVALID_ARG;
-  const NormArgs a{x,    x_stride, weight, bias, weight_type,
-                   aligned_to(weight, 16) && aligned_to(bias, 16), rows, dim, eps, y,
-                   rows > 1 ? y_stride : 0, mean, rstd};
+  const NormArgs a{x,   x_stride, weight,   bias, weight_type, rows,
+                   dim, eps,      y,        rows > 1 ? y_stride : 0, mean, rstd, 0};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (type == SPARCML_F32) forward_typed<float>(a, s);
-  else if (type == SPARCML_BF16) forward_typed<__nv_bfloat16>(a, s);
-  else forward_typed<__half>(a, s);
-  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  const bool ok = type == SPARCML_F32    ? forward_typed<float>(a, s)
+                  : type == SPARCML_BF16 ? forward_typed<__nv_bfloat16>(a, s)
+                                         : forward_typed<__half>(a, s);
+  if (launch_status() != SPARCML_OK || !ok) return SPARCML_ERR_CUDA;
   note_launches(1);
   return SPARCML_OK;
 }
@@ -616,7 +816,7 @@ extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, co
   float* part_b = part_w + (uint64_t)h.parts * dim;
   bool joined = !sums;
   if (rows) {
-    NormGradArgs a{dy, dy_stride, x, x_stride, weight, weight_type, aligned_to(weight, 16), mean,
+    NormGradArgs a{dy, dy_stride, x, x_stride, weight, weight_type, mean,
                    rstd, rows, dim, dx, rows > 1 ? dx_stride : 0, sums ? part_w : nullptr, part_b,
                    h.threads, nullptr, dweight, dbias, accumulate};
     if (sums && dim <= 512ull * kBackwardPer && h.parts * dim <= kTicketSums) {

@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace sparcml {
@@ -30,7 +32,38 @@ struct alignas(sizeof(T) * V) Pack {
   T e[V];
 };
 
-// V elements as they lie in memory: a 16-byte word group (V > 1), or one element.
+// Two fp32 values in a register pair: one instruction adds or multiplies both.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 split(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// V elements as they lie in memory (a 16-byte group of words), or, for V = 2, two elements
+// already in fp32.
 template <typename T, int V>
 struct Raw {
   uint4 w;
@@ -41,74 +74,67 @@ struct Raw {
   }
 };
 template <typename T>
-struct Raw<T, 1> {
-  T w;
+struct Raw<T, 2> {
+  F2 w;
   __device__ __forceinline__ void forget() {}
 };
 
 template <typename T>
-__device__ __forceinline__ float2 unpack2(uint32_t w);
+__device__ __forceinline__ F2 unpack2(uint32_t w);
 template <>
-__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+__device__ __forceinline__ F2 unpack2<__nv_bfloat16>(uint32_t w) {
+  return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 template <>
-__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+__device__ __forceinline__ F2 unpack2<__half>(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return f2(f.x, f.y);
 }
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
+__device__ __forceinline__ uint32_t pack2(F2 a);
 template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(F2 a) {
+  const float2 f = split(a);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
+__device__ __forceinline__ uint32_t pack2<__half>(F2 a) {
+  const float2 f = split(a);
+  const __half2 h = __floats2half2_rn(f.x, f.y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Raw values as V / 2 fp32 pairs.
 template <typename T, int V>
-__device__ __forceinline__ void unpack(const Raw<T, V>& r, float (&f)[V]) {
-  if constexpr (V == 1) {
-    f[0] = to_f32(r.w);
+__device__ __forceinline__ void unpack(const Raw<T, V>& r, F2 (&f)[V / 2]) {
+  if constexpr (V == 2) {
+    f[0] = r.w;
   } else if constexpr (V == 4) {
-    f[0] = __uint_as_float(r.w.x); f[1] = __uint_as_float(r.w.y);
-    f[2] = __uint_as_float(r.w.z); f[3] = __uint_as_float(r.w.w);
+    f[0] = f2(__uint_as_float(r.w.x), __uint_as_float(r.w.y));
+    f[1] = f2(__uint_as_float(r.w.z), __uint_as_float(r.w.w));
   } else {
-    const uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 p = unpack2<T>(w[e]);
-      f[2 * e] = p.x;
-      f[2 * e + 1] = p.y;
-    }
+    f[0] = unpack2<T>(r.w.x);
+    f[1] = unpack2<T>(r.w.y);
+    f[2] = unpack2<T>(r.w.z);
+    f[3] = unpack2<T>(r.w.w);
   }
 }
 template <typename T, int V>
-__device__ __forceinline__ Raw<T, V> pack(const float (&f)[V]) {
-  Raw<T, V> r;
-  if constexpr (V == 1) {
-    r.w = from_f32<T>(f[0]);
-  } else if constexpr (V == 4) {
-    r.w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                     __float_as_uint(f[3]));
+__device__ __forceinline__ uint4 pack(const F2 (&f)[V / 2]) {
+  if constexpr (V == 4) {
+    const float2 p = split(f[0]), q = split(f[1]);
+    return make_uint4(__float_as_uint(p.x), __float_as_uint(p.y), __float_as_uint(q.x),
+                      __float_as_uint(q.y));
   } else {
-    r.w = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]),
-                     pack2<T>(f[6], f[7]));
+    return make_uint4(pack2<T>(f[0]), pack2<T>(f[1]), pack2<T>(f[2]), pack2<T>(f[3]));
   }
-  return r;
 }
 template <typename T, int V>
 __device__ __forceinline__ Raw<T, V> load_raw(const T* p) {
   Raw<T, V> r;
-  r.w = *reinterpret_cast<const decltype(r.w)*>(p);
+  r.w = *reinterpret_cast<const uint4*>(p);
   return r;
-}
-template <typename T, int V>
-__device__ __forceinline__ void store_raw(T* p, const Raw<T, V>& r) {
-  *reinterpret_cast<decltype(Raw<T, V>::w)*>(p) = r.w;
 }
 
 // One element of an array whose type is a run-time code (enum sparcml_type).
@@ -124,6 +150,11 @@ __device__ __forceinline__ float warp_sum_f(float v) {
   return v;
 }
 
+template <typename T>
+constexpr int32_t type_of() {
+  return sizeof(T) == 4 ? SPARCML_F32
+         : std::is_same_v<T, __half> ? SPARCML_F16 : SPARCML_BF16;
+}
 inline size_t type_bytes(int32_t type) { return type == SPARCML_F32 ? 4 : 2; }
 inline bool type_ok(int32_t type) { return type >= SPARCML_F32 && type <= SPARCML_F16; }
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
