@@ -30,15 +30,20 @@ struct Group {
     else
       __syncwarp();
   }
+  template <int D>
+  static __device__ __forceinline__ void add(float2& v) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, D);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, D);
+  }
   __device__ __forceinline__ float sum(float2 v) { return sum2(make_float2(v.x + v.y, 0.f)).x; }
   // Sums of two values. `turn` alternates between the halves of the scratch from call to
   // call, so that one barrier per call is enough.
   __device__ __forceinline__ float2 sum2(float2 v) {
-    const uint32_t width = threads < 32 ? threads : 32;
-    for (uint32_t d = width >> 1; d > 0; d >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
-    }
+    if (threads >= 32) add<16>(v);
+    if (threads >= 16) add<8>(v);
+    add<4>(v);
+    add<2>(v);
+    add<1>(v);
     if (threads <= 32) return v;
     float2* s = scratch + 33 * (turn & 1u);
     ++turn;
@@ -46,10 +51,13 @@ struct Group {
     if (lane == 0) s[t >> 5] = v;
     sync();
     v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
-    for (uint32_t d = nw > 16 ? 16 : nw > 8 ? 8 : nw > 4 ? 4 : nw > 2 ? 2 : 1; d > 0; d >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, d);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, d);
+    if (nw > 8) {
+      if (nw > 16) add<16>(v);
+      add<8>(v);
     }
+    add<4>(v);
+    add<2>(v);
+    add<1>(v);
     // the lanes that were added up hold the sum; the first one tells the rest
     v.x = __shfl_sync(0xffffffffu, v.x, 0);
     v.y = __shfl_sync(0xffffffffu, v.y, 0);
@@ -357,6 +365,7 @@ norm_backward_kernel(const NormGradArgs a) {
   const uint32_t dim = (uint32_t)a.dim;
   constexpr bool PACKS = V > 2;
   constexpr int P = V / 2;
+  constexpr int kWide = sizeof(W) > sizeof(T) ? 2 : 1;  // 16-byte groups of weights per pack
   F2 gw[NV][P], gb[NV][P];
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
@@ -399,6 +408,35 @@ norm_backward_kernel(const NormGradArgs a) {
     for (uint32_t c = threadIdx.x; c < dim; c += blockDim.x)
       weights[c] = a.w ? load_any(a.w, a.w_type, c) : 1.f;
   }
+  // a thread's weights stay in its registers
+  Raw<W, V> own[PACKS ? NV : 1][PACKS ? kWide : 1];
+  if constexpr (PACKS) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const uint32_t c = column<V>(j, 0, threads, t);
+#pragma unroll
+      for (int q = 0; q < kWide; ++q)
+        if (a.w && c < dim)
+          own[j][q].w = *reinterpret_cast<const uint4*>(static_cast<const W*>(a.w) + c + 4 * q);
+    }
+  }
+  auto weights_at = [&](int j, uint32_t c, F2(&w)[P]) {
+    if constexpr (!PACKS) {
+      w[0] = pair_at(weights, c, c + threads, dim);
+    } else if (a.w == nullptr) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) w[i] = f2(1.f, 1.f);
+    } else if constexpr (kWide == 1) {
+      unpack<W, V>(own[j][0], w);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint4 f = own[j][q].w;
+        w[2 * q] = f2(__uint_as_float(f.x), __uint_as_float(f.y));
+        w[2 * q + 1] = f2(__uint_as_float(f.z), __uint_as_float(f.w));
+      }
+    }
+  };
   uint64_t base = (uint64_t)blockIdx.x * groups;
   float next_mean = 0.f, next_rstd = 0.f;
   if (base + g.index < a.rows) {
@@ -447,16 +485,12 @@ norm_backward_kernel(const NormGradArgs a) {
     slot = slot + 1 == kSlots ? 0 : slot + 1;
     F2 s0 = f2(0.f, 0.f), s1 = s0;
     const F2 minus = f2(-mean, -mean), by = f2(rstd, rstd);
-    auto weights_at = [&](uint32_t c, F2(&w)[P]) {
-      if constexpr (PACKS) load_affine<W, V>(a.w, c, 1.f, w);
-      else w[0] = pair_at(weights, c, c + threads, dim);
-    };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint32_t c = column<V>(j, 0, threads, t);
       if (active && c < dim) {
         F2 w[P], d[P], f[P];
-        weights_at(c, w);
+        weights_at(j, c, w);
         unpack<T, V>(vd[j], d);
         unpack<T, V>(vx[j], f);
 #pragma unroll
@@ -475,19 +509,21 @@ norm_backward_kernel(const NormGradArgs a) {
     const float2 t0 = split(s0), t1 = split(s1);
     const float2 s = g.sum2(make_float2(t0.x + t0.y, t1.x + t1.y));
     if (!active) continue;
-    const F2 c1 = f2(-s.x * inv, -s.x * inv), c2 = f2(-s.y * inv, -s.y * inv);
+    // dx = (x - mean) k2 + (d rstd + k1)
+    const float k1s = -s.x * inv * rstd, k2s = -s.y * inv * rstd * rstd;
+    const F2 k1 = f2(k1s, k1s), k2 = f2(k2s, k2s);
     T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint32_t c = column<V>(j, 0, threads, t);
       if (c < dim) {
         F2 w[P], d[P], f[P];
-        weights_at(c, w);
+        weights_at(j, c, w);
         unpack<T, V>(vd[j], d);
         unpack<T, V>(vx[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i)
-          f[i] = by * fma2((f[i] + minus) * by, c2, fma2(d[i], w[i], c1));
+          f[i] = fma2(f[i] + minus, k2, fma2(d[i] * w[i], by, k1));
         store_pack<T, V>(dx, j, threads, t, dim, f);
       }
     }
@@ -611,7 +647,7 @@ norm_join_kernel(const float* __restrict__ part_w, const float* __restrict__ par
   const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < dim) {
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t p = warp; p < parts; p += 16) s += part[(uint64_t)p * dim + c];
   }
   sums[warp][lane] = s;
@@ -689,9 +725,10 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
 
 constexpr uint32_t kBackwardPer = 16;  // elements per thread
 
-// Threads of a row and of a block, and the blocks, each with a row of partial sums:
-// three blocks per SM, no more than there are rows. A function of the sizes alone, so
-// that the workspace and the order of the sums do not depend on the device's state.
+// Threads of a row and of a block, and the blocks, each with a row of partial sums: what
+// the registers of the SMs hold at one time (kFit blocks of 256 threads each; with a
+// second, partial wave 16384 x 4096 fp32 took 271 us), no more than there are rows.
+constexpr uint32_t kFit = 2;
 struct BackwardShape {
   uint32_t threads, block, parts;
 };
@@ -701,7 +738,7 @@ BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
                                         : (uint32_t)std::min<uint64_t>(
                                               512, threads_for(dim, kBackwardPer));
   const uint32_t groups = std::max(1u, 256 / threads);
-  const uint64_t most = kSms * (threads <= 256 ? 3 : 1);
+  const uint64_t most = kSms * (threads <= 256 ? kFit : 1);
   return {threads, threads * groups,
           (uint32_t)std::max<uint64_t>(1, std::min((rows + groups - 1) / groups, most))};
 }
@@ -725,32 +762,43 @@ bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t
 }
 
 template <typename T>
-bool backward_typed(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
+bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const bool vec = a.dim % V == 0 && a.x_stride % V == 0 && a.dy_stride % V == 0 &&
                    a.dx_stride % V == 0 && aligned_to(a.x, 16) && aligned_to(a.dy, 16) &&
                    aligned_to(a.dx, 16) && aligned_to(a.w, 16);
-  if (a.dim > 512ull * kBackwardPer) {
+  const bool same = type_of<T>() == a.w_type || !a.w;
+  const bool packs = vec && (same || a.w_type == SPARCML_F32);
+  const bool longer = a.dim > 512ull * kBackwardPer;
+  const BackwardShape h = backward_shape(a.rows, a.dim);
+  a.threads = h.threads;
+  a.part_w = sums ? reinterpret_cast<float*>(ws + 256) : nullptr;
+  a.part_b = reinterpret_cast<float*>(ws + 256) + (uint64_t)h.parts * a.dim;
+  const bool ticket = sums && !longer && h.parts * a.dim <= kTicketSums;
+  if (ticket) a.ticket = reinterpret_cast<uint32_t*>(ws + kTicketOffset);
+  const bool small = h.block <= 256;
+  bool ok = true;
+  if (longer) {
     launch_pdl(norm_backward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
-    note_launches(1);
-    if (a.part_w) {
+    if (sums)
       launch_pdl(norm_columns_kernel<T>, dim3((unsigned)((a.dim + 255) / 256), h.parts), 256, 0, s,
                  a);
-      note_launches(1);
-    }
-    return true;
-  }
-  note_launches(1);
-  constexpr int kFit = sizeof(T) == 2 ? 3 : 2;  // blocks of 256 threads in the registers of an SM
-  const bool small = h.block <= 256;
-  if (vec && (type_of<T>() == a.w_type || !a.w))
-    return small ? launch_backward<T, T, V, 256, kFit>(a, h, s)
-                 : launch_backward<T, T, V, 512, 1>(a, h, s);
-  if (sizeof(T) == 2 && vec && a.w_type == SPARCML_F32)
-    return small ? launch_backward<T, float, V, 256, kFit>(a, h, s)
-                 : launch_backward<T, float, V, 512, 1>(a, h, s);
-  return small ? launch_backward<T, T, 2, 256, 2>(a, h, s)
+  } else if (packs && same) {
+    ok = small ? launch_backward<T, T, V, 256, kFit>(a, h, s)
+               : launch_backward<T, T, V, 512, 1>(a, h, s);
+  } else if (sizeof(T) == 2 && packs) {
+    ok = small ? launch_backward<T, float, V, 256, kFit>(a, h, s)
+               : launch_backward<T, float, V, 512, 1>(a, h, s);
+  } else {
+    ok = small ? launch_backward<T, T, 2, 256, kFit>(a, h, s)
                : launch_backward<T, T, 2, 512, 1>(a, h, s);
+  }
+  const bool join = sums && !ticket;
+  if (join)
+    launch_pdl(norm_join_kernel, dim3((unsigned)((a.dim + 31) / 32), 2), 512, 0, s, a.part_w,
+               a.part_b, h.parts, a.dim, a.dweight, a.dbias, a.accumulate);
+  note_launches(1 + (longer && sums) + join);
+  return ok;
 }
 
 bool rows_ok(uint64_t rows, uint64_t dim) {
@@ -810,27 +858,21 @@ extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, co
   if (ws_bytes < sparcml_layer_norm_backward_workspace_size(rows, dim))
     return SPARCML_ERR_WORKSPACE;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const BackwardShape h = backward_shape(rows, dim);
   const bool sums = dweight || dbias;
-  float* part_w = reinterpret_cast<float*>(static_cast<char*>(ws) + 256);
-  float* part_b = part_w + (uint64_t)h.parts * dim;
-  bool joined = !sums;
   if (rows) {
-    NormGradArgs a{dy, dy_stride, x, x_stride, weight, weight_type, mean,
-                   rstd, rows, dim, dx, rows > 1 ? dx_stride : 0, sums ? part_w : nullptr, part_b,
-                   h.threads, nullptr, dweight, dbias, accumulate};
-    if (sums && dim <= 512ull * kBackwardPer && h.parts * dim <= kTicketSums) {
-      a.ticket = reinterpret_cast<uint32_t*>(static_cast<char*>(ws) + kTicketOffset);
-      joined = true;
-    }
-    const bool ok = type == SPARCML_F32    ? backward_typed<float>(a, h, s)
-                    : type == SPARCML_BF16 ? backward_typed<__nv_bfloat16>(a, h, s)
-                                           : backward_typed<__half>(a, h, s);
-    if (launch_status() != SPARCML_OK || !ok) return SPARCML_ERR_CUDA;
+    const NormGradArgs a{dy,   dy_stride, x,    x_stride, weight, weight_type, mean,
+                         rstd, rows,      dim,  dx,       rows > 1 ? dx_stride : 0,
+                         nullptr, nullptr, 0,   nullptr,  dweight, dbias, accumulate};
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const bool ok = type == SPARCML_F32    ? backward_typed<float>(a, sums, w, s)
+                    : type == SPARCML_BF16 ? backward_typed<__nv_bfloat16>(a, sums, w, s)
+                                           : backward_typed<__half>(a, sums, w, s);
+    return launch_status() == SPARCML_OK && ok ? SPARCML_OK : SPARCML_ERR_CUDA;
   }
-  if (!joined) {
-    launch_pdl(norm_join_kernel, dim3((unsigned)((dim + 31) / 32), 2), 512, 0, s, part_w, part_b,
-               rows ? h.parts : 0u, dim, dweight, dbias, accumulate);
+  if (sums) {  // of no rows
+    launch_pdl(norm_join_kernel, dim3((unsigned)((dim + 31) / 32), 2), 512, 0, s,
+               static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), 0u, dim,
+               dweight, dbias, accumulate);
     if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
     note_launches(1);
   }
