@@ -11,7 +11,8 @@
 // One launch runs all steps: a persistent grid of one block per SM, whose
 // blocks wait for one another between the products (15 products of five steps;
 // as launches of their own they cost the host 70 us, more than the products of
-// a small matrix take).
+// a small matrix take). The matrices of a batch form two chains: a block works
+// on one while the other's results are on their way, and neither waits for the other.
 //
 // Numbers. Operands are fp16 with fp32 accumulators. X and S are scaled by 2^12
 // and P by 2^11: singular values stay near 1, so nothing overflows, and entries
@@ -52,8 +53,9 @@ struct GatherArgs {
   uint64_t m, n;
   uint32_t blocks;  // per matrix
   float* sums;      // [batch][blocks][3]
-  uint32_t* turns;  // the grid's barrier, zeroed here
+  uint32_t* turns;  // counters of arrivals, zeroed here: of the grid, of each chain
 };
+constexpr uint32_t kTurnStep = 8;  // words between counters
 
 // Sums of squares in three ranges (Blue, ACM TOMS 4, 1978), so that no square
 // overflows or vanishes: entries above 2^40 scaled by 2^-90, below 2^-50 by 2^80.
@@ -103,7 +105,7 @@ constexpr uint32_t kPiece = 512;
 __global__ void __launch_bounds__(256) gather_norm_kernel(const GatherArgs a) {
   griddep_wait();
   __shared__ float warp_sums[8][3];
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.turns = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 3) a.turns[threadIdx.x * kTurnStep] = 0;
   const uint64_t b = blockIdx.y, pieces = (a.n + kPiece - 1) / kPiece, total = a.m * pieces;
   const uint64_t warps = (uint64_t)a.blocks * 8, id = blockIdx.x * 8ull + (threadIdx.x >> 5);
   const uint64_t end = total * (id + 1) / warps;
@@ -171,20 +173,27 @@ struct Product {       // one product of a step, of every matrix of the batch
   uint32_t blocks;     // of 64 along the summed axis
   uint32_t tile_rows;  // tiles down, or 0: those on and below the diagonal
   uint32_t tiles;      // per matrix
-  uint32_t splits;     // parts of the summed axis, each a tile of its own
-  uint32_t items;      // batch * tiles * splits
+  uint32_t splits;     // parts of the summed axis, each an item of its own
+  uint32_t whole;      // items of full width; those after them are halves of tiles
+  uint32_t items;
+  uint32_t b0;         // the chain's first matrix
+  uint32_t offset;     // which block or pair takes item 0
+  uint32_t part0;      // the chain's first partial tile
 };
 
 struct Maps {
-  // operands are read in boxes of 64 x 64, 128-byte swizzled; what is added to the
-  // products in boxes of 32 x 32, 64-byte swizzled
-  CUtensorMap x_in[2], s_in, p_in, x_out[2], lo_out, s_out;
+  // What is added to the products, in boxes of 32 x 32, 64-byte swizzled.
+  CUtensorMap x_out[2], lo_out, s_out;
+  // Operands, one load of 128 rows (or one tile's columns) by 64 of the summed axis, 128-byte
+  // swizzled: [0] the first operand, [1] the second. With a load per 64 x 64 the issue of
+  // loads, over 100 cycles each, was what bounded the products.
+  CUtensorMap x_gram[2][2], s_poly[2], x_apply[2], p_apply;
 };
 
 struct StepArgs {
   GatherArgs g;
-  uint32_t batch, steps, tall;
-  Product gram, poly, apply;
+  uint32_t batch, steps, tall, chains;
+  Product product[2][3];  // of each chain: S, P, X
   float coeffs[3 * kMaxSteps];
   __half* hi[2];  // [batch][m][pitch]
   __half* lo;
@@ -203,7 +212,7 @@ struct StepArgs {
   int32_t* status;
 };
 
-enum Kind { kGram, kPart, kPoly, kApply, kLast };
+enum Kind { kGram, kPart, kJoin, kPoly, kApply, kLast };
 
 constexpr uint32_t kWriters = 8;  // warps that write results; then a loader and an issuer
 constexpr uint32_t kThreads = 32 * (kWriters + 2);
@@ -213,7 +222,7 @@ constexpr uint32_t kStepsSmem = kRingBytes + kWriters * 2 * kStageBuf + 1024;
 constexpr uint32_t kAccColumns = 256;  // two accumulators in the 512 columns of tensor memory
 
 struct Tile {
-  uint32_t b, row0, col0, first, last;  // blocks [first, last) of the summed axis
+  uint32_t b, row0, col0, n, first, last;  // blocks [first, last) of the summed axis
   bool mirror;                          // write its mirror image too
   bool none;                            // beyond the last column
 };
@@ -224,10 +233,19 @@ struct Tile {
 template <int CG>
 __device__ __forceinline__ Tile tile_of(const Product& p, uint32_t item) {
   Tile t;
-  const uint32_t split = item % p.splits;
-  uint32_t u = item / p.splits;
+  uint32_t split = 0, u = item, half = 0;
+  t.n = p.n;
+  if (p.splits > 1) {
+    u = item / p.splits;
+    split = item - u * p.splits;
+  } else if (item >= p.whole) {
+    u = p.whole + (item - p.whole) / 2;
+    half = (item - p.whole) & 1u;
+    t.n = p.n / 2;
+  }
   t.b = u / p.tiles;
   u -= t.b * p.tiles;
+  t.b += p.b0;
   uint32_t i, j;
   t.mirror = false;
   if (p.tile_rows) {
@@ -242,7 +260,7 @@ __device__ __forceinline__ Tile tile_of(const Product& p, uint32_t item) {
     t.mirror = j < ratio * i;
   }
   t.row0 = i * 128 * CG;
-  t.col0 = j * p.n;
+  t.col0 = j * p.n + half * t.n;
   t.none = t.col0 >= p.cols;
   t.first = (uint32_t)((uint64_t)p.blocks * split / p.splits);
   t.last = (uint32_t)((uint64_t)p.blocks * (split + 1) / p.splits);
@@ -295,53 +313,55 @@ struct Worker {
   uint32_t acc = 0;       // accumulators used so far (issuer, writers)
   uint32_t in_phase = 0;  // bit s: parity of buffer s's next load
   uint32_t turn = 0;      // chunks written so far
+
+  // The first of this block's items.
+  __device__ __forceinline__ uint32_t first_item(const Product& p) const {
+    return cluster >= p.offset ? cluster - p.offset : cluster + clusters - p.offset;
+  }
 };
 
 // The loader and the issuer run as whole warps, of which one lane issues: so the addresses
 // and the control flow are known to be uniform (a lane on its own took 700 cycles per
 // block of the summed axis, where the products take 512).
 template <int CG>
-__device__ void load_operands(Worker<CG>& w, const Product& p, const CUtensorMap* ma,
-                              const CUtensorMap* mb, bool a_mn, bool b_mn, const Tile& first_tile) {
-  const uint32_t b_rows = p.n / CG, bytes = 128 * 128 + b_rows * 128;
-  proxy_fence_global();  // the other blocks' results, read by asynchronous copies
-  for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
-    const Tile t = item == w.cluster ? first_tile : tile_of<CG>(p, item);
+__device__ __forceinline__ bool load_operands(Worker<CG>& w, const Product& p, const CUtensorMap* ma,
+                              const CUtensorMap* mb, bool a_mn, bool b_mn, Tile t) {
+  for (uint32_t item = w.first_item(p); item < p.items; item += w.clusters) {
+    if (item >= w.clusters) t = tile_of<CG>(p, item);
     if (t.none) continue;
-    const uint32_t ra = t.row0 + 128 * w.rank, rb = t.col0 + b_rows * w.rank;
+    const uint32_t bytes = 128 * 128 + p.n / CG * 128;  // halves of tiles use half of theirs
+    const uint32_t ra = t.row0 + 128 * w.rank, rb = t.col0 + t.n / CG * w.rank;
     for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return;
+      if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return false;
       if (w.leader) {
         if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, CG * bytes);
         const uint32_t bar = w.lead_full + 8 * s, k = i * 64;
-        uint32_t dst = w.ring + s * w.stage_bytes;
-#pragma unroll
-        for (uint32_t h = 0; h < 128; h += 64, dst += 8192)
-          tma_load_3d<CG>(dst, ma, a_mn ? ra + h : k, a_mn ? k : ra + h, t.b, bar);
-        for (uint32_t h = 0; h < b_rows; h += 64, dst += 8192)
-          tma_load_3d<CG>(dst, mb, b_mn ? rb + h : k, b_mn ? k : rb + h, t.b, bar);
+        const uint32_t dst = w.ring + s * w.stage_bytes;
+        tma_load_4d<CG>(dst, ma, a_mn ? 0 : k, a_mn ? k : ra, a_mn ? ra / 64 : 0, t.b, bar);
+        tma_load_4d<CG>(dst + 128 * 128, mb, b_mn ? 0 : k, b_mn ? k : rb, b_mn ? rb / 64 : 0, t.b,
+                        bar);
       }
       __syncwarp();
     }
   }
+  return true;
 }
 
 template <int CG>
-__device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool b_mn,
-                               const Tile& first_tile) {
-  const uint32_t idesc = mma_desc(128 * CG, p.n, a_mn, b_mn);
+__device__ __forceinline__ bool issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool b_mn, Tile t) {
   const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
-  for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
-    const Tile t = item == w.cluster ? first_tile : tile_of<CG>(p, item);
+  for (uint32_t item = w.first_item(p); item < p.items; item += w.clusters) {
+    if (item >= w.clusters) t = tile_of<CG>(p, item);
     if (t.none) continue;
+    const uint32_t idesc = mma_desc(128 * CG, t.n, a_mn, b_mn);
     const uint32_t a = w.acc & 1u;
-    if (!mbar_wait_warp(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return;
+    if (!mbar_wait_warp(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return false;
     tmem_fence_after();
     const uint32_t d = w.tmem + a * kAccColumns;
     for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.gave_up)) return;
+      if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.gave_up)) return false;
       tmem_fence_after();
       if (w.leader) {
         const uint32_t sa = w.ring + s * w.stage_bytes, sb = sa + 128 * 128;
@@ -357,6 +377,7 @@ __device__ void issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool 
     __syncwarp();
     ++w.acc;
   }
+  return true;
 }
 
 // A 32 x 32 fp16 box in shared memory to rows [row0, row0 + 32) below `rows`, from column
@@ -526,18 +547,18 @@ __device__ __forceinline__ void store_result(const StepArgs& a, uint32_t box, ui
 }
 
 template <int CG>
-__device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p,
-                              int kind, uint32_t step, const Tile& first_tile) {
+__device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p,
+                              int kind, uint32_t step, Tile t) {
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
-  const uint32_t quarter = warp & 3u, half = warp >> 2, chunks = p.n / 64;
+  const uint32_t quarter = warp & 3u, half = warp >> 2;
   const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
   const bool pairs = kind == kApply || kind == kLast, reads = kind == kPoly || pairs;
   if (reads && lane == 0) proxy_fence_global();  // the other blocks' results, fetched below
-  for (uint32_t item = w.cluster; item < p.items; item += w.clusters) {
-    const Tile t = item == w.cluster ? first_tile : tile_of<CG>(p, item);
+  for (uint32_t item = w.first_item(p); item < p.items; item += w.clusters) {
+    if (item >= w.clusters) t = tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t row0 = t.row0 + 128 * w.rank + 32 * quarter, row = row0 + lane;
-    const uint32_t tile_col = half * chunks * 32, col0 = t.col0 + tile_col;
+    const uint32_t chunks = t.n / 64, tile_col = half * chunks * 32, col0 = t.col0 + tile_col;
     uint32_t count = 0;  // of this warp's chunks, those that exist
     if (row0 < p.rows && col0 < p.cols) count = min(chunks, (p.cols - col0 + 31) / 32);
     const uint32_t turn0 = w.turn;
@@ -548,8 +569,8 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
         const uint32_t c = col0 + 32 * q;
         proxy_fence_shared();  // the buffer's last ordinary accesses come first
         mbar_expect_tx(bar, pairs ? 4096 : 2048);
-        tma_load_3d<1>(dst, pairs ? &m.x_out[step & 1] : &m.s_out, c, row0, t.b, bar);
-        if (pairs) tma_load_3d<1>(dst + 2048, &m.lo_out, c, row0, t.b, bar);
+        tma_load_3d(dst, pairs ? &m.x_out[step & 1] : &m.s_out, c, row0, t.b, bar);
+        if (pairs) tma_load_3d(dst + 2048, &m.lo_out, c, row0, t.b, bar);
       }
     };
     if (reads && count) fetch(0);
@@ -591,7 +612,7 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
     float other = column_diag(0);
 
     const uint32_t acc = w.acc & 1u;
-    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)) return;
+    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)) return false;
     tmem_fence_after();
     const uint32_t src = w.tmem + acc * kAccColumns + (quarter << 21) + tile_col;
     if (kind == kPart) count = chunks;
@@ -603,7 +624,8 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
       if (reads && kind != kLast && q + 1 < count) fetch(q + 1);
       const float next = column_diag(q + 1);
       if (reads) {
-        if (!mbar_wait_warp(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.gave_up)) return;
+        if (!mbar_wait_warp(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.gave_up))
+          return false;
         w.in_phase ^= 1u << slot;
       }
       const bool on_diag = !pairs && row0 == col;
@@ -614,7 +636,7 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
         tmem_load_wait(v);
         if (kind == kPart) {
           float* o = a.part +
-                     ((uint64_t)(item * CG + w.rank) * p.n + tile_col + 32 * q + 16 * h) * 128 +
+                     ((uint64_t)((p.part0 + item) * CG + w.rank) * p.n + tile_col + 32 * q + 16 * h) * 128 +
                      quarter * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i * 128] = v[i];
@@ -647,23 +669,27 @@ __device__ void write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, c
     if (lane == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
     ++w.acc;
   }
+  return true;
 }
 
 // S from the partial tiles of a split product, in the order of the splits: a warp takes
 // 32 rows and 8 columns, so that a few tiles give work to many SMs.
 template <int CG>
+__device__ __forceinline__ uint32_t join_units(const Product& p) {
+  return p.items / p.splits * 4 * CG * (p.n / 8);
+}
+template <int CG>
 __device__ void join_parts(const StepArgs& a, const Product& p) {
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
-  const uint32_t across = p.n / 8, per = 4 * CG * across;
-  const uint32_t total = a.batch * p.tiles * per;
-  for (uint32_t x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * (kThreads / 32)) {
+  const uint32_t across = p.n / 8, per = 4 * CG * across, total = join_units<CG>(p);
+  for (uint32_t x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * kWriters) {
     const uint32_t tile = x / per, r = x % per / across, q = x % across;
     const Tile t = tile_of<CG>(p, tile * p.splits);
     const uint32_t row0 = t.row0 + 32 * r, col = t.col0 + 8 * q, row = row0 + lane;
     if (row0 >= p.rows || col >= p.cols) continue;
     float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     const uint64_t step = (uint64_t)CG * p.n * 128;
-    const float* o = a.part + ((uint64_t)(tile * p.splits * CG + r / 4) * p.n + 8 * q) * 128 +
+    const float* o = a.part + ((uint64_t)((p.part0 + tile * p.splits) * CG + r / 4) * p.n + 8 * q) * 128 +
                      (r & 3u) * 32 + lane;
 #pragma unroll 4
     for (uint32_t s = 0; s < p.splits; ++s, o += step) {
@@ -732,10 +758,11 @@ __device__ void split_input(const StepArgs& a) {
   uint64_t b = line / g.m, r = line - b * g.m;
   bool known = false;
   float f0 = 0.f, f1 = 0.f;
+#pragma unroll 2
   for (; u < end; ++u) {
     if (!known) norm_factors(g, b, f0, f1);
     known = true;
-    const uint64_t c0 = piece * kPiece + lane_id() * 4;
+    const uint64_t c0 = piece * kPiece + lane_id() * 4, at = line * a.pitch;
     float v[4][4], mo[4][4];
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
@@ -762,8 +789,8 @@ __device__ void split_input(const StepArgs& a) {
         const float2 back = unpack_half(hw[i / 2]);
         lw[i / 2] = pack_half(x[0] - back.x, x[1] - back.y);
       }
-      *reinterpret_cast<uint2*>(a.hi[0] + line * a.pitch + c) = make_uint2(hw[0], hw[1]);
-      *reinterpret_cast<uint2*>(a.lo + line * a.pitch + c) = make_uint2(lw[0], lw[1]);
+      *reinterpret_cast<uint2*>(a.hi[0] + at + c) = make_uint2(hw[0], hw[1]);
+      *reinterpret_cast<uint2*>(a.lo + at + c) = make_uint2(lw[0], lw[1]);
     }
     if (++piece == pieces) {
       piece = 0;
@@ -777,52 +804,79 @@ __device__ void split_input(const StepArgs& a) {
   }
 }
 
-// Every block waits until all have come this far, and sees what they wrote. The
-// wait ends after a few seconds at worst.
-__device__ __forceinline__ void grid_turn(uint32_t* turns, uint32_t& turn, uint32_t* gave_up) {
-  __syncthreads();
-  ++turn;
-  if (threadIdx.x == 0) {
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(turns) : "memory");
-    if (*reinterpret_cast<volatile uint32_t*>(gave_up) == 0) {
-      const uint32_t want = turn * gridDim.x;
-      uint64_t end = 0;
-      for (uint32_t polls = 1;; ++polls) {
-        uint32_t now;
-        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(turns) : "memory");
-        if ((int32_t)(now - want) >= 0) break;
-        if ((polls & 63u) == 0) {
-          const uint64_t t = global_ns();
-          if (end == 0) end = t + 4 * kWaitNs;
-          if (t > end) {
-            *gave_up = 1;
-            break;
-          }
-        }
+// Whether a counter of arrivals has come to `want`; what the arriving blocks wrote before
+// is then visible. The wait ends after a few seconds at worst.
+__device__ __forceinline__ bool wait_count(const uint32_t* count, uint32_t want,
+                                           volatile uint32_t* gave_up) {
+  uint64_t end = 0;
+  for (uint32_t polls = 1;; ++polls) {
+    uint32_t now;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(count) : "memory");
+    if ((int32_t)(now - want) >= 0) return true;
+    if ((polls & 63u) == 0) {
+      const uint64_t t = global_ns();
+      if (end == 0) end = t + 4 * kWaitNs;
+      if (*gave_up != 0) return false;
+      if (t > end) {
+        *gave_up = 1;
+        return false;
       }
     }
   }
-  __syncthreads();
+}
+__device__ __forceinline__ void add_count(uint32_t* count) {
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+}
+
+// The order of work, the same for the loader, the issuer and the writers of every block:
+// step by step, product by product, chain by chain. f(step, kind, product, chain, count
+// of the chain's arrivals that the work has to wait for).
+template <int CG, typename F>
+__device__ __forceinline__ void in_order(const StepArgs& a, F f) {
+  uint32_t need[2] = {0, 0};
+#pragma unroll 1
+  for (uint32_t step = 0; step < a.steps; ++step) {
+#pragma unroll 1
+    for (uint32_t ph = 0; ph < 4; ++ph) {
+#pragma unroll 1
+      for (uint32_t chain = 0; chain < a.chains; ++chain) {
+        const Product& p = a.product[chain][ph < 2 ? 0 : ph - 1];
+        if (ph == 1 && p.splits == 1) continue;  // nothing to join
+        const int kind = ph == 0   ? (p.splits > 1 ? kPart : kGram)
+                         : ph == 1 ? kJoin
+                         : ph == 2 ? kPoly
+                                   : (step + 1 == a.steps ? kLast : kApply);
+        const uint32_t blocks = kind == kJoin ? min(join_units<CG>(p), gridDim.x)
+                                              : min(p.items, gridDim.x / CG) * CG;
+        const uint32_t n = chain ? need[1] : need[0];
+        if (!f(step, kind, p, chain, n)) return;
+        if (chain) need[1] += blocks;
+        else need[0] += blocks;
+      }
+    }
+  }
 }
 
 template <int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a) {
   extern __shared__ uint8_t raw[];
-  __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 4 + 2 * kWriters];
-  __shared__ uint32_t tmem_slot, gave_up;
+  __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 6 + 2 * kWriters];
+  __shared__ uint32_t tmem_slot, gave_up, written[2];
   griddep_wait();
   const uint32_t warp = threadIdx.x >> 5;
   Worker<CG> w;
   w.ring = (smem_addr(raw) + 1023u) & ~1023u;
-  const uint32_t widest = max(a.gram.n, max(a.poly.n, a.apply.n));
+  const Product* shape = a.product[0];
+  const uint32_t widest = max(shape[0].n, max(shape[1].n, shape[2].n));
   w.stage_bytes = 128 * 128 + widest / CG * 128;
   w.stages = min(kMaxStages, kRingBytes / w.stage_bytes);
   w.full = smem_addr(bars);
   w.empty = w.full + 8 * kMaxStages;
   w.acc_full = w.empty + 8 * kMaxStages;
   w.acc_empty = w.acc_full + 16;
-  w.in_bar = w.acc_empty + 16 + 16 * (warp % kWriters);
+  const uint32_t ready = w.acc_empty + 16;
+  w.in_bar = ready + 16 + 16 * (warp % kWriters);
   w.buf = w.ring + kRingBytes + (warp % kWriters) * 2 * kStageBuf;
   w.rank = CG == 1 ? 0 : cluster_rank();
   w.cluster = blockIdx.x / CG;
@@ -830,11 +884,12 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   w.gave_up = &gave_up;
   w.lead_full = CG == 1 ? w.full : cluster_addr(w.full, 0);
   w.lead_acc_empty = cluster_addr(w.acc_empty, 0);
+  w.leader = elect_one();
 
   if (threadIdx.x < sizeof(Maps) / sizeof(CUtensorMap))
     tma_prefetch_map(reinterpret_cast<const CUtensorMap*>(&m) + threadIdx.x);
   if (threadIdx.x == 0) {
-    gave_up = 0;
+    gave_up = written[0] = written[1] = 0;
     for (uint32_t s = 0; s < kMaxStages; ++s) {
       mbar_init(w.full + 8 * s, 1);
       mbar_init(w.empty + 8 * s, 1);
@@ -842,8 +897,9 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(w.acc_full + 8 * s, 1);
       mbar_init(w.acc_empty + 8 * s, CG * kWriters);
+      mbar_init(ready + 8 * s, 1);
     }
-    for (uint32_t s = 0; s < 2 * kWriters; ++s) mbar_init(w.acc_empty + 16 + 8 * s, 1);
+    for (uint32_t s = 0; s < 2 * kWriters; ++s) mbar_init(ready + 16 + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWriters) tmem_alloc<CG>(smem_addr(&tmem_slot), 2 * kAccColumns);
@@ -853,42 +909,86 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   tmem_fence_after();
   w.tmem = tmem_slot;
 
-  uint32_t turn = 0;
   const bool tall = a.tall != 0;
-  w.leader = elect_one();
-  // the first tile of each product is the same in every step
-  const Tile first[3] = {tile_of<CG>(a.gram, min(w.cluster, a.gram.items - 1)),
-                         tile_of<CG>(a.poly, min(w.cluster, a.poly.items - 1)),
-                         tile_of<CG>(a.apply, min(w.cluster, a.apply.items - 1))};
   split_input(a);
-  grid_turn(a.g.turns, turn, &gave_up);
-  for (uint32_t step = 0; step < a.steps; ++step) {
-    const CUtensorMap* x = &m.x_in[step & 1];
-#pragma unroll 1
-    for (uint32_t ph = 0; ph < 3; ++ph) {
-      const Product& p = ph == 0 ? a.gram : ph == 1 ? a.poly : a.apply;
-      const Tile t = ph == 0 ? first[0] : ph == 1 ? first[1] : first[2];
-      const CUtensorMap* ma = ph == 0 ? x : ph == 1 ? &m.s_in : tall ? x : &m.p_in;
-      const CUtensorMap* mb = ph == 0 ? x : ph == 1 ? &m.s_in : tall ? &m.p_in : x;
-      const bool a_mn = ph == 0 && tall, b_mn = (ph == 0 && tall) || (ph == 2 && !tall);
-      const int kind = ph == 0   ? (p.splits > 1 ? kPart : kGram)
-                       : ph == 1 ? kPoly
-                                 : (step + 1 == a.steps ? kLast : kApply);
-      if (!__any_sync(0xffffffffu, *w.gave_up != 0)) {
-        if (warp < kWriters) write_results(w, a, m, p, kind, step, t);
-        else if (warp == kWriters) load_operands(w, p, ma, mb, a_mn, b_mn, t);
-        else if (w.rank == 0) issue_products(w, p, a_mn, b_mn, t);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    add_count(a.g.turns);
+    wait_count(a.g.turns, gridDim.x, &gave_up);
+  }
+  __syncthreads();
+
+  auto a_major = [&](int kind) { return (kind == kGram || kind == kPart) && tall; };
+  auto b_major = [&](int kind) {
+    return kind == kGram || kind == kPart ? tall : kind != kPoly && !tall;
+  };
+  uint32_t* const turns = a.g.turns + kTurnStep;
+  // The loader waits for what the products read, and tells the block's writers; at most
+  // two of its messages can be unread (of three in a row two are of one chain, and the
+  // later one comes after the writers' arrival for the earlier), so two barriers in
+  // turn carry them.
+  uint32_t told = 0;
+  if (warp == kWriters) {
+    in_order<CG>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t need) {
+      const uint32_t item = w.first_item(p);
+      if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
+      Tile t = {};
+      if (kind != kJoin) t = tile_of<CG>(p, item);
+      bool come = true;
+      if (w.leader) {
+        come = wait_count(turns + chain * kTurnStep, need, &gave_up);
+        if (come) mbar_arrive(ready + 8 * (told & 1u));
+      }
+      if (!__all_sync(0xffffffffu, come)) return false;
+      ++told;
+      if (kind == kJoin) return true;
+      proxy_fence_global();  // the other blocks' results, read by asynchronous copies
+      const CUtensorMap *ma = &m.x_gram[step & 1][0], *mb = &m.x_gram[step & 1][1];
+      if (kind == kPoly) {
+        ma = &m.s_poly[0];
+        mb = &m.s_poly[1];
+      } else if (kind != kGram && kind != kPart) {
+        ma = tall ? &m.x_apply[step & 1] : &m.p_apply;
+        mb = tall ? &m.p_apply : &m.x_apply[step & 1];
+      }
+      return load_operands(w, p, ma, mb, a_major(kind), b_major(kind), t);
+    });
+  } else if (warp == kWriters + 1) {
+    if (w.rank == 0)
+      in_order<CG>(a, [&](uint32_t, int kind, const Product& p, uint32_t, uint32_t) {
+        const uint32_t item = w.first_item(p);
+        if (kind == kJoin || item >= p.items) return true;
+        return issue_products(w, p, a_major(kind), b_major(kind), tile_of<CG>(p, item));
+      });
+  } else {
+    in_order<CG>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t) {
+      const uint32_t item = w.first_item(p);
+      if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
+      Tile t = {};
+      if (kind != kJoin) t = tile_of<CG>(p, item);
+      if (!mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &gave_up)) return false;
+      ++told;
+      if (kind == kJoin) join_parts<CG>(a, p);
+      else if (!write_results(w, a, m, p, kind, step, t)) return false;
+      if (kind == kLast) return true;
+      // the last of the block's writers reports to the grid
+      __syncwarp();
+      if (w.leader) {
+        uint32_t before;
+        asm volatile("atom.acq_rel.cta.shared::cta.add.u32 %0, [%1], 1;"
+                     : "=r"(before)
+                     : "r"(smem_addr(&written[chain]))
+                     : "memory");
+        if (before == kWriters - 1) {
+          written[chain] = 0;
+          add_count(turns + chain * kTurnStep);
+        }
       }
       __syncwarp();
-      if (kind == kLast) break;
-      grid_turn(a.g.turns, turn, &gave_up);
-      if (kind == kPart) {
-        if (!__any_sync(0xffffffffu, *w.gave_up != 0)) join_parts<CG>(a, p);
-        __syncwarp();
-        grid_turn(a.g.turns, turn, &gave_up);
-      }
-    }
+      return true;
+    });
   }
+  __syncthreads();
   if (gave_up) {
     // Nothing of this block may still be in flight when its memory goes: wait, again
     // with a limit, for the loads and products that were begun.
@@ -932,18 +1032,41 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// fp16 [batch][rows][pitch], of which `cols` columns exist; boxes of box x box.
-bool make_map(CUtensorMap* map, const void* p, uint64_t batch, uint64_t rows, uint64_t cols,
-              uint64_t pitch, uint32_t box) {
+bool encode(CUtensorMap* map, const void* p, uint32_t rank, const cuuint64_t* dims,
+            const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   const EncodeTiled fn = encode_tiled();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {cols, rows, batch};
-  const cuuint64_t strides[2] = {pitch * 2, rows * pitch * 2};
-  const cuuint32_t size[3] = {box, box, 1}, step[3] = {1, 1, 1};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p), dims, strides, size,
-            step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            box == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(p), dims, strides,
+                  box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Matrices {  // fp16 [batch][rows][pitch], of which `cols` columns exist
+  const void* p;
+  uint64_t batch, rows, cols, pitch;
+};
+
+// Boxes of 32 x 32.
+bool box_map(CUtensorMap* map, const Matrices& a) {
+  const cuuint64_t dims[3] = {a.cols, a.rows, a.batch};
+  const cuuint64_t strides[2] = {a.pitch * 2, a.rows * a.pitch * 2};
+  const cuuint32_t box[3] = {32, 32, 1};
+  return encode(map, a.p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// An operand with `size` rows of the result's side per load. K-major: `size` rows of 64
+// columns, the columns being the summed axis. MN-major: 64 rows, the summed axis, of `size`
+// columns as groups of 64; the last group's columns beyond the matrix are the pitch's
+// padding, whatever it holds, and lead to rows or columns of the result that do not exist.
+bool operand_map(CUtensorMap* map, const Matrices& a, bool mn, uint32_t size) {
+  const cuuint64_t row = a.pitch * 2, all = a.rows * row;
+  const cuuint64_t k_dims[4] = {a.cols, a.rows, 1, a.batch}, k_strides[3] = {row, all, all};
+  const cuuint32_t k_box[4] = {64, size, 1, 1};
+  const cuuint64_t m_dims[4] = {64, a.rows, a.pitch / 64, a.batch}, m_strides[3] = {row, 128, all};
+  const cuuint32_t m_box[4] = {64, 64, size / 64, 1};
+  return encode(map, a.p, 4, mn ? m_dims : k_dims, mn ? m_strides : k_strides, mn ? m_box : k_box,
+                CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 constexpr uint32_t kSms = 152;
@@ -952,18 +1075,22 @@ struct Plan {
   uint64_t batch, m, n, k, l, pitch, kpitch;
   uint32_t blocks;  // of the norm, per matrix
   uint32_t pair;    // blocks that share a tile: 1 or 2
-  Product gram, poly, apply;
+  uint32_t chains;
+  Product product[2][3];
   size_t sums, hi0, hi1, lo, s, p, ds, dp, part, bytes;
 };
 
 uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
-// Tiles of a product and the time of its slowest worker, in products of 64 x 64 x 64.
+// Tiles of a product and the time of its slowest worker, in units of 128 cycles. A block
+// of 64 along the summed axis takes n / 64 of them on the tensor cores, and its operands
+// 58 bytes per cycle and SM from L2 when all SMs fetch; writing 64 columns of a tile takes
+// about 16, beside the next tile's product.
 Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t depth, bool symmetric,
-                      uint32_t pair, uint32_t n, bool may_split, double* time) {
+                      uint32_t pair, uint32_t n, bool may_split, uint64_t all, double* time) {
   Product p = {};
   const uint64_t workers = kSms / pair, tr = ceil_div(rows, 128 * pair), tc = ceil_div(cols, n);
-  const uint64_t ratio = 128 * pair / n ? 128 * pair / n : 1;
+  const uint64_t ratio = std::max<uint64_t>(1, 128 * pair / n);
   p.n = n;
   p.rows = (uint32_t)rows;
   p.cols = (uint32_t)cols;
@@ -972,18 +1099,24 @@ Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dep
   const uint64_t tiles = symmetric ? ratio * tr * (tr + 1) / 2 : tr * tc;
   p.tiles = (uint32_t)tiles;
   p.splits = 1;
-  // joining the parts costs a turn of the grid, the time of about 40 blocks
-  if (may_split && tiles * batch * 2 <= workers && p.blocks >= 64)
-    p.splits = (uint32_t)std::min<uint64_t>(workers / (tiles * batch), p.blocks / 8);
-  const uint64_t items = tiles * batch * p.splits;
-  p.items = items > 0xffffffffull ? 0 : (uint32_t)items;
-  // a block of 64 of the summed axis: the products, or the operands' way from L2 when
-  // many SMs fetch at one time
+  // joining the parts costs a turn of the grid
+  if (may_split && tiles * all * 2 <= workers && p.blocks >= 64)
+    p.splits = (uint32_t)std::min<uint64_t>(workers / (tiles * all), p.blocks / 8);
+  uint64_t items = tiles * batch * p.splits;
+  // a last round that at most half of the workers would have work in is done in half
+  // tiles, of 64 operand rows per block at least
+  const uint64_t left = items % workers;
+  const bool halves = p.splits == 1 && all == 1 && items > workers && n >= 128 * pair && left * 2 <= workers;
+  p.whole = (uint32_t)(halves ? items - left : items);
+  if (halves) items += left;
+  p.items = items > 0x7fffffffull ? 0 : (uint32_t)items;
   const double busy = std::min(1.0, (double)items / (double)workers);
-  const double each = std::max(n / 64.0, (128 + n / pair) / 45.0 * busy);
-  *time = (double)ceil_div(items, workers) *
-              ((double)ceil_div(p.blocks, p.splits) * each + 4.0 + n / 32.0) +
-          (p.splits > 1 ? 60.0 : 0.0);
+  const double each = std::max(n / 64.0, (128 + n / pair) / 58.0 * busy);
+  const double product = (double)ceil_div(p.blocks, p.splits) * each, write = n / 4.0;
+  const double rounds = (double)ceil_div(p.whole, workers) + (halves && left ? 0.5 : 0.0);
+  *time = product + (rounds - 1) * std::max(product, write) + write + (p.splits > 1 ? 60.0 : 0.0);
+  if (all > 1)  // two chains: each one's latency, or the work of both
+    *time = std::max((*time + product + write) / 2 + 20, rounds * std::max(product, write));
   return p;
 }
 
@@ -993,7 +1126,8 @@ Product best_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dept
   *best = 0;
   for (uint32_t n = 64 * pair; n <= 128 * pair; n *= 2) {
     double t;
-    const Product q = shape_product(batch, rows, cols, depth, symmetric, pair, n, may_split, &t);
+    const Product q =
+        shape_product(batch, rows, cols, depth, symmetric, pair, n, may_split, batch, &t);
     if (n == 64 * pair || t <= *best) {
       p = q;
       *best = t;
@@ -1013,8 +1147,9 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   q.l = std::max(m, n);
   q.pitch = align_up(n, 64);
   q.kpitch = align_up(q.k, 64);
-  q.blocks = (uint32_t)std::min<uint64_t>(ceil_div(m * ceil_div(n, kPiece), 8), kSms * 4);
+  q.blocks = (uint32_t)std::min<uint64_t>(ceil_div(m * ceil_div(n, kPiece), 8), kSms * 3);
   double best = 0;
+  uint32_t width[3] = {0, 0, 0};
   for (uint32_t pair = 1; pair <= 2; ++pair) {
     double t[3];
     const Product g = best_product(batch, q.k, q.k, q.l, true, pair, true, &t[0]);
@@ -1024,12 +1159,31 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
     if (pair == 1 || sum <= best) {
       best = sum;
       q.pair = pair;
-      q.gram = g;
-      q.poly = p;
-      q.apply = a;
+      width[0] = g.n;
+      width[1] = p.n;
+      width[2] = a.n;
     }
   }
-  if (batch && (!q.gram.items || !q.poly.items || !q.apply.items)) return false;
+  q.chains = batch > 1 ? 2 : 1;
+  size_t parts = 0;
+  for (uint32_t c = 0; c < q.chains; ++c) {
+    const uint64_t b0 = c ? (batch + 1) / 2 : 0;
+    const uint64_t some = q.chains == 1 ? batch : c ? batch / 2 : (batch + 1) / 2;
+    for (int i = 0; i < 3; ++i) {
+      double t;
+      Product& p = q.product[c][i];
+      p = shape_product(some, i < 2 ? q.k : m, i < 2 ? q.k : n, i == 0 ? q.l : q.k, i < 2, q.pair,
+                        width[i], i == 0, batch, &t);
+      if (batch && !p.items) return false;
+      p.b0 = (uint32_t)b0;
+      // the second chain starts beside the first one
+      p.offset = c ? q.product[0][i].items % (kSms / q.pair) : 0;
+      if (p.splits > 1) {
+        p.part0 = (uint32_t)parts;
+        parts += p.items;
+      }
+    }
+  }
   const size_t x = q.batch * m * q.pitch * 2, s = q.batch * q.k * q.kpitch * 2;
   size_t at = 256;
   auto take = [&](size_t bytes) {
@@ -1045,8 +1199,7 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   q.p = take(s);
   q.ds = take(q.batch * q.k * sizeof(float));
   q.dp = take(q.batch * q.k * sizeof(float));
-  q.part = take(q.gram.splits > 1
-                    ? (size_t)q.gram.items * q.pair * 128 * q.gram.n * sizeof(float) : 0);
+  q.part = take(parts * q.pair * 128 * width[0] * sizeof(float));
   q.bytes = at;
   return true;
 }
@@ -1085,15 +1238,21 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   char* w = static_cast<char*>(ws);
   char *hi0 = w + q.hi0, *hi1 = w + q.hi1, *lo = w + q.lo, *sm = w + q.s, *pm = w + q.p;
   Maps m;
-  if (!make_map(&m.x_in[0], hi0, q.batch, q.m, q.n, q.pitch, 64) ||
-      !make_map(&m.x_in[1], hi1, q.batch, q.m, q.n, q.pitch, 64) ||
-      !make_map(&m.s_in, sm, q.batch, q.k, q.k, q.kpitch, 64) ||
-      !make_map(&m.p_in, pm, q.batch, q.k, q.k, q.kpitch, 64) ||
-      !make_map(&m.x_out[0], hi0, q.batch, q.m, q.n, q.pitch, 32) ||
-      !make_map(&m.x_out[1], hi1, q.batch, q.m, q.n, q.pitch, 32) ||
-      !make_map(&m.lo_out, lo, q.batch, q.m, q.n, q.pitch, 32) ||
-      !make_map(&m.s_out, sm, q.batch, q.k, q.k, q.kpitch, 32))
-    return SPARCML_ERR_CUDA;
+  const bool tall = q.m > q.n;
+  const Matrices x[2] = {{hi0, q.batch, q.m, q.n, q.pitch}, {hi1, q.batch, q.m, q.n, q.pitch}};
+  const Matrices low = {lo, q.batch, q.m, q.n, q.pitch};
+  const Matrices sq = {sm, q.batch, q.k, q.k, q.kpitch}, pq = {pm, q.batch, q.k, q.k, q.kpitch};
+  uint32_t second[3];  // rows of the second operand that one block loads
+  for (int i = 0; i < 3; ++i) second[i] = q.product[0][i].n / q.pair;
+  bool ok = box_map(&m.lo_out, low) && box_map(&m.s_out, sq) &&
+            operand_map(&m.s_poly[0], sq, false, 128) &&
+            operand_map(&m.s_poly[1], sq, false, second[1]) &&
+            operand_map(&m.p_apply, pq, false, tall ? second[2] : 128);
+  for (int i = 0; i < 2 && ok; ++i)
+    ok = box_map(&m.x_out[i], x[i]) && operand_map(&m.x_gram[i][0], x[i], tall, 128) &&
+         operand_map(&m.x_gram[i][1], x[i], tall, second[0]) &&
+         operand_map(&m.x_apply[i], x[i], !tall, tall ? 128 : second[2]);
+  if (!ok) return SPARCML_ERR_CUDA;
   const int64_t ge = g.g_type == SPARCML_F32 ? 16 : 8;
   g.vec_g = aligned_to(g.g, ge) && g.g_batch % 4 == 0 && g.g_stride % 4 == 0;
   g.vec_m = aligned_to(g.mom, 16) && g.m_batch % 4 == 0 && g.m_stride % 4 == 0;
@@ -1106,10 +1265,9 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   a.g = g;
   a.batch = (uint32_t)q.batch;
   a.steps = (uint32_t)steps;
-  a.tall = q.m > q.n;
-  a.gram = q.gram;
-  a.poly = q.poly;
-  a.apply = q.apply;
+  a.tall = tall;
+  a.chains = q.chains;
+  for (uint32_t c = 0; c < q.chains; ++c) std::copy(q.product[c], q.product[c] + 3, a.product[c]);
   std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
   a.hi[0] = reinterpret_cast<__half*>(hi0);
   a.hi[1] = reinterpret_cast<__half*>(hi1);
