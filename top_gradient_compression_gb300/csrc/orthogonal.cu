@@ -262,9 +262,22 @@ __device__ __forceinline__ Tile tile_of(const Product& p, uint32_t item) {
   t.row0 = i * 128 * CG;
   t.col0 = j * p.n + half * t.n;
   t.none = t.col0 >= p.cols;
-  t.first = (uint32_t)((uint64_t)p.blocks * split / p.splits);
-  t.last = (uint32_t)((uint64_t)p.blocks * (split + 1) / p.splits);
+  t.first = 0;
+  t.last = p.blocks;
+  if (p.splits > 1) {  // at most 2^18 blocks in at most 152 parts
+    t.first = p.blocks * split / p.splits;
+    t.last = p.blocks * (split + 1) / p.splits;
+  }
   return t;
+}
+// Has the tile worked out, or the product's parameters read, here and not where they are
+// first used.
+__device__ __forceinline__ void pin(Tile& t) {
+  asm volatile("" : "+r"(t.b), "+r"(t.row0), "+r"(t.col0), "+r"(t.n), "+r"(t.first), "+r"(t.last));
+}
+__device__ __forceinline__ void pin(Product& p) {
+  asm volatile("" : "+r"(p.n), "+r"(p.rows), "+r"(p.cols), "+r"(p.items), "+r"(p.splits),
+               "+r"(p.tiles), "+r"(p.part0));
 }
 
 // Byte offset of 16-byte piece c of row r in a 32 x 32 fp16 box, 64-byte swizzled.
@@ -553,7 +566,6 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
   const uint32_t quarter = warp & 3u, half = warp >> 2;
   const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
   const bool pairs = kind == kApply || kind == kLast, reads = kind == kPoly || pairs;
-  if (reads && lane == 0) proxy_fence_global();  // the other blocks' results, fetched below
   for (uint32_t item = w.first_item(p); item < p.items; item += w.clusters) {
     if (item >= w.clusters) t = tile_of<CG>(p, item);
     if (t.none) continue;
@@ -679,7 +691,8 @@ __device__ __forceinline__ uint32_t join_units(const Product& p) {
   return p.items / p.splits * 4 * CG * (p.n / 8);
 }
 template <int CG>
-__device__ void join_parts(const StepArgs& a, const Product& p) {
+__device__ void join_parts(const StepArgs& a, Product p) {
+  pin(p);
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
   const uint32_t across = p.n / 8, per = 4 * CG * across, total = join_units<CG>(p);
   for (uint32_t x = blockIdx.x + gridDim.x * warp; x < total; x += gridDim.x * kWriters) {
@@ -911,6 +924,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
 
   const bool tall = a.tall != 0;
   split_input(a);
+  proxy_fence_global();
   __syncthreads();
   if (threadIdx.x == 0) {
     add_count(a.g.turns);
@@ -934,6 +948,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
       Tile t = {};
       if (kind != kJoin) t = tile_of<CG>(p, item);
+      pin(t);
       bool come = true;
       if (w.leader) {
         come = wait_count(turns + chain * kTurnStep, need, &gave_up);
@@ -942,7 +957,6 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       if (!__all_sync(0xffffffffu, come)) return false;
       ++told;
       if (kind == kJoin) return true;
-      proxy_fence_global();  // the other blocks' results, read by asynchronous copies
       const CUtensorMap *ma = &m.x_gram[step & 1][0], *mb = &m.x_gram[step & 1][1];
       if (kind == kPoly) {
         ma = &m.s_poly[0];
@@ -958,7 +972,9 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       in_order<CG>(a, [&](uint32_t, int kind, const Product& p, uint32_t, uint32_t) {
         const uint32_t item = w.first_item(p);
         if (kind == kJoin || item >= p.items) return true;
-        return issue_products(w, p, a_major(kind), b_major(kind), tile_of<CG>(p, item));
+        Tile t = tile_of<CG>(p, item);
+        pin(t);
+        return issue_products(w, p, a_major(kind), b_major(kind), t);
       });
   } else {
     in_order<CG>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t) {
@@ -966,12 +982,15 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
       Tile t = {};
       if (kind != kJoin) t = tile_of<CG>(p, item);
+      pin(t);
       if (!mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &gave_up)) return false;
       ++told;
       if (kind == kJoin) join_parts<CG>(a, p);
       else if (!write_results(w, a, m, p, kind, step, t)) return false;
       if (kind == kLast) return true;
-      // the last of the block's writers reports to the grid
+      // what was written is read by asynchronous copies; the last of the block's writers
+      // reports to the grid
+      proxy_fence_global();
       __syncwarp();
       if (w.leader) {
         uint32_t before;
