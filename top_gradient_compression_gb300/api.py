@@ -547,6 +547,11 @@ def _stat(t, rows: int, name: str):
     return ptr
 
 
+def _new_like(x):
+    return torch.empty_like(x) if x.is_contiguous() else \
+        torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
 def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None, rstd=None,
                stream=None):
     """Layer norm over the last axis of x (float32, bfloat16 or float16; the other
@@ -561,27 +566,26 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
         wt = bt
     elif b is not None and bt != wt:
         raise TypeError("weight and bias must have the same type")
-    lead = x.shape[:-1]
     if out is None:
-        out, ys = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
+        out, ys = _new_like(x), dim
     else:
         _typed(out, "out", x)
         ys = _rows(out, "out")[2]
         if out.shape != x.shape:
             raise ValueError("out and x shapes differ")
     if mean is None:
-        mean = torch.empty(lead, dtype=torch.float32, device=x.device)
-        mp = mean.data_ptr()
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
     else:
-        mp = _stat(mean, rows, "mean")
+        _stat(mean, rows, "mean")
     if rstd is None:
-        rstd = torch.empty(lead, dtype=torch.float32, device=x.device)
-        rp = rstd.data_ptr()
+        rstd = torch.empty_like(mean)
     else:
-        rp = _stat(rstd, rows, "rstd")
-    _check("sparcml_layer_norm", _lib.load().sparcml_layer_norm(
-        x.data_ptr(), code, xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys, mp, rp,
-        _raw_stream(stream, x)))
+        _stat(rstd, rows, "rstd")
+    r = (_lib._lib or _lib.load()).sparcml_layer_norm(
+        x.data_ptr(), code, xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys, mean.data_ptr(),
+        rstd.data_ptr(), _raw_stream(stream, x))
+    if r:
+        _check("sparcml_layer_norm", r)
     return out, mean, rstd
 
 
@@ -603,7 +607,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
         raise ValueError("dy and x shapes differ")
     w, wt = _vector(weight, dim, "weight")
     if dx is None:
-        dx, os = torch.empty(x.shape, dtype=x.dtype, device=x.device), dim
+        dx, os = _new_like(x), dim
     else:
         _typed(dx, "dx", x)
         os = _rows(dx, "dx")[2]
@@ -613,20 +617,20 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
         raise ValueError("accumulate needs dweight and dbias to add to")
     if dweight is None:
         dweight = torch.empty(dim, dtype=torch.float32, device=x.device)
-        dwp = dweight.data_ptr()
     else:
-        dwp = _stat(dweight, dim, "dweight")
+        _stat(dweight, dim, "dweight")
     if dbias is None:
-        dbias = torch.empty(dim, dtype=torch.float32, device=x.device)
-        dbp = dbias.data_ptr()
+        dbias = torch.empty_like(dweight)
     else:
-        dbp = _stat(dbias, dim, "dbias")
+        _stat(dbias, dim, "dbias")
     if ws is None:
         ws = workspace(layer_norm_backward_workspace_size(rows, dim), x.device)
-    _check("sparcml_layer_norm_backward", _lib.load().sparcml_layer_norm_backward(
+    r = (_lib._lib or _lib.load()).sparcml_layer_norm_backward(
         dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt, _stat(mean, rows, "mean"),
-        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dwp, dbp, int(accumulate),
-        ws.data_ptr(), ws.numel(), _raw_stream(stream, x)))
+        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dweight.data_ptr(),
+        dbias.data_ptr(), accumulate, ws.data_ptr(), ws.numel(), _raw_stream(stream, x))
+    if r:
+        _check("sparcml_layer_norm_backward", r)
     return dx, dweight, dbias
 
 

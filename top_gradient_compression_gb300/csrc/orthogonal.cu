@@ -1133,7 +1133,9 @@ Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dep
   const double each = std::max(n / 64.0, (128 + n / pair) / 58.0 * busy);
   const double product = (double)ceil_div(p.blocks, p.splits) * each, write = n / 4.0;
   const double rounds = (double)ceil_div(p.whole, workers) + (halves && left ? 0.5 : 0.0);
-  *time = product + (rounds - 1) * std::max(product, write) + write + (p.splits > 1 ? 60.0 : 0.0);
+  *time = product + (rounds - 1) * std::max(product, write) + write;
+  if (p.splits > 1)  // a turn of the grid, and the partial tiles' way to L2 and back
+    *time += 60.0 + (double)items * pair * 128 * n * 8 / (kSms * 40.0 * 128.0);
   if (all > 1)  // two chains: each one's latency, or the work of both
     *time = std::max((*time + product + write) / 2 + 20, rounds * std::max(product, write));
   return p;
