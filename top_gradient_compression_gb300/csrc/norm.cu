@@ -35,7 +35,27 @@ struct Group {
     v.x += __shfl_xor_sync(0xffffffffu, v.x, D);
     v.y += __shfl_xor_sync(0xffffffffu, v.y, D);
   }
-  __device__ __forceinline__ float sum(float2 v) { return sum2(make_float2(v.x + v.y, 0.f)).x; }
+  __device__ __forceinline__ float sum(float2 two) {
+    float v = two.x + two.y;
+    if (threads >= 32) v += __shfl_xor_sync(0xffffffffu, v, 16);
+    if (threads >= 16) v += __shfl_xor_sync(0xffffffffu, v, 8);
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if (threads <= 32) return v;
+    float2* s = scratch + 33 * (turn & 1u);
+    ++turn;
+    const uint32_t lane = lane_id(), nw = threads >> 5;
+    if (lane == 0) s[t >> 5].x = v;
+    sync();
+    v = lane < nw ? s[lane].x : 0.f;
+    if (nw > 8) {
+      if (nw > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
+      v += __shfl_xor_sync(0xffffffffu, v, 8);
+    }
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    return __shfl_sync(0xffffffffu, v, 0);
+  }
   // Sums of two values. `turn` alternates between the halves of the scratch from call to
   // call, so that one barrier per call is enough.
   __device__ __forceinline__ float2 sum2(float2 v) {
@@ -167,13 +187,18 @@ struct NormArgs {
 // way, which keeps 64 to 96 KB per SM in flight. Rows of whole, aligned packs go into
 // registers; others (V = 2) through shared memory, where the weights wait in fp32. (Loaded
 // from memory one element at a time, 16384 x 4095 bf16 took 181 us.)
-template <typename T, typename W, int V, int NV, int MAXT, int MINB>
+//
+// What bounds it in 16 bits is arithmetic: 16384 x 4096 bf16 needs 680 of the 700 issue
+// cycles that a row's bytes take when each pass over the row converts it again. With KEEP
+// the fp32 values, and then their deviations, stay in registers.
+template <typename T, typename W, int V, int NV, bool KEEP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs a) {
   griddep_wait();
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ float2 scratch[MAXT >= 64 ? 66 * (MAXT / 64) : 1];
   constexpr bool PACKS = V > 2;
   constexpr int P = V / 2;
+  constexpr bool PK = PACKS && !KEEP;
   Group g = make_group(a.threads, scratch);
   const uint32_t threads = a.threads, groups = blockDim.x / threads, dim = (uint32_t)a.dim;
   const uint32_t t = g.t;
@@ -231,19 +256,25 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
       turn ^= 1u;
       fetch(row + step, turn);
     }
+    F2 kept[KEEP ? NV : 1][P];
     F2 s = f2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (column<V>(j, 0, threads, t) < end) {
         F2 f[P];
         unpack<T, V>(v[j], f);
+        if constexpr (KEEP) {
+#pragma unroll
+          for (int i = 0; i < P; ++i) kept[j][i] = f[i];
+        } else {
+          v[j].forget();
+        }
 #pragma unroll
         for (int d = 1; d < P; d *= 2) {
 #pragma unroll
-          for (int i = 0; i < P; i += 2 * d) f[i] = f[i] + f[i + d];
+          for (int i = 0; i < P; i += 2 * d) f[i] = add2<PK>(f[i], f[i + d]);
         }
-        s = s + f[0];
-        v[j].forget();
+        s = add2<PK>(s, f[0]);
       }
     const float mean = g.sum(split(s)) * inv;
     s = f2(0.f, 0.f);
@@ -252,18 +283,19 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
     for (int j = 0; j < NV; ++j)
       if (column<V>(j, 0, threads, t) < end) {
         F2 f[P], q = f2(0.f, 0.f);
-        unpack<T, V>(v[j], f);
+        if constexpr (!KEEP) unpack<T, V>(v[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          f[i] = f[i] + minus;
+          f[i] = add2<PK>(KEEP ? kept[KEEP ? j : 0][i] : f[i], minus);
+          if (KEEP) kept[KEEP ? j : 0][i] = f[i];
           if (!PACKS && column<V>(j, 1, threads, t) >= dim) f[i] = f2(split(f[i]).x, 0.f);
-          q = fma2(f[i], f[i], q);
+          q = fma2<PK>(f[i], f[i], q);
         }
-        s = s + q;
+        s = add2<PK>(s, q);
         v[j].forget();
       }
     const float var = g.sum(split(s)) * inv;
-    const float rstd = 1.0f / sqrtf(var + a.eps);
+    const float rstd = rsqrtf(var + a.eps);
     if (!active) continue;
     if (t == 0) {
       a.mean[row] = mean;
@@ -283,9 +315,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
           w[0] = pair_at(affine, c, c + threads, dim);
           b[0] = pair_at(affine + dim, c, c + threads, dim);
         }
-        unpack<T, V>(v[j], f);
+        if constexpr (!KEEP) unpack<T, V>(v[j], f);
 #pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = fma2((f[i] + minus) * by, w[i], b[i]);
+        for (int i = 0; i < P; ++i)
+          f[i] = fma2<PK>(mul2<PK>(KEEP ? kept[KEEP ? j : 0][i] : add2<PK>(f[i], minus), by), w[i],
+                          b[i]);
         store_pack<T, V>(y, j, threads, t, dim, f);
       }
     }
@@ -485,6 +519,10 @@ norm_backward_kernel(const NormGradArgs a) {
     slot = slot + 1 == kSlots ? 0 : slot + 1;
     F2 s0 = f2(0.f, 0.f), s1 = s0;
     const F2 minus = f2(-mean, -mean), by = f2(rstd, rstd);
+    // 16-bit packs keep x - mean and dy w in fp32 for the second pass (84 us against 86 at
+    // 16384 x 4096); fp32 ones and pairs have no registers left, or nothing to convert.
+    constexpr bool KEEP = PACKS && sizeof(T) == 2;
+    F2 xc[KEEP ? NV : 1][P], kept[KEEP ? NV : 1][P];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const uint32_t c = column<V>(j, 0, threads, t);
@@ -495,12 +533,17 @@ norm_backward_kernel(const NormGradArgs a) {
         unpack<T, V>(vx[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          const F2 xh = (f[i] + minus) * by;
-          gw[j][i] = fma2(d[i], xh, gw[j][i]);
-          gb[j][i] = gb[j][i] + d[i];
-          const F2 dw = d[i] * w[i];
-          s0 = s0 + dw;
-          s1 = fma2(dw, xh, s1);
+          f[i] = add2<false>(f[i], minus);
+          const F2 xh = mul2<false>(f[i], by);
+          gw[j][i] = fma2<false>(d[i], xh, gw[j][i]);
+          gb[j][i] = add2<false>(gb[j][i], d[i]);
+          d[i] = mul2<false>(d[i], w[i]);
+          s0 = add2<false>(s0, d[i]);
+          s1 = fma2<false>(d[i], xh, s1);
+          if constexpr (KEEP) {
+            xc[j][i] = f[i];
+            kept[j][i] = d[i];
+          }
         }
         vx[j].forget();
         vd[j].forget();
@@ -518,12 +561,17 @@ norm_backward_kernel(const NormGradArgs a) {
       const uint32_t c = column<V>(j, 0, threads, t);
       if (c < dim) {
         F2 w[P], d[P], f[P];
-        weights_at(j, c, w);
-        unpack<T, V>(vd[j], d);
-        unpack<T, V>(vx[j], f);
+        if constexpr (!KEEP) {
+          weights_at(j, c, w);
+          unpack<T, V>(vd[j], d);
+          unpack<T, V>(vx[j], f);
+        }
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          f[i] = fma2(f[i] + minus, k2, fma2(d[i] * w[i], by, k1));
+        for (int i = 0; i < P; ++i) {
+          const F2 dv = KEEP ? kept[KEEP ? j : 0][i] : mul2<false>(d[i], w[i]);
+          const F2 xv = KEEP ? xc[KEEP ? j : 0][i] : add2<false>(f[i], minus);
+          f[i] = fma2<false>(xv, k2, fma2<false>(dv, by, k1));
+        }
         store_pack<T, V>(dx, j, threads, t, dim, f);
       }
     }
@@ -668,9 +716,9 @@ uint32_t threads_for(uint64_t dim, uint32_t per) {
 constexpr uint32_t kSms = 152;
 
 // `threads` for a row, blocks of at least `block` threads, `fit` of them per SM.
-template <typename T, typename W, int V, int NV, int MAXT, int MINB>
+template <typename T, typename W, int V, int NV, bool KEEP, int MAXT, int MINB>
 bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, cudaStream_t s) {
-  auto kernel = norm_forward_kernel<T, W, V, NV, MAXT, MINB>;
+  auto kernel = norm_forward_kernel<T, W, V, NV, KEEP, MAXT, MINB>;
   a.threads = threads;
   const uint32_t groups = std::max(1u, block / threads);
   size_t smem = 0;
@@ -686,21 +734,25 @@ bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, 
   return true;
 }
 
-// Up to 16 packs per lane a warp takes a row alone, which needs no barrier; short rows
-// share a warp, and longer ones take several.
+// Up to 16 packs per lane a warp takes a row alone, which needs no barrier (2048 fp32
+// columns: 53 us against 61 with four warps); short rows share a warp, and longer ones take
+// several. Few packs are kept in fp32: 65536 x 512 bf16 30 us against 36.
 template <typename T, typename W>
 bool forward_packs(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const uint64_t packs = a.dim / V;
   if (packs <= 32)
-    return launch_forward<T, W, V, 1, 128, 11>(a, packs <= 8 ? 8 : packs <= 16 ? 16 : 32, 128, 11,
-                                               s);
-  if (packs <= 64) return launch_forward<T, W, V, 2, 128, 10>(a, 32, 128, 10, s);
-  if (packs <= 128) return launch_forward<T, W, V, 4, 128, 7>(a, 32, 128, 7, s);
-  if (packs <= 256) return launch_forward<T, W, V, 8, 128, 4>(a, 32, 128, 4, s);
-  if (packs <= 512) return launch_forward<T, W, V, 16, 128, 3>(a, 32, 128, 3, s);
+    return launch_forward<T, W, V, 1, true, 128, 10>(
+        a, packs <= 8 ? 8 : packs <= 16 ? 16 : 32, 128, 10, s);
+  if (packs <= 64) return launch_forward<T, W, V, 2, true, 128, 8>(a, 32, 128, 8, s);
+  if (packs <= 128) return launch_forward<T, W, V, 4, false, 128, 7>(a, 32, 128, 7, s);
+  if (packs <= 256) return launch_forward<T, W, V, 8, false, 128, 4>(a, 32, 128, 4, s);
+  if (packs <= 512) return launch_forward<T, W, V, 16, false, 128, 3>(a, 32, 128, 3, s);
   const uint32_t threads = threads_for(packs, 4);
-  return launch_forward<T, W, V, 4, 1024, 1>(a, threads, threads, std::max(1u, 1024 / threads), s);
+  if (packs <= 2048)
+    return launch_forward<T, W, V, 4, true, 512, 1>(a, threads, threads,
+                                                    std::max(1u, 640 / threads), s);
+  return launch_forward<T, W, V, 4, false, 1024, 1>(a, threads, threads, 1, s);
 }
 
 // Whole packs: 16-byte aligned rows and weights of the rows' type or fp32. Everything else
@@ -716,8 +768,8 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
   if (a.dim <= 512 * 16) {
     const uint32_t threads = threads_for(a.dim, 16);
     if (threads <= 256)
-      return launch_forward<T, T, 2, 8, 256, 3>(a, threads, 256, 3, s);
-    return launch_forward<T, T, 2, 8, 512, 1>(a, threads, threads, 2, s);
+      return launch_forward<T, T, 2, 8, false, 256, 3>(a, threads, 256, 3, s);
+    return launch_forward<T, T, 2, 8, false, 512, 1>(a, threads, threads, 2, s);
   }
   launch_pdl(norm_forward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
   return true;
