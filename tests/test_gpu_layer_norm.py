@@ -128,6 +128,19 @@ def test_types_of_weights_may_differ_and_be_missing():
                        api.layer_norm_backward(dy, x, got[1], got[2], wt))
 
 
+@pytest.mark.parametrize("rows,dim", [(40, 768), (40, 769), (5, 9000), (5, 9001)])
+def test_in_place_gradients(rows, dim):
+    """dx over dy or over x: the sums and dx come from what stood there before."""
+    x, dy, w, b = make(rows, dim, torch.bfloat16, 21)
+    y, mean, rstd = api.layer_norm(x, w, b)
+    want = api.layer_norm_backward(dy, x, mean, rstd, w)
+    for which in ("dy", "x"):
+        args = {"dy": dy.clone(), "x": x.clone()}
+        got = api.layer_norm_backward(args["dy"], args["x"], mean, rstd, w, dx=args[which])
+        for p, q in zip(want, got):
+            assert torch.equal(p, q)
+
+
 def test_in_place_three_axes_and_no_rows():
     x, dy, w, b = make(24, 96, torch.float32, 3)
     y, mean, rstd = api.layer_norm(x, w, b)

@@ -326,9 +326,38 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
   }
 }
 
-// Rows too long for a block's registers: the row is read again for each sum
-// (from L2, where one row of any such length fits).
-template <typename T>
+// Rows too long for a block's registers: the row is read again for each sum (from L2, where
+// one row of any such length fits), in packs where it consists of them (V > 1).
+template <typename T, int V>
+__device__ __forceinline__ void load_floats(const T* p, uint64_t c, float (&f)[V]) {
+  if constexpr (V == 1) {
+    f[0] = to_f32(p[c]);
+  } else {
+    F2 q[V / 2];
+    unpack<T, V>(load_raw<T, V>(p + c), q);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = i & 1 ? q[i / 2].y : q[i / 2].x;
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_floats(T* p, uint64_t c, const float (&f)[V]) {
+  if constexpr (V == 1) {
+    p[c] = from_f32<T>(f[0]);
+  } else {
+    F2 q[V / 2];
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) q[i] = f2(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p + c) = pack<T, V>(q);
+  }
+}
+template <int V>
+__device__ __forceinline__ void weight_floats(const void* w, int32_t type, uint64_t c, float none,
+                                              float (&f)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = w ? load_any(w, type, c + i) : none;
+}
+
+template <typename T, int V>
 __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
@@ -337,22 +366,36 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs 
   T* y = static_cast<T*>(a.y) + (int64_t)blockIdx.x * a.y_stride;
   const float inv = 1.0f / (float)a.dim;
   float2 s = make_float2(0.f, 0.f);
-  for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) s.x += to_f32(x[c]);
-  const float mean = g.sum(s) * inv;
-  s.x = 0.f;
-  for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-    const float d = to_f32(x[c]) - mean;
-    s.x += d * d;
+#pragma unroll 2
+  for (uint64_t c = threadIdx.x * V; c < a.dim; c += blockDim.x * V) {
+    float f[V];
+    load_floats<T, V>(x, c, f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) (i & 1 ? s.y : s.x) += f[i];
   }
-  const float rstd = 1.0f / sqrtf(g.sum(s) * inv + a.eps);
+  const float mean = g.sum(s) * inv;
+  s = make_float2(0.f, 0.f);
+#pragma unroll 2
+  for (uint64_t c = threadIdx.x * V; c < a.dim; c += blockDim.x * V) {
+    float f[V];
+    load_floats<T, V>(x, c, f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) (i & 1 ? s.y : s.x) += (f[i] - mean) * (f[i] - mean);
+  }
+  const float rstd = rsqrtf(g.sum(s) * inv + a.eps);
   if (threadIdx.x == 0) {
     a.mean[blockIdx.x] = mean;
     a.rstd[blockIdx.x] = rstd;
   }
-  for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-    const float w = a.w ? load_any(a.w, a.w_type, c) : 1.f;
-    const float b = a.b ? load_any(a.b, a.w_type, c) : 0.f;
-    y[c] = from_f32<T>((to_f32(x[c]) - mean) * rstd * w + b);
+#pragma unroll 2
+  for (uint64_t c = threadIdx.x * V; c < a.dim; c += blockDim.x * V) {
+    float f[V], w[V], b[V];
+    load_floats<T, V>(x, c, f);
+    weight_floats<V>(a.w, a.w_type, c, 1.f, w);
+    weight_floats<V>(a.b, a.w_type, c, 0.f, b);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
+    store_floats<T, V>(y, c, f);
   }
 }
 
@@ -637,9 +680,9 @@ norm_backward_kernel(const NormGradArgs a) {
   if (threadIdx.x == 0) *a.ticket = 0;  // as the next call needs it
 }
 
-// Rows too long for a block's registers: dx by re-reading the row, the column
-// sums by norm_columns_kernel.
-template <typename T>
+// Rows too long for a block's registers: dx by re-reading the row, the column sums by
+// norm_columns_kernel.
+template <typename T, int V>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGradArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
@@ -650,35 +693,59 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGrad
   const float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
   const float inv = 1.0f / (float)a.dim;
   float2 s = make_float2(0.f, 0.f);
-  for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-    const float d = to_f32(dy[c]) * (a.w ? load_any(a.w, a.w_type, c) : 1.f);
-    s.x += d;
-    s.y += d * ((to_f32(x[c]) - mean) * rstd);
+#pragma unroll 2
+  for (uint64_t c = threadIdx.x * V; c < a.dim; c += blockDim.x * V) {
+    float f[V], d[V], w[V];
+    load_floats<T, V>(x, c, f);
+    load_floats<T, V>(dy, c, d);
+    weight_floats<V>(a.w, a.w_type, c, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      s.x += d[i] * w[i];
+      s.y += d[i] * w[i] * ((f[i] - mean) * rstd);
+    }
   }
   s = g.sum2(s);
   const float c1 = s.x * inv, c2 = s.y * inv;
-  for (uint64_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-    const float d = to_f32(dy[c]) * (a.w ? load_any(a.w, a.w_type, c) : 1.f);
-    const float xh = (to_f32(x[c]) - mean) * rstd;
-    dx[c] = from_f32<T>(rstd * (d - c1 - xh * c2));
+#pragma unroll 2
+  for (uint64_t c = threadIdx.x * V; c < a.dim; c += blockDim.x * V) {
+    float f[V], d[V], w[V];
+    load_floats<T, V>(x, c, f);
+    load_floats<T, V>(dy, c, d);
+    weight_floats<V>(a.w, a.w_type, c, 1.f, w);
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = rstd * (d[i] * w[i] - c1 - (f[i] - mean) * rstd * c2);
+    store_floats<T, V>(dx, c, f);
   }
 }
 
-// part[blockIdx.y][c] = sums over the rows blockIdx.y, blockIdx.y + gridDim.y, ...
-template <typename T>
-__global__ void __launch_bounds__(256) norm_columns_kernel(const NormGradArgs a) {
+// part[blockIdx.y][c] = sums over the rows blockIdx.y, blockIdx.y + gridDim.y, ... of x and dy
+// as they were: this kernel runs before the one above, which may write dx over either.
+template <typename T, int V>
+__global__ void __launch_bounds__(128) norm_columns_kernel(const NormGradArgs a) {
   griddep_wait();
-  const uint64_t c = (uint64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const uint64_t c = ((uint64_t)blockIdx.x * blockDim.x + threadIdx.x) * V;
   if (c >= a.dim) return;
-  float gw = 0.f, gb = 0.f;
+  float gw[V], gb[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) gw[i] = gb[i] = 0.f;
+#pragma unroll 4
   for (uint64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
-    const float g = to_f32(static_cast<const T*>(a.dy)[(int64_t)r * a.dy_stride + c]);
-    const float v = to_f32(static_cast<const T*>(a.x)[(int64_t)r * a.x_stride + c]);
-    gw += g * ((v - a.mean[r]) * a.rstd[r]);
-    gb += g;
+    float f[V], d[V];
+    load_floats<T, V>(static_cast<const T*>(a.dy) + (int64_t)r * a.dy_stride, c, d);
+    load_floats<T, V>(static_cast<const T*>(a.x) + (int64_t)r * a.x_stride, c, f);
+    const float mean = a.mean[r], rstd = a.rstd[r];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      gw[i] += d[i] * ((f[i] - mean) * rstd);
+      gb[i] += d[i];
+    }
   }
-  a.part_w[(uint64_t)blockIdx.y * a.dim + c] = gw;
-  a.part_b[(uint64_t)blockIdx.y * a.dim + c] = gb;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a.part_w[(uint64_t)blockIdx.y * a.dim + c + i] = gw[i];
+    a.part_b[(uint64_t)blockIdx.y * a.dim + c + i] = gb[i];
+  }
 }
 
 // out[c] (+)= sum of the `parts` partial sums of column c: 32 columns per block,
@@ -771,7 +838,10 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
       return launch_forward<T, T, 2, 8, false, 256, 3>(a, threads, 256, 3, s);
     return launch_forward<T, T, 2, 8, false, 512, 1>(a, threads, threads, 2, s);
   }
-  launch_pdl(norm_forward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
+  const bool wide = a.dim % V == 0 && a.x_stride % V == 0 && a.y_stride % V == 0 &&
+                    aligned_to(a.x, 16) && aligned_to(a.y, 16);
+  if (wide) launch_pdl(norm_forward_long_kernel<T, V>, (unsigned)a.rows, 1024, 0, s, a);
+  else launch_pdl(norm_forward_long_kernel<T, 1>, (unsigned)a.rows, 1024, 0, s, a);
   return true;
 }
 
@@ -831,10 +901,15 @@ bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
   const bool small = h.block <= 256;
   bool ok = true;
   if (longer) {
-    launch_pdl(norm_backward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
-    if (sums)
-      launch_pdl(norm_columns_kernel<T>, dim3((unsigned)((a.dim + 255) / 256), h.parts), 256, 0, s,
-                 a);
+    // the column sums first: dx may be written over x or dy
+    const unsigned across = (unsigned)((a.dim + 128 * V - 1) / (128 * V));
+    if (sums && vec)
+      launch_pdl(norm_columns_kernel<T, V>, dim3(across, h.parts), 128, 0, s, a);
+    else if (sums)
+      launch_pdl(norm_columns_kernel<T, 1>, dim3((unsigned)((a.dim + 127) / 128), h.parts), 128, 0,
+                 s, a);
+    if (vec) launch_pdl(norm_backward_long_kernel<T, V>, (unsigned)a.rows, 1024, 0, s, a);
+    else launch_pdl(norm_backward_long_kernel<T, 1>, (unsigned)a.rows, 1024, 0, s, a);
   } else if (packs && same) {
     ok = small ? launch_backward<T, T, V, 256, kFit>(a, h, s)
                : launch_backward<T, T, V, 512, 1>(a, h, s);
