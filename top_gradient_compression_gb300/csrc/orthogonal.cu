@@ -50,6 +50,8 @@ struct GatherArgs {
   float mu;
   int32_t nesterov;
   int32_t vec_g, vec_m;  // rows of g, of mom: four elements are one aligned access
+  int32_t flat;          // the rows of a matrix follow one another in both
+  int32_t vec_flat_g, vec_flat_m;  // and four elements of that one row are such an access
   uint64_t m, n;
   uint32_t blocks;  // per matrix
   float* sums;      // [batch][blocks][3]
@@ -97,34 +99,67 @@ __device__ __forceinline__ void load4(const void* p, int32_t type, uint64_t at, 
   }
 }
 
-// Rows are walked in pieces of 512 columns, a warp at a time, each lane with four
-// groups of four: 64 or 128 bytes per lane in flight.
+// A matrix is walked in pieces, a warp at a time, each lane with four groups of four columns:
+// 64 or 128 bytes per lane in flight. A piece is 512 columns of a row, or several whole rows of
+// at most 256 columns.
 constexpr uint32_t kPiece = 512;
+
+struct Pieces {
+  uint32_t groups;  // of four columns, in a row
+  uint32_t rows;    // in a piece, if there are several; else 1
+  uint64_t across, total;  // pieces in a row (of one row each), in a matrix
+
+  __host__ __device__ Pieces(uint64_t m, uint64_t n) {
+    const uint64_t all = (n + 3) / 4;
+    groups = all > 64 ? 0 : (uint32_t)all;
+    rows = groups ? 128 / groups : 1;
+    across = groups ? 1 : (n + kPiece - 1) / kPiece;
+    total = groups ? (m + rows - 1) / rows : m * across;
+  }
+};
+// Lane's group q of a piece: its row within the piece, and its first column.
+struct Slots {
+  uint32_t row[4], col[4];
+  __device__ __forceinline__ explicit Slots(const Pieces& p) {
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q) {
+      const uint32_t at = 32 * q + lane_id();
+      row[q] = p.groups ? at / p.groups : 0;
+      col[q] = 4 * (p.groups ? at - row[q] * p.groups : at);
+    }
+  }
+};
 
 // M <- mu M + G where there is a momentum, and the partial sums of squares of U.
 __global__ void __launch_bounds__(256) gather_norm_kernel(const GatherArgs a) {
   griddep_wait();
   __shared__ float warp_sums[8][3];
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x < 3) a.turns[threadIdx.x * kTurnStep] = 0;
-  const uint64_t b = blockIdx.y, pieces = (a.n + kPiece - 1) / kPiece, total = a.m * pieces;
+  const uint64_t b = blockIdx.y;
+  // where rows follow one another they are one long row here
+  const uint64_t m = a.flat ? 1 : a.m, n = a.flat ? a.m * a.n : a.n;
+  const bool vec_g = a.flat ? a.vec_flat_g : a.vec_g, vec_m = a.flat ? a.vec_flat_m : a.vec_m;
+  const Pieces pieces(m, n);
+  const Slots slots(pieces);
   const uint64_t warps = (uint64_t)a.blocks * 8, id = blockIdx.x * 8ull + (threadIdx.x >> 5);
-  const uint64_t end = total * (id + 1) / warps;
-  uint64_t u = total * id / warps, r = u / pieces, piece = u - r * pieces;
+  const uint64_t end = pieces.total * (id + 1) / warps;
+  uint64_t u = pieces.total * id / warps;
+  uint64_t r0 = u / pieces.across * pieces.rows, piece = u % pieces.across;
   float s[3] = {0.f, 0.f, 0.f};
   for (; u < end; ++u) {
-    const uint64_t c0 = piece * kPiece + lane_id() * 4;
-    const uint64_t at = b * a.g_batch + r * a.g_stride;
     float v[4][4], mo[4][4];
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-      const uint64_t c = c0 + 128 * q;
-      load4(a.g, a.g_type, at + c, c, a.n, a.vec_g, v[q]);
+      const uint64_t r = r0 + slots.row[q], c = piece * kPiece + slots.col[q];
+      const uint64_t in = slots.row[q] < pieces.rows && r < m ? n : 0;  // no columns, if no row
+      load4(a.g, a.g_type, b * a.g_batch + r * a.g_stride + c, c, in, vec_g, v[q]);
       if (a.mom)
-        load4(a.mom, SPARCML_F32, b * a.m_batch + r * a.m_stride + c, c, a.n, a.vec_m, mo[q]);
+        load4(a.mom, SPARCML_F32, b * a.m_batch + r * a.m_stride + c, c, in, vec_m, mo[q]);
     }
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-      const uint64_t c = c0 + 128 * q;
+      const uint64_t r = r0 + slots.row[q], c = piece * kPiece + slots.col[q];
+      const uint64_t in = slots.row[q] < pieces.rows && r < m ? n : 0;
       if (a.mom) {
         float* mp = a.mom + b * a.m_batch + r * a.m_stride + c;
 #pragma unroll
@@ -133,20 +168,20 @@ __global__ void __launch_bounds__(256) gather_norm_kernel(const GatherArgs a) {
           mo[q][i] = t;
           v[q][i] = a.nesterov ? v[q][i] + a.mu * t : t;
         }
-        if (a.vec_m && c + 4 <= a.n) {
+        if (vec_m && c + 4 <= in) {
           *reinterpret_cast<float4*>(mp) = make_float4(mo[q][0], mo[q][1], mo[q][2], mo[q][3]);
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (c + i < a.n) mp[i] = mo[q][i];
+            if (c + i < in) mp[i] = mo[q][i];
         }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) add_square(v[q][i], s);
     }
-    if (++piece == pieces) {
+    if (++piece == pieces.across) {
       piece = 0;
-      ++r;
+      r0 += pieces.rows;
     }
   }
 #pragma unroll
@@ -570,15 +605,16 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
     if (item >= w.clusters) t = tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t row0 = t.row0 + 128 * w.rank + 32 * quarter, row = row0 + lane;
-    const uint32_t chunks = t.n / 64, tile_col = half * chunks * 32, col0 = t.col0 + tile_col;
+    // the 32-column chunks of a tile alternate between the two warps of its rows
+    const uint32_t tile_col = half * 32, col0 = t.col0 + tile_col;
     uint32_t count = 0;  // of this warp's chunks, those that exist
-    if (row0 < p.rows && col0 < p.cols) count = min(chunks, (p.cols - col0 + 31) / 32);
+    if (row0 < p.rows && col0 < p.cols) count = min(t.n / 64, (p.cols - col0 + 63) / 64);
     const uint32_t turn0 = w.turn;
     auto fetch = [&](uint32_t q) {  // what is added to chunk q
       if (lane == 0) {
         const uint32_t slot = kind == kLast ? 0 : (turn0 + q) & 1u;
         const uint32_t dst = w.buf + slot * kStageBuf, bar = w.in_bar + 8 * slot;
-        const uint32_t c = col0 + 32 * q;
+        const uint32_t c = col0 + 64 * q;
         proxy_fence_shared();  // the buffer's last ordinary accesses come first
         mbar_expect_tx(bar, pairs ? 4096 : 2048);
         tma_load_3d(dst, pairs ? &m.x_out[step & 1] : &m.s_out, c, row0, t.b, bar);
@@ -618,7 +654,7 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
       u.rows = p.rows;
     }
     auto column_diag = [&](uint32_t q) {
-      const uint32_t c = col0 + 32 * q + lane;
+      const uint32_t c = col0 + 64 * q + lane;
       return columns && q < count && c < p.cols ? __ldcg(columns + c) : 0.f;
     };
     float other = column_diag(0);
@@ -627,10 +663,10 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
     if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)) return false;
     tmem_fence_after();
     const uint32_t src = w.tmem + acc * kAccColumns + (quarter << 21) + tile_col;
-    if (kind == kPart) count = chunks;
+    if (kind == kPart) count = t.n / 64;
 #pragma unroll 1
     for (uint32_t q = 0; q < count; ++q) {
-      const uint32_t col = col0 + 32 * q;
+      const uint32_t col = col0 + 64 * q;
       const uint32_t slot = kind == kLast ? 0 : w.turn & 1u;
       const uint32_t buf = w.buf + slot * kStageBuf, turned = w.buf + kStageBuf;
       if (reads && kind != kLast && q + 1 < count) fetch(q + 1);
@@ -644,12 +680,12 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
 #pragma unroll 1
       for (uint32_t h = 0; h < 2; ++h) {
         float v[16];
-        tmem_load16(src + 32 * q + 16 * h, v);
+        tmem_load16(src + 64 * q + 16 * h, v);
         tmem_load_wait(v);
         if (kind == kPart) {
           float* o = a.part +
-                     ((uint64_t)((p.part0 + item) * CG + w.rank) * p.n + tile_col + 32 * q + 16 * h) * 128 +
-                     quarter * 32 + lane;
+                     ((uint64_t)((p.part0 + item) * CG + w.rank) * p.n + tile_col + 64 * q +
+                      16 * h) * 128 + quarter * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i * 128] = v[i];
           continue;
@@ -704,7 +740,7 @@ __device__ void join_parts(const StepArgs& a, Product p) {
     const uint64_t step = (uint64_t)CG * p.n * 128;
     const float* o = a.part + ((uint64_t)((p.part0 + tile * p.splits) * CG + r / 4) * p.n + 8 * q) * 128 +
                      (r & 3u) * 32 + lane;
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t s = 0; s < p.splits; ++s, o += step) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] += __ldcg(o + i * 128);
@@ -762,32 +798,35 @@ __device__ __forceinline__ void norm_factors(const GatherArgs& g, uint64_t b, fl
 // The scaled input as a pair of fp16.
 __device__ void split_input(const StepArgs& a) {
   const GatherArgs& g = a.g;
-  const uint64_t pieces = (g.n + kPiece - 1) / kPiece, total = (uint64_t)a.batch * g.m * pieces;
+  const Pieces pieces(g.m, g.n);
+  const Slots slots(pieces);
+  const uint64_t total = a.batch * pieces.total;
   const uint64_t warps = (uint64_t)gridDim.x * (kThreads / 32);
   const uint64_t id = (uint64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   // each warp takes a run of pieces, which lies in few matrices
   const uint64_t end = total * (id + 1) / warps;
-  uint64_t u = total * id / warps, line = u / pieces, piece = u - line * pieces;
-  uint64_t b = line / g.m, r = line - b * g.m;
+  uint64_t u = total * id / warps, b = u / pieces.total, rest = u - b * pieces.total;
+  uint64_t r0 = rest / pieces.across * pieces.rows, piece = rest % pieces.across;
   bool known = false;
   float f0 = 0.f, f1 = 0.f;
 #pragma unroll 2
   for (; u < end; ++u) {
     if (!known) norm_factors(g, b, f0, f1);
     known = true;
-    const uint64_t c0 = piece * kPiece + lane_id() * 4, at = line * a.pitch;
     float v[4][4], mo[4][4];
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-      const uint64_t c = c0 + 128 * q;
-      load4(g.g, g.g_type, b * g.g_batch + r * g.g_stride + c, c, g.n, g.vec_g, v[q]);
+      const uint64_t r = r0 + slots.row[q], c = piece * kPiece + slots.col[q];
+      const uint64_t in = slots.row[q] < pieces.rows && r < g.m ? g.n : 0;
+      load4(g.g, g.g_type, b * g.g_batch + r * g.g_stride + c, c, in, g.vec_g, v[q]);
       if (g.mom)
-        load4(g.mom, SPARCML_F32, b * g.m_batch + r * g.m_stride + c, c, g.n, g.vec_m, mo[q]);
+        load4(g.mom, SPARCML_F32, b * g.m_batch + r * g.m_stride + c, c, in, g.vec_m, mo[q]);
     }
 #pragma unroll
     for (uint32_t q = 0; q < 4; ++q) {
-      const uint64_t c = c0 + 128 * q;
-      if (c >= g.n) continue;  // the row's padding takes what is left of the last four
+      const uint64_t r = r0 + slots.row[q], c = piece * kPiece + slots.col[q];
+      // the row's padding takes what is left of the last four
+      if (slots.row[q] >= pieces.rows || r >= g.m || c >= g.n) continue;
       uint32_t hw[2], lw[2];
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
@@ -802,14 +841,15 @@ __device__ void split_input(const StepArgs& a) {
         const float2 back = unpack_half(hw[i / 2]);
         lw[i / 2] = pack_half(x[0] - back.x, x[1] - back.y);
       }
-      *reinterpret_cast<uint2*>(a.hi[0] + at + c) = make_uint2(hw[0], hw[1]);
-      *reinterpret_cast<uint2*>(a.lo + at + c) = make_uint2(lw[0], lw[1]);
+      const uint64_t at = (b * g.m + r) * a.pitch + c;
+      *reinterpret_cast<uint2*>(a.hi[0] + at) = make_uint2(hw[0], hw[1]);
+      *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(lw[0], lw[1]);
     }
-    if (++piece == pieces) {
+    if (++piece == pieces.across) {
       piece = 0;
-      ++line;
-      if (++r == g.m) {
-        r = 0;
+      r0 += pieces.rows;
+      if (r0 >= g.m) {
+        r0 = 0;
         ++b;
         known = false;
       }
@@ -1131,7 +1171,8 @@ Product shape_product(uint64_t batch, uint64_t rows, uint64_t cols, uint64_t dep
   p.items = items > 0x7fffffffull ? 0 : (uint32_t)items;
   const double busy = std::min(1.0, (double)items / (double)workers);
   const double each = std::max(n / 64.0, (128 + n / pair) / 58.0 * busy);
-  const double product = (double)ceil_div(p.blocks, p.splits) * each, write = n / 4.0;
+  const double product = (double)ceil_div(p.blocks, p.splits) * each;
+  const double write = 6 + std::min<uint64_t>(n, align_up(cols, 64)) / 4.0;
   const double rounds = (double)ceil_div(p.whole, workers) + (halves && left ? 0.5 : 0.0);
   *time = product + (rounds - 1) * std::max(product, write) + write;
   if (p.splits > 1)  // a turn of the grid, and the partial tiles' way to L2 and back
@@ -1168,7 +1209,7 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   q.l = std::max(m, n);
   q.pitch = align_up(n, 64);
   q.kpitch = align_up(q.k, 64);
-  q.blocks = (uint32_t)std::min<uint64_t>(ceil_div(m * ceil_div(n, kPiece), 8), kSms * 3);
+  q.blocks = (uint32_t)std::min<uint64_t>(ceil_div(m * n, 8 * kPiece), kSms * 2);
   double best = 0;
   uint32_t width[3] = {0, 0, 0};
   for (uint32_t pair = 1; pair <= 2; ++pair) {
@@ -1277,6 +1318,11 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   const int64_t ge = g.g_type == SPARCML_F32 ? 16 : 8;
   g.vec_g = aligned_to(g.g, ge) && g.g_batch % 4 == 0 && g.g_stride % 4 == 0;
   g.vec_m = aligned_to(g.mom, 16) && g.m_batch % 4 == 0 && g.m_stride % 4 == 0;
+  g.flat = g.g_stride == (int64_t)q.n && (!g.mom || g.m_stride == (int64_t)q.n);
+  if (g.flat) {  // then only a matrix's start has to be aligned
+    g.vec_flat_g = aligned_to(g.g, ge) && g.g_batch % 4 == 0;
+    g.vec_flat_m = aligned_to(g.mom, 16) && g.m_batch % 4 == 0;
+  }
   g.m = q.m;
   g.n = q.n;
   g.blocks = q.blocks;
