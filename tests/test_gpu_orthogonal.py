@@ -60,6 +60,44 @@ def check(out, ref):
     assert worst <= (0.04 if k >= 32 else 0.3), float(worst)
 
 
+def check_small(out, ref, noise):
+    """A side of at most 64: X is read in three products of its halves and the steps are
+    fp32, so what is left beside the output's rounding is fp32's own in S, 2^-24, times
+    what the steps multiply a small singular value by."""
+    out, ref = out.double(), ref.double()
+    assert (out - ref).norm() <= noise * ref.norm()
+
+
+@pytest.mark.parametrize("power", [0.0, 0.5, 2.0, 4.0])
+@pytest.mark.parametrize("m,n", [(16, 16), (17, 900), (33, 64), (64, 64), (64, 5000), (4100, 48),
+                                 (20_000, 63)])
+def test_small_sides(m, n, power):
+    """An update in fp32, so that the result's error can be seen: 1e-3 of it at most (the
+    simulated roundings give up to 8e-4, for the 1/i^4 spectrum)."""
+    gen = torch.Generator(device=DEV).manual_seed(m + n)
+    k = min(m, n)
+    u, _ = torch.linalg.qr(torch.randn(m, k, generator=gen, device=DEV))
+    v, _ = torch.linalg.qr(torch.randn(n, k, generator=gen, device=DEV))
+    g = (u * torch.arange(1, k + 1, device=DEV).float().pow(-power)) @ v.t()
+    for coeffs, noise in ((COEFFS, 2e-3), (FITTED, 3e-2), (((1.5, -0.5, 0.0),) * 12, 2e-3)):
+        w, mom = torch.zeros(m, n, device=DEV), torch.zeros(m, n, device=DEV)
+        ws = api.workspace(api.orthogonalize_workspace_size(1, m, n), DEV)
+        api.muon_step(w, g, mom, lr=1.0, mu=0.0, scale=1.0, coeffs=coeffs, ws=ws)
+        assert api.get_status(ws) == 0
+        check_small(-w, reference(g, coeffs), noise)
+
+
+def test_many_small_matrices():
+    """More matrices than blocks, both chains, tall and wide."""
+    for m, n in ((24, 40), (70, 33), (64, 64)):
+        g = gradient((333, m, n), m)
+        out = api.orthogonalize(g, out_dtype=torch.float16)
+        ref = reference(g)
+        rel = (out.double() - ref).flatten(1).norm(dim=1) / ref.flatten(1).norm(dim=1)
+        assert float(rel.max()) <= 1e-3  # fp16's own rounding: 2^-11 / sqrt(3) / 1.4
+        assert torch.equal(out[200], api.orthogonalize(g[200], out_dtype=torch.float16))
+
+
 SHAPES = [(1, 1), (1, 7), (7, 1), (2, 3), (16, 16), (64, 64), (65, 63), (128, 128), (129, 127),
           (100, 1000), (1000, 100), (1, 5000), (257, 384), (333, 1000), (1000, 333), (512, 512),
           (640, 200), (1023, 1025), (40, 20_001)]

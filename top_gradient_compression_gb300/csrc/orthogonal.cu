@@ -28,7 +28,17 @@
 //     that diagonal was most of the error (0.15 to 0.2 % on flat spectra, 0.03 to
 //     0.07 % so).
 
+// A side of at most 64 needs no step of its own products. With S kept in fp32 all steps are
+// polynomials of it, X <- q(S) X with
+//     P = a + b S + c S S,  q <- P q,  S <- P S P,
+// which one block works out in shared memory; X is read for S and for q(S) X alone, in
+// products of all three leading pairs of the halves hi and lo. Three products in a row
+// in place of fifteen, and exact to 1e-3 even on a 1/i^4 spectrum. S loses its sign where it
+// is small against its own rounding, so this is left to coefficients that multiply small
+// singular values 1800 times at most.
+
 #include <algorithm>
+#include <cmath>
 
 #include "tensor.cuh"
 #include "types.cuh"
@@ -36,7 +46,8 @@
 namespace sparcml {
 namespace {
 
-constexpr float kScaleX = 4096.f, kScaleS = 4096.f, kScaleP = 2048.f;
+constexpr float kScaleX = 4096.f, kScaleS = 4096.f, kScaleP = 2048.f, kScaleQ = 32.f;
+constexpr uint32_t kSmall = 64;  // the smaller side that one block takes
 
 // ---------------------------------------------------------------------------
 // Momentum, norm and split of the input.
@@ -223,6 +234,7 @@ struct Maps {
   // swizzled: [0] the first operand, [1] the second. With a load per 64 x 64 the issue of
   // loads, over 100 cycles each, was what bounded the products.
   CUtensorMap x_gram[2][2], s_poly[2], x_apply[2], p_apply;
+  CUtensorMap lo_gram[2], lo_apply, q_lo;  // for a small side: the lower halves
 };
 
 struct StepArgs {
@@ -247,7 +259,7 @@ struct StepArgs {
   int32_t* status;
 };
 
-enum Kind { kGram, kPart, kJoin, kPoly, kApply, kLast };
+enum Kind { kGram, kPart, kJoin, kSolve, kPoly, kApply, kLast };
 
 constexpr uint32_t kWriters = 8;  // warps that write results; then a loader and an issuer
 constexpr uint32_t kThreads = 32 * (kWriters + 2);
@@ -371,32 +383,42 @@ struct Worker {
 // The loader and the issuer run as whole warps, of which one lane issues: so the addresses
 // and the control flow are known to be uniform (a lane on its own took 700 cycles per
 // block of the summed axis, where the products take 512).
-template <int CG>
-__device__ __forceinline__ bool load_operands(Worker<CG>& w, const Product& p, const CUtensorMap* ma,
-                              const CUtensorMap* mb, bool a_mn, bool b_mn, Tile t) {
+template <int CG, bool SMALL>
+__device__ __forceinline__ bool load_operands(Worker<CG>& w, const Product& p,
+                                              const CUtensorMap* ma, const CUtensorMap* mb,
+                                              const CUtensorMap* ma_lo, const CUtensorMap* mb_lo,
+                                              bool a_mn, bool b_mn, Tile t) {
   for (uint32_t item = w.first_item(p); item < p.items; item += w.clusters) {
     if (item >= w.clusters) t = tile_of<CG>(p, item);
     if (t.none) continue;
     const uint32_t bytes = 128 * 128 + p.n / CG * 128;  // halves of tiles use half of theirs
     const uint32_t ra = t.row0 + 128 * w.rank, rb = t.col0 + t.n / CG * w.rank;
-    for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
+    uint32_t rep = 0;
+    for (uint32_t i = t.first; i < t.last; w.next_stage()) {
       const uint32_t s = w.stage;
       if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return false;
+      // of a small side's operands hi hi, hi lo, lo hi; else hi hi alone
+      const CUtensorMap* const ua = SMALL && rep == 2 ? ma_lo : ma;
+      const CUtensorMap* const ub = SMALL && rep == 1 ? mb_lo : mb;
       if (w.leader) {
         if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, CG * bytes);
         const uint32_t bar = w.lead_full + 8 * s, k = i * 64;
         const uint32_t dst = w.ring + s * w.stage_bytes;
-        tma_load_4d<CG>(dst, ma, a_mn ? 0 : k, a_mn ? k : ra, a_mn ? ra / 64 : 0, t.b, bar);
-        tma_load_4d<CG>(dst + 128 * 128, mb, b_mn ? 0 : k, b_mn ? k : rb, b_mn ? rb / 64 : 0, t.b,
+        tma_load_4d<CG>(dst, ua, a_mn ? 0 : k, a_mn ? k : ra, a_mn ? ra / 64 : 0, t.b, bar);
+        tma_load_4d<CG>(dst + 128 * 128, ub, b_mn ? 0 : k, b_mn ? k : rb, b_mn ? rb / 64 : 0, t.b,
                         bar);
       }
       __syncwarp();
+      if (!SMALL || ++rep == 3) {
+        rep = 0;
+        ++i;
+      }
     }
   }
   return true;
 }
 
-template <int CG>
+template <int CG, bool SMALL>
 __device__ __forceinline__ bool issue_products(Worker<CG>& w, const Product& p, bool a_mn, bool b_mn, Tile t) {
   const uint32_t step_a = a_mn ? 2048 : 32, step_b = b_mn ? 2048 : 32;
   for (uint32_t item = w.first_item(p); item < p.items; item += w.clusters) {
@@ -407,7 +429,8 @@ __device__ __forceinline__ bool issue_products(Worker<CG>& w, const Product& p, 
     if (!mbar_wait_warp(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return false;
     tmem_fence_after();
     const uint32_t d = w.tmem + a * kAccColumns;
-    for (uint32_t i = t.first; i < t.last; ++i, w.next_stage()) {
+    const uint32_t blocks = (t.last - t.first) * (SMALL ? 3 : 1);
+    for (uint32_t i = 0; i < blocks; ++i, w.next_stage()) {
       const uint32_t s = w.stage;
       if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.gave_up)) return false;
       tmem_fence_after();
@@ -416,7 +439,7 @@ __device__ __forceinline__ bool issue_products(Worker<CG>& w, const Product& p, 
 #pragma unroll
         for (uint32_t k = 0; k < 4; ++k)
           mma_f16<CG>(d, tile_desc(sa + k * step_a, 8192, 1024),
-                      tile_desc(sb + k * step_b, 8192, 1024), idesc, i > t.first || k > 0);
+                      tile_desc(sb + k * step_b, 8192, 1024), idesc, i > 0 || k > 0);
         mma_commit<CG>(w.empty + 8 * s);
       }
       __syncwarp();
@@ -594,7 +617,7 @@ __device__ __forceinline__ void store_result(const StepArgs& a, uint32_t box, ui
   __syncwarp();
 }
 
-template <int CG>
+template <int CG, bool SMALL>
 __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p,
                               int kind, uint32_t step, Tile t) {
   const uint32_t warp = threadIdx.x >> 5, lane = lane_id();
@@ -638,8 +661,8 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
     } else if (pairs) {
       const float* d = a.diag_p + (uint64_t)t.b * a.k;
       columns = a.tall ? d : nullptr;
-      u.f = 1.f / kScaleP;
-      u.r0 = ca + (!a.tall && row < p.rows ? __ldcg(d + row) : 0.f);
+      u.f = SMALL ? 1.f / kScaleQ : 1.f / kScaleP;
+      u.r0 = (SMALL ? 0.f : ca) + (!a.tall && row < p.rows ? __ldcg(d + row) : 0.f);
       u.r1 = a.tall ? 1.f : 0.f;
       if (kind == kLast) {
         const float g = a.alpha / kScaleX;
@@ -683,11 +706,14 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
         tmem_load16(src + 64 * q + 16 * h, v);
         tmem_load_wait(v);
         if (kind == kPart) {
+          // columns of 128 rows, or of the 64 that a small side has
+          const uint32_t high = SMALL ? kSmall : 128;
           float* o = a.part +
                      ((uint64_t)((p.part0 + item) * CG + w.rank) * p.n + tile_col + 64 * q +
-                      16 * h) * 128 + quarter * 32 + lane;
+                      16 * h) * high + quarter * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i * 128] = v[i];
+          for (int i = 0; i < 16; ++i)
+            if (quarter * 32 < high) o[i * high] = v[i];
           continue;
         }
         finish16(v, h, buf, reads, pairs, columns != nullptr, other, u, on_diag, row);
@@ -770,6 +796,194 @@ __device__ void join_parts(const StepArgs& a, Product p) {
       }
     }
   }
+}
+
+// M consecutive floats of shared memory.
+template <int M>
+__device__ __forceinline__ void lds_floats(uint32_t a, float (&x)[M]) {
+  if constexpr (M == 4)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                 : "r"(a)
+                 : "memory");
+  else if constexpr (M == 2)
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(x[1]) : "r"(a) : "memory");
+  else
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x[0]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void writers_sync() {
+  asm volatile("bar.sync 1, 256;" ::: "memory");
+}
+
+// A B[0], ..., A B[N - 1] of symmetric matrices in shared memory, k <= 64 rows of 64 floats, zeros
+// beyond; f(n, e, i, j, value) takes a thread's entries e. A warp has R rows, a lane C
+// columns of them, 32 apart: A's R entries of a row are the same for all lanes, B's are
+// consecutive, so that each load is one access of shared memory (with tiles of 4 x 4 or
+// 4 x 8 entries, 16 bytes per lane, loads bound it: 5,200 cycles for a product of 64).
+template <int R, int C, int N, typename F>
+__device__ __forceinline__ void small_products(uint32_t a, const uint32_t (&b)[N], uint32_t k, F f) {
+  constexpr int ROWS = R == 8 ? 2 : 4;
+  const uint32_t i0 = (threadIdx.x >> 5) * R, lane = lane_id();
+  if (i0 < k) {
+    float v[N][R][C];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+      for (int e = 0; e < R * C; ++e) v[n][e / C][e % C] = 0.f;
+    }
+#pragma unroll 2
+    for (uint32_t r = 0; r < k; r += ROWS) {
+      float x[ROWS][R], y[ROWS][N][C];
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+        const uint32_t at = a + ((r + u) * kSmall + i0) * 4;
+        if constexpr (R == 8) {
+          float lo[4], hi[4];
+          lds_floats<4>(at, lo);
+          lds_floats<4>(at + 16, hi);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[u][i] = lo[i];
+            x[u][4 + i] = hi[i];
+          }
+        } else {
+          lds_floats<R>(at, x[u]);
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            float one[1];
+            lds_floats<1>(b[n] + ((r + u) * kSmall + lane + 32 * c) * 4, one);
+            y[u][n][c] = one[0];
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < ROWS; ++u) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+          for (int e = 0; e < R * C; ++e) v[n][e / C][e % C] += x[u][e / C] * y[u][n][e % C];
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+#pragma unroll
+      for (int e = 0; e < R * C; ++e) f(n, e, i0 + e / C, lane + 32 * (e % C), v[n][e / C][e % C]);
+    }
+  }
+  writers_sync();
+}
+
+// q(S) of one matrix, by its block's writers: S from the partial tiles in the order of the
+// splits, in fp32 as all that follows; then q's diagonal and the two halves of the rest.
+// `room`: four matrices of 64 x 64 floats.
+template <int R, int C>
+__device__ __noinline__ void solve_one(const StepArgs& a, uint32_t splits, uint32_t b,
+                                       uint32_t tile, float* room) {
+  constexpr uint32_t kCount = kSmall * kSmall;
+  const uint32_t k = a.k;
+  // the room is the writers' buffers: each has to be done with its own
+  writers_sync();
+  float *s = room, *pm = s + kCount, *q = pm + kCount, *t = q + kCount;
+  {
+    const float4* o = reinterpret_cast<const float4*>(a.part + (uint64_t)tile * kCount);
+    float4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (uint32_t c = 0; c < splits; ++c, o += kCount / 4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4 x = __ldcg(o + u * 256 + threadIdx.x);
+        v[u].x += x.x;
+        v[u].y += x.y;
+        v[u].z += x.z;
+        v[u].w += x.w;
+      }
+    }
+    const float f = 1.f / (kScaleX * kScaleX);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t e = 4 * (u * 256 + threadIdx.x), i = e / kSmall, j = e % kSmall;
+      // beyond the matrix the operands hold whatever its padding does
+      const bool row = i < k;
+      reinterpret_cast<float4*>(s)[e / 4] =
+          make_float4(row && j < k ? v[u].x * f : 0.f, row && j + 1 < k ? v[u].y * f : 0.f,
+                      row && j + 2 < k ? v[u].z * f : 0.f, row && j + 3 < k ? v[u].w * f : 0.f);
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      reinterpret_cast<float4*>(pm)[e / 4] = zero;
+      reinterpret_cast<float4*>(q)[e / 4] = zero;
+      reinterpret_cast<float4*>(t)[e / 4] = zero;
+    }
+  }
+  writers_sync();
+  for (uint32_t step = 0; step < a.steps; ++step) {
+    const float ca = a.coeffs[3 * step], cb = a.coeffs[3 * step + 1], cc = a.coeffs[3 * step + 2];
+    const bool last = step + 1 == a.steps;
+    float* const to = step == 0 ? q : pm;
+    {
+      const uint32_t other[1] = {smem_addr(s)};
+      small_products<R, C, 1>(smem_addr(s), other, k, [&](int, int, uint32_t i, uint32_t j, float v) {
+        const float x = (i == j && i < k ? ca : 0.f) + cb * s[i * kSmall + j] + cc * v;
+        to[i * kSmall + j] = x;
+      });
+    }
+    if (step == 0) {  // q = P
+      if (last) break;
+      const uint32_t other[1] = {smem_addr(s)};
+      small_products<R, C, 1>(smem_addr(q), other, k, [&](int, int, uint32_t i, uint32_t j, float v) {
+        t[i * kSmall + j] = v;
+      });
+      const uint32_t other2[1] = {smem_addr(q)};
+      small_products<R, C, 1>(smem_addr(t), other2, k, [&](int, int, uint32_t i, uint32_t j, float v) {
+        s[i * kSmall + j] = v;
+      });
+      continue;
+    }
+    if (last) {
+      const uint32_t other[1] = {smem_addr(q)};
+      small_products<R, C, 1>(smem_addr(pm), other, k, [&](int, int, uint32_t i, uint32_t j, float v) {
+        t[i * kSmall + j] = v;
+      });
+      q = t;
+      break;
+    }
+    // P q and P S in one pass; the second's entries wait in registers until S has been read
+    float keep[R * C];
+    const uint32_t both[2] = {smem_addr(q), smem_addr(s)};
+    small_products<R, C, 2>(smem_addr(pm), both, k, [&](int n, int e, uint32_t i, uint32_t j, float v) {
+      if (n == 0) t[i * kSmall + j] = v;
+      else keep[e] = v;
+    });
+    {
+      const uint32_t i0 = (threadIdx.x >> 5) * R;
+      if (i0 < k) {
+#pragma unroll
+        for (int e = 0; e < R * C; ++e)
+          q[(i0 + e / C) * kSmall + lane_id() + 32 * (e % C)] = keep[e];
+      }
+      writers_sync();
+    }
+    const uint32_t other[1] = {smem_addr(pm)};
+    small_products<R, C, 1>(smem_addr(q), other, k, [&](int, int, uint32_t i, uint32_t j, float v) {
+      s[i * kSmall + j] = v;
+    });
+    float* const now = t;
+    t = q;
+    q = now;
+  }
+  for (uint32_t e = threadIdx.x; e < k * kSmall; e += 32 * kWriters) {
+    const uint32_t i = e / kSmall, j = e % kSmall;
+    const float v = i == j ? 0.f : q[e] * kScaleQ;
+    if (i == j) a.diag_p[(uint64_t)b * k + i] = q[e];
+    const __half h = __float2half_rn(v);
+    a.p[((uint64_t)b * k) * kSmall + e] = h;  // k <= 64: the pitch is 64
+    a.s[((uint64_t)b * k) * kSmall + e] = __float2half_rn(v - __half2float(h));
+  }
+  writers_sync();
 }
 
 // 2^12 / |U| as two factors, each a normal number whatever the size of |U|.
@@ -884,21 +1098,22 @@ __device__ __forceinline__ void add_count(uint32_t* count) {
 // The order of work, the same for the loader, the issuer and the writers of every block:
 // step by step, product by product, chain by chain. f(step, kind, product, chain, count
 // of the chain's arrivals that the work has to wait for).
-template <int CG, typename F>
+template <int CG, bool SMALL, typename F>
 __device__ __forceinline__ void in_order(const StepArgs& a, F f) {
   uint32_t need[2] = {0, 0};
+  const uint32_t steps = SMALL ? 1 : a.steps;
 #pragma unroll 1
-  for (uint32_t step = 0; step < a.steps; ++step) {
+  for (uint32_t step = 0; step < steps; ++step) {
 #pragma unroll 1
     for (uint32_t ph = 0; ph < 4; ++ph) {
 #pragma unroll 1
       for (uint32_t chain = 0; chain < a.chains; ++chain) {
         const Product& p = a.product[chain][ph < 2 ? 0 : ph - 1];
-        if (ph == 1 && p.splits == 1) continue;  // nothing to join
-        const int kind = ph == 0   ? (p.splits > 1 ? kPart : kGram)
+        if (ph == 1 && (SMALL || p.splits == 1)) continue;  // nothing to join
+        const int kind = ph == 0   ? (SMALL || p.splits > 1 ? kPart : kGram)
                          : ph == 1 ? kJoin
-                         : ph == 2 ? kPoly
-                                   : (step + 1 == a.steps ? kLast : kApply);
+                         : ph == 2 ? (SMALL ? kSolve : kPoly)
+                                   : (step + 1 == steps ? kLast : kApply);
         const uint32_t blocks = kind == kJoin ? min(join_units<CG>(p), gridDim.x)
                                               : min(p.items, gridDim.x / CG) * CG;
         const uint32_t n = chain ? need[1] : need[0];
@@ -910,7 +1125,7 @@ __device__ __forceinline__ void in_order(const StepArgs& a, F f) {
   }
 }
 
-template <int CG>
+template <int CG, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1)
 steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a) {
   extern __shared__ uint8_t raw[];
@@ -983,11 +1198,11 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   // turn carry them.
   uint32_t told = 0;
   if (warp == kWriters) {
-    in_order<CG>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t need) {
+    in_order<CG, SMALL>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t need) {
       const uint32_t item = w.first_item(p);
       if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
       Tile t = {};
-      if (kind != kJoin) t = tile_of<CG>(p, item);
+      if (kind != kJoin && kind != kSolve) t = tile_of<CG>(p, item);
       pin(t);
       bool come = true;
       if (w.leader) {
@@ -996,7 +1211,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       }
       if (!__all_sync(0xffffffffu, come)) return false;
       ++told;
-      if (kind == kJoin) return true;
+      if (kind == kJoin || kind == kSolve) return true;
       const CUtensorMap *ma = &m.x_gram[step & 1][0], *mb = &m.x_gram[step & 1][1];
       if (kind == kPoly) {
         ma = &m.s_poly[0];
@@ -1005,28 +1220,46 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
         ma = tall ? &m.x_apply[step & 1] : &m.p_apply;
         mb = tall ? &m.p_apply : &m.x_apply[step & 1];
       }
-      return load_operands(w, p, ma, mb, a_major(kind), b_major(kind), t);
+      // the lower halves, where they take part
+      const CUtensorMap *ma_lo = &m.lo_gram[0], *mb_lo = &m.lo_gram[1];
+      if (kind == kLast) {
+        ma_lo = tall ? &m.lo_apply : &m.q_lo;
+        mb_lo = tall ? &m.q_lo : &m.lo_apply;
+      }
+      return load_operands<CG, SMALL>(w, p, ma, mb, ma_lo, mb_lo, a_major(kind), b_major(kind), t);
     });
   } else if (warp == kWriters + 1) {
     if (w.rank == 0)
-      in_order<CG>(a, [&](uint32_t, int kind, const Product& p, uint32_t, uint32_t) {
+      in_order<CG, SMALL>(a, [&](uint32_t, int kind, const Product& p, uint32_t, uint32_t) {
         const uint32_t item = w.first_item(p);
-        if (kind == kJoin || item >= p.items) return true;
+        if (kind == kJoin || kind == kSolve || item >= p.items) return true;
         Tile t = tile_of<CG>(p, item);
         pin(t);
-        return issue_products(w, p, a_major(kind), b_major(kind), t);
+        return issue_products<CG, SMALL>(w, p, a_major(kind), b_major(kind), t);
       });
   } else {
-    in_order<CG>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t) {
+    in_order<CG, SMALL>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t) {
       const uint32_t item = w.first_item(p);
       if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
       Tile t = {};
-      if (kind != kJoin) t = tile_of<CG>(p, item);
+      if (kind != kJoin && kind != kSolve) t = tile_of<CG>(p, item);
       pin(t);
       if (!mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &gave_up)) return false;
       ++told;
-      if (kind == kJoin) join_parts<CG>(a, p);
-      else if (!write_results(w, a, m, p, kind, step, t)) return false;
+      if (kind == kJoin) {
+        join_parts<CG>(a, p);
+      } else if (SMALL && kind == kSolve) {
+        float* room = reinterpret_cast<float*>(raw + (w.ring - smem_addr(raw)) + kRingBytes);
+        const Product& gram = a.product[chain][0];
+        for (uint32_t i = item; i < p.items; i += w.clusters) {
+          const uint32_t tile = gram.part0 + i * gram.splits;
+          if (a.k > 32) solve_one<8, 2>(a, gram.splits, p.b0 + i, tile, room);
+          else if (a.k > 16) solve_one<4, 1>(a, gram.splits, p.b0 + i, tile, room);
+          else solve_one<2, 1>(a, gram.splits, p.b0 + i, tile, room);
+        }
+      } else if (!write_results<CG, SMALL>(w, a, m, p, kind, step, t)) {
+        return false;
+      }
       if (kind == kLast) return true;
       // what was written is read by asynchronous copies; the last of the block's writers
       // reports to the grid
@@ -1136,6 +1369,7 @@ struct Plan {
   uint32_t pair;    // blocks that share a tile: 1 or 2
   uint32_t chains;
   Product product[2][3];
+  Product small[2][3];  // for a small side
   size_t sums, hi0, hi1, lo, s, p, ds, dp, part, bytes;
 };
 
@@ -1246,6 +1480,31 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
       }
     }
   }
+  size_t small_parts = 0;
+  if (q.k <= kSmall) {
+    // S in few parts, which one block adds up; then a block per matrix; then q(S) X
+    const uint64_t blocks = ceil_div(q.l, 64);
+    const uint32_t splits = (uint32_t)std::max<uint64_t>(
+        1, std::min({(uint64_t)16, blocks / 4, kSms / std::max<uint64_t>(1, q.batch)}));
+    for (uint32_t c = 0; c < q.chains; ++c) {
+      const uint64_t some = q.chains == 1 ? batch : c ? batch / 2 : (batch + 1) / 2;
+      double t;
+      for (int i = 0; i < 3; ++i) {
+        Product& p = q.small[c][i];
+        p = shape_product(some, i < 2 ? q.k : m, i < 2 ? q.k : n, i == 0 ? q.l : q.k, i < 2, 1,
+                          i < 2 ? 64 : 128, false, batch, &t);
+        p.b0 = q.product[c][i].b0;
+        if (i == 0) {
+          p.splits = splits;
+          p.tiles = 1;
+          p.part0 = (uint32_t)small_parts;
+          small_parts += some * splits;
+        }
+        if (i < 2) p.whole = p.items = (uint32_t)(some * (i == 0 ? splits : 1));
+        p.offset = c ? q.small[0][i].items % kSms : 0;
+      }
+    }
+  }
   const size_t x = q.batch * m * q.pitch * 2, s = q.batch * q.k * q.kpitch * 2;
   size_t at = 256;
   auto take = [&](size_t bytes) {
@@ -1261,8 +1520,27 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   q.p = take(s);
   q.ds = take(q.batch * q.k * sizeof(float));
   q.dp = take(q.batch * q.k * sizeof(float));
-  q.part = take(parts * q.pair * 128 * width[0] * sizeof(float));
+  q.part = take(std::max(parts * q.pair * 128 * width[0], small_parts * kSmall * kSmall) *
+                sizeof(float));
   q.bytes = at;
+  return true;
+}
+
+// Whether the steps may be taken as one polynomial of S: q(S) stays within 1800 and S's
+// own rounding within 1/64 of the largest singular value's square, over all singular values
+// that X can have.
+bool one_polynomial(const float* coeffs, int32_t steps) {
+  for (int j = 0; j <= 64; ++j) {
+    double s = (j / 64.0) * (j / 64.0), q = 1.0, grown = 1.0;
+    for (int32_t i = 0; i < steps; ++i) {
+      const double p = coeffs[3 * i] + s * (coeffs[3 * i + 1] + s * coeffs[3 * i + 2]);
+      q *= p;
+      s *= p * p;
+      if (!(std::abs(q) <= 1800.0) || !(s <= 16.0)) return false;
+      if (i + 1 < steps) grown *= p * p;
+      if (!(grown <= 262144.0)) return false;
+    }
+  }
   return true;
 }
 
@@ -1274,9 +1552,9 @@ struct Target {  // where the result goes
   float alpha, keep;
 };
 
-template <int CG>
+template <int CG, bool SMALL>
 int launch_steps(const Maps& m, const StepArgs& a, cudaStream_t s) {
-  auto kernel = steps_kernel<CG>;
+  auto kernel = steps_kernel<CG, SMALL>;
   if (!ensure_smem(reinterpret_cast<const void*>(kernel), kStepsSmem)) return SPARCML_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kSms);
@@ -1301,11 +1579,14 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   char *hi0 = w + q.hi0, *hi1 = w + q.hi1, *lo = w + q.lo, *sm = w + q.s, *pm = w + q.p;
   Maps m;
   const bool tall = q.m > q.n;
+  const bool small = q.k <= kSmall && one_polynomial(coeffs, steps);
+  const Product(*const product)[3] = small ? q.small : q.product;
+  const uint32_t pair = small ? 1 : q.pair;
   const Matrices x[2] = {{hi0, q.batch, q.m, q.n, q.pitch}, {hi1, q.batch, q.m, q.n, q.pitch}};
   const Matrices low = {lo, q.batch, q.m, q.n, q.pitch};
   const Matrices sq = {sm, q.batch, q.k, q.k, q.kpitch}, pq = {pm, q.batch, q.k, q.k, q.kpitch};
   uint32_t second[3];  // rows of the second operand that one block loads
-  for (int i = 0; i < 3; ++i) second[i] = q.product[0][i].n / q.pair;
+  for (int i = 0; i < 3; ++i) second[i] = product[0][i].n / pair;
   bool ok = box_map(&m.lo_out, low) && box_map(&m.s_out, sq) &&
             operand_map(&m.s_poly[0], sq, false, 128) &&
             operand_map(&m.s_poly[1], sq, false, second[1]) &&
@@ -1314,6 +1595,13 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
     ok = box_map(&m.x_out[i], x[i]) && operand_map(&m.x_gram[i][0], x[i], tall, 128) &&
          operand_map(&m.x_gram[i][1], x[i], tall, second[0]) &&
          operand_map(&m.x_apply[i], x[i], !tall, tall ? 128 : second[2]);
+  if (small)
+    ok = ok && operand_map(&m.lo_gram[0], low, tall, 128) &&
+         operand_map(&m.lo_gram[1], low, tall, second[0]) &&
+         operand_map(&m.lo_apply, low, !tall, tall ? 128 : second[2]) &&
+         operand_map(&m.q_lo, sq, false, tall ? second[2] : 128);
+  else
+    m.lo_gram[0] = m.lo_gram[1] = m.lo_apply = m.q_lo = m.s_out;  // not used
   if (!ok) return SPARCML_ERR_CUDA;
   const int64_t ge = g.g_type == SPARCML_F32 ? 16 : 8;
   g.vec_g = aligned_to(g.g, ge) && g.g_batch % 4 == 0 && g.g_stride % 4 == 0;
@@ -1334,7 +1622,7 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   a.steps = (uint32_t)steps;
   a.tall = tall;
   a.chains = q.chains;
-  for (uint32_t c = 0; c < q.chains; ++c) std::copy(q.product[c], q.product[c] + 3, a.product[c]);
+  for (uint32_t c = 0; c < q.chains; ++c) std::copy(product[c], product[c] + 3, a.product[c]);
   std::copy(coeffs, coeffs + 3 * steps, a.coeffs);
   a.hi[0] = reinterpret_cast<__half*>(hi0);
   a.hi[1] = reinterpret_cast<__half*>(hi1);
@@ -1357,7 +1645,9 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   a.status = reinterpret_cast<int32_t*>(w);
   launch_pdl(gather_norm_kernel, dim3(q.blocks, (unsigned)q.batch), 256, 0, s, g);
   if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
-  const int r = q.pair == 1 ? launch_steps<1>(m, a, s) : launch_steps<2>(m, a, s);
+  const int r = small       ? launch_steps<1, true>(m, a, s)
+                : pair == 1 ? launch_steps<1, false>(m, a, s)
+                            : launch_steps<2, false>(m, a, s);
   if (r != SPARCML_OK) return r;
   note_launches(2);
   return SPARCML_OK;
