@@ -39,6 +39,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
 
 #include "tensor.cuh"
 #include "types.cuh"
@@ -1472,8 +1474,6 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
                         width[i], i == 0, batch, &t);
       if (batch && !p.items) return false;
       p.b0 = (uint32_t)b0;
-      // the second chain starts beside the first one
-      p.offset = c ? q.product[0][i].items % (kSms / q.pair) : 0;
       if (p.splits > 1) {
         p.part0 = (uint32_t)parts;
         parts += p.items;
@@ -1501,7 +1501,6 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
           small_parts += some * splits;
         }
         if (i < 2) p.whole = p.items = (uint32_t)(some * (i == 0 ? splits : 1));
-        p.offset = c ? q.small[0][i].items % kSms : 0;
       }
     }
   }
@@ -1552,12 +1551,55 @@ struct Target {  // where the result goes
   float alpha, keep;
 };
 
+// Blocks (or pairs of blocks) of a kernel that run at one time on the current device, up to
+// one per SM; 0 if that cannot be found out. Asked for once per device.
 template <int CG, bool SMALL>
-int launch_steps(const Maps& m, const StepArgs& a, cudaStream_t s) {
+unsigned resident() {
+  static std::mutex lock;
+  static std::map<int, unsigned> known;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> hold(lock);
+  const auto it = known.find(device);
+  if (it != known.end()) return it->second;
   auto kernel = steps_kernel<CG, SMALL>;
-  if (!ensure_smem(reinterpret_cast<const void*>(kernel), kStepsSmem)) return SPARCML_ERR_CUDA;
+  if (!ensure_smem(reinterpret_cast<const void*>(kernel), kStepsSmem)) return 0;
+  int count = 0;
+  if (CG == 1) {
+    int per = 0, sms = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, kStepsSmem) !=
+            cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+      return 0;
+    count = std::min(per, 1) * sms;
+  } else {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kSms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kStepsSmem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CG;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) != cudaSuccess) return 0;
+  }
+  const unsigned fit = (unsigned)std::min<int>(count, kSms / CG);
+  known[device] = fit;
+  return fit;
+}
+
+template <int CG, bool SMALL>
+int launch_steps(const Maps& m, StepArgs& a, cudaStream_t s) {
+  auto kernel = steps_kernel<CG, SMALL>;
+  const unsigned clusters = resident<CG, SMALL>();
+  if (clusters == 0 || !ensure_smem(reinterpret_cast<const void*>(kernel), kStepsSmem))
+    return SPARCML_ERR_CUDA;
+  for (int i = 0; i < 3; ++i)  // the second chain starts beside the first one
+    a.product[1][i].offset = a.product[0][i].items % clusters;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kSms);
+  cfg.gridDim = dim3(clusters * CG);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kStepsSmem;
   cfg.stream = s;
