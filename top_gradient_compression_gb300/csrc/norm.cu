@@ -426,7 +426,7 @@ struct NormGradArgs {
 // together. Rows of whole, aligned packs come through a ring in shared memory, in which
 // each thread copies ahead and reads back its own packs alone, so the ring needs no
 // barrier; other rows (V = 2) as in the forward pass. At the
-// end the groups' sums are joined in their order, and the blocks' by the last block to
+// end the groups' sums are joined, and then the blocks', by the last block to
 // finish (`ticket`, few sums) or by norm_join_kernel. Every order is fixed.
 constexpr int kRing = 3;
 
@@ -624,28 +624,58 @@ norm_backward_kernel(const NormGradArgs a) {
   float* to_w = a.part_w + (uint64_t)blockIdx.x * a.dim;
   float* to_b = a.part_b + (uint64_t)blockIdx.x * a.dim;
   if (groups > 1) {
-    float* join = reinterpret_cast<float*>(dynamic);  // [2][dim]
+    // Groups that share a warp by shuffles, then a row of sums per warp or wider group, then
+    // a thread per column. (One group after the other, 1025 x 64 took 25 us in all.)
+    if (threads < 32) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          float2 w = split(gw[j][i]), b = split(gb[j][i]);
+          if (threads == 8) {
+            Group::add<8>(w);
+            Group::add<8>(b);
+          }
+          Group::add<16>(w);
+          Group::add<16>(b);
+          gw[j][i] = f2(w.x, w.y);
+          gb[j][i] = f2(b.x, b.y);
+        }
+      }
+    }
+    const uint32_t sets = min(groups, blockDim.x / 32);
+    float* join = reinterpret_cast<float*>(dynamic);  // [sets][2][dim]
     asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
-    for (uint32_t k = 0; k < groups; ++k) {
-      if (g.index == k) {
+    if (threads >= 32 || lane_id() < threads) {
+      float* set = join + (uint64_t)(threads < 32 ? threadIdx.x >> 5 : g.index) * 2 * dim;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
+      for (int j = 0; j < NV; ++j) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const uint32_t c = column<V>(j, i, threads, t);
-            if (c < a.dim) {
-              join[c] = (k ? join[c] : 0.f) + part(gw[j][i / 2], i);
-              join[a.dim + c] = (k ? join[a.dim + c] : 0.f) + part(gb[j][i / 2], i);
-            }
+        for (int i = 0; i < V; i += PACKS ? 4 : 1) {
+          const uint32_t c = column<V>(j, i, threads, t);
+          if (c >= dim) continue;
+          if constexpr (PACKS) {
+            const float2 w0 = split(gw[j][i / 2]), w1 = split(gw[j][i / 2 + 1]);
+            const float2 b0 = split(gb[j][i / 2]), b1 = split(gb[j][i / 2 + 1]);
+            *reinterpret_cast<float4*>(set + c) = make_float4(w0.x, w0.y, w1.x, w1.y);
+            *reinterpret_cast<float4*>(set + dim + c) = make_float4(b0.x, b0.y, b1.x, b1.y);
+          } else {
+            set[c] = part(gw[j][0], i);
+            set[dim + c] = part(gb[j][0], i);
           }
         }
       }
-      __syncthreads();
     }
-    for (uint32_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-      to_w[c] = join[c];
-      to_b[c] = join[a.dim + c];
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < dim; c += blockDim.x) {
+      float w = 0.f, b = 0.f;
+      for (uint32_t k = 0; k < sets; ++k) {
+        w += join[2 * k * dim + c];
+        b += join[(2 * k + 1) * dim + c];
+      }
+      to_w[c] = w;
+      to_b[c] = b;
     }
   } else {
 #pragma unroll
@@ -661,21 +691,48 @@ norm_backward_kernel(const NormGradArgs a) {
     }
   }
   if (a.ticket == nullptr) return;
-  __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  if (threadIdx.x == 0) {
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    __threadfence();
+  }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  for (uint32_t c = threadIdx.x; c < a.dim; c += blockDim.x) {
-    float w = 0.f, b = 0.f;
-#pragma unroll 4
-    for (uint32_t p = 0; p < gridDim.x; ++p) {
-      w += __ldcg(a.part_w + (uint64_t)p * a.dim + c);
-      b += __ldcg(a.part_b + (uint64_t)p * a.dim + c);
+  // Slices of `span` threads, a column each, share the blocks' sums of a narrow row.
+  const uint32_t span = min(blockDim.x, (dim + 31) / 32 * 32), slices = blockDim.x / span;
+  const uint32_t slice = threadIdx.x / span;
+  for (uint32_t c = threadIdx.x - slice * span; c < (dim + span - 1) / span * span; c += span) {
+    float2 sum = make_float2(0.f, 0.f);
+    if (c < dim && slice < slices) {
+      for (uint32_t p = slice; p < gridDim.x; p += 8 * slices) {
+        float2 v[8];  // on their way together
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+          const uint64_t at = (uint64_t)(p + k * slices) * dim + c;
+          const bool in = p + k * slices < gridDim.x;
+          v[k] = in ? make_float2(__ldcg(a.part_w + at), __ldcg(a.part_b + at))
+                    : make_float2(0.f, 0.f);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 8; ++k) {
+          sum.x += v[k].x;
+          sum.y += v[k].y;
+        }
+      }
     }
-    if (a.dweight) a.dweight[c] = a.accumulate ? a.dweight[c] + w : w;
-    if (a.dbias) a.dbias[c] = a.accumulate ? a.dbias[c] + b : b;
+    if (slices > 1) {  // then span covers the row
+      scratch[threadIdx.x] = sum;
+      __syncthreads();
+      for (uint32_t k = 1; k < slices && slice == 0; ++k) {
+        sum.x += scratch[k * span + c].x;
+        sum.y += scratch[k * span + c].y;
+      }
+    }
+    if (c < dim && slice == 0) {
+      if (a.dweight) a.dweight[c] = a.accumulate ? a.dweight[c] + sum.x : sum.x;
+      if (a.dbias) a.dbias[c] = a.accumulate ? a.dbias[c] + sum.y : sum.y;
+    }
   }
   if (threadIdx.x == 0) *a.ticket = 0;  // as the next call needs it
 }
@@ -833,7 +890,7 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
   if (vec && (type_of<T>() == a.w_type || (!a.w && !a.b))) return forward_packs<T, T>(a, s);
   if (sizeof(T) == 2 && vec && a.w_type == SPARCML_F32) return forward_packs<T, float>(a, s);
   if (a.dim <= 512 * 16) {
-    const uint32_t threads = threads_for(a.dim, 16);
+    const uint32_t threads = a.dim <= 128 ? 8 : a.dim <= 256 ? 16 : threads_for(a.dim, 16);
     if (threads <= 256)
       return launch_forward<T, T, 2, 8, false, 256, 3>(a, threads, 256, 3, s);
     return launch_forward<T, T, 2, 8, false, 512, 1>(a, threads, threads, 2, s);
@@ -864,8 +921,10 @@ BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
   return {threads, threads * groups,
           (uint32_t)std::max<uint64_t>(1, std::min((rows + groups - 1) / groups, most))};
 }
-// One block joins up to this many partial sums in less time than a launch takes.
-constexpr uint64_t kTicketSums = 16 * 1024;
+// Up to this many partial sums the last block to finish joins them: that saves the host a
+// launch (2 us of the 18 that a small call takes) and costs 0.8 to 1.7 us more on the device
+// (64 x 512 fp32 5.7 against 4.0 us). From 8 K sums on it costs more than 3.
+constexpr uint64_t kTicketSums = 4 * 1024;
 
 template <typename T, typename W, int V, int MAXT, int MINB>
 bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
@@ -876,7 +935,7 @@ bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t
                             : align_up(a.dim * sizeof(float), 16) +
                                   4ull * groups * slot_elements((uint32_t)a.dim, sizeof(T)) *
                                       sizeof(T);
-  const size_t join = groups > 1 ? 2 * a.dim * sizeof(float) : 0;
+  const size_t join = groups > 1 ? 2 * std::min(groups, h.block / 32) * a.dim * sizeof(float) : 0;
   const size_t smem = std::max(ring, join);
   if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
   launch_pdl(kernel, h.parts, h.block, smem, s, a);
