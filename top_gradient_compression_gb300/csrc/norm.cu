@@ -859,17 +859,23 @@ bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, 
 }
 
 // Up to 16 packs per lane a warp takes a row alone, which needs no barrier (2048 fp32
-// columns: 53 us against 61 with four warps); short rows share a warp, and longer ones take
-// several. Few packs are kept in fp32: 65536 x 512 bf16 30 us against 36.
+// columns: 53 us against 61 with four warps); longer ones take several. Shorter rows share a
+// warp, four packs per lane: 65536 x 256 bf16 15 us, against 24 with a warp for a row, of
+// which fewer are on their way at a time. For few rows the fewest steps count: 1 x 256 bf16
+// 1.8 us against 2.6.
 template <typename T, typename W>
 bool forward_packs(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const uint64_t packs = a.dim / V;
-  if (packs <= 32)
+  const bool few = a.rows <= 8 * kSms;
+  if (packs <= 8 || (few && packs <= 32))
     return launch_forward<T, W, V, 1, true, 128, 10>(
         a, packs <= 8 ? 8 : packs <= 16 ? 16 : 32, 128, 10, s);
-  if (packs <= 64) return launch_forward<T, W, V, 2, true, 128, 8>(a, 32, 128, 8, s);
-  if (packs <= 128) return launch_forward<T, W, V, 4, false, 128, 7>(a, 32, 128, 7, s);
+  if (packs <= 16 || (few && packs <= 64))
+    return launch_forward<T, W, V, 2, true, 128, 8>(a, packs <= 16 ? 8 : 32, 128, 8, s);
+  if (packs <= 128)
+    return launch_forward<T, W, V, 4, false, 128, 7>(
+        a, packs <= 32 ? 8 : packs <= 64 ? 16 : 32, 128, 7, s);
   if (packs <= 256) return launch_forward<T, W, V, 8, false, 128, 4>(a, 32, 128, 4, s);
   if (packs <= 512) return launch_forward<T, W, V, 16, false, 128, 3>(a, 32, 128, 3, s);
   const uint32_t threads = threads_for(packs, 4);
