@@ -120,51 +120,56 @@ __host__ __device__ constexpr uint32_t slot_elements(uint32_t dim, uint32_t byte
   return (dim + 2 * per - 2) / per * per + per;
 }
 
-// V weights of type W from column c, as fp32 pairs; `none` where there are none.
+// V weights of type W at `at`, as fp32 pairs; `none` where there are none.
 template <typename W, int V>
-__device__ __forceinline__ void load_affine(const void* w, uint32_t c, float none,
+__device__ __forceinline__ void load_affine(bool there, const W* at, float none,
                                             F2 (&out)[V / 2]) {
-  if (w == nullptr) {
+  if (!there) {
 #pragma unroll
     for (int e = 0; e < V / 2; ++e) out[e] = f2(none, none);
     return;
   }
-  const W* p = static_cast<const W*>(w) + c;
   if constexpr (sizeof(W) == 4) {
 #pragma unroll
     for (int q = 0; q < V / 4; ++q) {
-      const float4 f = *reinterpret_cast<const float4*>(p + 4 * q);
+      const float4 f = *reinterpret_cast<const float4*>(at + 4 * q);
       out[2 * q] = f2(f.x, f.y);
       out[2 * q + 1] = f2(f.z, f.w);
     }
   } else {
-    unpack<W, 8>(load_raw<W, 8>(p), out);
+    unpack<W, 8>(load_raw<W, 8>(at), out);
   }
 }
 
-// Columns of a thread. Rows of whole packs (V = 4 or 8): pack j of thread t starts at
-// column (j * threads + t) * V. Other rows (V = 2): its pair j is columns 2 j * threads + t
-// and `threads` further, so that a warp's accesses are consecutive elements.
-template <int V>
-__device__ __forceinline__ uint32_t column(int j, int i, uint32_t threads, uint32_t t) {
-  return V == 2 ? (2 * j + i) * threads + t : (j * threads + t) * V + i;
+// Columns of a thread: `first` and constant offsets from it, which the compiler folds into the
+// accesses' addresses (with offsets from the number of threads, 16384 x 4095 bf16 took 48
+// instructions per element). LANES neighbouring threads own LANES * NV * V columns in a row.
+// Whole packs (V = 4 or 8): pack j of a thread is LANES packs after its pack j - 1. Else (V = 2)
+// its pair j is two columns LANES apart, so that a warp's accesses are consecutive elements.
+template <int V, int NV, int LANES>
+__device__ __forceinline__ int first_column(uint32_t t) {
+  return (int)((t / LANES) * (NV * LANES * V) + (t % LANES) * (V == 2 ? 1 : V));
 }
-template <typename T, int V>
-__device__ __forceinline__ void store_pack(T* row, int j, uint32_t threads, uint32_t t,
-                                           uint32_t dim, const F2 (&f)[V / 2]) {
+template <int V, int LANES>
+__device__ __forceinline__ constexpr int offset(int j, int i) {
+  return V == 2 ? (2 * j + i) * LANES : j * LANES * V + i;
+}
+// A pack or pair to `to`, of whose row `left` columns are left.
+template <typename T, int V, int LANES>
+__device__ __forceinline__ void store_pack(T* to, int j, int left, const F2 (&f)[V / 2]) {
   if constexpr (V == 2) {
     const float2 p = split(f[0]);
-    const uint32_t c0 = column<V>(j, 0, threads, t), c1 = c0 + threads;
-    row[c0] = from_f32<T>(p.x);
-    if (c1 < dim) row[c1] = from_f32<T>(p.y);
+    to[offset<V, LANES>(j, 0)] = from_f32<T>(p.x);
+    if (offset<V, LANES>(j, 1) < left) to[offset<V, LANES>(j, 1)] = from_f32<T>(p.y);
   } else {
-    *reinterpret_cast<uint4*>(row + column<V>(j, 0, threads, t)) = pack<T, V>(f);
+    *reinterpret_cast<uint4*>(to + offset<V, LANES>(j, 0)) = pack<T, V>(f);
   }
 }
 // Such a pair of a vector in shared memory; zero beyond its end.
-template <typename T>
-__device__ __forceinline__ F2 pair_at(const T* v, uint32_t c0, uint32_t c1, uint32_t dim) {
-  return f2(to_f32(v[c0]), c1 < dim ? to_f32(v[c1]) : 0.f);
+template <typename T, int LANES>
+__device__ __forceinline__ F2 pair_at(const T* v, int j, int left) {
+  return f2(to_f32(v[offset<2, LANES>(j, 0)]),
+            offset<2, LANES>(j, 1) < left ? to_f32(v[offset<2, LANES>(j, 1)]) : 0.f);
 }
 
 struct NormArgs {
@@ -191,7 +196,7 @@ struct NormArgs {
 // What bounds it in 16 bits is arithmetic: 16384 x 4096 bf16 needs 680 of the 700 issue
 // cycles that a row's bytes take when each pass over the row converts it again. With KEEP
 // the fp32 values, and then their deviations, stay in registers.
-template <typename T, typename W, int V, int NV, bool KEEP, int MAXT, int MINB>
+template <typename T, typename W, int V, int NV, int LANES, bool KEEP, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs a) {
   griddep_wait();
   extern __shared__ __align__(16) uint8_t dynamic[];
@@ -204,6 +209,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
   const uint32_t t = g.t;
   const uint64_t step = (uint64_t)gridDim.x * groups;
   const float inv = 1.0f / (float)dim;
+  const int first = first_column<V, NV, LANES>(t), all = (int)dim - first;
   const T* xs = static_cast<const T*>(a.x);
   // V = 2: [2][dim] weights, then two slots for each group
   float* affine = reinterpret_cast<float*>(dynamic);
@@ -217,10 +223,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
       const T* x = xs + (int64_t)row * a.x_stride;
       if constexpr (PACKS) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const uint32_t c = column<V>(j, 0, threads, t);
-          if (c < dim) next[j] = load_raw<T, V>(x + c);
-        }
+        for (int j = 0; j < NV; ++j)
+          if (offset<V, LANES>(j, 0) < all)
+            next[j] = load_raw<T, V>(x + first + offset<V, LANES>(j, 0));
       } else {
         copy_row(slots + slot * slot_size, x, dim, row * (uint64_t)a.x_stride, g);
       }
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
   for (; base < a.rows; base += step) {  // the same turns for all groups
     const uint64_t row = base + g.index;
     const bool active = row < a.rows;
-    const uint32_t end = active ? dim : 0;
+    const int left = active ? all : 0;
     if constexpr (PACKS) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) v[j] = next[j];
@@ -247,12 +252,11 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
       g.sync();
-      const T* x = slots + turn * slot_size + (active ? row_skew(xs + (int64_t)row * a.x_stride) : 0);
+      const T* x = slots + turn * slot_size + first +
+                   (active ? row_skew(xs + (int64_t)row * a.x_stride) : 0);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const uint32_t c = column<V>(j, 0, threads, t);
-        if (c < end) v[j].w = pair_at(x, c, c + threads, dim);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (offset<V, LANES>(j, 0) < left) v[j].w = pair_at<T, LANES>(x, j, left);
       turn ^= 1u;
       fetch(row + step, turn);
     }
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
     F2 s = f2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (column<V>(j, 0, threads, t) < end) {
+      if (offset<V, LANES>(j, 0) < left) {
         F2 f[P];
         unpack<T, V>(v[j], f);
         if constexpr (KEEP) {
@@ -281,14 +285,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
     const F2 minus = f2(-mean, -mean);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (column<V>(j, 0, threads, t) < end) {
+      if (offset<V, LANES>(j, 0) < left) {
         F2 f[P], q = f2(0.f, 0.f);
         if constexpr (!KEEP) unpack<T, V>(v[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           f[i] = add2<PK>(KEEP ? kept[KEEP ? j : 0][i] : f[i], minus);
           if (KEEP) kept[KEEP ? j : 0][i] = f[i];
-          if (!PACKS && column<V>(j, 1, threads, t) >= dim) f[i] = f2(split(f[i]).x, 0.f);
+          if (!PACKS && offset<V, LANES>(j, 1) >= left) f[i] = f2(split(f[i]).x, 0.f);
           q = fma2<PK>(f[i], f[i], q);
         }
         s = add2<PK>(s, q);
@@ -302,25 +306,26 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
       a.rstd[row] = rstd;
     }
     const F2 by = f2(rstd, rstd);
-    T* y = static_cast<T*>(a.y) + (int64_t)row * a.y_stride;
+    T* y = static_cast<T*>(a.y) + (int64_t)row * a.y_stride + first;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t c = column<V>(j, 0, threads, t);
-      if (c < dim) {
+      if (offset<V, LANES>(j, 0) < all) {
         F2 w[P], b[P], f[P];
         if constexpr (PACKS) {
-          load_affine<W, V>(a.w, c, 1.f, w);
-          load_affine<W, V>(a.b, c, 0.f, b);
+          load_affine<W, V>(a.w, static_cast<const W*>(a.w) + first + offset<V, LANES>(j, 0), 1.f,
+                            w);
+          load_affine<W, V>(a.b, static_cast<const W*>(a.b) + first + offset<V, LANES>(j, 0), 0.f,
+                            b);
         } else {
-          w[0] = pair_at(affine, c, c + threads, dim);
-          b[0] = pair_at(affine + dim, c, c + threads, dim);
+          w[0] = pair_at<float, LANES>(affine + first, j, all);
+          b[0] = pair_at<float, LANES>(affine + dim + first, j, all);
         }
         if constexpr (!KEEP) unpack<T, V>(v[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i)
           f[i] = fma2<PK>(mul2<PK>(KEEP ? kept[KEEP ? j : 0][i] : add2<PK>(f[i], minus), by), w[i],
                           b[i]);
-        store_pack<T, V>(y, j, threads, t, dim, f);
+        store_pack<T, V, LANES>(y, j, all, f);
       }
     }
   }
@@ -430,7 +435,7 @@ struct NormGradArgs {
 // finish (`ticket`, few sums) or by norm_join_kernel. Every order is fixed.
 constexpr int kRing = 3;
 
-template <typename T, typename W, int V, int NV, int MAXT, int MINB>
+template <typename T, typename W, int V, int NV, int LANES, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB)
 norm_backward_kernel(const NormGradArgs a) {
   griddep_wait();
@@ -450,6 +455,7 @@ norm_backward_kernel(const NormGradArgs a) {
     for (int i = 0; i < P; ++i) gw[j][i] = gb[j][i] = f2(0.f, 0.f);
   }
   const float inv = 1.0f / (float)dim;
+  const int first = first_column<V, NV, LANES>(t), all = (int)dim - first;
   const uint64_t step = (uint64_t)gridDim.x * groups;
   const T* xs = static_cast<const T*>(a.x);
   const T* ds = static_cast<const T*>(a.dy);
@@ -465,13 +471,13 @@ norm_backward_kernel(const NormGradArgs a) {
       const T* x = xs + (int64_t)row * a.x_stride;
       const T* dy = ds + (int64_t)row * a.dy_stride;
       if constexpr (PACKS) {
-        uint8_t* to = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
+        uint8_t* to = dynamic + (slot * 2 * NV * MAXT + threadIdx.x) * 16;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-          const uint32_t c = column<V>(j, 0, threads, t);
-          if (c < dim) {
-            cp_async16(to + j * blockDim.x * 16, x + c);
-            cp_async16(to + (NV + j) * blockDim.x * 16, dy + c);
+          const int o = offset<V, LANES>(j, 0);
+          if (o < all) {
+            cp_async16(to + j * MAXT * 16, x + first + o);
+            cp_async16(to + (NV + j) * MAXT * 16, dy + first + o);
           }
         }
       } else {
@@ -490,16 +496,17 @@ norm_backward_kernel(const NormGradArgs a) {
   if constexpr (PACKS) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t c = column<V>(j, 0, threads, t);
+      const int o = offset<V, LANES>(j, 0);
 #pragma unroll
       for (int q = 0; q < kWide; ++q)
-        if (a.w && c < dim)
-          own[j][q].w = *reinterpret_cast<const uint4*>(static_cast<const W*>(a.w) + c + 4 * q);
+        if (a.w && o < all)
+          own[j][q].w =
+              *reinterpret_cast<const uint4*>(static_cast<const W*>(a.w) + first + o + 4 * q);
     }
   }
-  auto weights_at = [&](int j, uint32_t c, F2(&w)[P]) {
+  auto weights_at = [&](int j, F2(&w)[P]) {
     if constexpr (!PACKS) {
-      w[0] = pair_at(weights, c, c + threads, dim);
+      w[0] = pair_at<float, LANES>(weights + first, j, all);
     } else if (a.w == nullptr) {
 #pragma unroll
       for (int i = 0; i < P; ++i) w[i] = f2(1.f, 1.f);
@@ -527,6 +534,7 @@ norm_backward_kernel(const NormGradArgs a) {
   for (; base < a.rows; base += step) {  // the same turns for all groups
     const uint64_t row = base + g.index;
     const bool active = row < a.rows;
+    const int left = active ? all : 0;
     const float mean = next_mean, rstd = next_rstd;
     if (row + step < a.rows) {
       next_mean = a.mean[row + step];
@@ -535,26 +543,25 @@ norm_backward_kernel(const NormGradArgs a) {
     Raw<T, V> vx[NV], vd[NV];
     asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 2) : "memory");
     if constexpr (PACKS) {
-      const uint8_t* from = dynamic + ((uint64_t)slot * 2 * NV * blockDim.x + threadIdx.x) * 16;
+      const uint8_t* from = dynamic + (slot * 2 * NV * MAXT + threadIdx.x) * 16;
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        vx[j].w = *reinterpret_cast<const uint4*>(from + j * blockDim.x * 16);
-        vd[j].w = *reinterpret_cast<const uint4*>(from + (NV + j) * blockDim.x * 16);
+        vx[j].w = *reinterpret_cast<const uint4*>(from + j * MAXT * 16);
+        vd[j].w = *reinterpret_cast<const uint4*>(from + (NV + j) * MAXT * 16);
       }
     } else {
       g.sync();
-      const T* x = slots + (2 * slot) * slot_size;
-      const T* dy = slots + (2 * slot + 1) * slot_size;
+      const T* x = slots + (2 * slot) * slot_size + first;
+      const T* dy = slots + (2 * slot + 1) * slot_size + first;
       if (active) {
         x += row_skew(xs + (int64_t)row * a.x_stride);
         dy += row_skew(ds + (int64_t)row * a.dy_stride);
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const uint32_t c = column<V>(j, 0, threads, t);
-        if (active && c < dim) {
-          vx[j].w = pair_at(x, c, c + threads, dim);
-          vd[j].w = pair_at(dy, c, c + threads, dim);
+        if (offset<V, LANES>(j, 0) < left) {
+          vx[j].w = pair_at<T, LANES>(x, j, left);
+          vd[j].w = pair_at<T, LANES>(dy, j, left);
         }
       }
     }
@@ -568,10 +575,9 @@ norm_backward_kernel(const NormGradArgs a) {
     F2 xc[KEEP ? NV : 1][P], kept[KEEP ? NV : 1][P];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t c = column<V>(j, 0, threads, t);
-      if (active && c < dim) {
+      if (offset<V, LANES>(j, 0) < left) {
         F2 w[P], d[P], f[P];
-        weights_at(j, c, w);
+        weights_at(j, w);
         unpack<T, V>(vd[j], d);
         unpack<T, V>(vx[j], f);
 #pragma unroll
@@ -598,14 +604,13 @@ norm_backward_kernel(const NormGradArgs a) {
     // dx = (x - mean) k2 + (d rstd + k1)
     const float k1s = -s.x * inv * rstd, k2s = -s.y * inv * rstd * rstd;
     const F2 k1 = f2(k1s, k1s), k2 = f2(k2s, k2s);
-    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
+    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride + first;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const uint32_t c = column<V>(j, 0, threads, t);
-      if (c < dim) {
+      if (offset<V, LANES>(j, 0) < all) {
         F2 w[P], d[P], f[P];
         if constexpr (!KEEP) {
-          weights_at(j, c, w);
+          weights_at(j, w);
           unpack<T, V>(vd[j], d);
           unpack<T, V>(vx[j], f);
         }
@@ -615,7 +620,7 @@ norm_backward_kernel(const NormGradArgs a) {
           const F2 xv = KEEP ? xc[KEEP ? j : 0][i] : add2<false>(f[i], minus);
           f[i] = fma2<false>(xv, k2, fma2<false>(dv, by, k1));
         }
-        store_pack<T, V>(dx, j, threads, t, dim, f);
+        store_pack<T, V, LANES>(dx, j, all, f);
       }
     }
   }
@@ -653,7 +658,7 @@ norm_backward_kernel(const NormGradArgs a) {
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
         for (int i = 0; i < V; i += PACKS ? 4 : 1) {
-          const uint32_t c = column<V>(j, i, threads, t);
+          const uint32_t c = (uint32_t)(first + offset<V, LANES>(j, i));
           if (c >= dim) continue;
           if constexpr (PACKS) {
             const float2 w0 = split(gw[j][i / 2]), w1 = split(gw[j][i / 2 + 1]);
@@ -682,7 +687,7 @@ norm_backward_kernel(const NormGradArgs a) {
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint32_t c = column<V>(j, i, threads, t);
+        const uint32_t c = (uint32_t)(first + offset<V, LANES>(j, i));
         if (c < a.dim) {
           to_w[c] = part(gw[j][i / 2], i);
           to_b[c] = part(gb[j][i / 2], i);
@@ -840,9 +845,9 @@ uint32_t threads_for(uint64_t dim, uint32_t per) {
 constexpr uint32_t kSms = 152;
 
 // `threads` for a row, blocks of at least `block` threads, `fit` of them per SM.
-template <typename T, typename W, int V, int NV, bool KEEP, int MAXT, int MINB>
+template <typename T, typename W, int V, int NV, int LANES, bool KEEP, int MAXT, int MINB>
 bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, cudaStream_t s) {
-  auto kernel = norm_forward_kernel<T, W, V, NV, KEEP, MAXT, MINB>;
+  auto kernel = norm_forward_kernel<T, W, V, NV, LANES, KEEP, MAXT, MINB>;
   a.threads = threads;
   const uint32_t groups = std::max(1u, block / threads);
   size_t smem = 0;
@@ -868,21 +873,21 @@ bool forward_packs(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const uint64_t packs = a.dim / V;
   const bool few = a.rows <= 8 * kSms;
-  if (packs <= 8 || (few && packs <= 32))
-    return launch_forward<T, W, V, 1, true, 128, 10>(
-        a, packs <= 8 ? 8 : packs <= 16 ? 16 : 32, 128, 10, s);
-  if (packs <= 16 || (few && packs <= 64))
-    return launch_forward<T, W, V, 2, true, 128, 8>(a, packs <= 16 ? 8 : 32, 128, 8, s);
-  if (packs <= 128)
-    return launch_forward<T, W, V, 4, false, 128, 7>(
-        a, packs <= 32 ? 8 : packs <= 64 ? 16 : 32, 128, 7, s);
-  if (packs <= 256) return launch_forward<T, W, V, 8, false, 128, 4>(a, 32, 128, 4, s);
-  if (packs <= 512) return launch_forward<T, W, V, 16, false, 128, 3>(a, 32, 128, 3, s);
+  if (packs <= 8) return launch_forward<T, W, V, 1, 8, true, 128, 10>(a, 8, 128, 10, s);
+  if (few && packs <= 16) return launch_forward<T, W, V, 1, 16, true, 128, 10>(a, 16, 128, 10, s);
+  if (few && packs <= 32) return launch_forward<T, W, V, 1, 32, true, 128, 10>(a, 32, 128, 10, s);
+  if (packs <= 16) return launch_forward<T, W, V, 2, 8, true, 128, 8>(a, 8, 128, 8, s);
+  if (few && packs <= 64) return launch_forward<T, W, V, 2, 32, true, 128, 8>(a, 32, 128, 8, s);
+  if (packs <= 32) return launch_forward<T, W, V, 4, 8, false, 128, 7>(a, 8, 128, 7, s);
+  if (packs <= 64) return launch_forward<T, W, V, 4, 16, false, 128, 7>(a, 16, 128, 7, s);
+  if (packs <= 128) return launch_forward<T, W, V, 4, 32, false, 128, 7>(a, 32, 128, 7, s);
+  if (packs <= 256) return launch_forward<T, W, V, 8, 32, false, 128, 4>(a, 32, 128, 4, s);
+  if (packs <= 512) return launch_forward<T, W, V, 16, 32, false, 128, 3>(a, 32, 128, 3, s);
   const uint32_t threads = threads_for(packs, 4);
   if (packs <= 2048)
-    return launch_forward<T, W, V, 4, true, 512, 1>(a, threads, threads,
-                                                    std::max(1u, 640 / threads), s);
-  return launch_forward<T, W, V, 4, false, 1024, 1>(a, threads, threads, 1, s);
+    return launch_forward<T, W, V, 4, 32, true, 512, 1>(a, threads, threads,
+                                                        std::max(1u, 640 / threads), s);
+  return launch_forward<T, W, V, 4, 32, false, 1024, 1>(a, threads, threads, 1, s);
 }
 
 // Whole packs: 16-byte aligned rows and weights of the rows' type or fp32. Everything else
@@ -896,10 +901,12 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
   if (vec && (type_of<T>() == a.w_type || (!a.w && !a.b))) return forward_packs<T, T>(a, s);
   if (sizeof(T) == 2 && vec && a.w_type == SPARCML_F32) return forward_packs<T, float>(a, s);
   if (a.dim <= 512 * 16) {
-    const uint32_t threads = a.dim <= 128 ? 8 : a.dim <= 256 ? 16 : threads_for(a.dim, 16);
+    const uint32_t threads = threads_for(a.dim, 16);
+    if (a.dim <= 128) return launch_forward<T, T, 2, 8, 8, false, 256, 3>(a, 8, 256, 3, s);
+    if (a.dim <= 256) return launch_forward<T, T, 2, 8, 16, false, 256, 3>(a, 16, 256, 3, s);
     if (threads <= 256)
-      return launch_forward<T, T, 2, 8, false, 256, 3>(a, threads, 256, 3, s);
-    return launch_forward<T, T, 2, 8, false, 512, 1>(a, threads, threads, 2, s);
+      return launch_forward<T, T, 2, 8, 32, false, 256, 3>(a, threads, 256, 3, s);
+    return launch_forward<T, T, 2, 8, 32, false, 512, 1>(a, threads, threads, 2, s);
   }
   const bool wide = a.dim % V == 0 && a.x_stride % V == 0 && a.y_stride % V == 0 &&
                     aligned_to(a.x, 16) && aligned_to(a.y, 16);
@@ -932,12 +939,12 @@ BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
 // (64 x 512 fp32 5.7 against 4.0 us). From 8 K sums on it costs more than 3.
 constexpr uint64_t kTicketSums = 4 * 1024;
 
-template <typename T, typename W, int V, int MAXT, int MINB>
+template <typename T, typename W, int V, int LANES, int MAXT, int MINB>
 bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
   constexpr int NV = kBackwardPer / V;
-  auto kernel = norm_backward_kernel<T, W, V, NV, MAXT, MINB>;
+  auto kernel = norm_backward_kernel<T, W, V, NV, LANES, MAXT, MINB>;
   const uint32_t groups = h.block / h.threads;
-  const size_t ring = V > 2 ? (size_t)kRing * 2 * NV * h.block * 16
+  const size_t ring = V > 2 ? (size_t)kRing * 2 * NV * MAXT * 16
                             : align_up(a.dim * sizeof(float), 16) +
                                   4ull * groups * slot_elements((uint32_t)a.dim, sizeof(T)) *
                                       sizeof(T);
@@ -946,6 +953,14 @@ bool launch_backward(const NormGradArgs& a, const BackwardShape& h, cudaStream_t
   if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
   launch_pdl(kernel, h.parts, h.block, smem, s, a);
   return true;
+}
+
+template <typename T, typename W, int V>
+bool launch_backward_shape(const NormGradArgs& a, const BackwardShape& h, cudaStream_t s) {
+  if (h.threads == 8) return launch_backward<T, W, V, 8, 256, kFit>(a, h, s);
+  if (h.threads == 16) return launch_backward<T, W, V, 16, 256, kFit>(a, h, s);
+  if (h.block <= 256) return launch_backward<T, W, V, 32, 256, kFit>(a, h, s);
+  return launch_backward<T, W, V, 32, 512, 1>(a, h, s);
 }
 
 template <typename T>
@@ -963,7 +978,6 @@ bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
   a.part_b = reinterpret_cast<float*>(ws + 256) + (uint64_t)h.parts * a.dim;
   const bool ticket = sums && !longer && h.parts * a.dim <= kTicketSums;
   if (ticket) a.ticket = reinterpret_cast<uint32_t*>(ws + kTicketOffset);
-  const bool small = h.block <= 256;
   bool ok = true;
   if (longer) {
     // the column sums first: dx may be written over x or dy
@@ -976,14 +990,11 @@ bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
     if (vec) launch_pdl(norm_backward_long_kernel<T, V>, (unsigned)a.rows, 1024, 0, s, a);
     else launch_pdl(norm_backward_long_kernel<T, 1>, (unsigned)a.rows, 1024, 0, s, a);
   } else if (packs && same) {
-    ok = small ? launch_backward<T, T, V, 256, kFit>(a, h, s)
-               : launch_backward<T, T, V, 512, 1>(a, h, s);
+    ok = launch_backward_shape<T, T, V>(a, h, s);
   } else if (sizeof(T) == 2 && packs) {
-    ok = small ? launch_backward<T, float, V, 256, kFit>(a, h, s)
-               : launch_backward<T, float, V, 512, 1>(a, h, s);
+    ok = launch_backward_shape<T, float, V>(a, h, s);
   } else {
-    ok = small ? launch_backward<T, T, 2, 256, kFit>(a, h, s)
-               : launch_backward<T, T, 2, 512, 1>(a, h, s);
+    ok = launch_backward_shape<T, T, 2>(a, h, s);
   }
   const bool join = sums && !ticket;
   if (join)
