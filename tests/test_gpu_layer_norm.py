@@ -245,3 +245,23 @@ def test_refusals():
         api.layer_norm_backward(dy, x, mean, rstd, w, accumulate=True)
     with pytest.raises(api.SparcmlError):
         api.layer_norm_backward(dy, x, mean, rstd, w, ws=api.workspace(256, DEV))
+
+
+# (rows, dim): many and few rows of one to 64 packs and of odd widths beside them, which share a
+# warp in different ways; blocks' sums just within and beyond what the last block joins
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,dim", [(1217, 8), (1217, 40), (2049, 45), (1301, 72), (1300, 128),
+                                      (1250, 130), (1219, 249), (1217, 256), (1217, 264),
+                                      (1217, 512), (65, 512), (64, 512), (73, 512), (129, 129),
+                                      (700, 16), (40, 104)])
+def test_rows_that_share_warps_and_sums_that_are_joined(rows, dim, dtype):
+    x, dy, w, b = make(rows, dim, dtype, rows + dim)
+    got = api.layer_norm(x, w, b, 1e-5)
+    check_forward(x, w, b, 1e-5, got)
+    y, mean, rstd = got
+    ws = api.workspace(api.layer_norm_backward_workspace_size(rows, dim), DEV)
+    first = api.layer_norm_backward(dy, x, mean, rstd, w, ws=ws)
+    check_backward(x, dy, w, mean, rstd, first)
+    again = api.layer_norm_backward(dy, x, mean, rstd, w, ws=ws)  # the same workspace, and bits
+    for p, q in zip(first, again):
+        assert torch.equal(p, q)
