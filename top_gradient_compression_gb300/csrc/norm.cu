@@ -193,17 +193,18 @@ struct NormArgs {
 // registers; others (V = 2) through shared memory, where the weights wait in fp32. (Loaded
 // from memory one element at a time, 16384 x 4095 bf16 took 181 us.)
 //
-// What bounds it in 16 bits is arithmetic: 16384 x 4096 bf16 needs 680 of the 700 issue
-// cycles that a row's bytes take when each pass over the row converts it again. With KEEP
-// the fp32 values, and then their deviations, stay in registers.
-template <typename T, typename W, int V, int NV, int LANES, bool KEEP, int MAXT, int MINB>
+// What bounds it in 16 bits is arithmetic: 16384 x 4096 bf16 takes 50 us (0.79 of the copy
+// rate) with 1,830 warp instructions per row, which are 460 issue cycles of the 700 that its
+// bytes take, and 12 warps per SM fill 55 % of the issue slots. Each pass over a row converts it
+// anew: fp32 copies of the row cost as much in registers as they save (48.2 us either way at
+// 8192 x 8192). fp32 rows run at the copy rate less 7 %.
+template <typename T, typename W, int V, int NV, int LANES, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs a) {
   griddep_wait();
   extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ float2 scratch[MAXT >= 64 ? 66 * (MAXT / 64) : 1];
   constexpr bool PACKS = V > 2;
   constexpr int P = V / 2;
-  constexpr bool PK = PACKS && !KEEP;
   Group g = make_group(a.threads, scratch);
   const uint32_t threads = a.threads, groups = blockDim.x / threads, dim = (uint32_t)a.dim;
   const uint32_t t = g.t;
@@ -260,25 +261,19 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
       turn ^= 1u;
       fetch(row + step, turn);
     }
-    F2 kept[KEEP ? NV : 1][P];
     F2 s = f2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
       if (offset<V, LANES>(j, 0) < left) {
         F2 f[P];
         unpack<T, V>(v[j], f);
-        if constexpr (KEEP) {
-#pragma unroll
-          for (int i = 0; i < P; ++i) kept[j][i] = f[i];
-        } else {
-          v[j].forget();
-        }
+        v[j].forget();
 #pragma unroll
         for (int d = 1; d < P; d *= 2) {
 #pragma unroll
-          for (int i = 0; i < P; i += 2 * d) f[i] = add2<PK>(f[i], f[i + d]);
+          for (int i = 0; i < P; i += 2 * d) f[i] = add2<PACKS>(f[i], f[i + d]);
         }
-        s = add2<PK>(s, f[0]);
+        s = add2<PACKS>(s, f[0]);
       }
     const float mean = g.sum(split(s)) * inv;
     s = f2(0.f, 0.f);
@@ -287,15 +282,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
     for (int j = 0; j < NV; ++j)
       if (offset<V, LANES>(j, 0) < left) {
         F2 f[P], q = f2(0.f, 0.f);
-        if constexpr (!KEEP) unpack<T, V>(v[j], f);
+        unpack<T, V>(v[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          f[i] = add2<PK>(KEEP ? kept[KEEP ? j : 0][i] : f[i], minus);
-          if (KEEP) kept[KEEP ? j : 0][i] = f[i];
+          f[i] = add2<PACKS>(f[i], minus);
           if (!PACKS && offset<V, LANES>(j, 1) >= left) f[i] = f2(split(f[i]).x, 0.f);
-          q = fma2<PK>(f[i], f[i], q);
+          q = fma2<PACKS>(f[i], f[i], q);
         }
-        s = add2<PK>(s, q);
+        s = add2<PACKS>(s, q);
         v[j].forget();
       }
     const float var = g.sum(split(s)) * inv;
@@ -320,11 +314,10 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(const NormArgs
           w[0] = pair_at<float, LANES>(affine + first, j, all);
           b[0] = pair_at<float, LANES>(affine + dim + first, j, all);
         }
-        if constexpr (!KEEP) unpack<T, V>(v[j], f);
+        unpack<T, V>(v[j], f);
 #pragma unroll
         for (int i = 0; i < P; ++i)
-          f[i] = fma2<PK>(mul2<PK>(KEEP ? kept[KEEP ? j : 0][i] : add2<PK>(f[i], minus), by), w[i],
-                          b[i]);
+          f[i] = fma2<PACKS>(mul2<PACKS>(add2<PACKS>(f[i], minus), by), w[i], b[i]);
         store_pack<T, V, LANES>(y, j, all, f);
       }
     }
@@ -569,7 +562,7 @@ norm_backward_kernel(const NormGradArgs a) {
     slot = slot + 1 == kSlots ? 0 : slot + 1;
     F2 s0 = f2(0.f, 0.f), s1 = s0;
     const F2 minus = f2(-mean, -mean), by = f2(rstd, rstd);
-    // 16-bit packs keep x - mean and dy w in fp32 for the second pass (84 us against 86 at
+    // 16-bit packs keep x - mean and dy w in fp32 for the second pass (82.6 us against 88.5 at
     // 16384 x 4096); fp32 ones and pairs have no registers left, or nothing to convert.
     constexpr bool KEEP = PACKS && sizeof(T) == 2;
     F2 xc[KEEP ? NV : 1][P], kept[KEEP ? NV : 1][P];
@@ -845,9 +838,9 @@ uint32_t threads_for(uint64_t dim, uint32_t per) {
 constexpr uint32_t kSms = 152;
 
 // `threads` for a row, blocks of at least `block` threads, `fit` of them per SM.
-template <typename T, typename W, int V, int NV, int LANES, bool KEEP, int MAXT, int MINB>
+template <typename T, typename W, int V, int NV, int LANES, int MAXT, int MINB>
 bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, cudaStream_t s) {
-  auto kernel = norm_forward_kernel<T, W, V, NV, LANES, KEEP, MAXT, MINB>;
+  auto kernel = norm_forward_kernel<T, W, V, NV, LANES, MAXT, MINB>;
   a.threads = threads;
   const uint32_t groups = std::max(1u, block / threads);
   size_t smem = 0;
@@ -866,28 +859,28 @@ bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, 
 // Up to 16 packs per lane a warp takes a row alone, which needs no barrier (2048 fp32
 // columns: 53 us against 61 with four warps); longer ones take several. Shorter rows share a
 // warp, four packs per lane: 65536 x 256 bf16 15 us, against 24 with a warp for a row, of
-// which fewer are on their way at a time. For few rows the fewest steps count: 1 x 256 bf16
-// 1.8 us against 2.6.
+// which fewer are on their way at a time. For few rows the fewest steps count: 2432 x 256 bf16
+// 2.0 us against 2.6, 4864 rows 3.3 against 3.0.
 template <typename T, typename W>
 bool forward_packs(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const uint64_t packs = a.dim / V;
-  const bool few = a.rows <= 8 * kSms;
-  if (packs <= 8) return launch_forward<T, W, V, 1, 8, true, 128, 10>(a, 8, 128, 10, s);
-  if (few && packs <= 16) return launch_forward<T, W, V, 1, 16, true, 128, 10>(a, 16, 128, 10, s);
-  if (few && packs <= 32) return launch_forward<T, W, V, 1, 32, true, 128, 10>(a, 32, 128, 10, s);
-  if (packs <= 16) return launch_forward<T, W, V, 2, 8, true, 128, 8>(a, 8, 128, 8, s);
-  if (few && packs <= 64) return launch_forward<T, W, V, 2, 32, true, 128, 8>(a, 32, 128, 8, s);
-  if (packs <= 32) return launch_forward<T, W, V, 4, 8, false, 128, 7>(a, 8, 128, 7, s);
-  if (packs <= 64) return launch_forward<T, W, V, 4, 16, false, 128, 7>(a, 16, 128, 7, s);
-  if (packs <= 128) return launch_forward<T, W, V, 4, 32, false, 128, 7>(a, 32, 128, 7, s);
-  if (packs <= 256) return launch_forward<T, W, V, 8, 32, false, 128, 4>(a, 32, 128, 4, s);
-  if (packs <= 512) return launch_forward<T, W, V, 16, 32, false, 128, 3>(a, 32, 128, 3, s);
+  const bool few = a.rows <= 16 * kSms;
+  if (packs <= 8) return launch_forward<T, W, V, 1, 8, 128, 10>(a, 8, 128, 10, s);
+  if (few && packs <= 16) return launch_forward<T, W, V, 1, 16, 128, 10>(a, 16, 128, 10, s);
+  if (few && packs <= 32) return launch_forward<T, W, V, 1, 32, 128, 10>(a, 32, 128, 10, s);
+  if (packs <= 16) return launch_forward<T, W, V, 2, 8, 128, 8>(a, 8, 128, 8, s);
+  if (few && packs <= 64) return launch_forward<T, W, V, 2, 32, 128, 8>(a, 32, 128, 8, s);
+  if (packs <= 32) return launch_forward<T, W, V, 4, 8, 128, 7>(a, 8, 128, 7, s);
+  if (packs <= 64) return launch_forward<T, W, V, 4, 16, 128, 7>(a, 16, 128, 7, s);
+  if (packs <= 128) return launch_forward<T, W, V, 4, 32, 128, 7>(a, 32, 128, 7, s);
+  if (packs <= 256) return launch_forward<T, W, V, 8, 32, 128, 4>(a, 32, 128, 4, s);
+  if (packs <= 512) return launch_forward<T, W, V, 16, 32, 128, 3>(a, 32, 128, 3, s);
   const uint32_t threads = threads_for(packs, 4);
   if (packs <= 2048)
-    return launch_forward<T, W, V, 4, 32, true, 512, 1>(a, threads, threads,
-                                                        std::max(1u, 640 / threads), s);
-  return launch_forward<T, W, V, 4, 32, false, 1024, 1>(a, threads, threads, 1, s);
+    return launch_forward<T, W, V, 4, 32, 512, 1>(a, threads, threads,
+                                                  std::max(1u, 640 / threads), s);
+  return launch_forward<T, W, V, 4, 32, 1024, 1>(a, threads, threads, 1, s);
 }
 
 // Whole packs: 16-byte aligned rows and weights of the rows' type or fp32. Everything else
@@ -902,11 +895,11 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
   if (sizeof(T) == 2 && vec && a.w_type == SPARCML_F32) return forward_packs<T, float>(a, s);
   if (a.dim <= 512 * 16) {
     const uint32_t threads = threads_for(a.dim, 16);
-    if (a.dim <= 128) return launch_forward<T, T, 2, 8, 8, false, 256, 3>(a, 8, 256, 3, s);
-    if (a.dim <= 256) return launch_forward<T, T, 2, 8, 16, false, 256, 3>(a, 16, 256, 3, s);
+    if (a.dim <= 128) return launch_forward<T, T, 2, 8, 8, 256, 3>(a, 8, 256, 3, s);
+    if (a.dim <= 256) return launch_forward<T, T, 2, 8, 16, 256, 3>(a, 16, 256, 3, s);
     if (threads <= 256)
-      return launch_forward<T, T, 2, 8, 32, false, 256, 3>(a, threads, 256, 3, s);
-    return launch_forward<T, T, 2, 8, 32, false, 512, 1>(a, threads, threads, 2, s);
+      return launch_forward<T, T, 2, 8, 32, 256, 3>(a, threads, 256, 3, s);
+    return launch_forward<T, T, 2, 8, 32, 512, 1>(a, threads, threads, 2, s);
   }
   const bool wide = a.dim % V == 0 && a.x_stride % V == 0 && a.y_stride % V == 0 &&
                     aligned_to(a.x, 16) && aligned_to(a.y, 16);
