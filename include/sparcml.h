@@ -30,8 +30,9 @@
  *     non-blocking collectives). Only sparcml_get_status synchronises.
  *   - Workspace header. The first 256 bytes of every workspace hold the
  *     device status word (bytes 0..3), a ticket word (bytes 16..19) and the
- *     fault-injection word (bytes 32..35, see sparcml_set_fault_injection). Zero the first 64 bytes when
- *     a workspace is created; the library keeps them from then on.
+ *     fault-injection word (bytes 32..35, see
+ *     sparcml_set_fault_injection). Zero the first 64 bytes when a
+ *     workspace is created; the library keeps them from then on.
  *   - Errors. A return value other than SPARCML_OK means nothing was
  *     enqueued (bad argument, workspace too small, capacity too small) or
  *     a CUDA launch failed (SPARCML_ERR_CUDA). Problems found on the device
