@@ -817,8 +817,14 @@ norm_join_kernel(const float* __restrict__ part_w, const float* __restrict__ par
   const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < dim) {
-#pragma unroll 8
-    for (uint32_t p = warp; p < parts; p += 16) s += part[(uint64_t)p * dim + c];
+    for (uint32_t p = warp; p < parts; p += 16 * 20) {
+      float v[20];  // on their way together
+#pragma unroll
+      for (uint32_t k = 0; k < 20; ++k)
+        v[k] = p + 16 * k < parts ? part[(uint64_t)(p + 16 * k) * dim + c] : 0.f;
+#pragma unroll
+      for (uint32_t k = 0; k < 20; ++k) s += v[k];
+    }
   }
   sums[warp][lane] = s;
   __syncthreads();
