@@ -488,9 +488,7 @@ NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
 
 
 # These calls are short: what they check of their arguments costs as much as a launch.
-def _raw_stream(stream, t):
-    if stream is not None:
-        return stream.cuda_stream
+def _raw_stream(t):
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
@@ -558,6 +556,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
     axes may be strided as one). weight and bias: vectors of one type, not
     necessarily x's, or None. Returns (y, mean, rstd), the last two float32 with
     one element per row, for layer_norm_backward. ``out`` may be x."""
+    if stream is not None:  # what the call allocates belongs to the stream that uses it
+        with torch.cuda.stream(stream):
+            return layer_norm(x, weight, bias, eps, out, mean, rstd)
     code = _typed(x, "x")
     rows, dim, xs = _rows(x, "x")
     w, wt = _vector(weight, dim, "weight")
@@ -583,7 +584,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
         _stat(rstd, rows, "rstd")
     r = (_lib._lib or _lib.load()).sparcml_layer_norm(
         x.data_ptr(), code, xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys, mean.data_ptr(),
-        rstd.data_ptr(), _raw_stream(stream, x))
+        rstd.data_ptr(), _raw_stream(x))
     if r:
         _check("sparcml_layer_norm", r)
     return out, mean, rstd
@@ -599,6 +600,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     vectors, for example the layer's slices of a node's flat gradient; with
     ``accumulate`` the sums are added to what the given ones hold. ``dx`` may be
     dy or x."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return layer_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate,
+                                       ws)
     code = _typed(x, "x")
     rows, dim, xs = _rows(x, "x")
     _typed(dy, "dy", x)
@@ -628,7 +633,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     r = (_lib._lib or _lib.load()).sparcml_layer_norm_backward(
         dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt, _stat(mean, rows, "mean"),
         _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dweight.data_ptr(),
-        dbias.data_ptr(), accumulate, ws.data_ptr(), ws.numel(), _raw_stream(stream, x))
+        dbias.data_ptr(), accumulate, ws.data_ptr(), ws.numel(), _raw_stream(x))
     if r:
         _check("sparcml_layer_norm_backward", r)
     return dx, dweight, dbias
@@ -665,6 +670,9 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     Newton-Schulz step per (a, b, c) of ``coeffs``: singular values of g / |g|_F go
     through a s + b s^3 + c s^5 of each step, singular vectors stay. Returns a
     tensor of ``out_dtype`` (bfloat16 or float16)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return orthogonalize(g, coeffs, out, out_dtype, ws)
     batch, m, n, gb, gs = _matrices(g, "g")
     if out is None:
         out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
@@ -676,7 +684,7 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
         ws = workspace(orthogonalize_workspace_size(batch, m, n), g.device)
     _check("sparcml_orthogonalize", _lib.load().sparcml_orthogonalize(
         g.data_ptr(), TYPES[g.dtype], gb, gs, out.data_ptr(), TYPES[out.dtype], ob, os, batch, m,
-        n, c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(stream, g)))
+        n, c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(g)))
     return out
 
 
@@ -691,6 +699,10 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     weight, grad: [m, n] or [batch, m, n], float32, bfloat16 or float16; momentum
     float32. grad is, for example, the layer's slice of a dense reduced gradient.
     ``scale`` defaults to sqrt(max(1, m / n)). Returns (weight, momentum)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return muon_step(weight, grad, momentum, lr, mu, nesterov, weight_decay, scale, coeffs,
+                             ws)
     batch, m, n, wb, wst = _matrices(weight, "weight")
     _, _, _, gb, gs = _matrices(grad, "grad", weight.shape)
     _, _, _, mb, ms = _matrices(momentum, "momentum", weight.shape)
@@ -704,5 +716,5 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     _check("sparcml_muon_step", _lib.load().sparcml_muon_step(
         weight.data_ptr(), TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb,
         gs, momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
-        c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(stream, weight)))
+        c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(weight)))
     return weight, momentum
