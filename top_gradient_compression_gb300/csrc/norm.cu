@@ -186,6 +186,7 @@ struct NormArgs {
   float* mean;
   float* rstd;
   uint32_t threads;  // that share a row
+  bool w_packs;      // long rows: weights of the rows' type, 16-byte aligned
 };
 
 // A persistent grid: while a row is reduced and written, the next one is already on its
@@ -348,15 +349,21 @@ __device__ __forceinline__ void store_floats(T* p, uint64_t c, const float (&f)[
     *reinterpret_cast<uint4*>(p + c) = pack<T, V>(q);
   }
 }
-template <int V>
-__device__ __forceinline__ void weight_floats(const void* w, int32_t type, uint64_t c, float none,
-                                              float (&f)[V]) {
+// Weights at column c; `packs`: they have the rows' type and lie on 16 bytes. (Read one by one,
+// the gradients of 4096 x 16384 bf16 took 205 us, and 183 so.)
+template <typename T, int V>
+__device__ __forceinline__ void weight_floats(const void* w, int32_t type, bool packs, uint64_t c,
+                                              float none, float (&f)[V]) {
+  if (packs && w) {
+    load_floats<T, V>(static_cast<const T*>(w), c, f);
+  } else {
 #pragma unroll
-  for (int i = 0; i < V; ++i) f[i] = w ? load_any(w, type, c + i) : none;
+    for (int i = 0; i < V; ++i) f[i] = w ? load_any(w, type, c + i) : none;
+  }
 }
 
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, V == 8 ? 1 : 2) norm_forward_long_kernel(const NormArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
   Group g = make_group(blockDim.x, scratch);
@@ -389,8 +396,8 @@ __global__ void __launch_bounds__(1024) norm_forward_long_kernel(const NormArgs 
   for (uint64_t c = threadIdx.x * V; c < a.dim; c += blockDim.x * V) {
     float f[V], w[V], b[V];
     load_floats<T, V>(x, c, f);
-    weight_floats<V>(a.w, a.w_type, c, 1.f, w);
-    weight_floats<V>(a.b, a.w_type, c, 0.f, b);
+    weight_floats<T, V>(a.w, a.w_type, a.w_packs, c, 1.f, w);
+    weight_floats<T, V>(a.b, a.w_type, a.w_packs, c, 0.f, b);
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = (f[i] - mean) * rstd * w[i] + b[i];
     store_floats<T, V>(y, c, f);
@@ -413,6 +420,7 @@ struct NormGradArgs {
   float* part_w;  // [gridDim.x][dim] partial sums over the block's rows, or null
   float* part_b;
   uint32_t threads;  // that share a row
+  bool w_packs;      // as in NormArgs
   uint32_t* ticket;  // null: norm_join_kernel joins the blocks' sums
   float* dweight;
   float* dbias;
@@ -738,7 +746,8 @@ norm_backward_kernel(const NormGradArgs a) {
 // Rows too long for a block's registers: dx by re-reading the row, the column sums by
 // norm_columns_kernel.
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(1024, V == 8 ? 1 : 2)
+norm_backward_long_kernel(const NormGradArgs a) {
   griddep_wait();
   __shared__ float2 scratch[66];
   Group g = make_group(blockDim.x, scratch);
@@ -753,7 +762,7 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGrad
     float f[V], d[V], w[V];
     load_floats<T, V>(x, c, f);
     load_floats<T, V>(dy, c, d);
-    weight_floats<V>(a.w, a.w_type, c, 1.f, w);
+    weight_floats<T, V>(a.w, a.w_type, a.w_packs, c, 1.f, w);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       s.x += d[i] * w[i];
@@ -767,7 +776,7 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormGrad
     float f[V], d[V], w[V];
     load_floats<T, V>(x, c, f);
     load_floats<T, V>(dy, c, d);
-    weight_floats<V>(a.w, a.w_type, c, 1.f, w);
+    weight_floats<T, V>(a.w, a.w_type, a.w_packs, c, 1.f, w);
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] = rstd * (d[i] * w[i] - c1 - (f[i] - mean) * rstd * c2);
     store_floats<T, V>(dx, c, f);
@@ -843,6 +852,11 @@ uint32_t threads_for(uint64_t dim, uint32_t per) {
 
 constexpr uint32_t kSms = 152;
 
+// Threads of a block for a row beyond registers: two blocks of an SM, of 1024 threads where 32
+// registers are enough, else (packs of eight) of 512 (4096 x 16384 bf16 161 us against 183 for
+// the gradients with one block of 1024; fp32 229, against 251 with blocks of 512).
+unsigned long_threads(int v, uint64_t rows) { return v == 8 && rows > kSms ? 512 : 1024; }
+
 // `threads` for a row, blocks of at least `block` threads, `fit` of them per SM.
 template <typename T, typename W, int V, int NV, int LANES, int MAXT, int MINB>
 bool launch_forward(NormArgs a, uint32_t threads, uint32_t block, uint32_t fit, cudaStream_t s) {
@@ -892,7 +906,7 @@ bool forward_packs(const NormArgs& a, cudaStream_t s) {
 // Whole packs: 16-byte aligned rows and weights of the rows' type or fp32. Everything else
 // goes element by element.
 template <typename T>
-bool forward_typed(const NormArgs& a, cudaStream_t s) {
+bool forward_typed(NormArgs a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const bool vec = a.dim % V == 0 && a.dim <= 4096 * V && a.x_stride % V == 0 &&
                    a.y_stride % V == 0 && aligned_to(a.x, 16) && aligned_to(a.y, 16) &&
@@ -909,8 +923,9 @@ bool forward_typed(const NormArgs& a, cudaStream_t s) {
   }
   const bool wide = a.dim % V == 0 && a.x_stride % V == 0 && a.y_stride % V == 0 &&
                     aligned_to(a.x, 16) && aligned_to(a.y, 16);
-  if (wide) launch_pdl(norm_forward_long_kernel<T, V>, (unsigned)a.rows, 1024, 0, s, a);
-  else launch_pdl(norm_forward_long_kernel<T, 1>, (unsigned)a.rows, 1024, 0, s, a);
+  a.w_packs = type_of<T>() == a.w_type && aligned_to(a.w, 16) && aligned_to(a.b, 16);
+  launch_pdl(wide ? norm_forward_long_kernel<T, V> : norm_forward_long_kernel<T, 1>,
+             (unsigned)a.rows, long_threads(wide ? V : 1, a.rows), 0, s, a);
   return true;
 }
 
@@ -978,6 +993,7 @@ bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
   const bool ticket = sums && !longer && h.parts * a.dim <= kTicketSums;
   if (ticket) a.ticket = reinterpret_cast<uint32_t*>(ws + kTicketOffset);
   bool ok = true;
+  a.w_packs = same && aligned_to(a.w, 16);
   if (longer) {
     // the column sums first: dx may be written over x or dy
     const unsigned across = (unsigned)((a.dim + 128 * V - 1) / (128 * V));
@@ -986,8 +1002,8 @@ bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
     else if (sums)
       launch_pdl(norm_columns_kernel<T, 1>, dim3((unsigned)((a.dim + 127) / 128), h.parts), 128, 0,
                  s, a);
-    if (vec) launch_pdl(norm_backward_long_kernel<T, V>, (unsigned)a.rows, 1024, 0, s, a);
-    else launch_pdl(norm_backward_long_kernel<T, 1>, (unsigned)a.rows, 1024, 0, s, a);
+    launch_pdl(vec ? norm_backward_long_kernel<T, V> : norm_backward_long_kernel<T, 1>,
+               (unsigned)a.rows, long_threads(vec ? V : 1, a.rows), 0, s, a);
   } else if (packs && same) {
     ok = launch_backward_shape<T, T, V>(a, h, s);
   } else if (sizeof(T) == 2 && packs) {
@@ -1025,7 +1041,7 @@ extern "C" int sparcml_layer_norm(const void* x, int32_t type, int64_t x_stride,
       !aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, we) || !aligned_to(bias, we))
     return SPARCML_ERR_INVALID_ARG;
   const NormArgs a{x,   x_stride, weight,   bias, weight_type, rows,
-                   dim, eps,      y,        rows > 1 ? y_stride : 0, mean, rstd, 0};
+                   dim, eps,      y,        rows > 1 ? y_stride : 0, mean, rstd, 0, false};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool ok = type == SPARCML_F32    ? forward_typed<float>(a, s)
                   : type == SPARCML_BF16 ? forward_typed<__nv_bfloat16>(a, s)
@@ -1064,7 +1080,7 @@ extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, co
   if (rows) {
     const NormGradArgs a{dy,   dy_stride, x,    x_stride, weight, weight_type, mean,
                          rstd, rows,      dim,  dx,       rows > 1 ? dx_stride : 0,
-                         nullptr, nullptr, 0,   nullptr,  dweight, dbias, accumulate};
+                         nullptr, nullptr, 0,   false, nullptr, dweight, dbias, accumulate};
     uint8_t* w = static_cast<uint8_t*>(ws);
     const bool ok = type == SPARCML_F32    ? backward_typed<float>(a, sums, w, s)
                     : type == SPARCML_BF16 ? backward_typed<__nv_bfloat16>(a, sums, w, s)
