@@ -1439,6 +1439,11 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
   if (batch < 0 || batch > 65535 || m < 1 || n < 1 || m > (1u << 24) || n > (1u << 24) ||
       std::min(m, n) > 32768)
     return false;
+  if (batch == 0) {  // nothing to shape: a workspace of a header, and no launch
+    q = Plan{};
+    q.bytes = 256;
+    return true;
+  }
   q.batch = batch;
   q.m = m;
   q.n = n;
@@ -1473,7 +1478,7 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
       Product& p = q.product[c][i];
       p = shape_product(some, i < 2 ? q.k : m, i < 2 ? q.k : n, i == 0 ? q.l : q.k, i < 2, q.pair,
                         width[i], i == 0, batch, &t);
-      if (batch && !p.items) return false;
+      if (!p.items) return false;
       p.b0 = (uint32_t)b0;
       if (p.splits > 1) {
         p.part0 = (uint32_t)parts;
@@ -1486,7 +1491,7 @@ bool make_plan(int32_t batch, uint64_t m, uint64_t n, Plan& q) {
     // S in few parts, which one block adds up; then a block per matrix; then q(S) X
     const uint64_t blocks = ceil_div(q.l, 64);
     const uint32_t splits = (uint32_t)std::max<uint64_t>(
-        1, std::min({(uint64_t)16, blocks / 4, kSms / std::max<uint64_t>(1, q.batch)}));
+        1, std::min({(uint64_t)16, blocks / 4, kSms / q.batch}));
     for (uint32_t c = 0; c < q.chains; ++c) {
       const uint64_t some = q.chains == 1 ? batch : c ? batch / 2 : (batch + 1) / 2;
       double t;
