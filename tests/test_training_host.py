@@ -30,3 +30,20 @@ def test_an_empty_batch_of_any_size(m, n):
     # sizes out of range are refused without matrices too
     assert lib.sparcml_orthogonalize_workspace_size(0, 0, n) == 0
     assert lib.sparcml_orthogonalize_workspace_size(0, m, (1 << 24) + 1) == 0
+
+
+def test_statistics_off_their_alignment_are_refused():
+    """mean and rstd two bytes past a float would be misaligned accesses on the device."""
+    lib = _lib.load()
+    forward = [FAKE, 0, 16, FAKE, FAKE, 0, 4, 16, 1e-5, FAKE, 16, FAKE, FAKE, None]
+    ws = lib.sparcml_layer_norm_backward_workspace_size(4, 16)
+    backward = [FAKE, 16, FAKE, 16, 1, FAKE, 0, FAKE, FAKE, 4, 16, FAKE, 16, FAKE, FAKE, 0, FAKE,
+                ws, None]
+    for i in (11, 12):
+        a = list(forward)
+        a[i] = FAKE + 2
+        assert lib.sparcml_layer_norm(*a) == 1
+    for i in (7, 8):
+        a = list(backward)
+        a[i] = FAKE + 2
+        assert lib.sparcml_layer_norm_backward(*a) == 1

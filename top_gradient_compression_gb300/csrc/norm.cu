@@ -1038,7 +1038,8 @@ extern "C" int sparcml_layer_norm(const void* x, int32_t type, int64_t x_stride,
   if (rows == 0) return SPARCML_OK;
   const size_t e = type_bytes(type), we = type_bytes(weight_type);
   if (!x || !y || !mean || !rstd || x_stride < 0 || (rows > 1 && y_stride < (int64_t)dim) ||
-      !aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, we) || !aligned_to(bias, we))
+      !aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(weight, we) || !aligned_to(bias, we) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
     return SPARCML_ERR_INVALID_ARG;
   const NormArgs a{x,   x_stride, weight,   bias, weight_type, rows,
                    dim, eps,      y,        rows > 1 ? y_stride : 0, mean, rstd, 0, false};
@@ -1071,7 +1072,8 @@ extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, co
   if (rows > 0 &&
       (!dy || !x || !mean || !rstd || !dx || dy_stride < 0 || x_stride < 0 ||
        (rows > 1 && dx_stride < (int64_t)dim) || !aligned_to(x, e) || !aligned_to(dy, e) ||
-       !aligned_to(dx, e) || !aligned_to(weight, type_bytes(weight_type))))
+       !aligned_to(dx, e) || !aligned_to(weight, type_bytes(weight_type)) ||
+       !aligned_to(mean, 4) || !aligned_to(rstd, 4)))
     return SPARCML_ERR_INVALID_ARG;
   if (ws_bytes < sparcml_layer_norm_backward_workspace_size(rows, dim))
     return SPARCML_ERR_WORKSPACE;
