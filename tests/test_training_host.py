@@ -5,6 +5,7 @@ import sys
 
 import numpy as np
 import pytest
+import torch
 
 from top_gradient_compression_gb300 import _lib, api
 
@@ -47,3 +48,95 @@ def test_statistics_off_their_alignment_are_refused():
         a = list(backward)
         a[i] = FAKE + 2
         assert lib.sparcml_layer_norm_backward(*a) == 1
+
+
+class Placed(torch.Tensor):
+    """A host tensor that says it lies on a GPU."""
+    index = 0
+    is_cuda = True
+
+    def get_device(self):
+        return self.index
+
+
+def placed(*shape, index=0, dtype=torch.float32):
+    t = torch.Tensor._make_subclass(Placed, torch.zeros(*shape, dtype=dtype))
+    t.index = index
+    return t
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """Entry points that record the current device and the stream they were given."""
+    made, current = [], [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *_):
+            current[0] = self.before
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: made.append((name, current[0], a[-1])) or 0
+    monkeypatch.setattr(api._lib, "_lib", Library())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    return made
+
+
+def operands(name):
+    """Each operand of a call, as keywords."""
+    wide = {"dtype": torch.bfloat16}
+    return {
+        "layer_norm": {"x": placed(4, 8), "weight": placed(8), "bias": placed(8),
+                       "out": placed(4, 8), "mean": placed(4), "rstd": placed(4)},
+        "layer_norm_backward": {"dy": placed(4, 8), "x": placed(4, 8), "mean": placed(4),
+                                "rstd": placed(4), "weight": placed(8), "dx": placed(4, 8),
+                                "dweight": placed(8), "dbias": placed(8),
+                                "ws": placed(4096, dtype=torch.uint8)},
+        "orthogonalize": {"g": placed(4, 8), "out": placed(4, 8, **wide),
+                          "ws": placed(4096, dtype=torch.uint8)},
+        "muon_step": {"weight": placed(4, 8), "grad": placed(4, 8), "momentum": placed(4, 8),
+                      "ws": placed(4096, dtype=torch.uint8)},
+    }[name]
+
+
+OPERATORS = ["layer_norm", "layer_norm_backward", "orthogonalize", "muon_step"]
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_operands_on_two_devices_are_refused(name, calls):
+    extra = {"lr": 0.1} if name == "muon_step" else {}
+    for odd in operands(name):
+        args = operands(name)
+        args[odd].index = 1
+        with pytest.raises(ValueError, match="one device"):
+            getattr(api, name)(**args, **extra)
+    assert calls == []
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_the_operands_device_is_current_during_the_call(name, calls):
+    extra = {"lr": 0.1} if name == "muon_step" else {}
+    for index in (0, 1):
+        args = operands(name)
+        for t in args.values():
+            t.index = index
+        getattr(api, name)(**args, **extra)
+    assert calls == [(f"sparcml_{name}", i, 1000 + i) for i in (0, 1)]
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_a_stream_of_another_device_is_refused(name, calls):
+    class Stream:
+        device = torch.device("cuda", 1)
+    extra = {"lr": 0.1} if name == "muon_step" else {}
+    with pytest.raises(ValueError, match="stream"):
+        getattr(api, name)(**operands(name), **extra, stream=Stream())
+    assert calls == []

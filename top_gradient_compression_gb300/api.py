@@ -488,8 +488,39 @@ NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
 
 
 # These calls are short: what they check of their arguments costs as much as a launch.
-def _raw_stream(t):
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _raw_stream(device: int):
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _one_device(first, *others) -> int:
+    """The index of the device that all the tensors (None: not given) are on."""
+    device = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors of a call must be on one device, cuda:{device} here")
+    return device
+
+
+def _call(name: str, device: int, *args):
+    """Enqueue an entry point on the device's current stream. The library launches on the
+    current device, so another one is made current for the call."""
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return _call(name, device, *args)
+    r = getattr(_lib._lib or _lib.load(), name)(*args, _raw_stream(device))
+    if r:
+        _check(name, r)
+
+
+def _on(stream, t):
+    """Context in which `stream` is the current one of t's device."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and stream.device.index != t.get_device():
+        raise ValueError(f"the stream is one of {stream.device}, the tensors of {t.device}")
+    return torch.cuda.stream(stream)
 
 
 def _typed(t, name: str, like=None):
@@ -557,7 +588,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
     necessarily x's, or None. Returns (y, mean, rstd), the last two float32 with
     one element per row, for layer_norm_backward. ``out`` may be x."""
     if stream is not None:  # what the call allocates belongs to the stream that uses it
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return layer_norm(x, weight, bias, eps, out, mean, rstd)
     code = _typed(x, "x")
     rows, dim, xs = _rows(x, "x")
@@ -582,11 +613,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
         rstd = torch.empty_like(mean)
     else:
         _stat(rstd, rows, "rstd")
-    r = (_lib._lib or _lib.load()).sparcml_layer_norm(
-        x.data_ptr(), code, xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys, mean.data_ptr(),
-        rstd.data_ptr(), _raw_stream(x))
-    if r:
-        _check("sparcml_layer_norm", r)
+    device = _one_device(x, weight, bias, out, mean, rstd)
+    _call("sparcml_layer_norm", device, x.data_ptr(), code, xs, w, b, wt, rows, dim, eps,
+          out.data_ptr(), ys, mean.data_ptr(), rstd.data_ptr())
     return out, mean, rstd
 
 
@@ -601,7 +630,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     ``accumulate`` the sums are added to what the given ones hold. ``dx`` may be
     dy or x."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return layer_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate,
                                        ws)
     code = _typed(x, "x")
@@ -611,6 +640,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     if dy.shape != x.shape:
         raise ValueError("dy and x shapes differ")
     w, wt = _vector(weight, dim, "weight")
+    mp, rp = _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd")
     if dx is None:
         dx, os = _new_like(x), dim
     else:
@@ -630,12 +660,11 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
         _stat(dbias, dim, "dbias")
     if ws is None:
         ws = workspace(layer_norm_backward_workspace_size(rows, dim), x.device)
-    r = (_lib._lib or _lib.load()).sparcml_layer_norm_backward(
-        dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt, _stat(mean, rows, "mean"),
-        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dweight.data_ptr(),
-        dbias.data_ptr(), accumulate, ws.data_ptr(), ws.numel(), _raw_stream(x))
-    if r:
-        _check("sparcml_layer_norm_backward", r)
+    device = _one_device(x, dy, mean, rstd, weight, dx, dweight, dbias, ws)
+    _call("sparcml_layer_norm_backward", device, dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt,
+          mp, rp, rows, dim, dx.data_ptr(), os, dweight.data_ptr(), dbias.data_ptr(), accumulate,
+          ws.data_ptr(),
+          ws.numel())
     return dx, dweight, dbias
 
 
@@ -671,7 +700,7 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     through a s + b s^3 + c s^5 of each step, singular vectors stay. Returns a
     tensor of ``out_dtype`` (bfloat16 or float16)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, g):
             return orthogonalize(g, coeffs, out, out_dtype, ws)
     batch, m, n, gb, gs = _matrices(g, "g")
     if out is None:
@@ -682,9 +711,9 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     c = _coeffs(coeffs)
     if ws is None:
         ws = workspace(orthogonalize_workspace_size(batch, m, n), g.device)
-    _check("sparcml_orthogonalize", _lib.load().sparcml_orthogonalize(
-        g.data_ptr(), TYPES[g.dtype], gb, gs, out.data_ptr(), TYPES[out.dtype], ob, os, batch, m,
-        n, c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(g)))
+    _call("sparcml_orthogonalize", _one_device(g, out, ws), g.data_ptr(), TYPES[g.dtype], gb, gs,
+          out.data_ptr(), TYPES[out.dtype], ob, os, batch, m, n, c.ctypes.data, c.shape[0], ws.data_ptr(),
+          ws.numel())
     return out
 
 
@@ -700,7 +729,7 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     float32. grad is, for example, the layer's slice of a dense reduced gradient.
     ``scale`` defaults to sqrt(max(1, m / n)). Returns (weight, momentum)."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, weight):
             return muon_step(weight, grad, momentum, lr, mu, nesterov, weight_decay, scale, coeffs,
                              ws)
     batch, m, n, wb, wst = _matrices(weight, "weight")
@@ -713,8 +742,9 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     c = _coeffs(coeffs)
     if ws is None:
         ws = workspace(orthogonalize_workspace_size(batch, m, n), weight.device)
-    _check("sparcml_muon_step", _lib.load().sparcml_muon_step(
-        weight.data_ptr(), TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb,
-        gs, momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
-        c.ctypes.data, c.shape[0], ws.data_ptr(), ws.numel(), _raw_stream(weight)))
+    _call("sparcml_muon_step", _one_device(weight, grad, momentum, ws), weight.data_ptr(),
+          TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb, gs,
+          momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
+          c.ctypes.data, c.shape[0], ws.data_ptr(),
+          ws.numel())
     return weight, momentum
