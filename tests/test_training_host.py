@@ -92,7 +92,7 @@ def calls(monkeypatch):
 
 def operands(name):
     """Each operand of a call, as keywords."""
-    wide = {"dtype": torch.bfloat16}
+    f32, wide = torch.float32, {"dtype": torch.bfloat16}
     return {
         "layer_norm": {"x": placed(4, 8), "weight": placed(8), "bias": placed(8),
                        "out": placed(4, 8), "mean": placed(4), "rstd": placed(4)},
@@ -101,7 +101,7 @@ def operands(name):
                                 "dweight": placed(8), "dbias": placed(8),
                                 "ws": placed(4096, dtype=torch.uint8)},
         "orthogonalize": {"g": placed(4, 8), "out": placed(4, 8, **wide),
-                          "ws": placed(4096, dtype=torch.uint8)},
+                          "ws": placed(4096, dtype=f32)},
         "muon_step": {"weight": placed(4, 8), "grad": placed(4, 8), "momentum": placed(4, 8),
                       "ws": placed(4096, dtype=torch.uint8)},
     }[name]
@@ -139,4 +139,17 @@ def test_a_stream_of_another_device_is_refused(name, calls):
     extra = {"lr": 0.1} if name == "muon_step" else {}
     with pytest.raises(ValueError, match="stream"):
         getattr(api, name)(**operands(name), **extra, stream=Stream())
+    assert calls == []
+
+
+@pytest.mark.parametrize("name", OPERATORS[1:])
+def test_a_workspace_has_to_be_contiguous_device_memory(name, calls):
+    extra = {"lr": 0.1} if name == "muon_step" else {}
+    args = operands(name)
+    args["ws"] = torch.zeros(4096, dtype=torch.uint8)
+    with pytest.raises(TypeError, match="ws"):
+        getattr(api, name)(**args, **extra)
+    args["ws"] = placed(1, dtype=torch.uint8).expand(4096)  # one byte
+    with pytest.raises(ValueError, match="ws"):
+        getattr(api, name)(**args, **extra)
     assert calls == []

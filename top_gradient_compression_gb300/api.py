@@ -523,6 +523,15 @@ def _on(stream, t):
     return torch.cuda.stream(stream)
 
 
+def _space(ws):
+    """(pointer, bytes) of a workspace."""
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda:
+        raise TypeError("ws must be a CUDA tensor")
+    if not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _typed(t, name: str, like=None):
     """The type code of a CUDA tensor of one of the three types (of `like`'s)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -660,11 +669,11 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
         _stat(dbias, dim, "dbias")
     if ws is None:
         ws = workspace(layer_norm_backward_workspace_size(rows, dim), x.device)
+    space = _space(ws)
     device = _one_device(x, dy, mean, rstd, weight, dx, dweight, dbias, ws)
     _call("sparcml_layer_norm_backward", device, dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt,
           mp, rp, rows, dim, dx.data_ptr(), os, dweight.data_ptr(), dbias.data_ptr(), accumulate,
-          ws.data_ptr(),
-          ws.numel())
+          *space)
     return dx, dweight, dbias
 
 
@@ -711,9 +720,9 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     c = _coeffs(coeffs)
     if ws is None:
         ws = workspace(orthogonalize_workspace_size(batch, m, n), g.device)
+    space = _space(ws)
     _call("sparcml_orthogonalize", _one_device(g, out, ws), g.data_ptr(), TYPES[g.dtype], gb, gs,
-          out.data_ptr(), TYPES[out.dtype], ob, os, batch, m, n, c.ctypes.data, c.shape[0], ws.data_ptr(),
-          ws.numel())
+          out.data_ptr(), TYPES[out.dtype], ob, os, batch, m, n, c.ctypes.data, c.shape[0], *space)
     return out
 
 
@@ -742,9 +751,9 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     c = _coeffs(coeffs)
     if ws is None:
         ws = workspace(orthogonalize_workspace_size(batch, m, n), weight.device)
+    space = _space(ws)
     _call("sparcml_muon_step", _one_device(weight, grad, momentum, ws), weight.data_ptr(),
           TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb, gs,
           momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
-          c.ctypes.data, c.shape[0], ws.data_ptr(),
-          ws.numel())
+          c.ctypes.data, c.shape[0], *space)
     return weight, momentum
