@@ -520,6 +520,17 @@ int sparcml_orthogonalize(const void* g, int32_t g_type, int64_t g_batch_stride,
                           uint64_t m, uint64_t n, const float* coeffs, int32_t steps, void* ws,
                           size_t ws_bytes, void* stream);
 
+/* How the general path lays out the products of such a call, so that tests can tell which of
+ * its ways a size takes (host only). Writes
+ *   plan[0]     SMs that share a tile: 1 or 2
+ *   plan[1]     chains of matrices that do not wait for each other: 1 or 2
+ *   plan[2..4]  columns of a tile of S = X X', of P = b S + c S S, of P X
+ *   plan[5]     parts of S's summed axis, joined in order when there are several
+ *   plan[6]     bit i: some tiles of product i are done in halves
+ *   plan[7]     1 where the smaller side is at most 64; there, coefficients that multiply small
+ *               singular values 1,800 times at most take a path of their own instead. */
+int sparcml_orthogonalize_plan(int32_t batch, uint64_t m, uint64_t n, int32_t* plan);
+
 /* One weight step with orthogonalised momentum:
  *     M <- mu M + G;   U = G + mu M if nesterov, else M
  *     W <- W (1 - lr weight_decay) - lr scale O(U)

@@ -9,6 +9,8 @@ import torch
 
 from top_gradient_compression_gb300 import _lib, api
 
+from training_cases import TALL, WAYS
+
 FAKE = 1 << 20  # non-null, aligned, never dereferenced
 COEFFS = np.array(api.NEWTON_SCHULZ, np.float32)
 
@@ -153,3 +155,16 @@ def test_a_workspace_has_to_be_contiguous_device_memory(name, calls):
     with pytest.raises(ValueError, match="ws"):
         getattr(api, name)(**args, **extra)
     assert calls == []
+
+
+def test_sizes_take_the_ways_that_the_gpu_tests_are_for():
+    for (batch, m, n), way in WAYS.items():
+        for size, want in (((batch, m, n), way),
+                           ((batch, n, m), TALL.get((batch, m, n), way))):
+            p = api.orthogonalize_plan(*size)
+            got = (p["pair"], p["chains"], p["widths"], p["splits"] > 1, p["halves"])
+            assert got == want and not p["small"], size
+    assert api.orthogonalize_plan(1, 64, 4096)["small"]
+    for bad in ((0, 64, 64), (1, 0, 4), (-1, 4, 4)):
+        with pytest.raises(api.SparcmlError):
+            api.orthogonalize_plan(*bad)

@@ -85,6 +85,7 @@ SIGNATURES = {
                                               C.c_int32, vp, vp, C.c_uint64, C.c_uint64, vp,
                                               C.c_int64, vp, vp, C.c_int32, vp, C.c_size_t, vp]),
     "sparcml_orthogonalize_workspace_size": (C.c_size_t, [C.c_int32, C.c_uint64, C.c_uint64]),
+    "sparcml_orthogonalize_plan": (C.c_int, [C.c_int32, C.c_uint64, C.c_uint64, vp]),
     "sparcml_orthogonalize": (C.c_int, [vp, C.c_int32, C.c_int64, C.c_int64, vp, C.c_int32,
                                         C.c_int64, C.c_int64, C.c_int32, C.c_uint64, C.c_uint64,
                                         vp, C.c_int32, vp, C.c_size_t, vp]),

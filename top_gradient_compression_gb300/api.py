@@ -702,6 +702,16 @@ def orthogonalize_workspace_size(batch: int, m: int, n: int) -> int:
     return int(_lib.load().sparcml_orthogonalize_workspace_size(batch, m, n))
 
 
+def orthogonalize_plan(batch: int, m: int, n: int) -> dict:
+    """How the products of a call of this size are laid out (include/sparcml.h): `pair` SMs
+    per tile, `chains`, `widths` of the three products' tiles, `splits` of S's summed axis,
+    which products have `halves` of tiles, and whether a side is `small`."""
+    p = (C.c_int32 * 8)()
+    _check("sparcml_orthogonalize_plan", _lib.load().sparcml_orthogonalize_plan(batch, m, n, p))
+    return {"pair": p[0], "chains": p[1], "widths": tuple(p[2:5]), "splits": p[5],
+            "halves": tuple(i for i in range(3) if p[6] >> i & 1), "small": bool(p[7])}
+
+
 def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, ws=None,
                   stream=None):
     """Orthogonalises g, [m, n] or [batch, m, n] (float32, bfloat16 or float16), by one

@@ -1730,6 +1730,22 @@ extern "C" size_t sparcml_orthogonalize_workspace_size(int32_t batch, uint64_t m
   return make_plan(batch, m, n, q) ? q.bytes : 0;
 }
 
+extern "C" int sparcml_orthogonalize_plan(int32_t batch, uint64_t m, uint64_t n, int32_t* plan) {
+  Plan q;
+  if (!plan || batch < 1 || !make_plan(batch, m, n, q)) return SPARCML_ERR_INVALID_ARG;
+  plan[0] = (int32_t)q.pair;
+  plan[1] = (int32_t)q.chains;
+  plan[5] = (int32_t)q.product[0][0].splits;
+  plan[6] = 0;
+  for (int i = 0; i < 3; ++i) {
+    plan[2 + i] = (int32_t)q.product[0][i].n;
+    for (uint32_t c = 0; c < q.chains; ++c)
+      if (q.product[c][i].whole < q.product[c][i].items) plan[6] |= 1 << i;
+  }
+  plan[7] = q.k <= kSmall;
+  return SPARCML_OK;
+}
+
 extern "C" int sparcml_orthogonalize(const void* g, int32_t g_type, int64_t g_batch_stride,
                                      int64_t g_stride, void* out, int32_t out_type,
                                      int64_t out_batch_stride, int64_t out_stride, int32_t batch,
