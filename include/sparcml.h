@@ -85,7 +85,10 @@ uint64_t sparcml_launch_count(void);
  *     thousand polls (milliseconds) instead of about two million. The
  *     waiting tiles record SPARCML_ERR_TIMEOUT in the status word and carry
  *     on; the outputs of such a call are unspecified, but every memory
- *     access stays in bounds and the call always completes.
+ *     access stays in bounds and the call always completes. In later
+ *     orthogonalisations and weight steps the first block withholds a
+ *     product, and the waits for it give up after 2 to 8 milliseconds
+ *     instead of 2 to 8 seconds, with the same consequences.
  *   mode 0: clears it (later calls are normal again).
  * The word stays as written across calls. A workspace whose first 64 bytes
  * were zeroed when it was created has no fault armed.

@@ -92,7 +92,8 @@ INJECT_WITHHOLD_FIRST = 1
 def set_fault_injection(ws: torch.Tensor, mode: int, stream=None):
     """Arm (mode INJECT_WITHHOLD_FIRST) or clear (0) the workspace's fault
     injection: later reduce / SSAR calls with ws see their look-back waits run
-    out and record SPARCML_ERR_TIMEOUT (include/sparcml.h)."""
+    out, and orthogonalisations and weight steps those for a product, and record
+    SPARCML_ERR_TIMEOUT (include/sparcml.h)."""
     _check("sparcml_set_fault_injection",
            _lib.load().sparcml_set_fault_injection(ws.data_ptr(), int(mode), _stream(stream)))
 

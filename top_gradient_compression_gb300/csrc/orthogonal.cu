@@ -260,6 +260,7 @@ struct StepArgs {
   int64_t out_batch, out_stride;
   float alpha, keep;  // weight: W <- keep W + alpha X; else X
   int32_t* status;
+  const uint32_t* inject;  // the workspace's fault-injection word
 };
 
 enum Kind { kGram, kPart, kJoin, kSolve, kPoly, kApply, kLast };
@@ -371,7 +372,7 @@ struct Worker {
   uint32_t buf;                            // this writer's two buffers
   uint32_t rank, cluster, clusters, tmem;
   bool leader;                             // the lane that issues for its warp
-  volatile uint32_t* gave_up;
+  Waits* waits;
   uint32_t stage = 0, phase = 0;  // next operand stage and its turn's parity (loader, issuer)
   uint32_t acc = 0;       // accumulators used so far (issuer, writers)
   uint32_t in_phase = 0;  // bit s: parity of buffer s's next load
@@ -399,7 +400,7 @@ __device__ __forceinline__ bool load_operands(Worker<CG>& w, const Product& p,
     uint32_t rep = 0;
     for (uint32_t i = t.first; i < t.last; w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.gave_up)) return false;
+      if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.waits)) return false;
       // of a small side's operands hi hi, hi lo, lo hi; else hi hi alone
       const CUtensorMap* const ua = SMALL && rep == 2 ? ma_lo : ma;
       const CUtensorMap* const ub = SMALL && rep == 1 ? mb_lo : mb;
@@ -429,13 +430,13 @@ __device__ __forceinline__ bool issue_products(Worker<CG>& w, const Product& p, 
     if (t.none) continue;
     const uint32_t idesc = mma_desc(128 * CG, t.n, a_mn, b_mn);
     const uint32_t a = w.acc & 1u;
-    if (!mbar_wait_warp(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.gave_up)) return false;
+    if (!mbar_wait_warp(w.acc_empty + 8 * a, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
     tmem_fence_after();
     const uint32_t d = w.tmem + a * kAccColumns;
     const uint32_t blocks = (t.last - t.first) * (SMALL ? 3 : 1);
     for (uint32_t i = 0; i < blocks; ++i, w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.gave_up)) return false;
+      if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.waits)) return false;
       tmem_fence_after();
       if (w.leader) {
         const uint32_t sa = w.ring + s * w.stage_bytes, sb = sa + 128 * 128;
@@ -465,6 +466,22 @@ __device__ __forceinline__ void store_box(uint32_t box, __half* out, uint64_t pi
 #pragma unroll
   for (uint32_t q = 0; q < 32; q += 8, o += 8 * pitch)
     if (row0 + q + r < rows) *reinterpret_cast<uint4*>(o) = lds128(box + box_at(q + r, c));
+}
+
+// Before a block leaves that gave up, or whose partner did: until the operands have landed. A
+// pair's loads all report to the first block, in one phase per stage for both blocks; where the
+// two stopped at different stages (`apart`) some phases never complete, and the loads get their
+// time instead.
+__device__ __noinline__ void land_operands(uint32_t full, uint32_t stages, uint32_t stage,
+                                           uint32_t phase, bool apart) {
+  if (apart) {
+    const uint64_t end = global_ns() + 1000ull * kLandUs;
+    while (global_ns() < end) __nanosleep(1000);
+    return;
+  }
+  Waits alone = {0, kLandUs};
+  for (uint32_t s = 0; s < stages; ++s)
+    mbar_wait(full + 8 * s, s < stage ? phase : phase ^ 1u, &alone);
 }
 
 // What becomes of a product's entry, for all products alike:
@@ -620,6 +637,15 @@ __device__ __forceinline__ void store_result(const StepArgs& a, uint32_t box, ui
   __syncwarp();
 }
 
+// Before a writer gives up: until buffer s's load, of parity `phase`'s bit s, has landed, for
+// each bit s of `slots`. (Not inlined, as all that only a wait beyond its first tries needs:
+// beside the loops it cost 8 x 1024 x 1024 3 %.)
+__device__ __noinline__ void land(uint32_t in_bar, uint32_t phase, uint32_t slots) {
+  Waits alone = {0, kLandUs};
+  for (uint32_t s = 0; s < 2; ++s)
+    if (slots >> s & 1u) mbar_wait_warp(in_bar + 8 * s, (phase >> s) & 1u, &alone);
+}
+
 template <int CG, bool SMALL>
 __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, const Maps& m, const Product& p,
                               int kind, uint32_t step, Tile t) {
@@ -686,7 +712,10 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
     float other = column_diag(0);
 
     const uint32_t acc = w.acc & 1u;
-    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.gave_up)) return false;
+    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) {
+      if (reads && count) land(w.in_bar, w.in_phase, kind == kLast ? 1u : 1u << (turn0 & 1u));
+      return false;
+    }
     tmem_fence_after();
     const uint32_t src = w.tmem + acc * kAccColumns + (quarter << 21) + tile_col;
     if (kind == kPart) count = t.n / 64;
@@ -698,8 +727,10 @@ __device__ __forceinline__ bool write_results(Worker<CG>& w, const StepArgs& a, 
       if (reads && kind != kLast && q + 1 < count) fetch(q + 1);
       const float next = column_diag(q + 1);
       if (reads) {
-        if (!mbar_wait_warp(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.gave_up))
+        if (!mbar_wait_warp(w.in_bar + 8 * slot, (w.in_phase >> slot) & 1u, w.waits)) {
+          land(w.in_bar, w.in_phase, kind != kLast && q + 1 < count ? 3u : 1u << slot);
           return false;
+        }
         w.in_phase ^= 1u << slot;
       }
       const bool on_diag = !pairs && row0 == col;
@@ -1075,24 +1106,29 @@ __device__ void split_input(const StepArgs& a) {
 }
 
 // Whether a counter of arrivals has come to `want`; what the arriving blocks wrote before
-// is then visible. The wait ends after a few seconds at worst.
-__device__ __forceinline__ bool wait_count(const uint32_t* count, uint32_t want,
-                                           volatile uint32_t* gave_up) {
-  uint64_t end = 0;
+// is then visible. wait_count ends after four times the waits' limit at worst.
+__device__ __forceinline__ bool count_is(const uint32_t* count, uint32_t want) {
+  uint32_t now;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(count) : "memory");
+  return (int32_t)(now - want) >= 0;
+}
+__device__ __noinline__ bool wait_count_long(const uint32_t* count, uint32_t want, Waits* waits) {
+  const uint64_t end = global_ns() + 4000ull * waits->limit_us;
   for (uint32_t polls = 1;; ++polls) {
-    uint32_t now;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(now) : "l"(count) : "memory");
-    if ((int32_t)(now - want) >= 0) return true;
+    if (count_is(count, want)) return true;
     if ((polls & 63u) == 0) {
-      const uint64_t t = global_ns();
-      if (end == 0) end = t + 4 * kWaitNs;
-      if (*gave_up != 0) return false;
-      if (t > end) {
-        *gave_up = 1;
+      if (waits->gave_up != 0) return false;
+      if (global_ns() > end) {
+        waits->gave_up = 1;
         return false;
       }
     }
   }
+}
+__device__ __forceinline__ bool wait_count(const uint32_t* count, uint32_t want, Waits* waits) {
+  for (uint32_t i = 0; i < 64; ++i)
+    if (count_is(count, want)) return true;
+  return wait_count_long(count, want, waits);
 }
 __device__ __forceinline__ void add_count(uint32_t* count) {
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
@@ -1132,8 +1168,12 @@ template <int CG, bool SMALL>
 __global__ void __launch_bounds__(kThreads, 1)
 steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a) {
   extern __shared__ uint8_t raw[];
-  __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 6 + 2 * kWriters];
-  __shared__ uint32_t tmem_slot, gave_up, written[2];
+  __shared__ alignas(8) uint64_t bars[2 * kMaxStages + 7 + 2 * kWriters];
+  __shared__ uint32_t tmem_slot, written[2];
+  __shared__ Waits waits;
+  // What the other block of a pair says at the end: whether it gave up, and the next stage that
+  // it would have loaded.
+  __shared__ uint32_t partner[2];
   griddep_wait();
   const uint32_t warp = threadIdx.x >> 5;
   Worker<CG> w;
@@ -1146,13 +1186,13 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   w.empty = w.full + 8 * kMaxStages;
   w.acc_full = w.empty + 8 * kMaxStages;
   w.acc_empty = w.acc_full + 16;
-  const uint32_t ready = w.acc_empty + 16;
+  const uint32_t ready = w.acc_empty + 16, finished = ready + 16 + 16 * kWriters;
   w.in_bar = ready + 16 + 16 * (warp % kWriters);
   w.buf = w.ring + kRingBytes + (warp % kWriters) * 2 * kStageBuf;
   w.rank = CG == 1 ? 0 : cluster_rank();
   w.cluster = blockIdx.x / CG;
   w.clusters = gridDim.x / CG;
-  w.gave_up = &gave_up;
+  w.waits = &waits;
   w.lead_full = CG == 1 ? w.full : cluster_addr(w.full, 0);
   w.lead_acc_empty = cluster_addr(w.acc_empty, 0);
   w.leader = elect_one();
@@ -1160,7 +1200,9 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   if (threadIdx.x < sizeof(Maps) / sizeof(CUtensorMap))
     tma_prefetch_map(reinterpret_cast<const CUtensorMap*>(&m) + threadIdx.x);
   if (threadIdx.x == 0) {
-    gave_up = written[0] = written[1] = 0;
+    waits.gave_up = written[0] = written[1] = 0;
+    waits.limit_us = kWaitUs;
+    partner[0] = partner[1] = 0;
     for (uint32_t s = 0; s < kMaxStages; ++s) {
       mbar_init(w.full + 8 * s, 1);
       mbar_init(w.empty + 8 * s, 1);
@@ -1171,6 +1213,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       mbar_init(ready + 8 * s, 1);
     }
     for (uint32_t s = 0; s < 2 * kWriters; ++s) mbar_init(ready + 16 + 8 * s, 1);
+    mbar_init(finished, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWriters) tmem_alloc<CG>(smem_addr(&tmem_slot), 2 * kAccColumns);
@@ -1181,12 +1224,14 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
   w.tmem = tmem_slot;
 
   const bool tall = a.tall != 0;
+  const bool armed = threadIdx.x == 0 && injected(a.inject);
   split_input(a);
   proxy_fence_global();
   __syncthreads();
   if (threadIdx.x == 0) {
+    if (armed) waits.limit_us = kInjectWaitUs;
     add_count(a.g.turns);
-    wait_count(a.g.turns, gridDim.x, &gave_up);
+    wait_count(a.g.turns, gridDim.x, &waits);
   }
   __syncthreads();
 
@@ -1209,7 +1254,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       pin(t);
       bool come = true;
       if (w.leader) {
-        come = wait_count(turns + chain * kTurnStep, need, &gave_up);
+        come = wait_count(turns + chain * kTurnStep, need, &waits);
         if (come) mbar_arrive(ready + 8 * (told & 1u));
       }
       if (!__all_sync(0xffffffffu, come)) return false;
@@ -1232,10 +1277,14 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       return load_operands<CG, SMALL>(w, p, ma, mb, ma_lo, mb_lo, a_major(kind), b_major(kind), t);
     });
   } else if (warp == kWriters + 1) {
+    // An injected fault: the first block (or pair) withholds its products from one on that adds
+    // to something, so that full stages, loads of writers and the grid's counters are waited for.
+    const bool withhold = w.cluster == 0 && waits.limit_us == kInjectWaitUs;
     if (w.rank == 0)
       in_order<CG, SMALL>(a, [&](uint32_t, int kind, const Product& p, uint32_t, uint32_t) {
         const uint32_t item = w.first_item(p);
         if (kind == kJoin || kind == kSolve || item >= p.items) return true;
+        if (withhold && (SMALL || kind == kPoly)) return false;
         Tile t = tile_of<CG>(p, item);
         pin(t);
         return issue_products<CG, SMALL>(w, p, a_major(kind), b_major(kind), t);
@@ -1247,7 +1296,7 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       Tile t = {};
       if (kind != kJoin && kind != kSolve) t = tile_of<CG>(p, item);
       pin(t);
-      if (!mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &gave_up)) return false;
+      if (!mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &waits)) return false;
       ++told;
       if (kind == kJoin) {
         join_parts<CG>(a, p);
@@ -1283,25 +1332,33 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
       return true;
     });
   }
-  __syncthreads();
-  if (gave_up) {
-    // Nothing of this block may still be in flight when its memory goes: wait, again
-    // with a limit, for the loads and products that were begun.
-    volatile uint32_t alone = 0;
-    if (warp == kWriters && w.leader && w.rank == 0)  // a pair's loads all report to rank 0
-      for (uint32_t i = 0; i < w.stages; ++i, w.next_stage())
-        mbar_wait(w.full + 8 * w.stage, w.phase ^ 1u, &alone);
-    if (warp == kWriters + 1 && w.leader && w.rank == 0) {
-      const uint32_t bar = w.acc_full + 8 * (w.acc & 1u);
-      mma_commit<CG>(bar);
-      mbar_wait(bar, (w.acc >> 1) & 1u, &alone);
+  tmem_fence_before();
+  __syncthreads();  // now it is settled whether this block gave up
+  if constexpr (CG > 1) {
+    const uint32_t to = cluster_addr(smem_addr(partner), w.rank ^ 1u);
+    if (threadIdx.x == 0) store_cluster(to, waits.gave_up);
+    if (warp == kWriters && w.leader) store_cluster(to + 4, 2 * w.stage + w.phase);
+    __syncwarp();
+    cluster_sync();
+  }
+  if (waits.gave_up || (CG > 1 && partner[0])) {
+    // Nothing may still be in flight when the shared and tensor memory go: wait, again with a
+    // limit, for the loads and products that were begun. (Writers have waited for their own.)
+    if (warp == kWriters && w.leader) {
+      const bool apart = CG > 1 && partner[1] != 2 * w.stage + w.phase;
+      if (w.rank == 0 || apart) land_operands(w.full, w.stages, w.stage, w.phase, apart);
+    }
+    if (warp == kWriters + 1 && w.leader) {
+      // arrives, in both blocks of a pair, once all products have completed
+      Waits alone = {0, kWaitUs};
+      if (w.rank == 0) mma_commit<CG>(finished);
+      mbar_wait(finished, 0, &alone);
     }
     __syncwarp();
     if (threadIdx.x == 0) set_status(a.status, SPARCML_ERR_TIMEOUT);
+    __syncthreads();
+    if constexpr (CG > 1) cluster_sync();
   }
-  tmem_fence_before();
-  __syncthreads();
-  if (CG > 1) cluster_sync();
   tmem_fence_after();
   if (warp == kWriters) tmem_free<CG>(w.tmem, 2 * kAccColumns);
 }
@@ -1691,6 +1748,7 @@ int run_steps(GatherArgs g, const Plan& q, const Target& to, const float* coeffs
   a.alpha = to.alpha;
   a.keep = to.keep;
   a.status = reinterpret_cast<int32_t*>(w);
+  a.inject = reinterpret_cast<const uint32_t*>(w + kInjectOffset);
   launch_pdl(gather_norm_kernel, dim3(q.blocks, (unsigned)q.batch), 256, 0, s, g);
   if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
   const int r = small       ? launch_steps<1, true>(m, a, s)

@@ -48,6 +48,9 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -71,31 +74,40 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-// How long a wait inside a kernel may last (the longest legitimate one is a
-// tile's product, well under a millisecond).
-constexpr uint64_t kWaitNs = 2000000000ull;
+// How long a wait inside a kernel may last, in microseconds, normally and while a fault is
+// injected. The longest legitimate one is for the last tile of another block: 2^18 blocks of 64
+// of the summed axis, at 512 cycles each, take 70 ms.
+constexpr uint32_t kWaitUs = 2000000, kInjectWaitUs = 2000;
+// What a copy that nothing holds up is given to land before a block leaves.
+constexpr uint32_t kLandUs = 20000;
 
-// Waits until the barrier's phase `parity` has completed. False, with *gave_up
-// set, when that takes longer than kWaitNs or another warp gave up meanwhile.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
-                                          volatile uint32_t* gave_up) {
-  for (uint32_t i = 0; i < 64; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t end = global_ns() + kWaitNs;
+// What a block's waits share: whether one of them has run out, and their limit.
+struct Waits {
+  volatile uint32_t gave_up, limit_us;
+};
+
+// Waits until the barrier's phase `parity` has completed. False, with gave_up
+// set, when that takes longer than the limit or another warp gave up meanwhile.
+__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, Waits* waits) {
+  const uint64_t end = global_ns() + 1000ull * waits->limit_us;
   while (!mbar_try_wait(bar, parity)) {
-    if (*gave_up != 0) return false;
+    if (waits->gave_up != 0) return false;
     if (global_ns() > end) {
-      *gave_up = 1;
+      waits->gave_up = 1;
       return false;
     }
   }
   return true;
 }
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Waits* waits) {
+  for (uint32_t i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_long(bar, parity, waits);
+}
 
 // The same for a whole warp: true only if every lane's wait ended well.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity,
-                                               volatile uint32_t* gave_up) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, gave_up));
+__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, Waits* waits) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, waits));
 }
 
 // Tiled loads. With a pair of blocks (CG = 2) the barrier may be the other block's.
