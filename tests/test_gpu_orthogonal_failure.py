@@ -42,6 +42,13 @@ def test_a_withheld_product(batch, m, n):
     times_out_and_recovers(batch, m, n)
 
 
+# one matrix, more matrices than blocks, two chains whose solves and products alternate
+@pytest.mark.parametrize("batch,m,n", [(1, 48, 300), (1, 64, 16384), (1, 20_001, 40),
+                                       (2, 64, 9000), (7, 33, 2000), (333, 24, 40)])
+def test_a_withheld_product_of_a_small_side(batch, m, n):
+    times_out_and_recovers(batch, m, n)
+
+
 def test_a_weight_step_and_a_fresh_workspace():
     g, w, mom = (gradient((200, 300), s) for s in (1, 2, 3))
     size = api.orthogonalize_workspace_size(1, 200, 300)

@@ -1290,14 +1290,21 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
         return issue_products<CG, SMALL>(w, p, a_major(kind), b_major(kind), t);
       });
   } else {
+    // A writer that gives up leaves, but for solve_one, whose barriers take all of a block's
+    // writers and have no limit: there it still works along, on whatever is there.
+    bool lost = false;
     in_order<CG, SMALL>(a, [&](uint32_t step, int kind, const Product& p, uint32_t chain, uint32_t) {
       const uint32_t item = w.first_item(p);
       if (kind == kJoin ? blockIdx.x >= join_units<CG>(p) : item >= p.items) return true;
       Tile t = {};
       if (kind != kJoin && kind != kSolve) t = tile_of<CG>(p, item);
       pin(t);
-      if (!mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &waits)) return false;
+      if (!lost && !mbar_wait_warp(ready + 8 * (told & 1u), (told >> 1) & 1u, &waits)) {
+        if (!SMALL) return false;
+        lost = true;
+      }
       ++told;
+      if (SMALL && lost && kind != kSolve) return true;
       if (kind == kJoin) {
         join_parts<CG>(a, p);
       } else if (SMALL && kind == kSolve) {
@@ -1310,9 +1317,10 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
           else solve_one<2, 1>(a, gram.splits, p.b0 + i, tile, room);
         }
       } else if (!write_results<CG, SMALL>(w, a, m, p, kind, step, t)) {
-        return false;
+        lost = true;
+        return SMALL;
       }
-      if (kind == kLast) return true;
+      if (lost || kind == kLast) return true;
       // what was written is read by asynchronous copies; the last of the block's writers
       // reports to the grid
       proxy_fence_global();
