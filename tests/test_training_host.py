@@ -57,6 +57,10 @@ class Placed(torch.Tensor):
     index = 0
     is_cuda = True
 
+    @property
+    def device(self):
+        return torch.device("cuda", self.index)
+
     def get_device(self):
         return self.index
 
@@ -73,8 +77,8 @@ def calls(monkeypatch):
     made, current = [], [0]
 
     class Device:
-        def __init__(self, index):
-            self.index = index
+        def __init__(self, device):
+            self.index = device.index
 
         def __enter__(self):
             self.before, current[0] = current[0], self.index
@@ -86,6 +90,8 @@ def calls(monkeypatch):
         def __getattr__(self, name):
             return lambda *a: made.append((name, current[0], a[-1])) or 0
     monkeypatch.setattr(api._lib, "_lib", Library())
+    monkeypatch.setattr(api, "_several", None)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
     monkeypatch.setattr(torch.cuda, "device", Device)

@@ -488,33 +488,28 @@ TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5
 
 
-# These calls are short: what they check of their arguments costs as much as a launch.
-def _raw_stream(device: int):
-    return torch._C._cuda_getCurrentRawStream(device)
+# These calls are short: what they check of their arguments costs as much as a launch. So the
+# operands' devices are looked at only where the process sees several (a microsecond or two).
+_several = None  # whether it does; found out by the first call
 
 
-def _current_device() -> int:
-    return torch._C._cuda_getDevice()
+def _raw_stream(t):
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _one_device(first, *others) -> int:
-    """The index of the device that all the tensors (None: not given) are on."""
+def _elsewhere(first, *others) -> bool:
+    """Whether the operands (None: not given) are on a device that is not the current one, which
+    is the one that the library launches on. All have to be on one."""
+    global _several
+    if _several is None:
+        _several = torch.cuda.device_count() > 1
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        return False  # refused for that later on
     device = first.get_device()
     for t in others:
-        if t is not None and t.get_device() != device:
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != device:
             raise ValueError(f"all tensors of a call must be on one device, cuda:{device} here")
-    return device
-
-
-def _call(name: str, device: int, *args):
-    """Enqueue an entry point on the device's current stream. The library launches on the
-    current device, so another one is made current for the call."""
-    if device != _current_device():
-        with torch.cuda.device(device):
-            return _call(name, device, *args)
-    r = getattr(_lib._lib or _lib.load(), name)(*args, _raw_stream(device))
-    if r:
-        _check(name, r)
+    return device != torch._C._cuda_getDevice()
 
 
 def _on(stream, t):
@@ -600,6 +595,9 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
     if stream is not None:  # what the call allocates belongs to the stream that uses it
         with _on(stream, x):
             return layer_norm(x, weight, bias, eps, out, mean, rstd)
+    if _several is not False and _elsewhere(x, weight, bias, out, mean, rstd):
+        with torch.cuda.device(x.device):
+            return layer_norm(x, weight, bias, eps, out, mean, rstd)
     code = _typed(x, "x")
     rows, dim, xs = _rows(x, "x")
     w, wt = _vector(weight, dim, "weight")
@@ -623,9 +621,11 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out=None, mean=None
         rstd = torch.empty_like(mean)
     else:
         _stat(rstd, rows, "rstd")
-    device = _one_device(x, weight, bias, out, mean, rstd)
-    _call("sparcml_layer_norm", device, x.data_ptr(), code, xs, w, b, wt, rows, dim, eps,
-          out.data_ptr(), ys, mean.data_ptr(), rstd.data_ptr())
+    r = (_lib._lib or _lib.load()).sparcml_layer_norm(
+        x.data_ptr(), code, xs, w, b, wt, rows, dim, eps, out.data_ptr(), ys, mean.data_ptr(),
+        rstd.data_ptr(), _raw_stream(x))
+    if r:
+        _check("sparcml_layer_norm", r)
     return out, mean, rstd
 
 
@@ -643,6 +643,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
         with _on(stream, x):
             return layer_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate,
                                        ws)
+    if _several is not False and _elsewhere(x, dy, mean, rstd, weight, dx, dweight, dbias, ws):
+        with torch.cuda.device(x.device):
+            return layer_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate,
+                                       ws)
     code = _typed(x, "x")
     rows, dim, xs = _rows(x, "x")
     _typed(dy, "dy", x)
@@ -650,7 +654,6 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     if dy.shape != x.shape:
         raise ValueError("dy and x shapes differ")
     w, wt = _vector(weight, dim, "weight")
-    mp, rp = _stat(mean, rows, "mean"), _stat(rstd, rows, "rstd")
     if dx is None:
         dx, os = _new_like(x), dim
     else:
@@ -670,11 +673,13 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
         _stat(dbias, dim, "dbias")
     if ws is None:
         ws = workspace(layer_norm_backward_workspace_size(rows, dim), x.device)
-    space = _space(ws)
-    device = _one_device(x, dy, mean, rstd, weight, dx, dweight, dbias, ws)
-    _call("sparcml_layer_norm_backward", device, dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt,
-          mp, rp, rows, dim, dx.data_ptr(), os, dweight.data_ptr(), dbias.data_ptr(), accumulate,
-          *space)
+    wp, wn = _space(ws)
+    r = (_lib._lib or _lib.load()).sparcml_layer_norm_backward(
+        dy.data_ptr(), ds, x.data_ptr(), xs, code, w, wt, _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dweight.data_ptr(),
+        dbias.data_ptr(), accumulate, wp, wn, _raw_stream(x))
+    if r:
+        _check("sparcml_layer_norm_backward", r)
     return dx, dweight, dbias
 
 
@@ -722,6 +727,9 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     if stream is not None:
         with _on(stream, g):
             return orthogonalize(g, coeffs, out, out_dtype, ws)
+    if _several is not False and _elsewhere(g, out, ws):
+        with torch.cuda.device(g.device):
+            return orthogonalize(g, coeffs, out, out_dtype, ws)
     batch, m, n, gb, gs = _matrices(g, "g")
     if out is None:
         out = torch.empty(g.shape, dtype=out_dtype, device=g.device)
@@ -731,9 +739,10 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     c = _coeffs(coeffs)
     if ws is None:
         ws = workspace(orthogonalize_workspace_size(batch, m, n), g.device)
-    space = _space(ws)
-    _call("sparcml_orthogonalize", _one_device(g, out, ws), g.data_ptr(), TYPES[g.dtype], gb, gs,
-          out.data_ptr(), TYPES[out.dtype], ob, os, batch, m, n, c.ctypes.data, c.shape[0], *space)
+    wp, wn = _space(ws)
+    _check("sparcml_orthogonalize", _lib.load().sparcml_orthogonalize(
+        g.data_ptr(), TYPES[g.dtype], gb, gs, out.data_ptr(), TYPES[out.dtype], ob, os, batch, m,
+        n, c.ctypes.data, c.shape[0], wp, wn, _raw_stream(g)))
     return out
 
 
@@ -752,6 +761,10 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
         with _on(stream, weight):
             return muon_step(weight, grad, momentum, lr, mu, nesterov, weight_decay, scale, coeffs,
                              ws)
+    if _several is not False and _elsewhere(weight, grad, momentum, ws):
+        with torch.cuda.device(weight.device):
+            return muon_step(weight, grad, momentum, lr, mu, nesterov, weight_decay, scale, coeffs,
+                             ws)
     batch, m, n, wb, wst = _matrices(weight, "weight")
     _, _, _, gb, gs = _matrices(grad, "grad", weight.shape)
     _, _, _, mb, ms = _matrices(momentum, "momentum", weight.shape)
@@ -762,9 +775,9 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
     c = _coeffs(coeffs)
     if ws is None:
         ws = workspace(orthogonalize_workspace_size(batch, m, n), weight.device)
-    space = _space(ws)
-    _call("sparcml_muon_step", _one_device(weight, grad, momentum, ws), weight.data_ptr(),
-          TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb, gs,
-          momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
-          c.ctypes.data, c.shape[0], *space)
+    wp, wn = _space(ws)
+    _check("sparcml_muon_step", _lib.load().sparcml_muon_step(
+        weight.data_ptr(), TYPES[weight.dtype], wb, wst, grad.data_ptr(), TYPES[grad.dtype], gb,
+        gs, momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
+        c.ctypes.data, c.shape[0], wp, wn, _raw_stream(weight)))
     return weight, momentum
