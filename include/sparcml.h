@@ -511,6 +511,10 @@ int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x
  *           below 24 (the usual sets stay below 1.3 and 9): the products take
  *           fp16 operands scaled by powers of two, and larger values overflow
  *           to inf, then NaN.
+ *   Accuracy: X is kept as a pair of fp16, the products read its upper half, and S and P
+ *           but for their diagonals are fp16; sums are fp32. Against 64 bits five usual
+ *           steps come out 0.01 to 0.14 % off in the Frobenius norm, before the result's
+ *           own rounding (with bf16's: 0.17 to 0.22 %). There is no form with more.
  *   ws      >= sparcml_orthogonalize_workspace_size(batch, m, n) bytes,
  *           256-byte aligned; 0 for sizes out of range (batch 0 .. 65535,
  *           m and n 1 .. 2^24, the smaller of them at most 32768). A wait
@@ -537,7 +541,9 @@ int sparcml_orthogonalize_plan(int32_t batch, uint64_t m, uint64_t n, int32_t* p
 /* One weight step with orthogonalised momentum:
  *     M <- mu M + G;   U = G + mu M if nesterov, else M
  *     W <- W (1 - lr weight_decay) - lr scale O(U)
- * with O as sparcml_orthogonalize computes it, in fp32 up to W's rounding.
+ * with O as sparcml_orthogonalize computes it, but not rounded to 16 bits: so the change of a
+ * weight is 0.01 to 0.14 % off, which for an fp32 weight is more than its own rounding (1e-6 of
+ * a weight that moves by 0.2 %). Momentum, norm and the sum with W are fp32.
  *   weight    type w_type; grad type g_type; momentum fp32. Strides as above,
  *             those of weight and momentum as for out; the three must not
  *             overlap. Workspace as for

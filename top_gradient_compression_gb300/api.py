@@ -723,7 +723,8 @@ def orthogonalize(g, coeffs=NEWTON_SCHULZ, out=None, out_dtype=torch.bfloat16, w
     """Orthogonalises g, [m, n] or [batch, m, n] (float32, bfloat16 or float16), by one
     Newton-Schulz step per (a, b, c) of ``coeffs``: singular values of g / |g|_F go
     through a s + b s^3 + c s^5 of each step, singular vectors stay. Returns a
-    tensor of ``out_dtype`` (bfloat16 or float16)."""
+    tensor of ``out_dtype`` (bfloat16 or float16). The products take fp16 operands: before
+    that rounding the result is 0.01 to 0.14 % off (include/sparcml.h)."""
     if stream is not None:
         with _on(stream, g):
             return orthogonalize(g, coeffs, out, out_dtype, ws)
@@ -756,7 +757,8 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
 
     weight, grad: [m, n] or [batch, m, n], float32, bfloat16 or float16; momentum
     float32. grad is, for example, the layer's slice of a dense reduced gradient.
-    ``scale`` defaults to sqrt(max(1, m / n)). Returns (weight, momentum)."""
+    ``scale`` defaults to sqrt(max(1, m / n)). Returns (weight, momentum). The products take
+    fp16 operands: the change of a weight is 0.01 to 0.14 % off, of an fp32 one too."""
     if stream is not None:
         with _on(stream, weight):
             return muon_step(weight, grad, momentum, lr, mu, nesterov, weight_decay, scale, coeffs,

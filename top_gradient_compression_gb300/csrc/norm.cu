@@ -194,9 +194,10 @@ struct NormArgs {
 // registers; others (V = 2) through shared memory, where the weights wait in fp32. (Loaded
 // from memory one element at a time, 16384 x 4095 bf16 took 181 us.)
 //
-// What bounds it in 16 bits is arithmetic: 16384 x 4096 bf16 takes 50 us (0.79 of the copy
-// rate) with 1,830 warp instructions per row, which are 460 issue cycles of the 700 that its
-// bytes take, and 12 warps per SM fill 55 % of the issue slots. Each pass over a row converts it
+// In 16 bits no unit is busy all the time: 16384 x 4096 bf16 takes 49 us (0.81 of the copy rate),
+// with 55 % of the issue slots filled and no pipe above 50 %, by the 12 warps of an SM that 160
+// registers a thread allow (1,830 warp instructions per row, 460 issue cycles of the 700 that its
+// bytes take); more warps would hide more latency. Each pass over a row converts it
 // anew: fp32 copies of the row cost as much in registers as they save (48.2 us either way at
 // 8192 x 8192). fp32 rows run at the copy rate less 7 %.
 template <typename T, typename W, int V, int NV, int LANES, int MAXT, int MINB>
@@ -949,8 +950,12 @@ BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
           (uint32_t)std::max<uint64_t>(1, std::min((rows + groups - 1) / groups, most))};
 }
 // Up to this many partial sums the last block to finish joins them: that saves the host a
-// launch (2 us of the 18 that a small call takes) and costs 0.8 to 1.7 us more on the device
-// (64 x 512 fp32 5.7 against 4.0 us). From 8 K sums on it costs more than 3.
+// launch, 2 us of a call that waits for the host (10.7 against 12.7 at every size up to 16 K
+// sums), and costs time on the device, ticket against launch: 450 sums 4.5 and 3.6 us, 2 K 5.3 and
+// 3.8, 4 K 5.8 to 6.6 and 4.1, 6 K 7.1 and 4.0, 8 K 7.0 to 9.1 and 4.2, 16 K 9.6 to 11.8 and 4.3,
+// 32 K 14 to 26 and 4.2 to 7.6. So it is worth it to a caller who is bound by launches up to where
+// the device loses as much as the host gains, and to no other; rows of more than 1,024 columns
+// lose it earlier (3 x 2048 fp32 9.0 and 4.4).
 constexpr uint64_t kTicketSums = 4 * 1024;
 
 template <typename T, typename W, int V, int LANES, int MAXT, int MINB>

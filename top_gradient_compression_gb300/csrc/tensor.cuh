@@ -55,9 +55,11 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Arrive at a barrier of any block of the cluster. Relaxed: it tells of tensor memory that
-// has been read, which tcgen05.fence orders, and of no other memory (with release it waits
-// a microsecond for the warp's stores).
+// Arrive at a barrier of any block of the cluster. Relaxed: it tells that tensor memory has been
+// read and may be written over, and of no other memory. What it rests on: tcgen05.wait::ld has
+// returned, so the values are in registers, before the tcgen05.fence on this side; the fence on
+// the other side comes after its wait. (With release it also waits for the warp's stores: 103 us
+// against 93 at 256 x 256, 335 against 317 at 8 x 1024 x 1024.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
