@@ -556,6 +556,146 @@ int sparcml_muon_step(void* weight, int32_t w_type, int64_t w_batch_stride, int6
                       const float* coeffs, int32_t steps, void* ws, size_t ws_bytes,
                       void* stream);
 
+/* ------------------------------------------------------------------------
+ * Operators that make a node's gradient: activations kept in 8 bits between
+ * the forward and the backward pass, the linear layers of experts, and the
+ * norm and rotation of queries and keys. Types, strides and determinism as
+ * for the operators of the training step above. */
+
+/* Activations in 8 bits. For every group of 128 columns of a row there is an
+ * exponent byte b, for every element a code c, and they stand for
+ *     c 2^(b - 127),
+ * with c = rint(x 2^(127 - b)), |c| <= 127, and b the least for which the
+ * group's largest |x| gives less than 127.5, but 1 <= b <= 248, and for
+ * SPARCML_F16 103 <= b <= 136: every c 2^(b - 127) is then a number of the
+ * type, and of bf16. What is above 127.5 of the largest step (65,280 in fp16,
+ * 2^128 (1 - 2^-8) else) becomes 127 of it. A group with a NaN or an inf has
+ * b = 255 and comes back as NaN.
+ *   x, y      type `type`, strides x_stride >= 0 and y_stride >= dim.
+ *   codes     [rows], codes_stride bytes apart: a multiple of 16, at least
+ *             dim rounded up to one; 16-byte aligned. checkpoint8 writes zeros
+ *             up to that multiple of 16.
+ *   exponents [rows], exponents_stride bytes apart, at least ceil(dim / 128).
+ *   rows 0 .. 2^31 - 1 (0: nothing is done), dim 1 .. 2^31 - 1.
+ * restore8 takes any b and any c, and rounds where its type does not hold the
+ * product. */
+#define SPARCML_GROUP8 128
+int sparcml_checkpoint8(const void* x, int32_t type, int64_t x_stride, uint64_t rows,
+                        uint64_t dim, int8_t* codes, int64_t codes_stride, uint8_t* exponents,
+                        int64_t exponents_stride, void* stream);
+int sparcml_restore8(const int8_t* codes, int64_t codes_stride, const uint8_t* exponents,
+                     int64_t exponents_stride, uint64_t rows, uint64_t dim, void* y,
+                     int32_t type, int64_t y_stride, void* stream);
+
+/* sparcml_layer_norm_backward with x kept in 8 bits: the same arguments, with
+ * codes and exponents in place of x, and its workspace. dx may be dy itself. */
+int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type,
+                                 const int8_t* codes, int64_t codes_stride,
+                                 const uint8_t* exponents, int64_t exponents_stride,
+                                 const void* weight, int32_t weight_type, const float* mean,
+                                 const float* rstd, uint64_t rows, uint64_t dim, void* dx,
+                                 int64_t dx_stride, float* dweight, float* dbias,
+                                 int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Linear layers of `experts` experts, of which each has a run of the rows:
+ * expert e the rows offsets[e] .. offsets[e + 1) and the matrix W_e [n][k].
+ *     y[r] = x[r] W_e'        dx[r] = dy[r] W_e
+ *     dW_e = sum over its rows of dy[r]' x[r]
+ * Sums are fp32, results rounded once. A NaN or an inf of a row reaches that
+ * row's result and its own expert's dW alone.
+ *   x, dx [rows][k], y, dy [rows][n], weight: type `type`, SPARCML_BF16 or
+ *             SPARCML_F16 (the tensor cores have no fp32 product); strides as
+ *             for layer norm, those of the matrices weight_batch_stride and
+ *             weight_stride >= 0.
+ *   offsets   DEVICE int32 [experts + 1], rising, from 0 at least to rows at
+ *             most; or NULL for one expert with all rows. Rows of no expert
+ *             are neither read nor written. An offset out of order or range
+ *             is taken as the nearest one that is not, and
+ *             SPARCML_ERR_BAD_STREAM recorded in the workspace.
+ *   dweight   fp32, dweight_stride >= k and dweight_batch_stride between rows
+ *             and matrices, no two elements at one address: for example the
+ *             layer's slice of a node's flat gradient, at any offset. An
+ *             expert without rows gets +0. accumulate != 0 adds to what it
+ *             holds.
+ *   dweight8  takes x in 8 bits; `type` is then dy's.
+ *   experts 1 .. 1024, rows 0 .. 2^31 - 1, n and k 1 .. 2^24.
+ *   ws        >= sparcml_expert_linear_workspace_size(...) bytes, 256-byte
+ *             aligned, for all of them. aligned != 0: every operand starts on 16
+ *             bytes, and its rows and matrices follow one another or are
+ *             multiples of 8 elements apart. What is not so (or has rows of
+ *             another length than a multiple of 8) is copied into the workspace
+ *             first. Bounded waits as for sparcml_orthogonalize.
+ * Outputs may not overlap inputs. */
+size_t sparcml_expert_linear_workspace_size(uint64_t rows, uint32_t experts, uint64_t n,
+                                            uint64_t k, int32_t aligned);
+int sparcml_expert_linear(const void* x, int64_t x_stride, const void* weight,
+                          int64_t weight_batch_stride, int64_t weight_stride, int32_t type,
+                          const int32_t* offsets, uint32_t experts, uint64_t rows, uint64_t n,
+                          uint64_t k, void* y, int64_t y_stride, void* ws, size_t ws_bytes,
+                          void* stream);
+int sparcml_expert_linear_dx(const void* dy, int64_t dy_stride, const void* weight,
+                             int64_t weight_batch_stride, int64_t weight_stride, int32_t type,
+                             const int32_t* offsets, uint32_t experts, uint64_t rows, uint64_t n,
+                             uint64_t k, void* dx, int64_t dx_stride, void* ws, size_t ws_bytes,
+                             void* stream);
+int sparcml_expert_linear_dweight(const void* dy, int64_t dy_stride, const void* x,
+                                  int64_t x_stride, int32_t type, const int32_t* offsets,
+                                  uint32_t experts, uint64_t rows, uint64_t n, uint64_t k,
+                                  float* dweight, int64_t dweight_batch_stride,
+                                  int64_t dweight_stride, int32_t accumulate, void* ws,
+                                  size_t ws_bytes, void* stream);
+int sparcml_expert_linear_dweight8(const void* dy, int64_t dy_stride, int32_t type,
+                                   const int8_t* codes, int64_t codes_stride,
+                                   const uint8_t* exponents, int64_t exponents_stride,
+                                   const int32_t* offsets, uint32_t experts, uint64_t rows,
+                                   uint64_t n, uint64_t k, float* dweight,
+                                   int64_t dweight_batch_stride, int64_t dweight_stride,
+                                   int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
+/* Queries and keys, each head of `dim` elements normed and then turned by its
+ * token's position p:
+ *     u = x w / sqrt(sum(x^2) / dim + eps)
+ *     pair i < turned / 2 of u: (u0, u1) <- (u0 c - u1 s, u0 s + u1 c),
+ *     c = cos(p freqs[i]), s = sin(p freqs[i])
+ * pairs being the elements i and turned / 2 + i, or, `interleaved`, 2 i and
+ * 2 i + 1. Elements from `turned` on are normed only.
+ *   q, k, q_out, k_out  [tokens][heads][dim] of type `type`, any strides >= 0
+ *             between tokens and heads, unit stride within a head; no two
+ *             elements of an output at one address. Outputs may be the inputs
+ *             themselves (same strides). q_heads or k_heads may be 0.
+ *   positions device int32 or, positions_int64, int64 [tokens], any value: the
+ *             angle is exact to 2^-33 of a turn and 2^-64 |p|.
+ *   freqs     device fp32 [turned / 2], radians per position, finite.
+ *   q_weight, k_weight  [dim] of type weight_type, each may be NULL (ones).
+ *   tokens 0 .. 2^31 - 1, dim 1 .. 512, turned even, 0 .. dim, heads 0 .. 65535. */
+int sparcml_head_norm_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                             uint32_t q_heads, const void* k, int64_t k_token_stride,
+                             int64_t k_head_stride, uint32_t k_heads, int32_t type,
+                             uint64_t tokens, uint32_t dim, const void* positions,
+                             int32_t positions_int64, const float* freqs, uint32_t turned,
+                             int32_t interleaved, const void* q_weight, const void* k_weight,
+                             int32_t weight_type, float eps, void* q_out,
+                             int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                             int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
+
+/* Its gradients from dq and dk, those of its results, and its inputs q and k:
+ * q_out and k_out get the inputs' gradients (each may be dq and dk themselves),
+ * q_dweight and k_dweight fp32 [dim], each may be NULL, the weights', summed
+ * over tokens and heads; accumulate != 0 adds to what they hold.
+ *   ws        >= the workspace size for it, 256-byte aligned. */
+size_t sparcml_head_norm_rotary_backward_workspace_size(uint64_t tokens, uint32_t q_heads,
+                                                        uint32_t k_heads, uint32_t dim);
+int sparcml_head_norm_rotary_backward(
+    const void* dq, int64_t dq_token_stride, int64_t dq_head_stride, const void* dk,
+    int64_t dk_token_stride, int64_t dk_head_stride, const void* q, int64_t q_token_stride,
+    int64_t q_head_stride, uint32_t q_heads, const void* k, int64_t k_token_stride,
+    int64_t k_head_stride, uint32_t k_heads, int32_t type, uint64_t tokens, uint32_t dim,
+    const void* positions, int32_t positions_int64, const float* freqs, uint32_t turned,
+    int32_t interleaved, const void* q_weight, const void* k_weight, int32_t weight_type,
+    float eps, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+    int64_t k_out_token_stride, int64_t k_out_head_stride, float* q_dweight, float* k_dweight,
+    int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -93,6 +93,42 @@ SIGNATURES = {
                                     C.c_int64, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32,
                                     C.c_uint64, C.c_uint64, C.c_float, C.c_int32, C.c_float,
                                     C.c_float, C.c_float, vp, C.c_int32, vp, C.c_size_t, vp]),
+    "sparcml_checkpoint8": (C.c_int, [vp, C.c_int32, C.c_int64, C.c_uint64, C.c_uint64, vp,
+                                      C.c_int64, vp, C.c_int64, vp]),
+    "sparcml_restore8": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_uint64, C.c_uint64, vp,
+                                   C.c_int32, C.c_int64, vp]),
+    "sparcml_layer_norm_backward8": (C.c_int, [vp, C.c_int64, C.c_int32, vp, C.c_int64, vp,
+                                               C.c_int64, vp, C.c_int32, vp, vp, C.c_uint64,
+                                               C.c_uint64, vp, C.c_int64, vp, vp, C.c_int32, vp,
+                                               C.c_size_t, vp]),
+    "sparcml_head_norm_rotary": (C.c_int, [vp, C.c_int64, C.c_int64, C.c_uint32, vp, C.c_int64,
+                                           C.c_int64, C.c_uint32, C.c_int32, C.c_uint64,
+                                           C.c_uint32, vp, C.c_int32, vp, C.c_uint32, C.c_int32,
+                                           vp, vp, C.c_int32, C.c_float, vp, C.c_int64, C.c_int64,
+                                           vp, C.c_int64, C.c_int64, vp]),
+    "sparcml_head_norm_rotary_backward_workspace_size": (C.c_size_t, [C.c_uint64, C.c_uint32,
+                                                                      C.c_uint32, C.c_uint32]),
+    "sparcml_head_norm_rotary_backward": (C.c_int, [
+        vp, C.c_int64, C.c_int64, vp, C.c_int64, C.c_int64, vp, C.c_int64, C.c_int64, C.c_uint32,
+        vp, C.c_int64, C.c_int64, C.c_uint32, C.c_int32, C.c_uint64, C.c_uint32, vp, C.c_int32, vp,
+        C.c_uint32, C.c_int32, vp, vp, C.c_int32, C.c_float, vp, C.c_int64, C.c_int64, vp,
+        C.c_int64, C.c_int64, vp, vp, C.c_int32, vp, C.c_size_t, vp]),
+    "sparcml_expert_linear_workspace_size": (C.c_size_t, [C.c_uint64, C.c_uint32, C.c_uint64,
+                                                          C.c_uint64, C.c_int32]),
+    "sparcml_expert_linear": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,
+                                        C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp,
+                                        C.c_int64, vp, C.c_size_t, vp]),
+    "sparcml_expert_linear_dx": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,
+                                           C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp,
+                                           C.c_int64, vp, C.c_size_t, vp]),
+    "sparcml_expert_linear_dweight": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int32, vp,
+                                                C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp,
+                                                C.c_int64, C.c_int64, C.c_int32, vp, C.c_size_t,
+                                                vp]),
+    "sparcml_expert_linear_dweight8": (C.c_int, [vp, C.c_int64, C.c_int32, vp, C.c_int64, vp,
+                                                 C.c_int64, vp, C.c_uint32, C.c_uint64, C.c_uint64,
+                                                 C.c_uint64, vp, C.c_int64, C.c_int64, C.c_int32,
+                                                 vp, C.c_size_t, vp]),
 }
 
 

@@ -638,7 +638,10 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, dx=None, dweight=None, d
     """Gradients of layer_norm: (dx, dweight, dbias). dweight and dbias are float32
     vectors, for example the layer's slices of a node's flat gradient; with
     ``accumulate`` the sums are added to what the given ones hold. ``dx`` may be
-    dy or x."""
+    dy or x. x may be a Checkpoint8 of it."""
+    if isinstance(x, Checkpoint8):
+        return _layer_norm_backward8(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate, ws,
+                                     stream)
     if stream is not None:
         with _on(stream, x):
             return layer_norm_backward(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate,
@@ -783,3 +786,424 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
         gs, momentum.data_ptr(), mb, ms, batch, m, n, mu, int(nesterov), lr, weight_decay, scale,
         c.ctypes.data, c.shape[0], wp, wn, _raw_stream(weight)))
     return weight, momentum
+
+
+# ---------------------------------------------------------------------------
+# Operators that make a node's gradient: activations in 8 bits, the linear layers
+# of experts, the norm and rotation of queries and keys.
+# ---------------------------------------------------------------------------
+GROUP8 = 128  # columns that share an exponent
+
+
+@dataclass(frozen=True)
+class Checkpoint8:
+    """An activation in 8 bits: ``codes`` int8 [..., dim rounded up to 16] and ``exponents``
+    uint8 [..., ceil(dim / 128)], both contiguous; an element is code * 2^(exponent - 127), and
+    NaN where the exponent is 255. ``dtype`` is the activation's own."""
+    codes: torch.Tensor
+    exponents: torch.Tensor
+    dim: int
+    dtype: torch.dtype
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.dim)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _stored(c, name: str, dtype=None):
+    """(codes, their stride, exponents, their stride, rows, dim) of a Checkpoint8."""
+    width, groups = (c.dim + 15) // 16 * 16, (c.dim + GROUP8 - 1) // GROUP8
+    p = _cuda(c.codes, torch.int8, name + ".codes")
+    e = _cuda(c.exponents, torch.uint8, name + ".exponents")
+    lead = c.codes.shape[:-1]
+    if c.dim < 1 or c.codes.dim() < 1 or c.codes.shape[-1] != width or \
+            c.exponents.shape != (*lead, groups):
+        raise ValueError(f"{name}: codes must be [..., {width}] and exponents [..., {groups}]")
+    if c.dtype not in TYPES:
+        raise TypeError(f"{name} must stand for float32, bfloat16 or float16, got {c.dtype}")
+    if dtype is not None and c.dtype != dtype:
+        raise TypeError(f"{name} must stand for {dtype}, got {c.dtype}")
+    return p, width, e, groups, lead.numel(), c.dim
+
+
+def checkpoint8(x, out=None, stream=None):
+    """x in 8 bits, as a Checkpoint8: for each 128 columns of its last axis a power of two, for
+    each element a whole number of at most 127 times that. It is within half a step of x, a step
+    being at most 1 / 63.5 of the group's largest magnitude; a NaN or an inf makes its group NaN.
+    x: float32, bfloat16 or float16, its other axes may be strided as one."""
+    if stream is not None:
+        with _on(stream, x):
+            return checkpoint8(x, out)
+    if _several is not False and _elsewhere(x, *(() if out is None else
+                                                 (out.codes, out.exponents))):
+        with torch.cuda.device(x.device):
+            return checkpoint8(x, out)
+    code = _typed(x, "x")
+    rows, dim, xs = _rows(x, "x")
+    if out is None:
+        lead = x.shape[:-1]
+        out = Checkpoint8(
+            torch.empty((*lead, (dim + 15) // 16 * 16), dtype=torch.int8, device=x.device),
+            torch.empty((*lead, (dim + GROUP8 - 1) // GROUP8), dtype=torch.uint8,
+                        device=x.device), dim, x.dtype)
+    elif out.shape != x.shape:
+        raise ValueError("out and x shapes differ")
+    p, ps, e, es, _, _ = _stored(out, "out", x.dtype)
+    r = (_lib._lib or _lib.load()).sparcml_checkpoint8(x.data_ptr(), code, xs, rows, dim, p, ps, e,
+                                                       es, _raw_stream(x))
+    if r:
+        _check("sparcml_checkpoint8", r)
+    return out
+
+
+def restore8(x, out=None, dtype=None, stream=None):
+    """What a Checkpoint8 stands for, in its own type or ``dtype``."""
+    if stream is not None:
+        with _on(stream, x.codes):
+            return restore8(x, out, dtype)
+    if _several is not False and _elsewhere(x.codes, x.exponents, out):
+        with torch.cuda.device(x.device):
+            return restore8(x, out, dtype)
+    p, ps, e, es, rows, dim = _stored(x, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+    elif out.shape != x.shape:
+        raise ValueError("out and x shapes differ")
+    code = _typed(out, "out")
+    r = (_lib._lib or _lib.load()).sparcml_restore8(p, ps, e, es, rows, dim, out.data_ptr(), code,
+                                                    _rows(out, "out")[2], _raw_stream(x.codes))
+    if r:
+        _check("sparcml_restore8", r)
+    return out
+
+
+def _layer_norm_backward8(dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate, ws, stream):
+    args = (dy, x, mean, rstd, weight, dx, dweight, dbias, accumulate, ws)
+    if stream is not None:
+        with _on(stream, x.codes):
+            return _layer_norm_backward8(*args, None)
+    if _several is not False and _elsewhere(x.codes, x.exponents, dy, mean, rstd, weight, dx,
+                                            dweight, dbias, ws):
+        with torch.cuda.device(x.device):
+            return _layer_norm_backward8(*args, None)
+    code = _typed(dy, "dy")
+    p, ps, e, es, rows, dim = _stored(x, "x", dy.dtype)
+    ds = _rows(dy, "dy")[2]
+    if dy.shape != x.shape:
+        raise ValueError("dy and x shapes differ")
+    w, wt = _vector(weight, dim, "weight")
+    if dx is None:
+        dx, os = _new_like(dy), dim
+    else:
+        _typed(dx, "dx", dy)
+        os = _rows(dx, "dx")[2]
+        if dx.shape != dy.shape:
+            raise ValueError("dx and dy shapes differ")
+    if accumulate and (dweight is None or dbias is None):
+        raise ValueError("accumulate needs dweight and dbias to add to")
+    if dweight is None:
+        dweight = torch.empty(dim, dtype=torch.float32, device=dy.device)
+    else:
+        _stat(dweight, dim, "dweight")
+    if dbias is None:
+        dbias = torch.empty_like(dweight)
+    else:
+        _stat(dbias, dim, "dbias")
+    if ws is None:
+        ws = workspace(layer_norm_backward_workspace_size(rows, dim), dy.device)
+    wp, wn = _space(ws)
+    r = (_lib._lib or _lib.load()).sparcml_layer_norm_backward8(
+        dy.data_ptr(), ds, code, p, ps, e, es, w, wt, _stat(mean, rows, "mean"),
+        _stat(rstd, rows, "rstd"), rows, dim, dx.data_ptr(), os, dweight.data_ptr(),
+        dbias.data_ptr(), accumulate, wp, wn, _raw_stream(dy))
+    if r:
+        _check("sparcml_layer_norm_backward8", r)
+    return dx, dweight, dbias
+
+
+def expert_linear_workspace_size(rows: int, experts: int, n: int, k: int,
+                                 aligned: bool = True) -> int:
+    """Bytes of a workspace for expert_linear and its backward pass. ``aligned``: every operand
+    starts on 16 bytes and is contiguous, or has strides that are multiples of 8 elements."""
+    return int(_lib.load().sparcml_expert_linear_workspace_size(rows, experts, n, k, aligned))
+
+
+def _half(t, name: str, like=None):
+    if _typed(t, name, like) == 0:
+        raise TypeError(f"{name} must be bfloat16 or float16: the tensor cores have no float32 "
+                        "product")
+
+
+def _row_matrix(t, name: str, rows=None, cols=None):
+    """(pointer, row stride) of a matrix with a contiguous last axis."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or \
+            (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be [{'rows' if rows is None else rows}, {cols}], got "
+                         f"{list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return t.data_ptr(), t.stride(0)
+
+
+def _experts(weight, name: str = "weight"):
+    """(batch stride, row stride, experts, n, k) of [experts, n, k], or of one [n, k]."""
+    if weight.dim() not in (2, 3):
+        raise ValueError(f"{name} must be [experts, n, k] or [n, k], got {weight.dim()} dims")
+    if weight.shape[-1] > 1 and weight.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    if weight.dim() == 2:
+        return 0, weight.stride(0), 1, *weight.shape
+    return weight.stride(0), weight.stride(1), *weight.shape
+
+
+def _offsets(offsets, weight):
+    """The pointer of the experts' row offsets."""
+    if offsets is None:
+        if weight.dim() != 2:
+            raise ValueError("several experts need offsets")
+        return None
+    p = _cuda(offsets, torch.int32, "offsets", 1)
+    experts = weight.shape[0] if weight.dim() == 3 else 1
+    if offsets.shape[0] != experts + 1:
+        raise ValueError(f"offsets must hold {experts + 1} elements")
+    return p
+
+
+def _fit(size, ws, device, *operands):
+    """The workspace, or a new one for operands of this alignment."""
+    if ws is None:
+        aligned = all(t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in t.stride()[:-1])
+                      for t in operands)
+        ws = workspace(expert_linear_workspace_size(*size, aligned), device)
+    return _space(ws)
+
+
+def expert_linear(x, weight, offsets=None, out=None, ws=None, stream=None):
+    """Linear layers of experts: rows offsets[e] .. offsets[e + 1] of x [rows, k] times the
+    transpose of weight[e], of weight [experts, n, k] (bfloat16 or float16). offsets: int32
+    [experts + 1] on the device, rising; a weight [n, k] without offsets takes all rows. Rows of
+    no expert are not written: without ``out`` they are unspecified. Returns [rows, n]."""
+    if stream is not None:
+        with _on(stream, x):
+            return expert_linear(x, weight, offsets, out, ws)
+    if _several is not False and _elsewhere(x, weight, offsets, out, ws):
+        with torch.cuda.device(x.device):
+            return expert_linear(x, weight, offsets, out, ws)
+    _half(x, "x")
+    _half(weight, "weight", x)
+    wb, wst, experts, n, k = _experts(weight)
+    xp, xs = _row_matrix(x, "x", None, k)
+    op = _offsets(offsets, weight)
+    rows = x.shape[0]
+    if out is None:
+        out = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+    _half(out, "out", x)
+    yp, ys = _row_matrix(out, "out", rows, n)
+    wp, wn = _fit((rows, experts, n, k), ws, x.device, x, weight)
+    r = (_lib._lib or _lib.load()).sparcml_expert_linear(
+        xp, xs, weight.data_ptr(), wb, wst, TYPES[x.dtype], op, experts, rows, n, k, yp, ys, wp, wn,
+        _raw_stream(x))
+    if r:
+        _check("sparcml_expert_linear", r)
+    return out
+
+
+def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
+                           accumulate: bool = False, need_dx: bool = True,
+                           need_dweight: bool = True, ws=None, stream=None):
+    """Gradients of expert_linear: (dx, dweight). dy: [rows, n]; x: [rows, k] or a Checkpoint8 of
+    it. dweight is float32 [experts, n, k] (or [n, k]), for example a view of a node's flat
+    gradient at any offset; with ``accumulate`` the sums are added to what it holds, else an expert
+    without rows gets zeros. need_dx, need_dweight: one that is False is left out (None). Rows of
+    no expert are neither read nor written."""
+    args = (dy, x, weight, offsets, dx, dweight, accumulate, need_dx, need_dweight, ws)
+    if stream is not None:
+        with _on(stream, dy):
+            return expert_linear_backward(*args)
+    stored = isinstance(x, Checkpoint8)
+    if _several is not False and _elsewhere(dy, weight, offsets, dx, dweight, ws,
+                                            *((x.codes, x.exponents) if stored else (x,))):
+        with torch.cuda.device(dy.device):
+            return expert_linear_backward(*args)
+    _half(dy, "dy")
+    _half(weight, "weight", dy)
+    wb, wst, experts, n, k = _experts(weight)
+    dp, ds = _row_matrix(dy, "dy", None, n)
+    op = _offsets(offsets, weight)
+    rows, t = dy.shape[0], TYPES[dy.dtype]
+    if stored:
+        p, ps, e, es, _, _ = _stored(x, "x", dy.dtype)
+        if x.shape != (rows, k):
+            raise ValueError(f"x must stand for [{rows}, {k}], got {list(x.shape)}")
+    else:
+        _half(x, "x", dy)
+        p, ps = _row_matrix(x, "x", rows, k)
+    if accumulate and need_dweight and dweight is None:
+        raise ValueError("accumulate needs dweight to add to")
+    if need_dx:
+        if dx is None:
+            dx = torch.empty((rows, k), dtype=dy.dtype, device=dy.device)
+        _half(dx, "dx", dy)
+        xp, xs = _row_matrix(dx, "dx", rows, k)
+    if need_dweight:
+        if dweight is None:
+            dweight = torch.empty(weight.shape, dtype=torch.float32, device=dy.device)
+        if not dweight.is_cuda or dweight.dtype != torch.float32 or dweight.shape != weight.shape:
+            raise TypeError(f"dweight must be a float32 CUDA tensor of {list(weight.shape)}")
+        gb, gs = _experts(dweight, "dweight")[:2]
+    wp, wn = _fit((rows, experts, n, k), ws, dy.device, dy, weight, *(() if stored else (x,)))
+    lib, s = _lib._lib or _lib.load(), _raw_stream(dy)
+    if need_dx:
+        r = lib.sparcml_expert_linear_dx(dp, ds, weight.data_ptr(), wb, wst, t, op, experts, rows,
+                                         n, k, xp, xs, wp, wn, s)
+        if r:
+            _check("sparcml_expert_linear_dx", r)
+    if need_dweight:
+        tail = (op, experts, rows, n, k, dweight.data_ptr(), gb, gs, int(accumulate), wp, wn, s)
+        if stored:
+            r = lib.sparcml_expert_linear_dweight8(dp, ds, t, p, ps, e, es, *tail)
+        else:
+            r = lib.sparcml_expert_linear_dweight(dp, ds, p, ps, t, *tail)
+        if r:
+            _check("sparcml_expert_linear_dweight", r)
+    return dx if need_dx else None, dweight if need_dweight else None
+
+
+def _heads(t, name: str, like=None, shape=None):
+    """(pointer, token stride, head stride, heads) of [tokens, heads, dim]; of None, no heads."""
+    if t is None:
+        return None, 0, 0, 0
+    _typed(t, name, like)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {t.dim()} dims")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name} must be contiguous along its last axis")
+    return t.data_ptr(), t.stride(0), t.stride(1), t.shape[1]
+
+
+def _head_args(q, k, positions, freqs, q_weight, k_weight):
+    """What both passes are given beside q and k: tokens, dim, and the arguments in order."""
+    if q is None and k is None:
+        raise ValueError("one of q and k has to be given")
+    x = k if q is None else q
+    if q is not None and k is not None and (q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2]):
+        raise ValueError("q and k must have the same tokens and elements per head")
+    tokens, _, dim = x.shape
+    if not isinstance(positions, torch.Tensor) or not positions.is_cuda or \
+            positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be a CUDA tensor of int32 or int64")
+    if positions.shape != (tokens,) or (tokens > 1 and positions.stride(0) != 1):
+        raise ValueError(f"positions must be a contiguous vector of {tokens} elements")
+    fp = _cuda(freqs, torch.float32, "freqs", 1)
+    turned = 2 * freqs.shape[0]
+    if turned > dim:
+        raise ValueError(f"freqs must hold at most {dim // 2} elements, one per pair")
+    qw, qt = _vector(q_weight, dim, "q_weight")
+    kw, kt = _vector(k_weight, dim, "k_weight")
+    if qw is not None and kw is not None and qt != kt:
+        raise TypeError("q_weight and k_weight must have the same type")
+    return tokens, dim, (positions.data_ptr(), int(positions.dtype == torch.int64), fp, turned), \
+        (qw, kw, qt if qw is not None else kt)
+
+
+def head_norm_rotary(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """Queries and keys [tokens, heads, dim] (float32, bfloat16 or float16; slices of one
+    projection will do), each head divided by its root mean square and multiplied by a weight,
+    then turned by its token's position: pair i by the angle positions * freqs[i]. Pairs are the
+    elements i and len(freqs) + i, or with ``interleaved`` 2 i and 2 i + 1; elements from
+    2 len(freqs) on are not turned. positions: int32 or int64, however large. q or k may be None.
+    Outputs may be the inputs. Returns (q_out, k_out)."""
+    x = k if q is None else q
+    args = (q, k, positions, freqs, q_weight, k_weight, eps, interleaved, q_out, k_out)
+    if stream is not None:
+        with _on(stream, x):
+            return head_norm_rotary(*args)
+    if _several is not False and _elsewhere(x, k, positions, freqs, q_weight, k_weight, q_out,
+                                            k_out):
+        with torch.cuda.device(x.device):
+            return head_norm_rotary(*args)
+    qa = _heads(q, "q")
+    ka = _heads(k, "k", x)
+    tokens, dim, turn, weights = _head_args(q, k, positions, freqs, q_weight, k_weight)
+    if q_out is None and q is not None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    qo = _heads(q_out if q is not None else None, "q_out", x, None if q is None else q.shape)
+    ko = _heads(k_out if k is not None else None, "k_out", x, None if k is None else k.shape)
+    r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary(
+        *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, int(interleaved), *weights, eps, *qo[:3],
+        *ko[:3], _raw_stream(x))
+    if r:
+        _check("sparcml_head_norm_rotary", r)
+    return q_out if q is not None else None, k_out if k is not None else None
+
+
+def head_norm_rotary_backward_workspace_size(tokens: int, q_heads: int, k_heads: int,
+                                             dim: int) -> int:
+    return int(_lib.load().sparcml_head_norm_rotary_backward_workspace_size(tokens, q_heads,
+                                                                            k_heads, dim))
+
+
+def head_norm_rotary_backward(dq, dk, q, k, positions, freqs, q_weight=None, k_weight=None,
+                              eps: float = 1e-6, interleaved: bool = False, dq_out=None,
+                              dk_out=None, dq_weight=None, dk_weight=None,
+                              accumulate: bool = False, ws=None, stream=None):
+    """Gradients of head_norm_rotary, from those of its results and its inputs: (dq, dk, dq_weight,
+    dk_weight), the last two float32 vectors, for example slices of a node's flat gradient; with
+    ``accumulate`` the sums are added to what the given ones hold. dq_out and dk_out may be dq and
+    dk."""
+    x = k if q is None else q
+    args = (dq, dk, q, k, positions, freqs, q_weight, k_weight, eps, interleaved, dq_out, dk_out,
+            dq_weight, dk_weight, accumulate, ws)
+    if stream is not None:
+        with _on(stream, x):
+            return head_norm_rotary_backward(*args)
+    if _several is not False and _elsewhere(x, k, dq, dk, positions, freqs, q_weight, k_weight,
+                                            dq_out, dk_out, dq_weight, dk_weight, ws):
+        with torch.cuda.device(x.device):
+            return head_norm_rotary_backward(*args)
+    qa = _heads(q, "q")
+    ka = _heads(k, "k", x)
+    tokens, dim, turn, weights = _head_args(q, k, positions, freqs, q_weight, k_weight)
+    if (q is None) != (dq is None) or (k is None) != (dk is None):
+        raise ValueError("q goes with dq, and k with dk")
+    gq = _heads(dq, "dq", x, None if q is None else q.shape)
+    gk = _heads(dk, "dk", x, None if k is None else k.shape)
+    if dq_out is None and q is not None:
+        dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if dk_out is None and k is not None:
+        dk_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    qo = _heads(dq_out if q is not None else None, "dq_out", x, None if q is None else q.shape)
+    ko = _heads(dk_out if k is not None else None, "dk_out", x, None if k is None else k.shape)
+    if accumulate and ((q is not None and dq_weight is None) or
+                       (k is not None and dk_weight is None)):
+        raise ValueError("accumulate needs dq_weight and dk_weight to add to")
+    if q is None:
+        dq_weight = None
+    elif dq_weight is None:
+        dq_weight = torch.empty(dim, dtype=torch.float32, device=x.device)
+    if k is None:
+        dk_weight = None
+    elif dk_weight is None:
+        dk_weight = torch.empty(dim, dtype=torch.float32, device=x.device)
+    sums = [None if t is None else _stat(t, dim, n)
+            for t, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight"))]
+    if ws is None:
+        ws = workspace(head_norm_rotary_backward_workspace_size(tokens, qa[3], ka[3], dim),
+                       x.device)
+    wp, wn = _space(ws)
+    r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary_backward(
+        *gq[:3], *gk[:3], *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, int(interleaved), *weights,
+        eps, *qo[:3], *ko[:3], *sums, int(accumulate), wp, wn, _raw_stream(x))
+    if r:
+        _check("sparcml_head_norm_rotary_backward", r)
+    return (dq_out if q is not None else None, dk_out if k is not None else None, dq_weight,
+            dk_weight)

@@ -1,0 +1,818 @@
+// Linear layers of experts, each on its own run of the rows, and their gradients:
+//
+//   y[r] = x[r] W_e',  dx[r] = dy[r] W_e,  dW_e = sum over the expert's rows of dy[r]' x[r]
+//
+// All three are one product on the tensor cores, out[j][i] = sum over s of P[i][s] Q[j][s]:
+//
+//            i     j     s     P                           Q
+//   forward  n     rows  k     W_e, s contiguous           x, s contiguous
+//   dx       k     rows  n     W_e, i contiguous           dy, s contiguous
+//   dW       k     n     rows  x, i contiguous             dy, j contiguous
+//
+// i, the results' contiguous axis, is what a pair of SMs has 256 of: a matrix's side, of any
+// size, while the ragged rows are the instruction's N, any multiple of 16 up to 256. So an expert
+// with few rows costs what reading its matrix costs and no more. No operand is transposed: the
+// tensor cores read either axis as the contiguous one.
+//
+// One launch, a persistent grid of pairs of SMs. Of a block's ten warps one loads operands by TMA,
+// one issues the products (for both blocks of a pair), eight turn accumulators into results while
+// the next tile is under way. Where the experts' runs begin and end is read on the device: every
+// block works out the same list of tiles from them. A long summed axis with few tiles is split; the
+// parts are added in order by a second launch.
+//
+// Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. For dW, the rows
+// of the last 64 that belong to the next expert are zeros in both operands, so that what stands
+// there, a NaN say, does not count.
+
+#include <algorithm>
+#include <map>
+#include <mutex>
+
+#include "stored.cuh"
+#include "tensor.cuh"
+
+namespace sparcml {
+namespace {
+
+constexpr uint32_t kMostExperts = 1024;
+constexpr uint32_t kSide = 256;      // i and j of a tile, at most
+constexpr uint32_t kPairs = 76;      // of SMs
+constexpr uint32_t kWriters = 8;     // warps that write results; then a loader and an issuer
+constexpr uint32_t kThreads = 32 * (kWriters + 2);
+constexpr uint32_t kOperand = 128 * 128;  // bytes of one operand's 64 of the summed axis, per block
+constexpr uint32_t kStageBytes = 2 * kOperand, kStages = 6;
+constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
+constexpr uint32_t kBox = 32;        // rows of Q per load
+constexpr uint32_t kLeastBlocks = 8;  // of 64 in a part of a split sum, at least
+constexpr uint32_t kBand = 8;        // tiles along j that are taken together, for L2's sake
+
+enum Form { kForward, kInput, kWeight };
+
+struct ExpertArgs {
+  const int32_t* offsets;  // or null: one expert with all rows
+  uint32_t experts, rows;
+  uint32_t i_size, j_size, s_size;  // j_size for dW, s_size for the others; the rest is rows
+  uint32_t splits;      // forward, dx: parts of the summed axis
+  uint32_t may_split;   // dW: whether long runs of rows are taken in parts
+  uint32_t wide;        // j of a partial tile
+  void* out;
+  int32_t out_type;
+  int64_t out_batch, out_stride;
+  int32_t accumulate;
+  uint32_t bf16;        // operands; else fp16
+  float* part;          // [item][wide][256]
+  int32_t* status;
+  const uint32_t* inject;
+};
+struct ExpertMaps {
+  CUtensorMap p, q;
+};
+
+// The experts' runs and tiles, in shared memory.
+struct Table {
+  int32_t begin[kMostExperts + 1];   // of the expert's rows; the last: where they end
+  uint32_t first[kMostExperts + 1];  // the expert's first item; the last: their number
+  uint32_t chunk;                    // dW: blocks of 64 rows in a part
+};
+
+struct Item {
+  uint32_t e, i0, j0, width;   // j0: a row of all rows (forward, dx), or of dW's matrix
+  uint32_t count;              // of its j, those that exist
+  uint32_t row, rows;          // the expert's run
+  uint32_t s0, s1;             // blocks of 64 of the summed axis
+  uint32_t split, splits;
+};
+
+__device__ __forceinline__ uint32_t ceil_of(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+
+// The table, by one warp. An offset out of order or range counts as the nearest that is not;
+// returns whether there was one.
+template <int FORM>
+__device__ bool make_table(const ExpertArgs& a, Table& t, uint32_t pairs) {
+  const uint32_t lane = lane_id();
+  bool bad = false;
+  int32_t carry = 0;
+  for (uint32_t base = 0; base <= a.experts; base += 32) {
+    const uint32_t e = base + lane;
+    const bool there = e <= a.experts;
+    const int32_t given = !there ? 0 : a.offsets ? a.offsets[e] : e ? (int32_t)a.rows : 0;
+    int32_t v = min(max(given, 0), (int32_t)a.rows);
+    if (lane == 0) v = max(v, carry);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int32_t o = __shfl_up_sync(0xffffffffu, v, d);
+      if (lane >= (uint32_t)d) v = max(v, o);
+    }
+    if (there) t.begin[e] = v;
+    bad |= there && v != given;
+    carry = __shfl_sync(0xffffffffu, v, 31);
+  }
+  __syncwarp();
+  const uint32_t ti = ceil_of(a.i_size, kSide);
+  const uint32_t tiles = FORM == kWeight ? ti * ceil_of(a.j_size, kSide) : 0;
+  uint32_t chunk = 0x7fffffffu;
+  if (FORM == kWeight && a.may_split) {  // shares of the whole work, one for each pair
+    uint32_t blocks = 0;
+    for (uint32_t e = lane; e < a.experts; e += 32)
+      blocks += ceil_of((uint32_t)(t.begin[e + 1] - t.begin[e]), 64);
+    const uint64_t all = (uint64_t)warp_sum(blocks) * tiles;
+    chunk = max(kLeastBlocks, (uint32_t)((all + pairs - 1) / pairs));
+  }
+  uint32_t sum = 0;
+  for (uint32_t base = 0; base < a.experts; base += 32) {
+    const uint32_t e = base + lane;
+    uint32_t n = 0;
+    if (e < a.experts) {
+      const uint32_t rows = (uint32_t)(t.begin[e + 1] - t.begin[e]);
+      n = FORM == kWeight ? tiles * max(1u, ceil_of(ceil_of(rows, 64), chunk))
+                          : ti * ceil_of(rows, kSide) * a.splits;
+    }
+    const uint32_t upto = warp_incl_sum(n);
+    if (e < a.experts) t.first[e] = sum + upto - n;
+    sum += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  if (lane == 0) {
+    t.first[a.experts] = sum;
+    t.chunk = chunk;
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
+template <int FORM>
+__device__ __forceinline__ Item item_of(const ExpertArgs& a, const Table& t, uint32_t index) {
+  uint32_t lo = 0, hi = a.experts;  // first[lo] <= index < first[hi]
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) / 2;
+    if (t.first[mid] <= index) lo = mid;
+    else hi = mid;
+  }
+  Item it;
+  it.e = lo;
+  it.row = (uint32_t)t.begin[lo];
+  it.rows = (uint32_t)t.begin[lo + 1] - it.row;
+  uint32_t u = index - t.first[lo];
+  const uint32_t blocks = ceil_of(FORM == kWeight ? it.rows : a.s_size, 64);
+  it.splits = FORM == kWeight ? max(1u, ceil_of(blocks, t.chunk)) : a.splits;
+  it.split = 0;
+  if (it.splits > 1) {
+    it.split = u % it.splits;
+    u /= it.splits;
+  }
+  it.s0 = (uint32_t)((uint64_t)blocks * it.split / it.splits);
+  it.s1 = (uint32_t)((uint64_t)blocks * (it.split + 1) / it.splits);
+  const uint32_t j_size = FORM == kWeight ? a.j_size : it.rows;
+  const uint32_t tj = ceil_of(j_size, kSide), ti = ceil_of(a.i_size, kSide);
+  // the rows of an expert are shared out evenly; of dW's matrix only the last tile is narrower
+  it.width = FORM == kWeight ? kSide : (ceil_of(j_size, tj) + 15) / 16 * 16;
+  const uint32_t band = u / (ti * kBand), rest = u - band * ti * kBand;
+  const uint32_t across = min(kBand, tj - band * kBand), i = rest / across;
+  const uint32_t j = (band * kBand + rest - i * across) * it.width;
+  it.i0 = i * kSide;
+  it.count = min(it.width, j_size - j);
+  it.j0 = FORM == kWeight ? j : it.row + j;
+  return it;
+}
+
+struct Worker {
+  uint32_t ring, full, empty, acc_full, acc_empty, tail;  // shared-memory addresses
+  uint32_t lead_full, lead_acc_empty, own_tail;           // in the cluster's shared memory
+  uint32_t rank, pair, pairs, tmem;
+  bool leader;  // the lane that issues for its warp
+  Waits* waits;
+  uint32_t stage = 0, phase = 0, acc = 0, tails = 0;
+  __device__ __forceinline__ void next_stage() {
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// Both blocks of a pair load their halves of P and Q; the first one's barriers count for both. The
+// last rows of an expert's run go to a barrier of the block's own, and are reported once those of
+// the next expert are zeros.
+template <int FORM>
+__device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const Item& it) {
+  const uint32_t i0 = it.i0 + 128 * w.rank, j0 = it.j0 + it.width / 2 * w.rank;
+  const uint32_t boxes = (it.width / 2 + kBox - 1) / kBox;
+  const uint32_t bytes = kOperand + (FORM == kWeight ? kOperand : boxes * kBox * 128);
+  for (uint32_t b = it.s0; b < it.s1; ++b, w.next_stage()) {
+    const uint32_t s = w.stage;
+    if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.waits)) return false;
+    const uint32_t left = FORM == kWeight ? it.rows - b * 64 : 64;  // rows of the block
+    const bool cut = FORM == kWeight && left < 64;
+    const uint32_t bar = cut ? w.own_tail : w.lead_full + 8 * s;
+    const uint32_t p = w.ring + s * kStageBytes, q = p + kOperand;
+    if (w.leader) {
+      if (cut) mbar_expect_tx(w.tail, bytes);
+      else if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, 2 * bytes);
+      else mbar_arrive_cluster(w.lead_full + 8 * s);
+      const uint32_t at = FORM == kWeight ? it.row + b * 64 : b * 64;
+      if constexpr (FORM == kForward) {
+        tma_load_3d_group<2>(p, &m.p, at, i0, it.e, bar);
+      } else {
+        const uint32_t z = FORM == kInput ? it.e : 0;
+        tma_load_3d_group<2>(p, &m.p, i0, at, z, bar);
+        tma_load_3d_group<2>(p + kOperand / 2, &m.p, i0 + 64, at, z, bar);
+      }
+      if constexpr (FORM == kWeight) {
+        tma_load_3d_group<2>(q, &m.q, j0, at, 0, bar);
+        tma_load_3d_group<2>(q + kOperand / 2, &m.q, j0 + 64, at, 0, bar);
+      } else {
+        for (uint32_t k = 0; k < boxes; ++k)
+          tma_load_3d_group<2>(q + k * kBox * 128, &m.q, at, j0 + k * kBox, 0, bar);
+      }
+    }
+    __syncwarp();
+    if constexpr (FORM == kWeight) {
+      if (!cut) continue;
+      if (!mbar_wait_warp(w.tail, w.tails & 1u, w.waits)) {
+        Waits alone = {0, kLandUs};  // what was begun has to land before the block leaves
+        mbar_wait_warp(w.tail, w.tails & 1u, &alone);
+        return false;
+      }
+      ++w.tails;
+      // a row is 128 bytes of each of the four boxes
+      for (uint32_t c = lane_id(); c < 4 * (64 - left) * 8; c += 32) {
+        const uint32_t box = c / ((64 - left) * 8), rest = c - box * (64 - left) * 8;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                         p + box * (kOperand / 2) + left * 128 + rest * 16),
+                     "r"(0)
+                     : "memory");
+      }
+      proxy_fence_shared();
+      __syncwarp();
+      if (w.leader) mbar_arrive_cluster_release(w.lead_full + 8 * s);
+      __syncwarp();
+    }
+  }
+  return true;
+}
+
+template <int FORM>
+__device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const Item& it) {
+  constexpr bool P_MN = FORM != kForward, Q_MN = FORM == kWeight;
+  constexpr uint32_t step_p = P_MN ? 2048 : 32, step_q = Q_MN ? 2048 : 32;
+  const uint32_t idesc = mma_desc(256, it.width, P_MN, Q_MN, a.bf16);
+  const uint32_t acc = w.acc & 1u;
+  if (!mbar_wait_warp(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
+  tmem_fence_after();
+  const uint32_t d = w.tmem + acc * kSide;
+  for (uint32_t b = it.s0; b < it.s1; ++b, w.next_stage()) {
+    const uint32_t s = w.stage;
+    if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.waits)) return false;
+    if (FORM == kWeight) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    tmem_fence_after();
+    if (w.leader) {
+      const uint32_t p = w.ring + s * kStageBytes, q = p + kOperand;
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        mma_f16<2>(d, tile_desc(p + k * step_p, 8192, 1024), tile_desc(q + k * step_q, 8192, 1024),
+                   idesc, b > it.s0 || k > 0);
+      mma_commit<2>(w.empty + 8 * s);
+    }
+    __syncwarp();
+  }
+  if (w.leader) mma_commit<2>(w.acc_full + 8 * acc);
+  __syncwarp();
+  ++w.acc;
+  return true;
+}
+
+__device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, float v) {
+  if (a.out_type == SPARCML_F32) {
+    float* o = static_cast<float*>(a.out) + at;
+    *o = a.accumulate ? *o + v : v;
+  } else if (a.out_type == SPARCML_BF16) {
+    static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+  } else {
+    static_cast<__half*>(a.out)[at] = __float2half_rn(v);
+  }
+}
+
+// An accumulator's rows are i, its columns j: a warp has 32 neighbouring i, so that it writes
+// whole stretches of a result's row as they come.
+template <int FORM>
+__device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const Item& it,
+                                           uint32_t index) {
+  const uint32_t warp = threadIdx.x >> 5, quarter = warp & 3u, half = warp >> 2;
+  const uint32_t side = 128 * w.rank + 32 * quarter + lane_id(), i = it.i0 + side;
+  const bool in = i < a.i_size, empty = it.s0 == it.s1;
+  const uint32_t acc = w.acc & 1u;
+  if (!empty) {
+    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
+    tmem_fence_after();
+  }
+  const uint32_t src = w.tmem + acc * kSide + (quarter << 21);
+  const int64_t out = (FORM == kWeight ? (int64_t)it.e * a.out_batch : 0) +
+                      (int64_t)it.j0 * a.out_stride + i;
+#pragma unroll 1
+  for (uint32_t c = 16 * half; c < it.count; c += 32) {
+    float v[16];
+    if (!empty) {
+      tmem_load16(src + c, v);
+      tmem_load_wait(v);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) v[q] = 0.f;
+    }
+    if (it.splits > 1) {
+      float* o = a.part + ((uint64_t)index * a.wide + c) * kSide + side;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) o[q * kSide] = v[q];
+    } else if (in) {
+#pragma unroll
+      for (uint32_t q = 0; q < 16; ++q)
+        if (c + q < it.count) put(a, out + (int64_t)(c + q) * a.out_stride, v[q]);
+    }
+  }
+  if (!empty) {
+    tmem_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
+    ++w.acc;
+  }
+  return true;
+}
+
+template <int FORM>
+__global__ void __launch_bounds__(kThreads, 1)
+experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ ExpertArgs a) {
+  extern __shared__ uint8_t raw[];
+  __shared__ alignas(8) uint64_t bars[2 * kStages + 5];
+  __shared__ uint32_t tmem_slot, partner[2];
+  __shared__ Waits waits;
+  __shared__ Table table;
+  griddep_wait();
+  const uint32_t warp = threadIdx.x >> 5;
+  Worker w;
+  w.ring = (smem_addr(raw) + 1023u) & ~1023u;
+  w.full = smem_addr(bars);
+  w.empty = w.full + 8 * kStages;
+  w.acc_full = w.empty + 8 * kStages;
+  w.acc_empty = w.acc_full + 16;
+  const uint32_t finished = w.acc_empty + 16;
+  w.rank = cluster_rank();
+  w.pair = blockIdx.x / 2;
+  w.pairs = gridDim.x / 2;
+  w.waits = &waits;
+  __shared__ alignas(8) uint64_t tail_bar;
+  w.tail = smem_addr(&tail_bar);
+  w.lead_full = cluster_addr(w.full, 0);
+  w.lead_acc_empty = cluster_addr(w.acc_empty, 0);
+  w.own_tail = cluster_addr(w.tail, w.rank);
+  w.leader = elect_one();
+  if (threadIdx.x < 2) tma_prefetch_map(threadIdx.x ? &m.q : &m.p);
+  if (threadIdx.x == 0) {
+    waits.gave_up = 0;
+    waits.limit_us = injected(a.inject) ? kInjectWaitUs : kWaitUs;
+    partner[0] = partner[1] = 0;
+    for (uint32_t s = 0; s < kStages; ++s) {
+      mbar_init(w.full + 8 * s, 2);
+      mbar_init(w.empty + 8 * s, 1);
+    }
+    for (uint32_t s = 0; s < 2; ++s) {
+      mbar_init(w.acc_full + 8 * s, 1);
+      mbar_init(w.acc_empty + 8 * s, 2 * kWriters);
+    }
+    mbar_init(finished, 1);
+    mbar_init(w.tail, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kWriters) tmem_alloc<2>(smem_addr(&tmem_slot), 2 * kSide);
+  if (warp == 1) {
+    const bool bad = make_table<FORM>(a, table, w.pairs);
+    if (bad && blockIdx.x == 0 && w.leader) set_status(a.status, SPARCML_ERR_BAD_STREAM);
+  }
+  tmem_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tmem_fence_after();
+  w.tmem = tmem_slot;
+
+  const uint32_t items = table.first[a.experts];
+  if (warp == kWriters) {
+    for (uint32_t x = w.pair; x < items; x += w.pairs)
+      if (!load_item<FORM>(w, m, item_of<FORM>(a, table, x))) break;
+  } else if (warp == kWriters + 1) {
+    // An injected fault: the first pair withholds its products.
+    const bool withhold = w.pair == 0 && waits.limit_us == kInjectWaitUs;
+    if (w.rank == 0 && !withhold)
+      for (uint32_t x = w.pair; x < items; x += w.pairs) {
+        const Item it = item_of<FORM>(a, table, x);
+        if (it.s0 < it.s1 && !issue_item<FORM>(w, a, it)) break;
+      }
+  } else {
+    for (uint32_t x = w.pair; x < items; x += w.pairs)
+      if (!write_item<FORM>(w, a, item_of<FORM>(a, table, x), x)) break;
+  }
+  tmem_fence_before();
+  __syncthreads();  // now it is settled whether this block gave up
+  {
+    const uint32_t to = cluster_addr(smem_addr(partner), w.rank ^ 1u);
+    if (threadIdx.x == 0) store_cluster(to, waits.gave_up);
+    if (warp == kWriters && w.leader) store_cluster(to + 4, 2 * w.stage + w.phase);
+    __syncwarp();
+    cluster_sync();
+  }
+  if (waits.gave_up || partner[0]) {
+    // Nothing may still be in flight when the shared and tensor memory go.
+    if (warp == kWriters && w.leader) {
+      const bool apart = partner[1] != 2 * w.stage + w.phase;
+      if (w.rank == 0 || apart) land_operands(w.full, kStages, w.stage, w.phase, apart);
+    }
+    if (warp == kWriters + 1 && w.leader) {
+      // arrives, in both blocks of a pair, once all products have completed
+      Waits alone = {0, kWaitUs};
+      if (w.rank == 0) mma_commit<2>(finished);
+      mbar_wait(finished, 0, &alone);
+    }
+    __syncwarp();
+    if (threadIdx.x == 0) set_status(a.status, SPARCML_ERR_TIMEOUT);
+    __syncthreads();
+    cluster_sync();
+  }
+  tmem_fence_after();
+  if (warp == kWriters) tmem_free<2>(w.tmem, 2 * kSide);
+}
+
+// The parts of split sums, added in their order: a warp takes 256 i of one j at a time.
+template <int FORM>
+__global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ ExpertArgs a,
+                                                         uint32_t pairs) {
+  __shared__ Table table;
+  griddep_wait();
+  if (threadIdx.x < 32) make_table<FORM>(a, table, pairs);
+  __syncthreads();
+  const uint32_t items = table.first[a.experts], lane = lane_id();
+  const uint32_t groups = a.wide / 16;  // of 16 j
+  for (uint32_t x = blockIdx.x; x < items * groups; x += gridDim.x) {
+    const uint32_t index = x / groups;
+    const Item it = item_of<FORM>(a, table, index);
+    if (it.splits == 1 || it.split != 0) continue;
+    const uint32_t j0 = 16 * (x - index * groups) + (threadIdx.x >> 5) * 2;
+#pragma unroll
+    for (uint32_t j = j0; j < j0 + 2; ++j) {
+      if (j >= it.count) continue;
+      float v[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[q] = 0.f;
+      const float* p = a.part + ((uint64_t)index * a.wide + j) * kSide + lane;
+#pragma unroll 4
+      for (uint32_t s = 0; s < it.splits; ++s, p += (uint64_t)a.wide * kSide) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] += __ldcg(p + 32 * q);
+      }
+      const int64_t out = (FORM == kWeight ? (int64_t)it.e * a.out_batch : 0) +
+                          (int64_t)(it.j0 + j) * a.out_stride + it.i0 + lane;
+#pragma unroll
+      for (uint32_t q = 0; q < 8; ++q)
+        if (it.i0 + lane + 32 * q < a.i_size) put(a, out + 32 * q, v[q]);
+    }
+  }
+}
+
+// An operand whose rows are not what TMA takes (16-byte aligned, 16 bytes a step), copied into
+// rows of `pitch` elements; 16 bytes per thread and turn.
+struct CopyArgs {
+  const uint16_t* from;
+  int64_t batch, stride;
+  uint16_t* to;
+  uint64_t pitch, rows, cols, all;  // all: rows of all matrices
+};
+__global__ void __launch_bounds__(256) copy_rows_kernel(const CopyArgs a) {
+  griddep_wait();
+  const uint64_t per = a.pitch / 8, total = a.all * per;
+  for (uint64_t x = blockIdx.x * (uint64_t)blockDim.x + threadIdx.x; x < total;
+       x += (uint64_t)gridDim.x * blockDim.x) {
+    const uint64_t r = x / per, c = (x - r * per) * 8, b = r / a.rows;
+    const uint16_t* p = a.from + (int64_t)b * a.batch + (int64_t)(r - b * a.rows) * a.stride + c;
+    uint32_t v[8];
+#pragma unroll
+    for (uint32_t i = 0; i < 8; ++i) v[i] = c + i < a.cols ? p[i] : 0u;
+    reinterpret_cast<uint4*>(a.to)[x] =
+        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+uint64_t ceil_div(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+struct Sizes {
+  uint64_t rows, experts, n, k;
+  bool ok() const {
+    return rows <= 0x7fffffffull && experts >= 1 && experts <= kMostExperts && n >= 1 &&
+           n <= (1u << 24) && k >= 1 && k <= (1u << 24) &&
+           // tiles are counted in 31 bits (what has more does not fit the memory)
+           ceil_div(std::max(n, k), kSide) * (rows / kSide + experts) < (1ull << 31) &&
+           experts * ceil_div(n, kSide) * ceil_div(k, kSide) < (1ull << 31);
+  }
+  // Parts of the summed axis for forward and dx: as many as the pairs of SMs leave room for where
+  // even the most tiles that the rows can make are at most half as many.
+  uint32_t splits(uint64_t i, uint64_t s) const {
+    const uint64_t most = ceil_div(i, kSide) * (std::min(experts, rows) + rows / kSide);
+    if (most == 0 || most * 2 > kPairs) return 1;
+    return (uint32_t)std::max<uint64_t>(
+        1, std::min<uint64_t>(kPairs / most, ceil_div(s, 64) / kLeastBlocks));
+  }
+  uint64_t weight_tiles() const { return experts * ceil_div(n, kSide) * ceil_div(k, kSide); }
+  bool weight_splits() const { return weight_tiles() < kPairs; }
+  uint32_t wide() const { return (uint32_t)std::min<uint64_t>(kSide, align_up(rows, 16)); }
+  size_t part_bytes() const {
+    size_t r = 0;
+    if (splits(n, k) > 1 || splits(k, n) > 1) r = (size_t)kPairs * wide() * kSide * 4;
+    if (weight_splits()) r = std::max(r, (size_t)(kPairs + weight_tiles()) * kSide * kSide * 4);
+    return align_up(r, 256);
+  }
+};
+
+struct Operand {  // `batches` matrices of `rows` rows of `cols` elements of 16 bits
+  const void* p;
+  int64_t batch, stride;
+  uint64_t batches, rows, cols;
+
+  uint64_t pitch() const { return align_up(cols, 8); }
+  size_t copy_bytes() const { return align_up(batches * rows * pitch() * 2, 256); }
+  bool fits() const {
+    return aligned_to(p, 16) && (rows == 1 || (stride % 8 == 0 && stride >= (int64_t)cols)) &&
+           (batches == 1 || (batch % 8 == 0 && batch >= (int64_t)cols));
+  }
+};
+
+// Takes the workspace's copies one after the other.
+struct Room {
+  uint8_t* at;
+  size_t left;
+  void* take(size_t bytes) {
+    if (bytes > left) return nullptr;
+    void* p = at;
+    at += bytes;
+    left -= bytes;
+    return p;
+  }
+};
+
+// Has the operand as TMA takes it; false if the workspace has no room for a copy.
+bool settle(Operand& o, Room& room, cudaStream_t s) {
+  if (o.fits() || o.rows == 0) return true;
+  uint16_t* to = static_cast<uint16_t*>(room.take(o.copy_bytes()));
+  if (!to) return false;
+  const CopyArgs a{static_cast<const uint16_t*>(o.p), o.batch, o.stride, to, o.pitch(), o.rows,
+                   o.cols, o.rows * o.batches};
+  launch_pdl(copy_rows_kernel, (unsigned)std::min<uint64_t>(ceil_div(a.all * a.pitch, 8 * 256), 152 * 8),
+             256, 0, s, a);
+  note_launches(1);
+  o.p = to;
+  o.stride = (int64_t)o.pitch();
+  o.batch = (int64_t)(o.pitch() * o.rows);
+  return true;
+}
+
+bool map_of(CUtensorMap* map, const Operand& o, bool bf16, uint32_t box_rows) {
+  const cuuint64_t row = (o.rows == 1 ? o.pitch() : (uint64_t)o.stride) * 2;
+  const cuuint64_t dims[3] = {o.cols, o.rows, o.batches};
+  const cuuint64_t strides[2] = {row, o.batches == 1 ? row : (uint64_t)o.batch * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  return encode_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    o.p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Pairs of SMs that run the kernel at one time on the current device; 0 if that cannot be found
+// out. Asked for once per device.
+template <int FORM>
+unsigned resident() {
+  static std::mutex lock;
+  static std::map<int, unsigned> known;
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> hold(lock);
+  const auto it = known.find(device);
+  if (it != known.end()) return it->second;
+  auto kernel = experts_kernel<FORM>;
+  if (!ensure_smem(reinterpret_cast<const void*>(kernel), kSmem)) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * kPairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int count = 0;
+  if (cudaOccupancyMaxActiveClusters(&count, kernel, &cfg) != cudaSuccess) return 0;
+  const unsigned fit = (unsigned)std::min<int>(count, kPairs);
+  known[device] = fit;
+  return fit;
+}
+
+template <int FORM>
+int launch_experts(const ExpertMaps& m, const ExpertArgs& a, uint64_t most_items, bool join,
+                   cudaStream_t s) {
+  auto kernel = experts_kernel<FORM>;
+  const unsigned fit = resident<FORM>();
+  if (fit == 0 || !ensure_smem(reinterpret_cast<const void*>(kernel), kSmem))
+    return SPARCML_ERR_CUDA;
+  const unsigned pairs = (unsigned)std::min<uint64_t>(fit, most_items);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  (void)cudaLaunchKernelEx(&cfg, kernel, m, a);
+  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  if (join) {
+    launch_pdl(join_parts_kernel<FORM>, 152 * 4, 256, 0, s, a, pairs);
+    if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  }
+  note_launches(1 + join);
+  return SPARCML_OK;
+}
+
+struct Call {
+  Sizes z;
+  int32_t type;
+  const int32_t* offsets;
+  void* out;
+  int32_t out_type;
+  int64_t out_batch, out_stride;
+  int32_t accumulate;
+  void* ws;
+  size_t ws_bytes;
+  cudaStream_t stream;
+};
+
+template <int FORM>
+int run(const Call& c, Operand p, Operand q) {
+  const Sizes& z = c.z;
+  uint8_t* w = static_cast<uint8_t*>(c.ws);
+  const size_t parts = z.part_bytes();
+  if (c.ws_bytes < 256 + parts + (p.fits() ? 0 : p.copy_bytes()) + (q.fits() ? 0 : q.copy_bytes()))
+    return SPARCML_ERR_WORKSPACE;
+  Room room{w + 256 + parts, c.ws_bytes - 256 - parts};
+  if (!settle(p, room, c.stream) || !settle(q, room, c.stream)) return SPARCML_ERR_WORKSPACE;
+  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  ExpertArgs a = {};
+  a.offsets = c.offsets;
+  a.experts = (uint32_t)z.experts;
+  a.rows = (uint32_t)z.rows;
+  a.i_size = (uint32_t)(FORM == kForward ? z.n : z.k);
+  a.j_size = FORM == kWeight ? (uint32_t)z.n : 0;
+  a.s_size = (uint32_t)(FORM == kForward ? z.k : FORM == kInput ? z.n : 0);
+  a.splits = FORM == kWeight ? 1 : z.splits(a.i_size, a.s_size);
+  a.may_split = FORM == kWeight && z.weight_splits();
+  a.wide = FORM == kWeight ? kSide : z.wide();
+  a.out = c.out;
+  a.out_type = c.out_type;
+  a.out_batch = c.out_batch;
+  a.out_stride = c.out_stride;
+  a.accumulate = c.accumulate;
+  a.bf16 = c.type == SPARCML_BF16;
+  a.part = reinterpret_cast<float*>(w + 256);
+  a.status = reinterpret_cast<int32_t*>(w);
+  a.inject = reinterpret_cast<const uint32_t*>(w + kInjectOffset);
+  ExpertMaps m;
+  if (FORM == kWeight && z.rows == 0) {  // no operand is read
+    p = q = Operand{w, 64, 64, 1, 1, 64};
+  }
+  if (!map_of(&m.p, p, a.bf16, FORM == kForward ? 128 : 64) ||
+      !map_of(&m.q, q, a.bf16, FORM == kWeight ? 64 : kBox))
+    return SPARCML_ERR_CUDA;
+  const bool join = FORM == kWeight ? a.may_split : a.splits > 1;
+  const uint64_t most = FORM == kWeight
+                            ? (a.may_split ? kPairs : z.weight_tiles())
+                            : ceil_div(a.i_size, kSide) *
+                                  (std::min(z.experts, z.rows) + z.rows / kSide) * a.splits;
+  return launch_experts<FORM>(m, a, std::max<uint64_t>(1, most), join, c.stream);
+}
+
+bool half_type(int32_t type) { return type == SPARCML_BF16 || type == SPARCML_F16; }
+
+// Whether rows of `cols` elements at these strides share no address.
+bool rows_apart(uint64_t rows, uint64_t cols, int64_t stride) {
+  return rows <= 1 || stride >= (int64_t)cols;
+}
+
+int check_call(const Call& c) {
+  if (!c.z.ok() || !half_type(c.type) || (!c.offsets && c.z.experts != 1) ||
+      !aligned_to(c.offsets, 4) || !c.ws || !aligned_to(c.ws, 256))
+    return SPARCML_ERR_INVALID_ARG;
+  return SPARCML_OK;
+}
+bool operand_ok(const Operand& o) {
+  return o.rows == 0 || (o.p && aligned_to(o.p, 2) && o.stride >= 0 && o.batch >= 0);
+}
+
+template <int FORM>
+int rows_product(const Call& c, const Operand& w, const Operand& q) {
+  int r = check_call(c);
+  if (r != SPARCML_OK) return r;
+  if (c.z.rows == 0) return SPARCML_OK;
+  if (!operand_ok(w) || !operand_ok(q) || !c.out || !aligned_to(c.out, 2) ||
+      !rows_apart(c.z.rows, FORM == kForward ? c.z.n : c.z.k, c.out_stride))
+    return SPARCML_ERR_INVALID_ARG;
+  return run<FORM>(c, w, q);
+}
+
+int weight_product(const Call& c, const Operand& x, const Operand& dy) {
+  const Sizes& z = c.z;
+  if (!operand_ok(x) || !operand_ok(dy) || !c.out || !aligned_to(c.out, 4) || c.out_stride < 0 ||
+      c.out_batch < 0 || !rows_apart(z.n, z.k, c.out_stride) ||
+      (z.experts > 1 && c.out_batch < (int64_t)z.k) ||
+      // matrices one after the other, or their rows in turn
+      !(z.experts == 1 || c.out_batch >= (int64_t)(z.n - 1) * c.out_stride + (int64_t)z.k ||
+        z.n == 1 ||
+        c.out_stride >= (int64_t)(z.experts - 1) * c.out_batch + (int64_t)z.k))
+    return SPARCML_ERR_INVALID_ARG;
+  return run<kWeight>(c, x, dy);
+}
+
+}  // namespace
+}  // namespace sparcml
+
+using namespace sparcml;
+
+extern "C" size_t sparcml_expert_linear_workspace_size(uint64_t rows, uint32_t experts, uint64_t n,
+                                                       uint64_t k, int32_t aligned) {
+  const Sizes z{rows, experts, n, k};
+  if (!z.ok()) return 0;
+  const Operand x{nullptr, 0, 0, 1, rows, k}, dy{nullptr, 0, 0, 1, rows, n},
+      w{nullptr, 0, 0, experts, n, k};
+  const bool odd_n = !aligned || n % 8 != 0, odd_k = !aligned || k % 8 != 0;
+  // x also where it is kept in 8 bits
+  return 256 + z.part_bytes() + x.copy_bytes() + (odd_n ? dy.copy_bytes() : 0) +
+         (odd_k ? w.copy_bytes() : 0);
+}
+
+extern "C" int sparcml_expert_linear(const void* x, int64_t x_stride, const void* weight,
+                                     int64_t weight_batch_stride, int64_t weight_stride,
+                                     int32_t type, const int32_t* offsets, uint32_t experts,
+                                     uint64_t rows, uint64_t n, uint64_t k, void* y,
+                                     int64_t y_stride, void* ws, size_t ws_bytes, void* stream) {
+  const ApiRange nvtx_range(__func__);
+  const Call c{{rows, experts, n, k}, type, offsets, y, type, 0, y_stride, 0, ws, ws_bytes,
+               static_cast<cudaStream_t>(stream)};
+  return rows_product<kForward>(c, {weight, weight_batch_stride, weight_stride, experts, n, k},
+                                {x, 0, x_stride, 1, rows, k});
+}
+
+extern "C" int sparcml_expert_linear_dx(const void* dy, int64_t dy_stride, const void* weight,
+                                        int64_t weight_batch_stride, int64_t weight_stride,
+                                        int32_t type, const int32_t* offsets, uint32_t experts,
+                                        uint64_t rows, uint64_t n, uint64_t k, void* dx,
+                                        int64_t dx_stride, void* ws, size_t ws_bytes,
+                                        void* stream) {
+  const ApiRange nvtx_range(__func__);
+  const Call c{{rows, experts, n, k}, type, offsets, dx, type, 0, dx_stride, 0, ws, ws_bytes,
+               static_cast<cudaStream_t>(stream)};
+  return rows_product<kInput>(c, {weight, weight_batch_stride, weight_stride, experts, n, k},
+                              {dy, 0, dy_stride, 1, rows, n});
+}
+
+extern "C" int sparcml_expert_linear_dweight(const void* dy, int64_t dy_stride, const void* x,
+                                             int64_t x_stride, int32_t type,
+                                             const int32_t* offsets, uint32_t experts,
+                                             uint64_t rows, uint64_t n, uint64_t k, float* dweight,
+                                             int64_t dweight_batch_stride, int64_t dweight_stride,
+                                             int32_t accumulate, void* ws, size_t ws_bytes,
+                                             void* stream) {
+  const ApiRange nvtx_range(__func__);
+  const Call c{{rows, experts, n, k}, type, offsets, dweight, SPARCML_F32, dweight_batch_stride,
+               dweight_stride, accumulate, ws, ws_bytes, static_cast<cudaStream_t>(stream)};
+  const int r = check_call(c);
+  if (r != SPARCML_OK) return r;
+  return weight_product(c, {x, 0, x_stride, 1, rows, k}, {dy, 0, dy_stride, 1, rows, n});
+}
+
+extern "C" int sparcml_expert_linear_dweight8(
+    const void* dy, int64_t dy_stride, int32_t type, const int8_t* codes, int64_t codes_stride,
+    const uint8_t* exponents, int64_t exponents_stride, const int32_t* offsets, uint32_t experts,
+    uint64_t rows, uint64_t n, uint64_t k, float* dweight, int64_t dweight_batch_stride,
+    int64_t dweight_stride, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+  const ApiRange nvtx_range(__func__);
+  Call c{{rows, experts, n, k}, type, offsets, dweight, SPARCML_F32, dweight_batch_stride,
+         dweight_stride, accumulate, ws, ws_bytes, static_cast<cudaStream_t>(stream)};
+  int r = check_call(c);
+  if (r != SPARCML_OK) return r;
+  Operand x{nullptr, 0, (int64_t)align_up(k, 8), 1, rows, k};
+  const size_t copy = x.copy_bytes();
+  if (ws_bytes < 256 + c.z.part_bytes() + copy) return SPARCML_ERR_WORKSPACE;
+  // x in 16 bits at the workspace's end
+  c.ws_bytes = (ws_bytes - copy) / 256 * 256;
+  x.p = static_cast<uint8_t*>(ws) + c.ws_bytes;
+  r = sparcml_restore8(codes, codes_stride, exponents, exponents_stride, rows, k,
+                       const_cast<void*>(x.p), type, x.stride, stream);
+  if (r != SPARCML_OK) return r;
+  return weight_product(c, x, {dy, 0, dy_stride, 1, rows, n});
+}

@@ -12,82 +12,10 @@
 
 #include <algorithm>
 
-#include "types.cuh"
+#include "rows.cuh"
 
 namespace sparcml {
 namespace {
-
-// The `threads` threads that share a row: 8, 16 or 32 lanes of a warp, or whole warps
-// with a named barrier and 2 * 33 float2 of shared memory of their own.
-struct Group {
-  uint32_t threads, index, t;  // their number, which group of the block, this thread's place
-  float2* scratch;
-  uint32_t turn;
-
-  __device__ __forceinline__ void sync() const {
-    if (threads > 32)
-      asm volatile("bar.sync %0, %1;" ::"r"(index + 1), "r"(threads) : "memory");
-    else
-      __syncwarp();
-  }
-  template <int D>
-  static __device__ __forceinline__ void add(float2& v) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, D);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, D);
-  }
-  __device__ __forceinline__ float sum(float2 two) {
-    float v = two.x + two.y;
-    if (threads >= 32) v += __shfl_xor_sync(0xffffffffu, v, 16);
-    if (threads >= 16) v += __shfl_xor_sync(0xffffffffu, v, 8);
-#pragma unroll
-    for (int d = 4; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    if (threads <= 32) return v;
-    float2* s = scratch + 33 * (turn & 1u);
-    ++turn;
-    const uint32_t lane = lane_id(), nw = threads >> 5;
-    if (lane == 0) s[t >> 5].x = v;
-    sync();
-    v = lane < nw ? s[lane].x : 0.f;
-    if (nw > 8) {
-      if (nw > 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-    }
-#pragma unroll
-    for (int d = 4; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return __shfl_sync(0xffffffffu, v, 0);
-  }
-  // Sums of two values. `turn` alternates between the halves of the scratch from call to
-  // call, so that one barrier per call is enough.
-  __device__ __forceinline__ float2 sum2(float2 v) {
-    if (threads >= 32) add<16>(v);
-    if (threads >= 16) add<8>(v);
-    add<4>(v);
-    add<2>(v);
-    add<1>(v);
-    if (threads <= 32) return v;
-    float2* s = scratch + 33 * (turn & 1u);
-    ++turn;
-    const uint32_t lane = lane_id(), nw = threads >> 5;
-    if (lane == 0) s[t >> 5] = v;
-    sync();
-    v = lane < nw ? s[lane] : make_float2(0.f, 0.f);
-    if (nw > 8) {
-      if (nw > 16) add<16>(v);
-      add<8>(v);
-    }
-    add<4>(v);
-    add<2>(v);
-    add<1>(v);
-    // the lanes that were added up hold the sum; the first one tells the rest
-    v.x = __shfl_sync(0xffffffffu, v.x, 0);
-    v.y = __shfl_sync(0xffffffffu, v.y, 0);
-    return v;
-  }
-};
-__device__ __forceinline__ Group make_group(uint32_t threads, float2* scratch) {
-  const uint32_t index = threadIdx.x / threads;
-  return {threads, index, threadIdx.x - index * threads, scratch + 66 * index, 0};
-}
 
 // A row on its way into shared memory, as the aligned pieces of 16 bytes that cover it;
 // element c comes to lie at slot + row_skew + c. What a first piece holds before the row
@@ -422,7 +350,7 @@ struct NormGradArgs {
   float* part_b;
   uint32_t threads;  // that share a row
   bool w_packs;      // as in NormArgs
-  uint32_t* ticket;  // null: norm_join_kernel joins the blocks' sums
+  uint32_t* ticket;  // null: join_columns_kernel joins the blocks' sums
   float* dweight;
   float* dbias;
   int32_t accumulate;
@@ -434,7 +362,7 @@ struct NormGradArgs {
 // each thread copies ahead and reads back its own packs alone, so the ring needs no
 // barrier; other rows (V = 2) as in the forward pass. At the
 // end the groups' sums are joined, and then the blocks', by the last block to
-// finish (`ticket`, few sums) or by norm_join_kernel. Every order is fixed.
+// finish (`ticket`, few sums) or by join_columns_kernel. Every order is fixed.
 constexpr int kRing = 3;
 
 template <typename T, typename W, int V, int NV, int LANES, int MAXT, int MINB>
@@ -813,46 +741,6 @@ __global__ void __launch_bounds__(128) norm_columns_kernel(const NormGradArgs a)
   }
 }
 
-// out[c] (+)= sum of the `parts` partial sums of column c: 32 columns per block,
-// 16 warps over the parts, joined in warp order. blockIdx.y: 0 dw, 1 db.
-__global__ void __launch_bounds__(512)
-norm_join_kernel(const float* __restrict__ part_w, const float* __restrict__ part_b,
-                 uint32_t parts, uint64_t dim, float* dw, float* db, int32_t accumulate) {
-  griddep_wait();
-  __shared__ float sums[16][33];
-  const float* part = blockIdx.y ? part_b : part_w;
-  float* out = blockIdx.y ? db : dw;
-  if (out == nullptr) return;
-  const uint32_t lane = lane_id(), warp = threadIdx.x >> 5;
-  const uint64_t c = (uint64_t)blockIdx.x * 32 + lane;
-  float s = 0.f;
-  if (c < dim) {
-    for (uint32_t p = warp; p < parts; p += 16 * 20) {
-      float v[20];  // on their way together
-#pragma unroll
-      for (uint32_t k = 0; k < 20; ++k)
-        v[k] = p + 16 * k < parts ? part[(uint64_t)(p + 16 * k) * dim + c] : 0.f;
-#pragma unroll
-      for (uint32_t k = 0; k < 20; ++k) s += v[k];
-    }
-  }
-  sums[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < dim) {
-    float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v += sums[k][lane];
-    out[c] = accumulate ? out[c] + v : v;
-  }
-}
-
-// Threads that share a row, in whole warps, when each holds `per` elements.
-uint32_t threads_for(uint64_t dim, uint32_t per) {
-  return (uint32_t)((dim + 32ull * per - 1) / (32ull * per)) * 32u;
-}
-
-constexpr uint32_t kSms = 152;
-
 // Threads of a block for a row beyond registers: two blocks of an SM, of 1024 threads where 32
 // registers are enough, else (packs of eight) of 512 (4096 x 16384 bf16 161 us against 183 for
 // the gradients with one block of 1024; fp32 229, against 251 with blocks of 512).
@@ -930,25 +818,6 @@ bool forward_typed(NormArgs a, cudaStream_t s) {
   return true;
 }
 
-constexpr uint32_t kBackwardPer = 16;  // elements per thread
-
-// Threads of a row and of a block, and the blocks, each with a row of partial sums: what
-// the registers of the SMs hold at one time (kFit blocks of 256 threads each; with a
-// second, partial wave 16384 x 4096 fp32 took 271 us), no more than there are rows.
-constexpr uint32_t kFit = 2;
-struct BackwardShape {
-  uint32_t threads, block, parts;
-};
-BackwardShape backward_shape(uint64_t rows, uint64_t dim) {
-  const uint32_t threads = dim <= 128   ? 8
-                           : dim <= 256 ? 16
-                                        : (uint32_t)std::min<uint64_t>(
-                                              512, threads_for(dim, kBackwardPer));
-  const uint32_t groups = std::max(1u, 256 / threads);
-  const uint64_t most = kSms * (threads <= 256 ? kFit : 1);
-  return {threads, threads * groups,
-          (uint32_t)std::max<uint64_t>(1, std::min((rows + groups - 1) / groups, most))};
-}
 // Up to this many partial sums the last block to finish joins them: that saves the host a
 // launch, 2 us of a call that waits for the host (10.7 against 12.7 at every size up to 16 K
 // sums), and costs time on the device, ticket against launch: 450 sums 4.5 and 3.6 us, 2 K 5.3 and
@@ -1018,7 +887,7 @@ bool backward_typed(NormGradArgs a, bool sums, uint8_t* ws, cudaStream_t s) {
   }
   const bool join = sums && !ticket;
   if (join)
-    launch_pdl(norm_join_kernel, dim3((unsigned)((a.dim + 31) / 32), 2), 512, 0, s, a.part_w,
+    launch_pdl(join_columns_kernel, dim3((unsigned)((a.dim + 31) / 32), 2), 512, 0, s, a.part_w,
                a.part_b, h.parts, a.dim, a.dweight, a.dbias, a.accumulate);
   note_launches(1 + (longer && sums) + join);
   return ok;
@@ -1095,7 +964,7 @@ extern "C" int sparcml_layer_norm_backward(const void* dy, int64_t dy_stride, co
     return launch_status() == SPARCML_OK && ok ? SPARCML_OK : SPARCML_ERR_CUDA;
   }
   if (sums) {  // of no rows
-    launch_pdl(norm_join_kernel, dim3((unsigned)((dim + 31) / 32), 2), 512, 0, s,
+    launch_pdl(join_columns_kernel, dim3((unsigned)((dim + 31) / 32), 2), 512, 0, s,
                static_cast<const float*>(nullptr), static_cast<const float*>(nullptr), 0u, dim,
                dweight, dbias, accumulate);
     if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;

@@ -468,22 +468,6 @@ __device__ __forceinline__ void store_box(uint32_t box, __half* out, uint64_t pi
     if (row0 + q + r < rows) *reinterpret_cast<uint4*>(o) = lds128(box + box_at(q + r, c));
 }
 
-// Before a block leaves that gave up, or whose partner did: until the operands have landed. A
-// pair's loads all report to the first block, in one phase per stage for both blocks; where the
-// two stopped at different stages (`apart`) some phases never complete, and the loads get their
-// time instead.
-__device__ __noinline__ void land_operands(uint32_t full, uint32_t stages, uint32_t stage,
-                                           uint32_t phase, bool apart) {
-  if (apart) {
-    const uint64_t end = global_ns() + 1000ull * kLandUs;
-    while (global_ns() < end) __nanosleep(1000);
-    return;
-  }
-  Waits alone = {0, kLandUs};
-  for (uint32_t s = 0; s < stages; ++s)
-    mbar_wait(full + 8 * s, s < stage ? phase : phase ^ 1u, &alone);
-}
-
 // What becomes of a product's entry, for all products alike:
 //     r = f acc + (r0 + r1 d_j) in_ij
 // with d the diagonal vector of column j, and in what stands at that place:
@@ -1374,32 +1358,9 @@ steps_kernel(const __grid_constant__ Maps m, const __grid_constant__ StepArgs a)
 // ---------------------------------------------------------------------------
 // Host side.
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
 bool encode(CUtensorMap* map, const void* p, uint32_t rank, const cuuint64_t* dims,
             const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
-  const EncodeTiled fn = encode_tiled();
-  const cuuint32_t step[4] = {1, 1, 1, 1};
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank, const_cast<void*>(p), dims, strides,
-                  box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, rank, dims, strides, box, swizzle);
 }
 
 struct Matrices {  // fp16 [batch][rows][pitch], of which `cols` columns exist

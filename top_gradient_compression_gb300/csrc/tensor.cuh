@@ -64,6 +64,11 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
 }
+// The same, ordering what this thread and those it has synchronised with wrote before.
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -90,7 +95,7 @@ struct Waits {
 
 // Waits until the barrier's phase `parity` has completed. False, with gave_up
 // set, when that takes longer than the limit or another warp gave up meanwhile.
-__device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, Waits* waits) {
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, Waits* waits) {
   const uint64_t end = global_ns() + 1000ull * waits->limit_us;
   while (!mbar_try_wait(bar, parity)) {
     if (waits->gave_up != 0) return false;
@@ -140,6 +145,19 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
+// A tile of three axes, also for one block of a pair.
+template <int CG>
+__device__ __forceinline__ void tma_load_3d_group(uint32_t dst, const CUtensorMap* map, uint32_t x,
+                                                  uint32_t y, uint32_t z, uint32_t bar) {
+  if constexpr (CG == 1)
+    tma_load_3d(dst, map, x, y, z, bar);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier"
+        "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
 // Orders this thread's ordinary accesses to global or to shared memory with the
 // asynchronous copies' ones.
 __device__ __forceinline__ void proxy_fence_global() {
@@ -158,9 +176,10 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead, uint
          ((uint64_t)(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: fp16 operands, fp32 accumulator, M x N.
-__host__ __device__ constexpr uint32_t mma_desc(uint32_t m, uint32_t n, bool a_mn, bool b_mn) {
-  return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) |
+// Instruction descriptor: fp16 (or bf16) operands, fp32 accumulator, M x N.
+__host__ __device__ constexpr uint32_t mma_desc(uint32_t m, uint32_t n, bool a_mn, bool b_mn,
+                                                bool bf16 = false) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) |
          ((m >> 4) << 24);
 }
 
@@ -242,6 +261,53 @@ __device__ __forceinline__ void tmem_load_wait(float (&v)[16]) {
                  "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
+}
+
+// Before a block leaves that gave up, or whose partner did: until the operands have landed. A
+// pair's loads all report to the first block, in one phase per stage for both blocks; where the
+// two stopped at different stages (`apart`) some phases never complete, and the loads get their
+// time instead.
+static __device__ __noinline__ void land_operands(uint32_t full, uint32_t stages, uint32_t stage,
+                                           uint32_t phase, bool apart) {
+  if (apart) {
+    const uint64_t end = global_ns() + 1000ull * kLandUs;
+    while (global_ns() < end) __nanosleep(1000);
+    return;
+  }
+  Waits alone = {0, kLandUs};
+  for (uint32_t s = 0; s < stages; ++s)
+    mbar_wait(full + 8 * s, s < stage ? phase : phase ^ 1u, &alone);
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiled encode_tiled() {
+  static EncodeTiled fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiled>(p);
+  }();
+  return fn;
+}
+
+inline bool encode_map(CUtensorMap* map, CUtensorMapDataType type, const void* p, uint32_t rank,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                       CUtensorMapSwizzle swizzle) {
+  const EncodeTiled fn = encode_tiled();
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn && fn(map, type, rank, const_cast<void*>(p), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace sparcml
