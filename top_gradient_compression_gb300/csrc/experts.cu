@@ -20,7 +20,10 @@
 // block works out the same list of tiles from them. A long summed axis with few tiles is split; the
 // parts are added in order by a second launch.
 //
-// Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. For dW, the rows
+// Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. The tensor cores
+// drop the bits that do not fit when they add to an accumulator, always towards zero: over 16,384
+// rows dW came out 1.9e-5 off, and that is an fp32 result. So an accumulator takes 512 rows, and
+// the writers' registers add those sums, rounded: 5e-7. For dW, the rows
 // of the last 64 that belong to the next expert are zeros in both operands, so that what stands
 // there, a NaN say, does not count.
 
@@ -44,6 +47,7 @@ constexpr uint32_t kStageBytes = 2 * kOperand, kStages = 6;
 constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
 constexpr uint32_t kBox = 32;        // rows of Q per load
 constexpr uint32_t kLeastBlocks = 8;  // of 64 in a part of a split sum, at least
+constexpr uint32_t kRun = 8;          // dW: blocks of 64 rows that one accumulator takes
 constexpr uint32_t kBand = 8;        // tiles along j that are taken together, for L2's sake
 
 enum Form { kForward, kInput, kWeight };
@@ -249,33 +253,60 @@ __device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const 
   return true;
 }
 
+// Until a stage is full. With dW, ordinary stores of either block may be part of that, so the wait
+// acquires for the pair. (As a fence of its own it took a microsecond for every block: 572 us
+// against 181 for 16384 x 2048 x 4096.)
+template <int FORM>
+__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity, Waits* waits) {
+  if constexpr (FORM != kWeight) return mbar_wait_warp(bar, parity, waits);
+  bool come = false;
+  for (uint32_t i = 0; i < 64 && !come; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    come = ok != 0;
+  }
+  if (!come) {
+    come = mbar_wait_long(bar, parity, waits);
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  }
+  return __all_sync(0xffffffffu, come);
+}
+
 template <int FORM>
 __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const Item& it) {
   constexpr bool P_MN = FORM != kForward, Q_MN = FORM == kWeight;
   constexpr uint32_t step_p = P_MN ? 2048 : 32, step_q = Q_MN ? 2048 : 32;
   const uint32_t idesc = mma_desc(256, it.width, P_MN, Q_MN, a.bf16);
-  const uint32_t acc = w.acc & 1u;
-  if (!mbar_wait_warp(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
-  tmem_fence_after();
-  const uint32_t d = w.tmem + acc * kSide;
-  for (uint32_t b = it.s0; b < it.s1; ++b, w.next_stage()) {
-    const uint32_t s = w.stage;
-    if (!mbar_wait_warp(w.full + 8 * s, w.phase, w.waits)) return false;
-    if (FORM == kWeight) asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  for (uint32_t b = it.s0; b < it.s1;) {
+    const uint32_t from = b, end = FORM == kWeight ? min(b + kRun, it.s1) : it.s1;
+    const uint32_t acc = w.acc & 1u;
+    if (!mbar_wait_warp(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
     tmem_fence_after();
-    if (w.leader) {
-      const uint32_t p = w.ring + s * kStageBytes, q = p + kOperand;
+    const uint32_t d = w.tmem + acc * kSide;
+    for (; b < end; ++b, w.next_stage()) {
+      const uint32_t s = w.stage;
+      if (!wait_full<FORM>(w.full + 8 * s, w.phase, w.waits)) return false;
+      tmem_fence_after();
+      if (w.leader) {
+        const uint32_t p = w.ring + s * kStageBytes, q = p + kOperand;
 #pragma unroll
-      for (uint32_t k = 0; k < 4; ++k)
-        mma_f16<2>(d, tile_desc(p + k * step_p, 8192, 1024), tile_desc(q + k * step_q, 8192, 1024),
-                   idesc, b > it.s0 || k > 0);
-      mma_commit<2>(w.empty + 8 * s);
+        for (uint32_t k = 0; k < 4; ++k)
+          mma_f16<2>(d, tile_desc(p + k * step_p, 8192, 1024),
+                     tile_desc(q + k * step_q, 8192, 1024), idesc, b > from || k > 0);
+        mma_commit<2>(w.empty + 8 * s);
+      }
+      __syncwarp();
     }
+    if (w.leader) mma_commit<2>(w.acc_full + 8 * acc);
     __syncwarp();
+    ++w.acc;
   }
-  if (w.leader) mma_commit<2>(w.acc_full + 8 * acc);
-  __syncwarp();
-  ++w.acc;
   return true;
 }
 
@@ -290,43 +321,77 @@ __device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, float v) {
   }
 }
 
+// Sixteen sums of a thread's i, from column c of the tile: to their results, or where the parts of
+// a split sum wait to be added up.
+template <int FORM>
+__device__ __forceinline__ void put16(const ExpertArgs& a, const Item& it, uint32_t index,
+                                      uint32_t side, uint32_t c, const float (&v)[16]) {
+  const uint32_t i = it.i0 + side;
+  if (it.splits > 1) {
+    float* o = a.part + ((uint64_t)index * a.wide + c) * kSide + side;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) o[q * kSide] = v[q];
+  } else if (i < a.i_size) {
+    const int64_t out = (FORM == kWeight ? (int64_t)it.e * a.out_batch : 0) +
+                        (int64_t)(it.j0 + c) * a.out_stride + i;
+#pragma unroll
+    for (uint32_t q = 0; q < 16; ++q)
+      if (c + q < it.count) put(a, out + (int64_t)q * a.out_stride, v[q]);
+  }
+}
+
 // An accumulator's rows are i, its columns j: a warp has 32 neighbouring i, so that it writes
-// whole stretches of a result's row as they come.
+// whole stretches of a result's row as they come. The two warps of a quarter of the i alternate
+// over the columns, sixteen at a time.
 template <int FORM>
 __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const Item& it,
                                            uint32_t index) {
   const uint32_t warp = threadIdx.x >> 5, quarter = warp & 3u, half = warp >> 2;
-  const uint32_t side = 128 * w.rank + 32 * quarter + lane_id(), i = it.i0 + side;
-  const bool in = i < a.i_size, empty = it.s0 == it.s1;
-  const uint32_t acc = w.acc & 1u;
-  if (!empty) {
+  const uint32_t side = 128 * w.rank + 32 * quarter + lane_id();
+  const uint32_t src = w.tmem + (quarter << 21);
+  if constexpr (FORM == kWeight) {
+    // The sums of kRun blocks are added up here, rounded to nearest.
+    float sum[8][16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) sum[k][q] = 0.f;
+    }
+    for (uint32_t b = it.s0; b < it.s1; b += kRun) {
+      const uint32_t acc = w.acc & 1u;
+      if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
+      tmem_fence_after();
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k) {
+        const uint32_t c = 32 * k + 16 * half;
+        if (c < it.count) {
+          float v[16];
+          tmem_load16(src + acc * kSide + c, v);
+          tmem_load_wait(v);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) sum[k][q] += v[q];
+        }
+      }
+      tmem_fence_before();
+      __syncwarp();
+      if (lane_id() == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
+      ++w.acc;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+      if (32 * k + 16 * half < it.count)
+        put16<FORM>(a, it, index, side, 32 * k + 16 * half, sum[k]);
+  } else {
+    const uint32_t acc = w.acc & 1u;
     if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
     tmem_fence_after();
-  }
-  const uint32_t src = w.tmem + acc * kSide + (quarter << 21);
-  const int64_t out = (FORM == kWeight ? (int64_t)it.e * a.out_batch : 0) +
-                      (int64_t)it.j0 * a.out_stride + i;
 #pragma unroll 1
-  for (uint32_t c = 16 * half; c < it.count; c += 32) {
-    float v[16];
-    if (!empty) {
-      tmem_load16(src + c, v);
+    for (uint32_t c = 16 * half; c < it.count; c += 32) {
+      float v[16];
+      tmem_load16(src + acc * kSide + c, v);
       tmem_load_wait(v);
-    } else {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) v[q] = 0.f;
+      put16<FORM>(a, it, index, side, c, v);
     }
-    if (it.splits > 1) {
-      float* o = a.part + ((uint64_t)index * a.wide + c) * kSide + side;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) o[q * kSide] = v[q];
-    } else if (in) {
-#pragma unroll
-      for (uint32_t q = 0; q < 16; ++q)
-        if (c + q < it.count) put(a, out + (int64_t)(c + q) * a.out_stride, v[q]);
-    }
-  }
-  if (!empty) {
     tmem_fence_before();
     __syncwarp();
     if (lane_id() == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
@@ -400,7 +465,7 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
     if (w.rank == 0 && !withhold)
       for (uint32_t x = w.pair; x < items; x += w.pairs) {
         const Item it = item_of<FORM>(a, table, x);
-        if (it.s0 < it.s1 && !issue_item<FORM>(w, a, it)) break;
+        if (!issue_item<FORM>(w, a, it)) break;
       }
   } else {
     for (uint32_t x = w.pair; x < items; x += w.pairs)
