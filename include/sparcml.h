@@ -617,7 +617,8 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  *             layer's slice of a node's flat gradient, at any offset. An
  *             expert without rows gets +0. accumulate != 0 adds to what it
  *             holds.
- *   dweight8  takes x in 8 bits; `type` is then dy's.
+ *   backward  dx or dweight NULL: that gradient is left out, and weight or x
+ *             is not read. backward8 takes x in 8 bits.
  *   experts 1 .. 1024, rows 0 .. 2^31 - 1, n and k 1 .. 2^24.
  *   ws        >= sparcml_expert_linear_workspace_size(...) bytes, 256-byte
  *             aligned, for all of them. aligned != 0: every operand starts on 16
@@ -633,24 +634,23 @@ int sparcml_expert_linear(const void* x, int64_t x_stride, const void* weight,
                           const int32_t* offsets, uint32_t experts, uint64_t rows, uint64_t n,
                           uint64_t k, void* y, int64_t y_stride, void* ws, size_t ws_bytes,
                           void* stream);
-int sparcml_expert_linear_dx(const void* dy, int64_t dy_stride, const void* weight,
-                             int64_t weight_batch_stride, int64_t weight_stride, int32_t type,
-                             const int32_t* offsets, uint32_t experts, uint64_t rows, uint64_t n,
-                             uint64_t k, void* dx, int64_t dx_stride, void* ws, size_t ws_bytes,
-                             void* stream);
-int sparcml_expert_linear_dweight(const void* dy, int64_t dy_stride, const void* x,
-                                  int64_t x_stride, int32_t type, const int32_t* offsets,
-                                  uint32_t experts, uint64_t rows, uint64_t n, uint64_t k,
-                                  float* dweight, int64_t dweight_batch_stride,
-                                  int64_t dweight_stride, int32_t accumulate, void* ws,
-                                  size_t ws_bytes, void* stream);
-int sparcml_expert_linear_dweight8(const void* dy, int64_t dy_stride, int32_t type,
-                                   const int8_t* codes, int64_t codes_stride,
-                                   const uint8_t* exponents, int64_t exponents_stride,
-                                   const int32_t* offsets, uint32_t experts, uint64_t rows,
-                                   uint64_t n, uint64_t k, float* dweight,
+int sparcml_expert_linear_backward(const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const void* weight,
+                                   int64_t weight_batch_stride, int64_t weight_stride,
+                                   int32_t type, const int32_t* offsets, uint32_t experts,
+                                   uint64_t rows, uint64_t n, uint64_t k, void* dx,
+                                   int64_t dx_stride, float* dweight,
                                    int64_t dweight_batch_stride, int64_t dweight_stride,
                                    int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+int sparcml_expert_linear_backward8(const void* dy, int64_t dy_stride, const int8_t* codes,
+                                    int64_t codes_stride, const uint8_t* exponents,
+                                    int64_t exponents_stride, const void* weight,
+                                    int64_t weight_batch_stride, int64_t weight_stride,
+                                    int32_t type, const int32_t* offsets, uint32_t experts,
+                                    uint64_t rows, uint64_t n, uint64_t k, void* dx,
+                                    int64_t dx_stride, float* dweight,
+                                    int64_t dweight_batch_stride, int64_t dweight_stride,
+                                    int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
 
 /* Queries and keys, each head of `dim` elements normed and then turned by its
  * token's position p:

@@ -118,17 +118,14 @@ SIGNATURES = {
     "sparcml_expert_linear": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,
                                         C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp,
                                         C.c_int64, vp, C.c_size_t, vp]),
-    "sparcml_expert_linear_dx": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,
-                                           C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp,
-                                           C.c_int64, vp, C.c_size_t, vp]),
-    "sparcml_expert_linear_dweight": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int32, vp,
-                                                C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp,
-                                                C.c_int64, C.c_int64, C.c_int32, vp, C.c_size_t,
-                                                vp]),
-    "sparcml_expert_linear_dweight8": (C.c_int, [vp, C.c_int64, C.c_int32, vp, C.c_int64, vp,
-                                                 C.c_int64, vp, C.c_uint32, C.c_uint64, C.c_uint64,
-                                                 C.c_uint64, vp, C.c_int64, C.c_int64, C.c_int32,
-                                                 vp, C.c_size_t, vp]),
+    "sparcml_expert_linear_backward": (C.c_int, [
+        vp, C.c_int64, vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp, C.c_uint32,
+        C.c_uint64, C.c_uint64, C.c_uint64, vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,
+        C.c_size_t, vp]),
+    "sparcml_expert_linear_backward8": (C.c_int, [
+        vp, C.c_int64, vp, C.c_int64, vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,
+        C.c_uint32, C.c_uint64, C.c_uint64, C.c_uint64, vp, C.c_int64, vp, C.c_int64, C.c_int64,
+        C.c_int32, vp, C.c_size_t, vp]),
 }
 
 

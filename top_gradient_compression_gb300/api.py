@@ -1036,40 +1036,35 @@ def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
     op = _offsets(offsets, weight)
     rows, t = dy.shape[0], TYPES[dy.dtype]
     if stored:
-        p, ps, e, es, _, _ = _stored(x, "x", dy.dtype)
+        xa = _stored(x, "x", dy.dtype)[:4]
         if x.shape != (rows, k):
             raise ValueError(f"x must stand for [{rows}, {k}], got {list(x.shape)}")
     else:
         _half(x, "x", dy)
-        p, ps = _row_matrix(x, "x", rows, k)
+        xa = _row_matrix(x, "x", rows, k)
     if accumulate and need_dweight and dweight is None:
         raise ValueError("accumulate needs dweight to add to")
+    xp, xs = None, k
     if need_dx:
         if dx is None:
             dx = torch.empty((rows, k), dtype=dy.dtype, device=dy.device)
         _half(dx, "dx", dy)
         xp, xs = _row_matrix(dx, "dx", rows, k)
+    gp, gb, gs = None, 0, k
     if need_dweight:
         if dweight is None:
             dweight = torch.empty(weight.shape, dtype=torch.float32, device=dy.device)
         if not dweight.is_cuda or dweight.dtype != torch.float32 or dweight.shape != weight.shape:
             raise TypeError(f"dweight must be a float32 CUDA tensor of {list(weight.shape)}")
         gb, gs = _experts(dweight, "dweight")[:2]
+        gp = dweight.data_ptr()
     wp, wn = _fit((rows, experts, n, k), ws, dy.device, dy, weight, *(() if stored else (x,)))
-    lib, s = _lib._lib or _lib.load(), _raw_stream(dy)
-    if need_dx:
-        r = lib.sparcml_expert_linear_dx(dp, ds, weight.data_ptr(), wb, wst, t, op, experts, rows,
-                                         n, k, xp, xs, wp, wn, s)
-        if r:
-            _check("sparcml_expert_linear_dx", r)
-    if need_dweight:
-        tail = (op, experts, rows, n, k, dweight.data_ptr(), gb, gs, int(accumulate), wp, wn, s)
-        if stored:
-            r = lib.sparcml_expert_linear_dweight8(dp, ds, t, p, ps, e, es, *tail)
-        else:
-            r = lib.sparcml_expert_linear_dweight(dp, ds, p, ps, t, *tail)
-        if r:
-            _check("sparcml_expert_linear_dweight", r)
+    lib = _lib._lib or _lib.load()
+    f = lib.sparcml_expert_linear_backward8 if stored else lib.sparcml_expert_linear_backward
+    r = f(dp, ds, *xa, weight.data_ptr(), wb, wst, t, op, experts, rows, n, k, xp, xs, gp, gb, gs,
+          accumulate, wp, wn, _raw_stream(dy))
+    if r:
+        _check("sparcml_expert_linear_backward", r)
     return dx if need_dx else None, dweight if need_dweight else None
 
 

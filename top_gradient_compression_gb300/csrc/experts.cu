@@ -501,7 +501,8 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   if (warp == kWriters) tmem_free<2>(w.tmem, 2 * kSide);
 }
 
-// The parts of split sums, added in their order: a warp takes 256 i of one j at a time.
+// The parts of split sums, added in their order: four rows of 256 i for a block at a time, four
+// neighbouring i for a thread.
 template <int FORM>
 __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__ ExpertArgs a,
                                                          uint32_t pairs) {
@@ -509,44 +510,54 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
   griddep_wait();
   if (threadIdx.x < 32) make_table<FORM>(a, table, pairs);
   __syncthreads();
-  const uint32_t items = table.first[a.experts], lane = lane_id();
-  const uint32_t groups = a.wide / 16;  // of 16 j
-  for (uint32_t x = blockIdx.x; x < items * groups; x += gridDim.x) {
-    const uint32_t index = x / groups;
-    const Item it = item_of<FORM>(a, table, index);
-    if (it.splits == 1 || it.split != 0) continue;
-    const uint32_t j0 = 16 * (x - index * groups) + (threadIdx.x >> 5) * 2;
-#pragma unroll
-    for (uint32_t j = j0; j < j0 + 2; ++j) {
-      if (j >= it.count) continue;
-      float v[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) v[q] = 0.f;
-      const float* p = a.part + ((uint64_t)index * a.wide + j) * kSide + lane;
-#pragma unroll 4
-      for (uint32_t s = 0; s < it.splits; ++s, p += (uint64_t)a.wide * kSide) {
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] += __ldcg(p + 32 * q);
-      }
-      const int64_t out = (FORM == kWeight ? (int64_t)it.e * a.out_batch : 0) +
-                          (int64_t)(it.j0 + j) * a.out_stride + it.i0 + lane;
-#pragma unroll
-      for (uint32_t q = 0; q < 8; ++q)
-        if (it.i0 + lane + 32 * q < a.i_size) put(a, out + 32 * q, v[q]);
+  const uint32_t groups = a.wide / 4;
+  const uint32_t each = ceil_of(a.i_size, kSide) * ceil_of(a.j_size, kSide);  // dW: tiles of one
+  const uint32_t tiles = FORM == kWeight ? a.experts * each : table.first[a.experts] / a.splits;
+  for (uint32_t x = blockIdx.x; x < tiles * groups; x += gridDim.x) {
+    const uint32_t tile = x / groups;
+    uint32_t index = tile * a.splits;
+    if (FORM == kWeight) {
+      const uint32_t e = tile / each;
+      const uint32_t splits = (table.first[e + 1] - table.first[e]) / each;
+      index = table.first[e] + (tile - e * each) * splits;
     }
+    const Item it = item_of<FORM>(a, table, index);
+    const uint32_t j = 4 * (x - tile * groups) + threadIdx.x / 64, i = 4 * (threadIdx.x % 64);
+    if (it.splits == 1 || j >= it.count || it.i0 + i >= a.i_size) continue;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* p =
+        reinterpret_cast<const float4*>(a.part + ((uint64_t)index * a.wide + j) * kSide + i);
+#pragma unroll 8
+    for (uint32_t s = 0; s < it.splits; ++s, p += (uint64_t)a.wide * kSide / 4) {
+      const float4 q = __ldcg(p);
+      v.x += q.x;
+      v.y += q.y;
+      v.z += q.z;
+      v.w += q.w;
+    }
+    const int64_t out = (FORM == kWeight ? (int64_t)it.e * a.out_batch : 0) +
+                        (int64_t)(it.j0 + j) * a.out_stride + it.i0 + i;
+    const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (uint32_t q = 0; q < 4; ++q)
+      if (it.i0 + i + q < a.i_size) put(a, out + q, f[q]);
   }
 }
 
-// An operand whose rows are not what TMA takes (16-byte aligned, 16 bytes a step), copied into
-// rows of `pitch` elements; 16 bytes per thread and turn.
-struct CopyArgs {
+// Operands whose rows are not what TMA takes (16-byte aligned, 16 bytes a step), copied into rows
+// of `pitch` elements; 16 bytes per thread and turn.
+struct Copy {
   const uint16_t* from;
   int64_t batch, stride;
   uint16_t* to;
   uint64_t pitch, rows, cols, all;  // all: rows of all matrices
 };
-__global__ void __launch_bounds__(256) copy_rows_kernel(const CopyArgs a) {
+struct CopyArgs {
+  Copy of[3];
+};
+__global__ void __launch_bounds__(256) copy_rows_kernel(const __grid_constant__ CopyArgs args) {
   griddep_wait();
+  const Copy& a = args.of[blockIdx.y];
   const uint64_t per = a.pitch / 8, total = a.all * per;
   for (uint64_t x = blockIdx.x * (uint64_t)blockDim.x + threadIdx.x; x < total;
        x += (uint64_t)gridDim.x * blockDim.x) {
@@ -583,7 +594,7 @@ struct Sizes {
         1, std::min<uint64_t>(kPairs / most, ceil_div(s, 64) / kLeastBlocks));
   }
   uint64_t weight_tiles() const { return experts * ceil_div(n, kSide) * ceil_div(k, kSide); }
-  bool weight_splits() const { return weight_tiles() < kPairs; }
+  bool weight_splits() const { return weight_tiles() < kPairs && rows > 64 * kLeastBlocks; }
   uint32_t wide() const { return (uint32_t)std::min<uint64_t>(kSide, align_up(rows, 16)); }
   size_t part_bytes() const {
     size_t r = 0;
@@ -606,34 +617,38 @@ struct Operand {  // `batches` matrices of `rows` rows of `cols` elements of 16 
   }
 };
 
-// Takes the workspace's copies one after the other.
-struct Room {
-  uint8_t* at;
-  size_t left;
-  void* take(size_t bytes) {
-    if (bytes > left) return nullptr;
-    void* p = at;
-    at += bytes;
-    left -= bytes;
-    return p;
+// Has operands (null: none) as TMA takes them, by copies where they are not; bytes(): what these
+// take.
+struct Settle {
+  Operand* of[3];
+  size_t bytes() const {
+    size_t r = 0;
+    for (const Operand* o : of)
+      if (o && o->rows && !o->fits()) r += o->copy_bytes();
+    return r;
+  }
+  void run(uint8_t* room, cudaStream_t s) const {
+    CopyArgs a = {};
+    unsigned count = 0;
+    uint64_t most = 0;
+    for (Operand* o : of) {
+      if (!o || !o->rows || o->fits()) continue;
+      Copy& c = a.of[count++];
+      c = {static_cast<const uint16_t*>(o->p), o->batch, o->stride,
+           reinterpret_cast<uint16_t*>(room), o->pitch(), o->rows, o->cols, o->rows * o->batches};
+      most = std::max(most, c.all * c.pitch);
+      room += o->copy_bytes();
+      o->p = c.to;
+      o->stride = (int64_t)c.pitch;
+      o->batch = (int64_t)(c.pitch * c.rows);
+    }
+    if (!count) return;
+    launch_pdl(copy_rows_kernel,
+               dim3((unsigned)std::min<uint64_t>(ceil_div(most, 8 * 256), 152 * 8), count), 256, 0,
+               s, a);
+    note_launches(1);
   }
 };
-
-// Has the operand as TMA takes it; false if the workspace has no room for a copy.
-bool settle(Operand& o, Room& room, cudaStream_t s) {
-  if (o.fits() || o.rows == 0) return true;
-  uint16_t* to = static_cast<uint16_t*>(room.take(o.copy_bytes()));
-  if (!to) return false;
-  const CopyArgs a{static_cast<const uint16_t*>(o.p), o.batch, o.stride, to, o.pitch(), o.rows,
-                   o.cols, o.rows * o.batches};
-  launch_pdl(copy_rows_kernel, (unsigned)std::min<uint64_t>(ceil_div(a.all * a.pitch, 8 * 256), 152 * 8),
-             256, 0, s, a);
-  note_launches(1);
-  o.p = to;
-  o.stride = (int64_t)o.pitch();
-  o.batch = (int64_t)(o.pitch() * o.rows);
-  return true;
-}
 
 bool map_of(CUtensorMap* map, const Operand& o, bool bf16, uint32_t box_rows) {
   const cuuint64_t row = (o.rows == 1 ? o.pitch() : (uint64_t)o.stride) * 2;
@@ -675,8 +690,9 @@ unsigned resident() {
 }
 
 template <int FORM>
-int launch_experts(const ExpertMaps& m, const ExpertArgs& a, uint64_t most_items, bool join,
-                   cudaStream_t s) {
+int launch_experts(const ExpertMaps& m, const ExpertArgs& a, uint64_t most_items,
+                   uint64_t join_units, cudaStream_t s) {
+  const bool join = join_units > 0;
   auto kernel = experts_kernel<FORM>;
   const unsigned fit = resident<FORM>();
   if (fit == 0 || !ensure_smem(reinterpret_cast<const void*>(kernel), kSmem))
@@ -698,7 +714,8 @@ int launch_experts(const ExpertMaps& m, const ExpertArgs& a, uint64_t most_items
   (void)cudaLaunchKernelEx(&cfg, kernel, m, a);
   if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
   if (join) {
-    launch_pdl(join_parts_kernel<FORM>, 152 * 4, 256, 0, s, a, pairs);
+    launch_pdl(join_parts_kernel<FORM>, (unsigned)std::min<uint64_t>(join_units, 152 * 8), 256, 0,
+               s, a, pairs);
     if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
   }
   note_launches(1 + join);
@@ -709,25 +726,17 @@ struct Call {
   Sizes z;
   int32_t type;
   const int32_t* offsets;
-  void* out;
-  int32_t out_type;
-  int64_t out_batch, out_stride;
-  int32_t accumulate;
   void* ws;
   size_t ws_bytes;
   cudaStream_t stream;
 };
 
+// The product of operands that TMA takes.
 template <int FORM>
-int run(const Call& c, Operand p, Operand q) {
+int run(const Call& c, Operand p, Operand q, void* out, int32_t out_type, int64_t out_batch,
+        int64_t out_stride, int32_t accumulate) {
   const Sizes& z = c.z;
   uint8_t* w = static_cast<uint8_t*>(c.ws);
-  const size_t parts = z.part_bytes();
-  if (c.ws_bytes < 256 + parts + (p.fits() ? 0 : p.copy_bytes()) + (q.fits() ? 0 : q.copy_bytes()))
-    return SPARCML_ERR_WORKSPACE;
-  Room room{w + 256 + parts, c.ws_bytes - 256 - parts};
-  if (!settle(p, room, c.stream) || !settle(q, room, c.stream)) return SPARCML_ERR_WORKSPACE;
-  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
   ExpertArgs a = {};
   a.offsets = c.offsets;
   a.experts = (uint32_t)z.experts;
@@ -738,27 +747,25 @@ int run(const Call& c, Operand p, Operand q) {
   a.splits = FORM == kWeight ? 1 : z.splits(a.i_size, a.s_size);
   a.may_split = FORM == kWeight && z.weight_splits();
   a.wide = FORM == kWeight ? kSide : z.wide();
-  a.out = c.out;
-  a.out_type = c.out_type;
-  a.out_batch = c.out_batch;
-  a.out_stride = c.out_stride;
-  a.accumulate = c.accumulate;
+  a.out = out;
+  a.out_type = out_type;
+  a.out_batch = out_batch;
+  a.out_stride = out_stride;
+  a.accumulate = accumulate;
   a.bf16 = c.type == SPARCML_BF16;
   a.part = reinterpret_cast<float*>(w + 256);
   a.status = reinterpret_cast<int32_t*>(w);
   a.inject = reinterpret_cast<const uint32_t*>(w + kInjectOffset);
   ExpertMaps m;
-  if (FORM == kWeight && z.rows == 0) {  // no operand is read
-    p = q = Operand{w, 64, 64, 1, 1, 64};
-  }
+  if (z.rows == 0) p = q = Operand{w, 64, 64, 1, 1, 64};  // no operand is read
   if (!map_of(&m.p, p, a.bf16, FORM == kForward ? 128 : 64) ||
       !map_of(&m.q, q, a.bf16, FORM == kWeight ? 64 : kBox))
     return SPARCML_ERR_CUDA;
-  const bool join = FORM == kWeight ? a.may_split : a.splits > 1;
-  const uint64_t most = FORM == kWeight
-                            ? (a.may_split ? kPairs : z.weight_tiles())
-                            : ceil_div(a.i_size, kSide) *
-                                  (std::min(z.experts, z.rows) + z.rows / kSide) * a.splits;
+  const uint64_t tiles = FORM == kWeight ? z.weight_tiles()
+                                         : ceil_div(a.i_size, kSide) *
+                                               (std::min(z.experts, z.rows) + z.rows / kSide);
+  const uint64_t join = a.may_split || a.splits > 1 ? tiles * (a.wide / 4) : 0;
+  const uint64_t most = a.may_split ? kPairs : tiles * a.splits;
   return launch_experts<FORM>(m, a, std::max<uint64_t>(1, most), join, c.stream);
 }
 
@@ -779,28 +786,59 @@ bool operand_ok(const Operand& o) {
   return o.rows == 0 || (o.p && aligned_to(o.p, 2) && o.stride >= 0 && o.batch >= 0);
 }
 
-template <int FORM>
-int rows_product(const Call& c, const Operand& w, const Operand& q) {
-  int r = check_call(c);
-  if (r != SPARCML_OK) return r;
-  if (c.z.rows == 0) return SPARCML_OK;
-  if (!operand_ok(w) || !operand_ok(q) || !c.out || !aligned_to(c.out, 2) ||
-      !rows_apart(c.z.rows, FORM == kForward ? c.z.n : c.z.k, c.out_stride))
-    return SPARCML_ERR_INVALID_ARG;
-  return run<FORM>(c, w, q);
+bool result_ok(const void* p, uint64_t rows, uint64_t cols, int64_t stride) {
+  return rows == 0 || (p && aligned_to(p, 2) && rows_apart(rows, cols, stride));
+}
+// dW: matrices one after the other, or their rows in turn.
+bool matrices_ok(const float* p, const Sizes& z, int64_t batch, int64_t stride) {
+  const int64_t n = (int64_t)z.n, k = (int64_t)z.k, e = (int64_t)z.experts;
+  if (!aligned_to(p, 4) || batch < 0 || stride < 0 || (n > 1 && stride < k)) return false;
+  return e == 1 || batch >= (n - 1) * stride + k ||
+         (batch >= k && (n == 1 || stride >= (e - 1) * batch + k));
 }
 
-int weight_product(const Call& c, const Operand& x, const Operand& dy) {
+struct Stored {  // x in 8 bits
+  const int8_t* codes;
+  int64_t codes_stride;
+  const uint8_t* exponents;
+  int64_t exponents_stride;
+};
+
+// dx and dW, each where it is wanted; x as it is, or in 8 bits.
+int backward(const Call& c, Operand dy, Operand x, const Stored* stored, Operand w, void* dx,
+             int64_t dx_stride, float* dweight, int64_t dw_batch, int64_t dw_stride,
+             int32_t accumulate) {
   const Sizes& z = c.z;
-  if (!operand_ok(x) || !operand_ok(dy) || !c.out || !aligned_to(c.out, 4) || c.out_stride < 0 ||
-      c.out_batch < 0 || !rows_apart(z.n, z.k, c.out_stride) ||
-      (z.experts > 1 && c.out_batch < (int64_t)z.k) ||
-      // matrices one after the other, or their rows in turn
-      !(z.experts == 1 || c.out_batch >= (int64_t)(z.n - 1) * c.out_stride + (int64_t)z.k ||
-        z.n == 1 ||
-        c.out_stride >= (int64_t)(z.experts - 1) * c.out_batch + (int64_t)z.k))
+  int r = check_call(c);
+  if (r != SPARCML_OK) return r;
+  if (!operand_ok(dy) || (dx && (!operand_ok(w) || !result_ok(dx, z.rows, z.k, dx_stride))) ||
+      (dweight && ((!stored && !operand_ok(x)) || !matrices_ok(dweight, z, dw_batch, dw_stride))))
     return SPARCML_ERR_INVALID_ARG;
-  return run<kWeight>(c, x, dy);
+  const bool rows = z.rows > 0;
+  const bool input = dx && rows, weights = dweight != nullptr;
+  Operand plain = x;
+  if (stored) plain = {nullptr, 0, (int64_t)align_up(z.k, 8), 1, z.rows, z.k};
+  const Settle copies{{input || weights ? &dy : nullptr, input ? &w : nullptr,
+                       weights && !stored ? &plain : nullptr}};
+  const size_t restored = stored && weights ? plain.copy_bytes() : 0;
+  const size_t parts = z.part_bytes(), copied = copies.bytes();
+  if (c.ws_bytes < 256 + parts + restored + copied) return SPARCML_ERR_WORKSPACE;
+  uint8_t* room = static_cast<uint8_t*>(c.ws) + 256 + parts;
+  if (restored) {
+    plain.p = room;
+    r = sparcml_restore8(stored->codes, stored->codes_stride, stored->exponents,
+                         stored->exponents_stride, z.rows, z.k, room, c.type, plain.stride,
+                         c.stream);
+    if (r != SPARCML_OK) return r;
+  }
+  copies.run(room + restored, c.stream);
+  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  if (input) {
+    r = run<kInput>(c, w, dy, dx, c.type, 0, dx_stride, 0);
+    if (r != SPARCML_OK) return r;
+  }
+  return weights ? run<kWeight>(c, plain, dy, dweight, SPARCML_F32, dw_batch, dw_stride, accumulate)
+                 : SPARCML_OK;
 }
 
 }  // namespace
@@ -826,58 +864,50 @@ extern "C" int sparcml_expert_linear(const void* x, int64_t x_stride, const void
                                      uint64_t rows, uint64_t n, uint64_t k, void* y,
                                      int64_t y_stride, void* ws, size_t ws_bytes, void* stream) {
   const ApiRange nvtx_range(__func__);
-  const Call c{{rows, experts, n, k}, type, offsets, y, type, 0, y_stride, 0, ws, ws_bytes,
+  const Call c{{rows, experts, n, k}, type, offsets, ws, ws_bytes,
                static_cast<cudaStream_t>(stream)};
-  return rows_product<kForward>(c, {weight, weight_batch_stride, weight_stride, experts, n, k},
-                                {x, 0, x_stride, 1, rows, k});
-}
-
-extern "C" int sparcml_expert_linear_dx(const void* dy, int64_t dy_stride, const void* weight,
-                                        int64_t weight_batch_stride, int64_t weight_stride,
-                                        int32_t type, const int32_t* offsets, uint32_t experts,
-                                        uint64_t rows, uint64_t n, uint64_t k, void* dx,
-                                        int64_t dx_stride, void* ws, size_t ws_bytes,
-                                        void* stream) {
-  const ApiRange nvtx_range(__func__);
-  const Call c{{rows, experts, n, k}, type, offsets, dx, type, 0, dx_stride, 0, ws, ws_bytes,
-               static_cast<cudaStream_t>(stream)};
-  return rows_product<kInput>(c, {weight, weight_batch_stride, weight_stride, experts, n, k},
-                              {dy, 0, dy_stride, 1, rows, n});
-}
-
-extern "C" int sparcml_expert_linear_dweight(const void* dy, int64_t dy_stride, const void* x,
-                                             int64_t x_stride, int32_t type,
-                                             const int32_t* offsets, uint32_t experts,
-                                             uint64_t rows, uint64_t n, uint64_t k, float* dweight,
-                                             int64_t dweight_batch_stride, int64_t dweight_stride,
-                                             int32_t accumulate, void* ws, size_t ws_bytes,
-                                             void* stream) {
-  const ApiRange nvtx_range(__func__);
-  const Call c{{rows, experts, n, k}, type, offsets, dweight, SPARCML_F32, dweight_batch_stride,
-               dweight_stride, accumulate, ws, ws_bytes, static_cast<cudaStream_t>(stream)};
   const int r = check_call(c);
   if (r != SPARCML_OK) return r;
-  return weight_product(c, {x, 0, x_stride, 1, rows, k}, {dy, 0, dy_stride, 1, rows, n});
+  Operand w{weight, weight_batch_stride, weight_stride, experts, n, k};
+  Operand q{x, 0, x_stride, 1, rows, k};
+  if (rows == 0) return SPARCML_OK;
+  if (!operand_ok(w) || !operand_ok(q) || !result_ok(y, rows, n, y_stride))
+    return SPARCML_ERR_INVALID_ARG;
+  const Settle copies{{&w, &q, nullptr}};
+  const size_t parts = c.z.part_bytes();
+  if (ws_bytes < 256 + parts + copies.bytes()) return SPARCML_ERR_WORKSPACE;
+  copies.run(static_cast<uint8_t*>(ws) + 256 + parts, c.stream);
+  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  return run<kForward>(c, w, q, y, type, 0, y_stride, 0);
 }
 
-extern "C" int sparcml_expert_linear_dweight8(
-    const void* dy, int64_t dy_stride, int32_t type, const int8_t* codes, int64_t codes_stride,
-    const uint8_t* exponents, int64_t exponents_stride, const int32_t* offsets, uint32_t experts,
-    uint64_t rows, uint64_t n, uint64_t k, float* dweight, int64_t dweight_batch_stride,
-    int64_t dweight_stride, int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+extern "C" int sparcml_expert_linear_backward(
+    const void* dy, int64_t dy_stride, const void* x, int64_t x_stride, const void* weight,
+    int64_t weight_batch_stride, int64_t weight_stride, int32_t type, const int32_t* offsets,
+    uint32_t experts, uint64_t rows, uint64_t n, uint64_t k, void* dx, int64_t dx_stride,
+    float* dweight, int64_t dweight_batch_stride, int64_t dweight_stride, int32_t accumulate,
+    void* ws, size_t ws_bytes, void* stream) {
   const ApiRange nvtx_range(__func__);
-  Call c{{rows, experts, n, k}, type, offsets, dweight, SPARCML_F32, dweight_batch_stride,
-         dweight_stride, accumulate, ws, ws_bytes, static_cast<cudaStream_t>(stream)};
-  int r = check_call(c);
-  if (r != SPARCML_OK) return r;
-  Operand x{nullptr, 0, (int64_t)align_up(k, 8), 1, rows, k};
-  const size_t copy = x.copy_bytes();
-  if (ws_bytes < 256 + c.z.part_bytes() + copy) return SPARCML_ERR_WORKSPACE;
-  // x in 16 bits at the workspace's end
-  c.ws_bytes = (ws_bytes - copy) / 256 * 256;
-  x.p = static_cast<uint8_t*>(ws) + c.ws_bytes;
-  r = sparcml_restore8(codes, codes_stride, exponents, exponents_stride, rows, k,
-                       const_cast<void*>(x.p), type, x.stride, stream);
-  if (r != SPARCML_OK) return r;
-  return weight_product(c, x, {dy, 0, dy_stride, 1, rows, n});
+  const Call c{{rows, experts, n, k}, type, offsets, ws, ws_bytes,
+               static_cast<cudaStream_t>(stream)};
+  return backward(c, {dy, 0, dy_stride, 1, rows, n}, {x, 0, x_stride, 1, rows, k}, nullptr,
+                  {weight, weight_batch_stride, weight_stride, experts, n, k}, dx, dx_stride,
+                  dweight, dweight_batch_stride, dweight_stride, accumulate);
+}
+
+extern "C" int sparcml_expert_linear_backward8(
+    const void* dy, int64_t dy_stride, const int8_t* codes, int64_t codes_stride,
+    const uint8_t* exponents, int64_t exponents_stride, const void* weight,
+    int64_t weight_batch_stride, int64_t weight_stride, int32_t type, const int32_t* offsets,
+    uint32_t experts, uint64_t rows, uint64_t n, uint64_t k, void* dx, int64_t dx_stride,
+    float* dweight, int64_t dweight_batch_stride, int64_t dweight_stride, int32_t accumulate,
+    void* ws, size_t ws_bytes, void* stream) {
+  const ApiRange nvtx_range(__func__);
+  const Call c{{rows, experts, n, k}, type, offsets, ws, ws_bytes,
+               static_cast<cudaStream_t>(stream)};
+  const Stored x{codes, codes_stride, exponents, exponents_stride};
+  if (dweight && rows && (!codes || !exponents)) return SPARCML_ERR_INVALID_ARG;
+  return backward(c, {dy, 0, dy_stride, 1, rows, n}, {}, &x,
+                  {weight, weight_batch_stride, weight_stride, experts, n, k}, dx, dx_stride,
+                  dweight, dweight_batch_stride, dweight_stride, accumulate);
 }

@@ -25,32 +25,6 @@ namespace {
 constexpr uint32_t kWarps = 8;      // per block
 constexpr uint32_t kMostDim = 512;  // elements of a head
 
-// V consecutive elements as they lie in memory: four (in 16 bits, 8 bytes: eight of them per lane
-// leave too few registers), or one.
-constexpr int kPack = 4;
-template <typename T, int V>
-struct Piece {
-  Pack<T, V> r;
-  __device__ __forceinline__ void load(const T* p) { r = *reinterpret_cast<const Pack<T, V>*>(p); }
-  __device__ __forceinline__ void get(float (&f)[V]) const {
-#pragma unroll
-    for (int i = 0; i < V; ++i) f[i] = to_f32(r.e[i]);
-  }
-  static __device__ __forceinline__ void put(T* p, const float (&f)[V]) {
-    Pack<T, V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.e[i] = from_f32<T>(f[i]);
-    *reinterpret_cast<Pack<T, V>*>(p) = r;
-  }
-};
-template <typename T>
-struct Piece<T, 1> {
-  T v;
-  __device__ __forceinline__ void load(const T* p) { v = *p; }
-  __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32(v); }
-  static __device__ __forceinline__ void put(T* p, const float (&f)[1]) { *p = from_f32<T>(f[0]); }
-};
-
 struct Heads {  // an array [tokens][heads][dim]
   const void* p;
   int64_t token, head;  // strides in elements
@@ -63,7 +37,7 @@ struct Side {  // queries, or keys
 struct HeadArgs {
   Side side[2];
   uint64_t tokens;
-  uint32_t dim, turned, units, lanes;  // units of V pairs; L
+  uint32_t dim, turned, units, lanes;  // units of V pairs each; L
   const void* positions;
   int32_t wide;  // positions are int64, else int32
   const float* freqs;
@@ -86,85 +60,199 @@ __device__ __forceinline__ uint64_t turn_fraction(float freq) {
 // of its pairs (PAIRS: neighbours, both pieces holding whole pairs), of the others any two
 // pieces. `second`: whether the second one exists (the last element of an odd head is alone).
 struct Place {
-  uint32_t at0, at1, pair;
-  bool there, second, turns;
+  uint32_t at0, at1;
+  bool there, second;
 };
 template <int V, bool PAIRS>
 __device__ __forceinline__ Place place_of(const HeadArgs& a, uint32_t unit) {
   Place p;
   const uint32_t half = a.turned / 2, p0 = unit * V;
+  const bool turns = p0 < half;
   p.there = unit < a.units;
-  p.turns = p0 < half;
-  p.pair = p0;
-  const uint32_t from = p.turns ? 0 : a.turned, q = p.turns ? p0 : p0 - half;
-  const uint32_t apart = p.turns ? half : (a.dim - a.turned + 1) / 2;
+  const uint32_t from = turns ? 0 : a.turned, q = turns ? p0 : p0 - half;
+  const uint32_t apart = turns ? half : (a.dim - a.turned + 1) / 2;
   p.at0 = from + (PAIRS ? 2 * q : q);
   p.at1 = p.at0 + (PAIRS ? V : apart);
   p.second = p.there && p.at1 < a.dim;
   return p;
 }
-
-// A lane's elements of one head: lo and hi are the members of its pairs.
-template <typename T, int V, bool PAIRS>
-__device__ __forceinline__ void members(const Piece<T, V>& a, const Piece<T, V>& b,
-                                        float (&lo)[V], float (&hi)[V]) {
-  float x[V], y[V];
-  a.get(x);
-  b.get(y);
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if constexpr (PAIRS && V > 1) {
-      lo[i] = 2 * i < V ? x[2 * i % V] : y[2 * i % V];
-      hi[i] = 2 * i < V ? x[2 * i % V + 1] : y[2 * i % V + 1];
-    } else {
-      lo[i] = x[i];
-      hi[i] = y[i];
-    }
-  }
-}
-template <typename T, int V, bool PAIRS>
-__device__ __forceinline__ void put_members(T* to, const Place& p, const float (&lo)[V],
-                                            const float (&hi)[V]) {
-  float x[V], y[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if constexpr (PAIRS && V > 1) {
-      x[i] = i & 1 ? hi[i / 2] : lo[i / 2];
-      y[i] = i & 1 ? hi[V / 2 + i / 2] : lo[V / 2 + i / 2];
-    } else {
-      x[i] = lo[i];
-      y[i] = hi[i];
-    }
-  }
-  if (p.there) Piece<T, V>::put(to + p.at0, x);
-  if (p.second) Piece<T, V>::put(to + p.at1, y);
-}
-
-// Weights of a lane's elements, in the order of lo and hi.
+// The elements of the unit's pair i.
 template <int V, bool PAIRS>
-__device__ __forceinline__ void load_weights(const HeadArgs& a, const void* w, const Place& p,
-                                             float (&lo)[V], float (&hi)[V]) {
+__device__ __forceinline__ uint2 pair_elements(const Place& p, uint32_t i) {
+  return PAIRS && V > 1 ? make_uint2(p.at0 + 2 * i, p.at0 + 2 * i + 1)
+                        : make_uint2(p.at0 + i, p.at1 + i);
+}
+
+// What a lane reads of one head: NU units of V pairs, each as two pieces, of which those that do
+// not exist are zeros. RING: on its way through shared memory, kRing jobs ahead, where a lane
+// copies and reads back its own pieces alone; else (16-bit elements one by one, which no
+// asynchronous copy takes) in registers, one job ahead. (With one job ahead in registers 24 KB of
+// an SM's reads were on their way at a time, and 16384 x 40 x 128 bf16 took 95 us.)
+constexpr int kRing = 4;
+template <typename T, int V, int NU>
+struct Piece {
+  static constexpr bool RING = V * sizeof(T) >= 4;
+  static constexpr uint32_t kBytes = V * sizeof(T);
+  static constexpr uint32_t kSlot = RING ? 2 * NU * kBytes : 0;  // of a lane
+  Pack<T, V> a[NU], b[NU];
+
+  // `to`: the lane's place in the slot's first piece, of 32 lanes each
+  __device__ __forceinline__ void load(const T* p, const Place (&at)[NU], bool active,
+                                       uint32_t to) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    lo[i] = hi[i] = 1.f;
-    const uint32_t c0 = PAIRS && V > 1 ? p.at0 + 2 * i : p.at0 + i;
-    const uint32_t c1 = PAIRS && V > 1 ? c0 + 1 : p.at1 + i;
-    if (w && p.there) lo[i] = load_any(w, a.w_type, c0);
-    if (w && p.second) hi[i] = load_any(w, a.w_type, c1);
+    for (int j = 0; j < NU; ++j) {
+      if constexpr (RING) {
+        copy(to + 2 * j * 32 * kBytes, p + (at[j].there ? at[j].at0 : 0), active && at[j].there);
+        copy(to + (2 * j + 1) * 32 * kBytes, p + (at[j].second ? at[j].at1 : 0),
+             active && at[j].second);
+      } else {
+        a[j] = b[j] = Pack<T, V>{};
+        if (active && at[j].there) a[j] = *reinterpret_cast<const Pack<T, V>*>(p + at[j].at0);
+        if (active && at[j].second) b[j] = *reinterpret_cast<const Pack<T, V>*>(p + at[j].at1);
+      }
+    }
+  }
+  static __device__ __forceinline__ void copy(uint32_t to, const T* from, bool there) {
+    const uint32_t bytes = there ? kBytes : 0;  // the rest is filled with zeros
+    if constexpr (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                   "l"(from), "r"(bytes)
+                   : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(to),
+                   "l"(from), "r"(bytes), "n"(kBytes)
+                   : "memory");
+  }
+  __device__ __forceinline__ void arrive(const uint8_t* from) {
+    if constexpr (RING) {
+#pragma unroll
+      for (int j = 0; j < NU; ++j) {
+        a[j] = *reinterpret_cast<const Pack<T, V>*>(from + 2 * j * 32 * kBytes);
+        b[j] = *reinterpret_cast<const Pack<T, V>*>(from + (2 * j + 1) * 32 * kBytes);
+      }
+    }
+  }
+  // lo and hi: the members of its pairs, two pairs to an F2. With V = 1 its units are the pairs.
+  template <bool PAIRS>
+  __device__ __forceinline__ void get(F2 (&lo)[V * NU / 2], F2 (&hi)[V * NU / 2]) const {
+#pragma unroll
+    for (int k = 0; k < V * NU; k += 2) {
+      const int j = k / V, i = k % V;
+      if constexpr (PAIRS && V > 1) {
+        const Pack<T, V>& from = 2 * i < V ? a[j] : b[j];
+        const F2 u = two(from, 2 * i % V), v = two(from, 2 * i % V + 2);
+        lo[k / 2] = f2(u.x, v.x);
+        hi[k / 2] = f2(u.y, v.y);
+      } else if constexpr (V > 1) {
+        lo[k / 2] = two(a[j], i);
+        hi[k / 2] = two(b[j], i);
+      } else {
+        lo[k / 2] = f2(to_f32(a[k].e[0]), to_f32(a[k + 1].e[0]));
+        hi[k / 2] = f2(to_f32(b[k].e[0]), to_f32(b[k + 1].e[0]));
+      }
+    }
+  }
+  // Elements i and i + 1 of a piece.
+  static __device__ __forceinline__ F2 two(const Pack<T, V>& p, int i) {
+    if constexpr (sizeof(T) == 4)
+      return f2(p.e[i], p.e[i + 1]);
+    else
+      return unpack2<T>(reinterpret_cast<const uint32_t*>(&p)[i / 2]);
+  }
+};
+template <typename T, int V>
+__device__ __forceinline__ void set_two(Pack<T, V>& p, int i, F2 v) {
+  if constexpr (sizeof(T) == 4) {
+    p.e[i] = v.x;
+    p.e[i + 1] = v.y;
+  } else {
+    reinterpret_cast<uint32_t*>(&p)[i / 2] = pack2<T>(v);
+  }
+}
+template <typename T, int V, int NU, bool PAIRS>
+__device__ __forceinline__ void put_members(T* to, const Place (&at)[NU],
+                                            const F2 (&lo)[V * NU / 2],
+                                            const F2 (&hi)[V * NU / 2]) {
+  auto one = [](const F2& v, int i) { return i & 1 ? v.y : v.x; };
+#pragma unroll
+  for (int j = 0; j < NU; ++j) {
+    Pack<T, V> x, y;
+    if constexpr (V == 1) {
+      x.e[0] = from_f32<T>(one(lo[j / 2], j));
+      y.e[0] = from_f32<T>(one(hi[j / 2], j));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        // elements i, i + 1 of the first piece are pair i / 2, of the second V / 2 + i / 2
+        const int p = j * V + i / 2, q = p + V / 2, k = (j * V + i) / 2;
+        set_two(x, i, PAIRS ? f2(one(lo[p / 2], p), one(hi[p / 2], p)) : lo[k]);
+        set_two(y, i, PAIRS ? f2(one(lo[q / 2], q), one(hi[q / 2], q)) : hi[k]);
+      }
+    }
+    if (at[j].there) *reinterpret_cast<Pack<T, V>*>(to + at[j].at0) = x;
+    if (at[j].second) *reinterpret_cast<Pack<T, V>*>(to + at[j].at1) = y;
   }
 }
 
-// BACK: the gradients, else the forward pass. NU units of V pairs per lane.
+// A lane's V * NU pairs of a vector in shared memory that holds one value for each pair.
+template <int V, int NU>
+__device__ __forceinline__ void from_table(const float* t, uint32_t l, uint32_t lanes,
+                                           F2 (&v)[V * NU / 2]) {
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int j = 0; j < NU; j += 2) v[j / 2] = f2(t[l + j * lanes], t[l + (j + 1) * lanes]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < NU; ++j) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(t + (l + j * lanes) * V + i);
+        v[(j * V + i) / 2] = f2(f.x, f.y);
+        v[(j * V + i) / 2 + 1] = f2(f.z, f.w);
+      }
+    }
+  }
+}
+
+// Where the rings begin in shared memory.
+__host__ __device__ __forceinline__ uint32_t ring_offset(uint32_t all, uint32_t half) {
+  return ((4 + 2 * kWarps) * all * 4 + half * 8 + 15) / 16 * 16;
+}
+
+// BACK: the gradients, else the forward pass. NU units of V pairs per lane. Arithmetic is on two
+// pairs at a time.
 template <typename T, int V, int NU, bool PAIRS, bool BACK, int MINB>
 __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs a) {
   griddep_wait();
-  // [turned / 2] fractions of a turn, then for each warp [turned / 2] cosines and sines; at the
-  // end of the backward pass [warps][dim] sums
+  constexpr int N = V * NU / 2;  // of F2
+  // Shared memory, `all` being the pairs of 32 lanes: both sides' weights of the pairs' first and
+  // second members [2][2][all], for each warp the cosines and the sines [2][all], the fractions
+  // of a turn [turned / 2], for each warp the ring of what it reads (x, and g); at the end of the
+  // backward pass [warps][dim] sums.
   extern __shared__ __align__(16) uint8_t dynamic[];
   const uint32_t half = a.turned / 2, lane = lane_id(), warp = threadIdx.x >> 5;
-  uint64_t* const fraction = reinterpret_cast<uint64_t*>(dynamic);
-  float2* const table = reinterpret_cast<float2*>(fraction + half) + warp * half;
+  const uint32_t all = a.lanes * V * NU;
+  float* const weights = reinterpret_cast<float*>(dynamic);
+  float* const cosine = weights + 4 * all + 2 * all * warp;
+  float* const sine = cosine + all;
+  uint64_t* const fraction = reinterpret_cast<uint64_t*>(weights + (4 + 2 * kWarps) * all);
+  using Mine = Piece<T, V, NU>;
+  constexpr uint32_t kSlot = 32 * Mine::kSlot * (BACK ? 2 : 1);
+  uint8_t* const ring = dynamic + ring_offset(all, half) + warp * kRing * kSlot +
+                        lane * Mine::kBytes;
   for (uint32_t i = threadIdx.x; i < half; i += blockDim.x) fraction[i] = turn_fraction(a.freqs[i]);
+  for (uint32_t i = threadIdx.x; i < 2 * all; i += blockDim.x) {
+    const uint32_t k = i >= all, c = i - k * all, unit = c / V;
+    const Place p = place_of<V, PAIRS>(a, unit);
+    const uint2 e = pair_elements<V, PAIRS>(p, c - unit * V);
+    const void* w = a.side[k].w;
+    weights[2 * k * all + c] = w && p.there ? load_any(w, a.w_type, e.x) : 1.f;
+    weights[(2 * k + 1) * all + c] = w && p.second ? load_any(w, a.w_type, e.y) : 1.f;
+  }
+  for (uint32_t i = lane; i < all; i += 32) {  // what is not turned: once and for all
+    cosine[i] = 1.f;
+    sine[i] = 0.f;
+  }
   __syncthreads();
 
   // this warp's side and run of jobs
@@ -179,150 +267,157 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
   const uint32_t slots = 32 / a.lanes, slot = lane / a.lanes, l = lane - slot * a.lanes;
   const float inv = 1.f / (float)a.dim;
   Place place[NU];
-  float w0[NU][V], w1[NU][V], s0[BACK ? NU : 1][V], s1[BACK ? NU : 1][V];
 #pragma unroll
-  for (int j = 0; j < NU; ++j) {
-    place[j] = place_of<V, PAIRS>(a, l + j * a.lanes);
-    load_weights<V, PAIRS>(a, side.w, place[j], w0[j], w1[j]);
-    if constexpr (BACK) {
+  for (int j = 0; j < NU; ++j) place[j] = place_of<V, PAIRS>(a, l + j * a.lanes);
+  // Backward: weights, and the sums of their gradients. Forward: the four products of weights
+  // with cosines and sines.
+  F2 w0[N], w1[N], s0[N], s1[N];
+  const float* const w_lo = weights + 2 * keys * all;
+  if constexpr (BACK) {
+    from_table<V, NU>(w_lo, l, a.lanes, w0);
+    from_table<V, NU>(w_lo + all, l, a.lanes, w1);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s0[j][i] = s1[j][i] = 0.f;
-    }
+    for (int i = 0; i < N; ++i) s0[i] = s1[i] = f2(0.f, 0.f);
   }
   uint64_t token = side.jobs ? job / side.jobs : 0;
   uint32_t part = (uint32_t)(job - token * side.jobs);
 
-  Piece<T, V> x0[NU], x1[NU], g0[BACK ? NU : 1], g1[BACK ? NU : 1];
-  auto fetch = [&](uint64_t tok, uint32_t part_) {
-    const uint32_t head = part_ * slots + slot;
-    if (head >= side.heads) return;
-    const T* x = static_cast<const T*>(side.x.p) + (int64_t)tok * side.x.token +
-                 (int64_t)head * side.x.head;
-    const T* g = static_cast<const T*>(side.g.p) + (int64_t)tok * side.g.token +
-                 (int64_t)head * side.g.head;
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      if (place[j].there) x0[j].load(x + place[j].at0);
-      if (place[j].second) x1[j].load(x + place[j].at1);
-      if constexpr (BACK) {
-        if (place[j].there) g0[j].load(g + place[j].at0);
-        if (place[j].second) g1[j].load(g + place[j].at1);
+  Mine x, g;
+  // the jobs are fetched in order, `ahead` of their turn
+  constexpr uint32_t kAhead = Mine::RING ? kRing - 1 : 1;
+  uint64_t next_token = token, next_job = job;
+  uint32_t next_part = part, slot_in = 0, slot_out = 0;
+  auto fetch = [&]() {
+    if (next_job < end) {
+      const bool active = next_part * slots + slot < side.heads;
+      const uint32_t head = min(next_part * slots + slot, side.heads - 1);
+      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring + slot_in * kSlot));
+      x.load(static_cast<const T*>(side.x.p) + (int64_t)next_token * side.x.token +
+                 (int64_t)head * side.x.head, place, active, to);
+      if constexpr (BACK)
+        g.load(static_cast<const T*>(side.g.p) + (int64_t)next_token * side.g.token +
+                   (int64_t)head * side.g.head, place, active, to + 32 * Mine::kSlot);
+      ++next_job;
+      if (++next_part == side.jobs) {
+        next_part = 0;
+        ++next_token;
       }
+      slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
     }
+    if constexpr (Mine::RING) asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (job < end) fetch(token, part);
+  for (uint32_t k = 0; k < kAhead; ++k) fetch();
   bool known = false;
-  float cs[NU][V], sn[NU][V];
   for (; job < end; ++job) {
     const uint32_t head = part * slots + slot;
     const bool active = head < side.heads;
-    float lo[NU][V], hi[NU][V], glo[BACK ? NU : 1][V], ghi[BACK ? NU : 1][V];
-#pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      members<T, V, PAIRS>(x0[j], x1[j], lo[j], hi[j]);
-      if constexpr (BACK) members<T, V, PAIRS>(g0[j], g1[j], glo[j], ghi[j]);
-      // what was not loaded counts as zero
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (!active || !place[j].there) lo[j][i] = 0.f;
-        if (!active || !place[j].second) hi[j][i] = 0.f;
-        if constexpr (BACK) {
-          if (!active || !place[j].there) glo[j][i] = 0.f;
-          if (!active || !place[j].second) ghi[j][i] = 0.f;
-        }
-      }
+    F2 lo[N], hi[N], glo[N], ghi[N];
+    if constexpr (Mine::RING) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      x.arrive(ring + slot_out * kSlot);
+      if constexpr (BACK) g.arrive(ring + slot_out * kSlot + 32 * Mine::kSlot);
+      slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
     }
+    x.template get<PAIRS>(lo, hi);
+    if constexpr (BACK) g.template get<PAIRS>(glo, ghi);
     const uint64_t now = token;
     if (++part == side.jobs) {
       part = 0;
       ++token;
     }
-    if (job + 1 < end) fetch(token, part);
+    fetch();
     if (!known) {
-      const int64_t position = a.wide ? static_cast<const int64_t*>(a.positions)[now]
-                                      : static_cast<const int32_t*>(a.positions)[now];
-      __syncwarp();
-      for (uint32_t i = lane; i < half; i += 32) {
-        const uint64_t turn = (uint64_t)position * fraction[i];
-        float sine, cosine;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sine, &cosine);
-        table[i] = make_float2(cosine, sine);
+      if (half) {
+        const int64_t position = a.wide ? static_cast<const int64_t*>(a.positions)[now]
+                                        : static_cast<const int32_t*>(a.positions)[now];
+        __syncwarp();
+        for (uint32_t i = lane; i < half; i += 32) {
+          const uint64_t turn = (uint64_t)position * fraction[i];
+          sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, sine + i, cosine + i);
+        }
+        __syncwarp();
       }
-      __syncwarp();
+      if constexpr (!BACK) {  // out = r (lo w0 c - hi w1 s), r (lo w0 s + hi w1 c)
+        F2 c[N], s[N], u[N], v[N];
+        from_table<V, NU>(cosine, l, a.lanes, c);
+        from_table<V, NU>(sine, l, a.lanes, s);
+        from_table<V, NU>(w_lo, l, a.lanes, u);
+        from_table<V, NU>(w_lo + all, l, a.lanes, v);
 #pragma unroll
-      for (int j = 0; j < NU; ++j) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float2 t = place[j].turns && place[j].there ? table[place[j].pair + i]
-                                                            : make_float2(1.f, 0.f);
-          cs[j][i] = t.x;
-          sn[j][i] = t.y;
+        for (int i = 0; i < N; ++i) {
+          w0[i] = mul2<true>(u[i], c[i]);
+          s0[i] = mul2<true>(u[i], s[i]);
+          w1[i] = mul2<true>(v[i], c[i]);
+          s1[i] = mul2<true>(v[i], f2(-s[i].x, -s[i].y));
         }
       }
     }
     known = token == now;
 
-    float2 s = make_float2(0.f, 0.f);
+    F2 ss = f2(0.f, 0.f), dot = f2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
+    for (int i = 0; i < N; ++i) {
+      ss = fma2<true>(lo[i], lo[i], ss);
+      ss = fma2<true>(hi[i], hi[i], ss);
+    }
+    if constexpr (BACK) {
+      F2 c[N], s[N];
+      from_table<V, NU>(cosine, l, a.lanes, c);
+      from_table<V, NU>(sine, l, a.lanes, s);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        s.x += lo[j][i] * lo[j][i];
-        s.x += hi[j][i] * hi[j][i];
-        if constexpr (BACK) {
-          const float t = glo[j][i] * cs[j][i] + ghi[j][i] * sn[j][i];
-          ghi[j][i] = ghi[j][i] * cs[j][i] - glo[j][i] * sn[j][i];
-          glo[j][i] = t;
-          s.y += t * w0[j][i] * lo[j][i];
-          s.y += ghi[j][i] * w1[j][i] * hi[j][i];
-        }
+      for (int i = 0; i < N; ++i) {  // the gradient turned back
+        const F2 t = fma2<true>(ghi[i], s[i], mul2<true>(glo[i], c[i]));
+        ghi[i] = fma2<true>(glo[i], f2(-s[i].x, -s[i].y), mul2<true>(ghi[i], c[i]));
+        glo[i] = t;
+        dot = fma2<true>(mul2<true>(glo[i], w0[i]), lo[i], dot);
+        dot = fma2<true>(mul2<true>(ghi[i], w1[i]), hi[i], dot);
       }
     }
+    float2 sum = make_float2(ss.x + ss.y, dot.x + dot.y);
     for (uint32_t d = a.lanes / 2; d > 0; d >>= 1) {
-      s.x += __shfl_xor_sync(0xffffffffu, s.x, d);
-      if constexpr (BACK) s.y += __shfl_xor_sync(0xffffffffu, s.y, d);
+      sum.x += __shfl_xor_sync(0xffffffffu, sum.x, d);
+      if constexpr (BACK) sum.y += __shfl_xor_sync(0xffffffffu, sum.y, d);
     }
-    const float r = rsqrtf(s.x * inv + a.eps);
+    const float r = rsqrtf(sum.x * inv + a.eps);
+    const F2 by = f2(r, r);
     T* out = static_cast<T*>(const_cast<void*>(side.out.p)) + (int64_t)now * side.out.token +
              (int64_t)head * side.out.head;
-    const float k = BACK ? -s.y * inv * r * r * r : 0.f;
+    if constexpr (BACK) {
+      const float k = -sum.y * inv * r * r * r;
+      const F2 kk = f2(k, k);
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
-      float o0[V], o1[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if constexpr (BACK) {
-          s0[j][i] += glo[j][i] * (lo[j][i] * r);
-          s1[j][i] += ghi[j][i] * (hi[j][i] * r);
-          o0[i] = glo[j][i] * w0[j][i] * r + lo[j][i] * k;
-          o1[i] = ghi[j][i] * w1[j][i] * r + hi[j][i] * k;
-        } else {
-          const float u0 = lo[j][i] * r * w0[j][i], u1 = hi[j][i] * r * w1[j][i];
-          o0[i] = u0 * cs[j][i] - u1 * sn[j][i];
-          o1[i] = u0 * sn[j][i] + u1 * cs[j][i];
-        }
+      for (int i = 0; i < N; ++i) {  // dx = r g w + k x
+        s0[i] = fma2<true>(glo[i], mul2<true>(lo[i], by), s0[i]);
+        s1[i] = fma2<true>(ghi[i], mul2<true>(hi[i], by), s1[i]);
+        lo[i] = fma2<true>(mul2<true>(glo[i], w0[i]), by, mul2<true>(lo[i], kk));
+        hi[i] = fma2<true>(mul2<true>(ghi[i], w1[i]), by, mul2<true>(hi[i], kk));
       }
-      if (active) put_members<T, V, PAIRS>(out, place[j], o0, o1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const F2 u = mul2<true>(lo[i], by), v = mul2<true>(hi[i], by);
+        lo[i] = fma2<true>(v, s1[i], mul2<true>(u, w0[i]));
+        hi[i] = fma2<true>(u, s0[i], mul2<true>(v, w1[i]));
+      }
     }
+    if (active) put_members<T, V, NU, PAIRS>(out, place, lo, hi);
   }
   if constexpr (BACK) {
     if (a.part[0] == nullptr) return;  // neither sum is wanted
     // a warp's slots by shuffles, then the block's warps in order
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncthreads();
     float* const sums = reinterpret_cast<float*>(dynamic) + warp * a.dim;
 #pragma unroll
-    for (int j = 0; j < NU; ++j) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        for (uint32_t d = a.lanes; d < 32; d <<= 1) {
-          s0[j][i] += __shfl_xor_sync(0xffffffffu, s0[j][i], d);
-          s1[j][i] += __shfl_xor_sync(0xffffffffu, s1[j][i], d);
-        }
-        const uint32_t c0 = PAIRS && V > 1 ? place[j].at0 + 2 * i : place[j].at0 + i;
-        const uint32_t c1 = PAIRS && V > 1 ? c0 + 1 : place[j].at1 + i;
-        if (slot == 0 && place[j].there) sums[c0] = s0[j][i];
-        if (slot == 0 && place[j].second) sums[c1] = s1[j][i];
+    for (int k = 0; k < 2 * N; ++k) {
+      float u = k & 1 ? s0[k / 2].y : s0[k / 2].x, v = k & 1 ? s1[k / 2].y : s1[k / 2].x;
+      for (uint32_t d = a.lanes; d < 32; d <<= 1) {
+        u += __shfl_xor_sync(0xffffffffu, u, d);
+        v += __shfl_xor_sync(0xffffffffu, v, d);
       }
+      const uint2 e = pair_elements<V, PAIRS>(place[k / V], k % V);
+      if (slot == 0 && place[k / V].there) sums[e.x] = u;
+      if (slot == 0 && place[k / V].second) sums[e.y] = v;
     }
     __syncthreads();
     const uint32_t id0 = blockIdx.x * kWarps;
@@ -346,7 +441,7 @@ uint32_t grid_for(uint64_t jobs, uint32_t fit) {
   return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((jobs + kWarps - 1) / kWarps, kSms * fit));
 }
 
-// Each returns the blocks of its grid.
+// Each returns the blocks of its grid, 0 if the launch failed.
 template <typename T, int V, int NU, bool PAIRS, bool BACK, int FIT>
 uint32_t launch_heads(HeadArgs a, cudaStream_t s) {
   const uint32_t slots = 32 / a.lanes;
@@ -363,9 +458,13 @@ uint32_t launch_heads(HeadArgs a, cudaStream_t s) {
   if (a.side[1].jobs) a.warps[0] = std::min(warps - 1, a.warps[0]);
   a.warps[1] = warps - a.warps[0];
   if (a.part[0]) a.part[1] = a.part[0] + (uint64_t)grid * a.dim;
-  const size_t half = a.turned / 2;
-  const size_t smem = std::max(half * 8 * (1 + kWarps), BACK ? kWarps * a.dim * sizeof(float) : 0);
-  launch_pdl(heads_kernel<T, V, NU, PAIRS, BACK, FIT>, grid, 32 * kWarps, smem, s, a);
+  const size_t all = (size_t)a.lanes * V * NU;
+  size_t smem = ring_offset((uint32_t)all, a.turned / 2) +
+                kWarps * kRing * 32 * Piece<T, V, NU>::kSlot * (BACK ? 2 : 1);
+  if (BACK) smem = std::max(smem, kWarps * a.dim * sizeof(float));
+  auto kernel = heads_kernel<T, V, NU, PAIRS, BACK, FIT>;
+  if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return 0;
+  launch_pdl(kernel, grid, 32 * kWarps, smem, s, a);
   return grid;
 }
 
@@ -376,39 +475,50 @@ uint32_t lanes_for(uint32_t units, uint32_t nu) {
   return l;
 }
 
+// `pack` neighbouring elements are one access, 1 where they are not aligned.
 template <typename T, bool PAIRS, bool BACK>
-uint32_t heads_typed(HeadArgs a, bool packs, cudaStream_t s) {
-  const uint32_t pairs = (a.dim + 1) / 2;
-  a.units = packs ? pairs / kPack : pairs;
-  // two units per lane where 32 lanes do not hold a head: more than 256 elements
-  if (packs && a.units <= 32) {
-    a.lanes = lanes_for(a.units, 1);
-    return launch_heads<T, kPack, 1, PAIRS, BACK, BACK ? 2 : 4>(a, s);
-  }
-  if (packs) {
+uint32_t heads_typed(HeadArgs a, uint32_t pack, cudaStream_t s) {
+  a.units = (a.dim + 1) / 2 / pack;
+  if (pack == 1) {
+    a.units = (a.dim + 1) / 2;
+    if (a.units <= 64) {
+      a.lanes = lanes_for(a.units, 2);
+      return launch_heads<T, 1, 2, PAIRS, BACK, BACK ? 2 : 4>(a, s);
+    }
     a.lanes = 32;
-    return launch_heads<T, kPack, 2, PAIRS, BACK, BACK ? 1 : 2>(a, s);
+    return launch_heads<T, 1, 8, PAIRS, BACK, 1>(a, s);
   }
-  if (a.units <= 64) {
-    a.lanes = lanes_for(a.units, 2);
-    return launch_heads<T, 1, 2, PAIRS, BACK, BACK ? 2 : 4>(a, s);
+  if constexpr (sizeof(T) == 2) {
+    if (pack == 8) {
+      a.lanes = lanes_for(a.units, 1);
+      return launch_heads<T, 8, 1, PAIRS, BACK, BACK ? 2 : 3>(a, s);
+    }
+  }
+  // two units per lane where 32 lanes do not hold a head: more than 256 elements
+  if (a.units <= 32) {
+    a.lanes = lanes_for(a.units, 1);
+    return launch_heads<T, 4, 1, PAIRS, BACK, BACK ? 2 : 4>(a, s);
   }
   a.lanes = 32;
-  return launch_heads<T, 1, 8, PAIRS, BACK, 1>(a, s);
+  return launch_heads<T, 4, 2, PAIRS, BACK, BACK ? 1 : 2>(a, s);
 }
 
 template <typename T>
 uint32_t heads_any(const HeadArgs& a, bool pairs, bool back, cudaStream_t s) {
-  bool packs = a.turned % (2 * kPack) == 0 && (a.dim - a.turned) % (2 * kPack) == 0;
-  for (const Side& d : a.side)
-    for (const Heads* h : {&d.x, &d.g, &d.out})
-      packs = packs && (!d.heads || (aligned_to(h->p, sizeof(Pack<T, kPack>)) &&
-                                   h->token % kPack == 0 && h->head % kPack == 0));
+  auto packs = [&](uint32_t v) {
+    bool fit = a.turned % (2 * v) == 0 && (a.dim - a.turned) % (2 * v) == 0;
+    for (const Side& d : a.side)
+      for (const Heads* h : {&d.x, &d.g, &d.out})
+        fit = fit && (!d.heads || (aligned_to(h->p, v * sizeof(T)) && h->token % v == 0 &&
+                                   h->head % v == 0));
+    return fit;
+  };
+  const uint32_t pack = sizeof(T) == 2 && packs(8) ? 8 : packs(4) ? 4 : 1;
   if (back)
-    return pairs ? heads_typed<T, true, true>(a, packs, s)
-                 : heads_typed<T, false, true>(a, packs, s);
-  return pairs ? heads_typed<T, true, false>(a, packs, s)
-               : heads_typed<T, false, false>(a, packs, s);
+    return pairs ? heads_typed<T, true, true>(a, pack, s)
+                 : heads_typed<T, false, true>(a, pack, s);
+  return pairs ? heads_typed<T, true, false>(a, pack, s)
+               : heads_typed<T, false, false>(a, pack, s);
 }
 
 // Whether no two elements of [tokens][heads][dim] share an address: heads within tokens, or
@@ -477,10 +587,10 @@ extern "C" int sparcml_head_norm_rotary(
   if (r != SPARCML_OK) return r;
   if (tokens == 0 || q_heads + k_heads == 0) return SPARCML_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (type == SPARCML_F32) heads_any<float>(a, interleaved, false, s);
-  else if (type == SPARCML_BF16) heads_any<__nv_bfloat16>(a, interleaved, false, s);
-  else heads_any<__half>(a, interleaved, false, s);
-  if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+  const uint32_t blocks = type == SPARCML_F32    ? heads_any<float>(a, interleaved, false, s)
+                          : type == SPARCML_BF16 ? heads_any<__nv_bfloat16>(a, interleaved, false, s)
+                                                 : heads_any<__half>(a, interleaved, false, s);
+  if (launch_status() != SPARCML_OK || !blocks) return SPARCML_ERR_CUDA;
   note_launches(1);
   return SPARCML_OK;
 }
@@ -537,7 +647,7 @@ extern "C" int sparcml_head_norm_rotary_backward(
     parts = type == SPARCML_F32    ? heads_any<float>(a, interleaved, true, s)
             : type == SPARCML_BF16 ? heads_any<__nv_bfloat16>(a, interleaved, true, s)
                                    : heads_any<__half>(a, interleaved, true, s);
-    if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
+    if (launch_status() != SPARCML_OK || !parts) return SPARCML_ERR_CUDA;
     note_launches(1);
   }
   if (sums) {

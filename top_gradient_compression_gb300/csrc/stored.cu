@@ -16,43 +16,64 @@
 namespace sparcml {
 namespace {
 
-// Sixteen consecutive elements, those from `left` on as zeros; PACKS: they are aligned and all
-// there.
-template <typename T, bool PACKS>
-__device__ __forceinline__ void load16(const T* p, int left, float (&f)[16]) {
-  if constexpr (PACKS) {
-    constexpr int V = 16 / sizeof(T);
-#pragma unroll
-    for (int q = 0; q < 16 / V; ++q) {
-      F2 two[V / 2];
-      unpack<T, V>(load_raw<T, V>(p + q * V), two);
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) {
-        f[q * V + 2 * i] = two[i].x;
-        f[q * V + 2 * i + 1] = two[i].y;
-      }
-    }
+// An octet of lanes has a group of 128 columns, a lane sixteen of them: 16 / V pieces of V, the 16
+// bytes of an access, so that the octet's accesses are whole stretches of 128 bytes.
+template <int V>
+__device__ __forceinline__ uint32_t piece_column(uint32_t octet_lane, int q) {
+  return 8 * V * q + V * octet_lane;
+}
+// A lane's V elements from p, those from `left` on as zeros; `packs`: they are aligned.
+template <typename T, int V = 16 / sizeof(T)>
+__device__ __forceinline__ void load_piece(const T* p, int64_t left, bool packs, F2 (&f)[V / 2]) {
+  if (packs && left >= V) {
+    unpack<T, V>(load_raw<T, V>(p), f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = i < left ? to_f32(p[i]) : 0.f;
+    for (int i = 0; i < V / 2; ++i)
+      f[i] = f2(2 * i < left ? to_f32(p[2 * i]) : 0.f,
+                2 * i + 1 < left ? to_f32(p[2 * i + 1]) : 0.f);
   }
 }
-template <typename T, bool PACKS>
-__device__ __forceinline__ void store16(T* p, int left, const float (&f)[16]) {
-  if constexpr (PACKS) {
-    constexpr int V = 16 / sizeof(T);
-#pragma unroll
-    for (int q = 0; q < 16 / V; ++q) {
-      F2 two[V / 2];
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i) two[i] = f2(f[q * V + 2 * i], f[q * V + 2 * i + 1]);
-      *reinterpret_cast<uint4*>(p + q * V) = pack<T, V>(two);
-    }
+template <typename T, int V = 16 / sizeof(T)>
+__device__ __forceinline__ void store_piece(T* p, int64_t left, bool packs,
+                                            const F2 (&f)[V / 2]) {
+  if (packs && left >= V) {
+    *reinterpret_cast<uint4*>(p) = pack<T, V>(f);
   } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) p[i] = from_f32<T>(f[i]);
+    for (int i = 0; i < V; ++i)
+      if (i < left) p[i] = from_f32<T>(i & 1 ? f[i / 2].y : f[i / 2].x);
   }
+}
+// V codes, as one access.
+template <int V>
+struct Codes {
+  uint32_t w[V / 4];
+};
+template <int V>
+__device__ __forceinline__ Codes<V> load_codes(const int8_t* p) {
+  Codes<V> c;
+  if constexpr (V == 8) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    c.w[0] = v.x;
+    c.w[1] = v.y;
+  } else {
+    c.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  return c;
+}
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t* p, const Codes<V>& c) {
+  if constexpr (V == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(c.w[0], c.w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(p) = c.w[0];
+}
+template <int V>
+__device__ __forceinline__ void codes_f2(const Codes<V>& c, F2 (&f)[V / 2]) {
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i)
+    f[i] = f2(code_at(c.w[i / 2], 2 * i % 4), code_at(c.w[i / 2], 2 * i % 4 + 1));
 }
 
 struct StoreArgs {
@@ -98,84 +119,120 @@ __device__ __forceinline__ uint32_t exponent_byte(uint32_t bits, int least, int 
   return (uint32_t)min(max(b, least), most);
 }
 
+// The largest of the magnitudes' bits in a word of two 16-bit elements, or in an fp32.
+template <typename T>
+__device__ __forceinline__ uint32_t largest(uint32_t a, uint32_t w) {
+  if constexpr (sizeof(T) == 4) return max(a, w & 0x7fffffffu);
+  return __vmaxu2(a, w & 0x7fff7fffu);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t float_bits(uint32_t a) {
+  if constexpr (sizeof(T) == 4) return a;
+  a = max(a & 0xffffu, a >> 16);
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) return a << 16;
+  return __float_as_uint(__half2float(__ushort_as_half((uint16_t)a)));
+}
+
 template <typename T, bool PACKS>
 __global__ void __launch_bounds__(256) store_kernel(const StoreArgs a) {
   griddep_wait();
   constexpr bool kHalf = std::is_same_v<T, __half>;
+  constexpr int V = 16 / sizeof(T), Q = 16 / V;
+  constexpr int kLeast = kHalf ? 103 : 1, kMost = kHalf ? 136 : 248;
   GroupWalk at(a.groups);
   const uint32_t lane = lane_id() & 7u;
   // every lane of a warp takes part in its shuffles: the warp goes on while any octet has work
   for (; __any_sync(0xffffffffu, at.row < a.rows); at.next()) {
     const bool active = at.row < a.rows;
-    const uint64_t c = (uint64_t)at.group * kGroup + 16 * lane;
-    const int left = active && c < a.dim ? (a.dim - c < 16 ? (int)(a.dim - c) : 16) : 0;
-    float f[16];
-    const T* x = static_cast<const T*>(a.x) + (int64_t)at.row * a.x_stride + c;
-    if (left == 16) {
-      load16<T, PACKS>(x, 16, f);
-    } else {
-      load16<T, false>(x, left, f);
-    }
+    const uint64_t c0 = (uint64_t)at.group * kGroup;
+    const T* x = static_cast<const T*>(a.x) + (int64_t)at.row * a.x_stride + c0;
+    const int64_t left = active ? (int64_t)(a.dim - c0) : 0;
+    F2 f[Q][V / 2];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t c = piece_column<V>(lane, q);
+      if (PACKS && left >= c + V) {
+        const Raw<T, V> r = load_raw<T, V>(x + c);
+        top = largest<T>(largest<T>(largest<T>(largest<T>(top, r.w.x), r.w.y), r.w.z), r.w.w);
+        unpack<T, V>(r, f[q]);
+      } else {
+        load_piece<T>(x + c, left - c, false, f[q]);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const T e = from_f32<T>(i & 1 ? f[q][i / 2].y : f[q][i / 2].x);  // as it was
+          if constexpr (sizeof(T) == 4) top = largest<T>(top, __float_as_uint(e));
+          else top = largest<T>(top, *reinterpret_cast<const uint16_t*>(&e));
+        }
+      }
+    }
+    top = float_bits<T>(top);
 #pragma unroll
     for (int d = 4; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const uint32_t b = exponent_byte(top, kHalf ? 103 : 1, kHalf ? 136 : 248);
+    const uint32_t b = exponent_byte(top, kLeast, kMost);
     const bool fine = b != kNanExponent;
-    const float by = __uint_as_float((fine ? 254u - b : 127u) << 23);  // 2^-e
-    uint32_t w[4];
+    const float scale = __uint_as_float((fine ? 254u - b : 127u) << 23);  // 2^-e
+    const F2 by = f2(scale, scale), magic = f2(12582912.f, 12582912.f);  // 1.5 2^23
+    if (b == (uint32_t)kMost) {  // the largest step, of which there may be more than 127
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t r[4];
+      for (int q = 0; q < Q; ++q) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // clamped for the largest exponent's sake; 1.5 2^23 leaves the code in the low byte
-        const float v = fminf(fmaxf(f[4 * q + i] * by, -127.f), 127.f);
-        r[i] = __float_as_uint(v + 12582912.f);
+        for (int i = 0; i < V / 2; ++i) {
+          const float most = 127.f / scale;
+          f[q][i].x = fminf(fmaxf(f[q][i].x, -most), most);
+          f[q][i].y = fminf(fmaxf(f[q][i].y, -most), most);
+        }
       }
-      w[q] = fine ? __byte_perm(__byte_perm(r[0], r[1], 0x0040), __byte_perm(r[2], r[3], 0x0040),
-                                0x5410)
-                  : 0u;
     }
-    if (left > 0)  // the row's padding to whole 16 bytes is written as zeros
-      *reinterpret_cast<uint4*>(a.codes + (int64_t)at.row * a.codes_stride + c) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      Codes<V> codes;
+#pragma unroll
+      for (int k = 0; k < V / 4; ++k) {
+        // the product is exact, the sum rounds it to a whole number, in the low byte
+        const F2 lo = fma2<true>(f[q][2 * k], by, magic);
+        const F2 hi = fma2<true>(f[q][2 * k + 1], by, magic);
+        const uint32_t w =
+            __byte_perm(__byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x0040),
+                        __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x0040), 0x5410);
+        codes.w[k] = fine ? w : 0u;
+      }
+      // the row's padding to whole 16 bytes is written as zeros
+      const uint32_t c = piece_column<V>(lane, q);
+      if (left > 0 && c < (uint32_t)(left >= kGroup ? kGroup : (left + 15) / 16 * 16))
+        store_codes<V>(a.codes + (int64_t)at.row * a.codes_stride + c0 + c, codes);
+    }
     if (active && lane == 0)
       a.exponents[(int64_t)at.row * a.exponents_stride + at.group] = (uint8_t)b;
-  }
-}
-
-// Sixteen codes as floats, without their scale.
-__device__ __forceinline__ void codes16(uint4 v, float (&f)[16]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[4 * q + i] = code_at(w[q], i);
   }
 }
 
 template <typename T, bool PACKS>
 __global__ void __launch_bounds__(256) restore_kernel(const StoreArgs a) {
   griddep_wait();
+  constexpr int V = 16 / sizeof(T), Q = 16 / V;
   GroupWalk at(a.groups);
   const uint32_t lane = lane_id() & 7u;
   for (; at.row < a.rows; at.next()) {
-    const uint64_t c = (uint64_t)at.group * kGroup + 16 * lane;
-    if (c >= a.dim) continue;
-    const int left = a.dim - c < 16 ? (int)(a.dim - c) : 16;
+    const uint64_t c0 = (uint64_t)at.group * kGroup;
+    const int64_t left = (int64_t)(a.dim - c0);
+    const int8_t* from = a.codes + (int64_t)at.row * a.codes_stride + c0;
     const float scale =
         scale_of(a.exponents[(int64_t)at.row * a.exponents_stride + at.group]);
-    float f[16];
-    codes16(*reinterpret_cast<const uint4*>(a.codes + (int64_t)at.row * a.codes_stride + c), f);
+    T* y = static_cast<T*>(a.x) + (int64_t)at.row * a.x_stride + c0;
+    Codes<V> codes[Q] = {};
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] *= scale;
-    T* y = static_cast<T*>(a.x) + (int64_t)at.row * a.x_stride + c;
-    if (left == 16)
-      store16<T, PACKS>(y, 16, f);
-    else
-      store16<T, false>(y, left, f);
+    for (int q = 0; q < Q; ++q)
+      if (piece_column<V>(lane, q) < left) codes[q] = load_codes<V>(from + piece_column<V>(lane, q));
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t c = piece_column<V>(lane, q);
+      F2 f[V / 2];
+      codes_f2<V>(codes[q], f);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) f[i] = mul2<true>(f[i], f2(scale, scale));
+      if (c < left) store_piece<T>(y + c, left - c, PACKS, f);
+    }
   }
 }
 
@@ -201,137 +258,31 @@ struct Norm8Args {
   uint32_t threads;  // that share a row
 };
 
-// Sixteen columns per thread, whose sums over the rows stay in its registers, as do its weights.
-// PACKS: the columns are consecutive; else LANES apart, so that neighbouring threads read
-// neighbouring elements at any alignment.
-template <typename T, bool PACKS, int LANES, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8Args a) {
-  griddep_wait();
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ float2 scratch[66 * (MAXT / 64)];
-  Group g = make_group(a.threads, scratch);
-  const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
+// The sums of a block's rows: of its groups of threads one after the other, in shared memory
+// (`join`: [groups][2][dim]), or as they are. `column(i)`: of the thread's i-th sum.
+template <typename F>
+__device__ __forceinline__ void write_sums(const Norm8Args& a, const Group& g, uint32_t groups,
+                                           float* join, const float (&gw)[16],
+                                           const float (&gb)[16], F column) {
   const uint32_t dim = (uint32_t)a.dim;
-  const float inv = 1.0f / (float)dim;
-  const uint32_t first = PACKS ? 16 * t : t / LANES * (16 * LANES) + t % LANES;
-  const int left = (int)dim - (int)first;
-  auto column = [&](int i) { return PACKS ? i : i * LANES; };  // from the first
-  float w[16], gw[16], gb[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    gw[i] = gb[i] = 0.f;
-    w[i] = a.w && column(i) < left ? load_any(a.w, a.w_type, first + column(i)) : 1.f;
-  }
-  const uint64_t step = (uint64_t)gridDim.x * groups;
-  constexpr int kScales = PACKS ? 1 : LANES / 8;  // groups of 128 that the columns lie in
-  constexpr int kDy = PACKS ? (int)sizeof(T) : 1;  // 16-byte pieces of dy
-  uint4 dy_next[kDy], codes_next;
-  uint32_t exp_next = 0;
-  float mean_next = 0.f, rstd_next = 0.f;
-  auto fetch = [&](uint64_t row) {
-    if (row >= a.rows) return;
-    mean_next = a.mean[row];
-    rstd_next = a.rstd[row];
-    if constexpr (PACKS) {
-      if (left <= 0) return;
-      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride + first;
-#pragma unroll
-      for (int q = 0; q < kDy; ++q) dy_next[q] = reinterpret_cast<const uint4*>(dy)[q];
-      codes_next =
-          *reinterpret_cast<const uint4*>(a.codes + (int64_t)row * a.codes_stride + first);
-      exp_next = a.exponents[(int64_t)row * a.exponents_stride + first / kGroup];
-    }
-  };
-  uint64_t base = (uint64_t)blockIdx.x * groups;
-  fetch(base + g.index);
-  for (; base < a.rows; base += step) {  // the same turns for all groups of threads
-    const uint64_t row = base + g.index;
-    const bool active = row < a.rows;
-    const int in = active ? left : 0;
-    const float mean = mean_next, rstd = rstd_next;
-    float xh[16], d[16];
-    if constexpr (PACKS) {
-      if (in > 0) {
-        constexpr int V = 16 / sizeof(T);
-#pragma unroll
-        for (int q = 0; q < kDy; ++q) {
-          Raw<T, V> r;
-          r.w = dy_next[q];
-          F2 two[V / 2];
-          unpack<T, V>(r, two);
-#pragma unroll
-          for (int i = 0; i < V / 2; ++i) {
-            d[q * V + 2 * i] = two[i].x;
-            d[q * V + 2 * i + 1] = two[i].y;
-          }
-        }
-        codes16(codes_next, xh);
-        const float by = scale_of(exp_next);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) xh[i] = (xh[i] * by - mean) * rstd;
-      }
-      fetch(row + step);
-    } else {
-      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride + first;
-      const int8_t* x = a.codes + (int64_t)row * a.codes_stride + first;
-      const uint8_t* ex = a.exponents + (int64_t)row * a.exponents_stride + first / kGroup;
-      float by[kScales];
-#pragma unroll
-      for (int k = 0; k < kScales; ++k) by[k] = k * 128 < in ? scale_of(ex[k]) : 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const bool there = column(i) < in;
-        d[i] = there ? to_f32(dy[column(i)]) : 0.f;
-        xh[i] = there ? ((float)x[column(i)] * by[i * kScales / 16] - mean) * rstd : 0.f;
-      }
-      fetch(row + step);
-    }
-    float2 s = make_float2(0.f, 0.f);
-    if (!PACKS || in > 0) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        gw[i] += d[i] * xh[i];
-        gb[i] += d[i];
-        d[i] *= w[i];
-        s.x += d[i];
-        s.y += d[i] * xh[i];
-      }
-    }
-    s = g.sum2(s);
-    if (in <= 0) continue;
-    // dx = rstd (d - sum(d) / dim - xh sum(d xh) / dim)
-    const float k1 = -s.x * inv * rstd, k2 = -s.y * inv * rstd;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) d[i] = xh[i] * k2 + (d[i] * rstd + k1);
-    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride + first;
-    if constexpr (PACKS) {
-      store16<T, true>(dx, 16, d);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (column(i) < in) dx[column(i)] = from_f32<T>(d[i]);
-    }
-  }
-  if (a.part_w == nullptr) return;  // neither sum is wanted
   float* to_w = a.part_w + (uint64_t)blockIdx.x * a.dim;
   float* to_b = a.part_b + (uint64_t)blockIdx.x * a.dim;
   if (groups == 1) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
-      if (column(i) < left) {
-        to_w[first + column(i)] = gw[i];
-        to_b[first + column(i)] = gb[i];
+      if (column(i) < dim) {
+        to_w[column(i)] = gw[i];
+        to_b[column(i)] = gb[i];
       }
     return;
   }
-  // the groups' sums one after the other, in shared memory
-  float* join = reinterpret_cast<float*>(dynamic);  // [groups][2][dim]
+  __syncthreads();
   float* set = join + (uint64_t)g.index * 2 * dim;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (column(i) < left) {
-      set[first + column(i)] = gw[i];
-      set[dim + first + column(i)] = gb[i];
+    if (column(i) < dim) {
+      set[column(i)] = gw[i];
+      set[dim + column(i)] = gb[i];
     }
   __syncthreads();
   for (uint32_t c = threadIdx.x; c < dim; c += blockDim.x) {
@@ -343,6 +294,209 @@ __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8A
     to_w[c] = sw;
     to_b[c] = sb;
   }
+}
+
+// Sixteen columns per thread, whose sums over the rows stay in its registers, as do its weights.
+// Here the rows are whole, aligned pieces, which come through a ring in shared memory: a thread
+// copies ahead and reads back its own pieces alone, so that the ring needs no barrier. (With one
+// row ahead in registers 24 KB of an SM's reads were on their way at a time, and 16384 x 4096
+// bf16 took 79 us.)
+constexpr int kRing = 4;
+
+template <typename T, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8Args a) {
+  griddep_wait();
+  constexpr int V = 16 / sizeof(T), Q = 16 / V, P = V / 2;
+  extern __shared__ __align__(16) uint8_t dynamic[];  // [kRing][Q of dy, 1 of codes][MAXT] of 16 bytes
+  __shared__ float2 scratch[66 * (MAXT / 64)];
+  Group g = make_group(a.threads, scratch);
+  const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
+  const uint32_t dim = (uint32_t)a.dim, first = t / 8 * kGroup;
+  const float inv = 1.0f / (float)dim;
+  auto column = [&](int i) { return first + piece_column<V>(t & 7u, i / V) + i % V; };
+  bool there[Q];
+  F2 w[Q][P], gw[Q][P], gb[Q][P];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    there[q] = column(q * V) < dim;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const uint32_t c = column(q * V + 2 * i);
+      gw[q][i] = gb[q][i] = f2(0.f, 0.f);
+      w[q][i] = a.w && there[q] ? f2(load_any(a.w, a.w_type, c), load_any(a.w, a.w_type, c + 1))
+                                : f2(1.f, 1.f);
+    }
+  }
+  const uint64_t step = (uint64_t)gridDim.x * groups;
+  constexpr uint32_t kSlot = (Q + 1) * MAXT * 16;
+  uint8_t* const mine = dynamic + threadIdx.x * 16;
+  float mean_next[kRing - 1], rstd_next[kRing - 1];
+  uint32_t exp_next[kRing - 1];
+  auto fetch = [&](uint64_t row, uint32_t slot) {
+    if (row < a.rows) {
+      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
+      const int8_t* x = a.codes + (int64_t)row * a.codes_stride;
+      uint8_t* to = mine + slot * kSlot;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        if (there[q]) {
+          cp_async16(to + q * MAXT * 16, dy + column(q * V));
+          const uint32_t at = static_cast<uint32_t>(
+              __cvta_generic_to_shared(to + Q * MAXT * 16 + q * V));
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at),
+                       "l"(x + column(q * V)), "n"(V)
+                       : "memory");
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto fetch_small = [&](uint64_t row, float& mean, float& rstd, uint32_t& e) {
+    if (row < a.rows) {
+      mean = a.mean[row];
+      rstd = a.rstd[row];
+      if (first < dim) e = a.exponents[(int64_t)row * a.exponents_stride + first / kGroup];
+    }
+  };
+  uint64_t base = (uint64_t)blockIdx.x * groups;
+#pragma unroll
+  for (int k = 0; k < kRing - 1; ++k) {
+    mean_next[k] = rstd_next[k] = 0.f;
+    exp_next[k] = 0;
+    fetch(base + g.index + k * step, k);
+    fetch_small(base + g.index + k * step, mean_next[k], rstd_next[k], exp_next[k]);
+  }
+  uint32_t slot = 0;
+  for (; base < a.rows; base += step) {  // the same turns for all groups of threads
+    const uint64_t row = base + g.index;
+    const bool active = row < a.rows;
+    const float mean = mean_next[0], rstd = rstd_next[0], scale = scale_of(exp_next[0]);
+#pragma unroll
+    for (int k = 0; k < kRing - 2; ++k) {
+      mean_next[k] = mean_next[k + 1];
+      rstd_next[k] = rstd_next[k + 1];
+      exp_next[k] = exp_next[k + 1];
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    const F2 by = f2(scale, scale), minus = f2(-mean, -mean), r2 = f2(rstd, rstd);
+    F2 xh[Q][P], d[Q][P], s0 = f2(0.f, 0.f), s1 = s0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const uint8_t* from = mine + slot * kSlot;
+      Raw<T, V> raw;
+      raw.w = *reinterpret_cast<const uint4*>(from + q * MAXT * 16);
+      unpack<T, V>(raw, d[q]);
+      codes_f2<V>(load_codes<V>(reinterpret_cast<const int8_t*>(from + Q * MAXT * 16 + q * V)),
+                  xh[q]);
+      if (active && there[q]) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+          // c 2^e is exact, and so its difference from the mean is rounded once
+          xh[q][i] = mul2<true>(fma2<true>(xh[q][i], by, minus), r2);
+          gw[q][i] = fma2<true>(d[q][i], xh[q][i], gw[q][i]);
+          gb[q][i] = add2<true>(gb[q][i], d[q][i]);
+          d[q][i] = mul2<true>(d[q][i], w[q][i]);
+          s0 = add2<true>(s0, d[q][i]);
+          s1 = fma2<true>(d[q][i], xh[q][i], s1);
+        }
+      }
+    }
+    const uint64_t later = row + (kRing - 1) * step;
+    fetch(later, slot == 0 ? kRing - 1 : slot - 1);
+    fetch_small(later, mean_next[kRing - 2], rstd_next[kRing - 2], exp_next[kRing - 2]);
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    const float2 s = g.sum2(make_float2(s0.x + s0.y, s1.x + s1.y));
+    if (!active) continue;
+    // dx = rstd (d - sum(d) / dim - xh sum(d xh) / dim)
+    const float k1s = -s.x * inv * rstd, k2s = -s.y * inv * rstd;
+    const F2 k1 = f2(k1s, k1s), k2 = f2(k2s, k2s);
+    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      if (there[q]) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          d[q][i] = fma2<true>(xh[q][i], k2, fma2<true>(d[q][i], r2, k1));
+        *reinterpret_cast<uint4*>(dx + column(q * V)) = pack<T, V>(d[q]);
+      }
+  }
+  if (a.part_w == nullptr) return;  // neither sum is wanted
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  float fw[16], fb[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const F2 u = gw[i / V][i % V / 2], v = gb[i / V][i % V / 2];
+    fw[i] = i & 1 ? u.y : u.x;
+    fb[i] = i & 1 ? v.y : v.x;
+  }
+  write_sums(a, g, groups, reinterpret_cast<float*>(dynamic), fw, fb, column);
+}
+
+// Any width, stride and alignment, element by element: a thread's columns are LANES apart, so
+// that neighbouring threads read neighbouring elements.
+template <typename T, int LANES, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm8_backward_any_kernel(const Norm8Args a) {
+  griddep_wait();
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  __shared__ float2 scratch[66 * (MAXT / 64)];
+  Group g = make_group(a.threads, scratch);
+  const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
+  const uint32_t dim = (uint32_t)a.dim;
+  const float inv = 1.0f / (float)dim;
+  const uint32_t first = t / LANES * (16 * LANES) + t % LANES;
+  const int left = (int)dim - (int)first;
+  auto column = [&](int i) { return first + i * LANES; };
+  float w[16], gw[16], gb[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    gw[i] = gb[i] = 0.f;
+    w[i] = a.w && i * LANES < left ? load_any(a.w, a.w_type, column(i)) : 1.f;
+  }
+  const uint64_t step = (uint64_t)gridDim.x * groups;
+  constexpr int kScales = LANES / 8;  // groups of 128 that the columns lie in
+  float mean_next = 0.f, rstd_next = 0.f;
+  auto fetch = [&](uint64_t row) {
+    if (row >= a.rows) return;
+    mean_next = a.mean[row];
+    rstd_next = a.rstd[row];
+  };
+  uint64_t base = (uint64_t)blockIdx.x * groups;
+  fetch(base + g.index);
+  for (; base < a.rows; base += step) {  // the same turns for all groups of threads
+    const uint64_t row = base + g.index;
+    const int in = row < a.rows ? left : 0;
+    const float mean = mean_next, rstd = rstd_next;
+    const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
+    const int8_t* x = a.codes + (int64_t)row * a.codes_stride;
+    const uint8_t* e = a.exponents + (int64_t)row * a.exponents_stride;
+    float xh[16], d[16], scale[kScales];
+#pragma unroll
+    for (int k = 0; k < kScales; ++k)
+      scale[k] = k * kGroup < in ? scale_of(e[first / kGroup + k]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const bool there = i * LANES < in;
+      d[i] = there ? to_f32(dy[column(i)]) : 0.f;
+      xh[i] = there ? ((float)x[column(i)] * scale[i * kScales / 16] - mean) * rstd : 0.f;
+    }
+    fetch(row + step);
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      gw[i] += d[i] * xh[i];
+      gb[i] += d[i];
+      d[i] *= w[i];
+      s.x += d[i];
+      s.y += d[i] * xh[i];
+    }
+    s = g.sum2(s);
+    const float k1 = -s.x * inv * rstd, k2 = -s.y * inv * rstd;
+    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i * LANES < in) dx[column(i)] = from_f32<T>(xh[i] * k2 + (d[i] * rstd + k1));
+  }
+  if (a.part_w == nullptr) return;  // neither sum is wanted
+  write_sums(a, g, groups, reinterpret_cast<float*>(dynamic), gw, gb, column);
 }
 
 // Rows too long for a block's registers: dx by reading the row twice, the column sums by a
@@ -391,28 +545,40 @@ __global__ void __launch_bounds__(128) norm8_columns_kernel(const Norm8Args a) {
   a.part_b[(uint64_t)blockIdx.y * a.dim + c] = gb;
 }
 
-template <typename T, bool PACKS, int LANES, int MAXT, int MINB>
+template <typename T, int MAXT, int MINB>
 bool launch_norm8(const Norm8Args& a, const BackwardShape& h, cudaStream_t s) {
-  auto kernel = norm8_backward_kernel<T, PACKS, LANES, MAXT, MINB>;
+  auto kernel = norm8_backward_kernel<T, MAXT, MINB>;
+  const uint32_t groups = h.block / h.threads;
+  const size_t ring = (size_t)kRing * (sizeof(T) + 1) * MAXT * 16;
+  const size_t smem = std::max(ring, groups > 1 ? (size_t)2 * groups * a.dim * sizeof(float) : (size_t)0);
+  if (!ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
+  launch_pdl(kernel, h.parts, h.block, smem, s, a);
+  return true;
+}
+template <typename T, int LANES, int MAXT, int MINB>
+bool launch_norm8_any(const Norm8Args& a, const BackwardShape& h, cudaStream_t s) {
+  auto kernel = norm8_backward_any_kernel<T, LANES, MAXT, MINB>;
   const uint32_t groups = h.block / h.threads;
   const size_t smem = groups > 1 ? 2ull * groups * a.dim * sizeof(float) : 0;
   if (smem > 40 * 1024 && !ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
   launch_pdl(kernel, h.parts, h.block, smem, s, a);
   return true;
 }
-template <typename T, bool PACKS>
-bool launch_norm8_shape(const Norm8Args& a, const BackwardShape& h, cudaStream_t s) {
-  if (h.threads == 8) return launch_norm8<T, PACKS, 8, 256, kFit>(a, h, s);
-  if (h.threads == 16) return launch_norm8<T, PACKS, 16, 256, kFit>(a, h, s);
-  if (h.block <= 256) return launch_norm8<T, PACKS, 32, 256, kFit>(a, h, s);
-  return launch_norm8<T, PACKS, 32, 512, 1>(a, h, s);
+template <typename T>
+bool launch_norm8_shape(const Norm8Args& a, const BackwardShape& h, bool packs, cudaStream_t s) {
+  if (packs && h.block <= 256) return launch_norm8<T, 256, kFit>(a, h, s);
+  if (packs) return launch_norm8<T, 512, 1>(a, h, s);
+  if (h.threads == 8) return launch_norm8_any<T, 8, 256, kFit>(a, h, s);
+  if (h.threads == 16) return launch_norm8_any<T, 16, 256, kFit>(a, h, s);
+  if (h.block <= 256) return launch_norm8_any<T, 32, 256, kFit>(a, h, s);
+  return launch_norm8_any<T, 32, 512, 1>(a, h, s);
 }
 
 template <typename T>
 bool norm8_typed(Norm8Args a, float* dweight, float* dbias, int32_t accumulate, uint8_t* ws,
                  cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const bool packs = a.dim % 16 == 0 && a.dy_stride % V == 0 && a.dx_stride % V == 0 &&
+  const bool packs = a.dim % V == 0 && a.dy_stride % V == 0 && a.dx_stride % V == 0 &&
                      aligned_to(a.dy, 16) && aligned_to(a.dx, 16);
   const bool sums = dweight || dbias;
   const BackwardShape h = backward_shape(a.rows, a.dim);
@@ -427,7 +593,7 @@ bool norm8_typed(Norm8Args a, float* dweight, float* dbias, int32_t accumulate, 
                  s, a);
     launch_pdl(norm8_backward_long_kernel<T>, (unsigned)a.rows, 1024, 0, s, a);
   } else {
-    ok = packs ? launch_norm8_shape<T, true>(a, h, s) : launch_norm8_shape<T, false>(a, h, s);
+    ok = launch_norm8_shape<T>(a, h, packs, s);
   }
   if (sums)
     launch_pdl(join_columns_kernel, dim3((unsigned)((a.dim + 31) / 32), 2), 512, 0, s, a.part_w,
