@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
   const uint32_t among = a.warps[keys], index = keys ? id - a.warps[0] : id;
   const bool works = index < among;
   const uint64_t jobs = a.tokens * side.jobs;
-  uint64_t job = works ? jobs * index / among : 0;
+  const uint64_t job = works ? jobs * index / among : 0;
   const uint64_t end = works ? jobs * (index + 1) / among : 0;
   const uint32_t slots = 32 / a.lanes, slot = lane / a.lanes, l = lane - slot * a.lanes;
   const float inv = 1.f / (float)a.dim;
@@ -283,53 +283,67 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
   uint32_t part = (uint32_t)(job - token * side.jobs);
 
   Mine x, g;
-  // the jobs are fetched in order, `ahead` of their turn
+  // The jobs are fetched in order, kAhead before their turn; pointers go on from head to head and
+  // from token to token.
   constexpr uint32_t kAhead = Mine::RING ? kRing - 1 : 1;
-  uint64_t next_token = token, next_job = job;
-  uint32_t next_part = part, slot_in = 0, slot_out = 0;
+  struct Walk {
+    const T* at;     // this lane's head
+    int64_t heads_on, token_on;  // to the next job of the token, from the last one to the next token
+    __device__ __forceinline__ Walk(const Heads& h, uint64_t token, uint32_t part, uint32_t jobs,
+                                    uint32_t slots, uint32_t slot) {
+      heads_on = (int64_t)slots * h.head;
+      token_on = h.token - (int64_t)(jobs - 1) * heads_on;
+      at = static_cast<const T*>(h.p) + (int64_t)token * h.token +
+           (int64_t)(part * slots + slot) * h.head;
+    }
+    __device__ __forceinline__ void next(bool last) { at += last ? token_on : heads_on; }
+  };
+  Walk from_x(side.x, token, part, side.jobs, slots, slot);
+  Walk from_g(side.g, token, part, side.jobs, slots, slot);
+  Walk to_out(side.out, token, part, side.jobs, slots, slot);
+  const uint32_t in_last = side.heads - (side.jobs - 1) * slots;  // heads of a token's last job
+  uint32_t next_part = part, left = (uint32_t)(end - job);
+  uint32_t to_fetch = left;
+  const uint32_t ring0 = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  uint32_t slot_in = 0, slot_out = 0;
   auto fetch = [&]() {
-    if (next_job < end) {
-      const bool active = next_part * slots + slot < side.heads;
-      const uint32_t head = min(next_part * slots + slot, side.heads - 1);
-      const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(ring + slot_in * kSlot));
-      x.load(static_cast<const T*>(side.x.p) + (int64_t)next_token * side.x.token +
-                 (int64_t)head * side.x.head, place, active, to);
-      if constexpr (BACK)
-        g.load(static_cast<const T*>(side.g.p) + (int64_t)next_token * side.g.token +
-                   (int64_t)head * side.g.head, place, active, to + 32 * Mine::kSlot);
-      ++next_job;
-      if (++next_part == side.jobs) {
-        next_part = 0;
-        ++next_token;
+    if (to_fetch > 0) {
+      const bool last = next_part + 1 == side.jobs;
+      // a lane without a head in the last job reads nothing, and so its pointer does not matter
+      const bool active = !last || slot < in_last;
+      x.load(from_x.at, place, active, ring0 + slot_in);
+      from_x.next(last);
+      if constexpr (BACK) {
+        g.load(from_g.at, place, active, ring0 + slot_in + 32 * Mine::kSlot);
+        from_g.next(last);
       }
-      slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
+      --to_fetch;
+      next_part = last ? 0 : next_part + 1;
+      slot_in = slot_in == (kRing - 1) * kSlot ? 0 : slot_in + kSlot;
     }
     if constexpr (Mine::RING) asm volatile("cp.async.commit_group;" ::: "memory");
   };
   for (uint32_t k = 0; k < kAhead; ++k) fetch();
   bool known = false;
-  for (; job < end; ++job) {
-    const uint32_t head = part * slots + slot;
-    const bool active = head < side.heads;
+  for (; left > 0; --left) {
+    const bool last = part + 1 == side.jobs, active = !last || slot < in_last;
     F2 lo[N], hi[N], glo[N], ghi[N];
     if constexpr (Mine::RING) {
       asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
-      x.arrive(ring + slot_out * kSlot);
-      if constexpr (BACK) g.arrive(ring + slot_out * kSlot + 32 * Mine::kSlot);
-      slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
+      x.arrive(ring + slot_out);
+      if constexpr (BACK) g.arrive(ring + slot_out + 32 * Mine::kSlot);
+      slot_out = slot_out == (kRing - 1) * kSlot ? 0 : slot_out + kSlot;
     }
     x.template get<PAIRS>(lo, hi);
     if constexpr (BACK) g.template get<PAIRS>(glo, ghi);
-    const uint64_t now = token;
-    if (++part == side.jobs) {
-      part = 0;
-      ++token;
-    }
+    T* const out = const_cast<T*>(to_out.at);
+    to_out.next(last);
+    part = last ? 0 : part + 1;
     fetch();
     if (!known) {
       if (half) {
-        const int64_t position = a.wide ? static_cast<const int64_t*>(a.positions)[now]
-                                        : static_cast<const int32_t*>(a.positions)[now];
+        const int64_t position = a.wide ? static_cast<const int64_t*>(a.positions)[token]
+                                        : static_cast<const int32_t*>(a.positions)[token];
         __syncwarp();
         for (uint32_t i = lane; i < half; i += 32) {
           const uint64_t turn = (uint64_t)position * fraction[i];
@@ -352,7 +366,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
         }
       }
     }
-    known = token == now;
+    known = !last;
+    token += last;
 
     F2 ss = f2(0.f, 0.f), dot = f2(0.f, 0.f);
 #pragma unroll
@@ -380,8 +395,6 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
     }
     const float r = rsqrtf(sum.x * inv + a.eps);
     const F2 by = f2(r, r);
-    T* out = static_cast<T*>(const_cast<void*>(side.out.p)) + (int64_t)now * side.out.token +
-             (int64_t)head * side.out.head;
     if constexpr (BACK) {
       const float k = -sum.y * inv * r * r * r;
       const F2 kk = f2(k, k);
