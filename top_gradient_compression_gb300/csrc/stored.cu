@@ -318,93 +318,57 @@ __device__ __forceinline__ void write_sums(const Norm8Args& a, const Group& g, u
   }
 }
 
-// Sums of four values over the threads of a group, two values of each of two rows. `room`: of the
-// group, [2][16][4] floats; `turn` alternates between its halves, so that one barrier is enough.
-__device__ __forceinline__ void sum4(const Group& g, float* room, uint32_t turn, float (&v)[4]) {
-  const uint32_t lane = lane_id();
-  if (g.threads <= 32) {
-    for (uint32_t d = g.threads / 2; d > 0; d >>= 1) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], d);
-    }
-    return;
-  }
-  // each half of the lanes goes on with half of the values: lane bits 4 and 3 say which one
-  const bool up = lane & 16, right = lane & 8;
-  const float a = up ? v[2] : v[0], b = up ? v[3] : v[1];
-  const float c = a + __shfl_xor_sync(0xffffffffu, up ? v[0] : v[2], 16);
-  const float d = b + __shfl_xor_sync(0xffffffffu, up ? v[1] : v[3], 16);
-  float e = (right ? d : c) + __shfl_xor_sync(0xffffffffu, right ? c : d, 8);
-#pragma unroll
-  for (int k = 4; k > 0; k >>= 1) e += __shfl_xor_sync(0xffffffffu, e, k);
-  room += 64 * (turn & 1u);
-  const uint32_t warps = g.threads / 32;
-  if ((lane & 7u) == 0) room[(g.t / 32) * 4 + lane / 8] = e;
-  g.sync();
-  // lane: value lane % 4 of warp lane / 4, and of warp lane / 4 + 8
-  e = lane / 4 < warps ? room[lane] : 0.f;
-  if (lane / 4 + 8 < warps) e += room[lane + 32];
-#pragma unroll
-  for (int k = 16; k > 2; k >>= 1) e += __shfl_xor_sync(0xffffffffu, e, k);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(0xffffffffu, e, i);
-}
+// Sixteen columns per thread, whose sums over the rows stay in its registers, as do its weights.
+// Here the rows are whole, aligned pieces, which come through a ring in shared memory: a thread
+// copies ahead and reads back its own pieces alone, so that the ring needs no barrier.
+//
+// 16384 x 4096 bf16 takes 79 us, 4.2 TB/s: half of the issue slots are filled by the 16 warps of an
+// SM that 119 registers allow, and a row's reduction is what they wait for. Two rows at a time, read
+// from the ring a second time after their sums (80 registers, 24 warps, 63 % of the slots, but 1.34
+// times the instructions), took 86; arithmetic single in place of packed, or one row ahead in
+// registers in place of three in the ring, 79 as well.
+constexpr int kRing = 4;
 
-// Sixteen columns per thread, whose sums over the rows stay in its registers. Here the rows are
-// whole, aligned pieces, which come through a ring in shared memory: a thread copies ahead and
-// reads back its own pieces alone, so that the ring needs no barrier. Two rows are taken at a time
-// and read from the ring twice, before and after their sums: what one row waits for, the
-// reduction above all, the other fills. (One row at a time, kept in registers between, allows 16
-// warps per SM and took 79 us for 16384 x 4096 bf16, whether its loads were ahead by one row or by
-// three, and its arithmetic single or packed.) One block per SM, so that few partial sums are left.
-constexpr int kTurns = 2;  // pairs of rows in the ring
-template <typename T>
-constexpr int kNorm8Threads = sizeof(T) == 2 ? 768 : 512;
-template <typename T>
-constexpr uint32_t kNorm8Slot = (sizeof(T) + 1) * kNorm8Threads<T> * 16;  // a row
-
-template <typename T>
-__global__ void __launch_bounds__(kNorm8Threads<T>, 1) norm8_backward_kernel(const Norm8Args a) {
+template <typename T, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8Args a) {
   griddep_wait();
-  constexpr int V = 16 / sizeof(T), Q = 16 / V, P = V / 2, MAXT = kNorm8Threads<T>;
-  constexpr uint32_t kSlot = kNorm8Slot<T>;
-  // [kTurns][2][Q of dy, 1 of codes][MAXT] of 16 bytes; weights [dim]
-  extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ float room[(MAXT / 64) * 128];
-  const Group g = make_group(a.threads, nullptr);
+  constexpr int V = 16 / sizeof(T), Q = 16 / V, P = V / 2;
+  extern __shared__ __align__(16) uint8_t dynamic[];  // [kRing][Q of dy, 1 of codes][MAXT] of 16 bytes
+  __shared__ float2 scratch[66 * (MAXT / 64)];
+  Group g = make_group(a.threads, scratch);
   const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
   const uint32_t dim = (uint32_t)a.dim, first = t / 8 * kGroup;
   const float inv = 1.0f / (float)dim;
   auto column = [&](int i) { return first + piece_column<V>(t & 7u, i / V) + i % V; };
-  float* const weights = reinterpret_cast<float*>(dynamic + kTurns * 2 * kSlot);
-  for (uint32_t c = threadIdx.x; c < dim; c += blockDim.x)
-    weights[c] = a.w ? load_any(a.w, a.w_type, c) : 1.f;
   bool there[Q];
-  F2 gw[Q][P], gb[Q][P];
+  F2 w[Q][P], gw[Q][P], gb[Q][P];
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     there[q] = column(q * V) < dim;
 #pragma unroll
-    for (int i = 0; i < P; ++i) gw[q][i] = gb[q][i] = f2(0.f, 0.f);
+    for (int i = 0; i < P; ++i) {
+      const uint32_t c = column(q * V + 2 * i);
+      gw[q][i] = gb[q][i] = f2(0.f, 0.f);
+      w[q][i] = a.w && there[q] ? f2(load_any(a.w, a.w_type, c), load_any(a.w, a.w_type, c + 1))
+                                : f2(1.f, 1.f);
+    }
   }
-  const uint64_t step = (uint64_t)gridDim.x * groups * 2;
+  const uint64_t step = (uint64_t)gridDim.x * groups;
+  constexpr uint32_t kSlot = (Q + 1) * MAXT * 16;
   uint8_t* const mine = dynamic + threadIdx.x * 16;
-  float mean_next[2] = {0.f, 0.f}, rstd_next[2] = {0.f, 0.f};
-  uint32_t exp_next[2] = {0, 0};
-  auto fetch = [&](uint64_t row0, uint32_t turn) {
-#pragma unroll
-    for (uint32_t r = 0; r < 2; ++r) {
-      const uint64_t row = row0 + r;
-      if (row >= a.rows) continue;
+  float mean_next[kRing - 1], rstd_next[kRing - 1];
+  uint32_t exp_next[kRing - 1];
+  auto fetch = [&](uint64_t row, uint32_t slot) {
+    if (row < a.rows) {
       const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
       const int8_t* x = a.codes + (int64_t)row * a.codes_stride;
-      uint8_t* to = mine + (2 * turn + r) * kSlot;
+      uint8_t* to = mine + slot * kSlot;
 #pragma unroll
       for (int q = 0; q < Q; ++q)
         if (there[q]) {
           cp_async16(to + q * MAXT * 16, dy + column(q * V));
-          const uint32_t at =
-              static_cast<uint32_t>(__cvta_generic_to_shared(to + Q * MAXT * 16 + q * V));
+          const uint32_t at = static_cast<uint32_t>(
+              __cvta_generic_to_shared(to + Q * MAXT * 16 + q * V));
           asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at),
                        "l"(x + column(q * V)), "n"(V)
                        : "memory");
@@ -412,105 +376,74 @@ __global__ void __launch_bounds__(kNorm8Threads<T>, 1) norm8_backward_kernel(con
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto fetch_small = [&](uint64_t row0) {
-#pragma unroll
-    for (uint32_t r = 0; r < 2; ++r)
-      if (row0 + r < a.rows) {
-        mean_next[r] = a.mean[row0 + r];
-        rstd_next[r] = a.rstd[row0 + r];
-        if (first < dim)
-          exp_next[r] = a.exponents[(int64_t)(row0 + r) * a.exponents_stride + first / kGroup];
-      }
-  };
-  uint64_t base = (uint64_t)blockIdx.x * groups * 2;
-  const uint64_t of = 2 * g.index;
-#pragma unroll
-  for (int k = 0; k < kTurns; ++k) fetch(base + of + k * step, k);
-  fetch_small(base + of);
-  __syncthreads();
-  uint32_t turn = 0, sums = 0;
-  for (; base < a.rows; base += step) {  // the same turns for all groups of threads
-    const uint64_t row0 = base + of;
-    F2 by[2], minus[2], r2[2];
-    float rstd[2];
-    bool active[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const float scale = scale_of(exp_next[r]);
-      rstd[r] = rstd_next[r];
-      by[r] = f2(scale, scale);
-      minus[r] = f2(-mean_next[r], -mean_next[r]);
-      r2[r] = f2(rstd[r], rstd[r]);
-      active[r] = row0 + r < a.rows;
+  auto fetch_small = [&](uint64_t row, float& mean, float& rstd, uint32_t& e) {
+    if (row < a.rows) {
+      mean = a.mean[row];
+      rstd = a.rstd[row];
+      if (first < dim) e = a.exponents[(int64_t)row * a.exponents_stride + first / kGroup];
     }
-    fetch_small(row0 + step);
-    // dy and xh of piece q of row r; c 2^e is exact, so its difference from the mean is rounded
-    // once
-    auto read = [&](int q, int r, F2(&d)[P], F2(&xh)[P]) {
-      const uint8_t* from = mine + (2 * turn + r) * kSlot;
-      Raw<T, V> raw;
-      raw.w = *reinterpret_cast<const uint4*>(from + q * MAXT * 16);
-      unpack<T, V>(raw, d);
-      codes_f2<V>(load_codes<V>(reinterpret_cast<const int8_t*>(from + Q * MAXT * 16 + q * V)), xh);
+  };
+  uint64_t base = (uint64_t)blockIdx.x * groups;
 #pragma unroll
-      for (int i = 0; i < P; ++i) xh[i] = mul2<true>(fma2<true>(xh[i], by[r], minus[r]), r2[r]);
-    };
-    auto read_weights = [&](int q, F2(&w)[P]) {
+  for (int k = 0; k < kRing - 1; ++k) {
+    mean_next[k] = rstd_next[k] = 0.f;
+    exp_next[k] = 0;
+    fetch(base + g.index + k * step, k);
+    fetch_small(base + g.index + k * step, mean_next[k], rstd_next[k], exp_next[k]);
+  }
+  uint32_t slot = 0;
+  for (; base < a.rows; base += step) {  // the same turns for all groups of threads
+    const uint64_t row = base + g.index;
+    const bool active = row < a.rows;
+    const float mean = mean_next[0], rstd = rstd_next[0], scale = scale_of(exp_next[0]);
 #pragma unroll
-      for (int i = 0; i < P; i += 2) {
-        const float4 f = *reinterpret_cast<const float4*>(weights + column(q * V) + 2 * i);
-        w[i] = f2(f.x, f.y);
-        w[i + 1] = f2(f.z, f.w);
-      }
-    };
-    asm volatile("cp.async.wait_group %0;" ::"n"(kTurns - 1) : "memory");
-    F2 s0[2], s1[2];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) s0[r] = s1[r] = f2(0.f, 0.f);
+    for (int k = 0; k < kRing - 2; ++k) {
+      mean_next[k] = mean_next[k + 1];
+      rstd_next[k] = rstd_next[k + 1];
+      exp_next[k] = exp_next[k + 1];
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+    const F2 by = f2(scale, scale), minus = f2(-mean, -mean), r2 = f2(rstd, rstd);
+    F2 xh[Q][P], d[Q][P], s0 = f2(0.f, 0.f), s1 = s0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
-      if (!there[q]) continue;
-      F2 w[P];
-      read_weights(q, w);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (!active[r]) continue;
-        F2 d[P], xh[P];
-        read(q, r, d, xh);
+      const uint8_t* from = mine + slot * kSlot;
+      Raw<T, V> raw;
+      raw.w = *reinterpret_cast<const uint4*>(from + q * MAXT * 16);
+      unpack<T, V>(raw, d[q]);
+      codes_f2<V>(load_codes<V>(reinterpret_cast<const int8_t*>(from + Q * MAXT * 16 + q * V)),
+                  xh[q]);
+      if (active && there[q]) {
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-          gw[q][i] = fma2<true>(d[i], xh[i], gw[q][i]);
-          gb[q][i] = add2<true>(gb[q][i], d[i]);
-          d[i] = mul2<true>(d[i], w[i]);
-          s0[r] = add2<true>(s0[r], d[i]);
-          s1[r] = fma2<true>(d[i], xh[i], s1[r]);
+          // c 2^e is exact, and so its difference from the mean is rounded once
+          xh[q][i] = mul2<true>(fma2<true>(xh[q][i], by, minus), r2);
+          gw[q][i] = fma2<true>(d[q][i], xh[q][i], gw[q][i]);
+          gb[q][i] = add2<true>(gb[q][i], d[q][i]);
+          d[q][i] = mul2<true>(d[q][i], w[q][i]);
+          s0 = add2<true>(s0, d[q][i]);
+          s1 = fma2<true>(d[q][i], xh[q][i], s1);
         }
       }
     }
-    float s[4] = {s0[0].x + s0[0].y, s1[0].x + s1[0].y, s0[1].x + s0[1].y, s1[1].x + s1[1].y};
-    sum4(g, room + 128 * g.index, sums++, s);
+    const uint64_t later = row + (kRing - 1) * step;
+    fetch(later, slot == 0 ? kRing - 1 : slot - 1);
+    fetch_small(later, mean_next[kRing - 2], rstd_next[kRing - 2], exp_next[kRing - 2]);
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    const float2 s = g.sum2(make_float2(s0.x + s0.y, s1.x + s1.y));
+    if (!active) continue;
     // dx = rstd (d - sum(d) / dim - xh sum(d xh) / dim)
+    const float k1s = -s.x * inv * rstd, k2s = -s.y * inv * rstd;
+    const F2 k1 = f2(k1s, k1s), k2 = f2(k2s, k2s);
+    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      if (!there[q]) continue;
-      F2 w[P];
-      read_weights(q, w);
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (!active[r]) continue;
-        const float k1 = -s[2 * r] * inv * rstd[r], k2 = -s[2 * r + 1] * inv * rstd[r];
-        F2 d[P], xh[P];
-        read(q, r, d, xh);
+    for (int q = 0; q < Q; ++q)
+      if (there[q]) {
 #pragma unroll
         for (int i = 0; i < P; ++i)
-          d[i] = fma2<true>(xh[i], f2(k2, k2),
-                            fma2<true>(mul2<true>(d[i], w[i]), r2[r], f2(k1, k1)));
-        T* dx = static_cast<T*>(a.dx) + (int64_t)(row0 + r) * a.dx_stride;
-        *reinterpret_cast<uint4*>(dx + column(q * V)) = pack<T, V>(d);
+          d[q][i] = fma2<true>(xh[q][i], k2, fma2<true>(d[q][i], r2, k1));
+        *reinterpret_cast<uint4*>(dx + column(q * V)) = pack<T, V>(d[q]);
       }
-    }
-    fetch(row0 + kTurns * step, turn);
-    turn = turn + 1 == kTurns ? 0 : turn + 1;
   }
   if (a.part_w == nullptr) return;  // neither sum is wanted
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -638,17 +571,12 @@ __global__ void __launch_bounds__(128) norm8_columns_kernel(const Norm8Args a) {
   a.part_b[(uint64_t)blockIdx.y * a.dim + c] = gb;
 }
 
-// One block per SM of as many groups of threads as fit, fewer where there are few rows; never more
-// blocks than backward_shape has, by which the workspace is sized.
-template <typename T>
-bool launch_norm8(const Norm8Args& a, BackwardShape& h, cudaStream_t s) {
-  auto kernel = norm8_backward_kernel<T>;
-  const uint32_t least = std::max(1u, 256 / h.threads), most = kNorm8Threads<T> / h.threads;
-  const uint32_t groups = (uint32_t)std::min<uint64_t>(
-      most, std::max<uint64_t>(least, align_up((a.rows + 2 * kSms - 1) / (2 * kSms), least)));
-  h.block = groups * h.threads;
-  h.parts = (uint32_t)std::min<uint64_t>(kSms, (a.rows + 2 * groups - 1) / (2 * groups));
-  const size_t smem = kTurns * 2 * kNorm8Slot<T> + a.dim * sizeof(float);
+template <typename T, int MAXT, int MINB>
+bool launch_norm8(const Norm8Args& a, const BackwardShape& h, cudaStream_t s) {
+  auto kernel = norm8_backward_kernel<T, MAXT, MINB>;
+  const uint32_t groups = h.block / h.threads;
+  const size_t ring = (size_t)kRing * (sizeof(T) + 1) * MAXT * 16;
+  const size_t smem = std::max(ring, groups > 1 ? (size_t)2 * groups * a.dim * sizeof(float) : (size_t)0);
   if (!ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
   launch_pdl(kernel, h.parts, h.block, smem, s, a);
   return true;
@@ -663,8 +591,9 @@ bool launch_norm8_any(const Norm8Args& a, const BackwardShape& h, cudaStream_t s
   return true;
 }
 template <typename T>
-bool launch_norm8_shape(const Norm8Args& a, BackwardShape& h, bool packs, cudaStream_t s) {
-  if (packs) return launch_norm8<T>(a, h, s);
+bool launch_norm8_shape(const Norm8Args& a, const BackwardShape& h, bool packs, cudaStream_t s) {
+  if (packs && h.block <= 256) return launch_norm8<T, 256, kFit>(a, h, s);
+  if (packs) return launch_norm8<T, 512, 1>(a, h, s);
   if (h.threads == 8) return launch_norm8_any<T, 8, 256, kFit>(a, h, s);
   if (h.threads == 16) return launch_norm8_any<T, 16, 256, kFit>(a, h, s);
   if (h.block <= 256) return launch_norm8_any<T, 32, 256, kFit>(a, h, s);
@@ -678,7 +607,7 @@ bool norm8_typed(Norm8Args a, float* dweight, float* dbias, int32_t accumulate, 
   const bool packs = a.dim % V == 0 && a.dy_stride % V == 0 && a.dx_stride % V == 0 &&
                      aligned_to(a.dy, 16) && aligned_to(a.dx, 16);
   const bool sums = dweight || dbias;
-  BackwardShape h = backward_shape(a.rows, a.dim);  // as launched, in the end
+  const BackwardShape h = backward_shape(a.rows, a.dim);
   a.threads = h.threads;
   a.part_w = sums ? reinterpret_cast<float*>(ws + 256) : nullptr;
   a.part_b = reinterpret_cast<float*>(ws + 256) + (uint64_t)h.parts * a.dim;
