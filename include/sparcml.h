@@ -664,7 +664,7 @@ int sparcml_expert_linear_backward8(const void* dy, int64_t dy_stride, const int
  *             elements of an output at one address. Outputs may be the inputs
  *             themselves (same strides). q_heads or k_heads may be 0.
  *   positions device int32 or, positions_int64, int64 [tokens], any value: the
- *             angle is exact to 2^-33 of a turn and 2^-64 |p|.
+ *             angle is off by at most 2^-26 of a turn and 2^-64 |p|.
  *   freqs     device fp32 [turned / 2], radians per position, finite.
  *   q_weight, k_weight  [dim] of type weight_type, each may be NULL (ones).
  *   tokens 0 .. 2^31 - 1, dim 1 .. 512, turned even, 0 .. dim, heads 0 .. 65535. */
