@@ -605,8 +605,8 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  * row's result and its own expert's dW alone.
  *   x, dx [rows][k], y, dy [rows][n], weight: type `type`, SPARCML_BF16 or
  *             SPARCML_F16 (the tensor cores have no fp32 product); strides as
- *             for layer norm, those of the matrices weight_batch_stride and
- *             weight_stride >= 0.
+ *             for layer norm, those of the matrices weight_batch_stride (0: one
+ *             for all experts) and weight_stride >= 0.
  *   offsets   DEVICE int32 [experts + 1], rising, from 0 at least to rows at
  *             most; or NULL for one expert with all rows. Rows of no expert
  *             are neither read nor written. An offset out of order or range

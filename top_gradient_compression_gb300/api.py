@@ -928,7 +928,8 @@ def _layer_norm_backward8(dy, x, mean, rstd, weight, dx, dweight, dbias, accumul
 def expert_linear_workspace_size(rows: int, experts: int, n: int, k: int,
                                  aligned: bool = True) -> int:
     """Bytes of a workspace for expert_linear and its backward pass. ``aligned``: every operand
-    starts on 16 bytes and is contiguous, or has strides that are multiples of 8 elements."""
+    starts on 16 bytes and is contiguous, or has strides that are multiples of 8 elements and rows
+    that do not overlap."""
     return int(_lib.load().sparcml_expert_linear_workspace_size(rows, experts, n, k, aligned))
 
 
@@ -976,8 +977,8 @@ def _offsets(offsets, weight):
 def _fit(size, ws, device, *operands):
     """The workspace, or a new one for operands of this alignment."""
     if ws is None:
-        aligned = all(t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in t.stride()[:-1])
-                      for t in operands)
+        aligned = all(t.data_ptr() % 16 == 0 and t.stride(-2) >= t.shape[-1] and
+                      all(s % 8 == 0 for s in t.stride()[:-1]) for t in operands)
         ws = workspace(expert_linear_workspace_size(*size, aligned), device)
     return _space(ws)
 

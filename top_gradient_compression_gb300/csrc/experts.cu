@@ -59,6 +59,7 @@ struct ExpertArgs {
   uint32_t splits;      // forward, dx: parts of the summed axis
   uint32_t may_split;   // dW: whether long runs of rows are taken in parts
   uint32_t wide;        // j of a partial tile
+  uint32_t shared;      // one matrix for all experts
   void* out;
   int32_t out_type;
   int64_t out_batch, out_stride;
@@ -196,7 +197,8 @@ struct Worker {
 // last rows of an expert's run go to a barrier of the block's own, and are reported once those of
 // the next expert are zeros.
 template <int FORM>
-__device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const Item& it) {
+__device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const ExpertArgs& a,
+                                          const Item& it) {
   const uint32_t i0 = it.i0 + 128 * w.rank, j0 = it.j0 + it.width / 2 * w.rank;
   const uint32_t boxes = (it.width / 2 + kBox - 1) / kBox;
   const uint32_t bytes = kOperand + (FORM == kWeight ? kOperand : boxes * kBox * 128);
@@ -213,9 +215,9 @@ __device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const 
       else mbar_arrive_cluster(w.lead_full + 8 * s);
       const uint32_t at = FORM == kWeight ? it.row + b * 64 : b * 64;
       if constexpr (FORM == kForward) {
-        tma_load_3d_group<2>(p, &m.p, at, i0, it.e, bar);
+        tma_load_3d_group<2>(p, &m.p, at, i0, a.shared ? 0 : it.e, bar);
       } else {
-        const uint32_t z = FORM == kInput ? it.e : 0;
+        const uint32_t z = FORM == kInput && !a.shared ? it.e : 0;
         tma_load_3d_group<2>(p, &m.p, i0, at, z, bar);
         tma_load_3d_group<2>(p + kOperand / 2, &m.p, i0 + 64, at, z, bar);
       }
@@ -458,7 +460,7 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   const uint32_t items = table.first[a.experts];
   if (warp == kWriters) {
     for (uint32_t x = w.pair; x < items; x += w.pairs)
-      if (!load_item<FORM>(w, m, item_of<FORM>(a, table, x))) break;
+      if (!load_item<FORM>(w, m, a, item_of<FORM>(a, table, x))) break;
   } else if (warp == kWriters + 1) {
     // An injected fault: the first pair withholds its products.
     const bool withhold = w.pair == 0 && waits.limit_us == kInjectWaitUs;
@@ -609,6 +611,11 @@ struct Operand {  // `batches` matrices of `rows` rows of `cols` elements of 16 
   int64_t batch, stride;
   uint64_t batches, rows, cols;
 
+  // The matrices of all experts, of which there is one where they lie at one place.
+  static Operand matrices(const void* p, int64_t batch, int64_t stride, const Sizes& z) {
+    return {p, batch, stride, batch == 0 ? 1 : z.experts, z.n, z.k};
+  }
+
   uint64_t pitch() const { return align_up(cols, 8); }
   size_t copy_bytes() const { return align_up(batches * rows * pitch() * 2, 256); }
   bool fits() const {
@@ -752,6 +759,7 @@ int run(const Call& c, Operand p, Operand q, void* out, int32_t out_type, int64_
   a.out_batch = out_batch;
   a.out_stride = out_stride;
   a.accumulate = accumulate;
+  a.shared = FORM != kWeight && p.batches == 1;
   a.bf16 = c.type == SPARCML_BF16;
   a.part = reinterpret_cast<float*>(w + 256);
   a.status = reinterpret_cast<int32_t*>(w);
@@ -868,7 +876,7 @@ extern "C" int sparcml_expert_linear(const void* x, int64_t x_stride, const void
                static_cast<cudaStream_t>(stream)};
   const int r = check_call(c);
   if (r != SPARCML_OK) return r;
-  Operand w{weight, weight_batch_stride, weight_stride, experts, n, k};
+  Operand w = Operand::matrices(weight, weight_batch_stride, weight_stride, c.z);
   Operand q{x, 0, x_stride, 1, rows, k};
   if (rows == 0) return SPARCML_OK;
   if (!operand_ok(w) || !operand_ok(q) || !result_ok(y, rows, n, y_stride))
@@ -891,7 +899,7 @@ extern "C" int sparcml_expert_linear_backward(
   const Call c{{rows, experts, n, k}, type, offsets, ws, ws_bytes,
                static_cast<cudaStream_t>(stream)};
   return backward(c, {dy, 0, dy_stride, 1, rows, n}, {x, 0, x_stride, 1, rows, k}, nullptr,
-                  {weight, weight_batch_stride, weight_stride, experts, n, k}, dx, dx_stride,
+                  Operand::matrices(weight, weight_batch_stride, weight_stride, c.z), dx, dx_stride,
                   dweight, dweight_batch_stride, dweight_stride, accumulate);
 }
 
@@ -908,6 +916,6 @@ extern "C" int sparcml_expert_linear_backward8(
   const Stored x{codes, codes_stride, exponents, exponents_stride};
   if (dweight && rows && (!codes || !exponents)) return SPARCML_ERR_INVALID_ARG;
   return backward(c, {dy, 0, dy_stride, 1, rows, n}, {}, &x,
-                  {weight, weight_batch_stride, weight_stride, experts, n, k}, dx, dx_stride,
+                  Operand::matrices(weight, weight_batch_stride, weight_stride, c.z), dx, dx_stride,
                   dweight, dweight_batch_stride, dweight_stride, accumulate);
 }
