@@ -618,7 +618,8 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  *             expert without rows gets +0. accumulate != 0 adds to what it
  *             holds.
  *   backward  dx or dweight NULL: that gradient is left out, and weight or x
- *             is not read. backward8 takes x in 8 bits.
+ *             is not read. backward8 takes x in 8 bits, its exponents as
+ *             checkpoint8 writes them for `type`.
  *   experts 1 .. 1024, rows 0 .. 2^31 - 1, n and k 1 .. 2^24.
  *   ws        >= sparcml_expert_linear_workspace_size(...) bytes, 256-byte
  *             aligned, for all of them. aligned != 0: every operand starts on 16

@@ -14,18 +14,19 @@
 // with few rows costs what reading its matrix costs and no more. No operand is transposed: the
 // tensor cores read either axis as the contiguous one.
 //
-// One launch, a persistent grid of pairs of SMs. Of a block's ten warps one loads operands by TMA,
-// one issues the products (for both blocks of a pair), eight turn accumulators into results while
-// the next tile is under way. Where the experts' runs begin and end is read on the device: every
-// block works out the same list of tiles from them. A long summed axis with few tiles is split; the
-// parts are added in order by a second launch.
+// One launch, a persistent grid of pairs of SMs. Of a block's twelve warps one loads operands by
+// TMA, one issues the products (for both blocks of a pair), eight turn accumulators into results
+// while the next tile is under way, one clears rows (below). Where the experts' runs begin and end
+// is read on the device: every block works out the same list of tiles from them, and they are handed
+// out as pairs get to them. A long summed axis is split where there are few tiles, and for dW, whose
+// tiles are as deep as the experts' runs, in those tiles that no whole round of all pairs is left
+// for; the parts are added in order by a second launch.
 //
 // Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. The tensor cores
 // drop the bits that do not fit when they add to an accumulator, always towards zero: over 16,384
 // rows dW came out 1.9e-5 off, and that is an fp32 result. So an accumulator takes 512 rows, and
-// the writers' registers add those sums, rounded: 5e-7. For dW, the rows
-// of the last 64 that belong to the next expert are zeros in both operands, so that what stands
-// there, a NaN say, does not count.
+// the writers' registers add those sums, rounded: 5e-7. For dW, the rows of the last 64 that belong to
+// the next expert are zeros in both operands, so that what stands there, a NaN say, does not count.
 
 #include <algorithm>
 #include <map>
@@ -33,6 +34,7 @@
 
 #include "stored.cuh"
 #include "tensor.cuh"
+#include "types.cuh"
 
 namespace sparcml {
 namespace {
@@ -40,24 +42,44 @@ namespace {
 constexpr uint32_t kMostExperts = 1024;
 constexpr uint32_t kSide = 256;      // i and j of a tile, at most
 constexpr uint32_t kPairs = 76;      // of SMs
-constexpr uint32_t kWriters = 8;     // warps that write results; then a loader and an issuer
-constexpr uint32_t kThreads = 32 * (kWriters + 2);
+constexpr uint32_t kWriters = 8;     // warps that write results; then a loader, an issuer, a clearer
+constexpr uint32_t kThreads = 32 * (kWriters + 4);
 constexpr uint32_t kOperand = 128 * 128;  // bytes of one operand's 64 of the summed axis, per block
 constexpr uint32_t kStageBytes = 2 * kOperand, kStages = 6;
 constexpr uint32_t kSmem = kStages * kStageBytes + 1024;
 constexpr uint32_t kBox = 32;        // rows of Q per load
-constexpr uint32_t kLeastBlocks = 8;  // of 64 in a part of a split sum, at least
+constexpr uint32_t kLeastBlocks = 8;  // forward, dx: of 64 in a part of a split sum, at least
+constexpr uint32_t kJoinBlocks = 28;  // dW: blocks of 64 rows that take as long as adding up parts
+constexpr uint32_t kSorted = 256;     // dW: experts, at most, that are taken by falling depth
+constexpr uint32_t kFeed = 4;         // items that a pair's first loader can be ahead
+// The workspace header's word that counts the items handed out; zero between kernels.
+constexpr size_t kItemsOffset = 48;
 constexpr uint32_t kRun = 8;          // dW: blocks of 64 rows that one accumulator takes
 constexpr uint32_t kBand = 8;        // tiles along j that are taken together, for L2's sake
 
 enum Form { kForward, kInput, kWeight };
+
+// x from its 8 bits into 16, for dW: a side job of the two warps that dx has nothing to do for, 16
+// columns per lane at a time. c 2^e is a number of either type, so nothing is rounded. (Converting in
+// the dW kernel itself, on the way to the products, took 500 us in all for 16384 x 2048 x 4096
+// against 165 for x in 16 bits: four warps are too few for it, and shared memory, whose bandwidth
+// the products' operands take up, is written and read twice more. A kernel of its own takes 32.)
+struct Restore {
+  const int8_t* codes;  // or null: nothing to do
+  int64_t codes_stride;
+  const uint8_t* exponents;
+  int64_t exponents_stride;
+  void* to;        // [rows][pitch]
+  uint64_t pitch;  // a multiple of 8
+  uint32_t rows, dim;
+};
 
 struct ExpertArgs {
   const int32_t* offsets;  // or null: one expert with all rows
   uint32_t experts, rows;
   uint32_t i_size, j_size, s_size;  // j_size for dW, s_size for the others; the rest is rows
   uint32_t splits;      // forward, dx: parts of the summed axis
-  uint32_t may_split;   // dW: whether long runs of rows are taken in parts
+  uint32_t may_split;   // dW: whether tiles may be taken in parts
   uint32_t wide;        // j of a partial tile
   uint32_t shared;      // one matrix for all experts
   void* out;
@@ -65,35 +87,43 @@ struct ExpertArgs {
   int64_t out_batch, out_stride;
   int32_t accumulate;
   uint32_t bf16;        // operands; else fp16
-  float* part;          // [item][wide][256]
+  float* part;          // [slot][wide][256]
   int32_t* status;
   const uint32_t* inject;
+  uint32_t* handed_out;
+  Restore restore;      // dx: the side job
 };
 struct ExpertMaps {
   CUtensorMap p, q;
 };
 
-// The experts' runs and tiles, in shared memory.
+// The experts' runs and items, in shared memory. An item is a tile, or a part of its summed axis.
+// Of forward and dx all tiles are in `splits` parts. dW takes the experts by falling depth: whole
+// tiles first, of which `whole` fill rounds of all pairs, then `rest` tiles in `splits` parts.
 struct Table {
   int32_t begin[kMostExperts + 1];   // of the expert's rows; the last: where they end
-  uint32_t first[kMostExperts + 1];  // the expert's first item; the last: their number
-  uint32_t chunk;                    // dW: blocks of 64 rows in a part
+  uint32_t first[kMostExperts + 1];  // the first item (dW: tile) of the experts in their order
+  uint16_t order[kMostExperts];      // dW
+  uint32_t items, whole, rest, splits;
 };
 
+constexpr uint32_t kNone = 0xffffffffu;
 struct Item {
-  uint32_t e, i0, j0, width;   // j0: a row of all rows (forward, dx), or of dW's matrix
-  uint32_t count;              // of its j, those that exist
-  uint32_t row, rows;          // the expert's run
-  uint32_t s0, s1;             // blocks of 64 of the summed axis
-  uint32_t split, splits;
+  uint32_t e, i0, j0, width;  // j0: a row of all rows (forward, dx), or of dW's matrix
+  uint32_t count;             // of its j, those that exist
+  uint32_t row, rows;         // the expert's run
+  uint32_t s0, s1;            // blocks of 64 of the summed axis
+  uint32_t slot;              // where it is a part: which one, else kNone
 };
 
 __device__ __forceinline__ uint32_t ceil_of(uint32_t a, uint32_t b) { return (a + b - 1) / b; }
+__device__ __forceinline__ uint32_t rows_of(const Table& t, uint32_t e) {
+  return (uint32_t)(t.begin[e + 1] - t.begin[e]);
+}
 
-// The table, by one warp. An offset out of order or range counts as the nearest that is not;
-// returns whether there was one.
-template <int FORM>
-__device__ bool make_table(const ExpertArgs& a, Table& t, uint32_t pairs) {
+// Where the experts' runs begin, by one warp. An offset out of order or range counts as the
+// nearest that is not; returns whether there was one.
+__device__ __forceinline__ bool make_runs(const ExpertArgs& a, Table& t) {
   const uint32_t lane = lane_id();
   bool bad = false;
   int32_t carry = 0;
@@ -112,59 +142,102 @@ __device__ bool make_table(const ExpertArgs& a, Table& t, uint32_t pairs) {
     bad |= there && v != given;
     carry = __shfl_sync(0xffffffffu, v, 31);
   }
-  __syncwarp();
-  const uint32_t ti = ceil_of(a.i_size, kSide);
-  const uint32_t tiles = FORM == kWeight ? ti * ceil_of(a.j_size, kSide) : 0;
-  uint32_t chunk = 0x7fffffffu;
-  if (FORM == kWeight && a.may_split) {  // shares of the whole work, one for each pair
-    uint32_t blocks = 0;
-    for (uint32_t e = lane; e < a.experts; e += 32)
-      blocks += ceil_of((uint32_t)(t.begin[e + 1] - t.begin[e]), 64);
-    const uint64_t all = (uint64_t)warp_sum(blocks) * tiles;
-    chunk = max(kLeastBlocks, (uint32_t)((all + pairs - 1) / pairs));
+  return __any_sync(0xffffffffu, bad);
+}
+
+// The rest of the table, from all of a block's threads (and between their barriers).
+template <int FORM>
+__device__ __forceinline__ void make_items(const ExpertArgs& a, Table& t, uint32_t pairs) {
+  // By falling depth, so that the last tiles are the short ones: an expert's place is how many go
+  // before it. (Beyond kSorted that count would take longer than it is worth.)
+  if (FORM == kWeight) {
+    for (uint32_t e = threadIdx.x; e < a.experts; e += blockDim.x) {
+      uint32_t place = e;
+      if (a.experts <= kSorted) {
+        const uint32_t rows = rows_of(t, e);
+        place = 0;
+        for (uint32_t o = 0; o < a.experts; ++o) {
+          const uint32_t r = rows_of(t, o);
+          place += r > rows || (r == rows && o < e);
+        }
+      }
+      t.order[place] = (uint16_t)e;
+    }
+    __syncthreads();
   }
+  if (threadIdx.x >= 32) return;
+  const uint32_t lane = lane_id();
+  const uint32_t ti = ceil_of(a.i_size, kSide), tj = ceil_of(a.j_size, kSide);
   uint32_t sum = 0;
   for (uint32_t base = 0; base < a.experts; base += 32) {
     const uint32_t e = base + lane;
     uint32_t n = 0;
-    if (e < a.experts) {
-      const uint32_t rows = (uint32_t)(t.begin[e + 1] - t.begin[e]);
-      n = FORM == kWeight ? tiles * max(1u, ceil_of(ceil_of(rows, 64), chunk))
-                          : ti * ceil_of(rows, kSide) * a.splits;
-    }
+    if (e < a.experts)
+      n = FORM == kWeight ? ti * tj : ti * ceil_of(rows_of(t, e), kSide) * a.splits;
     const uint32_t upto = warp_incl_sum(n);
     if (e < a.experts) t.first[e] = sum + upto - n;
     sum += __shfl_sync(0xffffffffu, upto, 31);
   }
+  if (FORM != kWeight) {
+    if (lane == 0) {
+      t.first[a.experts] = t.items = sum;
+      t.splits = a.splits;
+    }
+    return;
+  }
+  // The rest after whole rounds, in as many parts as it is done soonest with. Rounds of parts of
+  // the rest's deepest tile count, and kJoinBlocks for adding the parts up.
+  const uint32_t rest = sum % pairs, whole = sum - rest;
+  uint32_t splits = 1;
+  if (a.may_split && rest) {
+    const uint32_t depth = ceil_of(rows_of(t, t.order[whole / (ti * tj)]), 64);
+    const uint32_t most = min(2 * pairs / rest, depth / kLeastBlocks);
+    auto cost = [](uint32_t blocks, uint32_t parts) {  // blocks, then parts (at most 152)
+      return min(blocks, 0xffffffu) << 8 | parts;
+    };
+    uint32_t best = cost(depth, 1);
+    for (uint32_t c = 2 + lane; c <= most; c += 32)
+      best = min(best, cost(ceil_of(rest * c, pairs) * ceil_of(depth, c) + kJoinBlocks, c));
+    splits = __reduce_min_sync(0xffffffffu, best) & 255u;
+  }
   if (lane == 0) {
     t.first[a.experts] = sum;
-    t.chunk = chunk;
+    t.whole = whole;
+    t.rest = rest;
+    t.splits = splits;
+    t.items = whole + rest * splits;
   }
-  return __any_sync(0xffffffffu, bad);
 }
 
 template <int FORM>
 __device__ __forceinline__ Item item_of(const ExpertArgs& a, const Table& t, uint32_t index) {
-  uint32_t lo = 0, hi = a.experts;  // first[lo] <= index < first[hi]
+  uint32_t tile = index, split = 0, splits = 1;
+  if (FORM == kWeight && index >= t.whole) {
+    // all tiles' first parts, then their second ones: neighbours read the same rows
+    split = (index - t.whole) / t.rest;
+    tile = index - split * t.rest;
+    splits = t.splits;
+  }
+  uint32_t lo = 0, hi = a.experts;  // first[lo] <= tile < first[hi]
   while (hi - lo > 1) {
     const uint32_t mid = (lo + hi) / 2;
-    if (t.first[mid] <= index) lo = mid;
+    if (t.first[mid] <= tile) lo = mid;
     else hi = mid;
   }
+  uint32_t u = tile - t.first[lo];
   Item it;
-  it.e = lo;
-  it.row = (uint32_t)t.begin[lo];
-  it.rows = (uint32_t)t.begin[lo + 1] - it.row;
-  uint32_t u = index - t.first[lo];
-  const uint32_t blocks = ceil_of(FORM == kWeight ? it.rows : a.s_size, 64);
-  it.splits = FORM == kWeight ? max(1u, ceil_of(blocks, t.chunk)) : a.splits;
-  it.split = 0;
-  if (it.splits > 1) {
-    it.split = u % it.splits;
-    u /= it.splits;
+  it.e = FORM == kWeight ? t.order[lo] : lo;
+  it.row = (uint32_t)t.begin[it.e];
+  it.rows = rows_of(t, it.e);
+  if (FORM != kWeight && a.splits > 1) {
+    splits = a.splits;
+    split = u % splits;
+    u /= splits;
   }
-  it.s0 = (uint32_t)((uint64_t)blocks * it.split / it.splits);
-  it.s1 = (uint32_t)((uint64_t)blocks * (it.split + 1) / it.splits);
+  it.slot = splits == 1 ? kNone : FORM == kWeight ? index - t.whole : index;
+  const uint32_t blocks = ceil_of(FORM == kWeight ? it.rows : a.s_size, 64);
+  it.s0 = (uint32_t)((uint64_t)blocks * split / splits);
+  it.s1 = (uint32_t)((uint64_t)blocks * (split + 1) / splits);
   const uint32_t j_size = FORM == kWeight ? a.j_size : it.rows;
   const uint32_t tj = ceil_of(j_size, kSide), ti = ceil_of(a.i_size, kSide);
   // the rows of an expert are shared out evenly; of dW's matrix only the last tile is narrower
@@ -180,22 +253,85 @@ __device__ __forceinline__ Item item_of(const ExpertArgs& a, const Table& t, uin
 
 struct Worker {
   uint32_t ring, full, empty, acc_full, acc_empty, tail;  // shared-memory addresses
+  uint32_t fed, lead_fed_empty, feed_full;  // of the feed: its values and barriers
   uint32_t lead_full, lead_acc_empty, own_tail;           // in the cluster's shared memory
-  uint32_t rank, pair, pairs, tmem;
+  uint32_t rank, pair, pairs, items, tmem;
   bool leader;  // the lane that issues for its warp
   Waits* waits;
   uint32_t stage = 0, phase = 0, acc = 0, tails = 0;
+  uint32_t feed = 0, feed_phase = 0;  // the feed's next slot, and its turn's parity
   __device__ __forceinline__ void next_stage() {
     if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
     }
   }
+  __device__ __forceinline__ void skip(uint32_t blocks) {  // stages that others go through
+    const uint32_t at = stage + blocks;
+    stage = at % kStages;
+  }
+  __device__ __forceinline__ void next_feed() {
+    if (++feed == kFeed) {
+      feed = 0;
+      feed_phase ^= 1u;
+    }
+  }
 };
 
+// Items are handed out as pairs get to them: the first of each is its own number, of the others the
+// loader of a pair's first block draws the number when it begins the one before, and feeds it to
+// all other warps of both blocks. (With every 76th tile to each pair, 16384 rows in 8 unequal runs
+// took 234 us for 4096 x 2048, and with shares of one stream of blocks, which no longer read the
+// same rows at the same time, 237.)
+//
+// Every pair draws until it gets a number past the end; who draws the last of those resets the
+// counter for the next kernel.
+__device__ __forceinline__ uint32_t draw_item(const Worker& w, const ExpertArgs& a) {
+  uint32_t drawn = 0;
+  if (w.leader) drawn = atomicAdd(a.handed_out, 1u);
+  return drawn;
+}
+__device__ __forceinline__ uint32_t drawn_item(const Worker& w, const ExpertArgs& a,
+                                               uint32_t drawn) {
+  if (w.leader && drawn == w.items - 1) *a.handed_out = 0;
+  const uint32_t lane = __ffs(__ballot_sync(0xffffffffu, w.leader)) - 1;
+  const uint32_t x = w.pairs + __shfl_sync(0xffffffffu, drawn, lane);
+  return x < w.items ? x : kNone;
+}
+// Tells both blocks' warps; kNone if they do not get to it in time.
+__device__ __forceinline__ uint32_t feed_item(Worker& w, uint32_t fed_empty, uint32_t x) {
+  const uint32_t s = w.feed;
+  if (!mbar_wait_warp_inline(fed_empty + 8 * s, w.feed_phase ^ 1u, w.waits)) return kNone;
+  if (w.leader) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(w.fed + 4 * s), "r"(x) : "memory");
+    mbar_arrive(w.feed_full + 8 * s);
+    // (released for the pair by an arrival, it would take this warp a microsecond)
+    store_cluster_async(cluster_addr(w.fed + 4 * s, 1), x, cluster_addr(w.feed_full + 8 * s, 1));
+  }
+  __syncwarp();
+  w.next_feed();
+  return x;
+}
+// The next item of any other warp. LOADER: the second block's, which has the feed's barrier expect
+// the word.
+template <bool LOADER = false>
+__device__ __forceinline__ uint32_t next_item(Worker& w) {
+  if (w.items <= w.pairs) return kNone;
+  const uint32_t s = w.feed;
+  if (LOADER && w.leader) mbar_expect_tx(w.feed_full + 8 * s, 4);
+  if (!mbar_wait_warp_inline<true>(w.feed_full + 8 * s, w.feed_phase, w.waits)) return kNone;
+  uint32_t x;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(w.fed + 4 * s) : "memory");
+  __syncwarp();
+  if (w.leader) mbar_arrive_cluster(w.lead_fed_empty + 8 * s);  // releasing would await its stores
+  __syncwarp();
+  w.next_feed();
+  return x;
+}
+
 // Both blocks of a pair load their halves of P and Q; the first one's barriers count for both. The
-// last rows of an expert's run go to a barrier of the block's own, and are reported once those of
-// the next expert are zeros.
+// last rows of an expert's run go to a barrier of the block's own, and are reported by its clearer
+// once those of the next expert are zeros.
 template <int FORM>
 __device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const ExpertArgs& a,
                                           const Item& it) {
@@ -204,13 +340,12 @@ __device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const 
   const uint32_t bytes = kOperand + (FORM == kWeight ? kOperand : boxes * kBox * 128);
   for (uint32_t b = it.s0; b < it.s1; ++b, w.next_stage()) {
     const uint32_t s = w.stage;
-    if (!mbar_wait_warp(w.empty + 8 * s, w.phase ^ 1u, w.waits)) return false;
-    const uint32_t left = FORM == kWeight ? it.rows - b * 64 : 64;  // rows of the block
-    const bool cut = FORM == kWeight && left < 64;
-    const uint32_t bar = cut ? w.own_tail : w.lead_full + 8 * s;
+    if (!mbar_wait_warp_inline(w.empty + 8 * s, w.phase ^ 1u, w.waits)) return false;
+    const bool cut = FORM == kWeight && it.rows - b * 64 < 64;
+    const uint32_t bar = cut ? w.own_tail + 8 * s : w.lead_full + 8 * s;
     const uint32_t p = w.ring + s * kStageBytes, q = p + kOperand;
     if (w.leader) {
-      if (cut) mbar_expect_tx(w.tail, bytes);
+      if (cut) mbar_expect_tx(w.tail + 8 * s, bytes);
       else if (w.rank == 0) mbar_expect_tx(w.full + 8 * s, 2 * bytes);
       else mbar_arrive_cluster(w.lead_full + 8 * s);
       const uint32_t at = FORM == kWeight ? it.row + b * 64 : b * 64;
@@ -230,54 +365,91 @@ __device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const 
       }
     }
     __syncwarp();
-    if constexpr (FORM == kWeight) {
-      if (!cut) continue;
-      if (!mbar_wait_warp(w.tail, w.tails & 1u, w.waits)) {
+  }
+  return true;
+}
+
+// The clearer: waits for an item's last block where that is cut, and clears the rows behind the
+// run. (When the loader did so, it began the next loads 3 us later: 190 us in place of 161 for 4
+// runs of odd lengths.)
+__device__ __forceinline__ bool clear_item(Worker& w, const Item& it) {
+  const uint32_t blocks = it.s1 - it.s0;
+  if (blocks > 0) {
+    const uint32_t left = it.rows - (it.s1 - 1) * 64;  // rows of the last block
+    w.skip(blocks - 1);
+    if (left < 64) {
+      const uint32_t s = w.stage, p = w.ring + s * kStageBytes;
+      if (!mbar_wait_warp_inline(w.tail + 8 * s, w.tails >> s & 1u, w.waits)) {
         Waits alone = {0, kLandUs};  // what was begun has to land before the block leaves
-        mbar_wait_warp(w.tail, w.tails & 1u, &alone);
+        mbar_wait_warp_inline(w.tail + 8 * s, w.tails >> s & 1u, &alone);
         return false;
       }
-      ++w.tails;
-      // a row is 128 bytes of each of the four boxes
-      for (uint32_t c = lane_id(); c < 4 * (64 - left) * 8; c += 32) {
-        const uint32_t box = c / ((64 - left) * 8), rest = c - box * (64 - left) * 8;
-        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
-                         p + box * (kOperand / 2) + left * 128 + rest * 16),
-                     "r"(0)
-                     : "memory");
-      }
+      w.tails ^= 1u << s;
+      // a row is 128 bytes of each of the boxes of 8 KB: two of P, two of Q
+#pragma unroll
+      for (uint32_t box = 0; box < 4; ++box)
+        for (uint32_t at = left * 128 + 16 * lane_id(); at < 64 * 128; at += 512)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                           p + box * (kOperand / 2) + at),
+                       "r"(0)
+                       : "memory");
       proxy_fence_shared();
       __syncwarp();
       if (w.leader) mbar_arrive_cluster_release(w.lead_full + 8 * s);
       __syncwarp();
     }
+    w.skip(1);
   }
   return true;
 }
 
-// Until a stage is full. With dW, ordinary stores of either block may be part of that, so the wait
-// acquires for the pair. (As a fence of its own it took a microsecond for every block: 572 us
-// against 181 for 16384 x 2048 x 4096.)
-template <int FORM>
-__device__ __forceinline__ bool wait_full(uint32_t bar, uint32_t parity, Waits* waits) {
-  if constexpr (FORM != kWeight) return mbar_wait_warp(bar, parity, waits);
-  bool come = false;
-  for (uint32_t i = 0; i < 64 && !come; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred q;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    come = ok != 0;
+// Eight pieces of a lane are on their way at a time. (With two the side job took 100 us longer than
+// the products beside it.)
+template <typename T>
+__device__ __forceinline__ void restore_rows(const Restore& x, uint32_t thread, uint32_t threads) {
+  constexpr int kBatch = 8;
+  const uint32_t pieces = ceil_of(x.dim, 16);
+  uint32_t row = thread / pieces, piece = thread - row * pieces;
+  const uint32_t rows_on = threads / pieces, pieces_on = threads - rows_on * pieces;
+  while (row < x.rows) {
+    uint4 w[kBatch];
+    uint32_t e[kBatch];
+    uint4* to[kBatch];
+    bool both[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      to[q] = nullptr;
+      if (row < x.rows) {
+        w[q] = __ldg(reinterpret_cast<const uint4*>(x.codes + (int64_t)row * x.codes_stride) +
+                     piece);
+        e[q] = __ldg(x.exponents + (int64_t)row * x.exponents_stride + piece / (kGroup / 16));
+        to[q] = reinterpret_cast<uint4*>(static_cast<T*>(x.to) + row * x.pitch + 16 * piece);
+        both[q] = 16 * piece + 8 < x.pitch;
+      }
+      row += rows_on;
+      piece += pieces_on;
+      if (piece >= pieces) {
+        piece -= pieces;
+        ++row;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      if (!to[q]) continue;
+      const float scale = scale_of(e[q]);
+      const uint32_t words[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+      F2 lo[4], hi[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        lo[k] = f2(code_at(words[k / 2], 2 * k % 4) * scale,
+                   code_at(words[k / 2], 2 * k % 4 + 1) * scale);
+        hi[k] = f2(code_at(words[2 + k / 2], 2 * k % 4) * scale,
+                   code_at(words[2 + k / 2], 2 * k % 4 + 1) * scale);
+      }
+      to[q][0] = pack<T, 8>(lo);
+      if (both[q]) to[q][1] = pack<T, 8>(hi);
+    }
   }
-  if (!come) {
-    come = mbar_wait_long(bar, parity, waits);
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-  }
-  return __all_sync(0xffffffffu, come);
 }
 
 template <int FORM>
@@ -288,12 +460,15 @@ __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const
   for (uint32_t b = it.s0; b < it.s1;) {
     const uint32_t from = b, end = FORM == kWeight ? min(b + kRun, it.s1) : it.s1;
     const uint32_t acc = w.acc & 1u;
-    if (!mbar_wait_warp(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
+    if (!mbar_wait_warp_inline(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
     tmem_fence_after();
     const uint32_t d = w.tmem + acc * kSide;
     for (; b < end; ++b, w.next_stage()) {
       const uint32_t s = w.stage;
-      if (!wait_full<FORM>(w.full + 8 * s, w.phase, w.waits)) return false;
+      // With dW, ordinary stores of either block may be part of the stage, so the wait acquires for
+      // the pair. (As a fence of its own that took a microsecond for every block: 572 us against
+      // 190 for 16384 x 2048 x 4096.)
+      if (!mbar_wait_warp_inline<FORM == kWeight>(w.full + 8 * s, w.phase, w.waits)) return false;
       tmem_fence_after();
       if (w.leader) {
         const uint32_t p = w.ring + s * kStageBytes, q = p + kOperand;
@@ -326,11 +501,11 @@ __device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, float v) {
 // Sixteen sums of a thread's i, from column c of the tile: to their results, or where the parts of
 // a split sum wait to be added up.
 template <int FORM>
-__device__ __forceinline__ void put16(const ExpertArgs& a, const Item& it, uint32_t index,
-                                      uint32_t side, uint32_t c, const float (&v)[16]) {
+__device__ __forceinline__ void put16(const ExpertArgs& a, const Item& it, uint32_t side,
+                                      uint32_t c, const float (&v)[16]) {
   const uint32_t i = it.i0 + side;
-  if (it.splits > 1) {
-    float* o = a.part + ((uint64_t)index * a.wide + c) * kSide + side;
+  if (it.slot != kNone) {
+    float* o = a.part + ((uint64_t)it.slot * a.wide + c) * kSide + side;
 #pragma unroll
     for (int q = 0; q < 16; ++q) o[q * kSide] = v[q];
   } else if (i < a.i_size) {
@@ -346,8 +521,7 @@ __device__ __forceinline__ void put16(const ExpertArgs& a, const Item& it, uint3
 // whole stretches of a result's row as they come. The two warps of a quarter of the i alternate
 // over the columns, sixteen at a time.
 template <int FORM>
-__device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const Item& it,
-                                           uint32_t index) {
+__device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const Item& it) {
   const uint32_t warp = threadIdx.x >> 5, quarter = warp & 3u, half = warp >> 2;
   const uint32_t side = 128 * w.rank + 32 * quarter + lane_id();
   const uint32_t src = w.tmem + (quarter << 21);
@@ -361,7 +535,7 @@ __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const
     }
     for (uint32_t b = it.s0; b < it.s1; b += kRun) {
       const uint32_t acc = w.acc & 1u;
-      if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
+      if (!mbar_wait_warp_inline(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
       tmem_fence_after();
 #pragma unroll
       for (uint32_t k = 0; k < 8; ++k) {
@@ -382,17 +556,17 @@ __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)
       if (32 * k + 16 * half < it.count)
-        put16<FORM>(a, it, index, side, 32 * k + 16 * half, sum[k]);
+        put16<FORM>(a, it, side, 32 * k + 16 * half, sum[k]);
   } else {
     const uint32_t acc = w.acc & 1u;
-    if (!mbar_wait_warp(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
+    if (!mbar_wait_warp_inline(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
     tmem_fence_after();
 #pragma unroll 1
     for (uint32_t c = 16 * half; c < it.count; c += 32) {
       float v[16];
       tmem_load16(src + acc * kSide + c, v);
       tmem_load_wait(v);
-      put16<FORM>(a, it, index, side, c, v);
+      put16<FORM>(a, it, side, c, v);
     }
     tmem_fence_before();
     __syncwarp();
@@ -406,8 +580,8 @@ template <int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
 experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ ExpertArgs a) {
   extern __shared__ uint8_t raw[];
-  __shared__ alignas(8) uint64_t bars[2 * kStages + 5];
-  __shared__ uint32_t tmem_slot, partner[2];
+  __shared__ alignas(8) uint64_t bars[3 * kStages + 5 + 2 * kFeed];
+  __shared__ uint32_t tmem_slot, partner[2], fed[kFeed];
   __shared__ Waits waits;
   __shared__ Table table;
   griddep_wait();
@@ -418,16 +592,18 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   w.empty = w.full + 8 * kStages;
   w.acc_full = w.empty + 8 * kStages;
   w.acc_empty = w.acc_full + 16;
-  const uint32_t finished = w.acc_empty + 16;
+  w.tail = w.acc_empty + 16;
+  w.feed_full = w.tail + 8 * kStages;
+  const uint32_t fed_empty = w.feed_full + 8 * kFeed, finished = fed_empty + 8 * kFeed;
+  w.fed = smem_addr(fed);
   w.rank = cluster_rank();
   w.pair = blockIdx.x / 2;
   w.pairs = gridDim.x / 2;
   w.waits = &waits;
-  __shared__ alignas(8) uint64_t tail_bar;
-  w.tail = smem_addr(&tail_bar);
   w.lead_full = cluster_addr(w.full, 0);
   w.lead_acc_empty = cluster_addr(w.acc_empty, 0);
   w.own_tail = cluster_addr(w.tail, w.rank);
+  w.lead_fed_empty = cluster_addr(fed_empty, 0);
   w.leader = elect_one();
   if (threadIdx.x < 2) tma_prefetch_map(threadIdx.x ? &m.q : &m.p);
   if (threadIdx.x == 0) {
@@ -437,41 +613,67 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
     for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(w.full + 8 * s, 2);
       mbar_init(w.empty + 8 * s, 1);
+      mbar_init(w.tail + 8 * s, 1);
     }
     for (uint32_t s = 0; s < 2; ++s) {
       mbar_init(w.acc_full + 8 * s, 1);
       mbar_init(w.acc_empty + 8 * s, 2 * kWriters);
     }
     mbar_init(finished, 1);
-    mbar_init(w.tail, 1);
+    for (uint32_t s = 0; s < kFeed; ++s) {
+      mbar_init(w.feed_full + 8 * s, 1);
+      // both blocks' writers and clearers, one issuer and one loader
+      mbar_init(fed_empty + 8 * s, 2 * (kWriters + (FORM == kWeight ? 1 : 0)) + 2);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWriters) tmem_alloc<2>(smem_addr(&tmem_slot), 2 * kSide);
   if (warp == 1) {
-    const bool bad = make_table<FORM>(a, table, w.pairs);
+    const bool bad = make_runs(a, table);
     if (bad && blockIdx.x == 0 && w.leader) set_status(a.status, SPARCML_ERR_BAD_STREAM);
   }
+  __syncthreads();
+  make_items<FORM>(a, table, w.pairs);
   tmem_fence_before();
   __syncthreads();
   cluster_sync();
   tmem_fence_after();
   w.tmem = tmem_slot;
+  w.items = table.items;
 
-  const uint32_t items = table.first[a.experts];
-  if (warp == kWriters) {
-    for (uint32_t x = w.pair; x < items; x += w.pairs)
+  uint32_t x = w.pair;
+  if (warp < kWriters) {
+    for (; x < w.items; x = next_item(w))
+      if (!write_item<FORM>(w, a, item_of<FORM>(a, table, x))) break;
+  } else if (warp == kWriters && w.rank == 0) {
+    const bool draws = w.items > w.pairs;
+    while (x < w.items) {
+      uint32_t drawn = draws ? draw_item(w, a) : 0;
+      const bool loaded = load_item<FORM>(w, m, a, item_of<FORM>(a, table, x));
+      x = draws ? drawn_item(w, a, drawn) : kNone;
+      if (!draws || (loaded && feed_item(w, fed_empty, x) == x)) continue;
+      while (x != kNone) {  // given up: the counter is left as the next kernel needs it all the same
+        drawn = draw_item(w, a);
+        x = drawn_item(w, a, drawn);
+      }
+    }
+  } else if (warp == kWriters) {
+    for (; x < w.items; x = next_item<true>(w))
       if (!load_item<FORM>(w, m, a, item_of<FORM>(a, table, x))) break;
   } else if (warp == kWriters + 1) {
     // An injected fault: the first pair withholds its products.
     const bool withhold = w.pair == 0 && waits.limit_us == kInjectWaitUs;
     if (w.rank == 0 && !withhold)
-      for (uint32_t x = w.pair; x < items; x += w.pairs) {
-        const Item it = item_of<FORM>(a, table, x);
-        if (!issue_item<FORM>(w, a, it)) break;
-      }
-  } else {
-    for (uint32_t x = w.pair; x < items; x += w.pairs)
-      if (!write_item<FORM>(w, a, item_of<FORM>(a, table, x), x)) break;
+      for (; x < w.items; x = next_item(w))
+        if (!issue_item<FORM>(w, a, item_of<FORM>(a, table, x))) break;
+  } else if (FORM == kWeight) {
+    if (warp == kWriters + 2)
+      for (; x < w.items; x = next_item(w))
+        if (!clear_item(w, item_of<FORM>(a, table, x))) break;
+  } else if (FORM == kInput && a.restore.codes) {
+    const uint32_t thread = 64 * blockIdx.x + (threadIdx.x - 32 * (kWriters + 2));
+    if (a.bf16) restore_rows<__nv_bfloat16>(a.restore, thread, 64 * gridDim.x);
+    else restore_rows<__half>(a.restore, thread, 64 * gridDim.x);
   }
   tmem_fence_before();
   __syncthreads();  // now it is settled whether this block gave up
@@ -486,13 +688,21 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
     // Nothing may still be in flight when the shared and tensor memory go.
     if (warp == kWriters && w.leader) {
       const bool apart = partner[1] != 2 * w.stage + w.phase;
-      if (w.rank == 0 || apart) land_operands(w.full, kStages, w.stage, w.phase, apart);
+      // Both blocks' loads report to the first one, in one phase of a stage; where the two stopped
+      // at different stages some phases never complete, and the loads get their time instead.
+      Waits alone = {0, kLandUs};
+      const uint64_t end = global_ns() + 1000ull * kLandUs;
+      if (apart)
+        while (global_ns() < end) __nanosleep(1000);
+      else if (w.rank == 0)
+        for (uint32_t s = 0; s < kStages; ++s)
+          mbar_wait_inline(w.full + 8 * s, s < w.stage ? w.phase : w.phase ^ 1u, &alone);
     }
     if (warp == kWriters + 1 && w.leader) {
       // arrives, in both blocks of a pair, once all products have completed
       Waits alone = {0, kWaitUs};
       if (w.rank == 0) mma_commit<2>(finished);
-      mbar_wait(finished, 0, &alone);
+      mbar_wait_inline(finished, 0, &alone);
     }
     __syncwarp();
     if (threadIdx.x == 0) set_status(a.status, SPARCML_ERR_TIMEOUT);
@@ -510,28 +720,26 @@ __global__ void __launch_bounds__(256) join_parts_kernel(const __grid_constant__
                                                          uint32_t pairs) {
   __shared__ Table table;
   griddep_wait();
-  if (threadIdx.x < 32) make_table<FORM>(a, table, pairs);
+  if (threadIdx.x < 32) make_runs(a, table);
   __syncthreads();
-  const uint32_t groups = a.wide / 4;
-  const uint32_t each = ceil_of(a.i_size, kSide) * ceil_of(a.j_size, kSide);  // dW: tiles of one
-  const uint32_t tiles = FORM == kWeight ? a.experts * each : table.first[a.experts] / a.splits;
+  make_items<FORM>(a, table, pairs);
+  __syncthreads();
+  const uint32_t groups = a.wide / 4, splits = table.splits;
+  if (splits == 1) return;
+  const uint32_t tiles = FORM == kWeight ? table.rest : table.items / splits;
+  const uint32_t from = FORM == kWeight ? table.whole : 0;
+  // a tile's parts: neighbours, or (dW) a round apart
+  const uint32_t on = FORM == kWeight ? table.rest : 1, step = FORM == kWeight ? 1 : splits;
   for (uint32_t x = blockIdx.x; x < tiles * groups; x += gridDim.x) {
-    const uint32_t tile = x / groups;
-    uint32_t index = tile * a.splits;
-    if (FORM == kWeight) {
-      const uint32_t e = tile / each;
-      const uint32_t splits = (table.first[e + 1] - table.first[e]) / each;
-      index = table.first[e] + (tile - e * each) * splits;
-    }
-    const Item it = item_of<FORM>(a, table, index);
+    const uint32_t tile = x / groups, slot = tile * step;
+    const Item it = item_of<FORM>(a, table, from + slot);
     const uint32_t j = 4 * (x - tile * groups) + threadIdx.x / 64, i = 4 * (threadIdx.x % 64);
-    if (it.splits == 1 || j >= it.count || it.i0 + i >= a.i_size) continue;
+    if (j >= it.count || it.i0 + i >= a.i_size) continue;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* p =
-        reinterpret_cast<const float4*>(a.part + ((uint64_t)index * a.wide + j) * kSide + i);
 #pragma unroll 8
-    for (uint32_t s = 0; s < it.splits; ++s, p += (uint64_t)a.wide * kSide / 4) {
-      const float4 q = __ldcg(p);
+    for (uint32_t s = 0; s < splits; ++s) {
+      const float4 q = __ldcg(reinterpret_cast<const float4*>(
+          a.part + ((uint64_t)(slot + s * on) * a.wide + j) * kSide + i));
       v.x += q.x;
       v.y += q.y;
       v.z += q.z;
@@ -583,9 +791,9 @@ struct Sizes {
   bool ok() const {
     return rows <= 0x7fffffffull && experts >= 1 && experts <= kMostExperts && n >= 1 &&
            n <= (1u << 24) && k >= 1 && k <= (1u << 24) &&
-           // tiles are counted in 31 bits (what has more does not fit the memory)
+           // what is counted in 32 bits on the device (more would not fit the memory, or take minutes)
            ceil_div(std::max(n, k), kSide) * (rows / kSide + experts) < (1ull << 31) &&
-           experts * ceil_div(n, kSide) * ceil_div(k, kSide) < (1ull << 31);
+           (rows / 64 + experts) * ceil_div(n, kSide) * ceil_div(k, kSide) < (1ull << 31);
   }
   // Parts of the summed axis for forward and dx: as many as the pairs of SMs leave room for where
   // even the most tiles that the rows can make are at most half as many.
@@ -596,12 +804,12 @@ struct Sizes {
         1, std::min<uint64_t>(kPairs / most, ceil_div(s, 64) / kLeastBlocks));
   }
   uint64_t weight_tiles() const { return experts * ceil_div(n, kSide) * ceil_div(k, kSide); }
-  bool weight_splits() const { return weight_tiles() < kPairs && rows > 64 * kLeastBlocks; }
+  bool weight_splits() const { return rows > 64 * kJoinBlocks; }
   uint32_t wide() const { return (uint32_t)std::min<uint64_t>(kSide, align_up(rows, 16)); }
   size_t part_bytes() const {
     size_t r = 0;
     if (splits(n, k) > 1 || splits(k, n) > 1) r = (size_t)kPairs * wide() * kSide * 4;
-    if (weight_splits()) r = std::max(r, (size_t)(kPairs + weight_tiles()) * kSide * kSide * 4);
+    if (weight_splits()) r = std::max(r, (size_t)2 * kPairs * kSide * kSide * 4);
     return align_up(r, 256);
   }
 };
@@ -738,10 +946,17 @@ struct Call {
   cudaStream_t stream;
 };
 
-// The product of operands that TMA takes.
+struct Stored {  // x in 8 bits
+  const int8_t* codes;
+  int64_t codes_stride;
+  const uint8_t* exponents;
+  int64_t exponents_stride;
+};
+
+// The product of operands that TMA takes; dx with a side job, or none.
 template <int FORM>
 int run(const Call& c, Operand p, Operand q, void* out, int32_t out_type, int64_t out_batch,
-        int64_t out_stride, int32_t accumulate) {
+        int64_t out_stride, int32_t accumulate, const Restore& side = {}) {
   const Sizes& z = c.z;
   uint8_t* w = static_cast<uint8_t*>(c.ws);
   ExpertArgs a = {};
@@ -764,6 +979,8 @@ int run(const Call& c, Operand p, Operand q, void* out, int32_t out_type, int64_
   a.part = reinterpret_cast<float*>(w + 256);
   a.status = reinterpret_cast<int32_t*>(w);
   a.inject = reinterpret_cast<const uint32_t*>(w + kInjectOffset);
+  a.handed_out = reinterpret_cast<uint32_t*>(w + kItemsOffset);
+  a.restore = side;
   ExpertMaps m;
   if (z.rows == 0) p = q = Operand{w, 64, 64, 1, 1, 64};  // no operand is read
   if (!map_of(&m.p, p, a.bf16, FORM == kForward ? 128 : 64) ||
@@ -772,9 +989,9 @@ int run(const Call& c, Operand p, Operand q, void* out, int32_t out_type, int64_
   const uint64_t tiles = FORM == kWeight ? z.weight_tiles()
                                          : ceil_div(a.i_size, kSide) *
                                                (std::min(z.experts, z.rows) + z.rows / kSide);
-  const uint64_t join = a.may_split || a.splits > 1 ? tiles * (a.wide / 4) : 0;
+  const uint64_t joined = a.may_split ? kPairs : a.splits > 1 ? tiles : 0;
   const uint64_t most = a.may_split ? kPairs : tiles * a.splits;
-  return launch_experts<FORM>(m, a, std::max<uint64_t>(1, most), join, c.stream);
+  return launch_experts<FORM>(m, a, std::max<uint64_t>(1, most), joined * (a.wide / 4), c.stream);
 }
 
 bool half_type(int32_t type) { return type == SPARCML_BF16 || type == SPARCML_F16; }
@@ -805,13 +1022,6 @@ bool matrices_ok(const float* p, const Sizes& z, int64_t batch, int64_t stride) 
          (batch >= k && (n == 1 || stride >= (e - 1) * batch + k));
 }
 
-struct Stored {  // x in 8 bits
-  const int8_t* codes;
-  int64_t codes_stride;
-  const uint8_t* exponents;
-  int64_t exponents_stride;
-};
-
 // dx and dW, each where it is wanted; x as it is, or in 8 bits.
 int backward(const Call& c, Operand dy, Operand x, const Stored* stored, Operand w, void* dx,
              int64_t dx_stride, float* dweight, int64_t dw_batch, int64_t dw_stride,
@@ -824,25 +1034,30 @@ int backward(const Call& c, Operand dy, Operand x, const Stored* stored, Operand
     return SPARCML_ERR_INVALID_ARG;
   const bool rows = z.rows > 0;
   const bool input = dx && rows, weights = dweight != nullptr;
+  const bool restored = stored && weights && rows;
   Operand plain = x;
-  if (stored) plain = {nullptr, 0, (int64_t)align_up(z.k, 8), 1, z.rows, z.k};
+  if (restored) plain = {nullptr, 0, (int64_t)align_up(z.k, 8), 1, z.rows, z.k};
   const Settle copies{{input || weights ? &dy : nullptr, input ? &w : nullptr,
                        weights && !stored ? &plain : nullptr}};
-  const size_t restored = stored && weights ? plain.copy_bytes() : 0;
-  const size_t parts = z.part_bytes(), copied = copies.bytes();
-  if (c.ws_bytes < 256 + parts + restored + copied) return SPARCML_ERR_WORKSPACE;
+  const size_t parts = z.part_bytes(), more = restored ? plain.copy_bytes() : 0;
+  if (c.ws_bytes < 256 + parts + more + copies.bytes()) return SPARCML_ERR_WORKSPACE;
   uint8_t* room = static_cast<uint8_t*>(c.ws) + 256 + parts;
-  if (restored) {
+  Restore side = {};
+  if (restored) {  // beside dx, or before dW
     plain.p = room;
-    r = sparcml_restore8(stored->codes, stored->codes_stride, stored->exponents,
-                         stored->exponents_stride, z.rows, z.k, room, c.type, plain.stride,
-                         c.stream);
+    if (input)
+      side = {stored->codes, stored->codes_stride, stored->exponents, stored->exponents_stride,
+              room, plain.pitch(), (uint32_t)z.rows, (uint32_t)z.k};
+    else
+      r = sparcml_restore8(stored->codes, stored->codes_stride, stored->exponents,
+                           stored->exponents_stride, z.rows, z.k, room, c.type, plain.stride,
+                           c.stream);
     if (r != SPARCML_OK) return r;
   }
-  copies.run(room + restored, c.stream);
+  copies.run(room + more, c.stream);
   if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
   if (input) {
-    r = run<kInput>(c, w, dy, dx, c.type, 0, dx_stride, 0);
+    r = run<kInput>(c, w, dy, dx, c.type, 0, dx_stride, 0, side);
     if (r != SPARCML_OK) return r;
   }
   return weights ? run<kWeight>(c, plain, dy, dweight, SPARCML_F32, dw_batch, dw_stride, accumulate)
@@ -862,8 +1077,8 @@ extern "C" size_t sparcml_expert_linear_workspace_size(uint64_t rows, uint32_t e
       w{nullptr, 0, 0, experts, n, k};
   const bool odd_n = !aligned || n % 8 != 0, odd_k = !aligned || k % 8 != 0;
   // x also where it is kept in 8 bits
-  return 256 + z.part_bytes() + x.copy_bytes() + (odd_n ? dy.copy_bytes() : 0) +
-         (odd_k ? w.copy_bytes() : 0);
+  return 256 + z.part_bytes() + x.copy_bytes() + (odd_k ? w.copy_bytes() : 0) +
+         (odd_n ? dy.copy_bytes() : 0);
 }
 
 extern "C" int sparcml_expert_linear(const void* x, int64_t x_stride, const void* weight,
@@ -914,7 +1129,10 @@ extern "C" int sparcml_expert_linear_backward8(
   const Call c{{rows, experts, n, k}, type, offsets, ws, ws_bytes,
                static_cast<cudaStream_t>(stream)};
   const Stored x{codes, codes_stride, exponents, exponents_stride};
-  if (dweight && rows && (!codes || !exponents)) return SPARCML_ERR_INVALID_ARG;
+  if (dweight && rows &&
+      (!codes || !exponents || !aligned_to(codes, 16) || codes_stride % 16 != 0 ||
+       codes_stride < (int64_t)align_up(k, 16) || exponents_stride < (int64_t)ceil_div(k, kGroup)))
+    return SPARCML_ERR_INVALID_ARG;
   return backward(c, {dy, 0, dy_stride, 1, rows, n}, {}, &x,
                   Operand::matrices(weight, weight_batch_stride, weight_stride, c.z), dx, dx_stride,
                   dweight, dweight_batch_stride, dweight_stride, accumulate);

@@ -51,6 +51,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void store_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+// A word to a block of the cluster, which counts 4 bytes towards that block's barrier as it lands.
+__device__ __forceinline__ void store_cluster_async(uint32_t addr, uint32_t v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr),
+      "r"(v), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -74,6 +81,19 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
       "mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// The same, acquiring what either block of a pair released.
+__device__ __forceinline__ bool mbar_try_wait_pair(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 q, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(ok)
       : "r"(bar), "r"(parity)
@@ -110,6 +130,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Waits* 
   for (uint32_t i = 0; i < 64; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait_long(bar, parity, waits);
+}
+
+// The same without a call, for kernels whose registers leave no room for one. PAIR: acquires for both blocks of a pair.
+template <bool PAIR = false>
+__device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, Waits* waits) {
+  // the clock is slow to read: every 64 tries will do
+  for (uint64_t end = 0;;) {
+    for (uint32_t i = 0; i < 64; ++i)
+      if (PAIR ? mbar_try_wait_pair(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (waits->gave_up != 0) return false;
+    const uint64_t now = global_ns();
+    if (end == 0) end = now + 1000ull * waits->limit_us;
+    if (now > end) {
+      waits->gave_up = 1;
+      return false;
+    }
+  }
+}
+template <bool PAIR = false>
+__device__ __forceinline__ bool mbar_wait_warp_inline(uint32_t bar, uint32_t parity, Waits* waits) {
+  return __all_sync(0xffffffffu, mbar_wait_inline<PAIR>(bar, parity, waits));
 }
 
 // The same for a whole warp: true only if every lane's wait ended well.
