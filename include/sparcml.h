@@ -29,9 +29,10 @@
  *     the calls are non-blocking in the sense of §7 (MPI-3 style
  *     non-blocking collectives). Only sparcml_get_status synchronises.
  *   - Workspace header. The first 256 bytes of every workspace hold the
- *     device status word (bytes 0..3), a ticket word (bytes 16..19) and the
+ *     device status word (bytes 0..3), a ticket word (bytes 16..19), the
  *     fault-injection word (bytes 32..35, see
- *     sparcml_set_fault_injection). Zero the first 64 bytes when a
+ *     sparcml_set_fault_injection) and a count of work handed out (bytes
+ *     48..51). Zero the first 64 bytes when a
  *     workspace is created; the library keeps them from then on.
  *   - Errors. A return value other than SPARCML_OK means nothing was
  *     enqueued (bad argument, workspace too small, capacity too small) or
@@ -88,7 +89,8 @@ uint64_t sparcml_launch_count(void);
  *     access stays in bounds and the call always completes. In later
  *     orthogonalisations and weight steps the first block withholds a
  *     product, and the waits for it give up after 2 to 8 milliseconds
- *     instead of 2 to 8 seconds, with the same consequences.
+ *     instead of 2 to 8 seconds, with the same consequences; likewise in
+ *     experts' linear layers and their gradients.
  *   mode 0: clears it (later calls are normal again).
  * The word stays as written across calls. A workspace whose first 64 bytes
  * were zeroed when it was created has no fault armed.

@@ -92,8 +92,8 @@ INJECT_WITHHOLD_FIRST = 1
 def set_fault_injection(ws: torch.Tensor, mode: int, stream=None):
     """Arm (mode INJECT_WITHHOLD_FIRST) or clear (0) the workspace's fault
     injection: later reduce / SSAR calls with ws see their look-back waits run
-    out, and orthogonalisations and weight steps those for a product, and record
-    SPARCML_ERR_TIMEOUT (include/sparcml.h)."""
+    out, and orthogonalisations, weight steps and experts' linear layers those for a
+    product, and record SPARCML_ERR_TIMEOUT (include/sparcml.h)."""
     _check("sparcml_set_fault_injection",
            _lib.load().sparcml_set_fault_injection(ws.data_ptr(), int(mode), _stream(stream)))
 
@@ -795,15 +795,14 @@ def muon_step(weight, grad, momentum, lr: float, mu: float = 0.95, nesterov: boo
 GROUP8 = 128  # columns that share an exponent
 
 
-@dataclass(frozen=True)
 class Checkpoint8:
     """An activation in 8 bits: ``codes`` int8 [..., dim rounded up to 16] and ``exponents``
     uint8 [..., ceil(dim / 128)], both contiguous; an element is code * 2^(exponent - 127), and
     NaN where the exponent is 255. ``dtype`` is the activation's own."""
-    codes: torch.Tensor
-    exponents: torch.Tensor
-    dim: int
-    dtype: torch.dtype
+    __slots__ = ("codes", "exponents", "dim", "dtype")
+
+    def __init__(self, codes: torch.Tensor, exponents: torch.Tensor, dim: int, dtype: torch.dtype):
+        self.codes, self.exponents, self.dim, self.dtype = codes, exponents, dim, dtype
 
     @property
     def shape(self):
@@ -812,6 +811,9 @@ class Checkpoint8:
     @property
     def device(self):
         return self.codes.device
+
+    def __repr__(self):
+        return f"Checkpoint8({list(self.shape)}, {self.dtype}, {self.device})"
 
 
 def _stored(c, name: str, dtype=None):
@@ -845,14 +847,15 @@ def checkpoint8(x, out=None, stream=None):
     code = _typed(x, "x")
     rows, dim, xs = _rows(x, "x")
     if out is None:
-        lead = x.shape[:-1]
-        out = Checkpoint8(
-            torch.empty((*lead, (dim + 15) // 16 * 16), dtype=torch.int8, device=x.device),
-            torch.empty((*lead, (dim + GROUP8 - 1) // GROUP8), dtype=torch.uint8,
-                        device=x.device), dim, x.dtype)
-    elif out.shape != x.shape:
-        raise ValueError("out and x shapes differ")
-    p, ps, e, es, _, _ = _stored(out, "out", x.dtype)
+        ps, es, lead = (dim + 15) // 16 * 16, (dim + GROUP8 - 1) // GROUP8, x.shape[:-1]
+        codes = x.new_empty(*lead, ps, dtype=torch.int8)
+        exponents = x.new_empty(*lead, es, dtype=torch.uint8)
+        out, p, e = Checkpoint8(codes, exponents, dim, x.dtype), codes.data_ptr(), \
+            exponents.data_ptr()
+    else:
+        if out.shape != x.shape:
+            raise ValueError("out and x shapes differ")
+        p, ps, e, es, _, _ = _stored(out, "out", x.dtype)
     r = (_lib._lib or _lib.load()).sparcml_checkpoint8(x.data_ptr(), code, xs, rows, dim, p, ps, e,
                                                        es, _raw_stream(x))
     if r:
@@ -870,12 +873,13 @@ def restore8(x, out=None, dtype=None, stream=None):
             return restore8(x, out, dtype)
     p, ps, e, es, rows, dim = _stored(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype or x.dtype, device=x.device)
+        out, ys = x.codes.new_empty(*x.shape, dtype=dtype or x.dtype), dim
     elif out.shape != x.shape:
         raise ValueError("out and x shapes differ")
-    code = _typed(out, "out")
-    r = (_lib._lib or _lib.load()).sparcml_restore8(p, ps, e, es, rows, dim, out.data_ptr(), code,
-                                                    _rows(out, "out")[2], _raw_stream(x.codes))
+    else:
+        ys = _rows(out, "out")[2]
+    r = (_lib._lib or _lib.load()).sparcml_restore8(p, ps, e, es, rows, dim, out.data_ptr(),
+                                                    _typed(out, "out"), ys, _raw_stream(x.codes))
     if r:
         _check("sparcml_restore8", r)
     return out
@@ -1001,7 +1005,7 @@ def expert_linear(x, weight, offsets=None, out=None, ws=None, stream=None):
     op = _offsets(offsets, weight)
     rows = x.shape[0]
     if out is None:
-        out = torch.empty((rows, n), dtype=x.dtype, device=x.device)
+        out = x.new_empty(rows, n)
     _half(out, "out", x)
     yp, ys = _row_matrix(out, "out", rows, n)
     wp, wn = _fit((rows, experts, n, k), ws, x.device, x, weight)
@@ -1048,13 +1052,13 @@ def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
     xp, xs = None, k
     if need_dx:
         if dx is None:
-            dx = torch.empty((rows, k), dtype=dy.dtype, device=dy.device)
+            dx = dy.new_empty(rows, k)
         _half(dx, "dx", dy)
         xp, xs = _row_matrix(dx, "dx", rows, k)
     gp, gb, gs = None, 0, k
     if need_dweight:
         if dweight is None:
-            dweight = torch.empty(weight.shape, dtype=torch.float32, device=dy.device)
+            dweight = dy.new_empty(*weight.shape, dtype=torch.float32)
         if not dweight.is_cuda or dweight.dtype != torch.float32 or dweight.shape != weight.shape:
             raise TypeError(f"dweight must be a float32 CUDA tensor of {list(weight.shape)}")
         gb, gs = _experts(dweight, "dweight")[:2]
@@ -1074,13 +1078,35 @@ def _heads(t, name: str, like=None, shape=None):
     if t is None:
         return None, 0, 0, 0
     _typed(t, name, like)
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, dim], got {t.dim()} dims")
-    if shape is not None and t.shape != shape:
+    size, stride = t.shape, t.stride()
+    if len(size) != 3:
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {len(size)} dims")
+    if shape is not None and size != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if stride[2] != 1 and size[2] > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t.data_ptr(), t.stride(0), t.stride(1), t.shape[1]
+    return t.data_ptr(), stride[0], stride[1], size[1]
+
+
+def _heads_out(t, name: str, x):
+    """(output, pointer, token stride, head stride) for an input x, or for none."""
+    if x is None:
+        return None, None, 0, 0
+    if t is None:
+        tokens, heads, dim = x.shape
+        t = x.new_empty(tokens, heads, dim)
+        return t, t.data_ptr(), heads * dim, dim
+    return (t, *_heads(t, name, x, x.shape)[:3])
+
+
+def _sum_out(t, name: str, x):
+    """(float32 vector, pointer) for a weight's gradient, or for none."""
+    if x is None:
+        return None, None
+    if t is None:
+        t = x.new_empty(x.shape[2], dtype=torch.float32)
+        return t, t.data_ptr()
+    return t, _stat(t, x.shape[2], name)
 
 
 def _head_args(q, k, positions, freqs, q_weight, k_weight):
@@ -1128,18 +1154,14 @@ def head_norm_rotary(q, k, positions, freqs, q_weight=None, k_weight=None, eps: 
     qa = _heads(q, "q")
     ka = _heads(k, "k", x)
     tokens, dim, turn, weights = _head_args(q, k, positions, freqs, q_weight, k_weight)
-    if q_out is None and q is not None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    qo = _heads(q_out if q is not None else None, "q_out", x, None if q is None else q.shape)
-    ko = _heads(k_out if k is not None else None, "k_out", x, None if k is None else k.shape)
+    q_out, *qo = _heads_out(q_out, "q_out", q)
+    k_out, *ko = _heads_out(k_out, "k_out", k)
     r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary(
-        *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, int(interleaved), *weights, eps, *qo[:3],
-        *ko[:3], _raw_stream(x))
+        *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, interleaved, *weights, eps, *qo,
+        *ko, _raw_stream(x))
     if r:
         _check("sparcml_head_norm_rotary", r)
-    return q_out if q is not None else None, k_out if k is not None else None
+    return q_out, k_out
 
 
 def head_norm_rotary_backward_workspace_size(tokens: int, q_heads: int, k_heads: int,
@@ -1173,33 +1195,20 @@ def head_norm_rotary_backward(dq, dk, q, k, positions, freqs, q_weight=None, k_w
         raise ValueError("q goes with dq, and k with dk")
     gq = _heads(dq, "dq", x, None if q is None else q.shape)
     gk = _heads(dk, "dk", x, None if k is None else k.shape)
-    if dq_out is None and q is not None:
-        dq_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if dk_out is None and k is not None:
-        dk_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    qo = _heads(dq_out if q is not None else None, "dq_out", x, None if q is None else q.shape)
-    ko = _heads(dk_out if k is not None else None, "dk_out", x, None if k is None else k.shape)
+    dq_out, *qo = _heads_out(dq_out, "dq_out", q)
+    dk_out, *ko = _heads_out(dk_out, "dk_out", k)
     if accumulate and ((q is not None and dq_weight is None) or
                        (k is not None and dk_weight is None)):
         raise ValueError("accumulate needs dq_weight and dk_weight to add to")
-    if q is None:
-        dq_weight = None
-    elif dq_weight is None:
-        dq_weight = torch.empty(dim, dtype=torch.float32, device=x.device)
-    if k is None:
-        dk_weight = None
-    elif dk_weight is None:
-        dk_weight = torch.empty(dim, dtype=torch.float32, device=x.device)
-    sums = [None if t is None else _stat(t, dim, n)
-            for t, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight"))]
+    dq_weight, qs = _sum_out(dq_weight, "dq_weight", q)
+    dk_weight, ks = _sum_out(dk_weight, "dk_weight", k)
     if ws is None:
         ws = workspace(head_norm_rotary_backward_workspace_size(tokens, qa[3], ka[3], dim),
                        x.device)
     wp, wn = _space(ws)
     r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary_backward(
-        *gq[:3], *gk[:3], *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, int(interleaved), *weights,
-        eps, *qo[:3], *ko[:3], *sums, int(accumulate), wp, wn, _raw_stream(x))
+        *gq[:3], *gk[:3], *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, interleaved, *weights, eps,
+        *qo, *ko, qs, ks, accumulate, wp, wn, _raw_stream(x))
     if r:
         _check("sparcml_head_norm_rotary_backward", r)
-    return (dq_out if q is not None else None, dk_out if k is not None else None, dq_weight,
-            dk_weight)
+    return dq_out, dk_out, dq_weight, dk_weight

@@ -323,10 +323,11 @@ __device__ __forceinline__ void write_sums(const Norm8Args& a, const Group& g, u
 // copies ahead and reads back its own pieces alone, so that the ring needs no barrier.
 //
 // 16384 x 4096 bf16 takes 79 us, 4.2 TB/s: half of the issue slots are filled by the 16 warps of an
-// SM that 119 registers allow, and a row's reduction is what they wait for. Two rows at a time, read
-// from the ring a second time after their sums (80 registers, 24 warps, 63 % of the slots, but 1.34
-// times the instructions), took 86; arithmetic single in place of packed, or one row ahead in
-// registers in place of three in the ring, 79 as well.
+// SM that 119 registers allow. Without its arithmetic and its barrier the kernel takes 57; the
+// reduction over the row is 10 of the rest, the weights' sums 10, making floats of codes 10. Not
+// faster: what was read kept in place of the floats made of it (80 registers, 24 warps, but 1.5
+// times the instructions) 81 us; two rows at a time, read from the ring again after their sums, 86;
+// arithmetic single in place of packed, or one row ahead in registers, 79.
 constexpr int kRing = 4;
 
 template <typename T, int MAXT, int MINB>
