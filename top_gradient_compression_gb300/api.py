@@ -982,6 +982,7 @@ def _fit(size, ws, device, *operands):
     """The workspace, or a new one for operands of this alignment."""
     if ws is None:
         aligned = all(t.data_ptr() % 16 == 0 and t.stride(-2) >= t.shape[-1] and
+                      (t.dim() == 2 or not 0 < t.stride(0) < t.shape[-1]) and
                       all(s % 8 == 0 for s in t.stride()[:-1]) for t in operands)
         ws = workspace(expert_linear_workspace_size(*size, aligned), device)
     return _space(ws)

@@ -1034,10 +1034,11 @@ int backward(const Call& c, Operand dy, Operand x, const Stored* stored, Operand
     return SPARCML_ERR_INVALID_ARG;
   const bool rows = z.rows > 0;
   const bool input = dx && rows, weights = dweight != nullptr;
+  if (!input && !weights) return SPARCML_OK;
   const bool restored = stored && weights && rows;
   Operand plain = x;
   if (restored) plain = {nullptr, 0, (int64_t)align_up(z.k, 8), 1, z.rows, z.k};
-  const Settle copies{{input || weights ? &dy : nullptr, input ? &w : nullptr,
+  const Settle copies{{&dy, input ? &w : nullptr,
                        weights && !stored ? &plain : nullptr}};
   const size_t parts = z.part_bytes(), more = restored ? plain.copy_bytes() : 0;
   if (c.ws_bytes < 256 + parts + more + copies.bytes()) return SPARCML_ERR_WORKSPACE;
