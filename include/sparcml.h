@@ -670,16 +670,38 @@ int sparcml_expert_linear_backward8(const void* dy, int64_t dy_stride, const int
  *             angle is off by at most 2^-26 of a turn and 2^-64 |p|.
  *   freqs     device fp32 [turned / 2], radians per position, finite.
  *   q_weight, k_weight  [dim] of type weight_type, each may be NULL (ones).
- *   tokens 0 .. 2^31 - 1, dim 1 .. 512, turned even, 0 .. dim, heads 0 .. 65535. */
-int sparcml_head_norm_rotary(const void* q, int64_t q_token_stride, int64_t q_head_stride,
-                             uint32_t q_heads, const void* k, int64_t k_token_stride,
-                             int64_t k_head_stride, uint32_t k_heads, int32_t type,
-                             uint64_t tokens, uint32_t dim, const void* positions,
-                             int32_t positions_int64, const float* freqs, uint32_t turned,
-                             int32_t interleaved, const void* q_weight, const void* k_weight,
-                             int32_t weight_type, float eps, void* q_out,
-                             int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
-                             int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream);
+ *   tokens 0 .. 2^31 - 1, dim 1 .. 512, turned even, 0 .. dim, heads 0 .. 65535.
+ * The struct `args` is HOST memory, read during the call only. */
+struct sparcml_head_args { /* of both passes; strides in elements */
+  const void* q;
+  int64_t q_token_stride, q_head_stride, q_heads;
+  const void* k;
+  int64_t k_token_stride, k_head_stride, k_heads;
+  int64_t type, tokens, dim;
+  const void* positions;
+  int64_t positions_int64; /* else int32 */
+  const float* freqs;
+  int64_t turned, interleaved;
+  const void* q_weight;
+  const void* k_weight;
+  int64_t weight_type;
+  double eps;
+  void* q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+  void* k_out;
+  int64_t k_out_token_stride, k_out_head_stride;
+  /* the rest is read by the backward pass alone */
+  const void* dq;
+  int64_t dq_token_stride, dq_head_stride;
+  const void* dk;
+  int64_t dk_token_stride, dk_head_stride;
+  float* q_dweight;
+  float* k_dweight;
+  int64_t accumulate;
+  void* ws;
+  int64_t ws_bytes;
+};
+int sparcml_head_norm_rotary(const struct sparcml_head_args* args, void* stream);
 
 /* Its gradients from dq and dk, those of its results, and its inputs q and k:
  * q_out and k_out get the inputs' gradients (each may be dq and dk themselves),
@@ -688,16 +710,7 @@ int sparcml_head_norm_rotary(const void* q, int64_t q_token_stride, int64_t q_he
  *   ws        >= the workspace size for it, 256-byte aligned. */
 size_t sparcml_head_norm_rotary_backward_workspace_size(uint64_t tokens, uint32_t q_heads,
                                                         uint32_t k_heads, uint32_t dim);
-int sparcml_head_norm_rotary_backward(
-    const void* dq, int64_t dq_token_stride, int64_t dq_head_stride, const void* dk,
-    int64_t dk_token_stride, int64_t dk_head_stride, const void* q, int64_t q_token_stride,
-    int64_t q_head_stride, uint32_t q_heads, const void* k, int64_t k_token_stride,
-    int64_t k_head_stride, uint32_t k_heads, int32_t type, uint64_t tokens, uint32_t dim,
-    const void* positions, int32_t positions_int64, const float* freqs, uint32_t turned,
-    int32_t interleaved, const void* q_weight, const void* k_weight, int32_t weight_type,
-    float eps, void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
-    int64_t k_out_token_stride, int64_t k_out_head_stride, float* q_dweight, float* k_dweight,
-    int32_t accumulate, void* ws, size_t ws_bytes, void* stream);
+int sparcml_head_norm_rotary_backward(const struct sparcml_head_args* args, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,9 +1,14 @@
 """Host-side validation of the entry points that make a node's gradient: 8-bit activations, linear
 layers of experts, norm and rotation of queries and keys. Nothing here reaches a GPU."""
+import os
+import re
+
 import pytest
 
 from top_gradient_compression_gb300 import _lib, api
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "sparcml.h")
 FAKE = 1 << 20  # non-null, aligned, never dereferenced
 OK, BAD, WORKSPACE = 0, 1, 2
 
@@ -123,45 +128,61 @@ def test_expert_linear_backward_arguments(stored):
     assert call({10 + o: 0, 15 + o: None}) == OK
 
 
-def test_head_norm_rotary_arguments():
-    lib = _lib.load()
-    # q, token, head, heads, k, token, head, heads, type, tokens, dim, positions, int64, freqs,
-    # turned, interleaved, q_weight, k_weight, weight_type, eps, q_out, t, h, k_out, t, h, stream
-    good = [FAKE, 512, 64, 8, FAKE, 128, 64, 2, 1, 10, 64, FAKE, 0, FAKE, 64, 0, FAKE, FAKE, 1, 1e-6,
-            FAKE, 512, 64, FAKE, 128, 64, None]
-    call = caller(lib.sparcml_head_norm_rotary, good)
-    for i in (0, 4, 11, 13, 20, 23):
-        assert call({i: None}) == BAD
-    assert call({8: 3}) == BAD and call({18: 3}) == BAD and call({19: -1.0}) == BAD
-    assert call({19: float("nan")}) == BAD and call({9: 1 << 31}) == BAD
-    assert call({10: 0}) == BAD and call({10: 513}) == BAD
-    assert call({14: 66}) == BAD and call({14: 63}) == BAD
-    assert call({1: -1}) == BAD and call({6: -1}) == BAD and call({3: 65536}) == BAD
-    assert call({0: FAKE + 1}) == BAD and call({16: FAKE + 1}) == BAD and call({11: FAKE + 2}) == BAD
-    assert call({11: FAKE + 4, 12: 1}) == BAD
-    # results over one another
-    assert call({21: 511}) == BAD and call({22: 63}) == BAD and call({24: -1}) == BAD
-    assert call({9: 0}) == OK
-    assert call({3: 0, 7: 0, 0: None, 4: None, 20: None, 23: None}) == OK  # no heads at all
+HEADS = dict(q=FAKE, q_token_stride=512, q_head_stride=64, q_heads=8, k=FAKE, k_token_stride=128,
+             k_head_stride=64, k_heads=2, type=1, tokens=10, dim=64, positions=FAKE,
+             positions_int64=0, freqs=FAKE, turned=64, interleaved=0, q_weight=FAKE, k_weight=FAKE,
+             weight_type=1, eps=1e-6, q_out=FAKE, q_out_token_stride=512, q_out_head_stride=64,
+             k_out=FAKE, k_out_token_stride=128, k_out_head_stride=64, dq=FAKE,
+             dq_token_stride=512, dq_head_stride=64, dk=FAKE, dk_token_stride=128,
+             dk_head_stride=64, q_dweight=FAKE, k_dweight=FAKE, accumulate=0, ws=FAKE)
 
+
+def test_head_args_are_the_headers():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    members = re.search(r"struct sparcml_head_args \{(.*?)\};", text, re.S)[1]
+    names = [re.sub(r".*[ *]", "", m.strip()) for m in re.split(r"[;,]", members) if m.strip()]
+    assert names == _lib.HEAD_ARGS
+    kinds = {m.strip().split()[0] if "*" not in m else "pointer"
+             for m in members.split(";") if m.strip()}
+    assert kinds == {"pointer", "int64_t", "double"}
+
+
+@pytest.mark.parametrize("back", [False, True])
+def test_head_norm_rotary_arguments(back):
+    lib = _lib.load()
     size = lib.sparcml_head_norm_rotary_backward_workspace_size
     assert size(10, 8, 2, 0) == 0 and size(10, 8, 2, 513) == 0 and size(1 << 31, 8, 2, 64) == 0
     ws = size(10, 8, 2, 64)
     assert 256 < ws and ws % 256 == 0 and size(16384, 32, 8, 512) < 4 << 20
-    # dq, token, head, dk, token, head, then as above up to eps and the outputs, q_dweight,
-    # k_dweight, accumulate, ws, ws_bytes, stream
-    call = caller(lib.sparcml_head_norm_rotary_backward,
-                  [FAKE, 512, 64, FAKE, 128, 64, *good[:26], FAKE, FAKE, 0, FAKE, ws, None])
-    for i in (0, 3, 6, 10, 17, 19, 26, 29, 35):
-        assert call({i: None}) == BAD
-    assert call({1: -1}) == BAD and call({32: FAKE + 2}) == BAD and call({33: FAKE + 2}) == BAD
-    assert call({35: FAKE + 128}) == BAD and call({36: ws - 1}) == WORKSPACE
-    assert call({15: 0, 32: None, 33: None}) == OK
+    f = lib.sparcml_head_norm_rotary_backward if back else lib.sparcml_head_norm_rotary
+
+    def call(**change):
+        args = {**HEADS, "ws_bytes": ws, **change}
+        return f(_lib.pack_head_args(*(args[m] for m in _lib.HEAD_ARGS)), None)
+    assert f(None, None) == BAD
+    for name in ("q", "k", "positions", "freqs", "q_out", "k_out") + \
+            (("dq", "dk", "ws") if back else ()):
+        assert call(**{name: 0}) == BAD, name
+    for name in ("q_token_stride", "q_head_stride", "k_token_stride", "k_head_stride") + \
+            (("dq_token_stride", "dk_head_stride") if back else ()):
+        assert call(**{name: -1}) == BAD, name
+    for name, bad in (("type", 3), ("type", -1), ("type", 1 << 32), ("weight_type", 3),
+                      ("eps", -1.0), ("eps", float("nan")), ("tokens", 1 << 31), ("tokens", -1),
+                      ("dim", 0), ("dim", 513), ("dim", (1 << 32) + 64), ("turned", 66),
+                      ("turned", 63), ("turned", -2), ("q_heads", 65536), ("k_heads", -1),
+                      ("q", FAKE + 1), ("q_weight", FAKE + 1), ("positions", FAKE + 2),
+                      # results over one another
+                      ("q_out_token_stride", 511), ("q_out_head_stride", 63),
+                      ("k_out_token_stride", -1)):
+        assert call(**{name: bad}) == BAD, (name, bad)
+    assert call(positions=FAKE + 4, positions_int64=1) == BAD
+    none = dict(q_heads=0, k_heads=0, q=0, k=0, q_out=0, k_out=0, q_dweight=0, k_dweight=0)
+    assert call(tokens=0, q_dweight=0, k_dweight=0) == OK and call(**none) == OK
+    if back:
+        assert call(q_dweight=FAKE + 2) == BAD and call(ws=FAKE + 128) == BAD
+        assert call(ws_bytes=ws - 1) == WORKSPACE and call(ws_bytes=-1) == WORKSPACE
 
 
 def test_group_size_is_the_headers():
-    import os
-    import re
-    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
-    text = open(os.path.join(root, "include", "sparcml.h")).read()
+    text = open(HEADER).read()
     assert int(re.search(r"#define SPARCML_GROUP8 (\d+)", text)[1]) == api.GROUP8

@@ -7,6 +7,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 import threading
 
 from . import build as _build
@@ -16,6 +17,14 @@ _lib = None
 
 u32p = C.c_void_p  # device pointers travel as plain addresses
 vp = C.c_void_p
+
+# struct sparcml_head_args, in bytes: its members are pointers and int64, but for eps
+HEAD_ARGS = ("q q_token_stride q_head_stride q_heads k k_token_stride k_head_stride k_heads type "
+             "tokens dim positions positions_int64 freqs turned interleaved q_weight k_weight "
+             "weight_type eps q_out q_out_token_stride q_out_head_stride k_out k_out_token_stride "
+             "k_out_head_stride dq dq_token_stride dq_head_stride dk dk_token_stride "
+             "dk_head_stride q_dweight k_dweight accumulate ws ws_bytes").split()
+pack_head_args = struct.Struct("=" + "".join("d" if m == "eps" else "q" for m in HEAD_ARGS)).pack
 
 # name -> (restype, argtypes), in the order of include/sparcml.h
 SIGNATURES = {
@@ -101,18 +110,10 @@ SIGNATURES = {
                                                C.c_int64, vp, C.c_int32, vp, vp, C.c_uint64,
                                                C.c_uint64, vp, C.c_int64, vp, vp, C.c_int32, vp,
                                                C.c_size_t, vp]),
-    "sparcml_head_norm_rotary": (C.c_int, [vp, C.c_int64, C.c_int64, C.c_uint32, vp, C.c_int64,
-                                           C.c_int64, C.c_uint32, C.c_int32, C.c_uint64,
-                                           C.c_uint32, vp, C.c_int32, vp, C.c_uint32, C.c_int32,
-                                           vp, vp, C.c_int32, C.c_float, vp, C.c_int64, C.c_int64,
-                                           vp, C.c_int64, C.c_int64, vp]),
+    "sparcml_head_norm_rotary": (C.c_int, [C.c_char_p, vp]),
     "sparcml_head_norm_rotary_backward_workspace_size": (C.c_size_t, [C.c_uint64, C.c_uint32,
                                                                       C.c_uint32, C.c_uint32]),
-    "sparcml_head_norm_rotary_backward": (C.c_int, [
-        vp, C.c_int64, C.c_int64, vp, C.c_int64, C.c_int64, vp, C.c_int64, C.c_int64, C.c_uint32,
-        vp, C.c_int64, C.c_int64, C.c_uint32, C.c_int32, C.c_uint64, C.c_uint32, vp, C.c_int32, vp,
-        C.c_uint32, C.c_int32, vp, vp, C.c_int32, C.c_float, vp, C.c_int64, C.c_int64, vp,
-        C.c_int64, C.c_int64, vp, vp, C.c_int32, vp, C.c_size_t, vp]),
+    "sparcml_head_norm_rotary_backward": (C.c_int, [C.c_char_p, vp]),
     "sparcml_expert_linear_workspace_size": (C.c_size_t, [C.c_uint64, C.c_uint32, C.c_uint64,
                                                           C.c_uint64, C.c_int32]),
     "sparcml_expert_linear": (C.c_int, [vp, C.c_int64, vp, C.c_int64, C.c_int64, C.c_int32, vp,

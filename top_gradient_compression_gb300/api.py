@@ -848,8 +848,9 @@ def checkpoint8(x, out=None, stream=None):
     rows, dim, xs = _rows(x, "x")
     if out is None:
         ps, es, lead = (dim + 15) // 16 * 16, (dim + GROUP8 - 1) // GROUP8, x.shape[:-1]
-        codes = x.new_empty(*lead, ps, dtype=torch.int8)
-        exponents = x.new_empty(*lead, es, dtype=torch.uint8)
+        device = x.device
+        codes = torch.empty(*lead, ps, dtype=torch.int8, device=device)
+        exponents = torch.empty(*lead, es, dtype=torch.uint8, device=device)
         out, p, e = Checkpoint8(codes, exponents, dim, x.dtype), codes.data_ptr(), \
             exponents.data_ptr()
     else:
@@ -873,7 +874,7 @@ def restore8(x, out=None, dtype=None, stream=None):
             return restore8(x, out, dtype)
     p, ps, e, es, rows, dim = _stored(x, "x")
     if out is None:
-        out, ys = x.codes.new_empty(*x.shape, dtype=dtype or x.dtype), dim
+        out, ys = torch.empty(*x.shape, dtype=dtype or x.dtype, device=x.device), dim
     elif out.shape != x.shape:
         raise ValueError("out and x shapes differ")
     else:
@@ -1006,7 +1007,7 @@ def expert_linear(x, weight, offsets=None, out=None, ws=None, stream=None):
     op = _offsets(offsets, weight)
     rows = x.shape[0]
     if out is None:
-        out = x.new_empty(rows, n)
+        out = torch.empty(rows, n, dtype=x.dtype, device=x.device)
     _half(out, "out", x)
     yp, ys = _row_matrix(out, "out", rows, n)
     wp, wn = _fit((rows, experts, n, k), ws, x.device, x, weight)
@@ -1053,13 +1054,13 @@ def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
     xp, xs = None, k
     if need_dx:
         if dx is None:
-            dx = dy.new_empty(rows, k)
+            dx = torch.empty(rows, k, dtype=dy.dtype, device=dy.device)
         _half(dx, "dx", dy)
         xp, xs = _row_matrix(dx, "dx", rows, k)
     gp, gb, gs = None, 0, k
     if need_dweight:
         if dweight is None:
-            dweight = dy.new_empty(*weight.shape, dtype=torch.float32)
+            dweight = torch.empty(*weight.shape, dtype=torch.float32, device=dy.device)
         if not dweight.is_cuda or dweight.dtype != torch.float32 or dweight.shape != weight.shape:
             raise TypeError(f"dweight must be a float32 CUDA tensor of {list(weight.shape)}")
         gb, gs = _experts(dweight, "dweight")[:2]
@@ -1077,7 +1078,7 @@ def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
 def _heads(t, name: str, like=None, shape=None):
     """(pointer, token stride, head stride, heads) of [tokens, heads, dim]; of None, no heads."""
     if t is None:
-        return None, 0, 0, 0
+        return 0, 0, 0, 0
     _typed(t, name, like)
     size, stride = t.shape, t.stride()
     if len(size) != 3:
@@ -1089,13 +1090,16 @@ def _heads(t, name: str, like=None, shape=None):
     return t.data_ptr(), stride[0], stride[1], size[1]
 
 
+_NO_GRADIENTS = (0,) * 11  # what the forward pass does not read
+
+
 def _heads_out(t, name: str, x):
     """(output, pointer, token stride, head stride) for an input x, or for none."""
     if x is None:
-        return None, None, 0, 0
+        return None, 0, 0, 0
     if t is None:
-        tokens, heads, dim = x.shape
-        t = x.new_empty(tokens, heads, dim)
+        _, heads, dim = x.shape
+        t = torch.empty_like(x, memory_format=torch.contiguous_format)
         return t, t.data_ptr(), heads * dim, dim
     return (t, *_heads(t, name, x, x.shape)[:3])
 
@@ -1103,9 +1107,9 @@ def _heads_out(t, name: str, x):
 def _sum_out(t, name: str, x):
     """(float32 vector, pointer) for a weight's gradient, or for none."""
     if x is None:
-        return None, None
+        return None, 0
     if t is None:
-        t = x.new_empty(x.shape[2], dtype=torch.float32)
+        t = torch.empty(x.shape[2], dtype=torch.float32, device=x.device)
         return t, t.data_ptr()
     return t, _stat(t, x.shape[2], name)
 
@@ -1131,8 +1135,8 @@ def _head_args(q, k, positions, freqs, q_weight, k_weight):
     kw, kt = _vector(k_weight, dim, "k_weight")
     if qw is not None and kw is not None and qt != kt:
         raise TypeError("q_weight and k_weight must have the same type")
-    return tokens, dim, (positions.data_ptr(), int(positions.dtype == torch.int64), fp, turned), \
-        (qw, kw, qt if qw is not None else kt)
+    return tokens, dim, (positions.data_ptr(), positions.dtype == torch.int64, fp, turned), \
+        (qw or 0, kw or 0, qt if qw is not None else kt)
 
 
 def head_norm_rotary(q, k, positions, freqs, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -1157,9 +1161,9 @@ def head_norm_rotary(q, k, positions, freqs, q_weight=None, k_weight=None, eps: 
     tokens, dim, turn, weights = _head_args(q, k, positions, freqs, q_weight, k_weight)
     q_out, *qo = _heads_out(q_out, "q_out", q)
     k_out, *ko = _heads_out(k_out, "k_out", k)
-    r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary(
-        *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, interleaved, *weights, eps, *qo,
-        *ko, _raw_stream(x))
+    args = _lib.pack_head_args(*qa, *ka, TYPES[x.dtype], tokens, dim, *turn, interleaved, *weights,
+                               eps, *qo, *ko, *_NO_GRADIENTS)
+    r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary(args, _raw_stream(x))
     if r:
         _check("sparcml_head_norm_rotary", r)
     return q_out, k_out
@@ -1207,9 +1211,9 @@ def head_norm_rotary_backward(dq, dk, q, k, positions, freqs, q_weight=None, k_w
         ws = workspace(head_norm_rotary_backward_workspace_size(tokens, qa[3], ka[3], dim),
                        x.device)
     wp, wn = _space(ws)
-    r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary_backward(
-        *gq[:3], *gk[:3], *qa, *ka, TYPES[x.dtype], tokens, dim, *turn, interleaved, *weights, eps,
-        *qo, *ko, qs, ks, accumulate, wp, wn, _raw_stream(x))
+    args = _lib.pack_head_args(*qa, *ka, TYPES[x.dtype], tokens, dim, *turn, interleaved, *weights,
+                               eps, *qo, *ko, *gq[:3], *gk[:3], qs, ks, accumulate, wp, wn)
+    r = (_lib._lib or _lib.load()).sparcml_head_norm_rotary_backward(args, _raw_stream(x))
     if r:
         _check("sparcml_head_norm_rotary_backward", r)
     return dq_out, dk_out, dq_weight, dk_weight

@@ -549,15 +549,16 @@ bool input_ok(const Heads& h, uint32_t heads, size_t bytes) {
 }
 
 // What both passes check.
-int check_heads(const HeadArgs& a, int32_t type, int32_t weight_type) {
-  if (!type_ok(type) || !type_ok(weight_type) || a.tokens > 0x7fffffffull || a.dim < 1 ||
+int check_heads(const HeadArgs& a, int64_t type, int64_t weight_type) {
+  const auto known = [](int64_t t) { return t >= SPARCML_F32 && t <= SPARCML_F16; };
+  if (!known(type) || !known(weight_type) || a.tokens > 0x7fffffffull || a.dim < 1 ||
       a.dim > kMostDim || a.turned > a.dim || a.turned % 2 || !(a.eps >= 0.f))
     return SPARCML_ERR_INVALID_ARG;
   for (const Side& d : a.side)
-    if (d.heads > 65535 || (d.heads && !aligned_to(d.w, type_bytes(weight_type))))
+    if (d.heads > 65535 || (d.heads && !aligned_to(d.w, type_bytes((int32_t)weight_type))))
       return SPARCML_ERR_INVALID_ARG;
   if (a.tokens == 0 || a.side[0].heads + a.side[1].heads == 0) return SPARCML_OK;
-  const size_t e = type_bytes(type);
+  const size_t e = type_bytes((int32_t)type);
   if (a.turned && (!a.positions || !aligned_to(a.positions, a.wide ? 8 : 4) || !a.freqs ||
                    !aligned_to(a.freqs, 4)))
     return SPARCML_ERR_INVALID_ARG;
@@ -573,36 +574,47 @@ int check_heads(const HeadArgs& a, int32_t type, int32_t weight_type) {
 
 using namespace sparcml;
 
-extern "C" int sparcml_head_norm_rotary(
-    const void* q, int64_t q_token_stride, int64_t q_head_stride, uint32_t q_heads, const void* k,
-    int64_t k_token_stride, int64_t k_head_stride, uint32_t k_heads, int32_t type, uint64_t tokens,
-    uint32_t dim, const void* positions, int32_t positions_int64, const float* freqs,
-    uint32_t turned, int32_t interleaved, const void* q_weight, const void* k_weight,
-    int32_t weight_type, float eps, void* q_out, int64_t q_out_token_stride,
-    int64_t q_out_head_stride, void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
-    void* stream) {
+// The arguments of both passes; false where one is out of range.
+static bool read_args(const sparcml_head_args* p, bool back, HeadArgs& a) {
+  if (!p || p->tokens < 0 || p->dim < 0 || p->dim > kMostDim || p->q_heads < 0 ||
+      p->q_heads > 65535 || p->k_heads < 0 || p->k_heads > 65535 || p->turned < 0 ||
+      p->turned > kMostDim)
+    return false;
+  a = {};
+  a.side[0] = {{p->q, p->q_token_stride, p->q_head_stride}, {nullptr, 0, 0},
+               {p->q_out, p->q_out_token_stride, p->q_out_head_stride}, p->q_weight,
+               (uint32_t)p->q_heads, 0};
+  a.side[1] = {{p->k, p->k_token_stride, p->k_head_stride}, {nullptr, 0, 0},
+               {p->k_out, p->k_out_token_stride, p->k_out_head_stride}, p->k_weight,
+               (uint32_t)p->k_heads, 0};
+  if (back) {
+    a.side[0].g = {p->dq, p->dq_token_stride, p->dq_head_stride};
+    a.side[1].g = {p->dk, p->dk_token_stride, p->dk_head_stride};
+  }
+  a.tokens = (uint64_t)p->tokens;
+  a.dim = (uint32_t)p->dim;
+  a.turned = (uint32_t)p->turned;
+  a.positions = p->positions;
+  a.wide = p->positions_int64 != 0;
+  a.freqs = p->freqs;
+  a.w_type = (int32_t)p->weight_type;
+  a.eps = (float)p->eps;
+  return true;
+}
+
+extern "C" int sparcml_head_norm_rotary(const sparcml_head_args* args, void* stream) {
   const ApiRange nvtx_range(__func__);
-  HeadArgs a = {};
-  const Heads none = {nullptr, 0, 0};
-  a.side[0] = {{q, q_token_stride, q_head_stride}, none,
-               {q_out, q_out_token_stride, q_out_head_stride}, q_weight, q_heads, 0};
-  a.side[1] = {{k, k_token_stride, k_head_stride}, none,
-               {k_out, k_out_token_stride, k_out_head_stride}, k_weight, k_heads, 0};
-  a.tokens = tokens;
-  a.dim = dim;
-  a.turned = turned;
-  a.positions = positions;
-  a.wide = positions_int64;
-  a.freqs = freqs;
-  a.w_type = weight_type;
-  a.eps = eps;
-  const int r = check_heads(a, type, weight_type);
+  HeadArgs a;
+  if (!read_args(args, false, a)) return SPARCML_ERR_INVALID_ARG;
+  const int64_t type = args->type;
+  const int r = check_heads(a, type, args->weight_type);
   if (r != SPARCML_OK) return r;
-  if (tokens == 0 || q_heads + k_heads == 0) return SPARCML_OK;
+  if (a.tokens == 0 || a.side[0].heads + a.side[1].heads == 0) return SPARCML_OK;
+  const bool pairs = args->interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const uint32_t blocks = type == SPARCML_F32    ? heads_any<float>(a, interleaved, false, s)
-                          : type == SPARCML_BF16 ? heads_any<__nv_bfloat16>(a, interleaved, false, s)
-                                                 : heads_any<__half>(a, interleaved, false, s);
+  const uint32_t blocks = type == SPARCML_F32    ? heads_any<float>(a, pairs, false, s)
+                          : type == SPARCML_BF16 ? heads_any<__nv_bfloat16>(a, pairs, false, s)
+                                                 : heads_any<__half>(a, pairs, false, s);
   if (launch_status() != SPARCML_OK || !blocks) return SPARCML_ERR_CUDA;
   note_launches(1);
   return SPARCML_OK;
@@ -619,55 +631,41 @@ extern "C" size_t sparcml_head_norm_rotary_backward_workspace_size(uint64_t toke
   return 256 + align_up(2ull * most * dim * sizeof(float), 256);
 }
 
-extern "C" int sparcml_head_norm_rotary_backward(
-    const void* dq, int64_t dq_token_stride, int64_t dq_head_stride, const void* dk,
-    int64_t dk_token_stride, int64_t dk_head_stride, const void* q, int64_t q_token_stride,
-    int64_t q_head_stride, uint32_t q_heads, const void* k, int64_t k_token_stride,
-    int64_t k_head_stride, uint32_t k_heads, int32_t type, uint64_t tokens, uint32_t dim,
-    const void* positions, int32_t positions_int64, const float* freqs, uint32_t turned,
-    int32_t interleaved, const void* q_weight, const void* k_weight, int32_t weight_type, float eps,
-    void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
-    int64_t k_out_token_stride, int64_t k_out_head_stride, float* q_dweight, float* k_dweight,
-    int32_t accumulate, void* ws, size_t ws_bytes, void* stream) {
+extern "C" int sparcml_head_norm_rotary_backward(const sparcml_head_args* args, void* stream) {
   const ApiRange nvtx_range(__func__);
-  HeadArgs a = {};
-  a.side[0] = {{q, q_token_stride, q_head_stride}, {dq, dq_token_stride, dq_head_stride},
-               {q_out, q_out_token_stride, q_out_head_stride}, q_weight, q_heads, 0};
-  a.side[1] = {{k, k_token_stride, k_head_stride}, {dk, dk_token_stride, dk_head_stride},
-               {k_out, k_out_token_stride, k_out_head_stride}, k_weight, k_heads, 0};
-  a.tokens = tokens;
-  a.dim = dim;
-  a.turned = turned;
-  a.positions = positions;
-  a.wide = positions_int64;
-  a.freqs = freqs;
-  a.w_type = weight_type;
-  a.eps = eps;
-  const int r = check_heads(a, type, weight_type);
+  HeadArgs a;
+  if (!read_args(args, true, a)) return SPARCML_ERR_INVALID_ARG;
+  const int64_t type = args->type;
+  const int r = check_heads(a, type, args->weight_type);
   if (r != SPARCML_OK) return r;
-  if (!ws || !aligned_to(ws, 256) || !aligned_to(q_dweight, 4) || !aligned_to(k_dweight, 4))
+  float *const dq = args->q_dweight, *const dk = args->k_dweight;
+  uint8_t* const ws = static_cast<uint8_t*>(args->ws);
+  if (!ws || !aligned_to(ws, 256) || !aligned_to(dq, 4) || !aligned_to(dk, 4))
     return SPARCML_ERR_INVALID_ARG;
-  const bool work = tokens && q_heads + k_heads;
+  const uint32_t heads[2] = {a.side[0].heads, a.side[1].heads};
+  const bool work = a.tokens && heads[0] + heads[1];
   for (const Side& d : a.side)
-    if (work && !input_ok(d.g, d.heads, type_bytes(type))) return SPARCML_ERR_INVALID_ARG;
-  if (ws_bytes < sparcml_head_norm_rotary_backward_workspace_size(tokens, q_heads, k_heads, dim))
+    if (work && !input_ok(d.g, d.heads, type_bytes((int32_t)type))) return SPARCML_ERR_INVALID_ARG;
+  if (args->ws_bytes < 0 ||
+      (uint64_t)args->ws_bytes < sparcml_head_norm_rotary_backward_workspace_size(
+                                     a.tokens, heads[0], heads[1], a.dim))
     return SPARCML_ERR_WORKSPACE;
+  const bool sums = dq || dk, pairs = args->interleaved != 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const bool sums = q_dweight || k_dweight;
   uint32_t parts = 0;
   if (work) {
-    if (sums) a.part[0] = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + 256);
-    parts = type == SPARCML_F32    ? heads_any<float>(a, interleaved, true, s)
-            : type == SPARCML_BF16 ? heads_any<__nv_bfloat16>(a, interleaved, true, s)
-                                   : heads_any<__half>(a, interleaved, true, s);
+    if (sums) a.part[0] = reinterpret_cast<float*>(ws + 256);
+    parts = type == SPARCML_F32    ? heads_any<float>(a, pairs, true, s)
+            : type == SPARCML_BF16 ? heads_any<__nv_bfloat16>(a, pairs, true, s)
+                                   : heads_any<__half>(a, pairs, true, s);
     if (launch_status() != SPARCML_OK || !parts) return SPARCML_ERR_CUDA;
     note_launches(1);
   }
   if (sums) {
-    launch_pdl(join_columns_kernel, dim3((dim + 31) / 32, 2), 512, 0, s,
-               static_cast<const float*>(a.part[0]),
-               static_cast<const float*>(a.part[0] + (uint64_t)parts * dim), parts, (uint64_t)dim,
-               q_dweight, k_dweight, accumulate);
+    const float* part = reinterpret_cast<const float*>(ws + 256);
+    launch_pdl(join_columns_kernel, dim3((a.dim + 31) / 32, 2), 512, 0, s, part,
+               part + (uint64_t)parts * a.dim, parts, (uint64_t)a.dim, dq, dk,
+               (int32_t)(args->accumulate != 0));
     if (launch_status() != SPARCML_OK) return SPARCML_ERR_CUDA;
     note_launches(1);
   }
