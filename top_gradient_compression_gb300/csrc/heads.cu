@@ -504,7 +504,8 @@ uint32_t heads_typed(HeadArgs a, uint32_t pack, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (pack == 8) {
       a.lanes = lanes_for(a.units, 1);
-      return launch_heads<T, 8, 1, PAIRS, BACK, BACK ? 2 : 3>(a, s);
+      // (three blocks per SM forward, of 80 registers: 68 us against 63 at 16384 x 40 x 128)
+      return launch_heads<T, 8, 1, PAIRS, BACK, 2>(a, s);
     }
   }
   // two units per lane where 32 lanes do not hold a head: more than 256 elements
