@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ ExpertArgs a) {
   extern __shared__ uint8_t raw[];
   __shared__ alignas(8) uint64_t bars[3 * kStages + 5 + 2 * kFeed];
-  __shared__ uint32_t tmem_slot, partner[2], fed[kFeed];
+  __shared__ uint32_t tmem_slot, partner, fed[kFeed];  // partner: whether the other block gave up
   __shared__ Waits waits;
   __shared__ Table table;
   griddep_wait();
@@ -609,7 +609,7 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   if (threadIdx.x == 0) {
     waits.gave_up = 0;
     waits.limit_us = injected(a.inject) ? kInjectWaitUs : kWaitUs;
-    partner[0] = partner[1] = 0;
+    partner = 0;
     for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(w.full + 8 * s, 2);
       mbar_init(w.empty + 8 * s, 1);
@@ -677,26 +677,15 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   }
   tmem_fence_before();
   __syncthreads();  // now it is settled whether this block gave up
-  {
-    const uint32_t to = cluster_addr(smem_addr(partner), w.rank ^ 1u);
-    if (threadIdx.x == 0) store_cluster(to, waits.gave_up);
-    if (warp == kWriters && w.leader) store_cluster(to + 4, 2 * w.stage + w.phase);
-    __syncwarp();
-    cluster_sync();
-  }
-  if (waits.gave_up || partner[0]) {
-    // Nothing may still be in flight when the shared and tensor memory go.
+  if (threadIdx.x == 0) store_cluster(cluster_addr(smem_addr(&partner), w.rank ^ 1u), waits.gave_up);
+  __syncwarp();
+  cluster_sync();
+  if (waits.gave_up || partner) {
+    // Nothing may still be in flight when the shared and tensor memory go: loads and what was fed
+    // get their time to land, products are waited for.
     if (warp == kWriters && w.leader) {
-      const bool apart = partner[1] != 2 * w.stage + w.phase;
-      // Both blocks' loads report to the first one, in one phase of a stage; where the two stopped
-      // at different stages some phases never complete, and the loads get their time instead.
-      Waits alone = {0, kLandUs};
       const uint64_t end = global_ns() + 1000ull * kLandUs;
-      if (apart)
-        while (global_ns() < end) __nanosleep(1000);
-      else if (w.rank == 0)
-        for (uint32_t s = 0; s < kStages; ++s)
-          mbar_wait_inline(w.full + 8 * s, s < w.stage ? w.phase : w.phase ^ 1u, &alone);
+      while (global_ns() < end) __nanosleep(1000);
     }
     if (warp == kWriters + 1 && w.leader) {
       // arrives, in both blocks of a pair, once all products have completed
