@@ -230,6 +230,16 @@ def test_far_positions(position):
         assert torch.equal(narrow[0, 0].double() / 2 ** 0.5, got)
 
 
+@pytest.mark.parametrize("t", TYPES, ids=str)
+def test_no_epsilon(t, monkeypatch):
+    """With heads that leave lanes idle, which must add nothing to the weights' gradients."""
+    monkeypatch.setitem(globals(), "EPS", 0.0)
+    for dim in (64, 40, 6):
+        c = Case(t, 3, 3, 1, dim, dim // 4 * 2, False)
+        c.check_forward(c.forward())
+        c.check_backward(c.backward())
+
+
 def test_nan_stays_in_its_head():
     c = Case(torch.bfloat16, 6, 4, 2, 64, 64, False)
     c.x[0][3, 1, 5] = float("nan")

@@ -288,7 +288,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
   constexpr uint32_t kAhead = Mine::RING ? kRing - 1 : 1;
   struct Walk {
     const T* at;     // this lane's head
-    int64_t heads_on, token_on;  // to the next job of the token, from the last one to the next token
+    // to the next job of the token, and from its last one to the next token
+    int64_t heads_on, token_on;
     __device__ __forceinline__ Walk(const Heads& h, uint64_t token, uint32_t part, uint32_t jobs,
                                     uint32_t slots, uint32_t slot) {
       heads_on = (int64_t)slots * h.head;
@@ -393,7 +394,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
       sum.x += __shfl_xor_sync(0xffffffffu, sum.x, d);
       if constexpr (BACK) sum.y += __shfl_xor_sync(0xffffffffu, sum.y, d);
     }
-    const float r = rsqrtf(sum.x * inv + a.eps);
+    // (of lanes without a head: without an epsilon it would be an infinity, times zeros)
+    const float r = BACK && !active ? 0.f : rsqrtf(sum.x * inv + a.eps);
     const F2 by = f2(r, r);
     if constexpr (BACK) {
       const float k = -sum.y * inv * r * r * r;
@@ -451,7 +453,8 @@ __global__ void __launch_bounds__(32 * kWarps, MINB) heads_kernel(const HeadArgs
 // more than there are jobs.
 constexpr uint32_t kBackFit = 2;
 uint32_t grid_for(uint64_t jobs, uint32_t fit) {
-  return (uint32_t)std::max<uint64_t>(1, std::min<uint64_t>((jobs + kWarps - 1) / kWarps, kSms * fit));
+  const uint64_t blocks = std::min<uint64_t>((jobs + kWarps - 1) / kWarps, kSms * fit);
+  return (uint32_t)std::max<uint64_t>(1, blocks);
 }
 
 // Each returns the blocks of its grid, 0 if the launch failed.
