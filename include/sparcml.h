@@ -668,7 +668,8 @@ int sparcml_expert_linear_backward8(const void* dy, int64_t dy_stride, const int
  *             themselves (same strides). q_heads or k_heads may be 0.
  *   positions device int32 or, positions_int64, int64 [tokens], any value: the
  *             angle is off by at most 2^-26 of a turn and 2^-64 |p|.
- *   freqs     device fp32 [turned / 2], radians per position, finite.
+ *   freqs     device fp32 [turned / 2], radians per position, of either sign
+ *             and at most 2^40.
  *   q_weight, k_weight  [dim] of type weight_type, each may be NULL (ones).
  *   tokens 0 .. 2^31 - 1, dim 1 .. 512, turned even, 0 .. dim, heads 0 .. 65535.
  * The struct `args` is HOST memory, read during the call only. */

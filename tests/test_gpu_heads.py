@@ -230,6 +230,21 @@ def test_far_positions(position):
         assert torch.equal(narrow[0, 0].double() / 2 ** 0.5, got)
 
 
+@pytest.mark.parametrize("position", [12345, (1 << 31) - 1, (1 << 40) + 12347])
+def test_frequencies_of_either_sign(position):
+    """-f turns the other way by the same angle, at far positions too; bounds as above."""
+    f = torch.tensor([0.7310585, 1e-4, 3.0, 1.1e-7], dtype=torch.float32, device=DEV)
+    x = torch.zeros(1, 1, 16, device=DEV)
+    x[..., :8] = 1.0
+    p = torch.tensor([position], dtype=torch.int64, device=DEV)
+    got = api.head_norm_rotary(x, None, p, torch.cat([f, -f]), eps=0.0)[0][0, 0].double() / 2 ** 0.5
+    angles = torch.tensor([exact_angle(position, float(v)) for v in f.tolist()],
+                          dtype=torch.float64, device=DEV)
+    want = torch.cat([angles.cos(), angles.cos(), angles.sin(), -angles.sin()])
+    bound = 6.2832 * (2.0 ** -26 + position * 2.0 ** -64) + 2.0 ** -22
+    assert bool(((got - want).abs() <= bound).all())
+
+
 @pytest.mark.parametrize("t", TYPES, ids=str)
 def test_no_epsilon(t, monkeypatch):
     """With heads that leave lanes idle, which must add nothing to the weights' gradients."""

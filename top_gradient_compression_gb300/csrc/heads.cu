@@ -15,7 +15,8 @@
 //
 // Angles. A frequency is kept as 64 bits of a turn, f / 2 pi 2^64, so that position times
 // frequency modulo 2^64 is the angle without whole turns and without a rounding, however far the
-// position: the error is 2^-65 of a turn times the position. Its upper 32 bits go to sincospif.
+// position: the error is 2^-64 of a turn times the position, for frequencies up to 2^40. Its upper
+// 32 bits go to sincospif.
 
 #include "rows.cuh"
 
@@ -48,11 +49,11 @@ struct HeadArgs {
 };
 
 // f / 2 pi of a turn, in 2^-64: the product with 1 / 2 pi in two parts, of which whole turns
-// are dropped.
+// are dropped. What is left of the first one is at most half a turn of either sign, exactly.
 __device__ __forceinline__ uint64_t turn_fraction(float freq) {
   const double inv = 0.15915494309189535, low = -9.839338337591243e-18;  // 1 / 2 pi = inv + low
   const double f = freq, hi = f * inv, rest = fma(f, inv, -hi) + f * low;
-  const uint64_t a = __double2ull_rn((hi - floor(hi)) * 0x1p64);
+  const uint64_t a = (uint64_t)__double2ll_rn((hi - rint(hi)) * 0x1p64);
   return a + (uint64_t)__double2ll_rn(rest * 0x1p64);
 }
 
