@@ -249,3 +249,12 @@ def test_captured_and_replayed():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(back, x) and not torch.equal(got[1], want[1])
+
+
+def test_a_type_that_the_output_does_not_have():
+    c = api.checkpoint8(torch.ones(3, 40, dtype=torch.bfloat16, device=DEV))
+    out = torch.zeros(3, 40, device=DEV)
+    with pytest.raises(TypeError):
+        api.restore8(c, out=out, dtype=torch.bfloat16)
+    assert float(out.abs().sum()) == 0.0
+    assert api.restore8(c, out=out, dtype=torch.float32) is out and bool((out == 1).all())

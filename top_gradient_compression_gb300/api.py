@@ -835,7 +835,9 @@ def _stored(c, name: str, dtype=None):
 def checkpoint8(x, out=None, stream=None):
     """x in 8 bits, as a Checkpoint8: for each 128 columns of its last axis a power of two, for
     each element a whole number of at most 127 times that. It is within half a step of x, a step
-    being at most 1 / 63.5 of the group's largest magnitude; a NaN or an inf makes its group NaN.
+    being at most 1 / 63.5 of the group's largest magnitude or the type's least one above 0 (2^-126
+    if that is less), and within a step of what fp16 has above 65,280; a NaN or an inf makes its
+    group NaN.
     x: float32, bfloat16 or float16, its other axes may be strided as one."""
     if stream is not None:
         with _on(stream, x):
@@ -877,6 +879,8 @@ def restore8(x, out=None, dtype=None, stream=None):
         out, ys = torch.empty(*x.shape, dtype=dtype or x.dtype, device=x.device), dim
     elif out.shape != x.shape:
         raise ValueError("out and x shapes differ")
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, got {out.dtype}")
     else:
         ys = _rows(out, "out")[2]
     r = (_lib._lib or _lib.load()).sparcml_restore8(p, ps, e, es, rows, dim, out.data_ptr(),
