@@ -17,16 +17,22 @@
 // One launch, a persistent grid of pairs of SMs. Of a block's twelve warps one loads operands by
 // TMA, one issues the products (for both blocks of a pair), eight turn accumulators into results
 // while the next tile is under way, one clears rows (below). Where the experts' runs begin and end
-// is read on the device: every block works out the same list of tiles from them, and they are handed
-// out as pairs get to them. A long summed axis is split where there are few tiles, and for dW, whose
-// tiles are as deep as the experts' runs, in those tiles that no whole round of all pairs is left
-// for; the parts are added in order by a second launch.
+// is read on the device: every block works out the same list of tiles from them, and they are
+// handed out as pairs get to them. A long summed axis is split where there are few tiles, and for
+// dW, whose tiles are as deep as the experts' runs, in those tiles that no whole round of all pairs
+// is left for; the parts are added in order by a second launch.
 //
 // Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. The tensor cores
 // drop the bits that do not fit when they add to an accumulator, always towards zero: over 16,384
 // rows dW came out 1.9e-5 off, and that is an fp32 result. So an accumulator takes 512 rows, and
-// the writers' registers add those sums, rounded: 5e-7. For dW, the rows of the last 64 that belong to
-// the next expert are zeros in both operands, so that what stands there, a NaN say, does not count.
+// the writers' registers add those sums, rounded: 5e-7. For dW, the rows of the last 64 that belong
+// to the next expert are zeros in both operands, so that what stands there, a NaN say, does not
+// count.
+//
+// What bounds it is the tensor cores' rate. 16384 rows of one expert, 2048 x 4096 bf16 (143 us at
+// the rate of a large library product): forward 147 us, dx 155, dW 164; 8 runs of unequal lengths,
+// 4096 x 2048: 163 to 169, 163 to 168, 189 to 197. With few rows it is reading the matrices: 9 us
+// for a batch of single tokens whose matrices take 5 at the copy rate.
 
 #include <algorithm>
 #include <map>
@@ -42,7 +48,7 @@ namespace {
 constexpr uint32_t kMostExperts = 1024;
 constexpr uint32_t kSide = 256;      // i and j of a tile, at most
 constexpr uint32_t kPairs = 76;      // of SMs
-constexpr uint32_t kWriters = 8;     // warps that write results; then a loader, an issuer, a clearer
+constexpr uint32_t kWriters = 8;     // warps that write results; then loader, issuer, clearer
 constexpr uint32_t kThreads = 32 * (kWriters + 4);
 constexpr uint32_t kOperand = 128 * 128;  // bytes of one operand's 64 of the summed axis, per block
 constexpr uint32_t kStageBytes = 2 * kOperand, kStages = 6;
@@ -60,8 +66,8 @@ constexpr uint32_t kBand = 8;        // tiles along j that are taken together, f
 enum Form { kForward, kInput, kWeight };
 
 // x from its 8 bits into 16, for dW: a side job of the two warps that dx has nothing to do for, 16
-// columns per lane at a time. c 2^e is a number of either type, so nothing is rounded. (Converting in
-// the dW kernel itself, on the way to the products, took 500 us in all for 16384 x 2048 x 4096
+// columns per lane at a time. c 2^e is a number of either type, so nothing is rounded. (Converting
+// in the dW kernel itself, on the way to the products, took 500 us in all for 16384 x 2048 x 4096
 // against 165 for x in 16 bits: four warps are too few for it, and shared memory, whose bandwidth
 // the products' operands take up, is written and read twice more. A kernel of its own takes 32.)
 struct Restore {
@@ -460,7 +466,8 @@ __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const
   for (uint32_t b = it.s0; b < it.s1;) {
     const uint32_t from = b, end = FORM == kWeight ? min(b + kRun, it.s1) : it.s1;
     const uint32_t acc = w.acc & 1u;
-    if (!mbar_wait_warp_inline(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits)) return false;
+    if (!mbar_wait_warp_inline(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits))
+      return false;
     tmem_fence_after();
     const uint32_t d = w.tmem + acc * kSide;
     for (; b < end; ++b, w.next_stage()) {
@@ -652,7 +659,7 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
       const bool loaded = load_item<FORM>(w, m, a, item_of<FORM>(a, table, x));
       x = draws ? drawn_item(w, a, drawn) : kNone;
       if (!draws || (loaded && feed_item(w, fed_empty, x) == x)) continue;
-      while (x != kNone) {  // given up: the counter is left as the next kernel needs it all the same
+      while (x != kNone) {  // given up: the counter is left as the next kernel needs it
         drawn = draw_item(w, a);
         x = drawn_item(w, a, drawn);
       }
@@ -677,7 +684,8 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   }
   tmem_fence_before();
   __syncthreads();  // now it is settled whether this block gave up
-  if (threadIdx.x == 0) store_cluster(cluster_addr(smem_addr(&partner), w.rank ^ 1u), waits.gave_up);
+  if (threadIdx.x == 0)
+    store_cluster(cluster_addr(smem_addr(&partner), w.rank ^ 1u), waits.gave_up);
   __syncwarp();
   cluster_sync();
   if (waits.gave_up || partner) {
@@ -780,7 +788,7 @@ struct Sizes {
   bool ok() const {
     return rows <= 0x7fffffffull && experts >= 1 && experts <= kMostExperts && n >= 1 &&
            n <= (1u << 24) && k >= 1 && k <= (1u << 24) &&
-           // what is counted in 32 bits on the device (more would not fit the memory, or take minutes)
+           // counted in 32 bits on the device (more would not fit the memory, or take minutes)
            ceil_div(std::max(n, k), kSide) * (rows / kSide + experts) < (1ull << 31) &&
            (rows / 64 + experts) * ceil_div(n, kSide) * ceil_div(k, kSide) < (1ull << 31);
   }

@@ -245,7 +245,8 @@ __global__ void __launch_bounds__(256) restore_kernel(const StoreArgs a) {
     Codes<V> codes[Q] = {};
 #pragma unroll
     for (int q = 0; q < Q; ++q)
-      if (piece_column<V>(lane, q) < left) codes[q] = load_codes<V>(from + piece_column<V>(lane, q));
+      if (piece_column<V>(lane, q) < left)
+        codes[q] = load_codes<V>(from + piece_column<V>(lane, q));
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const uint32_t c = piece_column<V>(lane, q);
@@ -334,7 +335,8 @@ template <typename T, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8Args a) {
   griddep_wait();
   constexpr int V = 16 / sizeof(T), Q = 16 / V, P = V / 2;
-  extern __shared__ __align__(16) uint8_t dynamic[];  // [kRing][Q of dy, 1 of codes][MAXT] of 16 bytes
+  // [kRing][Q of dy, 1 of codes][MAXT] of 16 bytes
+  extern __shared__ __align__(16) uint8_t dynamic[];
   __shared__ float2 scratch[66 * (MAXT / 64)];
   Group g = make_group(a.threads, scratch);
   const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
@@ -577,7 +579,8 @@ bool launch_norm8(const Norm8Args& a, const BackwardShape& h, cudaStream_t s) {
   auto kernel = norm8_backward_kernel<T, MAXT, MINB>;
   const uint32_t groups = h.block / h.threads;
   const size_t ring = (size_t)kRing * (sizeof(T) + 1) * MAXT * 16;
-  const size_t smem = std::max(ring, groups > 1 ? (size_t)2 * groups * a.dim * sizeof(float) : (size_t)0);
+  const size_t join = groups > 1 ? (size_t)2 * groups * a.dim * sizeof(float) : 0;
+  const size_t smem = std::max(ring, join);
   if (!ensure_smem(reinterpret_cast<const void*>(kernel), smem)) return false;
   launch_pdl(kernel, h.parts, h.block, smem, s, a);
   return true;

@@ -132,7 +132,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, Waits* 
   return mbar_wait_long(bar, parity, waits);
 }
 
-// The same without a call, for kernels whose registers leave no room for one. PAIR: acquires for both blocks of a pair.
+// The same without a call, for kernels whose registers leave no room for one. PAIR: acquires for
+// both blocks of a pair.
 template <bool PAIR = false>
 __device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, Waits* waits) {
   // the clock is slow to read: every 64 tries will do
@@ -220,8 +221,8 @@ __device__ __forceinline__ uint64_t tile_desc(uint32_t addr, uint32_t lead, uint
 // Instruction descriptor: fp16 (or bf16) operands, fp32 accumulator, M x N.
 __host__ __device__ constexpr uint32_t mma_desc(uint32_t m, uint32_t n, bool a_mn, bool b_mn,
                                                 bool bf16 = false) {
-  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) |
-         ((m >> 4) << 24);
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 template <int CG>
