@@ -591,7 +591,6 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   __shared__ uint32_t tmem_slot, partner, fed[kFeed];  // partner: whether the other block gave up
   __shared__ Waits waits;
   __shared__ Table table;
-  griddep_wait();
   const uint32_t warp = threadIdx.x >> 5;
   Worker w;
   w.ring = (smem_addr(raw) + 1023u) & ~1023u;
@@ -615,7 +614,6 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   if (threadIdx.x < 2) tma_prefetch_map(threadIdx.x ? &m.q : &m.p);
   if (threadIdx.x == 0) {
     waits.gave_up = 0;
-    waits.limit_us = injected(a.inject) ? kInjectWaitUs : kWaitUs;
     partner = 0;
     for (uint32_t s = 0; s < kStages; ++s) {
       mbar_init(w.full + 8 * s, 2);
@@ -635,6 +633,8 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kWriters) tmem_alloc<2>(smem_addr(&tmem_slot), 2 * kSide);
+  griddep_wait();  // up to here nothing is read or written that another kernel may have
+  if (threadIdx.x == 0) waits.limit_us = injected(a.inject) ? kInjectWaitUs : kWaitUs;
   if (warp == 1) {
     const bool bad = make_runs(a, table);
     if (bad && blockIdx.x == 0 && w.leader) set_status(a.status, SPARCML_ERR_BAD_STREAM);
