@@ -618,7 +618,7 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  *             and matrices, no two elements at one address: for example the
  *             layer's slice of a node's flat gradient, at any offset. An
  *             expert without rows gets +0. accumulate != 0 adds to what it
- *             holds.
+ *             holds (one rounded addition; numbers below 2^-126 count as 0).
  *   backward  dx or dweight NULL: that gradient is left out, and weight or x
  *             is not read. backward8 takes x in 8 bits, its exponents as
  *             checkpoint8 writes them for `type`.

@@ -269,6 +269,21 @@ def test_weight_gradients_added_into_a_flat_gradient():
     assert float(dw[1].abs().sum()) == 0.0
 
 
+@pytest.mark.parametrize("sizes, n, k", [([40, 0, 70], 56, 40), ([3900, 1100], 264, 72),
+                                         ([300] * 20, 520, 513)], ids=["short", "deep", "many"])
+def test_what_is_added_is_what_would_be_written(sizes, n, k):
+    """One addition, rounded once, whether the sums come in one piece or in parts."""
+    c = Case(torch.bfloat16, sizes, n, k)
+    plain = api.expert_linear_backward(c.dy, c.x, c.w, c.offsets, need_dx=False)[1]
+    before = normal(9, len(sizes) * n * k + 5)
+    flat = before.clone()
+    dw = flat[1:-4].view(len(sizes), n, k)
+    api.expert_linear_backward(c.dy, c.x, c.w, c.offsets, dweight=dw, accumulate=True,
+                               need_dx=False)
+    assert torch.equal(flat[1:-4], before[1:-4] + plain.view(-1))
+    assert torch.equal(flat[:1], before[:1]) and torch.equal(flat[-4:], before[-4:])
+
+
 @pytest.mark.parametrize("stored", [False, True])
 def test_no_rows(stored):
     w = normal(1, 4, 72, 40).to(torch.bfloat16)
