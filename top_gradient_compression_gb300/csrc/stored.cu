@@ -323,13 +323,42 @@ __device__ __forceinline__ void write_sums(const Norm8Args& a, const Group& g, u
 // Here the rows are whole, aligned pieces, which come through a ring in shared memory: a thread
 // copies ahead and reads back its own pieces alone, so that the ring needs no barrier.
 //
-// 16384 x 4096 bf16 takes 79 us, 4.2 TB/s: half of the issue slots are filled by the 16 warps of an
-// SM that 119 registers allow. Without its arithmetic and its barrier the kernel takes 57; the
-// reduction over the row is 10 of the rest, the weights' sums 10, making floats of codes 10. Not
-// faster: what was read kept in place of the floats made of it (80 registers, 24 warps, but 1.5
-// times the instructions) 81 us; two rows at a time, read from the ring again after their sums, 86;
-// arithmetic single in place of packed, or one row ahead in registers, 79.
+// 16384 x 4096 bf16 takes 70 us, 4.8 TB/s: half of the issue slots are filled by the 16 warps of an
+// SM that 127 registers allow (its traffic alone takes 57 in this shape). What it took to come from
+// 79 was fewer instructions, 46 to 37 million: pointers that go on by a stride in place of a
+// product each, rows and columns that do not exist as zeros in place of branches, and sums over a
+// row by half the shuffles. Not faster: what was read kept in place of the floats made of it (80
+// registers, 24 warps), two rows at a time, a row's result in the turn after that of its sums (76),
+// arithmetic single in place of packed, three rows in the ring (71) or five.
 constexpr int kRing = 4;
+
+// The sums of two values over a row's threads. Of more than a warp: the halves of a warp add up one
+// of the values each, and all threads add up the warps' sums, of WARPS at most (those that are not
+// there are zeros, which the group's scratch, [2][16], holds from the start).
+template <int WARPS>
+__device__ __forceinline__ F2 row_sums(Group& g, float2 v) {
+  if (g.threads <= 32) {
+    v = g.sum2(v);
+    return f2(v.x, v.y);
+  }
+  const uint32_t lane = lane_id();
+  const bool second = lane & 16;
+  float u = second ? v.y : v.x;
+  u += __shfl_xor_sync(0xffffffffu, second ? v.x : v.y, 16);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) u += __shfl_xor_sync(0xffffffffu, u, d);
+  float2* s = g.scratch + 16 * (g.turn & 1u);
+  ++g.turn;
+  if ((lane & 15u) == 0) reinterpret_cast<float*>(s)[g.t / 16] = u;
+  g.sync();
+  F2 sum = f2(0.f, 0.f);
+#pragma unroll
+  for (int k = 0; k < WARPS; k += 2) {
+    const float4 two = *reinterpret_cast<const float4*>(s + k);
+    sum = add2<true>(sum, add2<true>(f2(two.x, two.y), f2(two.z, two.w)));
+  }
+  return sum;
+}
 
 template <typename T, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8Args a) {
@@ -337,10 +366,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8A
   constexpr int V = 16 / sizeof(T), Q = 16 / V, P = V / 2;
   // [kRing][Q of dy, 1 of codes][MAXT] of 16 bytes
   extern __shared__ __align__(16) uint8_t dynamic[];
-  __shared__ float2 scratch[66 * (MAXT / 64)];
-  Group g = make_group(a.threads, scratch);
-  const uint32_t threads = a.threads, groups = blockDim.x / threads, t = g.t;
-  const uint32_t dim = (uint32_t)a.dim, first = t / 8 * kGroup;
+  __shared__ alignas(16) float2 scratch[32 * (MAXT / 8)];
+  const uint32_t threads = a.threads, groups = blockDim.x / threads;
+  for (uint32_t i = threadIdx.x; i < 32 * groups; i += blockDim.x)
+    scratch[i] = make_float2(0.f, 0.f);
+  __syncthreads();
+  const uint32_t index = threadIdx.x / threads, t = threadIdx.x - index * threads;
+  Group g = {threads, index, t, scratch + 32 * index, 0};
+  const uint32_t dim = (uint32_t)a.dim, rows = (uint32_t)a.rows, first = t / 8 * kGroup;
   const float inv = 1.0f / (float)dim;
   auto column = [&](int i) { return first + piece_column<V>(t & 7u, i / V) + i % V; };
   bool there[Q];
@@ -356,55 +389,54 @@ __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8A
                                 : f2(1.f, 1.f);
     }
   }
-  const uint64_t step = (uint64_t)gridDim.x * groups;
+  const uint32_t step = gridDim.x * groups;
   constexpr uint32_t kSlot = (Q + 1) * MAXT * 16;
   uint8_t* const mine = dynamic + threadIdx.x * 16;
-  float mean_next[kRing - 1], rstd_next[kRing - 1];
-  uint32_t exp_next[kRing - 1];
-  auto fetch = [&](uint64_t row, uint32_t slot) {
-    if (row < a.rows) {
-      const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
-      const int8_t* x = a.codes + (int64_t)row * a.codes_stride;
-      uint8_t* to = mine + slot * kSlot;
+  const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+  float mean_of[kRing], rstd_of[kRing];
+  uint32_t exp_of[kRing];
+  // Rows are read in order, kRing - 1 ahead; what is not there, of a row or of rows, as zeros, so
+  // that its turn adds nothing to any sum.
+  uint32_t base = blockIdx.x * groups, next = base + index;
+  const T* dy = static_cast<const T*>(a.dy) + (int64_t)next * a.dy_stride + column(0);
+  const int8_t* x = a.codes + (int64_t)next * a.codes_stride + column(0);
+  const uint8_t* e = a.exponents + (int64_t)next * a.exponents_stride + first / kGroup;
+  T* dx = static_cast<T*>(a.dx) + (int64_t)next * a.dx_stride + column(0);
+  const int64_t dy_on = step * a.dy_stride, x_on = step * a.codes_stride,
+                e_on = step * a.exponents_stride, dx_on = step * a.dx_stride;
+  auto fetch = [&](uint32_t slot, float& mean, float& rstd, uint32_t& exponent) {
+    const bool active = next < rows;
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (there[q]) {
-          cp_async16(to + q * MAXT * 16, dy + column(q * V));
-          const uint32_t at = static_cast<uint32_t>(
-              __cvta_generic_to_shared(to + Q * MAXT * 16 + q * V));
-          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at),
-                       "l"(x + column(q * V)), "n"(V)
-                       : "memory");
-        }
+    for (int q = 0; q < Q; ++q) {
+      const uint32_t to = ring + slot * kSlot + q * MAXT * 16;
+      const bool here = active && there[q];
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to),
+                   "l"(dy + 8 * V * q), "r"(here ? 16 : 0)
+                   : "memory");
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(
+                       ring + slot * kSlot + Q * MAXT * 16 + q * V),
+                   "l"(x + 8 * V * q), "n"(V), "r"(here ? V : 0)
+                   : "memory");
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  auto fetch_small = [&](uint64_t row, float& mean, float& rstd, uint32_t& e) {
-    if (row < a.rows) {
-      mean = a.mean[row];
-      rstd = a.rstd[row];
-      if (first < dim) e = a.exponents[(int64_t)row * a.exponents_stride + first / kGroup];
+    mean = rstd = 0.f;
+    exponent = 0;
+    if (active) {
+      mean = a.mean[next];
+      rstd = a.rstd[next];
+      if (there[0]) exponent = *e;
     }
+    next += step;
+    dy += dy_on;
+    x += x_on;
+    e += e_on;
   };
-  uint64_t base = (uint64_t)blockIdx.x * groups;
 #pragma unroll
-  for (int k = 0; k < kRing - 1; ++k) {
-    mean_next[k] = rstd_next[k] = 0.f;
-    exp_next[k] = 0;
-    fetch(base + g.index + k * step, k);
-    fetch_small(base + g.index + k * step, mean_next[k], rstd_next[k], exp_next[k]);
-  }
-  uint32_t slot = 0;
-  for (; base < a.rows; base += step) {  // the same turns for all groups of threads
-    const uint64_t row = base + g.index;
-    const bool active = row < a.rows;
-    const float mean = mean_next[0], rstd = rstd_next[0], scale = scale_of(exp_next[0]);
-#pragma unroll
-    for (int k = 0; k < kRing - 2; ++k) {
-      mean_next[k] = mean_next[k + 1];
-      rstd_next[k] = rstd_next[k + 1];
-      exp_next[k] = exp_next[k + 1];
-    }
+  for (int k = 0; k < kRing - 1; ++k) fetch(k, mean_of[k], rstd_of[k], exp_of[k]);
+  // A row, whose small parts are the k-th; those of the one that is fetched become the `later`-th.
+  auto turn = [&](uint32_t slot, uint32_t free, int k, int later) {
+    const bool active = base + index < rows;
+    const float mean = mean_of[k], rstd = rstd_of[k], scale = scale_of(exp_of[k]);
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
     const F2 by = f2(scale, scale), minus = f2(-mean, -mean), r2 = f2(rstd, rstd);
     F2 xh[Q][P], d[Q][P], s0 = f2(0.f, 0.f), s1 = s0;
@@ -416,37 +448,56 @@ __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8A
       unpack<T, V>(raw, d[q]);
       codes_f2<V>(load_codes<V>(reinterpret_cast<const int8_t*>(from + Q * MAXT * 16 + q * V)),
                   xh[q]);
-      if (active && there[q]) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-          // c 2^e is exact, and so its difference from the mean is rounded once
-          xh[q][i] = mul2<true>(fma2<true>(xh[q][i], by, minus), r2);
-          gw[q][i] = fma2<true>(d[q][i], xh[q][i], gw[q][i]);
-          gb[q][i] = add2<true>(gb[q][i], d[q][i]);
-          d[q][i] = mul2<true>(d[q][i], w[q][i]);
-          s0 = add2<true>(s0, d[q][i]);
-          s1 = fma2<true>(d[q][i], xh[q][i], s1);
-        }
+      for (int i = 0; i < P; ++i) {
+        // c 2^e is exact, and so its difference from the mean is rounded once
+        xh[q][i] = mul2<true>(fma2<true>(xh[q][i], by, minus), r2);
+        gw[q][i] = fma2<true>(d[q][i], xh[q][i], gw[q][i]);
+        gb[q][i] = add2<true>(gb[q][i], d[q][i]);
+        d[q][i] = mul2<true>(d[q][i], w[q][i]);
+        s0 = add2<true>(s0, d[q][i]);
+        s1 = fma2<true>(d[q][i], xh[q][i], s1);
       }
     }
-    const uint64_t later = row + (kRing - 1) * step;
-    fetch(later, slot == 0 ? kRing - 1 : slot - 1);
-    fetch_small(later, mean_next[kRing - 2], rstd_next[kRing - 2], exp_next[kRing - 2]);
-    slot = slot + 1 == kRing ? 0 : slot + 1;
-    const float2 s = g.sum2(make_float2(s0.x + s0.y, s1.x + s1.y));
-    if (!active) continue;
+    fetch(free, mean_of[later], rstd_of[later], exp_of[later]);
+    const F2 s = row_sums<MAXT / 32>(g, make_float2(s0.x + s0.y, s1.x + s1.y));
     // dx = rstd (d - sum(d) / dim - xh sum(d xh) / dim)
     const float k1s = -s.x * inv * rstd, k2s = -s.y * inv * rstd;
     const F2 k1 = f2(k1s, k1s), k2 = f2(k2s, k2s);
-    T* dx = static_cast<T*>(a.dx) + (int64_t)row * a.dx_stride;
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (there[q]) {
+    for (int q = 0; q < Q; ++q) {
 #pragma unroll
-        for (int i = 0; i < P; ++i)
-          d[q][i] = fma2<true>(xh[q][i], k2, fma2<true>(d[q][i], r2, k1));
-        *reinterpret_cast<uint4*>(dx + column(q * V)) = pack<T, V>(d[q]);
+      for (int i = 0; i < P; ++i)
+        d[q][i] = fma2<true>(xh[q][i], k2, fma2<true>(d[q][i], r2, k1));
+      if (active && there[q])
+        *reinterpret_cast<uint4*>(dx + 8 * V * q) = pack<T, V>(d[q]);
+    }
+    dx += dx_on;
+  };
+  // The same turns for all groups of threads. In 16 bits the ring's turns are written out, so that
+  // no small part has to be there before its row's turn to be handed on; in fp32 that makes four
+  // times the code slower (16384 x 4096: 105 us in place of 95).
+  if constexpr (sizeof(T) == 2) {
+    while (base < rows) {
+#pragma unroll
+      for (int k = 0; k < kRing; ++k) {
+        if (base >= rows) break;
+        turn(k, (k + kRing - 1) % kRing, k, (k + kRing - 1) % kRing);
+        base += step;
       }
+    }
+  } else {
+    for (uint32_t slot = 0; base < rows; base += step) {
+      const uint32_t free = slot == 0 ? kRing - 1 : slot - 1;
+      turn(slot, free, 0, kRing - 1);
+#pragma unroll
+      for (int k = 0; k < kRing - 1; ++k) {
+        mean_of[k] = mean_of[k + 1];
+        rstd_of[k] = rstd_of[k + 1];
+        exp_of[k] = exp_of[k + 1];
+      }
+      slot = slot + 1 == kRing ? 0 : slot + 1;
+    }
   }
   if (a.part_w == nullptr) return;  // neither sum is wanted
   asm volatile("cp.async.wait_all;" ::: "memory");
@@ -482,18 +533,18 @@ __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_any_kernel(const No
   }
   const uint64_t step = (uint64_t)gridDim.x * groups;
   constexpr int kScales = LANES / 8;  // groups of 128 that the columns lie in
-  float mean_next = 0.f, rstd_next = 0.f;
+  float mean_of = 0.f, rstd_of = 0.f;
   auto fetch = [&](uint64_t row) {
     if (row >= a.rows) return;
-    mean_next = a.mean[row];
-    rstd_next = a.rstd[row];
+    mean_of = a.mean[row];
+    rstd_of = a.rstd[row];
   };
   uint64_t base = (uint64_t)blockIdx.x * groups;
   fetch(base + g.index);
   for (; base < a.rows; base += step) {  // the same turns for all groups of threads
     const uint64_t row = base + g.index;
     const int in = row < a.rows ? left : 0;
-    const float mean = mean_next, rstd = rstd_next;
+    const float mean = mean_of, rstd = rstd_of;
     const T* dy = static_cast<const T*>(a.dy) + (int64_t)row * a.dy_stride;
     const int8_t* x = a.codes + (int64_t)row * a.codes_stride;
     const uint8_t* e = a.exponents + (int64_t)row * a.exponents_stride;
