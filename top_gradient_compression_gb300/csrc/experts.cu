@@ -84,6 +84,7 @@ struct ExpertArgs {
   const int32_t* offsets;  // or null: one expert with all rows
   uint32_t experts, rows;
   uint32_t i_size, j_size, s_size;  // j_size for dW, s_size for the others; the rest is rows
+  uint32_t tall;        // forward, dx: j of a tile, at most
   uint32_t splits;      // forward, dx: parts of the summed axis
   uint32_t may_split;   // dW: whether tiles may be taken in parts
   uint32_t wide;        // j of a partial tile
@@ -178,7 +179,7 @@ __device__ __forceinline__ void make_items(const ExpertArgs& a, Table& t, uint32
     const uint32_t e = base + lane;
     uint32_t n = 0;
     if (e < a.experts)
-      n = FORM == kWeight ? ti * tj : ti * ceil_of(rows_of(t, e), kSide) * a.splits;
+      n = FORM == kWeight ? ti * tj : ti * ceil_of(rows_of(t, e), a.tall) * a.splits;
     const uint32_t upto = warp_incl_sum(n);
     if (e < a.experts) t.first[e] = sum + upto - n;
     sum += __shfl_sync(0xffffffffu, upto, 31);
@@ -244,7 +245,8 @@ __device__ __forceinline__ Item item_of(const ExpertArgs& a, const Table& t, uin
   it.s0 = (uint32_t)((uint64_t)blocks * split / splits);
   it.s1 = (uint32_t)((uint64_t)blocks * (split + 1) / splits);
   const uint32_t j_size = FORM == kWeight ? a.j_size : it.rows;
-  const uint32_t tj = ceil_of(j_size, kSide), ti = ceil_of(a.i_size, kSide);
+  const uint32_t tj = ceil_of(j_size, FORM == kWeight ? kSide : a.tall);
+  const uint32_t ti = ceil_of(a.i_size, kSide);
   // the rows of an expert are shared out evenly; of dW's matrix only the last tile is narrower
   it.width = FORM == kWeight ? kSide : (ceil_of(j_size, tj) + 15) / 16 * 16;
   const uint32_t band = u / (ti * kBand), rest = u - band * ti * kBand;
@@ -810,20 +812,42 @@ struct Sizes {
            ceil_div(std::max(n, k), kSide) * (rows / kSide + experts) < (1ull << 31) &&
            (rows / 64 + experts) * ceil_div(n, kSide) * ceil_div(k, kSide) < (1ull << 31);
   }
-  // Parts of the summed axis for forward and dx: as many as the pairs of SMs leave room for where
-  // even the most tiles that the rows can make are at most half as many.
-  uint32_t splits(uint64_t i, uint64_t s) const {
-    const uint64_t most = ceil_div(i, kSide) * (std::min(experts, rows) + rows / kSide);
-    if (most == 0 || most * 2 > kPairs) return 1;
-    return (uint32_t)std::max<uint64_t>(
-        1, std::min<uint64_t>(kPairs / most, ceil_div(s, 64) / kLeastBlocks));
+  // Forward and dx: the most tiles that the rows can make where one takes `tall` of them.
+  uint64_t most_tiles(uint64_t i, uint32_t tall) const {
+    return ceil_div(i, kSide) * (std::min(experts, rows) + rows / tall);
+  }
+  // Forward and dx: the most rows of a tile, and the parts of the summed axis, where all tiles and
+  // parts together are one round of all pairs (else 256, and one part): what takes least by times
+  // in ns that were measured on short calls. A block of 64 takes 240 with 64 rows and 272 with
+  // 256, writing 12.5 a row, adding up parts 3,000. (64 rows in place of 256, us: 1237 rows of 5 x 776
+  // x 336 dx 9.0 for 12.8, 512 of 2048 x 2048 13.4 for 14.9; but dx of 300 rows of 8192 x 2048
+  // 19.8 with 256 rows and 4 parts, 34.7 with 64 and one.)
+  struct Plan {
+    uint32_t tall, splits;
+  };
+  Plan plan(uint64_t i, uint64_t s) const {
+    const uint64_t blocks = ceil_div(s, 64);
+    Plan best = {kSide, 1};
+    uint64_t least = ~0ull;
+    for (uint32_t tall = kSide; tall >= 64; tall /= 2) {
+      const uint64_t tiles = most_tiles(i, tall);
+      for (uint64_t c = 1; c * tiles <= kPairs && (c == 1 || c * kLeastBlocks <= blocks); ++c) {
+        const uint64_t ns = ceil_div(blocks, c) * (230 + tall / 6) + tall * 25 / 2 +
+                            (c > 1 ? 3000 : 0);
+        if (ns < least) {
+          least = ns;
+          best = {tall, (uint32_t)c};
+        }
+      }
+    }
+    return best;
   }
   uint64_t weight_tiles() const { return experts * ceil_div(n, kSide) * ceil_div(k, kSide); }
   bool weight_splits() const { return rows > 64 * kJoinBlocks; }
-  uint32_t wide() const { return (uint32_t)std::min<uint64_t>(kSide, align_up(rows, 16)); }
   size_t part_bytes() const {
     size_t r = 0;
-    if (splits(n, k) > 1 || splits(k, n) > 1) r = (size_t)kPairs * wide() * kSide * 4;
+    if (plan(n, k).splits > 1 || plan(k, n).splits > 1)
+      r = (size_t)kPairs * std::min<uint64_t>(kSide, align_up(rows, 16)) * kSide * 4;
     if (weight_splits()) r = std::max(r, (size_t)2 * kPairs * kSide * kSide * 4);
     return align_up(r, 256);
   }
@@ -981,9 +1005,11 @@ int run(const Call& c, Operand p, Operand q, void* out, int64_t out_batch, int64
   a.i_size = (uint32_t)(FORM == kForward ? z.n : z.k);
   a.j_size = FORM == kWeight ? (uint32_t)z.n : 0;
   a.s_size = (uint32_t)(FORM == kForward ? z.k : FORM == kInput ? z.n : 0);
-  a.splits = FORM == kWeight ? 1 : z.splits(a.i_size, a.s_size);
+  const Sizes::Plan plan = FORM == kWeight ? Sizes::Plan{kSide, 1} : z.plan(a.i_size, a.s_size);
+  a.tall = plan.tall;
+  a.splits = plan.splits;
   a.may_split = FORM == kWeight && z.weight_splits();
-  a.wide = FORM == kWeight ? kSide : z.wide();
+  a.wide = FORM == kWeight ? kSide : (uint32_t)std::min<uint64_t>(a.tall, align_up(z.rows, 16));
   a.out = out;
   a.out_batch = out_batch;
   a.out_stride = out_stride;
@@ -1000,9 +1026,7 @@ int run(const Call& c, Operand p, Operand q, void* out, int64_t out_batch, int64
   if (!map_of(&m.p, p, a.bf16, FORM == kForward ? 128 : 64) ||
       !map_of(&m.q, q, a.bf16, FORM == kWeight ? 64 : kBox))
     return SPARCML_ERR_CUDA;
-  const uint64_t tiles = FORM == kWeight ? z.weight_tiles()
-                                         : ceil_div(a.i_size, kSide) *
-                                               (std::min(z.experts, z.rows) + z.rows / kSide);
+  const uint64_t tiles = FORM == kWeight ? z.weight_tiles() : z.most_tiles(a.i_size, a.tall);
   const uint64_t joined = a.may_split ? kPairs : a.splits > 1 ? tiles : 0;
   const uint64_t most = a.may_split ? kPairs : tiles * a.splits;
   return launch_experts<FORM>(m, a, std::max<uint64_t>(1, most), joined * (a.wide / 4), c.stream);
