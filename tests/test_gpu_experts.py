@@ -137,6 +137,18 @@ def test_split_sums(sizes, n, k):
         assert all(torch.equal(a, b) for a, b in zip(first, got))
 
 
+@pytest.mark.parametrize("sizes,n,k", [([256], 4096, 1024), ([300], 8192, 2048),
+                                       ([120, 0, 250, 65], 520, 640), ([333, 14], 1033, 4100)])
+def test_fewer_rows_per_tile_where_tiles_are_few(sizes, n, k):
+    """64, 128 and 256 rows, with and without parts of the summed axis."""
+    c = Case(torch.bfloat16, sizes, n, k, before=2, behind=7)
+    ws = api.workspace(api.expert_linear_workspace_size(c.rows, len(sizes), n, k), DEV)
+    y = api.expert_linear(c.x, c.w, c.offsets, ws=ws)
+    dx, _ = api.expert_linear_backward(c.dy, c.x, c.w, c.offsets, need_dweight=False, ws=ws)
+    c.check(y, dx)
+    assert api.get_status(ws) == 0
+
+
 @pytest.mark.parametrize("sizes,n,k", [([5000], 264, 96), ([700, 0, 3000, 77], 256, 256),
                                        ([1025, 511, 512, 513], 300, 257), ([9000, 1], 40, 24)])
 def test_split_weight_gradients(sizes, n, k):
