@@ -516,7 +516,7 @@ uint32_t heads_typed(HeadArgs a, uint32_t pack, cudaStream_t s) {
   if constexpr (sizeof(T) == 2) {
     if (pack == 8) {
       a.lanes = lanes_for(a.units, 1);
-      // (three blocks per SM forward, of 80 registers: 68 us against 63 at 16384 x 40 x 128)
+      // (three blocks per SM forward, of 80 registers: 68 us where two took 63, 16384 x 40 x 128)
       return launch_heads<T, 8, 1, PAIRS, BACK, 2>(a, s);
     }
   }
