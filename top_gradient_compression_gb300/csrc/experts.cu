@@ -24,10 +24,10 @@
 //
 // Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. The tensor cores
 // drop the bits that do not fit when they add to an accumulator, always towards zero: over 16,384
-// rows dW came out 1.9e-5 off, and that is an fp32 result. So an accumulator takes 512 rows, and
-// the writers' registers add those sums, rounded: 5e-7. For dW, the rows of the last 64 that belong
-// to the next expert are zeros in both operands, so that what stands there, a NaN say, does not
-// count.
+// rows dW came out 1.9e-5 off, and over 2^20 products of one sign y 6e-3, five half steps of bf16.
+// So an accumulator takes 512 of the summed axis, and the writers' registers add those sums, rounded:
+// dW 5e-7. For dW, the rows of the last 64 that belong to the next expert are zeros in both
+// operands, so that what stands there, a NaN say, does not count.
 //
 // What bounds it is the tensor cores' rate. 16384 rows of one expert, 2048 x 4096 bf16 (143 us at
 // the rate of a large library product): forward 147 us, dx 155, dW 164; 8 runs of unequal lengths,
@@ -60,7 +60,7 @@ constexpr uint32_t kSorted = 256;     // dW: experts, at most, that are taken by
 constexpr uint32_t kFeed = 4;         // items that a pair's first loader can be ahead
 // The workspace header's word that counts the items handed out; zero between kernels.
 constexpr size_t kItemsOffset = 48;
-constexpr uint32_t kRun = 8;          // dW: blocks of 64 rows that one accumulator takes
+constexpr uint32_t kRun = 8;          // blocks of 64 of the summed axis that an accumulator takes
 constexpr uint32_t kBand = 8;        // tiles along j that are taken together, for L2's sake
 
 enum Form { kForward, kInput, kWeight };
@@ -465,7 +465,7 @@ __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const
   constexpr uint32_t step_p = P_MN ? 2048 : 32, step_q = Q_MN ? 2048 : 32;
   const uint32_t idesc = mma_desc(256, it.width, P_MN, Q_MN, a.bf16);
   for (uint32_t b = it.s0; b < it.s1;) {
-    const uint32_t from = b, end = FORM == kWeight ? min(b + kRun, it.s1) : it.s1;
+    const uint32_t from = b, end = min(b + kRun, it.s1);
     const uint32_t acc = w.acc & 1u;
     if (!mbar_wait_warp_inline(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits))
       return false;
@@ -499,10 +499,22 @@ __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const
 // (fp32) is added to what is there, by the memory itself: one addition to each element, so that
 // nothing depends on an order. (Read, added and written by the thread, 8 at a time, 16384 rows in 8
 // unequal runs took 308 us for 4096 x 2048, one by one 921; so it is 204, and 187 without adding.)
-template <typename T, int N>
-__device__ __forceinline__ void put_row(T* o, int64_t step, uint32_t count, bool accumulate,
-                                        const float* v) {
-  if (sizeof(T) == 4 && accumulate) {
+template <int FORM, int N>
+__device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, int64_t step, uint32_t count,
+                                    const float* v) {
+  if (FORM != kWeight) {
+    uint16_t* const o = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+    for (uint32_t q = 0; q < N; q += 2) {
+      const F2 two = f2(v[q], v[q + 1]);
+      const uint32_t b = pack2<__nv_bfloat16>(two), h = pack2<__half>(two), w = a.bf16 ? b : h;
+      if (q < count) o[(int64_t)q * step] = (uint16_t)w;
+      if (q + 1 < count) o[(int64_t)(q + 1) * step] = (uint16_t)(w >> 16);
+    }
+    return;
+  }
+  float* const o = static_cast<float*>(a.out) + at;
+  if (a.accumulate) {
 #pragma unroll
     for (uint32_t q = 0; q < N; ++q)
       if (q < count)
@@ -512,18 +524,8 @@ __device__ __forceinline__ void put_row(T* o, int64_t step, uint32_t count, bool
   } else {
 #pragma unroll
     for (uint32_t q = 0; q < N; ++q)
-      if (q < count) o[(int64_t)q * step] = from_f32<T>(v[q]);
+      if (q < count) o[(int64_t)q * step] = v[q];
   }
-}
-template <int FORM, int N>
-__device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, int64_t step, uint32_t count,
-                                    const float* v) {
-  if (FORM == kWeight)
-    put_row<float, N>(static_cast<float*>(a.out) + at, step, count, a.accumulate, v);
-  else if (a.bf16)
-    put_row<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(a.out) + at, step, count, false, v);
-  else
-    put_row<__half, N>(static_cast<__half*>(a.out) + at, step, count, false, v);
 }
 
 // Sixteen sums of a thread's i, from column c of the tile: to their results, or where the parts of
@@ -545,62 +547,72 @@ __device__ __forceinline__ void put16(const ExpertArgs& a, const Item& it, uint3
 
 // An accumulator's rows are i, its columns j: a warp has 32 neighbouring i, so that it writes
 // whole stretches of a result's row as they come. The two warps of a quarter of the i alternate
-// over the columns, sixteen at a time.
+// over the columns, sixteen at a time. A block that is done with its columns leaves what is written
+// out for the others by one jump: instructions that were not used yet take long to come. (With a jump
+// over each of them, and a way of its own for either type of y, 64 rows of 8 x 2048 x 1024 took 10.0
+// us in place of 9.1, and 1024 of 4864 x 4096 29.2 in place of 27.0.)
 template <int FORM>
 __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const Item& it) {
   const uint32_t warp = threadIdx.x >> 5, quarter = warp & 3u, half = warp >> 2;
   const uint32_t side = 128 * w.rank + 32 * quarter + lane_id();
   const uint32_t src = w.tmem + (quarter << 21);
-  if constexpr (FORM == kWeight) {
-    // The sums of kRun blocks are added up here, rounded to nearest.
-    float sum[8][16];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-#pragma unroll
-      for (int q = 0; q < 16; ++q) sum[k][q] = 0.f;
-    }
-    for (uint32_t b = it.s0; b < it.s1; b += kRun) {
-      const uint32_t acc = w.acc & 1u;
-      if (!mbar_wait_warp_inline(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
-      tmem_fence_after();
-#pragma unroll
-      for (uint32_t k = 0; k < 8; ++k) {
-        const uint32_t c = 32 * k + 16 * half;
-        if (c < it.count) {
-          float v[16];
-          tmem_load16(src + acc * kSide + c, v);
-          tmem_load_wait(v);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) sum[k][q] += v[q];
-        }
-      }
-      tmem_fence_before();
-      __syncwarp();
-      if (lane_id() == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
-      ++w.acc;
-    }
-#pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-      if (32 * k + 16 * half < it.count)
-        put16<FORM>(a, it, side, 32 * k + 16 * half, sum[k]);
-  } else {
+  auto next = [&]() {  // the next accumulator, once it is full
     const uint32_t acc = w.acc & 1u;
     if (!mbar_wait_warp_inline(w.acc_full + 8 * acc, (w.acc >> 1) & 1u, w.waits)) return false;
     tmem_fence_after();
+    return true;
+  };
+  auto done = [&]() {
+    tmem_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * (w.acc & 1u));
+    ++w.acc;
+  };
+  auto from = [&](uint32_t c) { return src + (w.acc & 1u) * kSide + c; };
+  if (it.s1 - it.s0 <= kRun) {  // one accumulator, or (dW) none
+    const bool any = it.s1 > it.s0;
+    if (any && !next()) return false;
 #pragma unroll 1
     for (uint32_t c = 16 * half; c < it.count; c += 64) {  // two loads on their way at a time
-      float u[16], v[16];
-      tmem_load16(src + acc * kSide + c, u);
-      tmem_load16(src + acc * kSide + min(c + 32, kSide - 16), v);
-      tmem_load_wait(u);
-      tmem_load_wait(v);
+      float u[16] = {}, v[16] = {};
+      if (any) {
+        tmem_load16(from(c), u);
+        tmem_load16(from(min(c + 32, kSide - 16)), v);
+        tmem_load_wait(u);
+        tmem_load_wait(v);
+      }
       put16<FORM>(a, it, side, c, u);
       if (c + 32 < it.count) put16<FORM>(a, it, side, c + 32, v);
     }
-    tmem_fence_before();
-    __syncwarp();
-    if (lane_id() == 0) mbar_arrive_cluster(w.lead_acc_empty + 8 * acc);
-    ++w.acc;
+    if (any) done();
+    return true;
+  }
+  // The sums of kRun blocks are added up here, rounded to nearest.
+  float sum[8][16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) sum[k][q] = 0.f;
+  }
+  for (uint32_t b = it.s0; b < it.s1; b += kRun) {
+    if (!next()) return false;
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k) {
+      const uint32_t c = 32 * k + 16 * half;
+      if (c >= it.count) break;
+      float v[16];
+      tmem_load16(from(c), v);
+      tmem_load_wait(v);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) sum[k][q] += v[q];
+    }
+    done();
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < 8; ++k) {
+    const uint32_t c = 32 * k + 16 * half;
+    if (c >= it.count) break;
+    put16<FORM>(a, it, side, c, sum[k]);
   }
   return true;
 }
