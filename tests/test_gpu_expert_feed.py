@@ -1,0 +1,33 @@
+"""Experts' linear layers with many more tiles than pairs of SMs, which are handed out one by one:
+each has to be done once, by all warps of a pair, and the workspace's count has to be back at zero
+for the next call."""
+import pytest
+import torch
+
+from top_gradient_compression_gb300 import api
+
+from test_gpu_experts import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("sizes,n,k", [([1] * 900, 40, 24), ([64, 0, 65, 1] * 60, 264, 520),
+                                       ([300] * 20, 520, 513)], ids=["tiny", "short", "many"])
+def test_short_tiles_one_after_the_other(sizes, n, k):
+    """900 tiles of one block each and the like, so that the words that tell pairs their next tile
+    follow one another as fast as they can."""
+    c = Case(torch.bfloat16, sizes, n, k)
+    ws = api.workspace(api.expert_linear_workspace_size(c.rows, len(sizes), n, k), c.x.device)
+    kept = api.checkpoint8(c.x)
+    c.x = api.restore8(kept)
+    want = c.want()
+    first = None
+    for turn in range(20):
+        y = api.expert_linear(c.x, c.w, c.offsets, ws=ws)
+        got = y, *api.expert_linear_backward(c.dy, kept if turn % 2 else c.x, c.w, c.offsets, ws=ws)
+        if first is None:
+            first = got
+            c.check(*got, want=want)
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+        assert int(ws[48:52].view(torch.int32)) == 0
+    assert api.get_status(ws) == 0

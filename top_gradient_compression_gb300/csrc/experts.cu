@@ -308,7 +308,7 @@ __device__ __forceinline__ uint32_t drawn_item(const Worker& w, const ExpertArgs
 // Tells both blocks' warps; kNone if they do not get to it in time.
 __device__ __forceinline__ uint32_t feed_item(Worker& w, uint32_t fed_empty, uint32_t x) {
   const uint32_t s = w.feed;
-  if (!mbar_wait_warp_inline(fed_empty + 8 * s, w.feed_phase ^ 1u, w.waits)) return kNone;
+  if (!mbar_wait_warp_inline<true>(fed_empty + 8 * s, w.feed_phase ^ 1u, w.waits)) return kNone;
   if (w.leader) {
     asm volatile("st.shared.u32 [%0], %1;" ::"r"(w.fed + 4 * s), "r"(x) : "memory");
     mbar_arrive(w.feed_full + 8 * s);
@@ -329,8 +329,12 @@ __device__ __forceinline__ uint32_t next_item(Worker& w) {
   if (!mbar_wait_warp_inline<true>(w.feed_full + 8 * s, w.feed_phase, w.waits)) return kNone;
   uint32_t x;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(w.fed + 4 * s) : "memory");
-  __syncwarp();
-  if (w.leader) mbar_arrive_cluster(w.lead_fed_empty + 8 * s);  // releasing would await its stores
+  // All lanes have read the same word, so this is always true; but it takes the word itself to find
+  // out, and so the reads are over before the arrival that lets the feeder write the slot again. (The
+  // arrival is relaxed: releasing, it would also wait for what the warp has stored, 194 us against
+  // 187 for dx of 16384 rows in 8 runs, 4096 x 2048, 210 against 204 for dW.)
+  const bool read = __all_sync(0xffffffffu, x == __shfl_sync(0xffffffffu, x, 0));
+  if (w.leader && read) mbar_arrive_cluster(w.lead_fed_empty + 8 * s);
   __syncwarp();
   w.next_feed();
   return x;

@@ -62,11 +62,12 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }
-// Arrive at a barrier of any block of the cluster. Relaxed: it tells that tensor memory has been
-// read and may be written over, and of no other memory. What it rests on: tcgen05.wait::ld has
-// returned, so the values are in registers, before the tcgen05.fence on this side; the fence on
-// the other side comes after its wait. (With release it also waits for the warp's stores: 103 us
-// against 93 at 256 x 256, 335 against 317 at 8 x 1024 x 1024.)
+// Arrive at a barrier of any block of the cluster. Relaxed: it orders no memory. It tells that
+// something has been read and may be written over, and the caller sees to it that the values are in
+// registers by then: of tensor memory by tcgen05.wait::ld and the tcgen05.fence that follow the
+// read (the fence on the other side comes after its wait), of shared memory by an arrival that
+// depends on the word. (With release it also waits for the warp's stores: 103 us against 93 at 256
+// x 256, 335 against 317 at 8 x 1024 x 1024, orthogonalised.)
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
