@@ -630,7 +630,8 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  *             bytes, and its rows and matrices follow one another or are
  *             multiples of 8 elements apart. What is not so (or has rows of
  *             another length than a multiple of 8) is copied into the workspace
- *             first. Bounded waits as for sparcml_orthogonalize.
+ *             first. Bounded waits as for sparcml_orthogonalize, each longer by
+ *             4 us for every 64 of the summed axis (for dW of the rows).
  * Outputs may not overlap inputs. */
 size_t sparcml_expert_linear_workspace_size(uint64_t rows, uint32_t experts, uint64_t n,
                                             uint64_t k, int32_t aligned);

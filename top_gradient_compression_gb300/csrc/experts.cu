@@ -626,7 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ ExpertArgs a) {
   extern __shared__ uint8_t raw[];
   __shared__ alignas(8) uint64_t bars[3 * kStages + 5 + 2 * kFeed];
-  __shared__ uint32_t tmem_slot, partner, fed[kFeed];  // partner: whether the other block gave up
+  // partner: whether the other block gave up; armed: whether a fault is injected
+  __shared__ uint32_t tmem_slot, partner, armed, fed[kFeed];
   __shared__ Waits waits;
   __shared__ Table table;
   const uint32_t warp = threadIdx.x >> 5;
@@ -672,7 +673,12 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
   }
   if (warp == kWriters) tmem_alloc<2>(smem_addr(&tmem_slot), 2 * kSide);
   griddep_wait();  // up to here nothing is read or written that another kernel may have
-  if (threadIdx.x == 0) waits.limit_us = injected(a.inject) ? kInjectWaitUs : kWaitUs;
+  if (threadIdx.x == 0) {
+    // A warp may have to wait for a whole tile (the clearer for its end, all for the next one), of up
+    // to 2^25 blocks of 64, which take 0.25 us each. So a block adds 4 us.
+    armed = injected(a.inject);
+    waits.limit_us = (armed ? kInjectWaitUs : kWaitUs) + (FORM == kWeight ? a.rows : a.s_size) / 16;
+  }
   if (warp == 1) {
     const bool bad = make_runs(a, table);
     if (bad && blockIdx.x == 0 && w.leader) set_status(a.status, SPARCML_ERR_BAD_STREAM);
@@ -707,7 +713,7 @@ experts_kernel(const __grid_constant__ ExpertMaps m, const __grid_constant__ Exp
       if (!load_item<FORM>(w, m, a, item_of<FORM>(a, table, x))) break;
   } else if (warp == kWriters + 1) {
     // An injected fault: the first pair withholds its products.
-    const bool withhold = w.pair == 0 && waits.limit_us == kInjectWaitUs;
+    const bool withhold = w.pair == 0 && armed;
     if (w.rank == 0 && !withhold)
       for (; x < w.items; x = next_item(w))
         if (!issue_item<FORM>(w, a, item_of<FORM>(a, table, x))) break;

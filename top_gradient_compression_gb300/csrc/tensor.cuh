@@ -103,8 +103,9 @@ __device__ __forceinline__ bool mbar_try_wait_pair(uint32_t bar, uint32_t parity
 }
 
 // How long a wait inside a kernel may last, in microseconds, normally and while a fault is
-// injected. The longest legitimate one is for the last tile of another block: 2^18 blocks of 64
-// of the summed axis, at 512 cycles each, take 70 ms.
+// injected. Of an orthogonalisation the longest legitimate one is for the last tile of another block:
+// 2^18 blocks of 64 of the summed axis, at 512 cycles each, take 70 ms. A kernel whose tiles may be
+// deeper adds to it by their depth.
 constexpr uint32_t kWaitUs = 2000000, kInjectWaitUs = 2000;
 // What a copy that nothing holds up is given to land before a block leaves.
 constexpr uint32_t kLandUs = 20000;
