@@ -60,11 +60,13 @@ bool ensure_smem(const void* func, size_t bytes);
 // Workspace header: the status word at byte 0, a ticket word at byte
 // kTicketOffset, the fault-injection word at
 // byte kInjectOffset (written by sparcml_set_fault_injection, kept across
-// calls). The word arms the injection only when it holds kInjectArmed, a
+// calls), a count of work handed out at byte kItemsOffset. The word arms the injection only when it holds kInjectArmed, a
 // pattern that a workspace left uninitialised is very unlikely to contain.
 constexpr size_t kInjectOffset = 32;
 // Counts the blocks of a kernel that have finished; zero between kernels.
 constexpr size_t kTicketOffset = 16;
+// Counts the tiles that a kernel has handed out; zero between kernels.
+constexpr size_t kItemsOffset = 48;
 constexpr uint8_t kInjectByte = 0xa5;
 constexpr uint32_t kInjectArmed = 0xa5a5a5a5u;
 // Polls of a bounded wait, normally and while a fault is injected (then a

@@ -58,8 +58,6 @@ constexpr uint32_t kLeastBlocks = 8;  // forward, dx: of 64 in a part of a split
 constexpr uint32_t kJoinBlocks = 28;  // dW: blocks of 64 rows that take as long as adding up parts
 constexpr uint32_t kSorted = 256;     // dW: experts, at most, that are taken by falling depth
 constexpr uint32_t kFeed = 4;         // items that a pair's first loader can be ahead
-// The workspace header's word that counts the items handed out; zero between kernels.
-constexpr size_t kItemsOffset = 48;
 constexpr uint32_t kRun = 8;          // blocks of 64 of the summed axis that an accumulator takes
 constexpr uint32_t kBand = 8;        // tiles along j that are taken together, for L2's sake
 
