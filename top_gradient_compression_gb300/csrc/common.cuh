@@ -60,7 +60,8 @@ bool ensure_smem(const void* func, size_t bytes);
 // Workspace header: the status word at byte 0, a ticket word at byte
 // kTicketOffset, the fault-injection word at
 // byte kInjectOffset (written by sparcml_set_fault_injection, kept across
-// calls), a count of work handed out at byte kItemsOffset. The word arms the injection only when it holds kInjectArmed, a
+// calls), a count of work handed out at byte kItemsOffset. The word arms the
+// injection only when it holds kInjectArmed, a
 // pattern that a workspace left uninitialised is very unlikely to contain.
 constexpr size_t kInjectOffset = 32;
 // Counts the blocks of a kernel that have finished; zero between kernels.

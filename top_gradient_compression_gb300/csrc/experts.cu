@@ -364,18 +364,18 @@ __device__ __forceinline__ bool load_item(Worker& w, const ExpertMaps& m, const 
       else mbar_arrive_cluster(w.lead_full + 8 * s);
       const uint32_t at = FORM == kWeight ? it.row + b * 64 : b * 64;
       if constexpr (FORM == kForward) {
-        tma_load_3d_group<2>(p, &m.p, at, i0, a.shared ? 0 : it.e, bar);
+        tma_load_3d_pair(p, &m.p, at, i0, a.shared ? 0 : it.e, bar);
       } else {
         const uint32_t z = FORM == kInput && !a.shared ? it.e : 0;
-        tma_load_3d_group<2>(p, &m.p, i0, at, z, bar);
-        tma_load_3d_group<2>(p + kOperand / 2, &m.p, i0 + 64, at, z, bar);
+        tma_load_3d_pair(p, &m.p, i0, at, z, bar);
+        tma_load_3d_pair(p + kOperand / 2, &m.p, i0 + 64, at, z, bar);
       }
       if constexpr (FORM == kWeight) {
-        tma_load_3d_group<2>(q, &m.q, j0, at, 0, bar);
-        tma_load_3d_group<2>(q + kOperand / 2, &m.q, j0 + 64, at, 0, bar);
+        tma_load_3d_pair(q, &m.q, j0, at, 0, bar);
+        tma_load_3d_pair(q + kOperand / 2, &m.q, j0 + 64, at, 0, bar);
       } else {
         for (uint32_t k = 0; k < boxes; ++k)
-          tma_load_3d_group<2>(q + k * kBox * 128, &m.q, at, j0 + k * kBox, 0, bar);
+          tma_load_3d_pair(q + k * kBox * 128, &m.q, at, j0 + k * kBox, 0, bar);
       }
     }
     __syncwarp();

@@ -468,6 +468,22 @@ __device__ __forceinline__ void store_box(uint32_t box, __half* out, uint64_t pi
     if (row0 + q + r < rows) *reinterpret_cast<uint4*>(o) = lds128(box + box_at(q + r, c));
 }
 
+// Before a block leaves that gave up, or whose partner did: until the operands have landed. A
+// pair's loads all report to the first block, in one phase per stage for both blocks; where the
+// two stopped at different stages (`apart`) some phases never complete, and the loads get their
+// time instead.
+__device__ __noinline__ void land_operands(uint32_t full, uint32_t stages, uint32_t stage,
+                                           uint32_t phase, bool apart) {
+  if (apart) {
+    const uint64_t end = global_ns() + 1000ull * kLandUs;
+    while (global_ns() < end) __nanosleep(1000);
+    return;
+  }
+  Waits alone = {0, kLandUs};
+  for (uint32_t s = 0; s < stages; ++s)
+    mbar_wait(full + 8 * s, s < stage ? phase : phase ^ 1u, &alone);
+}
+
 // What becomes of a product's entry, for all products alike:
 //     r = f acc + (r0 + r1 d_j) in_ij
 // with d the diagonal vector of column j, and in what stands at that place:

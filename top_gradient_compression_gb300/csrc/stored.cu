@@ -22,22 +22,10 @@ template <int V>
 __device__ __forceinline__ uint32_t piece_column(uint32_t octet_lane, int q) {
   return 8 * V * q + V * octet_lane;
 }
-// A lane's V elements from p, those from `left` on as zeros; `packs`: they are aligned.
+// A lane's V elements to p, those before `left` alone where that is less.
 template <typename T, int V = 16 / sizeof(T)>
-__device__ __forceinline__ void load_piece(const T* p, int64_t left, bool packs, F2 (&f)[V / 2]) {
-  if (packs && left >= V) {
-    unpack<T, V>(load_raw<T, V>(p), f);
-  } else {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i)
-      f[i] = f2(2 * i < left ? to_f32(p[2 * i]) : 0.f,
-                2 * i + 1 < left ? to_f32(p[2 * i + 1]) : 0.f);
-  }
-}
-template <typename T, int V = 16 / sizeof(T)>
-__device__ __forceinline__ void store_piece(T* p, int64_t left, bool packs,
-                                            const F2 (&f)[V / 2]) {
-  if (packs && left >= V) {
+__device__ __forceinline__ void store_piece(T* p, int64_t left, const F2 (&f)[V / 2]) {
+  if (left >= V) {
     *reinterpret_cast<uint4*>(p) = pack<T, V>(f);
   } else {
 #pragma unroll
@@ -294,7 +282,7 @@ __global__ void __launch_bounds__(256) restore_kernel(const StoreArgs a) {
       codes_f2<V>(codes[q], f);
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) f[i] = mul2<true>(f[i], f2(scale, scale));
-      if (c < left) store_piece<T>(y + c, left - c, PACKS, f);
+      if (c < left) store_piece<T>(y + c, left - c, f);
     }
   }
 }

@@ -189,18 +189,14 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
-// A tile of three axes, also for one block of a pair.
-template <int CG>
-__device__ __forceinline__ void tma_load_3d_group(uint32_t dst, const CUtensorMap* map, uint32_t x,
-                                                  uint32_t y, uint32_t z, uint32_t bar) {
-  if constexpr (CG == 1)
-    tma_load_3d(dst, map, x, y, z, bar);
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier"
-        "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
+// A tile of three axes for one block of a pair, reported to a barrier of either.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t x,
+                                                 uint32_t y, uint32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier"
+      "::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 // Orders this thread's ordinary accesses to global or to shared memory with the
 // asynchronous copies' ones.
@@ -305,22 +301,6 @@ __device__ __forceinline__ void tmem_load_wait(float (&v)[16]) {
                  "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                :
                : "memory");
-}
-
-// Before a block leaves that gave up, or whose partner did: until the operands have landed. A
-// pair's loads all report to the first block, in one phase per stage for both blocks; where the
-// two stopped at different stages (`apart`) some phases never complete, and the loads get their
-// time instead.
-static __device__ __noinline__ void land_operands(uint32_t full, uint32_t stages, uint32_t stage,
-                                           uint32_t phase, bool apart) {
-  if (apart) {
-    const uint64_t end = global_ns() + 1000ull * kLandUs;
-    while (global_ns() < end) __nanosleep(1000);
-    return;
-  }
-  Waits alone = {0, kLandUs};
-  for (uint32_t s = 0; s < stages; ++s)
-    mbar_wait(full + 8 * s, s < stage ? phase : phase ^ 1u, &alone);
 }
 
 // ---------------------------------------------------------------------------
