@@ -816,6 +816,11 @@ class Checkpoint8:
         return f"Checkpoint8({list(self.shape)}, {self.dtype}, {self.device})"
 
 
+def _checkpoint(c, name: str):
+    if not isinstance(c, Checkpoint8):
+        raise TypeError(f"{name} must be a Checkpoint8, got {type(c).__name__}")
+
+
 def _stored(c, name: str, dtype=None):
     """(codes, their stride, exponents, their stride, rows, dim) of a Checkpoint8."""
     width, groups = (c.dim + 15) // 16 * 16, (c.dim + GROUP8 - 1) // GROUP8
@@ -839,6 +844,8 @@ def checkpoint8(x, out=None, stream=None):
     if that is less), and within a step of what fp16 has above 65,280; a NaN or an inf makes its
     group NaN.
     x: float32, bfloat16 or float16, its other axes may be strided as one."""
+    if out is not None:
+        _checkpoint(out, "out")
     if stream is not None:
         with _on(stream, x):
             return checkpoint8(x, out)
@@ -868,6 +875,7 @@ def checkpoint8(x, out=None, stream=None):
 
 def restore8(x, out=None, dtype=None, stream=None):
     """What a Checkpoint8 stands for, in its own type or ``dtype``."""
+    _checkpoint(x, "x")
     if stream is not None:
         with _on(stream, x.codes):
             return restore8(x, out, dtype)
@@ -877,14 +885,16 @@ def restore8(x, out=None, dtype=None, stream=None):
     p, ps, e, es, rows, dim = _stored(x, "x")
     if out is None:
         out, ys = torch.empty(*x.shape, dtype=dtype or x.dtype, device=x.device), dim
-    elif out.shape != x.shape:
-        raise ValueError("out and x shapes differ")
-    elif dtype is not None and out.dtype != dtype:
-        raise TypeError(f"out must be {dtype}, got {out.dtype}")
+        code = _typed(out, "out")
     else:
+        code = _typed(out, "out")
+        if out.shape != x.shape:
+            raise ValueError("out and x shapes differ")
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out must be {dtype}, got {out.dtype}")
         ys = _rows(out, "out")[2]
-    r = (_lib._lib or _lib.load()).sparcml_restore8(p, ps, e, es, rows, dim, out.data_ptr(),
-                                                    _typed(out, "out"), ys, _raw_stream(x.codes))
+    r = (_lib._lib or _lib.load()).sparcml_restore8(p, ps, e, es, rows, dim, out.data_ptr(), code,
+                                                    ys, _raw_stream(x.codes))
     if r:
         _check("sparcml_restore8", r)
     return out
@@ -1065,7 +1075,8 @@ def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
     if need_dweight:
         if dweight is None:
             dweight = torch.empty(*weight.shape, dtype=torch.float32, device=dy.device)
-        if not dweight.is_cuda or dweight.dtype != torch.float32 or dweight.shape != weight.shape:
+        if not isinstance(dweight, torch.Tensor) or not dweight.is_cuda or \
+                dweight.dtype != torch.float32 or dweight.shape != weight.shape:
             raise TypeError(f"dweight must be a float32 CUDA tensor of {list(weight.shape)}")
         gb, gs = _experts(dweight, "dweight")[:2]
         gp = dweight.data_ptr()
