@@ -527,8 +527,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm8_backward_kernel(const Norm8A
       slot = slot + 1 == kRing ? 0 : slot + 1;
     }
   }
-  if (a.part_w == nullptr) return;  // neither sum is wanted
+  // also the zeros in place of rows behind the last one have to have come before the block leaves
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (a.part_w == nullptr) return;  // neither sum is wanted
   float fw[16], fb[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
