@@ -603,10 +603,11 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  * expert e the rows offsets[e] .. offsets[e + 1) and the matrix W_e [n][k].
  *     y[r] = x[r] W_e'        dx[r] = dy[r] W_e
  *     dW_e = sum over its rows of dy[r]' x[r]
- * Sums are fp32: of 512 of the summed axis on the tensor cores, which drop at
- * most 34 times 2^-22 of the products' magnitudes in all, and these sums added
- * with roundings to nearest. Results are rounded once. A NaN or an inf of a row
- * reaches that row's result and its own expert's dW alone.
+ * Sums are fp32: of 512 rows for dW, else of 1024 of the summed axis, on the
+ * tensor cores, which drop at most 34 (66) times 2^-22 of the products'
+ * magnitudes in all, and these sums added with roundings to nearest. Results
+ * are rounded once. A NaN or an inf of a row reaches that row's result and its
+ * own expert's dW alone.
  *   x, dx [rows][k], y, dy [rows][n], weight: type `type`, SPARCML_BF16 or
  *             SPARCML_F16 (the tensor cores have no fp32 product); strides as
  *             for layer norm, those of the matrices weight_batch_stride (0: one

@@ -24,10 +24,10 @@
 //
 // Numbers. Operands as they are (16 bits), sums in fp32, one rounding at the end. The tensor cores
 // drop the bits that do not fit when they add to an accumulator, always towards zero: over 16,384
-// rows dW came out 1.9e-5 off, and over 2^20 products of one sign y 6e-3, five half steps of bf16.
-// So an accumulator takes 512 of the summed axis, and the writers' registers add those sums, rounded:
-// dW 5e-7. For dW, the rows of the last 64 that belong to the next expert are zeros in both
-// operands, so that what stands there, a NaN say, does not count.
+// rows dW came out 1.9e-5 off, and over 2^20 products of one sign y 6e-3, 15 half steps of fp16.
+// So an accumulator takes 512 rows of dW, and 1024 of y's and dx's summed axis, and the writers'
+// registers add those sums, rounded: dW 5e-7. For dW, the rows of the last 64 that belong to the
+// next expert are zeros in both operands, so that what stands there, a NaN say, does not count.
 //
 // What bounds it is the tensor cores' rate. 16384 rows of one expert, 2048 x 4096 bf16 (143 us at
 // the rate of a large library product): forward 147 us, dx 155, dW 164; 8 runs of unequal lengths,
@@ -58,10 +58,16 @@ constexpr uint32_t kLeastBlocks = 8;  // forward, dx: of 64 in a part of a split
 constexpr uint32_t kJoinBlocks = 28;  // dW: blocks of 64 rows that take as long as adding up parts
 constexpr uint32_t kSorted = 256;     // dW: experts, at most, that are taken by falling depth
 constexpr uint32_t kFeed = 4;         // items that a pair's first loader can be ahead
-constexpr uint32_t kRun = 8;          // blocks of 64 of the summed axis that an accumulator takes
 constexpr uint32_t kBand = 8;        // tiles along j that are taken together, for L2's sake
 
 enum Form { kForward, kInput, kWeight };
+
+// Blocks of 64 of the summed axis that an accumulator takes. What y and dx lose in 1024, 6e-6 where
+// all products have one sign, is a 40th of fp16's least half step; dW is an fp32 result. (With 512
+// forward took 166 us in place of 162, 16384 rows of 4096 x 2048, one call by itself; in one
+// accumulator for the whole axis 159.)
+template <int FORM>
+constexpr uint32_t kRun = FORM == kWeight ? 8 : 16;
 
 // x from its 8 bits into 16, for dW: a side job of the two warps that dx has nothing to do for, 16
 // columns per lane at a time. c 2^e is a number of either type, so nothing is rounded. (Converting
@@ -472,7 +478,7 @@ __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const
   constexpr uint32_t step_p = P_MN ? 2048 : 32, step_q = Q_MN ? 2048 : 32;
   const uint32_t idesc = mma_desc(256, it.width, P_MN, Q_MN, a.bf16);
   for (uint32_t b = it.s0; b < it.s1;) {
-    const uint32_t from = b, end = min(b + kRun, it.s1);
+    const uint32_t from = b, end = min(b + kRun<FORM>, it.s1);
     const uint32_t acc = w.acc & 1u;
     if (!mbar_wait_warp_inline(w.acc_empty + 8 * acc, ((w.acc >> 1) & 1u) ^ 1u, w.waits))
       return false;
@@ -576,7 +582,7 @@ __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const
     ++w.acc;
   };
   auto from = [&](uint32_t c) { return src + (w.acc & 1u) * kSide + c; };
-  if (it.s1 - it.s0 <= kRun) {  // one accumulator, or (dW) none
+  if (it.s1 - it.s0 <= kRun<FORM>) {  // one accumulator, or (dW) none
     const bool any = it.s1 > it.s0;
     if (any && !next()) return false;
 #pragma unroll 1
@@ -594,14 +600,14 @@ __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const
     if (any) done();
     return true;
   }
-  // The sums of kRun blocks are added up here, rounded to nearest.
+  // The accumulators' sums are added up here, rounded to nearest.
   float sum[8][16];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
 #pragma unroll
     for (int q = 0; q < 16; ++q) sum[k][q] = 0.f;
   }
-  for (uint32_t b = it.s0; b < it.s1; b += kRun) {
+  for (uint32_t b = it.s0; b < it.s1; b += kRun<FORM>) {
     if (!next()) return false;
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {
