@@ -614,8 +614,8 @@ int sparcml_layer_norm_backward8(const void* dy, int64_t dy_stride, int32_t type
  *             for all experts) and weight_stride >= 0.
  *   offsets   DEVICE int32 [experts + 1], rising, from 0 at least to rows at
  *             most; or NULL for one expert with all rows. Rows of no expert
- *             are neither read nor written. An offset out of order or range
- *             is taken as the nearest one that is not, and
+ *             do not count, whatever they hold, and are not written. An offset
+ *             out of order or range is taken as the nearest one that is not, and
  *             SPARCML_ERR_BAD_STREAM recorded in the workspace.
  *   dweight   fp32, dweight_stride >= k and dweight_batch_stride between rows
  *             and matrices, no two elements at one address: for example the

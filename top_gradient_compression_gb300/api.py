@@ -1040,7 +1040,7 @@ def expert_linear_backward(dy, x, weight, offsets=None, dx=None, dweight=None,
     it. dweight is float32 [experts, n, k] (or [n, k]), for example a view of a node's flat
     gradient at any offset; with ``accumulate`` the sums are added to what it holds, else an expert
     without rows gets zeros. need_dx, need_dweight: one that is False is left out (None). Rows of
-    no expert are neither read nor written."""
+    no expert do not count, whatever they hold, and are not written."""
     args = (dy, x, weight, offsets, dx, dweight, accumulate, need_dx, need_dweight, ws)
     if stream is not None:
         with _on(stream, dy):

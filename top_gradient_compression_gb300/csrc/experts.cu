@@ -30,9 +30,10 @@
 // next expert are zeros in both operands, so that what stands there, a NaN say, does not count.
 //
 // What bounds it is the tensor cores' rate. 16384 rows of one expert, 2048 x 4096 bf16 (143 us at
-// the rate of a large library product): forward 147 us, dx 155, dW 164; 8 runs of unequal lengths,
-// 4096 x 2048: 163 to 169, 163 to 168, 189 to 197. With few rows it is reading the matrices: 9 us
-// for a batch of single tokens whose matrices take 5 at the copy rate.
+// the rate of a large library product) in loops of a few ms: forward 147 us, dx 158, dW 163; 8 runs
+// of unequal lengths, 4096 x 2048: 170, 169, 188. (Call after call for half a second, under the power
+// cap, that forward pass takes 190.) With few rows it is reading the matrices: 9 us for a batch of
+// single tokens whose matrices take 5 at the copy rate.
 
 #include <algorithm>
 #include <map>
@@ -511,7 +512,7 @@ __device__ __forceinline__ bool issue_item(Worker& w, const ExpertArgs& a, const
 // N sums of a thread to their results, `step` elements apart, of which `count` exist. dW alone
 // (fp32) is added to what is there, by the memory itself: one addition to each element, so that
 // nothing depends on an order. (Read, added and written by the thread, 8 at a time, 16384 rows in 8
-// unequal runs took 308 us for 4096 x 2048, one by one 921; so it is 204, and 187 without adding.)
+// unequal runs took 308 us for 4096 x 2048, one by one 921; so it is 205, and 188 without adding.)
 template <int FORM, int N>
 __device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, int64_t step, uint32_t count,
                                     const float* v) {
@@ -851,8 +852,8 @@ struct Sizes {
   // parts together are one round of all pairs (else 256, and one part): what takes least by times
   // in ns that were measured on short calls. A block of 64 takes 240 with 64 rows and 272 with
   // 256, writing 12.5 a row, adding up parts 3,000. (64 rows in place of 256, us: 1237 rows of 5 x 776
-  // x 336 dx 9.0 for 12.8, 512 of 2048 x 2048 13.4 for 14.9; but dx of 300 rows of 8192 x 2048
-  // 19.8 with 256 rows and 4 parts, 34.7 with 64 and one.)
+  // x 336 dx 9.9 for 12.2, 512 of 2048 x 2048 14.2 for 17.0; but dx of 300 rows of 8192 x 2048
+  // 22 with 256 rows and 4 parts, 36 with 64 and one.)
   struct Plan {
     uint32_t tall, splits;
   };

@@ -353,7 +353,7 @@ __device__ __forceinline__ void write_sums(const Norm8Args& a, const Group& g, u
 //
 // 16384 x 4096 bf16 takes 70 us, 4.8 TB/s: half of the issue slots are filled by the 16 warps of an
 // SM that 127 registers allow (its traffic alone takes 57 in this shape). What it took to come from
-// 79 was fewer instructions, 46 to 37 million: pointers that go on by a stride in place of a
+// 79 was fewer instructions, 46 to 35 million: pointers that go on by a stride in place of a
 // product each, rows and columns that do not exist as zeros in place of branches, and sums over a
 // row by half the shuffles. Not faster: what was read kept in place of the floats made of it (80
 // registers, 24 warps), two rows at a time, a row's result in the turn after that of its sums (76),
