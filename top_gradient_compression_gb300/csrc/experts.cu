@@ -561,10 +561,10 @@ __device__ __forceinline__ void put16(const ExpertArgs& a, const Item& it, uint3
 
 // An accumulator's rows are i, its columns j: a warp has 32 neighbouring i, so that it writes
 // whole stretches of a result's row as they come. The two warps of a quarter of the i alternate
-// over the columns, sixteen at a time. A block that is done with its columns leaves what is written
+// over the columns, sixteen at a time. A warp that is done with its columns leaves what is written
 // out for the others by one jump: instructions that were not used yet take long to come. (With a jump
-// over each of them, and a way of its own for either type of y, 64 rows of 8 x 2048 x 1024 took 10.0
-// us in place of 9.1, and 1024 of 4864 x 4096 29.2 in place of 27.0.)
+// over each of them, and a way of its own for either type of y, 1024 rows of 4864 x 4096 took 29.2 us
+// in place of 27.0, in pieces of 512.)
 template <int FORM>
 __device__ __forceinline__ bool write_item(Worker& w, const ExpertArgs& a, const Item& it) {
   const uint32_t warp = threadIdx.x >> 5, quarter = warp & 3u, half = warp >> 2;
